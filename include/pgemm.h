@@ -226,6 +226,84 @@ PGEMM_API pgemm_status gemm_bf16_ex(int M, int N, int K, float alpha, const uint
 PGEMM_API pgemm_status gemm_i8_ex(int M, int N, int K, int32_t alpha, const int8_t *A, const int8_t *B,
                         int32_t beta, int32_t *C, const pgemm_config *cfg, pgemm_stream_t stream);
 
+/* ---------------------------------------------------------- operators ---
+ * The products of a transformer with what surrounds them fused to them, on
+ * bf16 operands with fp32 accumulation (tcgen05).  The common rules above
+ * hold: device pointers owned by the caller, row-major and contiguous,
+ * 16-byte-aligned bases, work enqueued on `stream`, scratch from the
+ * library's pool, synchronous argument errors.  What is computed from a
+ * product is computed in fp32; a bf16 output is rounded once.
+ * Inputs and outputs must not overlap unless said otherwise. */
+
+/* Activations (`act`).  PGEMM_ACT_GELU is z Phi(z); PGEMM_ACT_GELU_TANH its
+ * tanh form z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2; PGEMM_ACT_SILU
+ * z / (1 + exp(-z)). */
+typedef enum {
+    PGEMM_ACT_NONE = 0,
+    PGEMM_ACT_RELU = 1,
+    PGEMM_ACT_GELU = 2,
+    PGEMM_ACT_GELU_TANH = 3,
+    PGEMM_ACT_SILU = 4
+} pgemm_act;
+
+/* Y <- act(X W + bias) + residual.  X is M x K, W K x N, bias N (NULL: none),
+ * residual M x N (NULL: none; may be Y itself), Y M x N.  preact (NULL: not
+ * kept): M x N fp32, receives X W + bias for linear_bf16_backward.  M, N,
+ * K >= 0; K == 0 counts X W as zero. */
+PGEMM_API pgemm_status linear_bf16(int M, int N, int K, const uint16_t *X, const uint16_t *W,
+                                   const uint16_t *bias, int act, const uint16_t *residual,
+                                   uint16_t *Y, float *preact, pgemm_stream_t stream);
+
+/* Gradients of linear_bf16 for dY (M x N): with Z = X W + bias and
+ * dZ = dY * act'(Z) (rounded to bf16, as the products' operand),
+ * dX (M x K) <- dZ W^T, dW (K x N) <- X^T dZ, dbias (N) <- column sums of dZ.
+ * Any of the three may be NULL: not computed.  preact: what linear_bf16 kept,
+ * or NULL: Z is computed again (act NONE needs neither).  The residual's
+ * gradient is dY. */
+PGEMM_API pgemm_status linear_bf16_backward(int M, int N, int K, const uint16_t *X,
+                                            const uint16_t *W, const uint16_t *bias, int act,
+                                            const uint16_t *dY, const float *preact, uint16_t *dX,
+                                            uint16_t *dW, uint16_t *dbias, pgemm_stream_t stream);
+
+/* H <- act(X Wg) * (X Wu), elementwise product.  X is M x K, Wg and Wu K x F,
+ * H M x F.  preact (NULL: not kept): 2 x M x F fp32, receives X Wg and X Wu
+ * for gated_bf16_backward. */
+PGEMM_API pgemm_status gated_bf16(int M, int F, int K, const uint16_t *X, const uint16_t *Wg,
+                                  const uint16_t *Wu, int act, uint16_t *H, float *preact,
+                                  pgemm_stream_t stream);
+
+/* Gradients of gated_bf16 for dH (M x F): with G = X Wg, U = X Wu,
+ * dG = dH * U * act'(G) and dU = dH * act(G) (each rounded to bf16, as the
+ * products' operands), dX (M x K) <- dG Wg^T + dU Wu^T, dWg and dWu (K x F)
+ * <- X^T dG, X^T dU.  dX, or dWg and dWu together, may be NULL.  preact: what
+ * gated_bf16 kept, or NULL: G and U are computed again. */
+PGEMM_API pgemm_status gated_bf16_backward(int M, int F, int K, const uint16_t *X,
+                                           const uint16_t *Wg, const uint16_t *Wu, int act,
+                                           const uint16_t *dH, const float *preact, uint16_t *dX,
+                                           uint16_t *dWg, uint16_t *dWu, pgemm_stream_t stream);
+
+/* Softmax cross entropy of T tokens over a vocabulary of V: with logits
+ * L = X W^T (X T x D; W V x D, one row a token of the vocabulary, as an
+ * embedding table is stored), lse[t] <- log sum_v exp L[t][v] and
+ * loss[t] <- lse[t] - L[t][target[t]].  A target outside [0, V) does not
+ * count: its loss is 0.  loss or lse may be NULL.  The logits are never
+ * stored.  V >= 1. */
+PGEMM_API pgemm_status xent_bf16(int T, int V, int D, const uint16_t *X, const uint16_t *W,
+                                 const int64_t *target, float *loss, float *lse,
+                                 pgemm_stream_t stream);
+
+/* xent_bf16 together with its gradients: with
+ * P[t][v] = (exp(L[t][v] - lse[t]) - (v == target[t])) * dloss[t] (rounded to
+ * bf16, as the products' operand; dloss NULL: ones; rows that do not count:
+ * zero), dX (T x D) <- P W and dW (V x D) <- P^T X.  Either may be NULL.
+ * workspace_bytes bounds the scratch that holds P (0: the library's choice,
+ * 2 GiB): a larger P goes by in pieces of the vocabulary.  Results of
+ * different bounds differ only in the order of fp32 sums. */
+PGEMM_API pgemm_status xent_bf16_grad(int T, int V, int D, const uint16_t *X, const uint16_t *W,
+                                      const int64_t *target, const float *dloss, float *loss,
+                                      float *lse, uint16_t *dX, uint16_t *dW,
+                                      long long workspace_bytes, pgemm_stream_t stream);
+
 /* The configuration the library picks for a shape (the per-shape table). */
 PGEMM_API pgemm_status pgemm_default_config(pgemm_dtype dtype, int M, int N, int K, pgemm_config *out);
 

@@ -21,7 +21,9 @@ __all__ = [
     "pgemm_kernel_attrs", "pgemm_get_device_status", "pgemm_selftest_wait_timeout",
     "pgemm_status_string", "pgemm_version", "gemm_i8_noalloc", "NOALLOC_SCRATCH_BYTES",
     "pgemm_stage_reuse_demo", "pgemm_schedule", "pgemm_stream_k_plan", "pgemm_trim_scratch",
-    "DTYPES", "STATUS", "EXPORTED", "PRODUCERS", "ENGINES",
+    "DTYPES", "STATUS", "EXPORTED", "PRODUCERS", "ENGINES", "ACTIVATIONS",
+    "linear_bf16", "linear_bf16_backward", "gated_bf16", "gated_bf16_backward", "xent_bf16",
+    "xent_bf16_grad",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -39,6 +41,8 @@ DTYPES = {"f32": 0, "bf16": 1, "i8": 2}
 PRODUCERS = {"tma": 0, "registers": 1, "staged": 2, "widen_in_kernel": 3}
 # pgemm_engine: which multiply-accumulate consumes the stages
 ENGINES = {"default": 0, "mma_sync": 1}
+# pgemm_act: the activations of the operators
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 # Every function include/pgemm.h declares.
 EXPORTED = [
     "gemm_f32", "gemm_bf16", "gemm_i8", "gemm_f32_ex", "gemm_bf16_ex", "gemm_i8_ex",
@@ -46,6 +50,8 @@ EXPORTED = [
     "pgemm_get_device_status", "pgemm_selftest_wait_timeout", "pgemm_status_string",
     "pgemm_version", "gemm_i8_noalloc", "pgemm_stage_reuse_demo", "pgemm_schedule",
     "pgemm_stream_k_plan", "pgemm_trim_scratch",
+    "linear_bf16", "linear_bf16_backward", "gated_bf16", "gated_bf16_backward", "xent_bf16",
+    "xent_bf16_grad",
 ]
 
 
@@ -106,6 +112,12 @@ def _declare(L: ctypes.CDLL) -> ctypes.CDLL:
         "pgemm_schedule": [i, cfgp, i, i, i, llp, ip, llp, ip, llp],
         "pgemm_stream_k_plan": [ll, i, i, i, llp, ip, ip, llp],
         "pgemm_trim_scratch": [],
+        "linear_bf16": [i, i, i, vp, vp, vp, i, vp, vp, vp, vp],
+        "linear_bf16_backward": [i, i, i, vp, vp, vp, i, vp, vp, vp, vp, vp, vp],
+        "gated_bf16": [i, i, i, vp, vp, vp, i, vp, vp, vp],
+        "gated_bf16_backward": [i, i, i, vp, vp, vp, i, vp, vp, vp, vp, vp, vp],
+        "xent_bf16": [i, i, i, vp, vp, vp, vp, vp, vp],
+        "xent_bf16_grad": [i, i, i, vp, vp, vp, vp, vp, vp, vp, vp, ll, vp],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -211,6 +223,95 @@ def gemm_bf16_ex(M, N, K, alpha, A, B, beta, C, config=None, stream=None):
 def gemm_i8_ex(M, N, K, alpha, A, B, beta, C, config=None, stream=None):
     _check(lib().gemm_i8_ex(M, N, K, int(alpha), _ptr(A), _ptr(B), int(beta), _ptr(C),
                             _cfg(config), _stream(stream)), "gemm_i8_ex")
+
+
+def _operand(x, name, count, itemsize) -> int:
+    """_ptr of an operator's operand, which must hold at least ``count``
+    elements of ``itemsize`` bytes (checked for tensors; None passes)."""
+    if x is None or isinstance(x, int):
+        return x or 0
+    p = _ptr(x)
+    if x.element_size() != itemsize:
+        raise ValueError(f"{name}: elements of {x.element_size()} bytes, {itemsize} wanted")
+    if x.numel() < count:
+        raise ValueError(f"{name}: {x.numel()} elements, at least {count} wanted")
+    return p
+
+
+def _act(act) -> int:
+    if isinstance(act, str):
+        if act not in ACTIVATIONS:
+            raise ValueError(f"unknown activation {act!r}: one of {', '.join(ACTIVATIONS)}")
+        return ACTIVATIONS[act]
+    return int(act)
+
+
+def linear_bf16(M, N, K, X, W, bias, act, residual, Y, preact=None, stream=None):
+    """Y <- act(X @ W + bias) + residual, bf16 with fp32 arithmetic.  X: M x K,
+    W: K x N; bias (N) and residual (M x N, may be Y) may be None; ``act`` is a
+    name of ACTIVATIONS.  ``preact`` (M x N fp32) receives X @ W + bias for the
+    backward call.  Asynchronous on ``stream``."""
+    _check(lib().linear_bf16(M, N, K, _operand(X, "X", M * K, 2), _operand(W, "W", K * N, 2),
+                             _operand(bias, "bias", N, 2), _act(act),
+                             _operand(residual, "residual", M * N, 2),
+                             _operand(Y, "Y", M * N, 2), _operand(preact, "preact", M * N, 4),
+                             _stream(stream)), "linear_bf16")
+
+
+def linear_bf16_backward(M, N, K, X, W, bias, act, dY, dX, dW, dbias, preact=None, stream=None):
+    """Gradients of linear_bf16 for dY (M x N) into dX (M x K), dW (K x N) and
+    dbias (N), each skipped when None.  ``preact``: what the forward call kept,
+    or None to compute it again.  Asynchronous."""
+    _check(lib().linear_bf16_backward(
+        M, N, K, _operand(X, "X", M * K, 2), _operand(W, "W", K * N, 2),
+        _operand(bias, "bias", N, 2), _act(act), _operand(dY, "dY", M * N, 2),
+        _operand(preact, "preact", M * N, 4), _operand(dX, "dX", M * K, 2),
+        _operand(dW, "dW", K * N, 2), _operand(dbias, "dbias", N, 2), _stream(stream)),
+        "linear_bf16_backward")
+
+
+def gated_bf16(M, F, K, X, Wg, Wu, act, H, preact=None, stream=None):
+    """H <- act(X @ Wg) * (X @ Wu), bf16 with fp32 arithmetic.  X: M x K, Wg and
+    Wu: K x F, H: M x F.  ``preact`` (2 x M x F fp32) receives both products
+    for the backward call.  Asynchronous on ``stream``."""
+    _check(lib().gated_bf16(M, F, K, _operand(X, "X", M * K, 2), _operand(Wg, "Wg", K * F, 2),
+                            _operand(Wu, "Wu", K * F, 2), _act(act), _operand(H, "H", M * F, 2),
+                            _operand(preact, "preact", 2 * M * F, 4), _stream(stream)),
+           "gated_bf16")
+
+
+def gated_bf16_backward(M, F, K, X, Wg, Wu, act, dH, dX, dWg, dWu, preact=None, stream=None):
+    """Gradients of gated_bf16 for dH (M x F) into dX (M x K), dWg and dWu
+    (K x F); dX, or dWg and dWu together, may be None.  ``preact``: what the
+    forward call kept, or None to compute it again.  Asynchronous."""
+    _check(lib().gated_bf16_backward(
+        M, F, K, _operand(X, "X", M * K, 2), _operand(Wg, "Wg", K * F, 2),
+        _operand(Wu, "Wu", K * F, 2), _act(act), _operand(dH, "dH", M * F, 2),
+        _operand(preact, "preact", 2 * M * F, 4), _operand(dX, "dX", M * K, 2),
+        _operand(dWg, "dWg", K * F, 2), _operand(dWu, "dWu", K * F, 2), _stream(stream)),
+        "gated_bf16_backward")
+
+
+def xent_bf16(T, V, D, X, W, target, loss, lse, stream=None):
+    """Softmax cross entropy of logits X @ W.T over a vocabulary: X: T x D, W:
+    V x D bf16, target: T int64 (outside [0, V): the row does not count, loss
+    0); loss and lse: T fp32, either may be None.  Asynchronous."""
+    _check(lib().xent_bf16(T, V, D, _operand(X, "X", T * D, 2), _operand(W, "W", V * D, 2),
+                           _operand(target, "target", T, 8), _operand(loss, "loss", T, 4),
+                           _operand(lse, "lse", T, 4), _stream(stream)), "xent_bf16")
+
+
+def xent_bf16_grad(T, V, D, X, W, target, dloss, loss, lse, dX, dW, workspace_bytes=0,
+                   stream=None):
+    """xent_bf16 with its gradients for dloss (T fp32; None: ones) into dX
+    (T x D) and dW (V x D), either of which may be None.  ``workspace_bytes``
+    bounds the scratch for the probabilities (0: the library's choice); larger
+    ones go by in pieces of the vocabulary.  Asynchronous."""
+    _check(lib().xent_bf16_grad(
+        T, V, D, _operand(X, "X", T * D, 2), _operand(W, "W", V * D, 2),
+        _operand(target, "target", T, 8), _operand(dloss, "dloss", T, 4),
+        _operand(loss, "loss", T, 4), _operand(lse, "lse", T, 4), _operand(dX, "dX", T * D, 2),
+        _operand(dW, "dW", V * D, 2), int(workspace_bytes), _stream(stream)), "xent_bf16_grad")
 
 
 def pgemm_stage_reuse_demo(X, rows, cols, perm, out, check_reuse, delay_warp=-1, delay_ns=0,

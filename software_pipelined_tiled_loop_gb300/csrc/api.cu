@@ -19,6 +19,7 @@
 #include "pgemm.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "op_host.h"
 
 namespace pg {
 
@@ -359,10 +360,9 @@ __global__ void repack_rows_kernel(RepackJob j0, RepackJob j1, int eb) {
 }
 
 // Repack one or two operands (rows = 0: none) in a single launch.
-static cudaError_t launch_repack(const void *src0, long long sld0, void *dst0, long long dld0,
-                                 int rows0, int cols0, const void *src1, long long sld1,
-                                 void *dst1, long long dld1, int rows1, int cols1, int eb,
-                                 int sm_count, cudaStream_t s) {
+cudaError_t launch_repack(const void *src0, long long sld0, void *dst0, long long dld0, int rows0,
+                          int cols0, const void *src1, long long sld1, void *dst1, long long dld1,
+                          int rows1, int cols1, int eb, int sm_count, cudaStream_t s) {
     if (cols0 <= 0) rows0 = 0;
     if (cols1 <= 0) rows1 = 0;
     const RepackJob j0{static_cast<const uint8_t *>(src0), sld0, static_cast<uint8_t *>(dst0),
@@ -642,6 +642,33 @@ static pgemm_status gemm_impl(int M, int N, int K, Sc alpha, const In *A, const 
         e = k->launch_i8(p, stream);
     }
     return e == cudaSuccess ? PGEMM_OK : PGEMM_ERR_CUDA;
+}
+
+// ---- services for the operators (op_host.h) ----
+pgemm_status op_device(OpDevice *out) {
+    std::lock_guard<std::mutex> lock(g_mu);
+    int dev = 0;
+    DeviceState *d = nullptr;
+    const pgemm_status st = device_setup(&dev, &d);
+    if (st != PGEMM_OK) return st;
+    out->sm_count = d->sm_count;
+    out->ctx = KernelCtx{d->status, kDefaultWaitLimitNs};
+    out->pool = d->pool;
+    out->state = d;
+    return PGEMM_OK;
+}
+
+pgemm_status op_kernel_setup(const OpDevice &dev, const KernelInfo &k, int *slots) {
+    std::lock_guard<std::mutex> lock(g_mu);
+    int blocks_per_sm = 0;
+    return kernel_setup(*static_cast<DeviceState *>(dev.state), k, &blocks_per_sm, slots);
+}
+
+pgemm_status op_encode(CUtensorMap *map, OpElem type, const void *base, long long inner,
+                       long long outer, long long ld, int box_x, int box_y) {
+    const bool f32 = type == OpElem::F32;
+    return encode_2d(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                     f32 ? 4 : 2, base, inner, outer, ld, box_x, box_y, true);
 }
 
 // A block that waits, with a short limit, on an mbarrier nothing arrives on.

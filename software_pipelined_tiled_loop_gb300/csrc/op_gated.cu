@@ -1,0 +1,292 @@
+// gated_bf16: H = act(X Wg) * (X Wu), and its gradients.
+//
+// Both projections run as one product: the left half of the accumulator is
+// X Wg, the right half X Wu for the same columns, so X is read once and an
+// epilogue thread holds both values of every element it writes.
+#include "op_act.cuh"
+#include "op_gemm.cuh"
+#include "op_host.h"
+
+namespace pg {
+
+struct EpiGated {
+    uint16_t *h;
+    float *preact;  // [2][M][F]: X Wg, X Wu; or nullptr
+    long long ld;   // F
+    int act;
+    int tma_h, tma_preact;
+
+    template <class Cfg, class Wait, class Rel>
+    __device__ __forceinline__ bool run(const EpiCtx &c, const OpMaps &maps, const OpArgs &,
+                                        const OpUnit &w, uint32_t t_row, int col0, bool have,
+                                        Wait wait, Rel release) const {
+        if (!wait()) return false;
+        if (col0 >= Cfg::TILE_N) {
+            release();
+            return true;
+        }
+        const int n = w.n0 + col0;
+        uint32_t p[32];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            uint32_t g[32], u[32];
+            acc_cols32(t_row + col0 + 32 * k, have, g);
+            acc_cols32(t_row + Cfg::TILE_N + col0 + 32 * k, have, u);
+            if (k == 1) release();
+            if (preact != nullptr) {
+                put_rows32(c, tma_preact ? &maps.c[1] : nullptr, preact, ld, c.m0, n + 32 * k, g);
+                put_rows32(c, tma_preact ? &maps.c[2] : nullptr, preact + ld * c.M, ld, c.m0,
+                           n + 32 * k, u);
+            }
+            with_act(act, [&](auto A) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    p[16 * k + j] =
+                        pack_bf16(act_value<decltype(A)::value>(__uint_as_float(g[2 * j])) *
+                                      __uint_as_float(u[2 * j]),
+                                  act_value<decltype(A)::value>(__uint_as_float(g[2 * j + 1])) *
+                                      __uint_as_float(u[2 * j + 1]));
+            });
+        }
+        put_rows64(c, tma_h ? &maps.c[0] : nullptr, h, ld, n, p);
+        return true;
+    }
+};
+
+// Epilogue of the recomputing backward pass: dG = dH * U * act'(G),
+// dU = dH * act(G) from fp32 G and U, each rounded to bf16 once as an operand
+// of the gradient products.
+struct EpiGatedGrad {
+    const uint16_t *dh;
+    long long ld;  // F
+    uint16_t *dg, *du;
+    long long dz_ld;
+    int act;
+
+    template <class Cfg, class Wait, class Rel>
+    __device__ __forceinline__ bool run(const EpiCtx &c, const OpMaps &maps, const OpArgs &,
+                                        const OpUnit &w, uint32_t t_row, int col0, bool have,
+                                        Wait wait, Rel release) const {
+        if (col0 >= Cfg::TILE_N) {
+            if (!wait()) return false;
+            release();
+            return true;
+        }
+        const int n = w.n0 + col0;
+        uint32_t r[32], p[32], s[32];
+        get_rows64(c, dh, ld, n, r);
+        if (!wait()) return false;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            uint32_t g[32], u[32];
+            acc_cols32(t_row + col0 + 32 * k, have, g);
+            acc_cols32(t_row + Cfg::TILE_N + col0 + 32 * k, have, u);
+            if (k == 1) release();
+            with_act(act, [&](auto A) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const uint32_t y = r[16 * k + j];
+                    const float y0 = bf16_lo(y), y1 = bf16_hi(y);
+                    float a0, a1;
+                    const float d0 =
+                        act_value_grad<decltype(A)::value>(__uint_as_float(g[2 * j]), a0);
+                    const float d1 =
+                        act_value_grad<decltype(A)::value>(__uint_as_float(g[2 * j + 1]), a1);
+                    p[16 * k + j] = pack_bf16(y0 * d0 * __uint_as_float(u[2 * j]),
+                                              y1 * d1 * __uint_as_float(u[2 * j + 1]));
+                    s[16 * k + j] = pack_bf16(y0 * a0, y1 * a1);
+                }
+            });
+        }
+        put_rows64(c, &maps.c[0], dg, dz_ld, n, p);
+        put_rows64(c, &maps.c[1], du, dz_ld, n, s);
+        return true;
+    }
+};
+
+template <class Cfg, class Epi>
+static pgemm_status launch_dual(const OpDevice &dev, int M, int F, int K, const OpMat &X,
+                                const OpMat &Wg, const OpMat &Wu, OpMaps &maps, const Epi &e,
+                                bool after, cudaStream_t s) {
+    if (K > 0) {
+        pgemm_status st = op_encode(&maps.a[0], OpElem::BF16, X.p, K, M, X.ld, 64, 128);
+        if (st == PGEMM_OK) st = op_encode(&maps.b[0], OpElem::BF16, Wg.p, F, K, Wg.ld, 64, 64);
+        if (st == PGEMM_OK) st = op_encode(&maps.b[1], OpElem::BF16, Wu.p, F, K, Wu.ld, 64, 64);
+        if (st != PGEMM_OK) return st;
+    }
+    constexpr int TM = Cfg::BM * Cfg::CG;
+    OpArgs a{};
+    a.M = M;
+    a.N = F;
+    a.K = K;
+    a.m_tiles = (M + TM - 1) / TM;
+    a.n_seg = a.n_tiles = (F + Cfg::TILE_N - 1) / Cfg::TILE_N;
+    a.k_seg = a.k_tiles = (K + Cfg::SBK - 1) / Cfg::SBK;
+    a.parts = 1;
+    return op_launch<Cfg, Epi>(dev, maps, a, e, after, s);
+}
+
+using DualPair = OpCfg<256, 3, 2, 2, false, false, true>;
+using DualOne = OpCfg<128, 6, 1, 1, false, false, true>;
+
+template <class Epi>
+static pgemm_status launch_dual_size(const OpDevice &dev, int M, int F, int K, const OpMat &X,
+                                     const OpMat &Wg, const OpMat &Wu, OpMaps &maps, const Epi &e,
+                                     bool after, cudaStream_t s) {
+    return op_use_pair(dev, M, F, 128, 64, 1)
+               ? launch_dual<DualPair>(dev, M, F, K, X, Wg, Wu, maps, e, after, s)
+               : launch_dual<DualOne>(dev, M, F, K, X, Wg, Wu, maps, e, after, s);
+}
+
+static bool act_known(int act) { return act >= PGEMM_ACT_NONE && act <= PGEMM_ACT_SILU; }
+
+static pgemm_status gated_forward(int M, int F, int K, const uint16_t *X, const uint16_t *Wg,
+                                  const uint16_t *Wu, int act, uint16_t *H, float *preact,
+                                  cudaStream_t s) {
+    if (M < 0 || F < 0 || K < 0 || !act_known(act)) return PGEMM_ERR_INVALID_VALUE;
+    if (M == 0 || F == 0) return PGEMM_OK;
+    if (!H || (K > 0 && (!X || !Wg || !Wu))) return PGEMM_ERR_INVALID_VALUE;
+    if (!op_aligned16(X) || !op_aligned16(Wg) || !op_aligned16(Wu) || !op_aligned16(H) ||
+        !op_aligned16(preact))
+        return PGEMM_ERR_MISALIGNED;
+    OpDevice dev;
+    pgemm_status st = op_device(&dev);
+    if (st != PGEMM_OK) return st;
+    OpArena arena(dev, s);
+    OpRelayout rl;
+    OpMat x, wg, wu;
+    if (K > 0) {
+        rl.add(&x, X, M, K, arena);
+        rl.add(&wg, Wg, K, F, arena);
+        rl.add(&wu, Wu, K, F, arena);
+    }
+    if ((st = arena.alloc()) != PGEMM_OK) return st;
+    if ((st = rl.run(dev, arena, s)) != PGEMM_OK) return st;
+    OpMaps maps{};
+    EpiGated e{H, preact, F, act, F % 8 == 0, preact != nullptr && F % 4 == 0};
+    if (e.tma_h) st = op_encode(&maps.c[0], OpElem::BF16, H, F, M, F, 64, 32);
+    if (e.tma_preact) {
+        if (st == PGEMM_OK) st = op_encode(&maps.c[1], OpElem::F32, preact, F, M, F, 32, 32);
+        if (st == PGEMM_OK)
+            st = op_encode(&maps.c[2], OpElem::F32, preact + static_cast<long long>(M) * F, F, M,
+                           F, 32, 32);
+    }
+    if (st != PGEMM_OK) return st;
+    return launch_dual_size(dev, M, F, K, x, wg, wu, maps, e, rl.any(), s);
+}
+
+static pgemm_status gated_backward(int M, int F, int K, const uint16_t *X, const uint16_t *Wg,
+                                   const uint16_t *Wu, int act, const uint16_t *dH,
+                                   const float *preact, uint16_t *dX, uint16_t *dWg,
+                                   uint16_t *dWu, cudaStream_t s) {
+    if (M < 0 || F < 0 || K < 0 || !act_known(act)) return PGEMM_ERR_INVALID_VALUE;
+    if ((dWg == nullptr) != (dWu == nullptr)) return PGEMM_ERR_INVALID_VALUE;
+    const bool want_x = dX && M > 0 && K > 0, want_w = dWg && K > 0 && F > 0;
+    if (!want_x && !want_w) return PGEMM_OK;  // K > 0 from here on
+    const bool some = M > 0 && F > 0;
+    if (some && (!dH || !Wg || !Wu || !X)) return PGEMM_ERR_INVALID_VALUE;
+    if (!op_aligned16(X) || !op_aligned16(Wg) || !op_aligned16(Wu) || !op_aligned16(dH) ||
+        !op_aligned16(preact) || !op_aligned16(dX) || !op_aligned16(dWg) || !op_aligned16(dWu))
+        return PGEMM_ERR_MISALIGNED;
+    OpDevice dev;
+    pgemm_status st = op_device(&dev);
+    if (st != PGEMM_OK) return st;
+    OpArena arena(dev, s);
+    OpRelayout rl;
+    OpMat x, wg, wu, dg, du;
+    long long dg_at = 0, du_at = 0;
+    if (some) {
+        rl.add(&x, X, M, K, arena);
+        rl.add(&wg, Wg, K, F, arena);
+        rl.add(&wu, Wu, K, F, arena);
+        dg.ld = du.ld = op_round_up(F, 64);
+        dg_at = arena.add(dg.ld * M * 2);
+        du_at = arena.add(du.ld * M * 2);
+    }
+    if ((st = arena.alloc()) != PGEMM_OK) return st;
+    if ((st = rl.run(dev, arena, s)) != PGEMM_OK) return st;
+    bool after = rl.any();
+    if (some) {
+        uint16_t *dg_buf = arena.at<uint16_t>(dg_at), *du_buf = arena.at<uint16_t>(du_at);
+        dg.p = dg_buf;
+        du.p = du_buf;
+        if (preact) {
+            OpActGrad g;
+            g.M = M;
+            g.N = F;
+            g.act = act;
+            g.z = preact;
+            g.u = preact + static_cast<long long>(M) * F;
+            g.dy = dH;
+            g.dy_ld = F;
+            g.dz = dg_buf;
+            g.du = du_buf;
+            g.dz_ld = dg.ld;
+            st = op_act_grad(dev, g, after, s);
+        } else {
+            OpMaps maps{};
+            EpiGatedGrad e{dH, F, dg_buf, du_buf, dg.ld, act};
+            st = op_encode(&maps.c[0], OpElem::BF16, dg_buf, F, M, dg.ld, 64, 32);
+            if (st == PGEMM_OK)
+                st = op_encode(&maps.c[1], OpElem::BF16, du_buf, F, M, du.ld, 64, 32);
+            if (st == PGEMM_OK)
+                st = launch_dual_size(dev, M, F, K, x, wg, wu, maps, e, after, s);
+        }
+        if (st != PGEMM_OK) return st;
+        after = true;
+    }
+    if (want_x) {
+        OpProduct p;
+        p.form = OpForm::NT;
+        p.M = M;
+        p.N = K;
+        p.K = F;
+        p.k_segments = 2;
+        p.A[0] = dg;
+        p.A[1] = du;
+        p.B[0] = wg;
+        p.B[1] = wu;
+        p.out[0] = dX;
+        p.after = after;
+        if ((st = op_product(dev, p, s)) != PGEMM_OK) return st;
+        after = true;
+    }
+    if (want_w) {
+        OpProduct p;
+        p.form = OpForm::TN;
+        p.M = K;
+        p.N = F;
+        p.K = M;
+        p.n_segments = 2;
+        p.A[0] = x;
+        p.B[0] = dg;
+        p.B[1] = du;
+        p.out[0] = dWg;
+        p.out[1] = dWu;
+        p.after = after;
+        if ((st = op_product(dev, p, s)) != PGEMM_OK) return st;
+    }
+    return PGEMM_OK;
+}
+
+}  // namespace pg
+
+extern "C" {
+
+pgemm_status gated_bf16(int M, int F, int K, const uint16_t *X, const uint16_t *Wg,
+                        const uint16_t *Wu, int act, uint16_t *H, float *preact,
+                        pgemm_stream_t stream) {
+    return pg::op_guard(
+        [&] { return pg::gated_forward(M, F, K, X, Wg, Wu, act, H, preact, stream); });
+}
+
+pgemm_status gated_bf16_backward(int M, int F, int K, const uint16_t *X, const uint16_t *Wg,
+                                 const uint16_t *Wu, int act, const uint16_t *dH,
+                                 const float *preact, uint16_t *dX, uint16_t *dWg, uint16_t *dWu,
+                                 pgemm_stream_t stream) {
+    return pg::op_guard([&] {
+        return pg::gated_backward(M, F, K, X, Wg, Wu, act, dH, preact, dX, dWg, dWu, stream);
+    });
+}
+
+}  // extern "C"

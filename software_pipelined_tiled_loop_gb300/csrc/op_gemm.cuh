@@ -1,0 +1,629 @@
+// Tensor-core product of the operators (linear, gated, cross entropy): the
+// pipelined tcgen05 kernel of tc_gemm.cuh with what those products need on
+// top of it -- operands in either major order, two operand pairs summed along
+// K or set side by side along N, a K range split into parts, and an epilogue
+// given as a type.
+//
+//   warp 0 (one lane)  producer: TMA copies of the A and B panels into an
+//                      S-stage ring (full / empty mbarriers).
+//   warp 1 (one lane)  MMA issuer: tcgen05.mma kind::f16 (bf16 operands, fp32
+//                      accumulators in tensor memory, two of them, so that a
+//                      unit's epilogue overlaps the next unit's main loop).
+//   warps 2..9         epilogue: two warps for each TMEM lane quadrant, each
+//                      half of the accumulator's columns.  A thread holds a
+//                      whole row segment, so row statistics need no shuffles.
+//
+// Operand layouts in shared memory, all with TMA's 128-byte swizzle:
+//   A K-major   (stored M x K): box 64 k x 128 rows; 8-row groups 1024 B
+//               apart; K = 16 -> + 32 B.
+//   A M-major   (stored K x M): two boxes of 64 m x 64 k-rows; 8-k-row groups
+//               1024 B apart, the 64-column blocks 8192 B; K = 16 -> + 2048 B.
+//   B N-major   (stored K x N): boxes of 64 n x 64 k-rows, as A M-major.
+//   B K-major   (stored N x K): one box 64 k x columns, as A K-major.
+// With a CTA pair (CG = 2) each CTA holds its 128 rows of A and half of B's
+// columns; the pair computes a 256-row tile with one M = 256 MMA.
+//
+// DUAL: the accumulator's left half is A * B0 and its right half A * B1 for
+// the same columns of two matrices, so that one epilogue thread holds both
+// products of an output element (the gate and the value of a gated block).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "op_host.h"
+#include "ptx.cuh"
+
+namespace pg {
+
+struct OpMaps {
+    CUtensorMap a[2], b[2], c[3];
+};
+
+// The schedule of one launch.  Units are (part, tile) pairs, all tiles of
+// part 0 first; part p of P covers K-tiles [p T / P, (p + 1) T / P).
+struct OpArgs {
+    int M, N;          // extents of one output (N: of one segment along N)
+    int K;             // columns of one K segment
+    int m_tiles;       // of BM * CG rows
+    int n_tiles;       // over all N segments
+    int n_seg;         // tiles of one N segment; tiles from n_seg on read b[1], write c[1]
+    int k_tiles;       // over all K segments
+    int k_seg;         // K-tiles of one K segment; from k_seg on a[1], b[1]
+    int parts;
+    int group_m;
+};
+
+template <int BN_, int STAGES_, int KSUB_, int CG_, bool A_MN_, bool B_K_, bool DUAL_ = false>
+struct OpCfg {
+    static constexpr int BM = 128, BN = BN_, BK = 64, STAGES = STAGES_, KSUB = KSUB_, CG = CG_;
+    static constexpr bool A_MN = A_MN_, B_K = B_K_, DUAL = DUAL_;
+    static constexpr int SBK = BK * KSUB;
+    static constexpr int B_COLS = BN / CG;          // B columns this CTA loads and holds
+    static constexpr int TILE_N = DUAL ? BN / 2 : BN;  // output columns of a tile
+    static constexpr int A_SUB = BM * BK * 2, B_SUB = B_COLS * BK * 2;
+    static constexpr int A_BYTES = A_SUB * KSUB, B_BYTES = B_SUB * KSUB;
+    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+    static constexpr int TX_BYTES = STAGE_BYTES * CG;
+    static constexpr int EPI = 8;
+    static constexpr int EPI_COLS = BN / 2;         // accumulator columns of an epilogue warp
+    static constexpr int STAGING_BYTES = EPI * 4096;
+    static constexpr int TMEM_COLS = 2 * BN;
+    static constexpr int THREADS = 64 + 32 * EPI;
+    static constexpr int STAGING_OFFSET = STAGES * STAGE_BYTES;
+    static constexpr int BAR_OFFSET = STAGING_OFFSET + STAGING_BYTES;
+    static constexpr int USED = BAR_OFFSET + (2 * STAGES + 5) * 8 + 16;
+    static constexpr int SMEM_BYTES = smem_request(USED + 1024, 1);  // one block per SM
+    static_assert(USED + 1024 <= 232448, "shared memory");
+    static_assert(BN == 128 || BN == 256, "BN");
+    static_assert(CG == 1 || (CG == 2 && BN == 256), "a pair computes 256 x 256 tiles");
+    static_assert(!DUAL || !B_K, "the two B matrices of a dual product are N-major");
+};
+
+// ------------------------------------------------------- epilogue helpers ---
+// Where one epilogue warp works: 32 rows from m0, its staging buffer, the
+// extents it may touch.
+struct EpiCtx {
+    uint8_t *buf;   // 4 KB of shared memory, 1024-byte aligned
+    int m0;         // first of the warp's 32 rows (may lie beyond M)
+    int M, N;
+    uint32_t lane;
+    __device__ __forceinline__ int row() const { return m0 + static_cast<int>(lane); }
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float bf16_lo(uint32_t p) { return __uint_as_float(p << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
+
+// Store 32 rows x 64 columns of 16-bit values, lane t's row in p[32] (pairs).
+// map != nullptr: one TMA store (clips at the edges); else coalesced 2-byte
+// stores, for pitches TMA cannot describe.
+__device__ __forceinline__ void put_rows64(const EpiCtx &c, const CUtensorMap *map, uint16_t *out,
+                                           long long ld, int col, const uint32_t (&p)[32]) {
+    if (c.m0 >= c.M || col >= c.N) return;
+    const uint32_t sbuf = smem_u32(c.buf);
+    if (c.lane == 0) bulk_wait_read<0>();  // the store that last used the buffer
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        sts128(sbuf + c.lane * 128 + ((j ^ (c.lane & 7)) << 4), p[4 * j], p[4 * j + 1],
+               p[4 * j + 2], p[4 * j + 3]);
+    if (map != nullptr) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (c.lane == 0) {
+            tma_store_2d(map, c.buf, col, c.m0);
+            bulk_commit();
+        }
+    } else {
+        __syncwarp();
+        const int rows = min(32, c.M - c.m0);
+        for (int h = 0; h < 2; ++h) {
+            const int cc = static_cast<int>(c.lane) + 32 * h;
+            if (col + cc < c.N) {
+                uint16_t *o = out + static_cast<long long>(c.m0) * ld + col + cc;
+#pragma unroll 4
+                for (int r = 0; r < rows; ++r, o += ld)
+                    *o = *reinterpret_cast<const uint16_t *>(
+                        c.buf + r * 128 + (((cc >> 3) ^ (r & 7)) << 4) + (cc & 7) * 2);
+            }
+        }
+        __syncwarp();
+    }
+}
+
+// The same for 32 rows x 32 columns of 32-bit values, v[32] lane t's row.
+__device__ __forceinline__ void put_rows32(const EpiCtx &c, const CUtensorMap *map, float *out,
+                                           long long ld, int row0, int col,
+                                           const uint32_t (&v)[32]) {
+    if (c.m0 >= c.M || col >= c.N) return;
+    const uint32_t sbuf = smem_u32(c.buf);
+    if (c.lane == 0) bulk_wait_read<0>();
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        sts128(sbuf + c.lane * 128 + ((j ^ (c.lane & 7)) << 4), v[4 * j], v[4 * j + 1],
+               v[4 * j + 2], v[4 * j + 3]);
+    if (map != nullptr) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (c.lane == 0) {
+            tma_store_2d(map, c.buf, col, row0);
+            bulk_commit();
+        }
+    } else {
+        __syncwarp();
+        const int rows = min(32, c.M - c.m0);
+        const int cc = static_cast<int>(c.lane);
+        if (col + cc < c.N) {
+            float *o = out + static_cast<long long>(row0) * ld + col + cc;
+#pragma unroll 4
+            for (int r = 0; r < rows; ++r, o += ld)
+                *o = __uint_as_float(lds32(sbuf + r * 128 + (((cc >> 2) ^ (r & 7)) << 4) +
+                                           (cc & 3) * 4));
+        }
+        __syncwarp();
+    }
+}
+
+// Read 32 rows x 64 columns of bf16, lane t's row into p[32] (zero outside).
+// Rows of 16-byte pitch are read by each lane as 16-byte vectors of its own
+// row; other pitches by coalesced 2-byte loads through the staging buffer.
+__device__ __forceinline__ void get_rows64(const EpiCtx &c, const uint16_t *in, long long ld,
+                                           int col, uint32_t (&p)[32]) {
+    const bool vec = (ld & 7) == 0;
+    if (vec) {
+        const bool row_in = c.row() < c.M;
+        const uint16_t *src = in + static_cast<long long>(c.row()) * ld + col;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            uint4 x = make_uint4(0u, 0u, 0u, 0u);
+            // pitches here are the row lengths rounded up to 8 at least, so a
+            // vector that starts inside a row may be read whole
+            if (row_in && col + 8 * j < c.N) x = *reinterpret_cast<const uint4 *>(src + 8 * j);
+            p[4 * j] = x.x;
+            p[4 * j + 1] = x.y;
+            p[4 * j + 2] = x.z;
+            p[4 * j + 3] = x.w;
+        }
+    } else {
+        const uint32_t sbuf = smem_u32(c.buf);
+        if (c.lane == 0) bulk_wait_read<0>();
+        __syncwarp();
+        const int rows = max(0, min(32, c.M - c.m0));
+        for (int h = 0; h < 2; ++h) {
+            const int cc = static_cast<int>(c.lane) + 32 * h;
+            const uint16_t *src = in + static_cast<long long>(c.m0) * ld + col + cc;
+#pragma unroll 8
+            for (int r = 0; r < 32; ++r) {
+                uint16_t x = 0;
+                if (r < rows && col + cc < c.N) x = src[static_cast<long long>(r) * ld];
+                *reinterpret_cast<uint16_t *>(c.buf + r * 128 + (((cc >> 3) ^ (r & 7)) << 4) +
+                                              (cc & 7) * 2) = x;
+            }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint4 x = lds_u4(sbuf + c.lane * 128 + ((j ^ (c.lane & 7)) << 4));
+            p[4 * j] = x.x;
+            p[4 * j + 1] = x.y;
+            p[4 * j + 2] = x.z;
+            p[4 * j + 3] = x.w;
+        }
+        __syncwarp();
+    }
+}
+
+// 32 values of a bf16 vector from index col (zero beyond n), the same in
+// every lane.  The vector's base is 16-byte aligned and col a multiple of 32.
+__device__ __forceinline__ void get_vec32(const uint16_t *v, int n, int col, float (&f)[32]) {
+    if (col + 32 <= n) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(v + col) + j);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f[8 * j + 2 * i] = bf16_lo(w[i]);
+                f[8 * j + 2 * i + 1] = bf16_hi(w[i]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            f[j] = col + j < n ? __uint_as_float(static_cast<uint32_t>(v[col + j]) << 16) : 0.0f;
+    }
+}
+
+// One unit as its epilogue sees it.
+struct OpUnit {
+    int tile, part, seg;  // seg: N segment (output c[seg])
+    int m0, n0;           // of the cluster's tile
+    int kb, ke;
+};
+
+template <class Cfg>
+__device__ __forceinline__ OpUnit op_unit(const OpArgs &a, int tiles, int u) {
+    OpUnit w;
+    w.part = u / tiles;
+    w.tile = u - w.part * tiles;
+    const int per_group = a.group_m * a.n_tiles;
+    const int g = w.tile / per_group;
+    const int first_m = g * a.group_m;
+    const int gm = min(a.m_tiles - first_m, a.group_m);
+    const int r = w.tile - g * per_group;
+    const int nt = r / gm;
+    w.m0 = (first_m + r % gm) * (Cfg::BM * Cfg::CG);
+    w.seg = nt >= a.n_seg ? 1 : 0;
+    w.n0 = (nt - w.seg * a.n_seg) * Cfg::TILE_N;
+    w.kb = static_cast<int>(static_cast<long long>(w.part) * a.k_tiles / a.parts);
+    w.ke = static_cast<int>(static_cast<long long>(w.part + 1) * a.k_tiles / a.parts);
+    return w;
+}
+
+// Epi: a struct of kernel parameters with
+//   template <class Cfg, ...> __device__ bool run(const EpiCtx &, const OpMaps &,
+//        const OpArgs &, const OpUnit &, uint32_t t_row, int col0, bool have,
+//        Wait wait, Release release) const
+// called by a whole warp for its 32 rows and the accumulator columns
+// [col0, col0 + EPI_COLS) (DUAL: the output columns [col0, col0 + 64) of both
+// halves, none when col0 >= TILE_N); t_row addresses the accumulator's first
+// column in the warp's lanes.  wait() blocks until the accumulator is complete
+// (false: the wait ran out, run returns false at once); release() hands it
+// back.  Each is called exactly once, in this order, around all reads.
+// have = false (an empty K range): the accumulator is not to be read and
+// counts as zero.
+template <class Cfg, class Epi>
+__global__ void __launch_bounds__(Cfg::THREADS, 1)
+    op_gemm_kernel(const __grid_constant__ OpMaps maps, const OpArgs args,
+                   const __grid_constant__ Epi epi, const KernelCtx ctx) {
+    constexpr int BM = Cfg::BM, BN = Cfg::BN, BK = Cfg::BK, STAGES = Cfg::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = align_1024(smem_raw);
+    uint8_t *sA = smem;
+    uint8_t *sB = smem + STAGES * Cfg::A_BYTES;
+    uint8_t *sStage = smem + Cfg::STAGING_OFFSET;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + Cfg::BAR_OFFSET);
+    uint64_t *empty = full + STAGES;
+    uint64_t *acc_full = empty + STAGES;  // [2]
+    uint64_t *acc_empty = acc_full + 2;   // [2]
+    uint64_t *mma_done = acc_empty + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
+
+    const uint32_t warp = warp_id_uniform();
+    const uint32_t lane = lane_id();
+    if (warp == 0 && lane == 0) {
+        if (args.k_tiles > 0) {
+            prefetch_tmap(&maps.a[0]);
+            prefetch_tmap(&maps.b[0]);
+        }
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], Cfg::EPI * Cfg::CG);
+        }
+        mbar_init(mma_done, 1);
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        if constexpr (Cfg::CG == 2) {
+            tmem_alloc_pair(tmem_slot, Cfg::TMEM_COLS);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(tmem_slot, Cfg::TMEM_COLS);
+            tmem_relinquish();
+        }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if constexpr (Cfg::CG == 2)
+        cluster_sync();
+    else
+        __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    // on-chip set-up is done; what follows may read what the kernel before wrote
+    grid_dependency_wait();
+
+    const int crank = Cfg::CG == 2 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int slot = static_cast<int>(blockIdx.x) / Cfg::CG;
+    const int slots = static_cast<int>(gridDim.x) / Cfg::CG;
+    const int tiles = args.m_tiles * args.n_tiles;
+    const int units = tiles * args.parts;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---------------- producer ----------------
+            uint32_t it = 0;
+            bool ok = true;
+            for (int u = slot; ok && u < units; u += slots) {
+                const OpUnit w = op_unit<Cfg>(args, tiles, u);
+                const int m0 = w.m0 + crank * BM;
+                for (int kt = w.kb; kt < w.ke; ++kt, ++it) {
+                    const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
+                    if (!mbar_wait(&empty[s], ph ^ 1u, ctx, kSiteProducerEmpty)) {
+                        ok = false;
+                        break;
+                    }
+                    const int ks = kt >= args.k_seg ? 1 : 0;
+                    const CUtensorMap *ma = &maps.a[ks];
+                    const uint32_t full_lead =
+                        Cfg::CG == 2 ? mapa_shared(smem_u32(&full[s]), 0) : smem_u32(&full[s]);
+                    if (crank == 0) mbar_arrive_expect_tx(&full[s], Cfg::TX_BYTES);
+                    auto load = [&](uint8_t *dst, const CUtensorMap *map, int x, int y) {
+                        if constexpr (Cfg::CG == 2)
+                            tma_load_2d_pair(dst, map, full_lead, x, y);
+                        else
+                            tma_load_2d(dst, map, &full[s], x, y);
+                    };
+#pragma unroll
+                    for (int q = 0; q < Cfg::KSUB; ++q) {
+                        const int k0 = (kt - ks * args.k_seg) * Cfg::SBK + q * BK;
+                        uint8_t *da = sA + s * Cfg::A_BYTES + q * Cfg::A_SUB;
+                        uint8_t *db = sB + s * Cfg::B_BYTES + q * Cfg::B_SUB;
+                        if constexpr (Cfg::A_MN) {
+#pragma unroll
+                            for (int j = 0; j < BM / 64; ++j)
+                                load(da + j * (BK * 128), ma, m0 + 64 * j, k0);
+                        } else {
+                            load(da, ma, k0, m0);
+                        }
+                        if constexpr (Cfg::DUAL) {
+                            // half h of the accumulator reads columns of b[h]; a
+                            // pair's CTA h holds exactly that half
+#pragma unroll
+                            for (int j = 0; j < Cfg::B_COLS / 64; ++j) {
+                                const int cb = crank * Cfg::B_COLS + 64 * j;  // accumulator column
+                                const int h = cb / Cfg::TILE_N;
+                                load(db + j * (BK * 128), &maps.b[h], w.n0 + cb - h * Cfg::TILE_N,
+                                     k0);
+                            }
+                        } else {
+                            const int nb = w.n0 + crank * Cfg::B_COLS;
+                            const CUtensorMap *mb = &maps.b[ks | w.seg];
+                            if constexpr (Cfg::B_K) {
+                                load(db, mb, k0, nb);
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < Cfg::B_COLS / 64; ++j)
+                                    load(db + j * (BK * 128), mb, nb + 64 * j, k0);
+                            }
+                        }
+                    }
+                }
+            }
+            if constexpr (Cfg::CG == 2) {
+                // the pair's last multicast releases of this CTA's barriers must
+                // have landed before the cluster is left
+                for (int i = 0; ok && i < STAGES; ++i, ++it) {
+                    const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
+                    ok = mbar_wait(&empty[s], ph ^ 1u, ctx, kSiteProducerEmpty);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && crank == 0) {
+            // ---------------- MMA issuer ----------------
+            constexpr uint32_t idesc = idesc_f16(BM * Cfg::CG, BN, 1, Cfg::A_MN ? 1 : 0,
+                                                 Cfg::B_K ? 0 : 1);
+            constexpr uint16_t kPair = 3;
+            uint32_t it = 0, gr = 0;
+            bool ok = true;
+            for (int u = slot; ok && u < units; u += slots) {
+                const OpUnit w = op_unit<Cfg>(args, tiles, u);
+                if (w.ke <= w.kb) continue;
+                const uint32_t ab = gr & 1u, aph = (gr >> 1) & 1u;
+                ++gr;
+                if (!mbar_wait(&acc_empty[ab], aph ^ 1u, ctx, kSiteMmaAccEmpty)) break;
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + ab * BN;
+                for (int kt = w.kb; kt < w.ke; ++kt, ++it) {
+                    const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
+                    if (!mbar_wait(&full[s], ph, ctx, kSiteMmaFull)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const int kk = kt >= args.k_seg ? kt - args.k_seg : kt;
+#pragma unroll
+                    for (int q = 0; q < Cfg::KSUB; ++q) {
+                        // a sub-tile wholly beyond K holds only zero fill
+                        if (q > 0 && kk * Cfg::SBK + q * BK >= args.K) break;
+                        const uint32_t a_addr = smem_u32(sA + s * Cfg::A_BYTES + q * Cfg::A_SUB);
+                        const uint32_t b_addr = smem_u32(sB + s * Cfg::B_BYTES + q * Cfg::B_SUB);
+#pragma unroll
+                        for (int k = 0; k < BK / 16; ++k) {
+                            const uint64_t ad =
+                                Cfg::A_MN ? smem_desc_sw128(a_addr + k * 2048, BK * 128, 1024)
+                                          : smem_desc_sw128(a_addr + k * 32, 16, 1024);
+                            const uint64_t bd =
+                                Cfg::B_K ? smem_desc_sw128(b_addr + k * 32, 16, 1024)
+                                         : smem_desc_sw128(b_addr + k * 2048, BK * 128, 1024);
+                            const uint32_t acc = (kt == w.kb && q == 0 && k == 0) ? 0u : 1u;
+                            if constexpr (Cfg::CG == 2)
+                                umma_f16_ss_pair(d_tmem, ad, bd, idesc, acc);
+                            else
+                                umma_f16_ss(d_tmem, ad, bd, idesc, acc);
+                        }
+                    }
+                    if constexpr (Cfg::CG == 2)
+                        umma_commit_pair_multicast(&empty[s], kPair);
+                    else
+                        umma_commit(&empty[s]);
+                }
+                if (ok) {
+                    if constexpr (Cfg::CG == 2)
+                        umma_commit_pair_multicast(&acc_full[ab], kPair);
+                    else
+                        umma_commit(&acc_full[ab]);
+                }
+            }
+            if constexpr (Cfg::CG == 2)
+                umma_commit_pair_multicast(mma_done, 1);
+            else
+                umma_commit(mma_done);
+            mbar_wait(mma_done, 0, ctx, kSiteMmaDone);
+        }
+    } else {
+        // ---------------- epilogue warps ----------------
+        const uint32_t e = warp - 2;
+        const uint32_t q = warp & 3u;  // the TMEM lane quadrant this warp may read
+        // DUAL: 64 output columns a warp (a 128-byte row of bf16), so with 64-wide
+        // tiles the warps e >= 4 only pass the accumulator on
+        const int col0 = static_cast<int>(e >> 2) * (Cfg::DUAL ? 64 : Cfg::EPI_COLS);
+        EpiCtx c;
+        c.buf = sStage + e * 4096;
+        c.M = args.M;
+        c.N = args.N;
+        c.lane = lane;
+        uint32_t gr = 0;
+        for (int u = slot; u < units; u += slots) {
+            const OpUnit w = op_unit<Cfg>(args, tiles, u);
+            const bool have = w.ke > w.kb;
+            const uint32_t ab = gr & 1u, aph = (gr >> 1) & 1u;
+            c.m0 = w.m0 + crank * BM + static_cast<int>(q * 32);
+            auto wait = [&]() -> bool {
+                if (!have) return true;
+                const bool ok = mbar_wait(&acc_full[ab], aph, ctx, kSiteEpilogueFull);
+                tc_fence_after();
+                return ok;
+            };
+            auto release = [&]() {
+                if (!have) return;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (Cfg::CG == 2)
+                        mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[ab]), 0));
+                    else
+                        mbar_arrive(&acc_empty[ab]);
+                }
+            };
+            const uint32_t t_row = tmem_base + ((q * 32u) << 16) + ab * BN;
+            if (!epi.template run<Cfg>(c, maps, args, w, t_row, col0, have, wait, release)) break;
+            if (have) ++gr;
+        }
+        if (lane == 0) bulk_wait_all();  // this warp's stores have landed
+        __syncwarp();
+    }
+
+    // ---------------- teardown ----------------
+    tc_fence_before();
+    __syncwarp();
+    if constexpr (Cfg::CG == 2)
+        cluster_sync();
+    else
+        __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        if constexpr (Cfg::CG == 2)
+            tmem_dealloc_pair(tmem_base, Cfg::TMEM_COLS);
+        else
+            tmem_dealloc(tmem_base, Cfg::TMEM_COLS);
+    }
+}
+
+// Read 32 accumulator columns (zeros when there is no accumulator).
+__device__ __forceinline__ void acc_cols32(uint32_t taddr, bool have, uint32_t (&v)[32]) {
+    if (have) {
+        tmem_ld_32x32b_x32(taddr, v);
+        tmem_ld_wait();
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = 0u;
+    }
+}
+
+// ------------------------------------------------------------------- host ---
+// Schedule slots: one block (or pair) per SM.
+template <class Cfg, class Epi>
+static cudaError_t op_slots(const LaunchCommon &p, int *slots) {
+    if constexpr (Cfg::CG == 1) {
+        *slots = p.sm_count;
+        return cudaSuccess;
+    } else {
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = Cfg::CG;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cudaLaunchConfig_t lc{};
+        lc.blockDim = dim3(Cfg::THREADS);
+        lc.dynamicSmemBytes = Cfg::SMEM_BYTES;
+        lc.gridDim = dim3(Cfg::CG * p.sm_count);
+        lc.attrs = attr;
+        lc.numAttrs = 1;
+        int clusters = 0;
+        cudaError_t e = cudaOccupancyMaxActiveClusters(&clusters, op_gemm_kernel<Cfg, Epi>, &lc);
+        if (e != cudaSuccess) return e;
+        if (clusters < 1) return cudaErrorInvalidConfiguration;
+        *slots = clusters;
+        return cudaSuccess;
+    }
+}
+
+template <class Cfg, class Epi>
+static KernelInfo op_info() {
+    KernelInfo k;
+    k.threads = Cfg::THREADS;
+    k.smem_bytes = Cfg::SMEM_BYTES;
+    k.schedule_slots = op_slots<Cfg, Epi>;
+    k.func = reinterpret_cast<const void *>(op_gemm_kernel<Cfg, Epi>);
+    return k;
+}
+
+// Sets the kernel up on the device (once), then launches it on `stream`.
+// `after`: it follows another kernel of the same call, whose results it reads
+// after grid_dependency_wait, so its prologue may overlap that kernel's tail.
+template <class Cfg, class Epi>
+static pgemm_status op_launch(const OpDevice &dev, const OpMaps &maps, OpArgs a, const Epi &epi,
+                              bool after, cudaStream_t stream) {
+    static const KernelInfo info = op_info<Cfg, Epi>();
+    int slots = 0;
+    const pgemm_status st = op_kernel_setup(dev, info, &slots);
+    if (st != PGEMM_OK) return st;
+    const long long units = static_cast<long long>(a.m_tiles) * a.n_tiles * a.parts;
+    if (units < 1) return PGEMM_OK;
+    if (units > 0x7fffffffll) return PGEMM_ERR_INVALID_VALUE;
+    // Raster groups: down group_m tile rows, then one tile column across, so
+    // that the blocks running at once share panels of A and B through L2 (the
+    // same widths as the plain products: 16 up to K = 4096, else 8).
+    a.group_m = static_cast<long long>(a.k_tiles) * Cfg::SBK / a.parts <= 4096 ? 16 : 8;
+    cudaLaunchAttribute attr[2];
+    int nattr = 0;
+    if (after) {
+        attr[nattr].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[nattr].val.programmaticStreamSerializationAllowed = 1;
+        ++nattr;
+    }
+    if constexpr (Cfg::CG == 2) {
+        attr[nattr].id = cudaLaunchAttributeClusterDimension;
+        attr[nattr].val.clusterDim.x = Cfg::CG;
+        attr[nattr].val.clusterDim.y = 1;
+        attr[nattr].val.clusterDim.z = 1;
+        ++nattr;
+    }
+    cudaLaunchConfig_t lc{};
+    lc.blockDim = dim3(Cfg::THREADS);
+    lc.gridDim = dim3(Cfg::CG * static_cast<int>(units < slots ? units : slots));
+    lc.dynamicSmemBytes = Cfg::SMEM_BYTES;
+    lc.stream = stream;
+    lc.attrs = attr;
+    lc.numAttrs = nattr;
+    return cudaLaunchKernelEx(&lc, op_gemm_kernel<Cfg, Epi>, maps, a, epi, dev.ctx) == cudaSuccess
+               ? PGEMM_OK
+               : PGEMM_ERR_CUDA;
+}
+
+}  // namespace pg

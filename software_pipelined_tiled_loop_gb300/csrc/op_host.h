@@ -1,0 +1,183 @@
+// Host-side services shared by the operators' dispatch (op_*.cu): the device
+// set-up and scratch pool of the library, tensor maps, operand relayout and
+// the generic product with its split-K join.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kernels.h"
+#include "pgemm.h"
+
+namespace pg {
+
+// The current device as the operators need it (api.cu sets it up once).
+struct OpDevice {
+    int sm_count = 0;
+    KernelCtx ctx{};
+    cudaMemPool_t pool = nullptr;
+    void *state = nullptr;  // the library's record of the device
+};
+
+pgemm_status op_device(OpDevice *out);  // the current device, set up
+// One-time set-up of a kernel (shared-memory attributes, schedule slots).
+pgemm_status op_kernel_setup(const OpDevice &dev, const KernelInfo &k, int *slots);
+// A 2-D tensor map of 16- or 32-bit elements: `inner` x `outer` with row pitch
+// `ld` (elements), boxes of box_x x box_y with the 128-byte swizzle.
+enum class OpElem { BF16, F32 };
+pgemm_status op_encode(CUtensorMap *map, OpElem type, const void *base, long long inner,
+                       long long outer, long long ld, int box_x, int box_y);
+cudaError_t launch_repack(const void *src0, long long sld0, void *dst0, long long dld0, int rows0,
+                          int cols0, const void *src1, long long sld1, void *dst1, long long dld1,
+                          int rows1, int cols1, int eb, int sm_count, cudaStream_t s);
+
+inline long long op_round_up(long long v, long long m) { return (v + m - 1) / m * m; }
+inline bool op_aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Stream-ordered scratch of one call: sizes are added first, allocated in one
+// piece from the library's pool, and given back on the stream when the call
+// returns.
+class OpArena {
+  public:
+    explicit OpArena(const OpDevice &d, cudaStream_t s) : dev_(d), stream_(s) {}
+    OpArena(const OpArena &) = delete;
+    OpArena &operator=(const OpArena &) = delete;
+    ~OpArena() {
+        if (base_) cudaFreeAsync(base_, stream_);
+    }
+    // bytes rounded up so that every part starts on a 1024-byte boundary
+    long long add(long long bytes) {
+        const long long at = total_;
+        total_ += op_round_up(bytes > 0 ? bytes : 0, 1024);
+        return at;
+    }
+    pgemm_status alloc() {
+        if (total_ == 0) return PGEMM_OK;
+        return cudaMallocFromPoolAsync(&base_, static_cast<size_t>(total_), dev_.pool, stream_) ==
+                       cudaSuccess
+                   ? PGEMM_OK
+                   : PGEMM_ERR_CUDA;
+    }
+    template <class T>
+    T *at(long long offset) const {
+        return reinterpret_cast<T *>(static_cast<uint8_t *>(base_) + offset);
+    }
+
+  private:
+    const OpDevice &dev_;
+    cudaStream_t stream_;
+    void *base_ = nullptr;
+    long long total_ = 0;
+};
+
+// A bf16 matrix as a product reads it: rows x cols, pitch ld (elements), rows
+// on 16-byte boundaries.
+struct OpMat {
+    const uint16_t *p = nullptr;
+    long long ld = 0;
+};
+
+// Makes caller matrices (contiguous rows) readable by TMA: a matrix whose rows
+// are not multiples of 16 bytes is copied to a 128-byte pitch.  plan() says
+// where, run() launches the copies (two matrices a launch) and fills in `out`.
+class OpRelayout {
+  public:
+    void add(OpMat *out, const uint16_t *src, long long rows, long long cols, OpArena &arena) {
+        out->p = src;
+        out->ld = cols;
+        if (cols % 8 == 0 || rows == 0 || cols == 0) return;
+        Job &j = jobs_[n_++];
+        j = Job{out, src, rows, cols, op_round_up(cols, 64), 0};
+        j.at = arena.add(j.rows * j.ld * 2);
+    }
+    // true when anything was launched
+    bool any() const { return n_ > 0; }
+    pgemm_status run(const OpDevice &dev, OpArena &arena, cudaStream_t s);
+
+  private:
+    struct Job {
+        OpMat *out;
+        const uint16_t *src;
+        long long rows, cols, ld, at;
+    };
+    Job jobs_[6];
+    int n_ = 0;
+};
+
+// How the two operands of a product lie in memory (A is M x K, B is K x N).
+enum class OpForm {
+    NN,  // A rows of K, B rows of N
+    NT,  // A rows of K, B stored N x K
+    TN,  // A stored K x M, B rows of N
+};
+
+// The epilogue of a product with bf16 output (EpiOut, op_products.cu).
+struct OpEpilogue {
+    const uint16_t *bias = nullptr;      // N
+    int act = PGEMM_ACT_NONE;
+    const uint16_t *residual = nullptr;  // M x N, rows of N
+    float *preact = nullptr;             // M x N fp32, rows of N: acc + bias
+};
+
+// out[j] (bf16, rows of N) = epilogue(sum over K segments of A * B).
+//   k_segments = 2: out[0] = A[0] B[0] + A[1] B[1] (both K columns each)
+//   n_segments = 2: out[j] = A[0] B[j]
+// Outputs are user matrices: any N; TMA stores where rows are 16-byte
+// multiples.  Few tiles with a long K are split along K into parts whose fp32
+// sums are joined in part order by a second kernel.
+struct OpProduct {
+    OpForm form = OpForm::NN;
+    int M = 0, N = 0, K = 0;
+    OpMat A[2], B[2];
+    uint16_t *out[2] = {nullptr, nullptr};
+    int k_segments = 1, n_segments = 1;
+    OpEpilogue epi;
+    // a caller's own area of fp32 parts instead (cross entropy sums the pieces
+    // of its vocabulary there): the parts are written, nothing is joined
+    float *parts_area = nullptr;
+    bool after = false;  // launched right behind a kernel of the same call
+};
+pgemm_status op_product(const OpDevice &dev, const OpProduct &p, cudaStream_t s);
+
+// Parts a product of these sizes would be split into (parts_area: M padded to
+// 256 rows, N to 64 columns, one such matrix a part and segment).
+int op_product_parts(const OpDevice &dev, int M, int N, int K, int segments);
+long long op_parts_ld(int N);
+long long op_parts_rows(int M);
+// out = epilogue(sum of `parts` matrices), in order.
+pgemm_status op_join_parts(const OpDevice &dev, const float *area, int parts, int segments, int M,
+                           int N, uint16_t *const out[2], const OpEpilogue &epi, bool after,
+                           cudaStream_t s);
+
+// The larger tile on a CTA pair, or 128 x 128 on one CTA: whichever needs
+// less time for this many rows and columns (op_products.cu explains).
+bool op_use_pair(const OpDevice &dev, long long M, long long N, long long pair_n, long long one_n,
+                 int segments);
+
+// dZ = dY * act'(Z) from kept fp32 pre-activations, and column sums of dZ
+// (act none and dz nullptr: of dY itself).  op_products.cu.
+struct OpActGrad {
+    int M = 0, N = 0, act = PGEMM_ACT_NONE;
+    const float *z = nullptr;        // M x N, rows of N; nullptr only with act none
+    const float *u = nullptr;        // gated: the value projection
+    const uint16_t *dy = nullptr;    // M x N, rows of dy_ld
+    long long dy_ld = 0;
+    uint16_t *dz = nullptr;          // rows of dz_ld, or nullptr
+    uint16_t *du = nullptr;          // gated
+    long long dz_ld = 0;
+    uint16_t *dbias = nullptr;       // N, or nullptr
+};
+pgemm_status op_act_grad(const OpDevice &dev, const OpActGrad &p, bool after, cudaStream_t s);
+
+// A C entry point's body: no C++ exception leaves it.
+template <class F>
+pgemm_status op_guard(F &&f) {
+    try {
+        return f();
+    } catch (...) {
+        return PGEMM_ERR_CUDA;
+    }
+}
+
+}  // namespace pg

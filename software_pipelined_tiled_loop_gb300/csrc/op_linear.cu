@@ -1,0 +1,239 @@
+// linear_bf16: Y = act(X W + b) + R, and its gradients.
+#include "op_act.cuh"
+#include "op_gemm.cuh"
+#include "op_host.h"
+
+namespace pg {
+
+// Epilogue of the recomputing backward pass: Z = acc + b stays in fp32 and
+// dZ = dY * act'(Z) is rounded to bf16 once, as the operand of the gradient
+// products.
+struct EpiLinearGrad {
+    const uint16_t *bias, *dy;
+    long long dy_ld;
+    uint16_t *dz;
+    long long dz_ld;
+    int act;
+
+    template <class Cfg, class Wait, class Rel>
+    __device__ __forceinline__ bool run(const EpiCtx &c, const OpMaps &maps, const OpArgs &,
+                                        const OpUnit &w, uint32_t t_row, int col0, bool have,
+                                        Wait wait, Rel release) const {
+        const int nf = w.n0 + col0;
+        uint32_t r[32];
+        get_rows64(c, dy, dy_ld, nf, r);  // travels while the products finish
+        if (!wait()) return false;
+#pragma unroll 1
+        for (int cc = 0; cc < Cfg::EPI_COLS; cc += 64) {
+            const int n = nf + cc;
+            uint32_t p[32];
+            if (cc > 0) get_rows64(c, dy, dy_ld, n, r);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t v[32];
+                acc_cols32(t_row + col0 + cc + 32 * h, have, v);
+                if (h == 1 && cc + 64 >= Cfg::EPI_COLS) release();
+                if (bias != nullptr) {
+                    float b[32];
+                    get_vec32(bias, c.N, n + 32 * h, b);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        v[j] = __float_as_uint(__uint_as_float(v[j]) + b[j]);
+                }
+                with_act(act, [&](auto A) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        float value;
+                        const uint32_t y = r[16 * h + j];
+                        const float lo = bf16_lo(y) * act_value_grad<decltype(A)::value>(
+                                                          __uint_as_float(v[2 * j]), value);
+                        const float hi = bf16_hi(y) * act_value_grad<decltype(A)::value>(
+                                                          __uint_as_float(v[2 * j + 1]), value);
+                        p[16 * h + j] = pack_bf16(lo, hi);
+                    }
+                });
+            }
+            put_rows64(c, &maps.c[0], dz, dz_ld, n, p);
+        }
+        return true;
+    }
+};
+
+template <class Cfg>
+static pgemm_status launch_grad(const OpDevice &dev, int M, int N, int K, const OpMat &X,
+                                const OpMat &W, const EpiLinearGrad &e, bool after,
+                                cudaStream_t s) {
+    OpMaps maps{};
+    pgemm_status st = PGEMM_OK;
+    if (K > 0) {
+        st = op_encode(&maps.a[0], OpElem::BF16, X.p, K, M, X.ld, 64, 128);
+        if (st == PGEMM_OK) st = op_encode(&maps.b[0], OpElem::BF16, W.p, N, K, W.ld, 64, 64);
+    }
+    if (st == PGEMM_OK) st = op_encode(&maps.c[0], OpElem::BF16, e.dz, N, M, e.dz_ld, 64, 32);
+    if (st != PGEMM_OK) return st;
+    constexpr int TM = Cfg::BM * Cfg::CG;
+    OpArgs a{};
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.m_tiles = (M + TM - 1) / TM;
+    a.n_seg = a.n_tiles = (N + Cfg::TILE_N - 1) / Cfg::TILE_N;
+    a.k_seg = a.k_tiles = (K + Cfg::SBK - 1) / Cfg::SBK;
+    a.parts = 1;
+    return op_launch<Cfg, EpiLinearGrad>(dev, maps, a, e, after, s);
+}
+
+static bool act_known(int act) { return act >= PGEMM_ACT_NONE && act <= PGEMM_ACT_SILU; }
+
+static pgemm_status linear_forward(int M, int N, int K, const uint16_t *X, const uint16_t *W,
+                                   const uint16_t *bias, int act, const uint16_t *residual,
+                                   uint16_t *Y, float *preact, cudaStream_t s) {
+    if (M < 0 || N < 0 || K < 0 || !act_known(act)) return PGEMM_ERR_INVALID_VALUE;
+    if (M == 0 || N == 0) return PGEMM_OK;
+    if (!Y || (K > 0 && (!X || !W))) return PGEMM_ERR_INVALID_VALUE;
+    if (!op_aligned16(X) || !op_aligned16(W) || !op_aligned16(bias) || !op_aligned16(residual) ||
+        !op_aligned16(Y) || !op_aligned16(preact))
+        return PGEMM_ERR_MISALIGNED;
+    OpDevice dev;
+    pgemm_status st = op_device(&dev);
+    if (st != PGEMM_OK) return st;
+    OpProduct p;
+    p.form = OpForm::NN;
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    p.out[0] = Y;
+    p.epi = OpEpilogue{bias, act, residual, preact};
+    OpArena arena(dev, s);
+    OpRelayout rl;
+    if (K > 0) {
+        rl.add(&p.A[0], X, M, K, arena);
+        rl.add(&p.B[0], W, K, N, arena);
+    }
+    if ((st = arena.alloc()) != PGEMM_OK) return st;
+    if ((st = rl.run(dev, arena, s)) != PGEMM_OK) return st;
+    p.after = rl.any();
+    return op_product(dev, p, s);
+}
+
+static pgemm_status linear_backward(int M, int N, int K, const uint16_t *X, const uint16_t *W,
+                                    const uint16_t *bias, int act, const uint16_t *dY,
+                                    const float *preact, uint16_t *dX, uint16_t *dW,
+                                    uint16_t *dbias, cudaStream_t s) {
+    if (M < 0 || N < 0 || K < 0 || !act_known(act)) return PGEMM_ERR_INVALID_VALUE;
+    const bool want_x = dX && M > 0 && K > 0, want_w = dW && K > 0 && N > 0;
+    const bool want_b = dbias && N > 0;
+    if (!want_x && !want_w && !want_b) return PGEMM_OK;
+    const bool some = M > 0 && N > 0;  // dY has elements
+    const bool recompute = some && act != PGEMM_ACT_NONE && !preact;
+    if (some && !dY) return PGEMM_ERR_INVALID_VALUE;
+    if (some && K > 0 && ((!X && (want_w || recompute)) || (!W && (want_x || recompute))))
+        return PGEMM_ERR_INVALID_VALUE;
+    if (!op_aligned16(X) || !op_aligned16(W) || !op_aligned16(bias) || !op_aligned16(dY) ||
+        !op_aligned16(preact) || !op_aligned16(dX) || !op_aligned16(dW) || !op_aligned16(dbias))
+        return PGEMM_ERR_MISALIGNED;
+    OpDevice dev;
+    pgemm_status st = op_device(&dev);
+    if (st != PGEMM_OK) return st;
+    if (want_b && M == 0 &&
+        cudaMemsetAsync(dbias, 0, static_cast<size_t>(N) * 2, s) != cudaSuccess)
+        return PGEMM_ERR_CUDA;
+
+    OpArena arena(dev, s);
+    OpRelayout rl;
+    OpMat x, w, dz;
+    if (some && K > 0) {
+        if (X && (want_w || recompute)) rl.add(&x, X, M, K, arena);
+        if (W && (want_x || recompute)) rl.add(&w, W, K, N, arena);
+    }
+    long long dz_at = 0;
+    if (some && act == PGEMM_ACT_NONE) {
+        rl.add(&dz, dY, M, N, arena);
+    } else if (some) {
+        dz.ld = op_round_up(N, 64);
+        dz_at = arena.add(dz.ld * M * 2);
+    }
+    if ((st = arena.alloc()) != PGEMM_OK) return st;
+    if ((st = rl.run(dev, arena, s)) != PGEMM_OK) return st;
+    bool after = rl.any();
+    if (some) {
+        uint16_t *dz_buf = nullptr;
+        if (act != PGEMM_ACT_NONE) dz.p = dz_buf = arena.at<uint16_t>(dz_at);
+        if (recompute) {
+            EpiLinearGrad e{bias, dY, N, dz_buf, dz.ld, act};
+            st = op_use_pair(dev, M, N, 256, 128, 1)
+                     ? launch_grad<OpCfg<256, 3, 2, 2, false, false>>(dev, M, N, K, x, w, e, after, s)
+                     : launch_grad<OpCfg<128, 6, 1, 1, false, false>>(dev, M, N, K, x, w, e, after, s);
+            if (st != PGEMM_OK) return st;
+            after = true;
+        }
+        OpActGrad g;
+        g.M = M;
+        g.N = N;
+        g.dbias = want_b ? dbias : nullptr;
+        if (act != PGEMM_ACT_NONE && preact) {
+            g.act = act;
+            g.z = preact;
+            g.dy = dY;
+            g.dy_ld = N;
+            g.dz = dz_buf;
+            g.dz_ld = dz.ld;
+        } else {  // column sums only: of dY, or of the dZ just recomputed
+            g.dy = act == PGEMM_ACT_NONE ? dY : dz_buf;
+            g.dy_ld = act == PGEMM_ACT_NONE ? N : dz.ld;
+        }
+        if (g.dz || g.dbias) {
+            if ((st = op_act_grad(dev, g, after, s)) != PGEMM_OK) return st;
+            after = true;
+        }
+    }
+    if (want_x) {
+        OpProduct p;
+        p.form = OpForm::NT;
+        p.M = M;
+        p.N = K;
+        p.K = N;
+        p.A[0] = dz;
+        p.B[0] = w;
+        p.out[0] = dX;
+        p.after = after;
+        if ((st = op_product(dev, p, s)) != PGEMM_OK) return st;
+        after = true;
+    }
+    if (want_w) {
+        OpProduct p;
+        p.form = OpForm::TN;
+        p.M = K;
+        p.N = N;
+        p.K = M;
+        p.A[0] = x;
+        p.B[0] = dz;
+        p.out[0] = dW;
+        p.after = after;
+        if ((st = op_product(dev, p, s)) != PGEMM_OK) return st;
+    }
+    return PGEMM_OK;
+}
+
+}  // namespace pg
+
+extern "C" {
+
+pgemm_status linear_bf16(int M, int N, int K, const uint16_t *X, const uint16_t *W,
+                         const uint16_t *bias, int act, const uint16_t *residual, uint16_t *Y,
+                         float *preact, pgemm_stream_t stream) {
+    return pg::op_guard([&] {
+        return pg::linear_forward(M, N, K, X, W, bias, act, residual, Y, preact, stream);
+    });
+}
+
+pgemm_status linear_bf16_backward(int M, int N, int K, const uint16_t *X, const uint16_t *W,
+                                  const uint16_t *bias, int act, const uint16_t *dY,
+                                  const float *preact, uint16_t *dX, uint16_t *dW,
+                                  uint16_t *dbias, pgemm_stream_t stream) {
+    return pg::op_guard([&] {
+        return pg::linear_backward(M, N, K, X, W, bias, act, dY, preact, dX, dW, dbias, stream);
+    });
+}
+
+}  // extern "C"

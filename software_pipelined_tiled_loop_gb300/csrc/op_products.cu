@@ -1,0 +1,525 @@
+// The generic product of the operators (forms NN, NT and TN, bf16 output with
+// an optional bias, activation and residual), its split along K, and the
+// elementwise gradient pass in front of the gradient products.
+#include <cuda_runtime.h>
+
+#include <mutex>
+
+#include "op_act.cuh"
+#include "op_gemm.cuh"
+#include "op_host.h"
+
+namespace pg {
+
+// ------------------------------------------------------------- epilogue ---
+// out = round(act(acc + bias) + residual) to bf16, once, from fp32; or, for a
+// product split along K, the accumulator itself as one of the parts.
+// FULL = false: no bias, activation, residual or kept pre-activation (the
+// gradient products), so that their kernels carry none of it.
+template <bool FULL>
+struct EpiOut {
+    const uint16_t *bias, *residual;
+    float *preact, *parts;
+    uint16_t *out[2];
+    long long ldo;          // row length of out, residual and preact
+    long long parts_ld, parts_rows;
+    int parts_segments;
+    int act;
+    int tma_out, tma_preact;
+
+    template <class Cfg, class Wait, class Rel>
+    __device__ __forceinline__ bool run(const EpiCtx &c, const OpMaps &maps, const OpArgs &,
+                                        const OpUnit &w, uint32_t t_row, int col0, bool have,
+                                        Wait wait, Rel release) const {
+        const int nf = w.n0 + col0;
+        if (parts != nullptr) {
+            if (!wait()) return false;
+            const int row0 = static_cast<int>(
+                (static_cast<long long>(w.part) * parts_segments + w.seg) * parts_rows + c.m0);
+#pragma unroll 1
+            for (int cc = 0; cc < Cfg::EPI_COLS; cc += 32) {
+                uint32_t v[32];
+                acc_cols32(t_row + col0 + cc, have, v);
+                if (cc + 32 >= Cfg::EPI_COLS) release();
+                put_rows32(c, &maps.c[0], nullptr, 0, row0, nf + cc, v);
+            }
+            return true;
+        }
+        uint32_t r[32];
+        bool have_r = false;
+        if constexpr (FULL) {
+            have_r = residual != nullptr;
+            // the first columns' residual travels while the products finish
+            if (have_r) get_rows64(c, residual, ldo, nf, r);
+        }
+        if (!wait()) return false;
+        const CUtensorMap *map = tma_out ? &maps.c[w.seg] : nullptr;
+        uint16_t *o = out[w.seg];
+#pragma unroll 1
+        for (int cc = 0; cc < Cfg::EPI_COLS; cc += 64) {
+            const int n = nf + cc;
+            uint32_t p[32];
+            if constexpr (FULL) {
+                if (have_r && cc > 0) get_rows64(c, residual, ldo, n, r);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t v[32];
+                acc_cols32(t_row + col0 + cc + 32 * h, have, v);
+                if (h == 1 && cc + 64 >= Cfg::EPI_COLS) release();
+                if constexpr (FULL) {
+                    if (bias != nullptr) {
+                        float b[32];
+                        get_vec32(bias, c.N, n + 32 * h, b);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            v[j] = __float_as_uint(__uint_as_float(v[j]) + b[j]);
+                    }
+                    if (preact != nullptr)
+                        put_rows32(c, tma_preact ? &maps.c[2] : nullptr, preact, ldo, c.m0,
+                                   n + 32 * h, v);
+                    if (act != PGEMM_ACT_NONE)
+                        with_act(act, [&](auto A) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                v[j] = __float_as_uint(
+                                    act_value<decltype(A)::value>(__uint_as_float(v[j])));
+                        });
+                    if (have_r) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            v[2 * j] = __float_as_uint(__uint_as_float(v[2 * j]) +
+                                                       bf16_lo(r[16 * h + j]));
+                            v[2 * j + 1] = __float_as_uint(__uint_as_float(v[2 * j + 1]) +
+                                                           bf16_hi(r[16 * h + j]));
+                        }
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    p[16 * h + j] =
+                        pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+            }
+            put_rows64(c, map, o, ldo, n, p);
+        }
+        return true;
+    }
+};
+
+// --------------------------------------------------------------- choice ---
+// Time of a product in units of one 64-wide K step of a 128 x 256 share of a
+// CTA pair's tile: a wave of pair tiles costs 1 a step, a wave of 128 x 128
+// tiles on single CTAs kOneStep (they do half the work at a lower rate: each
+// operand panel feeds half as many products).  Parts along K shorten the
+// waves and add the join's traffic: parts * M * N fp32 values written and read.
+constexpr double kStepUs = 0.36, kOneStep = 0.65;
+struct OpPlan {
+    bool pair;
+    int parts;
+};
+static OpPlan plan_product(int sm_count, long long M, long long N, long long K, int segments,
+                           bool split) {
+    const long long steps = (K + 63) / 64;
+    OpPlan best{false, 1};
+    double best_us = 1e30;
+    for (int pair = 0; pair < 2; ++pair) {
+        const long long bm = pair ? 256 : 128;
+        const long long tiles = ((M + bm - 1) / bm) * ((N + bm - 1) / bm) * segments;
+        const long long slots = pair ? sm_count / 2 : sm_count;
+        const int most = split ? 32 : 1;
+        for (int parts = 1; parts <= most; ++parts) {
+            if (parts > 1 && steps / parts < 8) break;
+            const double waves = static_cast<double>((tiles * parts + slots - 1) / slots);
+            double us = waves * ((pair ? 1.0 : kOneStep) * kStepUs * ((steps + parts - 1) / parts) + 1.0);
+            if (parts > 1) us += 4.0 + parts * 8e-6 * M * N * segments / 5.0;
+            if (us < best_us * 0.999) {
+                best_us = us;
+                best = OpPlan{pair != 0, parts};
+            }
+        }
+    }
+    return best;
+}
+
+bool op_use_pair(const OpDevice &dev, long long M, long long N, long long pair_n, long long one_n,
+                 int segments) {
+    const long long tp = ((M + 255) / 256) * ((N + pair_n - 1) / pair_n) * segments;
+    const long long t1 = ((M + 127) / 128) * ((N + one_n - 1) / one_n) * segments;
+    const long long sp = dev.sm_count / 2, s1 = dev.sm_count;
+    return static_cast<double>((tp + sp - 1) / sp) <=
+           kOneStep * static_cast<double>((t1 + s1 - 1) / s1);
+}
+
+int op_product_parts(const OpDevice &dev, int M, int N, int K, int segments) {
+    return plan_product(dev.sm_count, M, N, K, segments, true).parts;
+}
+long long op_parts_ld(int N) { return op_round_up(N, 64); }
+long long op_parts_rows(int M) { return op_round_up(M, 256); }
+
+// ----------------------------------------------------------------- launch ---
+template <class Cfg, bool FULL>
+static pgemm_status launch_form(const OpDevice &dev, const OpProduct &p, float *parts_area,
+                                int parts, cudaStream_t s) {
+    constexpr int TM = Cfg::BM * Cfg::CG, TN = Cfg::TILE_N;
+    OpMaps maps{};
+    for (int j = 0; j < 2; ++j) {
+        const OpMat &a = p.A[p.k_segments == 2 ? j : 0];
+        const OpMat &b = p.B[(p.k_segments == 2 || p.n_segments == 2) ? j : 0];
+        pgemm_status st;
+        if (p.K > 0) {
+            st = Cfg::A_MN ? op_encode(&maps.a[j], OpElem::BF16, a.p, p.M, p.K, a.ld, 64, 64)
+                           : op_encode(&maps.a[j], OpElem::BF16, a.p, p.K, p.M, a.ld, 64, 128);
+            if (st == PGEMM_OK)
+                st = Cfg::B_K ? op_encode(&maps.b[j], OpElem::BF16, b.p, p.K, p.N, b.ld, 64,
+                                          Cfg::B_COLS)
+                              : op_encode(&maps.b[j], OpElem::BF16, b.p, p.N, p.K, b.ld, 64, 64);
+            if (st != PGEMM_OK) return st;
+        }
+    }
+    EpiOut<FULL> e{};
+    e.act = p.epi.act;
+    e.bias = p.epi.bias;
+    e.residual = p.epi.residual;
+    e.preact = p.epi.preact;
+    e.out[0] = p.out[0];
+    e.out[1] = p.out[1];
+    e.ldo = p.N;
+    e.parts = parts_area;
+    if (parts_area != nullptr) {
+        e.parts_ld = op_parts_ld(p.N);
+        e.parts_rows = op_parts_rows(p.M);
+        e.parts_segments = p.n_segments;
+        const pgemm_status st =
+            op_encode(&maps.c[0], OpElem::F32, parts_area, e.parts_ld,
+                      e.parts_rows * parts * p.n_segments, e.parts_ld, 32, 32);
+        if (st != PGEMM_OK) return st;
+    } else {
+        e.tma_out = p.N % 8 == 0;
+        for (int j = 0; e.tma_out && j < p.n_segments; ++j) {
+            const pgemm_status st =
+                op_encode(&maps.c[j], OpElem::BF16, p.out[j], p.N, p.M, p.N, 64, 32);
+            if (st != PGEMM_OK) return st;
+        }
+        e.tma_preact = e.preact != nullptr && p.N % 4 == 0;
+        if (e.tma_preact) {
+            const pgemm_status st =
+                op_encode(&maps.c[2], OpElem::F32, e.preact, p.N, p.M, p.N, 32, 32);
+            if (st != PGEMM_OK) return st;
+        }
+    }
+    OpArgs a{};
+    a.M = p.M;
+    // the parts' padding columns are written too, so that the join reads whole vectors
+    a.N = parts_area != nullptr ? static_cast<int>(op_parts_ld(p.N)) : p.N;
+    a.K = p.K;
+    a.m_tiles = (p.M + TM - 1) / TM;
+    a.n_seg = (p.N + TN - 1) / TN;
+    a.n_tiles = a.n_seg * p.n_segments;
+    a.k_seg = (p.K + Cfg::SBK - 1) / Cfg::SBK;
+    a.k_tiles = a.k_seg * p.k_segments;
+    a.parts = parts;
+    return op_launch<Cfg, EpiOut<FULL>>(dev, maps, a, e, p.after, s);
+}
+
+template <bool A_MN, bool B_K>
+using PairCfg = OpCfg<256, 3, 2, 2, A_MN, B_K>;
+template <bool A_MN, bool B_K>
+using OneCfg = OpCfg<128, 6, 1, 1, A_MN, B_K>;
+
+template <bool FULL, bool A_MN, bool B_K>
+static pgemm_status launch_size(const OpDevice &dev, const OpProduct &p, float *area,
+                                const OpPlan &plan, cudaStream_t s) {
+    return plan.pair ? launch_form<PairCfg<A_MN, B_K>, FULL>(dev, p, area, plan.parts, s)
+                     : launch_form<OneCfg<A_MN, B_K>, FULL>(dev, p, area, plan.parts, s);
+}
+
+pgemm_status op_product(const OpDevice &dev, const OpProduct &p, cudaStream_t s) {
+    if (p.M <= 0 || p.N <= 0) return PGEMM_OK;
+    const OpPlan plan = plan_product(dev.sm_count, p.M, p.N,
+                                     static_cast<long long>(p.K) * p.k_segments, p.n_segments, true);
+    OpArena arena(dev, s);
+    float *area = p.parts_area;
+    const bool join = area == nullptr && plan.parts > 1;
+    if (join) {
+        const long long at = arena.add(op_parts_ld(p.N) * op_parts_rows(p.M) * 4 * plan.parts *
+                                       p.n_segments);
+        const pgemm_status st = arena.alloc();
+        if (st != PGEMM_OK) return st;
+        area = arena.at<float>(at);
+    }
+    pgemm_status st = PGEMM_ERR_INVALID_VALUE;
+    switch (p.form) {
+        case OpForm::NN: st = launch_size<true, false, false>(dev, p, area, plan, s); break;
+        case OpForm::NT: st = launch_size<false, false, true>(dev, p, area, plan, s); break;
+        case OpForm::TN: st = launch_size<false, true, false>(dev, p, area, plan, s); break;
+    }
+    if (st == PGEMM_OK && join)
+        st = op_join_parts(dev, area, plan.parts, p.n_segments, p.M, p.N, p.out, p.epi, true, s);
+    return st;
+}
+
+// ------------------------------------------------------------------- join ---
+// Memory-bound: reads parts * M * N fp32 values once, writes M * N bf16.  A
+// thread owns four columns of a row, so loads are 16 bytes and the parts are
+// added in order (the result does not depend on timing).
+struct JoinParams {
+    const float *area;
+    long long ld, rows;
+    int parts, segments, M, N;
+    uint16_t *out[2];
+    OpEpilogue e;
+};
+
+__global__ void __launch_bounds__(256) join_parts_kernel(const JoinParams p) {
+    grid_dependency_wait();
+    const int quads = (p.N + 3) / 4;
+    const long long total = static_cast<long long>(p.M) * quads * p.segments;
+    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+        const long long sm = i / quads;  // segment * M + row
+        const int n = static_cast<int>(i - sm * quads) * 4;
+        const int seg = sm >= p.M ? 1 : 0;
+        const long long m = sm - static_cast<long long>(seg) * p.M;
+        const float *src = p.area + (seg * p.rows + m) * p.ld + n;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int k = 0; k < p.parts; ++k) {
+            const float4 x = __ldcs(reinterpret_cast<const float4 *>(
+                src + static_cast<long long>(k) * p.segments * p.rows * p.ld));
+            v[0] += x.x;
+            v[1] += x.y;
+            v[2] += x.z;
+            v[3] += x.w;
+        }
+        const long long at = m * p.N + n;
+        const int cols = min(4, p.N - n);
+        for (int j = 0; j < cols; ++j) {
+            if (p.e.bias) v[j] += __uint_as_float(static_cast<uint32_t>(p.e.bias[n + j]) << 16);
+            if (p.e.preact) p.e.preact[at + j] = v[j];
+        }
+        with_act(p.e.act, [&](auto A) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = act_value<decltype(A)::value>(v[j]);
+        });
+        if (p.e.residual)
+            for (int j = 0; j < cols; ++j)
+                v[j] += __uint_as_float(static_cast<uint32_t>(p.e.residual[at + j]) << 16);
+        uint16_t *o = p.out[seg] + at;
+        const uint32_t lo = pack_bf16(v[0], v[1]), hi = pack_bf16(v[2], v[3]);
+        if (p.N % 4 == 0) {
+            *reinterpret_cast<uint2 *>(o) = make_uint2(lo, hi);
+        } else {
+            const uint32_t w[4] = {lo & 0xffffu, lo >> 16, hi & 0xffffu, hi >> 16};
+            for (int j = 0; j < cols; ++j) o[j] = static_cast<uint16_t>(w[j]);
+        }
+    }
+}
+
+// Launches `kernel` behind a kernel of the same call (programmatic stream
+// serialisation: the kernel itself waits before it reads anything).
+template <class... KArgs, class... Args>
+static pgemm_status launch_after(void (*kernel)(KArgs...), dim3 grid, dim3 block, bool after,
+                                 cudaStream_t s, Args... args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = grid;
+    lc.blockDim = block;
+    lc.stream = s;
+    lc.attrs = attr;
+    lc.numAttrs = after ? 1 : 0;
+    return cudaLaunchKernelEx(&lc, kernel, args...) == cudaSuccess ? PGEMM_OK : PGEMM_ERR_CUDA;
+}
+
+pgemm_status op_join_parts(const OpDevice &dev, const float *area, int parts, int segments, int M,
+                           int N, uint16_t *const out[2], const OpEpilogue &epi, bool after,
+                           cudaStream_t s) {
+    JoinParams p{};
+    p.area = area;
+    p.ld = op_parts_ld(N);
+    p.rows = op_parts_rows(M);
+    p.parts = parts;
+    p.segments = segments;
+    p.M = M;
+    p.N = N;
+    p.out[0] = out[0];
+    p.out[1] = out[1];
+    p.e = epi;
+    const long long blocks = (static_cast<long long>(M) * ((N + 3) / 4) * segments + 255) / 256;
+    const long long most = dev.sm_count * 8ll;
+    return launch_after(join_parts_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)),
+                        dim3(256), after, s, p);
+}
+
+// --------------------------------------------------- activation gradient ---
+// dZ = dY * act'(Z) (linear), dG = dH * U * act'(G) and dU = dH * act(G)
+// (gated), elementwise in fp32 from the kept fp32 pre-activations, rounded to
+// bf16 because the tensor core multiplies them next; column sums of the
+// unrounded dZ for the bias.  Memory-bound: 8 (gated 14) bytes an element.
+// A block covers 256 columns x kGradRows rows; a thread eight columns of every
+// eighth row, so its part of a column sum stays in registers.  VEC: the eight
+// columns are adjacent (16-byte accesses; row lengths multiples of 8), else 32
+// apart (coalesced single elements).
+constexpr int kGradRows = 64;
+
+struct ActGradParams {
+    OpActGrad g;
+    float *colsum;  // [row blocks][N] partial column sums, or nullptr
+};
+
+__device__ __forceinline__ void load8(const float *p, float (&f)[8]) {
+    const float4 a = __ldcs(reinterpret_cast<const float4 *>(p));
+    const float4 b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+
+template <bool VEC, bool GATED>
+__global__ void __launch_bounds__(256) act_grad_kernel(const ActGradParams p) {
+    grid_dependency_wait();
+    const OpActGrad &g = p.g;
+    const int lane = threadIdx.x & 31, rl = threadIdx.x >> 5;
+    const int c0 = blockIdx.x * 256;
+    auto col = [&](int i) { return VEC ? c0 + lane * 8 + i : c0 + lane + 32 * i; };
+    float sum[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
+    // row blocks blockIdx.y, blockIdx.y + gridDim.y, ...: rows of stride 8 in each
+    for (long long rr = static_cast<long long>(blockIdx.y) * kGradRows + rl; rr < g.M;
+         rr += ((rr & (kGradRows - 1)) + 8 < kGradRows
+                    ? 8
+                    : 8 + static_cast<long long>(gridDim.y - 1) * kGradRows)) {
+        const int r = static_cast<int>(rr);
+        const long long zi = static_cast<long long>(r) * g.N;
+        const long long yi = static_cast<long long>(r) * g.dy_ld;
+        float z[8], u[8], dy[8];
+        if (VEC) {
+            if (col(0) >= g.N) continue;
+            if (g.z) load8(g.z + zi + col(0), z);
+            if (GATED) load8(g.u + zi + col(0), u);
+            const uint4 x = *reinterpret_cast<const uint4 *>(g.dy + yi + col(0));
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                dy[2 * i] = bf16_lo(w[i]);
+                dy[2 * i + 1] = bf16_hi(w[i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const bool in = col(i) < g.N;
+                z[i] = in && g.z ? g.z[zi + col(i)] : 0.0f;
+                u[i] = GATED && in ? g.u[zi + col(i)] : 0.0f;
+                dy[i] = in ? __uint_as_float(static_cast<uint32_t>(g.dy[yi + col(i)]) << 16) : 0.0f;
+            }
+        }
+        float dz[8], du[8];
+        with_act(g.act, [&](auto A) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float value = 0.0f;
+                const float d = decltype(A)::value == PGEMM_ACT_NONE && !GATED
+                                    ? 1.0f
+                                    : act_value_grad<decltype(A)::value>(z[i], value);
+                dz[i] = dy[i] * d * (GATED ? u[i] : 1.0f);
+                du[i] = dy[i] * value;
+            }
+        });
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] += dz[i];
+        const long long oi = static_cast<long long>(r) * g.dz_ld;
+        auto put = [&](uint16_t *o, const float (&d)[8]) {
+            if (o == nullptr) return;
+            if (VEC) {
+                *reinterpret_cast<uint4 *>(o + oi + col(0)) =
+                    make_uint4(pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3]),
+                               pack_bf16(d[4], d[5]), pack_bf16(d[6], d[7]));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (col(i) < g.N)
+                        o[oi + col(i)] = static_cast<uint16_t>(pack_bf16(d[i], 0.0f) & 0xffffu);
+            }
+        };
+        put(g.dz, dz);
+        if (GATED) put(g.du, du);
+    }
+    if (p.colsum != nullptr) {
+        __shared__ float s[8][256];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[rl][VEC ? lane * 8 + i : lane + 32 * i] = sum[i];
+        __syncthreads();
+        const int c = c0 + threadIdx.x;
+        float t = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t += s[i][threadIdx.x];
+        if (c < g.N) p.colsum[static_cast<long long>(blockIdx.y) * g.N + c] = t;
+    }
+}
+
+// dbias = sum of the row blocks' column sums, in order.
+__global__ void __launch_bounds__(256)
+    colsum_join_kernel(const float *part, int blocks, int N, uint16_t *out) {
+    grid_dependency_wait();
+    __shared__ float s[8][32];
+    const int lane = threadIdx.x & 31, rl = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + lane;
+    float t = 0.0f;
+    if (c < N)
+        for (int b = rl; b < blocks; b += 8) t += part[static_cast<long long>(b) * N + c];
+    s[rl][lane] = t;
+    __syncthreads();
+    if (rl == 0 && c < N) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) t += s[i][lane];
+        out[c] = static_cast<uint16_t>(pack_bf16(t, 0.0f) & 0xffffu);
+    }
+}
+
+pgemm_status op_act_grad(const OpDevice &dev, const OpActGrad &g, bool after, cudaStream_t s) {
+    if (g.M <= 0 || g.N <= 0) return PGEMM_OK;
+    ActGradParams p{g, nullptr};
+    const int all_blocks = (g.M + kGradRows - 1) / kGradRows;
+    const int row_blocks = all_blocks < 512 ? all_blocks : 512;
+    OpArena arena(dev, s);
+    if (g.dbias != nullptr) {
+        const long long at = arena.add(static_cast<long long>(row_blocks) * g.N * 4);
+        const pgemm_status st = arena.alloc();
+        if (st != PGEMM_OK) return st;
+        p.colsum = arena.at<float>(at);
+    }
+    const dim3 grid((g.N + 255) / 256, row_blocks);
+    const bool vec = g.N % 8 == 0 && g.dy_ld % 8 == 0;
+    pgemm_status st;
+    if (g.u != nullptr)
+        st = vec ? launch_after(act_grad_kernel<true, true>, grid, dim3(256), after, s, p)
+                 : launch_after(act_grad_kernel<false, true>, grid, dim3(256), after, s, p);
+    else
+        st = vec ? launch_after(act_grad_kernel<true, false>, grid, dim3(256), after, s, p)
+                 : launch_after(act_grad_kernel<false, false>, grid, dim3(256), after, s, p);
+    if (st == PGEMM_OK && g.dbias != nullptr)
+        st = launch_after(colsum_join_kernel, dim3((g.N + 31) / 32), dim3(256), true, s,
+                          static_cast<const float *>(p.colsum), row_blocks, g.N, g.dbias);
+    return st;
+}
+
+// --------------------------------------------------------------- relayout ---
+pgemm_status OpRelayout::run(const OpDevice &dev, OpArena &arena, cudaStream_t s) {
+    for (int i = 0; i < n_; ++i) {
+        jobs_[i].out->p = arena.at<uint16_t>(jobs_[i].at);
+        jobs_[i].out->ld = jobs_[i].ld;
+    }
+    for (int i = 0; i < n_; i += 2) {
+        const Job &a = jobs_[i];
+        const Job *b = i + 1 < n_ ? &jobs_[i + 1] : nullptr;
+        if (launch_repack(a.src, a.cols, arena.at<uint16_t>(a.at), a.ld, static_cast<int>(a.rows),
+                          static_cast<int>(a.cols), b ? b->src : nullptr, b ? b->cols : 0,
+                          b ? arena.at<uint16_t>(b->at) : nullptr, b ? b->ld : 0,
+                          b ? static_cast<int>(b->rows) : 0, b ? static_cast<int>(b->cols) : 0, 2,
+                          dev.sm_count, s) != cudaSuccess)
+            return PGEMM_ERR_CUDA;
+    }
+    return PGEMM_OK;
+}
+
+}  // namespace pg
