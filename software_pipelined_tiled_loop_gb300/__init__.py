@@ -130,6 +130,8 @@ def _declare(L: ctypes.CDLL) -> ctypes.CDLL:
 def lib() -> ctypes.CDLL:
     """The loaded library.  Raises if it has not been built (no fallback)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(library_path):
@@ -154,18 +156,36 @@ def _ptr(x) -> int:
     raise TypeError(f"cannot take a device pointer from {type(x).__name__}")
 
 
+_current_raw_stream = None  # torch's current stream of the current device, once CUDA is up
+
+
 def _stream(s) -> int:
     if s is None:
-        try:
-            import torch
-            if torch.cuda.is_available():
-                return int(torch.cuda.current_stream().cuda_stream)
-        except ImportError:
-            pass
-        return 0
+        if _current_raw_stream is not None:
+            return _current_raw_stream()
+        return _find_current_stream()
     if isinstance(s, int):
         return s
     return int(s.cuda_stream)
+
+
+def _find_current_stream() -> int:
+    """torch's current stream (0 without torch or a GPU).  The first call that
+    finds torch's CUDA state initialised keeps the direct lookup, which takes
+    0.3 us a call instead of 3.8 through a Stream object."""
+    global _current_raw_stream
+    try:
+        import torch
+        if not torch.cuda.is_available():
+            return 0
+    except ImportError:
+        return 0
+    found = int(torch.cuda.current_stream().cuda_stream)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    device = getattr(torch._C, "_cuda_getDevice", None)
+    if torch.cuda.is_initialized() and raw is not None and device is not None:
+        _current_raw_stream = lambda: raw(device())  # noqa: E731
+    return found
 
 
 def _check(code: int, where: str) -> None:

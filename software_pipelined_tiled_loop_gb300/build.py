@@ -19,7 +19,8 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libpipegemm.so")
 SOURCES = ["api.cu", "gemm_f32.cu", "gemm_bf16.cu", "gemm_i8.cu", "gemm_i8_imma.cu",
            "gemm_i8_noalloc.cu",
-           "stage_reuse.cu", "op_products.cu", "op_linear.cu", "op_gated.cu", "op_xent.cu"]
+           "stage_reuse.cu", "op_products.cu", "op_linear.cu", "op_gated.cu", "op_xent.cu",
+           "op_tokens.cu"]
 HEADERS = ["ptx.cuh", "common.cuh", "tc_gemm.cuh", "kernels.h", "widen.cuh", "op_act.cuh",
            "op_gemm.cuh", "op_host.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

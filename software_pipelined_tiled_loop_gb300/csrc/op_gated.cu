@@ -107,7 +107,7 @@ struct EpiGatedGrad {
 template <class Cfg, class Epi>
 static pgemm_status launch_dual(const OpDevice &dev, int M, int F, int K, const OpMat &X,
                                 const OpMat &Wg, const OpMat &Wu, OpMaps &maps, const Epi &e,
-                                bool after, cudaStream_t s) {
+                                cudaStream_t s) {
     if (K > 0) {
         pgemm_status st = op_encode(&maps.a[0], OpElem::BF16, X.p, K, M, X.ld, 64, 128);
         if (st == PGEMM_OK) st = op_encode(&maps.b[0], OpElem::BF16, Wg.p, F, K, Wg.ld, 64, 64);
@@ -123,7 +123,7 @@ static pgemm_status launch_dual(const OpDevice &dev, int M, int F, int K, const 
     a.n_seg = a.n_tiles = (F + Cfg::TILE_N - 1) / Cfg::TILE_N;
     a.k_seg = a.k_tiles = (K + Cfg::SBK - 1) / Cfg::SBK;
     a.parts = 1;
-    return op_launch<Cfg, Epi>(dev, maps, a, e, after, s);
+    return op_launch<Cfg, Epi>(dev, maps, a, e, s);
 }
 
 using DualPair = OpCfg<256, 3, 2, 2, false, false, true>;
@@ -132,10 +132,10 @@ using DualOne = OpCfg<128, 6, 1, 1, false, false, true>;
 template <class Epi>
 static pgemm_status launch_dual_size(const OpDevice &dev, int M, int F, int K, const OpMat &X,
                                      const OpMat &Wg, const OpMat &Wu, OpMaps &maps, const Epi &e,
-                                     bool after, cudaStream_t s) {
+                                     cudaStream_t s) {
     return op_use_pair(dev, M, F, 128, 64, 1)
-               ? launch_dual<DualPair>(dev, M, F, K, X, Wg, Wu, maps, e, after, s)
-               : launch_dual<DualOne>(dev, M, F, K, X, Wg, Wu, maps, e, after, s);
+               ? launch_dual<DualPair>(dev, M, F, K, X, Wg, Wu, maps, e, s)
+               : launch_dual<DualOne>(dev, M, F, K, X, Wg, Wu, maps, e, s);
 }
 
 static bool act_known(int act) { return act >= PGEMM_ACT_NONE && act <= PGEMM_ACT_SILU; }
@@ -162,6 +162,7 @@ static pgemm_status gated_forward(int M, int F, int K, const uint16_t *X, const 
     }
     if ((st = arena.alloc()) != PGEMM_OK) return st;
     if ((st = rl.run(dev, arena, s)) != PGEMM_OK) return st;
+    if (M <= kTokensMax) return op_tokens_gated(dev, M, F, K, x, wg, wu, act, H, preact, s);
     OpMaps maps{};
     EpiGated e{H, preact, F, act, F % 8 == 0, preact != nullptr && F % 4 == 0};
     if (e.tma_h) st = op_encode(&maps.c[0], OpElem::BF16, H, F, M, F, 64, 32);
@@ -172,7 +173,7 @@ static pgemm_status gated_forward(int M, int F, int K, const uint16_t *X, const 
                            F, 32, 32);
     }
     if (st != PGEMM_OK) return st;
-    return launch_dual_size(dev, M, F, K, x, wg, wu, maps, e, rl.any(), s);
+    return launch_dual_size(dev, M, F, K, x, wg, wu, maps, e, s);
 }
 
 static pgemm_status gated_backward(int M, int F, int K, const uint16_t *X, const uint16_t *Wg,
@@ -205,7 +206,6 @@ static pgemm_status gated_backward(int M, int F, int K, const uint16_t *X, const
     }
     if ((st = arena.alloc()) != PGEMM_OK) return st;
     if ((st = rl.run(dev, arena, s)) != PGEMM_OK) return st;
-    bool after = rl.any();
     if (some) {
         uint16_t *dg_buf = arena.at<uint16_t>(dg_at), *du_buf = arena.at<uint16_t>(du_at);
         dg.p = dg_buf;
@@ -222,7 +222,7 @@ static pgemm_status gated_backward(int M, int F, int K, const uint16_t *X, const
             g.dz = dg_buf;
             g.du = du_buf;
             g.dz_ld = dg.ld;
-            st = op_act_grad(dev, g, after, s);
+            st = op_act_grad(dev, g, s);
         } else {
             OpMaps maps{};
             EpiGatedGrad e{dH, F, dg_buf, du_buf, dg.ld, act};
@@ -230,10 +230,9 @@ static pgemm_status gated_backward(int M, int F, int K, const uint16_t *X, const
             if (st == PGEMM_OK)
                 st = op_encode(&maps.c[1], OpElem::BF16, du_buf, F, M, du.ld, 64, 32);
             if (st == PGEMM_OK)
-                st = launch_dual_size(dev, M, F, K, x, wg, wu, maps, e, after, s);
+                st = launch_dual_size(dev, M, F, K, x, wg, wu, maps, e, s);
         }
         if (st != PGEMM_OK) return st;
-        after = true;
     }
     if (want_x) {
         OpProduct p;
@@ -247,9 +246,7 @@ static pgemm_status gated_backward(int M, int F, int K, const uint16_t *X, const
         p.B[0] = wg;
         p.B[1] = wu;
         p.out[0] = dX;
-        p.after = after;
         if ((st = op_product(dev, p, s)) != PGEMM_OK) return st;
-        after = true;
     }
     if (want_w) {
         OpProduct p;
@@ -263,7 +260,6 @@ static pgemm_status gated_backward(int M, int F, int K, const uint16_t *X, const
         p.B[1] = du;
         p.out[0] = dWg;
         p.out[1] = dWu;
-        p.after = after;
         if ((st = op_product(dev, p, s)) != PGEMM_OK) return st;
     }
     return PGEMM_OK;

@@ -334,6 +334,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     const uint32_t tmem_base = *tmem_slot;
     // on-chip set-up is done; what follows may read what the kernel before wrote
     grid_dependency_wait();
+    grid_launch_dependents();
 
     const int crank = Cfg::CG == 2 ? static_cast<int>(cluster_ctarank()) : 0;
     const int slot = static_cast<int>(blockIdx.x) / Cfg::CG;
@@ -584,11 +585,12 @@ static KernelInfo op_info() {
 }
 
 // Sets the kernel up on the device (once), then launches it on `stream`.
-// `after`: it follows another kernel of the same call, whose results it reads
-// after grid_dependency_wait, so its prologue may overlap that kernel's tail.
+// Programmatic stream serialisation: every thread waits for the kernel before
+// it (grid_dependency_wait) ahead of its first access to memory, so only the
+// prologue (barriers, tensor memory) overlaps that kernel's tail.
 template <class Cfg, class Epi>
 static pgemm_status op_launch(const OpDevice &dev, const OpMaps &maps, OpArgs a, const Epi &epi,
-                              bool after, cudaStream_t stream) {
+                              cudaStream_t stream) {
     static const KernelInfo info = op_info<Cfg, Epi>();
     int slots = 0;
     const pgemm_status st = op_kernel_setup(dev, info, &slots);
@@ -602,11 +604,9 @@ static pgemm_status op_launch(const OpDevice &dev, const OpMaps &maps, OpArgs a,
     a.group_m = static_cast<long long>(a.k_tiles) * Cfg::SBK / a.parts <= 4096 ? 16 : 8;
     cudaLaunchAttribute attr[2];
     int nattr = 0;
-    if (after) {
-        attr[nattr].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[nattr].val.programmaticStreamSerializationAllowed = 1;
-        ++nattr;
-    }
+    attr[nattr].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[nattr].val.programmaticStreamSerializationAllowed = 1;
+    ++nattr;
     if constexpr (Cfg::CG == 2) {
         attr[nattr].id = cudaLaunchAttributeClusterDimension;
         attr[nattr].val.clusterDim.x = Cfg::CG;
@@ -624,6 +624,22 @@ static pgemm_status op_launch(const OpDevice &dev, const OpMaps &maps, OpArgs a,
     return cudaLaunchKernelEx(&lc, op_gemm_kernel<Cfg, Epi>, maps, a, epi, dev.ctx) == cudaSuccess
                ? PGEMM_OK
                : PGEMM_ERR_CUDA;
+}
+
+// As op_launch launches: the kernel waits before it touches memory.
+template <class... KArgs, class... Args>
+static pgemm_status launch_small(void (*kernel)(KArgs...), dim3 grid, dim3 block,
+                                 cudaStream_t s, Args... args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = grid;
+    lc.blockDim = block;
+    lc.stream = s;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    return cudaLaunchKernelEx(&lc, kernel, args...) == cudaSuccess ? PGEMM_OK : PGEMM_ERR_CUDA;
 }
 
 }  // namespace pg

@@ -91,8 +91,6 @@ class OpRelayout {
         j = Job{out, src, rows, cols, op_round_up(cols, 64), 0};
         j.at = arena.add(j.rows * j.ld * 2);
     }
-    // true when anything was launched
-    bool any() const { return n_ > 0; }
     pgemm_status run(const OpDevice &dev, OpArena &arena, cudaStream_t s);
 
   private:
@@ -136,9 +134,16 @@ struct OpProduct {
     // a caller's own area of fp32 parts instead (cross entropy sums the pieces
     // of its vocabulary there): the parts are written, nothing is joined
     float *parts_area = nullptr;
-    bool after = false;  // launched right behind a kernel of the same call
 };
 pgemm_status op_product(const OpDevice &dev, const OpProduct &p, cudaStream_t s);
+
+// The same products of a few rows, bound by reading the weights (op_tokens.cu).
+constexpr int kTokensMax = 128;
+pgemm_status op_tokens_linear(const OpDevice &dev, int M, int N, int K, const OpMat &X,
+                              const OpMat &W, const OpEpilogue &e, uint16_t *Y, cudaStream_t s);
+pgemm_status op_tokens_gated(const OpDevice &dev, int M, int F, int K, const OpMat &X,
+                             const OpMat &Wg, const OpMat &Wu, int act, uint16_t *H,
+                             float *preact, cudaStream_t s);
 
 // Parts a product of these sizes would be split into (parts_area: M padded to
 // 256 rows, N to 64 columns, one such matrix a part and segment).
@@ -147,7 +152,7 @@ long long op_parts_ld(int N);
 long long op_parts_rows(int M);
 // out = epilogue(sum of `parts` matrices), in order.
 pgemm_status op_join_parts(const OpDevice &dev, const float *area, int parts, int segments, int M,
-                           int N, uint16_t *const out[2], const OpEpilogue &epi, bool after,
+                           int N, uint16_t *const out[2], const OpEpilogue &epi,
                            cudaStream_t s);
 
 // The larger tile on a CTA pair, or 128 x 128 on one CTA: whichever needs
@@ -168,7 +173,7 @@ struct OpActGrad {
     long long dz_ld = 0;
     uint16_t *dbias = nullptr;       // N, or nullptr
 };
-pgemm_status op_act_grad(const OpDevice &dev, const OpActGrad &p, bool after, cudaStream_t s);
+pgemm_status op_act_grad(const OpDevice &dev, const OpActGrad &p, cudaStream_t s);
 
 // A C entry point's body: no C++ exception leaves it.
 template <class F>

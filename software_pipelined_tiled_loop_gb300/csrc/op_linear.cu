@@ -61,8 +61,7 @@ struct EpiLinearGrad {
 
 template <class Cfg>
 static pgemm_status launch_grad(const OpDevice &dev, int M, int N, int K, const OpMat &X,
-                                const OpMat &W, const EpiLinearGrad &e, bool after,
-                                cudaStream_t s) {
+                                const OpMat &W, const EpiLinearGrad &e, cudaStream_t s) {
     OpMaps maps{};
     pgemm_status st = PGEMM_OK;
     if (K > 0) {
@@ -80,7 +79,7 @@ static pgemm_status launch_grad(const OpDevice &dev, int M, int N, int K, const 
     a.n_seg = a.n_tiles = (N + Cfg::TILE_N - 1) / Cfg::TILE_N;
     a.k_seg = a.k_tiles = (K + Cfg::SBK - 1) / Cfg::SBK;
     a.parts = 1;
-    return op_launch<Cfg, EpiLinearGrad>(dev, maps, a, e, after, s);
+    return op_launch<Cfg, EpiLinearGrad>(dev, maps, a, e, s);
 }
 
 static bool act_known(int act) { return act >= PGEMM_ACT_NONE && act <= PGEMM_ACT_SILU; }
@@ -112,7 +111,7 @@ static pgemm_status linear_forward(int M, int N, int K, const uint16_t *X, const
     }
     if ((st = arena.alloc()) != PGEMM_OK) return st;
     if ((st = rl.run(dev, arena, s)) != PGEMM_OK) return st;
-    p.after = rl.any();
+    if (M <= kTokensMax) return op_tokens_linear(dev, M, N, K, p.A[0], p.B[0], p.epi, Y, s);
     return op_product(dev, p, s);
 }
 
@@ -155,17 +154,15 @@ static pgemm_status linear_backward(int M, int N, int K, const uint16_t *X, cons
     }
     if ((st = arena.alloc()) != PGEMM_OK) return st;
     if ((st = rl.run(dev, arena, s)) != PGEMM_OK) return st;
-    bool after = rl.any();
     if (some) {
         uint16_t *dz_buf = nullptr;
         if (act != PGEMM_ACT_NONE) dz.p = dz_buf = arena.at<uint16_t>(dz_at);
         if (recompute) {
             EpiLinearGrad e{bias, dY, N, dz_buf, dz.ld, act};
             st = op_use_pair(dev, M, N, 256, 128, 1)
-                     ? launch_grad<OpCfg<256, 3, 2, 2, false, false>>(dev, M, N, K, x, w, e, after, s)
-                     : launch_grad<OpCfg<128, 6, 1, 1, false, false>>(dev, M, N, K, x, w, e, after, s);
+                     ? launch_grad<OpCfg<256, 3, 2, 2, false, false>>(dev, M, N, K, x, w, e, s)
+                     : launch_grad<OpCfg<128, 6, 1, 1, false, false>>(dev, M, N, K, x, w, e, s);
             if (st != PGEMM_OK) return st;
-            after = true;
         }
         OpActGrad g;
         g.M = M;
@@ -183,8 +180,7 @@ static pgemm_status linear_backward(int M, int N, int K, const uint16_t *X, cons
             g.dy_ld = act == PGEMM_ACT_NONE ? N : dz.ld;
         }
         if (g.dz || g.dbias) {
-            if ((st = op_act_grad(dev, g, after, s)) != PGEMM_OK) return st;
-            after = true;
+            if ((st = op_act_grad(dev, g, s)) != PGEMM_OK) return st;
         }
     }
     if (want_x) {
@@ -196,9 +192,7 @@ static pgemm_status linear_backward(int M, int N, int K, const uint16_t *X, cons
         p.A[0] = dz;
         p.B[0] = w;
         p.out[0] = dX;
-        p.after = after;
         if ((st = op_product(dev, p, s)) != PGEMM_OK) return st;
-        after = true;
     }
     if (want_w) {
         OpProduct p;
@@ -209,7 +203,6 @@ static pgemm_status linear_backward(int M, int N, int K, const uint16_t *X, cons
         p.A[0] = x;
         p.B[0] = dz;
         p.out[0] = dW;
-        p.after = after;
         if ((st = op_product(dev, p, s)) != PGEMM_OK) return st;
     }
     return PGEMM_OK;

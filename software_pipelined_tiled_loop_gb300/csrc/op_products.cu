@@ -218,7 +218,7 @@ static pgemm_status launch_form(const OpDevice &dev, const OpProduct &p, float *
     a.k_seg = (p.K + Cfg::SBK - 1) / Cfg::SBK;
     a.k_tiles = a.k_seg * p.k_segments;
     a.parts = parts;
-    return op_launch<Cfg, EpiOut<FULL>>(dev, maps, a, e, p.after, s);
+    return op_launch<Cfg, EpiOut<FULL>>(dev, maps, a, e, s);
 }
 
 template <bool A_MN, bool B_K>
@@ -254,7 +254,7 @@ pgemm_status op_product(const OpDevice &dev, const OpProduct &p, cudaStream_t s)
         case OpForm::TN: st = launch_size<false, true, false>(dev, p, area, plan, s); break;
     }
     if (st == PGEMM_OK && join)
-        st = op_join_parts(dev, area, plan.parts, p.n_segments, p.M, p.N, p.out, p.epi, true, s);
+        st = op_join_parts(dev, area, plan.parts, p.n_segments, p.M, p.N, p.out, p.epi, s);
     return st;
 }
 
@@ -272,6 +272,7 @@ struct JoinParams {
 
 __global__ void __launch_bounds__(256) join_parts_kernel(const JoinParams p) {
     grid_dependency_wait();
+    grid_launch_dependents();
     const int quads = (p.N + 3) / 4;
     const long long total = static_cast<long long>(p.M) * quads * p.segments;
     for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
@@ -314,25 +315,8 @@ __global__ void __launch_bounds__(256) join_parts_kernel(const JoinParams p) {
     }
 }
 
-// Launches `kernel` behind a kernel of the same call (programmatic stream
-// serialisation: the kernel itself waits before it reads anything).
-template <class... KArgs, class... Args>
-static pgemm_status launch_after(void (*kernel)(KArgs...), dim3 grid, dim3 block, bool after,
-                                 cudaStream_t s, Args... args) {
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t lc{};
-    lc.gridDim = grid;
-    lc.blockDim = block;
-    lc.stream = s;
-    lc.attrs = attr;
-    lc.numAttrs = after ? 1 : 0;
-    return cudaLaunchKernelEx(&lc, kernel, args...) == cudaSuccess ? PGEMM_OK : PGEMM_ERR_CUDA;
-}
-
 pgemm_status op_join_parts(const OpDevice &dev, const float *area, int parts, int segments, int M,
-                           int N, uint16_t *const out[2], const OpEpilogue &epi, bool after,
+                           int N, uint16_t *const out[2], const OpEpilogue &epi,
                            cudaStream_t s) {
     JoinParams p{};
     p.area = area;
@@ -347,8 +331,8 @@ pgemm_status op_join_parts(const OpDevice &dev, const float *area, int parts, in
     p.e = epi;
     const long long blocks = (static_cast<long long>(M) * ((N + 3) / 4) * segments + 255) / 256;
     const long long most = dev.sm_count * 8ll;
-    return launch_after(join_parts_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)),
-                        dim3(256), after, s, p);
+    return launch_small(join_parts_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)),
+                        dim3(256), s, p);
 }
 
 // --------------------------------------------------- activation gradient ---
@@ -377,6 +361,7 @@ __device__ __forceinline__ void load8(const float *p, float (&f)[8]) {
 template <bool VEC, bool GATED>
 __global__ void __launch_bounds__(256) act_grad_kernel(const ActGradParams p) {
     grid_dependency_wait();
+    grid_launch_dependents();
     const OpActGrad &g = p.g;
     const int lane = threadIdx.x & 31, rl = threadIdx.x >> 5;
     const int c0 = blockIdx.x * 256;
@@ -461,6 +446,7 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const ActGradParams p) {
 __global__ void __launch_bounds__(256)
     colsum_join_kernel(const float *part, int blocks, int N, uint16_t *out) {
     grid_dependency_wait();
+    grid_launch_dependents();
     __shared__ float s[8][32];
     const int lane = threadIdx.x & 31, rl = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
@@ -476,7 +462,7 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-pgemm_status op_act_grad(const OpDevice &dev, const OpActGrad &g, bool after, cudaStream_t s) {
+pgemm_status op_act_grad(const OpDevice &dev, const OpActGrad &g, cudaStream_t s) {
     if (g.M <= 0 || g.N <= 0) return PGEMM_OK;
     ActGradParams p{g, nullptr};
     const int all_blocks = (g.M + kGradRows - 1) / kGradRows;
@@ -492,13 +478,13 @@ pgemm_status op_act_grad(const OpDevice &dev, const OpActGrad &g, bool after, cu
     const bool vec = g.N % 8 == 0 && g.dy_ld % 8 == 0;
     pgemm_status st;
     if (g.u != nullptr)
-        st = vec ? launch_after(act_grad_kernel<true, true>, grid, dim3(256), after, s, p)
-                 : launch_after(act_grad_kernel<false, true>, grid, dim3(256), after, s, p);
+        st = vec ? launch_small(act_grad_kernel<true, true>, grid, dim3(256), s, p)
+                 : launch_small(act_grad_kernel<false, true>, grid, dim3(256), s, p);
     else
-        st = vec ? launch_after(act_grad_kernel<true, false>, grid, dim3(256), after, s, p)
-                 : launch_after(act_grad_kernel<false, false>, grid, dim3(256), after, s, p);
+        st = vec ? launch_small(act_grad_kernel<true, false>, grid, dim3(256), s, p)
+                 : launch_small(act_grad_kernel<false, false>, grid, dim3(256), s, p);
     if (st == PGEMM_OK && g.dbias != nullptr)
-        st = launch_after(colsum_join_kernel, dim3((g.N + 31) / 32), dim3(256), true, s,
+        st = launch_small(colsum_join_kernel, dim3((g.N + 31) / 32), dim3(256), s,
                           static_cast<const float *>(p.colsum), row_blocks, g.N, g.dbias);
     return st;
 }

@@ -1,0 +1,398 @@
+// Products of a few rows (up to 128 tokens of a decoding step): Y = act(X W + b)
+// + R and H = act(X Wg) * (X Wu), bound by streaming the weights once.
+//
+// The weights take the tensor core's M side: D[n][t] = sum_k W[k][n] X[t][k],
+// A = W^T read M-major straight from the K x N rows by TMA (64-column boxes of
+// 64 k-rows), B = X K-major with N = 16 .. 128 tokens.  An SM's ring then holds
+// weights, not padding of X: 128 x 128 tiles with a token a row would load as
+// many bytes for one token as for 128.  A thread owns one output column, so
+// bias, residual and stores run along n, coalesced for every token.
+//
+// Long axis: a cluster of S CTAs shares a 128-column tile, CTA r taking K steps
+// [r T / S, (r + 1) T / S).  The fp32 partial sums meet in the CTAs' own shared
+// memory: after a cluster barrier each CTA adds, in rank order, the partials of
+// its share of the tokens (a warp a token, a lane four columns, so that the
+// peers' sums come as 16-byte loads) and writes those outputs.  No scratch, no
+// second kernel, the same bits every time.
+//
+// Rings are sized for two CTAs an SM, and the next kernel in the stream may
+// start its CTAs while this one drains: before they wait for it they ask L2 for
+// their first weights.  That is safe whatever the kernel before writes, since
+// a prefetch moves nothing past L2, where all writes meet.
+#include <algorithm>
+
+#include "op_act.cuh"
+#include "op_gemm.cuh"
+#include "op_host.h"
+
+namespace pg {
+
+struct TokensArgs {
+    int M, N, K;
+    int k_tiles;
+    // linear
+    const uint16_t *bias, *residual;
+    // gated: preact holds both products
+    float *preact;
+    uint16_t *out;
+    int act;
+};
+
+struct TokensMaps {
+    CUtensorMap x, w[2];
+};
+
+// TOK: tokens of the MMA's N side; DUAL: two weight matrices (gated), whose
+// accumulators lie side by side in tensor memory.
+template <int TOK_, bool DUAL_>
+struct TokCfg {
+    static constexpr int TOK = TOK_, BN = 128, BK = 64;
+    static constexpr bool DUAL = DUAL_;
+    static constexpr int NW = DUAL ? 2 : 1;
+    static constexpr int W_SUB = BN * BK * 2;  // one matrix, 64 k-rows
+    static constexpr int X_SUB = TOK * BK * 2;
+    static constexpr int STAGE_BYTES = NW * W_SUB + X_SUB;
+    static constexpr int SUM_BYTES = NW * TOK * BN * 4;  // partial sums, over the drained ring
+    // two CTAs an SM, unless the partial sums alone are more than half of it
+    static constexpr int HALF_SM = kSmemPerSm / 2 - kSmemReservedPerBlock - 2048;
+    static constexpr int CTAS = SUM_BYTES <= HALF_SM ? 2 : 1;
+    static constexpr int STAGES = (CTAS == 2 ? HALF_SM : 232448 - 2048) / STAGE_BYTES;
+    static constexpr int RING = STAGES * STAGE_BYTES;
+    static constexpr int BAR_OFFSET = RING;
+    static constexpr int USED = BAR_OFFSET + (2 * STAGES + 1) * 8 + 16;
+    static constexpr int SMEM_BYTES = smem_request(USED + 1024, CTAS);
+    static constexpr int ACC = NW * TOK;
+    static constexpr int TMEM_COLS = ACC <= 32 ? 32 : ACC <= 64 ? 64 : ACC <= 128 ? 128 : 256;
+    static constexpr int EPI = 8;  // epilogue warps: two for each TMEM lane quadrant
+    static constexpr int THREADS = 64 + 32 * EPI;
+    static constexpr int PREFETCH = 4;  // K steps asked for ahead of the kernel before
+    static_assert(STAGES >= 2 && SUM_BYTES <= RING && SMEM_BYTES <= 232448, "shared memory");
+    static_assert(TOK % 16 == 0 && TOK <= 128, "TOK");
+};
+
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// Ask L2 for a box of a tensor.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap *map, int32_t x, int32_t y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y)
+                 : "memory");
+}
+
+// Four bf16 values (8-byte aligned with vec), of which `cols` exist.
+__device__ __forceinline__ void get4(const uint16_t *p, int cols, bool vec, float (&f)[4]) {
+    if (vec) {
+        const uint2 x = *reinterpret_cast<const uint2 *>(p);
+        f[0] = bf16_lo(x.x);
+        f[1] = bf16_hi(x.x);
+        f[2] = bf16_lo(x.y);
+        f[3] = bf16_hi(x.y);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            f[j] = j < cols ? __uint_as_float(static_cast<uint32_t>(p[j]) << 16) : 0.0f;
+    }
+}
+
+template <class Cfg>
+__global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
+    tokens_kernel(const __grid_constant__ TokensMaps maps, const TokensArgs a,
+                  const KernelCtx ctx) {
+    constexpr int TOK = Cfg::TOK, STAGES = Cfg::STAGES, BK = Cfg::BK, BN = Cfg::BN;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = align_1024(smem_raw);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + Cfg::BAR_OFFSET);
+    uint64_t *empty = full + STAGES;
+    uint64_t *done = empty + STAGES;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+    const uint32_t warp = warp_id_uniform(), lane = lane_id();
+    uint32_t S;
+    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(S));
+    const uint32_t rank = S > 1 ? cluster_ctarank() : 0u;
+    const int n0 = static_cast<int>(blockIdx.x / S) * BN;
+    const int kb = static_cast<int>(static_cast<long long>(rank) * a.k_tiles / S);
+    const int ke = static_cast<int>(static_cast<long long>(rank + 1) * a.k_tiles / S);
+
+    if (warp == 0 && lane == 0) {
+        if (a.k_tiles > 0) {
+            prefetch_tmap(&maps.x);
+            prefetch_tmap(&maps.w[0]);
+        }
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(done, 1);
+        fence_barrier_init();
+    }
+    if (warp == 2 && lane == 0) {
+        for (int kt = kb; kt < min(ke, kb + Cfg::PREFETCH); ++kt)
+#pragma unroll
+            for (int d = 0; d < Cfg::NW; ++d)
+#pragma unroll
+                for (int j = 0; j < BN / 64; ++j)
+                    if (n0 + 64 * j < a.N) tma_prefetch_2d(&maps.w[d], n0 + 64 * j, kt * BK);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, Cfg::TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int it = 0;
+            for (int kt = kb; kt < ke; ++kt, ++it) {
+                const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
+                if (!mbar_wait(&empty[s], ph ^ 1u, ctx, kSiteProducerEmpty)) break;
+                uint8_t *st = smem + s * Cfg::STAGE_BYTES;
+                mbar_arrive_expect_tx(&full[s], Cfg::STAGE_BYTES);
+#pragma unroll
+                for (int d = 0; d < Cfg::NW; ++d)
+#pragma unroll
+                    for (int j = 0; j < BN / 64; ++j)
+                        tma_load_2d(st + d * Cfg::W_SUB + j * (BK * 128), &maps.w[d], &full[s],
+                                    n0 + 64 * j, kt * BK);
+                tma_load_2d(st + Cfg::NW * Cfg::W_SUB, &maps.x, &full[s], kt * BK, 0);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = idesc_f16(BN, TOK, 1, /*A M-major*/ 1, /*B K-major*/ 0);
+            int it = 0;
+            for (int kt = kb; kt < ke; ++kt, ++it) {
+                const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
+                if (!mbar_wait(&full[s], ph, ctx, kSiteMmaFull)) break;
+                tc_fence_after();
+                const uint32_t st = smem_u32(smem + s * Cfg::STAGE_BYTES);
+#pragma unroll
+                for (int k = 0; k < BK / 16; ++k) {
+                    const uint64_t bd =
+                        smem_desc_sw128(st + Cfg::NW * Cfg::W_SUB + k * 32, 16, 1024);
+#pragma unroll
+                    for (int d = 0; d < Cfg::NW; ++d) {
+                        const uint64_t ad =
+                            smem_desc_sw128(st + d * Cfg::W_SUB + k * 2048, BK * 128, 1024);
+                        umma_f16_ss(tmem + d * TOK, ad, bd, idesc,
+                                    (kt == kb && k == 0) ? 0u : 1u);
+                    }
+                }
+                umma_commit(&empty[s]);
+            }
+            umma_commit(done);
+        }
+    }
+    // Every MMA of this CTA has completed: the ring is free, the sums final.
+    // (With an empty K range the commit arrives at once.)
+    const bool ok = mbar_wait(done, 0, ctx, kSiteEpilogueFull);
+    tc_fence_after();
+    __syncwarp();
+    float *sums = reinterpret_cast<float *>(smem);  // [NW][TOK][128]
+    if (warp >= 2) {
+        const uint32_t q = warp & 3u;
+        const int col = static_cast<int>(q * 32 + lane);
+        const uint32_t t_row = tmem + ((q * 32u) << 16);
+        // each of a quadrant's two warps every other 16 accumulator columns
+#pragma unroll 1
+        for (int c = static_cast<int>((warp - 2) >> 2) * 16; c < Cfg::ACC; c += 32) {
+            if (c % TOK >= a.M) continue;  // no tokens there
+            uint32_t v[16];
+            if (ke > kb && ok) {
+                tmem_ld_32x32b_x16(t_row + c, v);
+                tmem_ld_wait();
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = 0u;
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sums[(c + j) * BN + col] = __uint_as_float(v[j]);
+        }
+    }
+    __syncwarp();
+    if (S > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    if (warp >= 2 && ok) {
+        // tokens rank, rank + S, ... are this CTA's; its warps take them in turn
+        const int n = n0 + static_cast<int>(lane) * 4;
+        const int cols = a.N - n;
+        const bool vec = a.N % 4 == 0;  // rows on 8-byte boundaries
+        if (cols > 0) {
+            float b[4] = {0.f, 0.f, 0.f, 0.f};
+            if (!Cfg::DUAL && a.bias) get4(a.bias + n, cols, vec, b);
+            for (int t = static_cast<int>(rank + S * (warp - 2)); t < a.M;
+                 t += static_cast<int>(S) * Cfg::EPI) {
+                const long long at = static_cast<long long>(t) * a.N + n;
+                float r[4] = {0.f, 0.f, 0.f, 0.f};
+                if (!Cfg::DUAL && a.residual) get4(a.residual + at, cols, vec, r);
+                float4 part[Cfg::NW][8];
+#pragma unroll
+                for (int d = 0; d < Cfg::NW; ++d) {
+                    const float *p = sums + (d * TOK + t) * BN + lane * 4;
+                    const uint32_t local = smem_u32(p);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (i < static_cast<int>(S))
+                            part[d][i] = S == 1 ? *reinterpret_cast<const float4 *>(p)
+                                                : ld_cluster_f32x4(mapa_shared(local, i));
+                }
+                float z[Cfg::NW][4];
+#pragma unroll
+                for (int d = 0; d < Cfg::NW; ++d) {
+                    z[d][0] = part[d][0].x;
+                    z[d][1] = part[d][0].y;
+                    z[d][2] = part[d][0].z;
+                    z[d][3] = part[d][0].w;
+#pragma unroll
+                    for (int i = 1; i < 8; ++i)
+                        if (i < static_cast<int>(S)) {
+                            z[d][0] += part[d][i].x;
+                            z[d][1] += part[d][i].y;
+                            z[d][2] += part[d][i].z;
+                            z[d][3] += part[d][i].w;
+                        }
+                }
+                float y[4];
+                if constexpr (!Cfg::DUAL) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) z[0][j] += b[j];
+                }
+                if (a.preact) {
+#pragma unroll
+                    for (int d = 0; d < Cfg::NW; ++d)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (j < cols)
+                                a.preact[d * static_cast<long long>(a.M) * a.N + at + j] = z[d][j];
+                }
+                with_act(a.act, [&](auto A) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        y[j] = act_value<decltype(A)::value>(z[0][j]);
+                        y[j] = Cfg::DUAL ? y[j] * z[Cfg::NW - 1][j] : y[j] + r[j];
+                    }
+                });
+                const uint32_t lo = pack_bf16(y[0], y[1]), hi = pack_bf16(y[2], y[3]);
+                if (vec) {
+                    *reinterpret_cast<uint2 *>(a.out + at) = make_uint2(lo, hi);
+                } else {
+                    const uint32_t w[4] = {lo & 0xffffu, lo >> 16, hi & 0xffffu, hi >> 16};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (j < cols) a.out[at + j] = static_cast<uint16_t>(w[j]);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (S > 1)
+        cluster_sync();  // the peers have read this CTA's sums
+    else
+        __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, Cfg::TMEM_COLS);
+    }
+}
+
+// CTAs that share a tile along K: the S of 1, 2, 4, 8 whose waves (`slots` CTAs
+// at once, each 1 / S of a tile's K steps) end soonest, with at least four
+// steps a CTA, and half a step's worth for each doubling of the join.
+static int cluster_share(int slots, int n_tiles, int k_tiles) {
+    int best = 1;
+    double best_cost = 1e30, join = 0.0;
+    for (int S = 1; S <= 8; S *= 2, join += 0.5) {
+        if (S > 1 && k_tiles / S < 4) break;
+        const int per_wave = slots / S;
+        const double waves = (n_tiles + per_wave - 1) / per_wave;
+        const double cost = waves * ((k_tiles + S - 1) / S) + join;
+        if (cost < best_cost) {
+            best_cost = cost;
+            best = S;
+        }
+    }
+    return best;
+}
+
+template <class Cfg>
+static pgemm_status launch_tokens(const OpDevice &dev, TokensArgs a, const OpMat &X,
+                                  const OpMat *W, cudaStream_t s) {
+    static const KernelInfo info = [] {
+        KernelInfo k;
+        k.threads = Cfg::THREADS;
+        k.smem_bytes = Cfg::SMEM_BYTES;
+        k.func = reinterpret_cast<const void *>(tokens_kernel<Cfg>);
+        return k;
+    }();
+    int slots = 0;
+    pgemm_status st = op_kernel_setup(dev, info, &slots);
+    TokensMaps maps{};
+    if (a.K > 0) {
+        if (st == PGEMM_OK)
+            st = op_encode(&maps.x, OpElem::BF16, X.p, a.K, a.M, X.ld, 64, Cfg::TOK);
+        for (int d = 0; d < Cfg::NW && st == PGEMM_OK; ++d)
+            st = op_encode(&maps.w[d], OpElem::BF16, W[d].p, a.N, a.K, W[d].ld, 64, 64);
+    }
+    if (st != PGEMM_OK) return st;
+    a.k_tiles = (a.K + Cfg::BK - 1) / Cfg::BK;
+    const int n_tiles = (a.N + Cfg::BN - 1) / Cfg::BN;
+    const int S = cluster_share(dev.sm_count * Cfg::CTAS, n_tiles, a.k_tiles);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(S);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = dim3(static_cast<unsigned>(n_tiles) * S);
+    lc.blockDim = dim3(Cfg::THREADS);
+    lc.dynamicSmemBytes = Cfg::SMEM_BYTES;
+    lc.stream = s;
+    lc.attrs = attr;
+    lc.numAttrs = 2;
+    return cudaLaunchKernelEx(&lc, tokens_kernel<Cfg>, maps, a, dev.ctx) == cudaSuccess
+               ? PGEMM_OK
+               : PGEMM_ERR_CUDA;
+}
+
+template <bool DUAL>
+static pgemm_status launch_tokens_size(const OpDevice &dev, const TokensArgs &a, const OpMat &X,
+                                       const OpMat *W, cudaStream_t s) {
+    if (a.M <= 16) return launch_tokens<TokCfg<16, DUAL>>(dev, a, X, W, s);
+    if (a.M <= 32) return launch_tokens<TokCfg<32, DUAL>>(dev, a, X, W, s);
+    if (a.M <= 64) return launch_tokens<TokCfg<64, DUAL>>(dev, a, X, W, s);
+    return launch_tokens<TokCfg<128, DUAL>>(dev, a, X, W, s);
+}
+
+pgemm_status op_tokens_linear(const OpDevice &dev, int M, int N, int K, const OpMat &X,
+                              const OpMat &W, const OpEpilogue &e, uint16_t *Y, cudaStream_t s) {
+    const TokensArgs a{M, N, K, 0, e.bias, e.residual, e.preact, Y, e.act};
+    return launch_tokens_size<false>(dev, a, X, &W, s);
+}
+
+pgemm_status op_tokens_gated(const OpDevice &dev, int M, int F, int K, const OpMat &X,
+                             const OpMat &Wg, const OpMat &Wu, int act, uint16_t *H,
+                             float *preact, cudaStream_t s) {
+    const TokensArgs a{M, F, K, 0, nullptr, nullptr, preact, H, act};
+    const OpMat w[2] = {Wg, Wu};
+    return launch_tokens_size<true>(dev, a, X, w, s);
+}
+
+}  // namespace pg

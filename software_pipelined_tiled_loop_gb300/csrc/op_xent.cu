@@ -144,6 +144,7 @@ __global__ void __launch_bounds__(256)
                      long long V, const int64_t *target, const float *target_logit, float *loss,
                      float *lse) {
     grid_dependency_wait();
+    grid_launch_dependents();
     __shared__ float sm[8][32], ss[8][32];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int t = blockIdx.x * 32 + lane;
@@ -172,7 +173,7 @@ using XentOne = OpCfg<128, 6, 1, 1, false, true>;
 template <class Cfg, class Epi>
 static pgemm_status launch_logits(const OpDevice &dev, int T, int cols, int D, const OpMat &X,
                                   const OpMat &W, long long v0, OpMaps &maps, const Epi &e,
-                                  bool after, cudaStream_t s) {
+                                  cudaStream_t s) {
     if (D > 0) {
         pgemm_status st = op_encode(&maps.a[0], OpElem::BF16, X.p, D, T, X.ld, 64, 128);
         if (st == PGEMM_OK)
@@ -189,7 +190,7 @@ static pgemm_status launch_logits(const OpDevice &dev, int T, int cols, int D, c
     a.n_seg = a.n_tiles = (cols + Cfg::TILE_N - 1) / Cfg::TILE_N;
     a.k_seg = a.k_tiles = (D + Cfg::SBK - 1) / Cfg::SBK;
     a.parts = 1;
-    return op_launch<Cfg, Epi>(dev, maps, a, e, after, s);
+    return op_launch<Cfg, Epi>(dev, maps, a, e, s);
 }
 
 // Workspace of a gradient's P when the caller names none: 2 GiB (all of P up
@@ -263,12 +264,14 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
         OpMaps maps{};
         EpiXentStats e{target, arena.at<float>(at_m), arena.at<float>(at_s), rows,
                        arena.at<float>(at_t)};
-        st = pair ? launch_logits<XentPair>(dev, T, V, D, x, w, 0, maps, e, rl.any(), s)
-                  : launch_logits<XentOne>(dev, T, V, D, x, w, 0, maps, e, rl.any(), s);
+        st = pair ? launch_logits<XentPair>(dev, T, V, D, x, w, 0, maps, e, s)
+                  : launch_logits<XentOne>(dev, T, V, D, x, w, 0, maps, e, s);
         if (st != PGEMM_OK) return st;
-        xent_join_kernel<<<(T + 31) / 32, 256, 0, s>>>(e.part_m, e.part_s, rows, blocks, T, V,
-                                                       target, e.target_logit, loss, lse_buf);
-        if (cudaGetLastError() != cudaSuccess) return PGEMM_ERR_CUDA;
+        st = launch_small(xent_join_kernel, dim3((T + 31) / 32), dim3(256), s,
+                          static_cast<const float *>(e.part_m), static_cast<const float *>(e.part_s),
+                          rows, blocks, T, static_cast<long long>(V), target,
+                          static_cast<const float *>(e.target_logit), loss, lse_buf);
+        if (st != PGEMM_OK) return st;
     }
 
     int x_done = 0;
@@ -281,8 +284,8 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
             return st;
         EpiXentGrad e{target, lse_buf, dloss, v0, V};
         st = op_use_pair(dev, T, cols, 256, 128, 1)
-                 ? launch_logits<XentPair>(dev, T, cols, D, x, w, v0, maps, e, true, s)
-                 : launch_logits<XentOne>(dev, T, cols, D, x, w, v0, maps, e, true, s);
+                 ? launch_logits<XentPair>(dev, T, cols, D, x, w, v0, maps, e, s)
+                 : launch_logits<XentOne>(dev, T, cols, D, x, w, v0, maps, e, s);
         if (st != PGEMM_OK) return st;
         if (want_x) {
             OpProduct p;
@@ -293,7 +296,6 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
             p.A[0] = OpMat{P, piece};
             p.B[0] = OpMat{w.p + v0 * w.ld, w.ld};
             p.out[0] = dX;
-            p.after = true;
             if (x_pieces) {
                 p.parts_area = arena.at<float>(at_x) +
                                op_parts_ld(D) * op_parts_rows(T) * static_cast<long long>(x_done);
@@ -310,13 +312,12 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
             p.A[0] = OpMat{P, piece};
             p.B[0] = x;
             p.out[0] = dW + v0 * D;
-            p.after = true;
             if ((st = op_product(dev, p, s)) != PGEMM_OK) return st;
         }
     }
     if (x_pieces) {
         uint16_t *out[2] = {dX, nullptr};
-        st = op_join_parts(dev, arena.at<float>(at_x), x_parts, 1, T, D, out, OpEpilogue{}, true, s);
+        st = op_join_parts(dev, arena.at<float>(at_x), x_parts, 1, T, D, out, OpEpilogue{}, s);
     }
     return st;
 }

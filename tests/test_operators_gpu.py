@@ -44,7 +44,7 @@ def linear_inputs(M, N, K, seed, bias=True, residual=True):
 # one element; a token; odd everything; whole tiles; tails of rows, columns and
 # K; an empty K; rows whose pitch TMA cannot describe; a grid of CTA pairs; a
 # long K over few tiles (parts along K)
-LINEAR_SIZES = [(1, 1, 1), (1, 64, 64), (1, 1000, 520), (7, 33, 17), (16, 40, 2048), (33, 96, 72),
+LINEAR_SIZES = [(1, 1, 1), (1, 64, 64), (1, 1000, 520), (7, 33, 17), (16, 40, 2048), (24, 200, 1000), (33, 96, 72),
                 (64, 512, 136), (65, 129, 200), (128, 128, 64), (129, 257, 130), (300, 520, 96),
                 (5, 8, 0), (64, 4097, 40), (2500, 2600, 136), (96, 130, 4100), (200, 64, 8192),
                 (1, 264, 9000)]
@@ -136,7 +136,7 @@ def gated_inputs(M, F, K, seed):
             rnd(seed + 2, K, F, std=max(K, 1) ** -0.5))
 
 
-GATED_SIZES = [(1, 1, 1), (1, 64, 64), (1, 1000, 520), (7, 33, 17), (16, 40, 2048), (33, 96, 72),
+GATED_SIZES = [(1, 1, 1), (1, 64, 64), (1, 1000, 520), (7, 33, 17), (16, 40, 2048), (24, 200, 1000), (33, 96, 72),
                (64, 512, 136), (65, 129, 200), (129, 257, 130), (300, 520, 96), (5, 8, 0),
                (2500, 1300, 136), (1, 136, 9000)]
 
