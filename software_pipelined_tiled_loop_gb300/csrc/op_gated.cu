@@ -16,13 +16,14 @@ struct EpiGated {
     int act;
     int tma_h, tma_preact;
 
-    template <class Cfg, class Wait, class Rel>
+    template <class Cfg, class Acc>
     __device__ __forceinline__ bool run(const EpiCtx &c, const OpMaps &maps, const OpArgs &,
-                                        const OpUnit &w, uint32_t t_row, int col0, bool have,
-                                        Wait wait, Rel release) const {
-        if (!wait()) return false;
+                                        const OpUnit &w, Acc &acc, int col0) const {
+        if (!acc.wait()) return false;
+        const uint32_t t_row = acc.row();
+        const bool have = acc.have();
         if (col0 >= Cfg::TILE_N) {
-            release();
+            acc.release();
             return true;
         }
         const int n = w.n0 + col0;
@@ -32,7 +33,7 @@ struct EpiGated {
             uint32_t g[32], u[32];
             acc_cols32(t_row + col0 + 32 * k, have, g);
             acc_cols32(t_row + Cfg::TILE_N + col0 + 32 * k, have, u);
-            if (k == 1) release();
+            if (k == 1) acc.release();
             if (preact != nullptr) {
                 put_rows32(c, tma_preact ? &maps.c[1] : nullptr, preact, ld, c.m0, n + 32 * k, g);
                 put_rows32(c, tma_preact ? &maps.c[2] : nullptr, preact + ld * c.M, ld, c.m0,
@@ -63,25 +64,28 @@ struct EpiGatedGrad {
     long long dz_ld;
     int act;
 
-    template <class Cfg, class Wait, class Rel>
+    template <class Cfg, class Acc>
     __device__ __forceinline__ bool run(const EpiCtx &c, const OpMaps &maps, const OpArgs &,
-                                        const OpUnit &w, uint32_t t_row, int col0, bool have,
-                                        Wait wait, Rel release) const {
+                                        const OpUnit &w, Acc &acc, int col0) const {
         if (col0 >= Cfg::TILE_N) {
-            if (!wait()) return false;
-            release();
+            if (!acc.wait()) return false;
+        const uint32_t t_row = acc.row();
+        const bool have = acc.have();
+            acc.release();
             return true;
         }
         const int n = w.n0 + col0;
         uint32_t r[32], p[32], s[32];
         get_rows64(c, dh, ld, n, r);
-        if (!wait()) return false;
+        if (!acc.wait()) return false;
+        const uint32_t t_row = acc.row();
+        const bool have = acc.have();
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             uint32_t g[32], u[32];
             acc_cols32(t_row + col0 + 32 * k, have, g);
             acc_cols32(t_row + Cfg::TILE_N + col0 + 32 * k, have, u);
-            if (k == 1) release();
+            if (k == 1) acc.release();
             with_act(act, [&](auto A) {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {

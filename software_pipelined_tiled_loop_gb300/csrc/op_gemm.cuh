@@ -56,10 +56,15 @@ struct OpArgs {
     int group_m;
 };
 
-template <int BN_, int STAGES_, int KSUB_, int CG_, bool A_MN_, bool B_K_, bool DUAL_ = false>
+// ROUND: K-tiles of one accumulation round (0: all of a unit's K range).  The
+// accumulator is handed to the epilogue after every round and starts again at
+// zero; the epilogue adds the rounds in fp32 registers.
+template <int BN_, int STAGES_, int KSUB_, int CG_, bool A_MN_, bool B_K_, bool DUAL_ = false,
+          int ROUND_ = 0>
 struct OpCfg {
     static constexpr int BM = 128, BN = BN_, BK = 64, STAGES = STAGES_, KSUB = KSUB_, CG = CG_;
     static constexpr bool A_MN = A_MN_, B_K = B_K_, DUAL = DUAL_;
+    static constexpr int ROUND = ROUND_;
     static constexpr int SBK = BK * KSUB;
     static constexpr int B_COLS = BN / CG;          // B columns this CTA loads and holds
     static constexpr int TILE_N = DUAL ? BN / 2 : BN;  // output columns of a tile
@@ -268,18 +273,50 @@ __device__ __forceinline__ OpUnit op_unit(const OpArgs &a, int tiles, int u) {
     return w;
 }
 
+// The accumulators as an epilogue warp takes them, one round after another.
+template <class Cfg>
+struct OpAcc {
+    uint64_t *full, *empty;
+    uint32_t base;  // tensor memory, in the warp's lanes
+    uint32_t lane;
+    uint32_t gr;    // rounds taken so far: selects the accumulator and its phase
+    int rounds;     // of the present unit
+    const KernelCtx &ctx;
+
+    __device__ __forceinline__ bool have() const { return rounds > 0; }
+    __device__ __forceinline__ uint32_t row() const { return base + (gr & 1u) * Cfg::BN; }
+    __device__ __forceinline__ bool wait() const {
+        if (rounds == 0) return true;
+        const bool ok = mbar_wait(&full[gr & 1u], (gr >> 1) & 1u, ctx, kSiteEpilogueFull);
+        tc_fence_after();
+        return ok;
+    }
+    __device__ __forceinline__ void release() {
+        if (rounds == 0) return;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+            if constexpr (Cfg::CG == 2)
+                mbar_arrive_cluster(mapa_shared(smem_u32(&empty[gr & 1u]), 0));
+            else
+                mbar_arrive(&empty[gr & 1u]);
+        }
+        ++gr;
+    }
+};
+
 // Epi: a struct of kernel parameters with
-//   template <class Cfg, ...> __device__ bool run(const EpiCtx &, const OpMaps &,
-//        const OpArgs &, const OpUnit &, uint32_t t_row, int col0, bool have,
-//        Wait wait, Release release) const
+//   template <class Cfg, class Acc> __device__ bool run(const EpiCtx &, const OpMaps &,
+//        const OpArgs &, const OpUnit &, Acc acc, int col0) const
+// (acc: OpAcc)
 // called by a whole warp for its 32 rows and the accumulator columns
 // [col0, col0 + EPI_COLS) (DUAL: the output columns [col0, col0 + 64) of both
-// halves, none when col0 >= TILE_N); t_row addresses the accumulator's first
-// column in the warp's lanes.  wait() blocks until the accumulator is complete
-// (false: the wait ran out, run returns false at once); release() hands it
-// back.  Each is called exactly once, in this order, around all reads.
-// have = false (an empty K range): the accumulator is not to be read and
-// counts as zero.
+// halves, none when col0 >= TILE_N).  For each of the unit's `rounds` rounds,
+// wait() blocks until the accumulator is complete (false: the wait ran out, run
+// returns false at once), row() addresses its first column in the warp's lanes
+// and release() hands it back, once each and in this order; without ROUND that
+// is one round, or none (an empty K range: the accumulator counts as zero, and
+// wait and release do nothing).
 template <class Cfg, class Epi>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
     op_gemm_kernel(const __grid_constant__ OpMaps maps, const OpArgs args,
@@ -422,13 +459,17 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             bool ok = true;
             for (int u = slot; ok && u < units; u += slots) {
                 const OpUnit w = op_unit<Cfg>(args, tiles, u);
-                if (w.ke <= w.kb) continue;
+                for (int k_begin = w.kb; ok && k_begin < w.ke;) {
+                const int k_end = Cfg::ROUND > 0 ? min(w.ke, k_begin + Cfg::ROUND) : w.ke;
                 const uint32_t ab = gr & 1u, aph = (gr >> 1) & 1u;
                 ++gr;
-                if (!mbar_wait(&acc_empty[ab], aph ^ 1u, ctx, kSiteMmaAccEmpty)) break;
+                if (!mbar_wait(&acc_empty[ab], aph ^ 1u, ctx, kSiteMmaAccEmpty)) {
+                    ok = false;
+                    break;
+                }
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + ab * BN;
-                for (int kt = w.kb; kt < w.ke; ++kt, ++it) {
+                for (int kt = k_begin; kt < k_end; ++kt, ++it) {
                     const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
                     if (!mbar_wait(&full[s], ph, ctx, kSiteMmaFull)) {
                         ok = false;
@@ -450,7 +491,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                             const uint64_t bd =
                                 Cfg::B_K ? smem_desc_sw128(b_addr + k * 32, 16, 1024)
                                          : smem_desc_sw128(b_addr + k * 2048, BK * 128, 1024);
-                            const uint32_t acc = (kt == w.kb && q == 0 && k == 0) ? 0u : 1u;
+                            const uint32_t acc = (kt == k_begin && q == 0 && k == 0) ? 0u : 1u;
                             if constexpr (Cfg::CG == 2)
                                 umma_f16_ss_pair(d_tmem, ad, bd, idesc, acc);
                             else
@@ -467,6 +508,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                         umma_commit_pair_multicast(&acc_full[ab], kPair);
                     else
                         umma_commit(&acc_full[ab]);
+                }
+                k_begin = k_end;
                 }
             }
             if constexpr (Cfg::CG == 2)
@@ -487,32 +530,14 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         c.M = args.M;
         c.N = args.N;
         c.lane = lane;
-        uint32_t gr = 0;
+        OpAcc<Cfg> acc{acc_full, acc_empty, tmem_base + ((q * 32u) << 16), lane, 0u, 0, ctx};
         for (int u = slot; u < units; u += slots) {
             const OpUnit w = op_unit<Cfg>(args, tiles, u);
-            const bool have = w.ke > w.kb;
-            const uint32_t ab = gr & 1u, aph = (gr >> 1) & 1u;
             c.m0 = w.m0 + crank * BM + static_cast<int>(q * 32);
-            auto wait = [&]() -> bool {
-                if (!have) return true;
-                const bool ok = mbar_wait(&acc_full[ab], aph, ctx, kSiteEpilogueFull);
-                tc_fence_after();
-                return ok;
-            };
-            auto release = [&]() {
-                if (!have) return;
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if constexpr (Cfg::CG == 2)
-                        mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[ab]), 0));
-                    else
-                        mbar_arrive(&acc_empty[ab]);
-                }
-            };
-            const uint32_t t_row = tmem_base + ((q * 32u) << 16) + ab * BN;
-            if (!epi.template run<Cfg>(c, maps, args, w, t_row, col0, have, wait, release)) break;
-            if (have) ++gr;
+            acc.rounds = w.ke <= w.kb     ? 0
+                         : Cfg::ROUND > 0 ? (w.ke - w.kb + Cfg::ROUND - 1) / Cfg::ROUND
+                                          : 1;
+            if (!epi.template run<Cfg>(c, maps, args, w, acc, col0)) break;
         }
         if (lane == 0) bulk_wait_all();  // this warp's stores have landed
         __syncwarp();

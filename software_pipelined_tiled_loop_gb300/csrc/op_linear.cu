@@ -15,14 +15,15 @@ struct EpiLinearGrad {
     long long dz_ld;
     int act;
 
-    template <class Cfg, class Wait, class Rel>
+    template <class Cfg, class Acc>
     __device__ __forceinline__ bool run(const EpiCtx &c, const OpMaps &maps, const OpArgs &,
-                                        const OpUnit &w, uint32_t t_row, int col0, bool have,
-                                        Wait wait, Rel release) const {
+                                        const OpUnit &w, Acc &acc, int col0) const {
         const int nf = w.n0 + col0;
         uint32_t r[32];
         get_rows64(c, dy, dy_ld, nf, r);  // travels while the products finish
-        if (!wait()) return false;
+        if (!acc.wait()) return false;
+        const uint32_t t_row = acc.row();
+        const bool have = acc.have();
 #pragma unroll 1
         for (int cc = 0; cc < Cfg::EPI_COLS; cc += 64) {
             const int n = nf + cc;
@@ -32,7 +33,7 @@ struct EpiLinearGrad {
             for (int h = 0; h < 2; ++h) {
                 uint32_t v[32];
                 acc_cols32(t_row + col0 + cc + 32 * h, have, v);
-                if (h == 1 && cc + 64 >= Cfg::EPI_COLS) release();
+                if (h == 1 && cc + 64 >= Cfg::EPI_COLS) acc.release();
                 if (bias != nullptr) {
                     float b[32];
                     get_vec32(bias, c.N, n + 32 * h, b);

@@ -27,20 +27,21 @@ struct EpiOut {
     int act;
     int tma_out, tma_preact;
 
-    template <class Cfg, class Wait, class Rel>
+    template <class Cfg, class Acc>
     __device__ __forceinline__ bool run(const EpiCtx &c, const OpMaps &maps, const OpArgs &,
-                                        const OpUnit &w, uint32_t t_row, int col0, bool have,
-                                        Wait wait, Rel release) const {
+                                        const OpUnit &w, Acc &acc, int col0) const {
         const int nf = w.n0 + col0;
         if (parts != nullptr) {
-            if (!wait()) return false;
+            if (!acc.wait()) return false;
+        const uint32_t t_row = acc.row();
+        const bool have = acc.have();
             const int row0 = static_cast<int>(
                 (static_cast<long long>(w.part) * parts_segments + w.seg) * parts_rows + c.m0);
 #pragma unroll 1
             for (int cc = 0; cc < Cfg::EPI_COLS; cc += 32) {
                 uint32_t v[32];
                 acc_cols32(t_row + col0 + cc, have, v);
-                if (cc + 32 >= Cfg::EPI_COLS) release();
+                if (cc + 32 >= Cfg::EPI_COLS) acc.release();
                 put_rows32(c, &maps.c[0], nullptr, 0, row0, nf + cc, v);
             }
             return true;
@@ -52,7 +53,9 @@ struct EpiOut {
             // the first columns' residual travels while the products finish
             if (have_r) get_rows64(c, residual, ldo, nf, r);
         }
-        if (!wait()) return false;
+        if (!acc.wait()) return false;
+        const uint32_t t_row = acc.row();
+        const bool have = acc.have();
         const CUtensorMap *map = tma_out ? &maps.c[w.seg] : nullptr;
         uint16_t *o = out[w.seg];
 #pragma unroll 1
@@ -66,7 +69,7 @@ struct EpiOut {
             for (int h = 0; h < 2; ++h) {
                 uint32_t v[32];
                 acc_cols32(t_row + col0 + cc + 32 * h, have, v);
-                if (h == 1 && cc + 64 >= Cfg::EPI_COLS) release();
+                if (h == 1 && cc + 64 >= Cfg::EPI_COLS) acc.release();
                 if constexpr (FULL) {
                     if (bias != nullptr) {
                         float b[32];

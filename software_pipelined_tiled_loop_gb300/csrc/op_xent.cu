@@ -15,6 +15,7 @@
 // (rounded to bf16 once, as an operand of the gradient products).
 //
 // A row whose target lies outside [0, V) does not count: loss 0, gradient 0.
+#include <cuda_fp16.h>
 #include <math_constants.h>
 
 #include "op_gemm.cuh"
@@ -22,64 +23,89 @@
 
 namespace pg {
 
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// Running maximum and sum of one row segment.
+// For statistics: results below 2^-126 of the block's largest count as zero.
+// Probabilities themselves take exp2f, which keeps subnormal results.
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Softmax statistics are kept to base 2: m is the largest L log2(e) of a row's
+// column block, s the block's sum of 2^(L log2(e) - m).
+//
+// Accumulation rounds of 1024 products are added in fp32 registers.  The
+// tensor core truncates its running sum at every step of 16 products, always
+// toward zero: over the 256 steps of D = 4096 that shrinks every logit by some
+// 1e-5 of its size, which the statistics of a whole vocabulary do not average
+// out (lse off by 2e-6 of itself); four rounds of 64 steps and three rounded
+// additions leave a quarter of it.
+//
+// KEEP: the exponentials themselves are stored as fp16, 2^(L log2(e) - m) with
+// the block's own m, so that the gradient pass turns them into P without the
+// logits' product a second time.  They lie in (0, 1] and fp16 carries them to
+// 2^-11 of their size, an eighth of what rounding P to bf16 costs.
+template <bool KEEP>
 struct EpiXentStats {
-    const int64_t *target;
     float *part_m, *part_s;  // [column block][rows]
     long long rows;
-    float *target_logit;     // [rows]
 
-    template <class Cfg, class Wait, class Rel>
-    __device__ __forceinline__ bool run(const EpiCtx &c, const OpMaps &, const OpArgs &,
-                                        const OpUnit &w, uint32_t t_row, int col0, bool have,
-                                        Wait wait, Rel release) const {
+    template <class Cfg, class Acc>
+    __device__ __forceinline__ bool run(const EpiCtx &c, const OpMaps &maps, const OpArgs &,
+                                        const OpUnit &w, Acc &acc, int col0) const {
+        constexpr int COLS = Cfg::EPI_COLS;
         const int n0 = w.n0 + col0;
-        const bool in = c.row() < c.M;
-        // the target's column in this warp's segment (none: out of [0, EPI_COLS))
-        const int64_t y = in ? __ldg(target + c.row()) : -1;
-        const int64_t yc = y - n0;
-        if (!wait()) return false;
-        float m = -CUDART_INF_F, s = 0.0f;
+        float v[COLS];
+#pragma unroll
+        for (int j = 0; j < COLS; ++j) v[j] = 0.0f;
 #pragma unroll 1
-        for (int cc = 0; cc < Cfg::EPI_COLS; cc += 32) {
-            uint32_t v[32];
-            acc_cols32(t_row + col0 + cc, have, v);
-            if (cc + 32 >= Cfg::EPI_COLS) release();
-            const int left = c.N - (n0 + cc);  // columns of the vocabulary in this chunk
-            if (left <= 0) continue;
-            if (left < 32) {
+        for (int r = 0; r < acc.rounds; ++r) {
+            if (!acc.wait()) return false;
+            const uint32_t t_row = acc.row() + col0;
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    if (j >= left) v[j] = __float_as_uint(-CUDART_INF_F);
+            for (int cc = 0; cc < COLS; cc += 16) {
+                uint32_t x[16];
+                tmem_ld_32x32b_x16(t_row + cc, x);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[cc + j] += __uint_as_float(x[j]);
             }
-            float cm = m;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) cm = fmaxf(cm, __uint_as_float(v[j]));
-            // nothing but -inf so far: any finite reference gives exp(-inf) = 0
-            const float ref = cm == -CUDART_INF_F ? 0.0f : cm;
-            s *= exp2f((m - ref) * kLog2e);
-            float t0 = 0.0f, t1 = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-                t0 += exp2f((__uint_as_float(v[j]) - ref) * kLog2e);
-                t1 += exp2f((__uint_as_float(v[j + 1]) - ref) * kLog2e);
-            }
-            s += t0 + t1;
-            m = cm;
-            if (yc >= cc && yc < cc + 32 && y < c.N) {
-                float at = 0.0f;
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    if (j == static_cast<int>(yc) - cc) at = __uint_as_float(v[j]);
-                target_logit[c.row()] = at;
-            }
+            acc.release();
         }
-        if (in && n0 < c.N) {
-            const long long at = static_cast<long long>(n0 / Cfg::EPI_COLS) * rows + c.row();
+        const int left = c.N - n0;  // columns of the vocabulary in this block
+        if (left <= 0) return true;
+        if (left < COLS) {
+#pragma unroll
+            for (int j = 0; j < COLS; ++j)
+                if (j >= left) v[j] = -CUDART_INF_F;
+        }
+        float mx[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+        for (int j = 4; j < COLS; ++j) mx[j & 3] = fmaxf(mx[j & 3], v[j]);
+        const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kLog2e;
+        // nothing but -inf: any finite reference gives sums of zero
+        const float ref = m == -CUDART_INF_F ? 0.0f : m;
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int cc = 0; cc < COLS; cc += 64) {
+            uint32_t p[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                const float a = ex2(fmaf(v[cc + 2 * j], kLog2e, -ref));
+                const float b = ex2(fmaf(v[cc + 2 * j + 1], kLog2e, -ref));
+                s[(2 * j) & 3] += a;
+                s[(2 * j + 1) & 3] += b;
+                if constexpr (KEEP)
+                    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(p[j]) : "f"(b), "f"(a));
+            }
+            if constexpr (KEEP) put_rows64(c, &maps.c[0], nullptr, 0, n0 + cc, p);
+        }
+        if (c.row() < c.M) {
+            const long long at = static_cast<long long>(n0 / COLS) * rows + c.row();
             part_m[at] = m;
-            part_s[at] = s;
+            part_s[at] = (s[0] + s[1]) + (s[2] + s[3]);
         }
         return true;
     }
@@ -92,18 +118,19 @@ struct EpiXentGrad {
     long long v0;              // the piece's first token
     long long V;
 
-    template <class Cfg, class Wait, class Rel>
+    template <class Cfg, class Acc>
     __device__ __forceinline__ bool run(const EpiCtx &c, const OpMaps &maps, const OpArgs &,
-                                        const OpUnit &w, uint32_t t_row, int col0, bool have,
-                                        Wait wait, Rel release) const {
+                                        const OpUnit &w, Acc &acc, int col0) const {
         const int n0 = w.n0 + col0;
         const bool in = c.row() < c.M;
         const int64_t y = in ? __ldg(target + c.row()) : -1;
         const bool counts = y >= 0 && y < V;
-        const float l = counts ? lse[c.row()] : 0.0f;
+        const float l = counts ? lse[c.row()] * kLog2e : 0.0f;
         const float g = counts ? (dloss ? dloss[c.row()] : 1.0f) : 0.0f;
         const int64_t yc = y - v0 - n0;
-        if (!wait()) return false;
+        if (!acc.wait()) return false;
+        const uint32_t t_row = acc.row();
+        const bool have = acc.have();
 #pragma unroll 1
         for (int cc = 0; cc < Cfg::EPI_COLS; cc += 64) {
             uint32_t p[32];
@@ -111,10 +138,10 @@ struct EpiXentGrad {
             for (int h = 0; h < 2; ++h) {
                 uint32_t v[32];
                 acc_cols32(t_row + col0 + cc + 32 * h, have, v);
-                if (h == 1 && cc + 64 >= Cfg::EPI_COLS) release();
+                if (h == 1 && cc + 64 >= Cfg::EPI_COLS) acc.release();
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
-                    float x = exp2f((__uint_as_float(v[j]) - l) * kLog2e);
+                    float x = exp2f(fmaf(__uint_as_float(v[j]), kLog2e, -l));
                     if (yc == cc + 32 * h + j) x -= 1.0f;
                     v[j] = __float_as_uint(counts ? x * g : 0.0f);
                 }
@@ -129,44 +156,146 @@ struct EpiXentGrad {
     }
 };
 
-// lse and loss of a row from its column blocks' (m, s).  A block takes 32 rows
-// (a warp's loads are 128 consecutive bytes), eight warps every eighth column
-// block of them; a running (m, s) each, joined through shared memory.
+// lse and loss of a row from its column blocks' (m, s), and its target's logit
+// as an fp32 dot product of its own (the epilogues would have to pick one of
+// their registers by a runtime index).  A block takes eight rows: 32 threads a
+// row join every 32nd column block (8 adjacent rows make a 32-byte sector),
+// then a warp a row multiplies X[t] by W[target].
 __device__ __forceinline__ void join_ms(float &m, float &s, float m2, float s2) {
     const float n = fmaxf(m, m2);
     const float ref = n == -CUDART_INF_F ? 0.0f : n;
-    s = s * exp2f((m - ref) * kLog2e) + s2 * exp2f((m2 - ref) * kLog2e);
+    s = s * ex2(m - ref) + s2 * ex2(m2 - ref);
     m = n;
 }
 
 __global__ void __launch_bounds__(256)
     xent_join_kernel(const float *part_m, const float *part_s, long long rows, int blocks, int T,
-                     long long V, const int64_t *target, const float *target_logit, float *loss,
-                     float *lse) {
+                     long long V, int D, const OpMat X, const OpMat W, const int64_t *target,
+                     float *loss, float *lse) {
     grid_dependency_wait();
     grid_launch_dependents();
-    __shared__ float sm[8][32], ss[8][32];
+    __shared__ float sm[8][8], ss[8][8], dot[8];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int t = blockIdx.x * 32 + lane;
+    const int r = threadIdx.x & 7;
+    const int t = blockIdx.x * 8 + r;
     float m = -CUDART_INF_F, s = 0.0f;
     if (t < T) {
-#pragma unroll 4
-        for (int b = w; b < blocks; b += 8)
+#pragma unroll 8
+        for (int b = threadIdx.x >> 3; b < blocks; b += 32)
             join_ms(m, s, part_m[b * rows + t], part_s[b * rows + t]);
     }
-    sm[w][lane] = m;
-    ss[w][lane] = s;
-    __syncthreads();
-    if (w == 0 && t < T) {
 #pragma unroll
-        for (int i = 1; i < 8; ++i) join_ms(m, s, sm[i][lane], ss[i][lane]);
-        const float l = m + logf(s);
+    for (int o = 8; o <= 16; o *= 2) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, o);
+        const float s2 = __shfl_xor_sync(0xffffffffu, s, o);
+        join_ms(m, s, m2, s2);
+    }
+    if (lane < 8) {
+        sm[w][lane] = m;
+        ss[w][lane] = s;
+    }
+    {
+        const int tw = blockIdx.x * 8 + w;
+        const int64_t y = tw < T ? target[tw] : -1;
+        if (loss && y >= 0 && y < V) {
+            const uint16_t *x = X.p + tw * X.ld, *e = W.p + y * W.ld;  // 16-byte-aligned rows
+            float d = 0.0f;
+            for (int k = lane * 8; k < D; k += 256) {
+                const uint4 a = *reinterpret_cast<const uint4 *>(x + k);
+                const uint4 b = *reinterpret_cast<const uint4 *>(e + k);
+                const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (k + 2 * i < D) d = fmaf(bf16_lo(aw[i]), bf16_lo(bw[i]), d);
+                    if (k + 2 * i + 1 < D) d = fmaf(bf16_hi(aw[i]), bf16_hi(bw[i]), d);
+                }
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o /= 2) d += __shfl_xor_sync(0xffffffffu, d, o);
+            if (lane == 0) dot[w] = d;
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x < 8 && t < T) {
+        m = sm[0][r];
+        s = ss[0][r];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) join_ms(m, s, sm[i][r], ss[i][r]);
+        const float l = kLn2 * (m + log2f(s));
         const int64_t y = target[t];
         if (lse) lse[t] = l;
-        if (loss) loss[t] = y >= 0 && y < V ? l - target_logit[t] : 0.0f;
+        if (loss) loss[t] = y >= 0 && y < V ? l - dot[r] : 0.0f;
     }
 }
 
+// P from the kept exponentials, in place (fp16 to bf16):
+//   P = (E 2^(m - lse log2(e)) - [v = target]) dloss.
+// Memory-bound, 4 bytes an entry.  A block takes 32 rows x 1024 columns: the
+// factors of its column blocks first (loads of 32 adjacent rows), then 16-byte
+// vectors, a warp 512 adjacent bytes of a row.
+template <int COLS>
+__global__ void __launch_bounds__(256)
+    xent_scale_kernel(uint16_t *P, long long ld, int T, int V, const float *part_m, long long rows,
+                      const float *lse, const int64_t *target, const float *dloss) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    constexpr int NB = 1024 / COLS;
+    __shared__ float f[NB][32], g[32];
+    __shared__ int yc[32];  // the target's column within the block's 1024, or -1
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int across = (V + 1023) / 1024;
+    const int c0 = static_cast<int>(blockIdx.x % across) * 1024;
+    const int row0 = static_cast<int>(blockIdx.x / across) * 32;
+    const int t = row0 + lane;
+    const int64_t y = t < T ? target[t] : -1;
+    const bool counts = y >= 0 && y < V;
+    const float gt = counts ? (dloss ? dloss[t] : 1.0f) : 0.0f;
+    if (w == 0) {
+        g[lane] = gt;
+        yc[lane] = counts && y >= c0 && y < c0 + 1024 ? static_cast<int>(y - c0) : -1;
+    }
+    const float l = counts ? lse[t] * kLog2e : 0.0f;
+    for (int b = w; b < NB; b += 8) {
+        const int col = c0 + b * COLS;
+        f[b][lane] = counts && col < V
+                         ? exp2f(part_m[static_cast<long long>(col / COLS) * rows + t] - l) * gt
+                         : 0.0f;
+    }
+    __syncthreads();
+    // warp w: rows w, w + 8, ...; four vectors of 8 columns a lane and row
+    for (int r = w; r < 32; r += 8) {
+        if (row0 + r >= T) break;
+        uint16_t *row = P + static_cast<long long>(row0 + r) * ld + c0;
+        uint4 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (c0 + i * 256 + lane * 8 < V)
+                x[i] = *reinterpret_cast<const uint4 *>(row + i * 256 + lane * 8);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int col = i * 256 + lane * 8;
+            if (c0 + col >= V) continue;
+            const float fr = f[col / COLS][r];
+            const int hit = yc[r] - col;
+            const uint32_t in[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            uint32_t o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 e = __half22float2(*reinterpret_cast<const __half2 *>(&in[k]));
+                float a = e.x * fr, b = e.y * fr;
+                if (hit == 2 * k) a -= g[r];
+                if (hit == 2 * k + 1) b -= g[r];
+                // a row that does not count is zero whatever its logits were
+                o[k] = g[r] == 0.0f ? 0u : pack_bf16(a, b);
+            }
+            *reinterpret_cast<uint4 *>(row + col) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    }
+}
+
+// rounds of 1024 products for the statistics
+using StatsPair = OpCfg<256, 3, 2, 2, false, true, false, 8>;
+using StatsOne = OpCfg<128, 6, 1, 1, false, true, false, 16>;
 using XentPair = OpCfg<256, 3, 2, 2, false, true>;
 using XentOne = OpCfg<128, 6, 1, 1, false, true>;
 
@@ -197,6 +326,10 @@ static pgemm_status launch_logits(const OpDevice &dev, int T, int cols, int D, c
 // to 8192 tokens x 131072).
 constexpr long long kDefaultWorkspace = 2ll << 30;
 
+// Kept exponentials cost 4 bytes of traffic a logit, computing it again 2 D
+// operations: even near D = 600 at the measured peaks.
+constexpr int kKeepMinD = 640;
+
 static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t *W,
                          const int64_t *target, const float *dloss, float *loss, float *lse,
                          uint16_t *dX, uint16_t *dW, long long workspace, cudaStream_t s) {
@@ -216,7 +349,7 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
                    : PGEMM_ERR_CUDA;
 
     const bool pair = op_use_pair(dev, T, V, 256, 128, 1);
-    const int block_cols = pair ? XentPair::EPI_COLS : XentOne::EPI_COLS;
+    const int block_cols = pair ? StatsPair::EPI_COLS : StatsOne::EPI_COLS;
     const int blocks = (V + block_cols - 1) / block_cols;
     const long long rows = op_round_up(T, 32);
     // vocabulary pieces, whole tiles wide
@@ -243,7 +376,6 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
     }
     const long long at_m = arena.add(blocks * rows * 4);
     const long long at_s = arena.add(blocks * rows * 4);
-    const long long at_t = arena.add(rows * 4);
     const long long at_l = lse ? 0 : arena.add(rows * 4);
     const long long at_p = pieces ? arena.add(piece * T * 2) : 0;
     long long at_x = 0;
@@ -260,17 +392,28 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
     if ((st = rl.run(dev, arena, s)) != PGEMM_OK) return st;
     float *lse_buf = lse ? lse : arena.at<float>(at_l);
 
+    // One piece: its exponentials are kept and P follows from them.
+    const bool keep = pieces == 1 && D >= kKeepMinD;
+    float *part_m = arena.at<float>(at_m), *part_s = arena.at<float>(at_s);
+    uint16_t *P = pieces ? arena.at<uint16_t>(at_p) : nullptr;
     {
         OpMaps maps{};
-        EpiXentStats e{target, arena.at<float>(at_m), arena.at<float>(at_s), rows,
-                       arena.at<float>(at_t)};
-        st = pair ? launch_logits<XentPair>(dev, T, V, D, x, w, 0, maps, e, s)
-                  : launch_logits<XentOne>(dev, T, V, D, x, w, 0, maps, e, s);
+        if (keep) {
+            st = op_encode(&maps.c[0], OpElem::BF16, P, V, T, piece, 64, 32);
+            if (st != PGEMM_OK) return st;
+            const EpiXentStats<true> e{part_m, part_s, rows};
+            st = pair ? launch_logits<StatsPair>(dev, T, V, D, x, w, 0, maps, e, s)
+                      : launch_logits<StatsOne>(dev, T, V, D, x, w, 0, maps, e, s);
+        } else {
+            const EpiXentStats<false> e{part_m, part_s, rows};
+            st = pair ? launch_logits<StatsPair>(dev, T, V, D, x, w, 0, maps, e, s)
+                      : launch_logits<StatsOne>(dev, T, V, D, x, w, 0, maps, e, s);
+        }
         if (st != PGEMM_OK) return st;
-        st = launch_small(xent_join_kernel, dim3((T + 31) / 32), dim3(256), s,
-                          static_cast<const float *>(e.part_m), static_cast<const float *>(e.part_s),
-                          rows, blocks, T, static_cast<long long>(V), target,
-                          static_cast<const float *>(e.target_logit), loss, lse_buf);
+        st = launch_small(xent_join_kernel, dim3((T + 7) / 8), dim3(256), s,
+                          static_cast<const float *>(part_m), static_cast<const float *>(part_s),
+                          rows, blocks, T, static_cast<long long>(V), D, x, w, target, loss,
+                          lse_buf);
         if (st != PGEMM_OK) return st;
     }
 
@@ -278,14 +421,22 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
     for (int i = 0; i < pieces; ++i) {
         const long long v0 = i * piece;
         const int cols = static_cast<int>(V - v0 < piece ? V - v0 : piece);
-        uint16_t *P = arena.at<uint16_t>(at_p);
-        OpMaps maps{};
-        if ((st = op_encode(&maps.c[0], OpElem::BF16, P, cols, T, piece, 64, 32)) != PGEMM_OK)
-            return st;
-        EpiXentGrad e{target, lse_buf, dloss, v0, V};
-        st = op_use_pair(dev, T, cols, 256, 128, 1)
-                 ? launch_logits<XentPair>(dev, T, cols, D, x, w, v0, maps, e, s)
-                 : launch_logits<XentOne>(dev, T, cols, D, x, w, v0, maps, e, s);
+        if (keep) {
+            const dim3 grid(static_cast<unsigned>((V + 1023) / 1024) * ((T + 31) / 32));
+            st = launch_small(pair ? xent_scale_kernel<StatsPair::EPI_COLS>
+                                   : xent_scale_kernel<StatsOne::EPI_COLS>,
+                              grid, dim3(256), s, P, piece, T, V,
+                              static_cast<const float *>(part_m), rows,
+                              static_cast<const float *>(lse_buf), target, dloss);
+        } else {
+            OpMaps maps{};
+            st = op_encode(&maps.c[0], OpElem::BF16, P, cols, T, piece, 64, 32);
+            if (st != PGEMM_OK) return st;
+            const EpiXentGrad e{target, lse_buf, dloss, v0, V};
+            st = op_use_pair(dev, T, cols, 256, 128, 1)
+                     ? launch_logits<XentPair>(dev, T, cols, D, x, w, v0, maps, e, s)
+                     : launch_logits<XentOne>(dev, T, cols, D, x, w, v0, maps, e, s);
+        }
         if (st != PGEMM_OK) return st;
         if (want_x) {
             OpProduct p;

@@ -1,6 +1,8 @@
 """The operators (linear, gated, cross entropy) against their definitions in
 64 bits, forward and backward, at the sizes and values where they can go
 wrong.  Bounds: operator_reference.py."""
+import math
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -198,7 +200,8 @@ def xent_inputs(T, V, D, seed, padded=0.2):
 
 # one token of one; odd vocabularies; tails below and above a tile; pairs
 XENT_SIZES = [(1, 1, 8), (1, 3, 1), (1, 1000, 64), (5, 129, 33), (33, 257, 40), (64, 4096, 64),
-              (130, 1001, 72), (257, 515, 136), (3, 7, 0), (1100, 9000, 64), (2, 50257, 24)]
+              (130, 1001, 72), (257, 515, 136), (3, 7, 0), (1100, 9000, 64), (2, 50257, 24),
+              (65, 1001, 648), (1, 129, 1100), (40, 3000, 2500), (1100, 9001, 704)]
 
 
 @pytest.mark.parametrize("i,size", list(enumerate(XENT_SIZES)))
@@ -287,6 +290,20 @@ def test_xent_infinite_and_nan_logits():
     assert torch.isnan(lse[3]) and torch.isnan(loss[3])
     rest = torch.arange(T, device="cuda") != 3
     assert torch.isfinite(lse[rest]).all() and torch.isfinite(loss[rest]).all()
+
+
+def test_xent_column_blocks_of_nothing_but_minus_infinity():
+    # whole blocks of -inf logits beside a block of very negative ones
+    T, V, D = 9, 1024, 8
+    X = torch.ones(T, D, device="cuda", dtype=torch.bfloat16)
+    W = torch.full((V, D), float("-inf"), device="cuda", dtype=torch.bfloat16)
+    W[512:640] = -40.0
+    y = torch.arange(T, device="cuda") + 512
+    loss, lse = nan_like(T, dtype=torch.float32), nan_like(T, dtype=torch.float32)
+    pg.xent_bf16(T, V, D, X, W, y, loss, lse)
+    want = torch.full((T,), -320.0 + math.log(128), device="cuda")
+    assert torch.allclose(lse, want, rtol=1e-6)
+    assert torch.allclose(loss, torch.full_like(want, math.log(128)), rtol=1e-4)
 
 
 def test_xent_no_tokens():
