@@ -286,16 +286,23 @@ static bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 
 
 static pgemm_status encode_2d(CUtensorMap *map, CUtensorMapDataType type, int elem_bytes,
                               const void *base, long long inner, long long outer, long long ld,
-                              int box_x, int box_y, bool swizzle128) {
+                              int box_x, int box_y, CUtensorMapSwizzle swizzle) {
     cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
     cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * elem_bytes};
     cuuint32_t box[2] = {static_cast<cuuint32_t>(box_x), static_cast<cuuint32_t>(box_y)};
     cuuint32_t estr[2] = {1, 1};
     CUresult r = g_encode(map, type, 2, const_cast<void *>(base), dims, strides, box, estr,
                           CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                          swizzle,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? PGEMM_OK : PGEMM_ERR_CUDA;
+}
+
+static pgemm_status encode_2d(CUtensorMap *map, CUtensorMapDataType type, int elem_bytes,
+                              const void *base, long long inner, long long outer, long long ld,
+                              int box_x, int box_y, bool swizzle128) {
+    return encode_2d(map, type, elem_bytes, base, inner, outer, ld, box_x, box_y,
+                     swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 // Copies rows [0, rows) x [0, cols) of a row-major matrix with pitch `sld` to a
@@ -664,11 +671,18 @@ pgemm_status op_kernel_setup(const OpDevice &dev, const KernelInfo &k, int *slot
     return kernel_setup(*static_cast<DeviceState *>(dev.state), k, &blocks_per_sm, slots);
 }
 
-pgemm_status op_encode(CUtensorMap *map, OpElem type, const void *base, long long inner,
-                       long long outer, long long ld, int box_x, int box_y) {
+pgemm_status op_encode(CUtensorMap *map, const void *base, long long inner, long long outer,
+                       long long ld, int box_y) {
+    return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, inner, outer, ld, 64, box_y,
+                     true);
+}
+
+pgemm_status op_encode_out(CUtensorMap *map, OpElem type, const void *base, long long inner,
+                           long long outer, long long ld) {
     const bool f32 = type == OpElem::F32;
     return encode_2d(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                     f32 ? 4 : 2, base, inner, outer, ld, box_x, box_y, true);
+                     f32 ? 4 : 2, base, inner, outer, ld, f32 ? 16 : 32, 32,
+                     CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 // A block that waits, with a short limit, on an mbarrier nothing arrives on.

@@ -17,39 +17,42 @@ struct EpiGated {
     int tma_h, tma_preact;
 
     template <class Cfg, class Acc>
-    __device__ __forceinline__ bool run(const EpiCtx &c, const OpMaps &maps, const OpArgs &,
-                                        const OpUnit &w, Acc &acc, int col0) const {
-        if (!acc.wait()) return false;
-        const uint32_t t_row = acc.row();
+    __device__ __forceinline__ bool run(EpiCtx &c, const OpMaps &maps, const OpArgs &,
+                                        const OpUnit &w, Acc &acc, uint32_t e) const {
+        int col0, width;
+        const bool mine = epi_cols_dual<Cfg>(w, e, col0, width);
         const bool have = acc.have();
-        if (col0 >= Cfg::TILE_N) {
+        if (!acc.wait()) return false;
+        if (!mine) {
             acc.release();
             return true;
         }
-        const int n = w.n0 + col0;
-        uint32_t p[32];
-#pragma unroll
+        const uint32_t t_row = acc.row() + col0;
+#pragma unroll 1
         for (int k = 0; k < 2; ++k) {
-            uint32_t g[32], u[32];
-            acc_cols32(t_row + col0 + 32 * k, have, g);
-            acc_cols32(t_row + Cfg::TILE_N + col0 + 32 * k, have, u);
+            const int n = w.n0 + col0 + 32 * k;
+            uint32_t g[32], u[32], p[16];
+            acc_cols32(t_row + 32 * k, have, g);
+            acc_cols32(t_row + width + 32 * k, have, u);
             if (k == 1) acc.release();
             if (preact != nullptr) {
-                put_rows32(c, tma_preact ? &maps.c[1] : nullptr, preact, ld, c.m0, n + 32 * k, g);
-                put_rows32(c, tma_preact ? &maps.c[2] : nullptr, preact + ld * c.M, ld, c.m0,
-                           n + 32 * k, u);
+                const CUtensorMap *mg = tma_preact ? &maps.c[1] : nullptr;
+                const CUtensorMap *mu = tma_preact ? &maps.c[2] : nullptr;
+                put_words16(c, mg, preact, ld, c.m0, n, g);
+                put_words16(c, mg, preact, ld, c.m0, n + 16, g + 16);
+                put_words16(c, mu, preact + ld * c.M, ld, c.m0, n, u);
+                put_words16(c, mu, preact + ld * c.M, ld, c.m0, n + 16, u + 16);
             }
             with_act(act, [&](auto A) {
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
-                    p[16 * k + j] =
-                        pack_bf16(act_value<decltype(A)::value>(__uint_as_float(g[2 * j])) *
-                                      __uint_as_float(u[2 * j]),
-                                  act_value<decltype(A)::value>(__uint_as_float(g[2 * j + 1])) *
-                                      __uint_as_float(u[2 * j + 1]));
+                    p[j] = pack_bf16(act_value<decltype(A)::value>(__uint_as_float(g[2 * j])) *
+                                         __uint_as_float(u[2 * j]),
+                                     act_value<decltype(A)::value>(__uint_as_float(g[2 * j + 1])) *
+                                         __uint_as_float(u[2 * j + 1]));
             });
+            put_rows32(c, tma_h ? &maps.c[0] : nullptr, h, ld, n, p);
         }
-        put_rows64(c, tma_h ? &maps.c[0] : nullptr, h, ld, n, p);
         return true;
     }
 };
@@ -65,45 +68,45 @@ struct EpiGatedGrad {
     int act;
 
     template <class Cfg, class Acc>
-    __device__ __forceinline__ bool run(const EpiCtx &c, const OpMaps &maps, const OpArgs &,
-                                        const OpUnit &w, Acc &acc, int col0) const {
-        if (col0 >= Cfg::TILE_N) {
-            if (!acc.wait()) return false;
-        const uint32_t t_row = acc.row();
+    __device__ __forceinline__ bool run(EpiCtx &c, const OpMaps &maps, const OpArgs &,
+                                        const OpUnit &w, Acc &acc, uint32_t e) const {
+        int col0, width;
+        const bool mine = epi_cols_dual<Cfg>(w, e, col0, width);
         const bool have = acc.have();
+        RowsIn in{dh, ld};
+        if (mine) in.load(c, w.n0 + col0);  // travels while the products finish
+        if (!acc.wait()) return false;
+        if (!mine) {
             acc.release();
             return true;
         }
-        const int n = w.n0 + col0;
-        uint32_t r[32], p[32], s[32];
-        get_rows64(c, dh, ld, n, r);
-        if (!acc.wait()) return false;
-        const uint32_t t_row = acc.row();
-        const bool have = acc.have();
-#pragma unroll
+        const uint32_t t_row = acc.row() + col0;
+#pragma unroll 1
         for (int k = 0; k < 2; ++k) {
-            uint32_t g[32], u[32];
-            acc_cols32(t_row + col0 + 32 * k, have, g);
-            acc_cols32(t_row + Cfg::TILE_N + col0 + 32 * k, have, u);
+            const int n = w.n0 + col0 + 32 * k;
+            uint32_t g[32], u[32], r[16], p[16], q[16];
+            acc_cols32(t_row + 32 * k, have, g);
+            acc_cols32(t_row + width + 32 * k, have, u);
             if (k == 1) acc.release();
+            in.take(c, r);
+            if (k == 0) in.load(c, n + 32);
             with_act(act, [&](auto A) {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    const uint32_t y = r[16 * k + j];
-                    const float y0 = bf16_lo(y), y1 = bf16_hi(y);
+                    const float y0 = bf16_lo(r[j]), y1 = bf16_hi(r[j]);
                     float a0, a1;
                     const float d0 =
                         act_value_grad<decltype(A)::value>(__uint_as_float(g[2 * j]), a0);
                     const float d1 =
                         act_value_grad<decltype(A)::value>(__uint_as_float(g[2 * j + 1]), a1);
-                    p[16 * k + j] = pack_bf16(y0 * d0 * __uint_as_float(u[2 * j]),
-                                              y1 * d1 * __uint_as_float(u[2 * j + 1]));
-                    s[16 * k + j] = pack_bf16(y0 * a0, y1 * a1);
+                    p[j] = pack_bf16(y0 * d0 * __uint_as_float(u[2 * j]),
+                                     y1 * d1 * __uint_as_float(u[2 * j + 1]));
+                    q[j] = pack_bf16(y0 * a0, y1 * a1);
                 }
             });
+            put_rows32(c, &maps.c[0], dg, dz_ld, n, p);
+            put_rows32(c, &maps.c[1], du, dz_ld, n, q);
         }
-        put_rows64(c, &maps.c[0], dg, dz_ld, n, p);
-        put_rows64(c, &maps.c[1], du, dz_ld, n, s);
         return true;
     }
 };
@@ -113,9 +116,9 @@ static pgemm_status launch_dual(const OpDevice &dev, int M, int F, int K, const 
                                 const OpMat &Wg, const OpMat &Wu, OpMaps &maps, const Epi &e,
                                 cudaStream_t s) {
     if (K > 0) {
-        pgemm_status st = op_encode(&maps.a[0], OpElem::BF16, X.p, K, M, X.ld, 64, 128);
-        if (st == PGEMM_OK) st = op_encode(&maps.b[0], OpElem::BF16, Wg.p, F, K, Wg.ld, 64, 64);
-        if (st == PGEMM_OK) st = op_encode(&maps.b[1], OpElem::BF16, Wu.p, F, K, Wu.ld, 64, 64);
+        pgemm_status st = op_encode(&maps.a[0], X.p, K, M, X.ld, 128);
+        if (st == PGEMM_OK) st = op_encode(&maps.b[0], Wg.p, F, K, Wg.ld, 64);
+        if (st == PGEMM_OK) st = op_encode(&maps.b[1], Wu.p, F, K, Wu.ld, 64);
         if (st != PGEMM_OK) return st;
     }
     constexpr int TM = Cfg::BM * Cfg::CG;
@@ -169,12 +172,12 @@ static pgemm_status gated_forward(int M, int F, int K, const uint16_t *X, const 
     if (M <= kTokensMax) return op_tokens_gated(dev, M, F, K, x, wg, wu, act, H, preact, s);
     OpMaps maps{};
     EpiGated e{H, preact, F, act, F % 8 == 0, preact != nullptr && F % 4 == 0};
-    if (e.tma_h) st = op_encode(&maps.c[0], OpElem::BF16, H, F, M, F, 64, 32);
+    if (e.tma_h) st = op_encode_out(&maps.c[0], OpElem::BF16, H, F, M, F);
     if (e.tma_preact) {
-        if (st == PGEMM_OK) st = op_encode(&maps.c[1], OpElem::F32, preact, F, M, F, 32, 32);
+        if (st == PGEMM_OK) st = op_encode_out(&maps.c[1], OpElem::F32, preact, F, M, F);
         if (st == PGEMM_OK)
-            st = op_encode(&maps.c[2], OpElem::F32, preact + static_cast<long long>(M) * F, F, M,
-                           F, 32, 32);
+            st = op_encode_out(&maps.c[2], OpElem::F32, preact + static_cast<long long>(M) * F, F,
+                               M, F);
     }
     if (st != PGEMM_OK) return st;
     return launch_dual_size(dev, M, F, K, x, wg, wu, maps, e, s);
@@ -230,9 +233,9 @@ static pgemm_status gated_backward(int M, int F, int K, const uint16_t *X, const
         } else {
             OpMaps maps{};
             EpiGatedGrad e{dH, F, dg_buf, du_buf, dg.ld, act};
-            st = op_encode(&maps.c[0], OpElem::BF16, dg_buf, F, M, dg.ld, 64, 32);
+            st = op_encode_out(&maps.c[0], OpElem::BF16, dg_buf, F, M, dg.ld);
             if (st == PGEMM_OK)
-                st = op_encode(&maps.c[1], OpElem::BF16, du_buf, F, M, du.ld, 64, 32);
+                st = op_encode_out(&maps.c[1], OpElem::BF16, du_buf, F, M, du.ld);
             if (st == PGEMM_OK)
                 st = launch_dual_size(dev, M, F, K, x, wg, wu, maps, e, s);
         }

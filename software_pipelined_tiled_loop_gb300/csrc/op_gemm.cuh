@@ -19,7 +19,8 @@
 //   A M-major   (stored K x M): two boxes of 64 m x 64 k-rows; 8-k-row groups
 //               1024 B apart, the 64-column blocks 8192 B; K = 16 -> + 2048 B.
 //   B N-major   (stored K x N): boxes of 64 n x 64 k-rows, as A M-major.
-//   B K-major   (stored N x K): one box 64 k x columns, as A K-major.
+//   B K-major   (stored N x K): boxes of 64 k x 64 columns below one another,
+//               as A K-major.
 // With a CTA pair (CG = 2) each CTA holds its 128 rows of A and half of B's
 // columns; the pair computes a 256-row tile with one M = 256 MMA.
 //
@@ -54,6 +55,7 @@ struct OpArgs {
     int k_seg;         // K-tiles of one K segment; from k_seg on a[1], b[1]
     int parts;
     int group_m;
+    int half_tiles;    // leftover tiles that run as two half-width units each
 };
 
 // ROUND: K-tiles of one accumulation round (0: all of a unit's K range).  The
@@ -72,6 +74,8 @@ struct OpCfg {
     static constexpr int A_BYTES = A_SUB * KSUB, B_BYTES = B_SUB * KSUB;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int TX_BYTES = STAGE_BYTES * CG;
+    static constexpr bool HALVES = BN == 256 && CG == 2;  // half-width units
+    static constexpr int TX_BYTES_HALF = (A_BYTES + B_BYTES / 2) * CG;
     static constexpr int EPI = 8;
     static constexpr int EPI_COLS = BN / 2;         // accumulator columns of an epilogue warp
     static constexpr int STAGING_BYTES = EPI * 4096;
@@ -88,14 +92,24 @@ struct OpCfg {
 };
 
 // ------------------------------------------------------- epilogue helpers ---
-// Where one epilogue warp works: 32 rows from m0, its staging buffer, the
-// extents it may touch.
+// Where one epilogue warp works: 32 rows from m0, its two 2 KB staging buffers
+// (used in turn, so that a store is still being read by TMA while the next is
+// staged), the extents it may touch.
 struct EpiCtx {
-    uint8_t *buf;   // 4 KB of shared memory, 1024-byte aligned
+    uint8_t *bufs;  // 4 KB of shared memory, 1024-byte aligned
+    uint32_t n;     // blocks staged so far
     int m0;         // first of the warp's 32 rows (may lie beyond M)
     int M, N;
     uint32_t lane;
     __device__ __forceinline__ int row() const { return m0 + static_cast<int>(lane); }
+    // The next buffer, once the store that last used it has been read.  Every
+    // block staged commits one bulk group (empty when no TMA store was made),
+    // so that all but the last group being read means this buffer is free.
+    __device__ __forceinline__ uint32_t next_buf() {
+        if (lane == 0) bulk_wait_read<1>();
+        __syncwarp();
+        return smem_u32(bufs) + (n++ & 1u) * 2048u;
+    }
 };
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -106,125 +120,150 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 __device__ __forceinline__ float bf16_lo(uint32_t p) { return __uint_as_float(p << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
 
-// Store 32 rows x 64 columns of 16-bit values, lane t's row in p[32] (pairs).
-// map != nullptr: one TMA store (clips at the edges); else coalesced 2-byte
-// stores, for pitches TMA cannot describe.
-__device__ __forceinline__ void put_rows64(const EpiCtx &c, const CUtensorMap *map, uint16_t *out,
-                                           long long ld, int col, const uint32_t (&p)[32]) {
+// A staged block is 32 rows of 64 bytes with TMA's 64-byte swizzle: 16-byte
+// chunk j of row r lies at chunk j ^ (r / 2 % 4), so the 8 rows of a store
+// phase cover all banks.
+__device__ __forceinline__ uint32_t staged(uint32_t buf, uint32_t row, uint32_t chunk) {
+    return buf + row * 64u + ((chunk ^ ((row >> 1) & 3u)) << 4);
+}
+__device__ __forceinline__ uint16_t lds_u16(uint32_t a) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts32(uint32_t a, uint32_t v) {
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+
+// Store 32 rows x 32 columns of 16-bit values, lane t's row in p[16] (pairs).
+// map != nullptr: one TMA store (clips at the edges); else coalesced stores of
+// pairs, or of single elements where rows may start on odd ones, for pitches
+// TMA cannot describe.
+__device__ __forceinline__ void put_rows32(EpiCtx &c, const CUtensorMap *map, uint16_t *out,
+                                           long long ld, int col, const uint32_t *p) {
     if (c.m0 >= c.M || col >= c.N) return;
-    const uint32_t sbuf = smem_u32(c.buf);
-    if (c.lane == 0) bulk_wait_read<0>();  // the store that last used the buffer
-    __syncwarp();
+    const uint32_t buf = c.next_buf();
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        sts128(sbuf + c.lane * 128 + ((j ^ (c.lane & 7)) << 4), p[4 * j], p[4 * j + 1],
-               p[4 * j + 2], p[4 * j + 3]);
+    for (int j = 0; j < 4; ++j)
+        sts128(staged(buf, c.lane, j), p[4 * j], p[4 * j + 1], p[4 * j + 2], p[4 * j + 3]);
     if (map != nullptr) {
         fence_proxy_async_smem();
         __syncwarp();
-        if (c.lane == 0) {
-            tma_store_2d(map, c.buf, col, c.m0);
-            bulk_commit();
-        }
+        if (c.lane == 0) tma_store_2d(map, c.bufs + (buf - smem_u32(c.bufs)), col, c.m0);
     } else {
         __syncwarp();
         const int rows = min(32, c.M - c.m0);
-        for (int h = 0; h < 2; ++h) {
-            const int cc = static_cast<int>(c.lane) + 32 * h;
-            if (col + cc < c.N) {
-                uint16_t *o = out + static_cast<long long>(c.m0) * ld + col + cc;
+        uint16_t *o = out + static_cast<long long>(c.m0) * ld + col;
+        if (((ld | (reinterpret_cast<uintptr_t>(out) >> 1)) & 1) == 0) {
+            const uint32_t w = c.lane & 15u, h = c.lane >> 4;  // pair w of rows h, h + 2, ...
+            if (col + 2 * static_cast<int>(w) < c.N) {  // N is even here
 #pragma unroll 4
-                for (int r = 0; r < rows; ++r, o += ld)
-                    *o = *reinterpret_cast<const uint16_t *>(
-                        c.buf + r * 128 + (((cc >> 3) ^ (r & 7)) << 4) + (cc & 7) * 2);
+                for (int r = static_cast<int>(h); r < rows; r += 2)
+                    *reinterpret_cast<uint32_t *>(o + r * ld + 2 * w) =
+                        lds32(staged(buf, r, w >> 2) + (w & 3u) * 4u);
             }
-        }
-        __syncwarp();
-    }
-}
-
-// The same for 32 rows x 32 columns of 32-bit values, v[32] lane t's row.
-__device__ __forceinline__ void put_rows32(const EpiCtx &c, const CUtensorMap *map, float *out,
-                                           long long ld, int row0, int col,
-                                           const uint32_t (&v)[32]) {
-    if (c.m0 >= c.M || col >= c.N) return;
-    const uint32_t sbuf = smem_u32(c.buf);
-    if (c.lane == 0) bulk_wait_read<0>();
-    __syncwarp();
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        sts128(sbuf + c.lane * 128 + ((j ^ (c.lane & 7)) << 4), v[4 * j], v[4 * j + 1],
-               v[4 * j + 2], v[4 * j + 3]);
-    if (map != nullptr) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (c.lane == 0) {
-            tma_store_2d(map, c.buf, col, row0);
-            bulk_commit();
-        }
-    } else {
-        __syncwarp();
-        const int rows = min(32, c.M - c.m0);
-        const int cc = static_cast<int>(c.lane);
-        if (col + cc < c.N) {
-            float *o = out + static_cast<long long>(row0) * ld + col + cc;
-#pragma unroll 4
-            for (int r = 0; r < rows; ++r, o += ld)
-                *o = __uint_as_float(lds32(sbuf + r * 128 + (((cc >> 2) ^ (r & 7)) << 4) +
-                                           (cc & 3) * 4));
-        }
-        __syncwarp();
-    }
-}
-
-// Read 32 rows x 64 columns of bf16, lane t's row into p[32] (zero outside).
-// Rows of 16-byte pitch are read by each lane as 16-byte vectors of its own
-// row; other pitches by coalesced 2-byte loads through the staging buffer.
-__device__ __forceinline__ void get_rows64(const EpiCtx &c, const uint16_t *in, long long ld,
-                                           int col, uint32_t (&p)[32]) {
-    const bool vec = (ld & 7) == 0;
-    if (vec) {
-        const bool row_in = c.row() < c.M;
-        const uint16_t *src = in + static_cast<long long>(c.row()) * ld + col;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            // pitches here are the row lengths rounded up to 8 at least, so a
-            // vector that starts inside a row may be read whole
-            if (row_in && col + 8 * j < c.N) x = *reinterpret_cast<const uint4 *>(src + 8 * j);
-            p[4 * j] = x.x;
-            p[4 * j + 1] = x.y;
-            p[4 * j + 2] = x.z;
-            p[4 * j + 3] = x.w;
-        }
-    } else {
-        const uint32_t sbuf = smem_u32(c.buf);
-        if (c.lane == 0) bulk_wait_read<0>();
-        __syncwarp();
-        const int rows = max(0, min(32, c.M - c.m0));
-        for (int h = 0; h < 2; ++h) {
-            const int cc = static_cast<int>(c.lane) + 32 * h;
-            const uint16_t *src = in + static_cast<long long>(c.m0) * ld + col + cc;
+        } else if (col + static_cast<int>(c.lane) < c.N) {
 #pragma unroll 8
-            for (int r = 0; r < 32; ++r) {
-                uint16_t x = 0;
-                if (r < rows && col + cc < c.N) x = src[static_cast<long long>(r) * ld];
-                *reinterpret_cast<uint16_t *>(c.buf + r * 128 + (((cc >> 3) ^ (r & 7)) << 4) +
-                                              (cc & 7) * 2) = x;
+            for (int r = 0; r < rows; ++r)
+                o[r * ld + c.lane] = lds_u16(staged(buf, r, c.lane >> 3) + (c.lane & 7u) * 2u);
+        }
+    }
+    if (c.lane == 0) bulk_commit();
+    __syncwarp();
+}
+
+// The same for 32 rows x 16 columns of 32-bit values, v[16] lane t's row;
+// row0: the output row of m0.
+__device__ __forceinline__ void put_words16(EpiCtx &c, const CUtensorMap *map, float *out,
+                                            long long ld, int row0, int col, const uint32_t *v) {
+    if (c.m0 >= c.M || col >= c.N) return;
+    const uint32_t buf = c.next_buf();
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        sts128(staged(buf, c.lane, j), v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    if (map != nullptr) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (c.lane == 0) tma_store_2d(map, c.bufs + (buf - smem_u32(c.bufs)), col, row0);
+    } else {
+        __syncwarp();
+        const int rows = min(32, c.M - c.m0);
+        const uint32_t w = c.lane & 15u, h = c.lane >> 4;
+        if (col + static_cast<int>(w) < c.N) {
+            float *o = out + static_cast<long long>(row0) * ld + col + w;
+#pragma unroll 4
+            for (int r = static_cast<int>(h); r < rows; r += 2)
+                o[r * ld] = __uint_as_float(lds32(staged(buf, r, w >> 2) + (w & 3u) * 4u));
+        }
+    }
+    if (c.lane == 0) bulk_commit();
+    __syncwarp();
+}
+
+// Read 32 rows x 32 columns of bf16 in two steps, so that the loads travel
+// while something else is done: load() issues them, take() leaves lane t's row
+// in p[16] (zero outside).  Rows of 16-byte pitch: each lane reads 16-byte
+// vectors of its own row.  Other pitches: a lane reads pairs (w = lane % 16) of
+// rows lane / 16 + 2 i, as two single elements since rows may start on odd ones,
+// and take() turns them through a staging buffer.
+struct RowsIn {
+    const uint16_t *in;
+    long long ld;
+    uint32_t x[16];
+
+    __device__ __forceinline__ bool vec() const { return (ld & 7) == 0; }
+    __device__ __forceinline__ void load(const EpiCtx &c, int col) {
+        if (vec()) {
+            const bool row_in = c.row() < c.M;
+            const uint16_t *src = in + static_cast<long long>(c.row()) * ld + col;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint4 q = make_uint4(0u, 0u, 0u, 0u);
+                // a vector that starts inside a row lies inside the matrix: the
+                // pitch is N, a multiple of 8, or a padded one
+                if (row_in && col + 8 * j < c.N) q = *reinterpret_cast<const uint4 *>(src + 8 * j);
+                x[4 * j] = q.x;
+                x[4 * j + 1] = q.y;
+                x[4 * j + 2] = q.z;
+                x[4 * j + 3] = q.w;
+            }
+        } else {
+            const int cc = col + 2 * static_cast<int>(c.lane & 15u);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int r = c.m0 + 2 * i + static_cast<int>(c.lane >> 4);
+                const uint16_t *src = in + static_cast<long long>(r) * ld + cc;
+                uint32_t lo = 0, hi = 0;
+                if (r < c.M && cc < c.N) lo = src[0];
+                if (r < c.M && cc + 1 < c.N) hi = src[1];
+                x[i] = lo | (hi << 16);
             }
         }
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint4 x = lds_u4(sbuf + c.lane * 128 + ((j ^ (c.lane & 7)) << 4));
-            p[4 * j] = x.x;
-            p[4 * j + 1] = x.y;
-            p[4 * j + 2] = x.z;
-            p[4 * j + 3] = x.w;
-        }
-        __syncwarp();
     }
-}
+    __device__ __forceinline__ void take(EpiCtx &c, uint32_t (&p)[16]) const {
+        if (vec()) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) p[j] = x[j];
+        } else {
+            const uint32_t buf = c.next_buf();
+            const uint32_t w = c.lane & 15u;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                sts32(staged(buf, 2 * i + (c.lane >> 4), w >> 2) + (w & 3u) * 4u, x[i]);
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint4 q = lds_u4(staged(buf, c.lane, j));
+                p[4 * j] = q.x;
+                p[4 * j + 1] = q.y;
+                p[4 * j + 2] = q.z;
+                p[4 * j + 3] = q.w;
+            }
+            if (c.lane == 0) bulk_commit();
+            __syncwarp();
+        }
+    }
+};
 
 // 32 values of a bf16 vector from index col (zero beyond n), the same in
 // every lane.  The vector's base is 16-byte aligned and col a multiple of 32.
@@ -250,27 +289,66 @@ __device__ __forceinline__ void get_vec32(const uint16_t *v, int n, int col, flo
 // One unit as its epilogue sees it.
 struct OpUnit {
     int tile, part, seg;  // seg: N segment (output c[seg])
-    int m0, n0;           // of the cluster's tile
+    int m0, n0;           // of the cluster's tile (n0: of the unit's own columns)
     int kb, ke;
+    bool half;            // a half-width unit: BN / 2 accumulator columns
 };
 
+// Unit u of slot's list: whole tiles slot, slot + slots, ... first, then, when
+// the last wave's R leftover tiles fit twice on the slots, one half-width unit
+// (column half u % 2 of leftover tile u / 2) on each of 2 R slots, so that the
+// last wave is half as long, and so is its epilogue.
 template <class Cfg>
-__device__ __forceinline__ OpUnit op_unit(const OpArgs &a, int tiles, int u) {
-    OpUnit w;
-    w.part = u / tiles;
-    w.tile = u - w.part * tiles;
-    const int per_group = a.group_m * a.n_tiles;
-    const int g = w.tile / per_group;
-    const int first_m = g * a.group_m;
-    const int gm = min(a.m_tiles - first_m, a.group_m);
-    const int r = w.tile - g * per_group;
-    const int nt = r / gm;
-    w.m0 = (first_m + r % gm) * (Cfg::BM * Cfg::CG);
-    w.seg = nt >= a.n_seg ? 1 : 0;
-    w.n0 = (nt - w.seg * a.n_seg) * Cfg::TILE_N;
-    w.kb = static_cast<int>(static_cast<long long>(w.part) * a.k_tiles / a.parts);
-    w.ke = static_cast<int>(static_cast<long long>(w.part + 1) * a.k_tiles / a.parts);
-    return w;
+struct OpWalk {
+    int tiles, whole, slot, slots, units;
+
+    __device__ __forceinline__ OpWalk(const OpArgs &a, int slot_, int slots_)
+        : slot(slot_), slots(slots_) {
+        tiles = a.m_tiles * a.n_tiles;
+        whole = tiles * a.parts - a.half_tiles;
+        units = (slot < whole ? (whole - slot + slots - 1) / slots : 0) +
+                (slot < 2 * a.half_tiles ? 1 : 0);
+    }
+    __device__ __forceinline__ OpUnit unit(const OpArgs &a, int i) const {
+        OpUnit w;
+        int u = slot + i * slots;
+        int h = 0;
+        w.half = u >= whole;
+        if (w.half) {
+            u = whole + (slot >> 1);
+            h = slot & 1;
+        }
+        w.part = u / tiles;
+        w.tile = u - w.part * tiles;
+        const int per_group = a.group_m * a.n_tiles;
+        const int g = w.tile / per_group;
+        const int first_m = g * a.group_m;
+        const int gm = min(a.m_tiles - first_m, a.group_m);
+        const int r = w.tile - g * per_group;
+        const int nt = r / gm;
+        w.m0 = (first_m + r % gm) * (Cfg::BM * Cfg::CG);
+        w.seg = nt >= a.n_seg ? 1 : 0;
+        w.n0 = (nt - w.seg * a.n_seg) * Cfg::TILE_N + h * (Cfg::TILE_N / 2);
+        w.kb = static_cast<int>(static_cast<long long>(w.part) * a.k_tiles / a.parts);
+        w.ke = static_cast<int>(static_cast<long long>(w.part + 1) * a.k_tiles / a.parts);
+        return w;
+    }
+};
+
+// The accumulator columns of a unit that epilogue warp e (of 8) takes:
+// [col0, col0 + cols); cols is a multiple of 64.
+template <class Cfg>
+__device__ __forceinline__ void epi_cols(const OpUnit &w, uint32_t e, int &col0, int &cols) {
+    cols = Cfg::EPI_COLS > 64 && w.half ? Cfg::EPI_COLS / 2 : Cfg::EPI_COLS;
+    col0 = static_cast<int>(e >> 2) * cols;
+}
+// DUAL: 64 output columns a warp, [col0, col0 + 64) of both halves, the halves
+// `width` apart; none for the second four warps of a tile that is no wider.
+template <class Cfg>
+__device__ __forceinline__ bool epi_cols_dual(const OpUnit &w, uint32_t e, int &col0, int &width) {
+    width = w.half ? Cfg::TILE_N / 2 : Cfg::TILE_N;
+    col0 = static_cast<int>(e >> 2) * 64;
+    return col0 < width;
 }
 
 // The accumulators as an epilogue warp takes them, one round after another.
@@ -306,12 +384,11 @@ struct OpAcc {
 };
 
 // Epi: a struct of kernel parameters with
-//   template <class Cfg, class Acc> __device__ bool run(const EpiCtx &, const OpMaps &,
-//        const OpArgs &, const OpUnit &, Acc acc, int col0) const
+//   template <class Cfg, class Acc> __device__ bool run(EpiCtx &, const OpMaps &,
+//        const OpArgs &, const OpUnit &, Acc &acc, int e) const
 // (acc: OpAcc)
-// called by a whole warp for its 32 rows and the accumulator columns
-// [col0, col0 + EPI_COLS) (DUAL: the output columns [col0, col0 + 64) of both
-// halves, none when col0 >= TILE_N).  For each of the unit's `rounds` rounds,
+// called by warp e of the eight epilogue warps for its 32 rows and its columns
+// (epi_cols, epi_cols_dual).  For each of the unit's `rounds` rounds,
 // wait() blocks until the accumulator is complete (false: the wait ran out, run
 // returns false at once), row() addresses its first column in the warp's lanes
 // and release() hands it back, once each and in this order; without ROUND that
@@ -376,16 +453,15 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     const int crank = Cfg::CG == 2 ? static_cast<int>(cluster_ctarank()) : 0;
     const int slot = static_cast<int>(blockIdx.x) / Cfg::CG;
     const int slots = static_cast<int>(gridDim.x) / Cfg::CG;
-    const int tiles = args.m_tiles * args.n_tiles;
-    const int units = tiles * args.parts;
+    const OpWalk<Cfg> walk(args, slot, slots);
 
     if (warp == 0) {
         if (lane == 0) {
             // ---------------- producer ----------------
             uint32_t it = 0;
             bool ok = true;
-            for (int u = slot; ok && u < units; u += slots) {
-                const OpUnit w = op_unit<Cfg>(args, tiles, u);
+            for (int u = 0; ok && u < walk.units; ++u) {
+                const OpUnit w = walk.unit(args, u);
                 const int m0 = w.m0 + crank * BM;
                 for (int kt = w.kb; kt < w.ke; ++kt, ++it) {
                     const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
@@ -397,7 +473,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                     const CUtensorMap *ma = &maps.a[ks];
                     const uint32_t full_lead =
                         Cfg::CG == 2 ? mapa_shared(smem_u32(&full[s]), 0) : smem_u32(&full[s]);
-                    if (crank == 0) mbar_arrive_expect_tx(&full[s], Cfg::TX_BYTES);
+                    if (crank == 0)
+                        mbar_arrive_expect_tx(&full[s], w.half ? Cfg::TX_BYTES_HALF : Cfg::TX_BYTES);
                     auto load = [&](uint8_t *dst, const CUtensorMap *map, int x, int y) {
                         if constexpr (Cfg::CG == 2)
                             tma_load_2d_pair(dst, map, full_lead, x, y);
@@ -416,25 +493,29 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                         } else {
                             load(da, ma, k0, m0);
                         }
+                        const int bc = Cfg::HALVES && w.half ? Cfg::B_COLS / 2 : Cfg::B_COLS;
                         if constexpr (Cfg::DUAL) {
                             // half h of the accumulator reads columns of b[h]; a
                             // pair's CTA h holds exactly that half
 #pragma unroll
                             for (int j = 0; j < Cfg::B_COLS / 64; ++j) {
-                                const int cb = crank * Cfg::B_COLS + 64 * j;  // accumulator column
-                                const int h = cb / Cfg::TILE_N;
-                                load(db + j * (BK * 128), &maps.b[h], w.n0 + cb - h * Cfg::TILE_N,
-                                     k0);
+                                if (64 * j >= bc) break;
+                                const int h = Cfg::CG == 2 ? crank : j / (Cfg::TILE_N / 64);
+                                const int x = Cfg::CG == 2 ? 64 * j : 64 * j - h * Cfg::TILE_N;
+                                load(db + j * (BK * 128), &maps.b[h], w.n0 + x, k0);
                             }
                         } else {
-                            const int nb = w.n0 + crank * Cfg::B_COLS;
+                            const int nb = w.n0 + crank * bc;
                             const CUtensorMap *mb = &maps.b[ks | w.seg];
                             if constexpr (Cfg::B_K) {
-                                load(db, mb, k0, nb);
+                                // boxes of 64 rows (columns of B) below one another
+#pragma unroll
+                                for (int j = 0; j < Cfg::B_COLS / 64; ++j)
+                                    if (64 * j < bc) load(db + j * 8192, mb, k0, nb + 64 * j);
                             } else {
 #pragma unroll
                                 for (int j = 0; j < Cfg::B_COLS / 64; ++j)
-                                    load(db + j * (BK * 128), mb, nb + 64 * j, k0);
+                                    if (64 * j < bc) load(db + j * (BK * 128), mb, nb + 64 * j, k0);
                             }
                         }
                     }
@@ -452,13 +533,16 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     } else if (warp == 1) {
         if (lane == 0 && crank == 0) {
             // ---------------- MMA issuer ----------------
-            constexpr uint32_t idesc = idesc_f16(BM * Cfg::CG, BN, 1, Cfg::A_MN ? 1 : 0,
-                                                 Cfg::B_K ? 0 : 1);
+            constexpr uint32_t idesc_full = idesc_f16(BM * Cfg::CG, BN, 1, Cfg::A_MN ? 1 : 0,
+                                                      Cfg::B_K ? 0 : 1);
+            constexpr uint32_t idesc_half = idesc_f16(BM * Cfg::CG, BN / 2, 1, Cfg::A_MN ? 1 : 0,
+                                                      Cfg::B_K ? 0 : 1);
             constexpr uint16_t kPair = 3;
             uint32_t it = 0, gr = 0;
             bool ok = true;
-            for (int u = slot; ok && u < units; u += slots) {
-                const OpUnit w = op_unit<Cfg>(args, tiles, u);
+            for (int u = 0; ok && u < walk.units; ++u) {
+                const OpUnit w = walk.unit(args, u);
+                const uint32_t idesc = Cfg::HALVES && w.half ? idesc_half : idesc_full;
                 for (int k_begin = w.kb; ok && k_begin < w.ke;) {
                 const int k_end = Cfg::ROUND > 0 ? min(w.ke, k_begin + Cfg::ROUND) : w.ke;
                 const uint32_t ab = gr & 1u, aph = (gr >> 1) & 1u;
@@ -522,22 +606,20 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         // ---------------- epilogue warps ----------------
         const uint32_t e = warp - 2;
         const uint32_t q = warp & 3u;  // the TMEM lane quadrant this warp may read
-        // DUAL: 64 output columns a warp (a 128-byte row of bf16), so with 64-wide
-        // tiles the warps e >= 4 only pass the accumulator on
-        const int col0 = static_cast<int>(e >> 2) * (Cfg::DUAL ? 64 : Cfg::EPI_COLS);
         EpiCtx c;
-        c.buf = sStage + e * 4096;
+        c.bufs = sStage + e * 4096;
+        c.n = 0;
         c.M = args.M;
         c.N = args.N;
         c.lane = lane;
         OpAcc<Cfg> acc{acc_full, acc_empty, tmem_base + ((q * 32u) << 16), lane, 0u, 0, ctx};
-        for (int u = slot; u < units; u += slots) {
-            const OpUnit w = op_unit<Cfg>(args, tiles, u);
+        for (int u = 0; u < walk.units; ++u) {
+            const OpUnit w = walk.unit(args, u);
             c.m0 = w.m0 + crank * BM + static_cast<int>(q * 32);
             acc.rounds = w.ke <= w.kb     ? 0
                          : Cfg::ROUND > 0 ? (w.ke - w.kb + Cfg::ROUND - 1) / Cfg::ROUND
                                           : 1;
-            if (!epi.template run<Cfg>(c, maps, args, w, acc, col0)) break;
+            if (!epi.template run<Cfg>(c, maps, args, w, acc, e)) break;
         }
         if (lane == 0) bulk_wait_all();  // this warp's stores have landed
         __syncwarp();
@@ -623,6 +705,8 @@ static pgemm_status op_launch(const OpDevice &dev, const OpMaps &maps, OpArgs a,
     const long long units = static_cast<long long>(a.m_tiles) * a.n_tiles * a.parts;
     if (units < 1) return PGEMM_OK;
     if (units > 0x7fffffffll) return PGEMM_ERR_INVALID_VALUE;
+    const long long left = units % slots;
+    a.half_tiles = Cfg::HALVES && 2 * left <= slots ? static_cast<int>(left) : 0;
     // Raster groups: down group_m tile rows, then one tile column across, so
     // that the blocks running at once share panels of A and B through L2 (the
     // same widths as the plain products: 16 up to K = 4096, else 8).
@@ -641,7 +725,8 @@ static pgemm_status op_launch(const OpDevice &dev, const OpMaps &maps, OpArgs a,
     }
     cudaLaunchConfig_t lc{};
     lc.blockDim = dim3(Cfg::THREADS);
-    lc.gridDim = dim3(Cfg::CG * static_cast<int>(units < slots ? units : slots));
+    const long long most = units + a.half_tiles;
+    lc.gridDim = dim3(Cfg::CG * static_cast<int>(most < slots ? most : slots));
     lc.dynamicSmemBytes = Cfg::SMEM_BYTES;
     lc.stream = stream;
     lc.attrs = attr;

@@ -24,10 +24,14 @@ pgemm_status op_device(OpDevice *out);  // the current device, set up
 // One-time set-up of a kernel (shared-memory attributes, schedule slots).
 pgemm_status op_kernel_setup(const OpDevice &dev, const KernelInfo &k, int *slots);
 // A 2-D tensor map of 16- or 32-bit elements: `inner` x `outer` with row pitch
-// `ld` (elements), boxes of box_x x box_y with the 128-byte swizzle.
+// `ld` (elements).  op_encode: an operand, boxes of 64 columns x box_y rows with
+// the 128-byte swizzle.  op_encode_out: an output, boxes of 64 bytes x 32 rows
+// with the 64-byte swizzle of the epilogues' staging buffers.
+pgemm_status op_encode(CUtensorMap *map, const void *base, long long inner, long long outer,
+                       long long ld, int box_y);
 enum class OpElem { BF16, F32 };
-pgemm_status op_encode(CUtensorMap *map, OpElem type, const void *base, long long inner,
-                       long long outer, long long ld, int box_x, int box_y);
+pgemm_status op_encode_out(CUtensorMap *map, OpElem type, const void *base, long long inner,
+                           long long outer, long long ld);
 cudaError_t launch_repack(const void *src0, long long sld0, void *dst0, long long dld0, int rows0,
                           int cols0, const void *src1, long long sld1, void *dst1, long long dld1,
                           int rows1, int cols1, int eb, int sm_count, cudaStream_t s);

@@ -16,45 +16,44 @@ struct EpiLinearGrad {
     int act;
 
     template <class Cfg, class Acc>
-    __device__ __forceinline__ bool run(const EpiCtx &c, const OpMaps &maps, const OpArgs &,
-                                        const OpUnit &w, Acc &acc, int col0) const {
+    __device__ __forceinline__ bool run(EpiCtx &c, const OpMaps &maps, const OpArgs &,
+                                        const OpUnit &w, Acc &acc, uint32_t e) const {
+        int col0, cols;
+        epi_cols<Cfg>(w, e, col0, cols);
         const int nf = w.n0 + col0;
-        uint32_t r[32];
-        get_rows64(c, dy, dy_ld, nf, r);  // travels while the products finish
-        if (!acc.wait()) return false;
-        const uint32_t t_row = acc.row();
         const bool have = acc.have();
+        RowsIn in{dy, dy_ld};
+        in.load(c, nf);  // travels while the products finish
+        if (!acc.wait()) return false;
+        const uint32_t t_row = acc.row() + col0;
 #pragma unroll 1
-        for (int cc = 0; cc < Cfg::EPI_COLS; cc += 64) {
+        for (int cc = 0; cc < cols; cc += 32) {
             const int n = nf + cc;
-            uint32_t p[32];
-            if (cc > 0) get_rows64(c, dy, dy_ld, n, r);
+            uint32_t v[32], r[16], p[16];
+            acc_cols32(t_row + cc, have, v);
+            if (cc + 32 >= cols) acc.release();
+            if (bias != nullptr) {
+                float b[32];
+                get_vec32(bias, c.N, n, b);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t v[32];
-                acc_cols32(t_row + col0 + cc + 32 * h, have, v);
-                if (h == 1 && cc + 64 >= Cfg::EPI_COLS) acc.release();
-                if (bias != nullptr) {
-                    float b[32];
-                    get_vec32(bias, c.N, n + 32 * h, b);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        v[j] = __float_as_uint(__uint_as_float(v[j]) + b[j]);
-                }
-                with_act(act, [&](auto A) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        float value;
-                        const uint32_t y = r[16 * h + j];
-                        const float lo = bf16_lo(y) * act_value_grad<decltype(A)::value>(
-                                                          __uint_as_float(v[2 * j]), value);
-                        const float hi = bf16_hi(y) * act_value_grad<decltype(A)::value>(
-                                                          __uint_as_float(v[2 * j + 1]), value);
-                        p[16 * h + j] = pack_bf16(lo, hi);
-                    }
-                });
+                for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + b[j]);
             }
-            put_rows64(c, &maps.c[0], dz, dz_ld, n, p);
+            in.take(c, r);
+            if (cc + 32 < cols) in.load(c, n + 32);
+            with_act(act, [&](auto A) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    float value;
+                    const float lo =
+                        bf16_lo(r[j]) *
+                        act_value_grad<decltype(A)::value>(__uint_as_float(v[2 * j]), value);
+                    const float hi =
+                        bf16_hi(r[j]) *
+                        act_value_grad<decltype(A)::value>(__uint_as_float(v[2 * j + 1]), value);
+                    p[j] = pack_bf16(lo, hi);
+                }
+            });
+            put_rows32(c, &maps.c[0], dz, dz_ld, n, p);
         }
         return true;
     }
@@ -66,10 +65,10 @@ static pgemm_status launch_grad(const OpDevice &dev, int M, int N, int K, const 
     OpMaps maps{};
     pgemm_status st = PGEMM_OK;
     if (K > 0) {
-        st = op_encode(&maps.a[0], OpElem::BF16, X.p, K, M, X.ld, 64, 128);
-        if (st == PGEMM_OK) st = op_encode(&maps.b[0], OpElem::BF16, W.p, N, K, W.ld, 64, 64);
+        st = op_encode(&maps.a[0], X.p, K, M, X.ld, 128);
+        if (st == PGEMM_OK) st = op_encode(&maps.b[0], W.p, N, K, W.ld, 64);
     }
-    if (st == PGEMM_OK) st = op_encode(&maps.c[0], OpElem::BF16, e.dz, N, M, e.dz_ld, 64, 32);
+    if (st == PGEMM_OK) st = op_encode_out(&maps.c[0], OpElem::BF16, e.dz, N, M, e.dz_ld);
     if (st != PGEMM_OK) return st;
     constexpr int TM = Cfg::BM * Cfg::CG;
     OpArgs a{};

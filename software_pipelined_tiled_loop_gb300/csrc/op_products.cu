@@ -28,82 +28,78 @@ struct EpiOut {
     int tma_out, tma_preact;
 
     template <class Cfg, class Acc>
-    __device__ __forceinline__ bool run(const EpiCtx &c, const OpMaps &maps, const OpArgs &,
-                                        const OpUnit &w, Acc &acc, int col0) const {
+    __device__ __forceinline__ bool run(EpiCtx &c, const OpMaps &maps, const OpArgs &,
+                                        const OpUnit &w, Acc &acc, uint32_t e) const {
+        int col0, cols;
+        epi_cols<Cfg>(w, e, col0, cols);
         const int nf = w.n0 + col0;
+        const bool have = acc.have();
         if (parts != nullptr) {
             if (!acc.wait()) return false;
-        const uint32_t t_row = acc.row();
-        const bool have = acc.have();
+            const uint32_t t_row = acc.row() + col0;
             const int row0 = static_cast<int>(
                 (static_cast<long long>(w.part) * parts_segments + w.seg) * parts_rows + c.m0);
 #pragma unroll 1
-            for (int cc = 0; cc < Cfg::EPI_COLS; cc += 32) {
+            for (int cc = 0; cc < cols; cc += 32) {
                 uint32_t v[32];
-                acc_cols32(t_row + col0 + cc, have, v);
-                if (cc + 32 >= Cfg::EPI_COLS) acc.release();
-                put_rows32(c, &maps.c[0], nullptr, 0, row0, nf + cc, v);
+                acc_cols32(t_row + cc, have, v);
+                if (cc + 32 >= cols) acc.release();
+                put_words16(c, &maps.c[0], nullptr, 0, row0, nf + cc, v);
+                put_words16(c, &maps.c[0], nullptr, 0, row0, nf + cc + 16, v + 16);
             }
             return true;
         }
-        uint32_t r[32];
-        bool have_r = false;
-        if constexpr (FULL) {
-            have_r = residual != nullptr;
-            // the first columns' residual travels while the products finish
-            if (have_r) get_rows64(c, residual, ldo, nf, r);
-        }
+        // the residual's next columns travel while the products finish, and then
+        // while the present ones are worked on
+        RowsIn res{residual, ldo};
+        const bool have_r = FULL && residual != nullptr;
+        if (have_r) res.load(c, nf);
         if (!acc.wait()) return false;
-        const uint32_t t_row = acc.row();
-        const bool have = acc.have();
+        const uint32_t t_row = acc.row() + col0;
         const CUtensorMap *map = tma_out ? &maps.c[w.seg] : nullptr;
         uint16_t *o = out[w.seg];
 #pragma unroll 1
-        for (int cc = 0; cc < Cfg::EPI_COLS; cc += 64) {
+        for (int cc = 0; cc < cols; cc += 32) {
             const int n = nf + cc;
-            uint32_t p[32];
+            uint32_t v[32], p[16];
+            acc_cols32(t_row + cc, have, v);
+            if (cc + 32 >= cols) acc.release();
             if constexpr (FULL) {
-                if (have_r && cc > 0) get_rows64(c, residual, ldo, n, r);
-            }
+                if (bias != nullptr) {
+                    float b[32];
+                    get_vec32(bias, c.N, n, b);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t v[32];
-                acc_cols32(t_row + col0 + cc + 32 * h, have, v);
-                if (h == 1 && cc + 64 >= Cfg::EPI_COLS) acc.release();
-                if constexpr (FULL) {
-                    if (bias != nullptr) {
-                        float b[32];
-                        get_vec32(bias, c.N, n + 32 * h, b);
+                    for (int j = 0; j < 32; ++j)
+                        v[j] = __float_as_uint(__uint_as_float(v[j]) + b[j]);
+                }
+                if (preact != nullptr) {
+                    const CUtensorMap *mz = tma_preact ? &maps.c[2] : nullptr;
+                    put_words16(c, mz, preact, ldo, c.m0, n, v);
+                    put_words16(c, mz, preact, ldo, c.m0, n + 16, v + 16);
+                }
+                if (act != PGEMM_ACT_NONE)
+                    with_act(act, [&](auto A) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            v[j] = __float_as_uint(__uint_as_float(v[j]) + b[j]);
-                    }
-                    if (preact != nullptr)
-                        put_rows32(c, tma_preact ? &maps.c[2] : nullptr, preact, ldo, c.m0,
-                                   n + 32 * h, v);
-                    if (act != PGEMM_ACT_NONE)
-                        with_act(act, [&](auto A) {
+                            v[j] = __float_as_uint(
+                                act_value<decltype(A)::value>(__uint_as_float(v[j])));
+                    });
+                if (have_r) {
+                    uint32_t r[16];
+                    res.take(c, r);
+                    if (cc + 32 < cols) res.load(c, n + 32);
 #pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                v[j] = __float_as_uint(
-                                    act_value<decltype(A)::value>(__uint_as_float(v[j])));
-                        });
-                    if (have_r) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            v[2 * j] = __float_as_uint(__uint_as_float(v[2 * j]) +
-                                                       bf16_lo(r[16 * h + j]));
-                            v[2 * j + 1] = __float_as_uint(__uint_as_float(v[2 * j + 1]) +
-                                                           bf16_hi(r[16 * h + j]));
-                        }
+                    for (int j = 0; j < 16; ++j) {
+                        v[2 * j] = __float_as_uint(__uint_as_float(v[2 * j]) + bf16_lo(r[j]));
+                        v[2 * j + 1] =
+                            __float_as_uint(__uint_as_float(v[2 * j + 1]) + bf16_hi(r[j]));
                     }
                 }
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    p[16 * h + j] =
-                        pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
             }
-            put_rows64(c, map, o, ldo, n, p);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                p[j] = pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+            put_rows32(c, map, o, ldo, n, p);
         }
         return true;
     }
@@ -170,12 +166,11 @@ static pgemm_status launch_form(const OpDevice &dev, const OpProduct &p, float *
         const OpMat &b = p.B[(p.k_segments == 2 || p.n_segments == 2) ? j : 0];
         pgemm_status st;
         if (p.K > 0) {
-            st = Cfg::A_MN ? op_encode(&maps.a[j], OpElem::BF16, a.p, p.M, p.K, a.ld, 64, 64)
-                           : op_encode(&maps.a[j], OpElem::BF16, a.p, p.K, p.M, a.ld, 64, 128);
+            st = Cfg::A_MN ? op_encode(&maps.a[j], a.p, p.M, p.K, a.ld, 64)
+                           : op_encode(&maps.a[j], a.p, p.K, p.M, a.ld, 128);
             if (st == PGEMM_OK)
-                st = Cfg::B_K ? op_encode(&maps.b[j], OpElem::BF16, b.p, p.K, p.N, b.ld, 64,
-                                          Cfg::B_COLS)
-                              : op_encode(&maps.b[j], OpElem::BF16, b.p, p.N, p.K, b.ld, 64, 64);
+                st = Cfg::B_K ? op_encode(&maps.b[j], b.p, p.K, p.N, b.ld, 64)
+                              : op_encode(&maps.b[j], b.p, p.N, p.K, b.ld, 64);
             if (st != PGEMM_OK) return st;
         }
     }
@@ -193,20 +188,20 @@ static pgemm_status launch_form(const OpDevice &dev, const OpProduct &p, float *
         e.parts_rows = op_parts_rows(p.M);
         e.parts_segments = p.n_segments;
         const pgemm_status st =
-            op_encode(&maps.c[0], OpElem::F32, parts_area, e.parts_ld,
-                      e.parts_rows * parts * p.n_segments, e.parts_ld, 32, 32);
+            op_encode_out(&maps.c[0], OpElem::F32, parts_area, e.parts_ld,
+                          e.parts_rows * parts * p.n_segments, e.parts_ld);
         if (st != PGEMM_OK) return st;
     } else {
         e.tma_out = p.N % 8 == 0;
         for (int j = 0; e.tma_out && j < p.n_segments; ++j) {
             const pgemm_status st =
-                op_encode(&maps.c[j], OpElem::BF16, p.out[j], p.N, p.M, p.N, 64, 32);
+                op_encode_out(&maps.c[j], OpElem::BF16, p.out[j], p.N, p.M, p.N);
             if (st != PGEMM_OK) return st;
         }
         e.tma_preact = e.preact != nullptr && p.N % 4 == 0;
         if (e.tma_preact) {
             const pgemm_status st =
-                op_encode(&maps.c[2], OpElem::F32, e.preact, p.N, p.M, p.N, 32, 32);
+                op_encode_out(&maps.c[2], OpElem::F32, e.preact, p.N, p.M, p.N);
             if (st != PGEMM_OK) return st;
         }
     }

@@ -345,9 +345,9 @@ static pgemm_status launch_tokens(const OpDevice &dev, TokensArgs a, const OpMat
     TokensMaps maps{};
     if (a.K > 0) {
         if (st == PGEMM_OK)
-            st = op_encode(&maps.x, OpElem::BF16, X.p, a.K, a.M, X.ld, 64, Cfg::TOK);
+            st = op_encode(&maps.x, X.p, a.K, a.M, X.ld, Cfg::TOK);
         for (int d = 0; d < Cfg::NW && st == PGEMM_OK; ++d)
-            st = op_encode(&maps.w[d], OpElem::BF16, W[d].p, a.N, a.K, W[d].ld, 64, 64);
+            st = op_encode(&maps.w[d], W[d].p, a.N, a.K, W[d].ld, 64);
     }
     if (st != PGEMM_OK) return st;
     a.k_tiles = (a.K + Cfg::BK - 1) / Cfg::BK;

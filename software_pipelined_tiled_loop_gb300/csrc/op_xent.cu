@@ -53,9 +53,20 @@ struct EpiXentStats {
     long long rows;
 
     template <class Cfg, class Acc>
-    __device__ __forceinline__ bool run(const EpiCtx &c, const OpMaps &maps, const OpArgs &,
-                                        const OpUnit &w, Acc &acc, int col0) const {
+    __device__ __forceinline__ bool run(EpiCtx &c, const OpMaps &maps, const OpArgs &,
+                                        const OpUnit &w, Acc &acc, uint32_t e) const {
+        // whole column blocks: of a half-width unit the first four warps take
+        // the one it has
         constexpr int COLS = Cfg::EPI_COLS;
+        const int col0 = static_cast<int>(e >> 2) * COLS;
+        if (Cfg::HALVES && w.half && e >= 4) {
+#pragma unroll 1
+            for (int r = 0; r < acc.rounds; ++r) {
+                if (!acc.wait()) return false;
+                acc.release();
+            }
+            return true;
+        }
         const int n0 = w.n0 + col0;
         float v[COLS];
 #pragma unroll
@@ -89,10 +100,10 @@ struct EpiXentStats {
         const float ref = m == -CUDART_INF_F ? 0.0f : m;
         float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int cc = 0; cc < COLS; cc += 64) {
-            uint32_t p[32];
+        for (int cc = 0; cc < COLS; cc += 32) {
+            uint32_t p[16];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
+            for (int j = 0; j < 16; ++j) {
                 const float a = ex2(fmaf(v[cc + 2 * j], kLog2e, -ref));
                 const float b = ex2(fmaf(v[cc + 2 * j + 1], kLog2e, -ref));
                 s[(2 * j) & 3] += a;
@@ -100,7 +111,7 @@ struct EpiXentStats {
                 if constexpr (KEEP)
                     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(p[j]) : "f"(b), "f"(a));
             }
-            if constexpr (KEEP) put_rows64(c, &maps.c[0], nullptr, 0, n0 + cc, p);
+            if constexpr (KEEP) put_rows32(c, &maps.c[0], nullptr, 0, n0 + cc, p);
         }
         if (c.row() < c.M) {
             const long long at = static_cast<long long>(n0 / COLS) * rows + c.row();
@@ -119,9 +130,12 @@ struct EpiXentGrad {
     long long V;
 
     template <class Cfg, class Acc>
-    __device__ __forceinline__ bool run(const EpiCtx &c, const OpMaps &maps, const OpArgs &,
-                                        const OpUnit &w, Acc &acc, int col0) const {
+    __device__ __forceinline__ bool run(EpiCtx &c, const OpMaps &maps, const OpArgs &,
+                                        const OpUnit &w, Acc &acc, uint32_t e) const {
+        int col0, cols;
+        epi_cols<Cfg>(w, e, col0, cols);
         const int n0 = w.n0 + col0;
+        const bool have = acc.have();
         const bool in = c.row() < c.M;
         const int64_t y = in ? __ldg(target + c.row()) : -1;
         const bool counts = y >= 0 && y < V;
@@ -129,28 +143,22 @@ struct EpiXentGrad {
         const float g = counts ? (dloss ? dloss[c.row()] : 1.0f) : 0.0f;
         const int64_t yc = y - v0 - n0;
         if (!acc.wait()) return false;
-        const uint32_t t_row = acc.row();
-        const bool have = acc.have();
+        const uint32_t t_row = acc.row() + col0;
 #pragma unroll 1
-        for (int cc = 0; cc < Cfg::EPI_COLS; cc += 64) {
-            uint32_t p[32];
+        for (int cc = 0; cc < cols; cc += 32) {
+            uint32_t v[32], p[16];
+            acc_cols32(t_row + cc, have, v);
+            if (cc + 32 >= cols) acc.release();
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t v[32];
-                acc_cols32(t_row + col0 + cc + 32 * h, have, v);
-                if (h == 1 && cc + 64 >= Cfg::EPI_COLS) acc.release();
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    float x = exp2f(fmaf(__uint_as_float(v[j]), kLog2e, -l));
-                    if (yc == cc + 32 * h + j) x -= 1.0f;
-                    v[j] = __float_as_uint(counts ? x * g : 0.0f);
-                }
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    p[16 * h + j] =
-                        pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+            for (int j = 0; j < 32; ++j) {
+                float x = exp2f(fmaf(__uint_as_float(v[j]), kLog2e, -l));
+                if (yc == cc + j) x -= 1.0f;
+                v[j] = __float_as_uint(counts ? x * g : 0.0f);
             }
-            put_rows64(c, &maps.c[0], nullptr, 0, n0 + cc, p);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                p[j] = pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+            put_rows32(c, &maps.c[0], nullptr, 0, n0 + cc, p);
         }
         return true;
     }
@@ -304,10 +312,9 @@ static pgemm_status launch_logits(const OpDevice &dev, int T, int cols, int D, c
                                   const OpMat &W, long long v0, OpMaps &maps, const Epi &e,
                                   cudaStream_t s) {
     if (D > 0) {
-        pgemm_status st = op_encode(&maps.a[0], OpElem::BF16, X.p, D, T, X.ld, 64, 128);
+        pgemm_status st = op_encode(&maps.a[0], X.p, D, T, X.ld, 128);
         if (st == PGEMM_OK)
-            st = op_encode(&maps.b[0], OpElem::BF16, W.p + v0 * W.ld, D, cols, W.ld, 64,
-                           Cfg::B_COLS);
+            st = op_encode(&maps.b[0], W.p + v0 * W.ld, D, cols, W.ld, 64);
         if (st != PGEMM_OK) return st;
     }
     constexpr int TM = Cfg::BM * Cfg::CG;
@@ -399,7 +406,7 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
     {
         OpMaps maps{};
         if (keep) {
-            st = op_encode(&maps.c[0], OpElem::BF16, P, V, T, piece, 64, 32);
+            st = op_encode_out(&maps.c[0], OpElem::BF16, P, V, T, piece);
             if (st != PGEMM_OK) return st;
             const EpiXentStats<true> e{part_m, part_s, rows};
             st = pair ? launch_logits<StatsPair>(dev, T, V, D, x, w, 0, maps, e, s)
@@ -430,7 +437,7 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
                               static_cast<const float *>(lse_buf), target, dloss);
         } else {
             OpMaps maps{};
-            st = op_encode(&maps.c[0], OpElem::BF16, P, cols, T, piece, 64, 32);
+            st = op_encode_out(&maps.c[0], OpElem::BF16, P, cols, T, piece);
             if (st != PGEMM_OK) return st;
             const EpiXentGrad e{target, lse_buf, dloss, v0, V};
             st = op_use_pair(dev, T, cols, 256, 128, 1)
