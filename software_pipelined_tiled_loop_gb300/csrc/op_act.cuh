@@ -11,12 +11,13 @@
 // of Mathematical Functions, 7.1.26 (|error| <= 1.5e-7): with x = |z| / sqrt 2
 // and t = 1 / (1 + p x), Phi(-|z|) = (a1 t + ... + a5 t^5) exp(-x^2) / 2, so the
 // far negative side needs no cancelling difference and phi shares the
-// exponential.  erff took the epilogue of a 256 x 256 tile from 3 to 5 us
-// longer than none; this form costs what gelu_tanh does.
-// tanh is taken as 2 s(2y) - 1 and s by one exponential and one fast divide
-// (a few units in the last place of fp32; the results are rounded to bf16).
-// Large arguments: exp overflows to infinity and s to 0, whose limits are the
-// activations' own.
+// exponential.
+// tanh is taken as 2 s(2y) - 1 and s by one ex2.approx and one rcp.approx (a few
+// units in the last place of fp32; the results are rounded to bf16).  Large
+// arguments: the exponential overflows to infinity and s to 0, whose limits are
+// the activations' own.  What bounds an epilogue with an activation is the issue
+// of these instructions (two warps a scheduler, 128 columns a lane), so each is
+// spelled out with as few as it takes.
 #pragma once
 
 #include <type_traits>
@@ -25,37 +26,50 @@
 
 namespace pg {
 
-__device__ __forceinline__ float sigmoid_f32(float z) {
-    return __fdividef(1.0f, 1.0f + __expf(-z));
+// 2^x and 1 / x by the special-function unit, subnormals flushed to zero.
+__device__ __forceinline__ float ex2_ftz(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_ftz(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-// Phi(z) and exp(-z^2 / 2)
-__device__ __forceinline__ float normal_cdf(float z, float &e) {
-    const float x = fabsf(z) * 0.70710678118654752f;
-    const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
-    e = __expf(-0.5f * z * z);
-    float p = fmaf(1.061405429f, t, -1.453152027f);
-    p = fmaf(p, t, 1.421413741f);
-    p = fmaf(p, t, -0.284496736f);
-    p = fmaf(p, t, 0.254829592f);
-    const float h = 0.5f * p * t * e;
-    return z < 0.0f ? h : 1.0f - h;
+// s(x) of the argument scaled by -log2(e): 2^(-x log2 e) overflows to infinity
+// for large negative x, whose reciprocal is 0.
+__device__ __forceinline__ float sigmoid_neg2(float x) { return rcp_ftz(1.0f + ex2_ftz(x)); }
+
+// Phi(-|z|) and e = exp(-z^2 / 2)
+__device__ __forceinline__ float normal_tail(float z, float &e) {
+    const float t = rcp_ftz(fmaf(fabsf(z), 0.3275911f * 0.70710678118654752f, 1.0f));
+    e = ex2_ftz(z * z * -0.72134752044448170f);  // log2(e) / 2
+    float p = fmaf(0.5f * 1.061405429f, t, 0.5f * -1.453152027f);
+    p = fmaf(p, t, 0.5f * 1.421413741f);
+    p = fmaf(p, t, 0.5f * -0.284496736f);
+    p = fmaf(p, t, 0.5f * 0.254829592f);
+    return p * t * e;
 }
 
-// A fast divide returns 0 for divisors beyond 2^126, and exp(-z) of a large
-// negative z is infinite: 1 / inf = 0 either way, so s(z) -> 0.
+// c (z + a z^3) times -2 log2(e), the argument of sigmoid_neg2 for gelu_tanh:
+// (1 + tanh y) / 2 = s(2 y)
+constexpr float kTanhC = -2.0f * 0.79788456080286536f * 1.4426950408889634f;
+
 template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
     if constexpr (ACT == PGEMM_ACT_RELU) {
         return z < 0.0f ? 0.0f : z;  // a NaN stays one
     } else if constexpr (ACT == PGEMM_ACT_GELU) {
+        // z Phi(z) = max(z, 0) - |z| Phi(-|z|) on either side
         float e;
-        return z * normal_cdf(z, e);
+        const float h = normal_tail(z, e);
+        return fmaf(-fabsf(z), h, z < 0.0f ? 0.0f : z);
     } else if constexpr (ACT == PGEMM_ACT_GELU_TANH) {
-        const float y = 0.79788456080286536f * (z + 0.044715f * z * z * z);
-        return z * sigmoid_f32(2.0f * y);
+        return z * sigmoid_neg2(z * fmaf(z * z, kTanhC * 0.044715f, kTanhC));
     } else if constexpr (ACT == PGEMM_ACT_SILU) {
-        return z * sigmoid_f32(z);
+        return z * sigmoid_neg2(z * -1.4426950408889634f);
     } else {
         return z;
     }
@@ -69,20 +83,21 @@ __device__ __forceinline__ float act_value_grad(float z, float &value) {
         return z > 0.0f ? 1.0f : 0.0f;
     } else if constexpr (ACT == PGEMM_ACT_GELU) {
         float e;
-        const float cdf = normal_cdf(z, e);
-        value = z * cdf;
-        return fmaf(z * 0.39894228040143268f, e, cdf);
+        const float h = normal_tail(z, e);
+        value = fmaf(-fabsf(z), h, z < 0.0f ? 0.0f : z);
+        return fmaf(z * 0.39894228040143268f, e, z < 0.0f ? h : 1.0f - h);
     } else if constexpr (ACT == PGEMM_ACT_GELU_TANH) {
         const float z2 = z * z;
-        const float y = 0.79788456080286536f * z * (1.0f + 0.044715f * z2);
-        const float s = sigmoid_f32(2.0f * y);  // (1 + t) / 2; (1 - t^2) / 2 = 2 s (1 - s)
+        const float s = sigmoid_neg2(z * fmaf(z2, kTanhC * 0.044715f, kTanhC));
         value = z * s;
-        const float dy = 0.79788456080286536f * (1.0f + 0.134145f * z2);
+        // s + z (1 - t^2) y' / 2 with (1 - t^2) / 2 = 2 s (1 - s)
+        const float dy = fmaf(z2, 2.0f * 0.79788456080286536f * 0.134145f,
+                              2.0f * 0.79788456080286536f);
         // far out s (1 - s) is 0 before dy overflows; keep 0 * inf away
         const float w = s * (1.0f - s);
-        return w == 0.0f ? s : fmaf(2.0f * z * w, dy, s);
+        return w == 0.0f ? s : fmaf(z * w, dy, s);
     } else if constexpr (ACT == PGEMM_ACT_SILU) {
-        const float s = sigmoid_f32(z);
+        const float s = sigmoid_neg2(z * -1.4426950408889634f);
         value = z * s;
         return s * fmaf(z, 1.0f - s, 1.0f);
     } else {
