@@ -17,7 +17,7 @@ struct EpiGated {
     int tma_h, tma_preact;
 
     template <class Cfg, class Acc>
-    __device__ __forceinline__ bool run(EpiCtx &c, const OpMaps &maps, const OpArgs &,
+    __device__ __forceinline__ bool run(EpiCtx<Cfg::NBUF> &c, const OpMaps &maps, const OpArgs &,
                                         const OpUnit &w, Acc &acc, uint32_t e) const {
         int col0, width;
         const bool mine = epi_cols_dual<Cfg>(w, e, col0, width);
@@ -28,30 +28,46 @@ struct EpiGated {
             return true;
         }
         const uint32_t t_row = acc.row() + col0;
-#pragma unroll 1
-        for (int k = 0; k < 2; ++k) {
-            const int n = w.n0 + col0 + 32 * k;
-            uint32_t g[32], u[32], p[16];
-            acc_cols32(t_row + 32 * k, have, g);
-            acc_cols32(t_row + width + 32 * k, have, u);
-            if (k == 1) acc.release();
-            if (preact != nullptr) {
-                const CUtensorMap *mg = tma_preact ? &maps.c[1] : nullptr;
-                const CUtensorMap *mu = tma_preact ? &maps.c[2] : nullptr;
-                put_words16(c, mg, preact, ld, c.m0, n, g);
-                put_words16(c, mg, preact, ld, c.m0, n + 16, g + 16);
-                put_words16(c, mu, preact + ld * c.M, ld, c.m0, n, u);
-                put_words16(c, mu, preact + ld * c.M, ld, c.m0, n + 16, u + 16);
+        const int n0 = w.n0 + col0;
+        uint32_t g[2][32], u[2][32], p[32];
+        if (have) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                tmem_ld_32x32b_x32(t_row + 32 * k, g[k]);
+                tmem_ld_32x32b_x32(t_row + width + 32 * k, u[k]);
             }
-            with_act(act, [&](auto A) {
+            tmem_ld_wait();
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) g[0][j] = g[1][j] = u[0][j] = u[1][j] = 0u;
+        }
+        acc.release();
+        if (preact != nullptr) {
+            const CUtensorMap *mg = tma_preact ? &maps.c[1] : nullptr;
+            const CUtensorMap *mu = tma_preact ? &maps.c[2] : nullptr;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                put_words16(c, mg, preact, ld, c.m0, n0 + 16 * k, g[k / 2] + 16 * (k % 2));
+                put_words16(c, mu, preact + ld * c.M, ld, c.m0, n0 + 16 * k,
+                            u[k / 2] + 16 * (k % 2));
+            }
+        }
+        with_act(act, [&](auto A) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
-                    p[j] = pack_bf16(act_value<decltype(A)::value>(__uint_as_float(g[2 * j])) *
-                                         __uint_as_float(u[2 * j]),
-                                     act_value<decltype(A)::value>(__uint_as_float(g[2 * j + 1])) *
-                                         __uint_as_float(u[2 * j + 1]));
-            });
-            put_rows32(c, tma_h ? &maps.c[0] : nullptr, h, ld, n, p);
+                    p[16 * k + j] = pack_bf16(
+                        act_value<decltype(A)::value>(__uint_as_float(g[k][2 * j])) *
+                            __uint_as_float(u[k][2 * j]),
+                        act_value<decltype(A)::value>(__uint_as_float(g[k][2 * j + 1])) *
+                            __uint_as_float(u[k][2 * j + 1]));
+        });
+        if (tma_h) {
+            put_rows32_batch<2>(c, &maps.c[0], n0, p);
+        } else {
+            put_rows32(c, nullptr, h, ld, n0, p);
+            put_rows32(c, nullptr, h, ld, n0 + 32, p + 16);
         }
         return true;
     }
@@ -68,7 +84,7 @@ struct EpiGatedGrad {
     int act;
 
     template <class Cfg, class Acc>
-    __device__ __forceinline__ bool run(EpiCtx &c, const OpMaps &maps, const OpArgs &,
+    __device__ __forceinline__ bool run(EpiCtx<Cfg::NBUF> &c, const OpMaps &maps, const OpArgs &,
                                         const OpUnit &w, Acc &acc, uint32_t e) const {
         int col0, width;
         const bool mine = epi_cols_dual<Cfg>(w, e, col0, width);

@@ -61,8 +61,9 @@ struct OpArgs {
 // ROUND: K-tiles of one accumulation round (0: all of a unit's K range).  The
 // accumulator is handed to the epilogue after every round and starts again at
 // zero; the epilogue adds the rounds in fp32 registers.
+// NBUF: staging buffers of an epilogue warp.
 template <int BN_, int STAGES_, int KSUB_, int CG_, bool A_MN_, bool B_K_, bool DUAL_ = false,
-          int ROUND_ = 0>
+          int ROUND_ = 0, int NBUF_ = 2>
 struct OpCfg {
     static constexpr int BM = 128, BN = BN_, BK = 64, STAGES = STAGES_, KSUB = KSUB_, CG = CG_;
     static constexpr bool A_MN = A_MN_, B_K = B_K_, DUAL = DUAL_;
@@ -78,7 +79,8 @@ struct OpCfg {
     static constexpr int TX_BYTES_HALF = (A_BYTES + B_BYTES / 2) * CG;
     static constexpr int EPI = 8;
     static constexpr int EPI_COLS = BN / 2;         // accumulator columns of an epilogue warp
-    static constexpr int STAGING_BYTES = EPI * 4096;
+    static constexpr int NBUF = NBUF_;
+    static constexpr int STAGING_BYTES = EPI * NBUF * 2048;
     static constexpr int TMEM_COLS = 2 * BN;
     static constexpr int THREADS = 64 + 32 * EPI;
     static constexpr int STAGING_OFFSET = STAGES * STAGE_BYTES;
@@ -92,11 +94,13 @@ struct OpCfg {
 };
 
 // ------------------------------------------------------- epilogue helpers ---
-// Where one epilogue warp works: 32 rows from m0, its two 2 KB staging buffers
-// (used in turn, so that a store is still being read by TMA while the next is
+// Where one epilogue warp works: 32 rows from m0, its NB 2 KB staging buffers
+// (used in turn, so that stores are still being read by TMA while the next is
 // staged), the extents it may touch.
+template <int NB_>
 struct EpiCtx {
-    uint8_t *bufs;  // 4 KB of shared memory, 1024-byte aligned
+    static constexpr int NB = NB_;
+    uint8_t *bufs;  // 1024-byte aligned
     uint32_t n;     // blocks staged so far
     int m0;         // first of the warp's 32 rows (may lie beyond M)
     int M, N;
@@ -104,11 +108,19 @@ struct EpiCtx {
     __device__ __forceinline__ int row() const { return m0 + static_cast<int>(lane); }
     // The next buffer, once the store that last used it has been read.  Every
     // block staged commits one bulk group (empty when no TMA store was made),
-    // so that all but the last group being read means this buffer is free.
-    __device__ __forceinline__ uint32_t next_buf() {
-        if (lane == 0) bulk_wait_read<1>();
+    // so that all but the last NB - 1 groups being read means this buffer is
+    // free.  free(B): the next B buffers are.
+    template <int B>
+    __device__ __forceinline__ void free() {
+        if (lane == 0) bulk_wait_read<NB - B>();
         __syncwarp();
-        return smem_u32(bufs) + (n++ & 1u) * 2048u;
+    }
+    __device__ __forceinline__ uint32_t take_buf() {
+        return smem_u32(bufs) + (n++ % NB) * 2048u;
+    }
+    __device__ __forceinline__ uint32_t next_buf() {
+        free<1>();
+        return take_buf();
     }
 };
 
@@ -139,7 +151,8 @@ __device__ __forceinline__ void sts32(uint32_t a, uint32_t v) {
 // map != nullptr: one TMA store (clips at the edges); else coalesced stores of
 // pairs, or of single elements where rows may start on odd ones, for pitches
 // TMA cannot describe.
-__device__ __forceinline__ void put_rows32(EpiCtx &c, const CUtensorMap *map, uint16_t *out,
+template <class Ctx>
+__device__ __forceinline__ void put_rows32(Ctx &c, const CUtensorMap *map, uint16_t *out,
                                            long long ld, int col, const uint32_t *p) {
     if (c.m0 >= c.M || col >= c.N) return;
     const uint32_t buf = c.next_buf();
@@ -172,9 +185,41 @@ __device__ __forceinline__ void put_rows32(EpiCtx &c, const CUtensorMap *map, ui
     __syncwarp();
 }
 
+// B such blocks side by side (p[16 B]) by TMA: one fence and one wait for all.
+template <int B, class Ctx>
+__device__ __forceinline__ void put_rows32_batch(Ctx &c, const CUtensorMap *map, int col,
+                                                 const uint32_t *p) {
+    static_assert(B <= Ctx::NB, "staging buffers");
+    if (c.m0 >= c.M || col >= c.N) return;
+    c.template free<B>();
+    uint32_t buf[B];
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+        buf[b] = c.take_buf();
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            sts128(staged(buf[b], c.lane, j), p[16 * b + 4 * j], p[16 * b + 4 * j + 1],
+                   p[16 * b + 4 * j + 2], p[16 * b + 4 * j + 3]);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (c.lane == 0) {
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            if (col + 32 * b < c.N)
+                tma_store_2d(map, c.bufs + (buf[b] - smem_u32(c.bufs)), col + 32 * b, c.m0);
+        }
+        // one group holds all B stores; the others keep the count
+#pragma unroll
+        for (int b = 0; b < B; ++b) bulk_commit();
+    }
+    __syncwarp();
+}
+
 // The same for 32 rows x 16 columns of 32-bit values, v[16] lane t's row;
 // row0: the output row of m0.
-__device__ __forceinline__ void put_words16(EpiCtx &c, const CUtensorMap *map, float *out,
+template <class Ctx>
+__device__ __forceinline__ void put_words16(Ctx &c, const CUtensorMap *map, float *out,
                                             long long ld, int row0, int col, const uint32_t *v) {
     if (c.m0 >= c.M || col >= c.N) return;
     const uint32_t buf = c.next_buf();
@@ -212,7 +257,8 @@ struct RowsIn {
     uint32_t x[16];
 
     __device__ __forceinline__ bool vec() const { return (ld & 7) == 0; }
-    __device__ __forceinline__ void load(const EpiCtx &c, int col) {
+    template <class Ctx>
+    __device__ __forceinline__ void load(const Ctx &c, int col) {
         if (vec()) {
             const bool row_in = c.row() < c.M;
             const uint16_t *src = in + static_cast<long long>(c.row()) * ld + col;
@@ -240,7 +286,8 @@ struct RowsIn {
             }
         }
     }
-    __device__ __forceinline__ void take(EpiCtx &c, uint32_t (&p)[16]) const {
+    template <class Ctx>
+    __device__ __forceinline__ void take(Ctx &c, uint32_t (&p)[16]) const {
         if (vec()) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) p[j] = x[j];
@@ -384,7 +431,7 @@ struct OpAcc {
 };
 
 // Epi: a struct of kernel parameters with
-//   template <class Cfg, class Acc> __device__ bool run(EpiCtx &, const OpMaps &,
+//   template <class Cfg, class Acc> __device__ bool run(EpiCtx<Cfg::NBUF> &, const OpMaps &,
 //        const OpArgs &, const OpUnit &, Acc &acc, int e) const
 // (acc: OpAcc)
 // called by warp e of the eight epilogue warps for its 32 rows and its columns
@@ -606,8 +653,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         // ---------------- epilogue warps ----------------
         const uint32_t e = warp - 2;
         const uint32_t q = warp & 3u;  // the TMEM lane quadrant this warp may read
-        EpiCtx c;
-        c.bufs = sStage + e * 4096;
+        EpiCtx<Cfg::NBUF> c;
+        c.bufs = sStage + e * (Cfg::NBUF * 2048);
         c.n = 0;
         c.M = args.M;
         c.N = args.N;

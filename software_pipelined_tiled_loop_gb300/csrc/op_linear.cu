@@ -16,7 +16,7 @@ struct EpiLinearGrad {
     int act;
 
     template <class Cfg, class Acc>
-    __device__ __forceinline__ bool run(EpiCtx &c, const OpMaps &maps, const OpArgs &,
+    __device__ __forceinline__ bool run(EpiCtx<Cfg::NBUF> &c, const OpMaps &maps, const OpArgs &,
                                         const OpUnit &w, Acc &acc, uint32_t e) const {
         int col0, cols;
         epi_cols<Cfg>(w, e, col0, cols);

@@ -26,9 +26,10 @@ struct EpiOut {
     int parts_segments;
     int act;
     int tma_out, tma_preact;
+    int plain;  // no bias, activation, residual or kept pre-activation
 
     template <class Cfg, class Acc>
-    __device__ __forceinline__ bool run(EpiCtx &c, const OpMaps &maps, const OpArgs &,
+    __device__ __forceinline__ bool run(EpiCtx<Cfg::NBUF> &c, const OpMaps &maps, const OpArgs &,
                                         const OpUnit &w, Acc &acc, uint32_t e) const {
         int col0, cols;
         epi_cols<Cfg>(w, e, col0, cols);
@@ -49,15 +50,35 @@ struct EpiOut {
             }
             return true;
         }
-        // the residual's next columns travel while the products finish, and then
-        // while the present ones are worked on
+        const CUtensorMap *map = tma_out ? &maps.c[w.seg] : nullptr;
+        uint16_t *o = out[w.seg];
+        if (plain && map != nullptr && have && cols == Cfg::EPI_COLS) {
+            // nothing but rounding: read the whole accumulator at once, hand it
+            // back, and stage as much as fits in one go
+            if (!acc.wait()) return false;
+            const uint32_t t_row = acc.row() + col0;
+            constexpr int C = Cfg::EPI_COLS / 32, B = C < Cfg::NBUF ? C : Cfg::NBUF;
+            uint32_t v[32 * C];
+#pragma unroll
+            for (int b = 0; b < C; ++b)
+                tmem_ld_32x32b_x32(t_row + 32 * b, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * b));
+            tmem_ld_wait();
+            acc.release();
+#pragma unroll
+            for (int j = 0; j < 16 * C; ++j)
+                v[j] = pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+#pragma unroll
+            for (int b = 0; b < C; b += B)
+                put_rows32_batch<B>(c, map, nf + 32 * b, v + 16 * b);
+            return true;
+        }
+        // 32 columns at a time.  The residual's next columns travel while the
+        // products finish, and then while the present ones are worked on.
         RowsIn res{residual, ldo};
         const bool have_r = FULL && residual != nullptr;
         if (have_r) res.load(c, nf);
         if (!acc.wait()) return false;
         const uint32_t t_row = acc.row() + col0;
-        const CUtensorMap *map = tma_out ? &maps.c[w.seg] : nullptr;
-        uint16_t *o = out[w.seg];
 #pragma unroll 1
         for (int cc = 0; cc < cols; cc += 32) {
             const int n = nf + cc;
@@ -183,6 +204,7 @@ static pgemm_status launch_form(const OpDevice &dev, const OpProduct &p, float *
     e.out[1] = p.out[1];
     e.ldo = p.N;
     e.parts = parts_area;
+    e.plain = !e.bias && !e.residual && !e.preact && e.act == PGEMM_ACT_NONE;
     if (parts_area != nullptr) {
         e.parts_ld = op_parts_ld(p.N);
         e.parts_rows = op_parts_rows(p.M);
@@ -221,12 +243,22 @@ static pgemm_status launch_form(const OpDevice &dev, const OpProduct &p, float *
 
 template <bool A_MN, bool B_K>
 using PairCfg = OpCfg<256, 3, 2, 2, A_MN, B_K>;
+// Short K: a unit's epilogue takes longer than its products, so the ring gives
+// up a sixth for staging buffers that hold a warp's whole output (four instead
+// of two).  8192 x 8192 outputs, us with this and with three 128-column stages:
+// K = 64 35.2 against 43.5, K = 256 41.7 against 50.9, K = 512 57.0 against
+// 55.8, K = 2048 (4096 x 4096) 46.4 against 42.0.
+constexpr int kShortK = 384;
+template <bool A_MN, bool B_K>
+using ShortCfg = OpCfg<256, 5, 1, 2, A_MN, B_K, false, 0, 4>;
 template <bool A_MN, bool B_K>
 using OneCfg = OpCfg<128, 6, 1, 1, A_MN, B_K>;
 
 template <bool FULL, bool A_MN, bool B_K>
 static pgemm_status launch_size(const OpDevice &dev, const OpProduct &p, float *area,
                                 const OpPlan &plan, cudaStream_t s) {
+    if (plan.pair && static_cast<long long>(p.K) * p.k_segments <= kShortK)
+        return launch_form<ShortCfg<A_MN, B_K>, FULL>(dev, p, area, plan.parts, s);
     return plan.pair ? launch_form<PairCfg<A_MN, B_K>, FULL>(dev, p, area, plan.parts, s)
                      : launch_form<OneCfg<A_MN, B_K>, FULL>(dev, p, area, plan.parts, s);
 }

@@ -53,7 +53,7 @@ struct EpiXentStats {
     long long rows;
 
     template <class Cfg, class Acc>
-    __device__ __forceinline__ bool run(EpiCtx &c, const OpMaps &maps, const OpArgs &,
+    __device__ __forceinline__ bool run(EpiCtx<Cfg::NBUF> &c, const OpMaps &maps, const OpArgs &,
                                         const OpUnit &w, Acc &acc, uint32_t e) const {
         // whole column blocks: of a half-width unit the first four warps take
         // the one it has
@@ -130,7 +130,7 @@ struct EpiXentGrad {
     long long V;
 
     template <class Cfg, class Acc>
-    __device__ __forceinline__ bool run(EpiCtx &c, const OpMaps &maps, const OpArgs &,
+    __device__ __forceinline__ bool run(EpiCtx<Cfg::NBUF> &c, const OpMaps &maps, const OpArgs &,
                                         const OpUnit &w, Acc &acc, uint32_t e) const {
         int col0, cols;
         epi_cols<Cfg>(w, e, col0, cols);
