@@ -296,9 +296,11 @@ PGEMM_API pgemm_status xent_bf16(int T, int V, int D, const uint16_t *X, const u
  * P[t][v] = (exp(L[t][v] - lse[t]) - (v == target[t])) * dloss[t] (rounded to
  * bf16, as the products' operand; dloss NULL: ones; rows that do not count:
  * zero), dX (T x D) <- P W and dW (V x D) <- P^T X.  Either may be NULL.
- * workspace_bytes bounds the scratch that holds P (0: the library's choice,
- * 2 GiB): a larger P goes by in pieces of the vocabulary.  Results of
- * different bounds differ only in the order of fp32 sums. */
+ * workspace_bytes bounds the scratch that holds P, 2 T V bytes, or with
+ * T <= 64 the logits and P, 6 T V bytes (0: the library's choice, 2 GiB); more
+ * than that goes by in pieces of the vocabulary, whose logits are computed a
+ * second time.  Results under different bounds agree to the rounding of fp32
+ * sums and of P. */
 PGEMM_API pgemm_status xent_bf16_grad(int T, int V, int D, const uint16_t *X, const uint16_t *W,
                                       const int64_t *target, const float *dloss, float *loss,
                                       float *lse, uint16_t *dX, uint16_t *dW,

@@ -248,8 +248,12 @@ def gemm_i8_ex(M, N, K, alpha, A, B, beta, C, config=None, stream=None):
 def _operand(x, name, count, itemsize) -> int:
     """_ptr of an operator's operand, which must hold at least ``count``
     elements of ``itemsize`` bytes (checked for tensors; None passes)."""
-    if x is None or isinstance(x, int):
-        return x or 0
+    try:
+        if (x.is_cuda and x.element_size() == itemsize and x.numel() >= count
+                and x.is_contiguous()):
+            return x.data_ptr()
+    except AttributeError:
+        return _ptr(x)  # None, a raw pointer, or nothing that has an address
     p = _ptr(x)
     if x.element_size() != itemsize:
         raise ValueError(f"{name}: elements of {x.element_size()} bytes, {itemsize} wanted")

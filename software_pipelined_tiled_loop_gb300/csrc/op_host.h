@@ -150,7 +150,7 @@ pgemm_status op_tokens_gated(const OpDevice &dev, int M, int F, int K, const OpM
                              float *preact, cudaStream_t s);
 
 // Parts a product of these sizes would be split into (parts_area: M padded to
-// 256 rows, N to 64 columns, one such matrix a part and segment).
+// 32 rows, N to 64 columns, one such matrix a part and segment).
 int op_product_parts(const OpDevice &dev, int M, int N, int K, int segments);
 long long op_parts_ld(int N);
 long long op_parts_rows(int M);

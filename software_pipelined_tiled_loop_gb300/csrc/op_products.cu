@@ -132,7 +132,7 @@ struct EpiOut {
 // tiles on single CTAs kOneStep (they do half the work at a lower rate: each
 // operand panel feeds half as many products).  Parts along K shorten the
 // waves and add the join's traffic: parts * M * N fp32 values written and read.
-constexpr double kStepUs = 0.36, kOneStep = 0.65;
+constexpr double kStepUs = 0.36, kOneStep = 0.65, kHalfWave = 0.6;
 struct OpPlan {
     bool pair;
     int parts;
@@ -146,10 +146,12 @@ static OpPlan plan_product(int sm_count, long long M, long long N, long long K, 
         const long long bm = pair ? 256 : 128;
         const long long tiles = ((M + bm - 1) / bm) * ((N + bm - 1) / bm) * segments;
         const long long slots = pair ? sm_count / 2 : sm_count;
-        const int most = split ? 32 : 1;
-        for (int parts = 1; parts <= most; ++parts) {
-            if (parts > 1 && steps / parts < 8) break;
-            const double waves = static_cast<double>((tiles * parts + slots - 1) / slots);
+        for (const int parts : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
+            if (parts > 1 && (!split || steps / parts < 8)) break;
+            // a pair's leftover tiles run as half-width units where those fit
+            const long long units = tiles * parts, left = units % slots;
+            double waves = static_cast<double>(units / slots);
+            if (left > 0) waves += pair && 2 * left <= slots ? kHalfWave : 1.0;
             double us = waves * ((pair ? 1.0 : kOneStep) * kStepUs * ((steps + parts - 1) / parts) + 1.0);
             if (parts > 1) us += 4.0 + parts * 8e-6 * M * N * segments / 5.0;
             if (us < best_us * 0.999) {
@@ -166,15 +168,17 @@ bool op_use_pair(const OpDevice &dev, long long M, long long N, long long pair_n
     const long long tp = ((M + 255) / 256) * ((N + pair_n - 1) / pair_n) * segments;
     const long long t1 = ((M + 127) / 128) * ((N + one_n - 1) / one_n) * segments;
     const long long sp = dev.sm_count / 2, s1 = dev.sm_count;
-    return static_cast<double>((tp + sp - 1) / sp) <=
-           kOneStep * static_cast<double>((t1 + s1 - 1) / s1);
+    const long long left = tp % sp;
+    const double pair_waves =
+        static_cast<double>(tp / sp) + (left == 0 ? 0.0 : 2 * left <= sp ? kHalfWave : 1.0);
+    return pair_waves <= kOneStep * static_cast<double>((t1 + s1 - 1) / s1);
 }
 
 int op_product_parts(const OpDevice &dev, int M, int N, int K, int segments) {
     return plan_product(dev.sm_count, M, N, K, segments, true).parts;
 }
 long long op_parts_ld(int N) { return op_round_up(N, 64); }
-long long op_parts_rows(int M) { return op_round_up(M, 256); }
+long long op_parts_rows(int M) { return op_round_up(M, 32); }
 
 // ----------------------------------------------------------------- launch ---
 template <class Cfg, bool FULL>
@@ -312,14 +316,22 @@ __global__ void __launch_bounds__(256) join_parts_kernel(const JoinParams p) {
         const long long m = sm - static_cast<long long>(seg) * p.M;
         const float *src = p.area + (seg * p.rows + m) * p.ld + n;
         float v[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-        for (int k = 0; k < p.parts; ++k) {
-            const float4 x = __ldcs(reinterpret_cast<const float4 *>(
-                src + static_cast<long long>(k) * p.segments * p.rows * p.ld));
-            v[0] += x.x;
-            v[1] += x.y;
-            v[2] += x.z;
-            v[3] += x.w;
+        const long long step = p.segments * p.rows * p.ld;
+        constexpr int AHEAD = 8;  // loads in flight
+        for (int k = 0; k < p.parts; k += AHEAD) {
+            float4 x[AHEAD];
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j)
+                x[j] = k + j < p.parts
+                           ? __ldcs(reinterpret_cast<const float4 *>(src + (k + j) * step))
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) {
+                v[0] += x[j].x;
+                v[1] += x[j].y;
+                v[2] += x[j].z;
+                v[3] += x[j].w;
+            }
         }
         const long long at = m * p.N + n;
         const int cols = min(4, p.N - n);

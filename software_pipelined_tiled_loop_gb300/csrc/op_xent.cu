@@ -166,9 +166,10 @@ struct EpiXentGrad {
 
 // lse and loss of a row from its column blocks' (m, s), and its target's logit
 // as an fp32 dot product of its own (the epilogues would have to pick one of
-// their registers by a runtime index).  A block takes eight rows: 32 threads a
-// row join every 32nd column block (8 adjacent rows make a 32-byte sector),
-// then a warp a row multiplies X[t] by W[target].
+// their registers by a runtime index).  A block takes ROWS rows: 256 / ROWS
+// threads a row share its column blocks (8 adjacent rows make a 32-byte sector;
+// with few rows there are not enough blocks of 8 to hide the loads' latency,
+// and each row gets a block), then a warp a row multiplies X[t] by W[target].
 __device__ __forceinline__ void join_ms(float &m, float &s, float m2, float s2) {
     const float n = fmaxf(m, m2);
     const float ref = n == -CUDART_INF_F ? 0.0f : n;
@@ -176,39 +177,51 @@ __device__ __forceinline__ void join_ms(float &m, float &s, float m2, float s2) 
     m = n;
 }
 
+template <int ROWS>
 __global__ void __launch_bounds__(256)
     xent_join_kernel(const float *part_m, const float *part_s, long long rows, int blocks, int T,
                      long long V, int D, const OpMat X, const OpMat W, const int64_t *target,
                      float *loss, float *lse) {
     grid_dependency_wait();
     grid_launch_dependents();
-    __shared__ float sm[8][8], ss[8][8], dot[8];
+    __shared__ float sm[8][ROWS], ss[8][ROWS], dot[8];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int r = threadIdx.x & 7;
-    const int t = blockIdx.x * 8 + r;
+    const int r = threadIdx.x % ROWS;
+    const int t = blockIdx.x * ROWS + r;
     float m = -CUDART_INF_F, s = 0.0f;
     if (t < T) {
-#pragma unroll 8
-        for (int b = threadIdx.x >> 3; b < blocks; b += 32)
-            join_ms(m, s, part_m[b * rows + t], part_s[b * rows + t]);
+        constexpr int STEP = 256 / ROWS, AHEAD = 8;
+        for (int b = threadIdx.x / ROWS; b < blocks; b += STEP * AHEAD) {
+            float m2[AHEAD], s2[AHEAD];
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                const bool in = b + i * STEP < blocks;
+                m2[i] = in ? part_m[(b + i * STEP) * rows + t] : -CUDART_INF_F;
+                s2[i] = in ? part_s[(b + i * STEP) * rows + t] : 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) join_ms(m, s, m2[i], s2[i]);
+        }
     }
 #pragma unroll
-    for (int o = 8; o <= 16; o *= 2) {
+    for (int o = ROWS; o <= 16; o *= 2) {
         const float m2 = __shfl_xor_sync(0xffffffffu, m, o);
         const float s2 = __shfl_xor_sync(0xffffffffu, s, o);
         join_ms(m, s, m2, s2);
     }
-    if (lane < 8) {
+    if (lane < ROWS) {
         sm[w][lane] = m;
         ss[w][lane] = s;
     }
+    // the target's logit: a warp a row, or all eight warps for the one row
     {
-        const int tw = blockIdx.x * 8 + w;
+        const int tw = blockIdx.x * ROWS + (ROWS > 1 ? w : 0);
         const int64_t y = tw < T ? target[tw] : -1;
+        float d = 0.0f;
         if (loss && y >= 0 && y < V) {
             const uint16_t *x = X.p + tw * X.ld, *e = W.p + y * W.ld;  // 16-byte-aligned rows
-            float d = 0.0f;
-            for (int k = lane * 8; k < D; k += 256) {
+            for (int k = (ROWS > 1 ? lane : static_cast<int>(threadIdx.x)) * 8; k < D;
+                 k += ROWS > 1 ? 256 : 2048) {
                 const uint4 a = *reinterpret_cast<const uint4 *>(x + k);
                 const uint4 b = *reinterpret_cast<const uint4 *>(e + k);
                 const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
@@ -218,21 +231,25 @@ __global__ void __launch_bounds__(256)
                     if (k + 2 * i + 1 < D) d = fmaf(bf16_hi(aw[i]), bf16_hi(bw[i]), d);
                 }
             }
-#pragma unroll
-            for (int o = 16; o > 0; o /= 2) d += __shfl_xor_sync(0xffffffffu, d, o);
-            if (lane == 0) dot[w] = d;
         }
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2) d += __shfl_xor_sync(0xffffffffu, d, o);
+        if (lane == 0) dot[w] = d;
     }
     __syncthreads();
-    if (threadIdx.x < 8 && t < T) {
+    if (threadIdx.x < ROWS && t < T) {
         m = sm[0][r];
         s = ss[0][r];
+        float d = dot[r];
 #pragma unroll
-        for (int i = 1; i < 8; ++i) join_ms(m, s, sm[i][r], ss[i][r]);
+        for (int i = 1; i < 8; ++i) {
+            join_ms(m, s, sm[i][r], ss[i][r]);
+            if (ROWS == 1) d += dot[i];
+        }
         const float l = kLn2 * (m + log2f(s));
         const int64_t y = target[t];
         if (lse) lse[t] = l;
-        if (loss) loss[t] = y >= 0 && y < V ? l - dot[r] : 0.0f;
+        if (loss) loss[t] = y >= 0 && y < V ? l - d : 0.0f;
     }
 }
 
@@ -301,6 +318,285 @@ __global__ void __launch_bounds__(256)
     }
 }
 
+// ------------------------------------------------------------ few tokens ---
+// Up to 64 tokens: the pass is bound by reading W once.  The rows of W take the
+// tensor core's M side (128 of the vocabulary a tile), the tokens its N side, so
+// that a ring stage is 16 KB of W beside 2 to 8 KB of X; with a token a row it
+// would be half padding (V = 98392, D = 1472, 24 tokens: 72 us, 4.0 TB/s of W).
+// A thread holds one vocabulary entry's logits of 16 or 32 tokens and keeps
+// running (m, s) for each through all of its CTA's tiles; lanes and warps are
+// joined once at the end.  KEEP: the logits themselves are stored (fp32, T x V,
+// coalesced along v) for the gradient's P, which for so few tokens costs less
+// than anything read of W.
+template <int TOK_>
+struct FewCfg {
+    static constexpr int TOK = TOK_, BK = 64;
+    static constexpr int EPI = TOK == 16 ? 4 : 8;  // warps; two share a lane quadrant's tokens
+    static constexpr int TT = TOK * 4 / EPI;       // tokens of a warp
+    static constexpr int THREADS = 64 + 32 * EPI;
+    static constexpr int CTAS = TOK <= 32 ? 2 : 1;
+    static constexpr int W_BYTES = 128 * BK * 2, X_BYTES = TOK * BK * 2;
+    static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
+    static constexpr int ROOM =
+        (CTAS == 2 ? kSmemPerSm / 2 - kSmemReservedPerBlock : 232448) - 3072;
+    static constexpr int STAGES = ROOM / STAGE_BYTES;
+    static constexpr int ROUND = 16;  // K steps of a round: 1024 products, as above
+    static constexpr int BAR_OFFSET = STAGES * STAGE_BYTES;
+    static constexpr int SMEM_BYTES =
+        smem_request(BAR_OFFSET + (2 * STAGES + 5) * 8 + 16 + 1024, CTAS);
+    static constexpr int TMEM_COLS = 2 * TOK;
+    static constexpr int BN = TOK;  // OpAcc: accumulator stride
+    static constexpr int CG = 1;
+};
+
+struct FewArgs {
+    int T, V, D, k_tiles, tiles;
+    float *part_m, *part_s;  // [CTA][rows]
+    long long rows;
+    float *logits;           // T x V, pitch ld; or nullptr
+    long long ld;
+};
+
+template <class Cfg>
+__global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
+    xent_few_kernel(const __grid_constant__ CUtensorMap map_w,
+                    const __grid_constant__ CUtensorMap map_x, const FewArgs a,
+                    const KernelCtx ctx) {
+    constexpr int TOK = Cfg::TOK, TT = Cfg::TT, STAGES = Cfg::STAGES, BK = Cfg::BK;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = align_1024(smem_raw);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + Cfg::BAR_OFFSET);
+    uint64_t *empty = full + STAGES;
+    uint64_t *acc_full = empty + STAGES;
+    uint64_t *acc_empty = acc_full + 2;
+    uint64_t *mma_done = acc_empty + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
+    __shared__ float sm[4][TOK], ss[4][TOK];
+    const uint32_t warp = warp_id_uniform(), lane = lane_id();
+    if (warp == 0 && lane == 0) {
+        if (a.k_tiles > 0) {
+            prefetch_tmap(&map_w);
+            prefetch_tmap(&map_x);
+        }
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], Cfg::EPI);
+        }
+        mbar_init(mma_done, 1);
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, Cfg::TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (int tile = blockIdx.x; ok && tile < a.tiles; tile += gridDim.x) {
+                for (int kt = 0; kt < a.k_tiles; ++kt, ++it) {
+                    const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
+                    if (!mbar_wait(&empty[s], ph ^ 1u, ctx, kSiteProducerEmpty)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *st = smem + s * Cfg::STAGE_BYTES;
+                    mbar_arrive_expect_tx(&full[s], Cfg::STAGE_BYTES);
+                    tma_load_2d(st, &map_w, &full[s], kt * BK, tile * 128);
+                    tma_load_2d(st + Cfg::W_BYTES, &map_x, &full[s], kt * BK, 0);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = idesc_f16(128, TOK, 1, 0, 0);
+            uint32_t it = 0, gr = 0;
+            bool ok = true;
+            for (int tile = blockIdx.x; ok && tile < a.tiles; tile += gridDim.x) {
+                for (int k0 = 0; ok && k0 < a.k_tiles; k0 += Cfg::ROUND, ++gr) {
+                    const uint32_t ab = gr & 1u, aph = (gr >> 1) & 1u;
+                    if (!mbar_wait(&acc_empty[ab], aph ^ 1u, ctx, kSiteMmaAccEmpty)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const int k1 = min(a.k_tiles, k0 + Cfg::ROUND);
+                    for (int kt = k0; kt < k1; ++kt, ++it) {
+                        const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
+                        if (!mbar_wait(&full[s], ph, ctx, kSiteMmaFull)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t st = smem_u32(smem + s * Cfg::STAGE_BYTES);
+#pragma unroll
+                        for (int k = 0; k < BK / 16; ++k)
+                            umma_f16_ss(tmem + ab * TOK, smem_desc_sw128(st + k * 32, 16, 1024),
+                                        smem_desc_sw128(st + Cfg::W_BYTES + k * 32, 16, 1024),
+                                        idesc, (kt == k0 && k == 0) ? 0u : 1u);
+                        umma_commit(&empty[s]);
+                    }
+                    if (ok) umma_commit(&acc_full[ab]);
+                }
+            }
+            umma_commit(mma_done);
+            mbar_wait(mma_done, 0, ctx, kSiteMmaDone);
+        }
+    } else {
+        const uint32_t q = warp & 3u;
+        const int t0 = static_cast<int>((warp - 2) >> 2) * TT;  // this warp's tokens
+        OpAcc<Cfg> acc{acc_full, acc_empty, tmem + ((q * 32u) << 16) + t0, lane, 0u,
+                       (a.k_tiles + Cfg::ROUND - 1) / Cfg::ROUND, ctx};
+        float m[TT], s[TT];
+#pragma unroll
+        for (int j = 0; j < TT; ++j) {
+            m[j] = -CUDART_INF_F;
+            s[j] = 0.0f;
+        }
+        bool ok = true;
+        for (int tile = blockIdx.x; ok && tile < a.tiles; tile += gridDim.x) {
+            __syncwarp();
+            float x[TT];
+#pragma unroll
+            for (int j = 0; j < TT; ++j) x[j] = 0.0f;
+#pragma unroll 1
+            for (int r = 0; r < acc.rounds; ++r) {
+                if (!acc.wait()) {
+                    ok = false;
+                    break;
+                }
+#pragma unroll
+                for (int c = 0; c < TT; c += 16) {
+                    uint32_t y[16];
+                    tmem_ld_32x32b_x16(acc.row() + c, y);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) x[c + j] += __uint_as_float(y[j]);
+                }
+                acc.release();
+            }
+            const long long v = static_cast<long long>(tile) * 128 + q * 32 + lane;
+            if (!ok || v >= a.V) continue;
+#pragma unroll
+            for (int j = 0; j < TT; ++j) {
+                if (a.logits != nullptr && t0 + j < a.T)
+                    a.logits[static_cast<long long>(t0 + j) * a.ld + v] = x[j];
+                const float b = x[j] * kLog2e;
+                const float n = fmaxf(m[j], b);
+                const float ref = n == -CUDART_INF_F ? 0.0f : n;
+                s[j] = fmaf(s[j], ex2(m[j] - ref), ex2(b - ref));
+                m[j] = n;
+            }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < TT; ++j) {
+#pragma unroll
+            for (int o = 16; o > 0; o /= 2) {
+                const float m2 = __shfl_xor_sync(0xffffffffu, m[j], o);
+                const float s2 = __shfl_xor_sync(0xffffffffu, s[j], o);
+                join_ms(m[j], s[j], m2, s2);
+            }
+            if (lane == 0) {
+                sm[q][t0 + j] = m[j];
+                ss[q][t0 + j] = s[j];
+            }
+        }
+    }
+    tc_fence_before();
+    __syncwarp();
+    __syncthreads();
+    for (int t = static_cast<int>(threadIdx.x); t < a.T; t += Cfg::THREADS) {
+        float m = sm[0][t], s = ss[0][t];
+#pragma unroll
+        for (int i = 1; i < 4; ++i) join_ms(m, s, sm[i][t], ss[i][t]);
+        a.part_m[blockIdx.x * a.rows + t] = m;
+        a.part_s[blockIdx.x * a.rows + t] = s;
+    }
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, Cfg::TMEM_COLS);
+    }
+}
+
+// P from kept logits: a thread eight columns of a row.
+__global__ void __launch_bounds__(256)
+    xent_probs_kernel(const float *logits, uint16_t *P, long long ld, int T, int V,
+                      const float *lse, const int64_t *target, const float *dloss) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int octets = (V + 7) / 8;
+    const long long total = static_cast<long long>(T) * octets;
+    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+        const int t = static_cast<int>(i / octets);
+        const int c = static_cast<int>(i - static_cast<long long>(t) * octets) * 8;
+        const int64_t y = target[t];
+        const bool counts = y >= 0 && y < V;
+        const float g = counts ? (dloss ? dloss[t] : 1.0f) : 0.0f;
+        const float l = counts ? lse[t] * kLog2e : 0.0f;
+        const float4 *src = reinterpret_cast<const float4 *>(logits + t * ld + c);
+        const float4 p = src[0], q = src[1];
+        const float x[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+        float o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float e = exp2f(fmaf(x[j], kLog2e, -l));
+            if (y == c + j) e -= 1.0f;
+            o[j] = counts ? e * g : 0.0f;
+        }
+        *reinterpret_cast<uint4 *>(P + t * ld + c) =
+            make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]),
+                       pack_bf16(o[6], o[7]));
+    }
+}
+
+template <class Cfg>
+static pgemm_status launch_few(const OpDevice &dev, FewArgs a, const OpMat &X, const OpMat &W,
+                               int ctas, cudaStream_t s) {
+    static const KernelInfo info = [] {
+        KernelInfo k;
+        k.threads = Cfg::THREADS;
+        k.smem_bytes = Cfg::SMEM_BYTES;
+        k.func = reinterpret_cast<const void *>(xent_few_kernel<Cfg>);
+        return k;
+    }();
+    int slots = 0;
+    pgemm_status st = op_kernel_setup(dev, info, &slots);
+    CUtensorMap mw{}, mx{};
+    if (a.D > 0) {
+        if (st == PGEMM_OK) st = op_encode(&mw, W.p, a.D, a.V, W.ld, 128);
+        if (st == PGEMM_OK) st = op_encode(&mx, X.p, a.D, a.T, X.ld, Cfg::TOK);
+    }
+    if (st != PGEMM_OK) return st;
+    a.k_tiles = (a.D + Cfg::BK - 1) / Cfg::BK;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = dim3(static_cast<unsigned>(ctas));
+    lc.blockDim = dim3(Cfg::THREADS);
+    lc.dynamicSmemBytes = Cfg::SMEM_BYTES;
+    lc.stream = s;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    return cudaLaunchKernelEx(&lc, xent_few_kernel<Cfg>, mw, mx, a, dev.ctx) == cudaSuccess
+               ? PGEMM_OK
+               : PGEMM_ERR_CUDA;
+}
+constexpr int kFewMax = 64;
+
 // rounds of 1024 products for the statistics
 using StatsPair = OpCfg<256, 3, 2, 2, false, true, false, 8>;
 using StatsOne = OpCfg<128, 6, 1, 1, false, true, false, 16>;
@@ -355,9 +651,15 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
                    ? PGEMM_OK
                    : PGEMM_ERR_CUDA;
 
+    const bool few = T <= kFewMax;
     const bool pair = op_use_pair(dev, T, V, 256, 128, 1);
     const int block_cols = pair ? StatsPair::EPI_COLS : StatsOne::EPI_COLS;
-    const int blocks = (V + block_cols - 1) / block_cols;
+    // (m, s) of a row: one for each column block, or for each CTA
+    int blocks = (V + block_cols - 1) / block_cols;
+    if (few) {
+        const int tiles = (V + 127) / 128, ctas = dev.sm_count * (T <= 32 ? 2 : 1);
+        blocks = tiles < ctas ? tiles : ctas;
+    }
     const long long rows = op_round_up(T, 32);
     // vocabulary pieces, whole tiles wide
     const long long p_ld_all = op_round_up(V, 256);
@@ -365,7 +667,8 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
     int pieces = 0;
     if (want_x || want_w) {
         const long long cap = workspace > 0 ? workspace : kDefaultWorkspace;
-        piece = cap / (2ll * T) / 256 * 256;
+        // bytes an entry: P, and with few tokens its fp32 logits
+        piece = cap / ((few ? 6ll : 2ll) * T) / 256 * 256;
         if (piece < 256) piece = 256;
         if (piece > p_ld_all) piece = p_ld_all;
         pieces = static_cast<int>((V + piece - 1) / piece);
@@ -385,6 +688,8 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
     const long long at_s = arena.add(blocks * rows * 4);
     const long long at_l = lse ? 0 : arena.add(rows * 4);
     const long long at_p = pieces ? arena.add(piece * T * 2) : 0;
+    const bool keep_logits = few && pieces == 1;
+    const long long at_z = keep_logits ? arena.add(piece * T * 4) : 0;
     long long at_x = 0;
     int x_parts = 0;
     const bool x_pieces = want_x && pieces > 1;
@@ -400,12 +705,18 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
     float *lse_buf = lse ? lse : arena.at<float>(at_l);
 
     // One piece: its exponentials are kept and P follows from them.
-    const bool keep = pieces == 1 && D >= kKeepMinD;
+    const bool keep = pieces == 1 && D >= kKeepMinD && !few;
     float *part_m = arena.at<float>(at_m), *part_s = arena.at<float>(at_s);
     uint16_t *P = pieces ? arena.at<uint16_t>(at_p) : nullptr;
     {
         OpMaps maps{};
-        if (keep) {
+        if (few) {
+            const FewArgs a{T, V, D, 0, (V + 127) / 128, part_m, part_s, rows,
+                            keep_logits ? arena.at<float>(at_z) : nullptr, piece};
+            st = T <= 16   ? launch_few<FewCfg<16>>(dev, a, x, w, blocks, s)
+                 : T <= 32 ? launch_few<FewCfg<32>>(dev, a, x, w, blocks, s)
+                           : launch_few<FewCfg<64>>(dev, a, x, w, blocks, s);
+        } else if (keep) {
             st = op_encode_out(&maps.c[0], OpElem::BF16, P, V, T, piece);
             if (st != PGEMM_OK) return st;
             const EpiXentStats<true> e{part_m, part_s, rows};
@@ -417,7 +728,9 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
                       : launch_logits<StatsOne>(dev, T, V, D, x, w, 0, maps, e, s);
         }
         if (st != PGEMM_OK) return st;
-        st = launch_small(xent_join_kernel, dim3((T + 7) / 8), dim3(256), s,
+        const bool by_row = T < 8 * dev.sm_count;  // fewer than a block of 8 rows an SM
+        st = launch_small(by_row ? xent_join_kernel<1> : xent_join_kernel<8>,
+                          dim3(by_row ? T : (T + 7) / 8), dim3(256), s,
                           static_cast<const float *>(part_m), static_cast<const float *>(part_s),
                           rows, blocks, T, static_cast<long long>(V), D, x, w, target, loss,
                           lse_buf);
@@ -428,7 +741,13 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
     for (int i = 0; i < pieces; ++i) {
         const long long v0 = i * piece;
         const int cols = static_cast<int>(V - v0 < piece ? V - v0 : piece);
-        if (keep) {
+        if (keep_logits) {
+            const long long n = (static_cast<long long>(T) * ((V + 7) / 8) + 255) / 256;
+            const long long most = dev.sm_count * 8ll;
+            st = launch_small(xent_probs_kernel, dim3(static_cast<unsigned>(n < most ? n : most)),
+                              dim3(256), s, static_cast<const float *>(arena.at<float>(at_z)), P,
+                              piece, T, V, static_cast<const float *>(lse_buf), target, dloss);
+        } else if (keep) {
             const dim3 grid(static_cast<unsigned>((V + 1023) / 1024) * ((T + 31) / 32));
             st = launch_small(pair ? xent_scale_kernel<StatsPair::EPI_COLS>
                                    : xent_scale_kernel<StatsOne::EPI_COLS>,
