@@ -227,6 +227,26 @@ static pgemm_status gated_backward(int M, int F, int K, const uint16_t *X, const
         dg_at = arena.add(dg.ld * M * 2);
         du_at = arena.add(du.ld * M * 2);
     }
+    OpProduct px, pw;
+    if (want_x) {
+        px.form = OpForm::NT;
+        px.M = M;
+        px.N = K;
+        px.K = F;
+        px.k_segments = 2;
+        px.out[0] = dX;
+        op_product_plan(dev, px, arena);
+    }
+    if (want_w) {
+        pw.form = OpForm::TN;
+        pw.M = K;
+        pw.N = F;
+        pw.K = M;
+        pw.n_segments = 2;
+        pw.out[0] = dWg;
+        pw.out[1] = dWu;
+        op_product_plan(dev, pw, arena);
+    }
     if ((st = arena.alloc()) != PGEMM_OK) return st;
     if ((st = rl.run(dev, arena, s)) != PGEMM_OK) return st;
     if (some) {
@@ -245,7 +265,7 @@ static pgemm_status gated_backward(int M, int F, int K, const uint16_t *X, const
             g.dz = dg_buf;
             g.du = du_buf;
             g.dz_ld = dg.ld;
-            st = op_act_grad(dev, g, s);
+            st = op_act_grad(dev, g, arena, false, s);
         } else {
             OpMaps maps{};
             EpiGatedGrad e{dH, F, dg_buf, du_buf, dg.ld, act};
@@ -258,34 +278,21 @@ static pgemm_status gated_backward(int M, int F, int K, const uint16_t *X, const
         if (st != PGEMM_OK) return st;
     }
     if (want_x) {
-        OpProduct p;
-        p.form = OpForm::NT;
-        p.M = M;
-        p.N = K;
-        p.K = F;
-        p.k_segments = 2;
-        p.A[0] = dg;
-        p.A[1] = du;
-        p.B[0] = wg;
-        p.B[1] = wu;
-        p.out[0] = dX;
-        if ((st = op_product(dev, p, s)) != PGEMM_OK) return st;
+        px.A[0] = dg;
+        px.A[1] = du;
+        px.B[0] = wg;
+        px.B[1] = wu;
+        if ((st = op_product(dev, px, arena, s)) != PGEMM_OK) return st;
     }
     if (want_w) {
-        OpProduct p;
-        p.form = OpForm::TN;
-        p.M = K;
-        p.N = F;
-        p.K = M;
-        p.n_segments = 2;
-        p.A[0] = x;
-        p.B[0] = dg;
-        p.B[1] = du;
-        p.out[0] = dWg;
-        p.out[1] = dWu;
-        if ((st = op_product(dev, p, s)) != PGEMM_OK) return st;
+        pw.A[0] = x;
+        pw.B[0] = dg;
+        pw.B[1] = du;
+        pw.overlap = want_x;  // behind dX, which has waited for dG and dU
+        if ((st = op_product(dev, pw, arena, s)) != PGEMM_OK) return st;
     }
-    return PGEMM_OK;
+    if ((st = op_product_join(dev, px, arena, s)) != PGEMM_OK) return st;
+    return op_product_join(dev, pw, arena, s);
 }
 
 }  // namespace pg

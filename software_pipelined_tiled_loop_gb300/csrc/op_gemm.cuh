@@ -39,6 +39,22 @@
 
 namespace pg {
 
+// Programmatic stream serialisation, the two ways a kernel here uses it.
+// Ordinary: every thread waits for the kernel before it ahead of its first
+// access to memory, so that only its prologue overlaps that kernel's tail.
+// Overlapping (`overlap`): the kernel reads nothing that the kernel before it
+// writes, nor writes what that one touches, but only what was complete when that
+// one began (which let this one launch only after its own wait).  It starts
+// as SMs fall free and waits at its end instead, so that its completion still
+// implies everything before it.  The second of two gradient products runs so.
+__device__ __forceinline__ void op_begin(int overlap) {
+    if (!overlap) grid_dependency_wait();
+    grid_launch_dependents();
+}
+__device__ __forceinline__ void op_end(int overlap) {
+    if (overlap) grid_dependency_wait();
+}
+
 struct OpMaps {
     CUtensorMap a[2], b[2], c[3];
 };
@@ -56,6 +72,7 @@ struct OpArgs {
     int parts;
     int group_m;
     int half_tiles;    // leftover tiles that run as two half-width units each
+    int overlap;       // see op_begin
 };
 
 // ROUND: K-tiles of one accumulation round (0: all of a unit's K range).  The
@@ -494,8 +511,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     // on-chip set-up is done; what follows may read what the kernel before wrote
-    grid_dependency_wait();
-    grid_launch_dependents();
+    op_begin(args.overlap);
 
     const int crank = Cfg::CG == 2 ? static_cast<int>(cluster_ctarank()) : 0;
     const int slot = static_cast<int>(blockIdx.x) / Cfg::CG;
@@ -687,6 +703,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         else
             tmem_dealloc(tmem_base, Cfg::TMEM_COLS);
     }
+    op_end(args.overlap);
 }
 
 // Read 32 accumulator columns (zeros when there is no accumulator).

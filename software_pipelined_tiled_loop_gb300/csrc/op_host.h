@@ -128,6 +128,10 @@ struct OpEpilogue {
 // Outputs are user matrices: any N; TMA stores where rows are 16-byte
 // multiples.  Few tiles with a long K are split along K into parts whose fp32
 // sums are joined in part order by a second kernel.
+struct OpPlan {
+    bool pair;
+    int parts;
+};
 struct OpProduct {
     OpForm form = OpForm::NN;
     int M = 0, N = 0, K = 0;
@@ -138,8 +142,18 @@ struct OpProduct {
     // a caller's own area of fp32 parts instead (cross entropy sums the pieces
     // of its vocabulary there): the parts are written, nothing is joined
     float *parts_area = nullptr;
+    // behind another kernel that this product does not depend on (op_begin)
+    bool overlap = false;
+    OpPlan plan{};           // op_product_plan's
+    long long area_at = -1;  // the parts' place in the arena, if it is split
 };
-pgemm_status op_product(const OpDevice &dev, const OpProduct &p, cudaStream_t s);
+// In this order: choose the tiles and parts and reserve what the parts need in
+// the call's arena; launch; join the parts, if any.
+void op_product_plan(const OpDevice &dev, OpProduct &p, OpArena &arena);
+pgemm_status op_product(const OpDevice &dev, const OpProduct &p, const OpArena &arena,
+                        cudaStream_t s);
+pgemm_status op_product_join(const OpDevice &dev, const OpProduct &p, const OpArena &arena,
+                             cudaStream_t s);
 
 // The same products of a few rows, bound by reading the weights (op_tokens.cu).
 constexpr int kTokensMax = 128;
@@ -176,8 +190,14 @@ struct OpActGrad {
     uint16_t *du = nullptr;          // gated
     long long dz_ld = 0;
     uint16_t *dbias = nullptr;       // N, or nullptr
+    long long colsum_at = 0;         // op_act_grad_plan's
 };
-pgemm_status op_act_grad(const OpDevice &dev, const OpActGrad &p, cudaStream_t s);
+// Reserve the partial column sums; the elementwise pass; their sum into dbias.
+void op_act_grad_plan(OpActGrad &g, OpArena &arena);
+pgemm_status op_act_grad(const OpDevice &dev, const OpActGrad &g, const OpArena &arena,
+                         bool overlap, cudaStream_t s);
+pgemm_status op_act_grad_join(const OpDevice &dev, const OpActGrad &g, const OpArena &arena,
+                              bool overlap, cudaStream_t s);
 
 // A C entry point's body: no C++ exception leaves it.
 template <class F>

@@ -109,10 +109,13 @@ static pgemm_status linear_forward(int M, int N, int K, const uint16_t *X, const
         rl.add(&p.A[0], X, M, K, arena);
         rl.add(&p.B[0], W, K, N, arena);
     }
+    const bool tokens = M <= kTokensMax;
+    if (!tokens) op_product_plan(dev, p, arena);
     if ((st = arena.alloc()) != PGEMM_OK) return st;
     if ((st = rl.run(dev, arena, s)) != PGEMM_OK) return st;
-    if (M <= kTokensMax) return op_tokens_linear(dev, M, N, K, p.A[0], p.B[0], p.epi, Y, s);
-    return op_product(dev, p, s);
+    if (tokens) return op_tokens_linear(dev, M, N, K, p.A[0], p.B[0], p.epi, Y, s);
+    if ((st = op_product(dev, p, arena, s)) != PGEMM_OK) return st;
+    return op_product_join(dev, p, arena, s);
 }
 
 static pgemm_status linear_backward(int M, int N, int K, const uint16_t *X, const uint16_t *W,
@@ -145,67 +148,87 @@ static pgemm_status linear_backward(int M, int N, int K, const uint16_t *X, cons
         if (X && (want_w || recompute)) rl.add(&x, X, M, K, arena);
         if (W && (want_x || recompute)) rl.add(&w, W, K, N, arena);
     }
+    const bool own_dz = some && act != PGEMM_ACT_NONE;  // dZ is not dY itself
     long long dz_at = 0;
-    if (some && act == PGEMM_ACT_NONE) {
-        rl.add(&dz, dY, M, N, arena);
-    } else if (some) {
+    if (own_dz) {
         dz.ld = op_round_up(N, 64);
         dz_at = arena.add(dz.ld * M * 2);
+    } else if (some) {
+        rl.add(&dz, dY, M, N, arena);
     }
-    if ((st = arena.alloc()) != PGEMM_OK) return st;
-    if ((st = rl.run(dev, arena, s)) != PGEMM_OK) return st;
+    OpProduct px, pw;
+    if (want_x) {
+        px.form = OpForm::NT;
+        px.M = M;
+        px.N = K;
+        px.K = N;
+        px.out[0] = dX;
+        op_product_plan(dev, px, arena);
+    }
+    if (want_w) {
+        pw.form = OpForm::TN;
+        pw.M = K;
+        pw.N = N;
+        pw.K = M;
+        pw.out[0] = dW;
+        op_product_plan(dev, pw, arena);
+    }
+    OpActGrad g;
+    const bool elementwise = own_dz && preact;
     if (some) {
-        uint16_t *dz_buf = nullptr;
-        if (act != PGEMM_ACT_NONE) dz.p = dz_buf = arena.at<uint16_t>(dz_at);
-        if (recompute) {
-            EpiLinearGrad e{bias, dY, N, dz_buf, dz.ld, act};
-            st = op_use_pair(dev, M, N, 256, 128, 1)
-                     ? launch_grad<OpCfg<256, 3, 2, 2, false, false>>(dev, M, N, K, x, w, e, s)
-                     : launch_grad<OpCfg<128, 6, 1, 1, false, false>>(dev, M, N, K, x, w, e, s);
-            if (st != PGEMM_OK) return st;
-        }
-        OpActGrad g;
         g.M = M;
         g.N = N;
         g.dbias = want_b ? dbias : nullptr;
-        if (act != PGEMM_ACT_NONE && preact) {
+        op_act_grad_plan(g, arena);
+    }
+    if ((st = arena.alloc()) != PGEMM_OK) return st;
+    if ((st = rl.run(dev, arena, s)) != PGEMM_OK) return st;
+
+    // dZ first: from the kept Z elementwise, with the column sums beside it, or
+    // by the product that recomputes Z; then the products and column sums that
+    // read it, which overlap one another; then what joins their parts.
+    if (own_dz) {
+        uint16_t *dz_buf = arena.at<uint16_t>(dz_at);
+        dz.p = dz_buf;
+        if (elementwise) {
             g.act = act;
             g.z = preact;
             g.dy = dY;
             g.dy_ld = N;
             g.dz = dz_buf;
             g.dz_ld = dz.ld;
-        } else {  // column sums only: of dY, or of the dZ just recomputed
-            g.dy = act == PGEMM_ACT_NONE ? dY : dz_buf;
-            g.dy_ld = act == PGEMM_ACT_NONE ? N : dz.ld;
+            st = op_act_grad(dev, g, arena, false, s);
+        } else {
+            const EpiLinearGrad e{bias, dY, N, dz_buf, dz.ld, act};
+            st = op_use_pair(dev, M, N, 256, 128, 1)
+                     ? launch_grad<OpCfg<256, 3, 2, 2, false, false>>(dev, M, N, K, x, w, e, s)
+                     : launch_grad<OpCfg<128, 6, 1, 1, false, false>>(dev, M, N, K, x, w, e, s);
         }
-        if (g.dz || g.dbias) {
-            if ((st = op_act_grad(dev, g, s)) != PGEMM_OK) return st;
-        }
+        if (st != PGEMM_OK) return st;
     }
+    bool overlap = false;  // the first kernel that reads dZ waits for it
     if (want_x) {
-        OpProduct p;
-        p.form = OpForm::NT;
-        p.M = M;
-        p.N = K;
-        p.K = N;
-        p.A[0] = dz;
-        p.B[0] = w;
-        p.out[0] = dX;
-        if ((st = op_product(dev, p, s)) != PGEMM_OK) return st;
+        px.A[0] = dz;
+        px.B[0] = w;
+        if ((st = op_product(dev, px, arena, s)) != PGEMM_OK) return st;
+        overlap = true;
     }
     if (want_w) {
-        OpProduct p;
-        p.form = OpForm::TN;
-        p.M = K;
-        p.N = N;
-        p.K = M;
-        p.A[0] = x;
-        p.B[0] = dz;
-        p.out[0] = dW;
-        if ((st = op_product(dev, p, s)) != PGEMM_OK) return st;
+        pw.A[0] = x;
+        pw.B[0] = dz;
+        pw.overlap = overlap;
+        if ((st = op_product(dev, pw, arena, s)) != PGEMM_OK) return st;
+        overlap = true;
     }
-    return PGEMM_OK;
+    if (some && want_b && !elementwise) {
+        g.dy = own_dz ? dz.p : dY;
+        g.dy_ld = own_dz ? dz.ld : N;
+        if ((st = op_act_grad(dev, g, arena, overlap, s)) != PGEMM_OK) return st;
+        overlap = false;
+    }
+    if (some && (st = op_act_grad_join(dev, g, arena, overlap, s)) != PGEMM_OK) return st;
+    if ((st = op_product_join(dev, px, arena, s)) != PGEMM_OK) return st;
+    return op_product_join(dev, pw, arena, s);
 }
 
 }  // namespace pg

@@ -133,10 +133,6 @@ struct EpiOut {
 // operand panel feeds half as many products).  Parts along K shorten the
 // waves and add the join's traffic: parts * M * N fp32 values written and read.
 constexpr double kStepUs = 0.36, kOneStep = 0.65, kHalfWave = 0.6;
-struct OpPlan {
-    bool pair;
-    int parts;
-};
 static OpPlan plan_product(int sm_count, long long M, long long N, long long K, int segments,
                            bool split) {
     const long long steps = (K + 63) / 64;
@@ -242,6 +238,7 @@ static pgemm_status launch_form(const OpDevice &dev, const OpProduct &p, float *
     a.k_seg = (p.K + Cfg::SBK - 1) / Cfg::SBK;
     a.k_tiles = a.k_seg * p.k_segments;
     a.parts = parts;
+    a.overlap = p.overlap ? 1 : 0;
     return op_launch<Cfg, EpiOut<FULL>>(dev, maps, a, e, s);
 }
 
@@ -260,36 +257,39 @@ using OneCfg = OpCfg<128, 6, 1, 1, A_MN, B_K>;
 
 template <bool FULL, bool A_MN, bool B_K>
 static pgemm_status launch_size(const OpDevice &dev, const OpProduct &p, float *area,
-                                const OpPlan &plan, cudaStream_t s) {
+                                cudaStream_t s) {
+    const OpPlan &plan = p.plan;
     if (plan.pair && static_cast<long long>(p.K) * p.k_segments <= kShortK)
         return launch_form<ShortCfg<A_MN, B_K>, FULL>(dev, p, area, plan.parts, s);
     return plan.pair ? launch_form<PairCfg<A_MN, B_K>, FULL>(dev, p, area, plan.parts, s)
                      : launch_form<OneCfg<A_MN, B_K>, FULL>(dev, p, area, plan.parts, s);
 }
 
-pgemm_status op_product(const OpDevice &dev, const OpProduct &p, cudaStream_t s) {
+void op_product_plan(const OpDevice &dev, OpProduct &p, OpArena &arena) {
+    p.plan = plan_product(dev.sm_count, p.M, p.N, static_cast<long long>(p.K) * p.k_segments,
+                          p.n_segments, true);
+    if (p.plan.parts > 1 && p.parts_area == nullptr && p.M > 0 && p.N > 0)
+        p.area_at = arena.add(op_parts_ld(p.N) * op_parts_rows(p.M) * 4 * p.plan.parts *
+                              p.n_segments);
+}
+
+pgemm_status op_product(const OpDevice &dev, const OpProduct &p, const OpArena &arena,
+                        cudaStream_t s) {
     if (p.M <= 0 || p.N <= 0) return PGEMM_OK;
-    const OpPlan plan = plan_product(dev.sm_count, p.M, p.N,
-                                     static_cast<long long>(p.K) * p.k_segments, p.n_segments, true);
-    OpArena arena(dev, s);
-    float *area = p.parts_area;
-    const bool join = area == nullptr && plan.parts > 1;
-    if (join) {
-        const long long at = arena.add(op_parts_ld(p.N) * op_parts_rows(p.M) * 4 * plan.parts *
-                                       p.n_segments);
-        const pgemm_status st = arena.alloc();
-        if (st != PGEMM_OK) return st;
-        area = arena.at<float>(at);
-    }
-    pgemm_status st = PGEMM_ERR_INVALID_VALUE;
+    float *area = p.parts_area ? p.parts_area : p.area_at >= 0 ? arena.at<float>(p.area_at) : nullptr;
     switch (p.form) {
-        case OpForm::NN: st = launch_size<true, false, false>(dev, p, area, plan, s); break;
-        case OpForm::NT: st = launch_size<false, false, true>(dev, p, area, plan, s); break;
-        case OpForm::TN: st = launch_size<false, true, false>(dev, p, area, plan, s); break;
+        case OpForm::NN: return launch_size<true, false, false>(dev, p, area, s);
+        case OpForm::NT: return launch_size<false, false, true>(dev, p, area, s);
+        case OpForm::TN: return launch_size<false, true, false>(dev, p, area, s);
     }
-    if (st == PGEMM_OK && join)
-        st = op_join_parts(dev, area, plan.parts, p.n_segments, p.M, p.N, p.out, p.epi, s);
-    return st;
+    return PGEMM_ERR_INVALID_VALUE;
+}
+
+pgemm_status op_product_join(const OpDevice &dev, const OpProduct &p, const OpArena &arena,
+                             cudaStream_t s) {
+    if (p.area_at < 0) return PGEMM_OK;
+    return op_join_parts(dev, arena.at<float>(p.area_at), p.plan.parts, p.n_segments, p.M, p.N,
+                         p.out, p.epi, s);
 }
 
 // ------------------------------------------------------------------- join ---
@@ -391,6 +391,7 @@ constexpr int kGradRows = 64;
 struct ActGradParams {
     OpActGrad g;
     float *colsum;  // [row blocks][N] partial column sums, or nullptr
+    int overlap;
 };
 
 __device__ __forceinline__ void load8(const float *p, float (&f)[8]) {
@@ -402,8 +403,7 @@ __device__ __forceinline__ void load8(const float *p, float (&f)[8]) {
 
 template <bool VEC, bool GATED>
 __global__ void __launch_bounds__(256) act_grad_kernel(const ActGradParams p) {
-    grid_dependency_wait();
-    grid_launch_dependents();
+    op_begin(p.overlap);
     const OpActGrad &g = p.g;
     const int lane = threadIdx.x & 31, rl = threadIdx.x >> 5;
     const int c0 = blockIdx.x * 256;
@@ -482,13 +482,13 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const ActGradParams p) {
         for (int i = 0; i < 8; ++i) t += s[i][threadIdx.x];
         if (c < g.N) p.colsum[static_cast<long long>(blockIdx.y) * g.N + c] = t;
     }
+    op_end(p.overlap);
 }
 
 // dbias = sum of the row blocks' column sums, in order.
 __global__ void __launch_bounds__(256)
-    colsum_join_kernel(const float *part, int blocks, int N, uint16_t *out) {
-    grid_dependency_wait();
-    grid_launch_dependents();
+    colsum_join_kernel(const float *part, int blocks, int N, uint16_t *out, int overlap) {
+    op_begin(overlap);
     __shared__ float s[8][32];
     const int lane = threadIdx.x & 31, rl = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
@@ -502,33 +502,37 @@ __global__ void __launch_bounds__(256)
         for (int i = 1; i < 8; ++i) t += s[i][lane];
         out[c] = static_cast<uint16_t>(pack_bf16(t, 0.0f) & 0xffffu);
     }
+    op_end(overlap);
 }
 
-pgemm_status op_act_grad(const OpDevice &dev, const OpActGrad &g, cudaStream_t s) {
+static int grad_row_blocks(const OpActGrad &g) {
+    const int all = (g.M + kGradRows - 1) / kGradRows;
+    return all < 512 ? all : 512;
+}
+
+void op_act_grad_plan(OpActGrad &g, OpArena &arena) {
+    if (g.dbias != nullptr) g.colsum_at = arena.add(grad_row_blocks(g) * 4ll * g.N);
+}
+
+pgemm_status op_act_grad(const OpDevice &, const OpActGrad &g, const OpArena &arena, bool overlap,
+                         cudaStream_t s) {
     if (g.M <= 0 || g.N <= 0) return PGEMM_OK;
-    ActGradParams p{g, nullptr};
-    const int all_blocks = (g.M + kGradRows - 1) / kGradRows;
-    const int row_blocks = all_blocks < 512 ? all_blocks : 512;
-    OpArena arena(dev, s);
-    if (g.dbias != nullptr) {
-        const long long at = arena.add(static_cast<long long>(row_blocks) * g.N * 4);
-        const pgemm_status st = arena.alloc();
-        if (st != PGEMM_OK) return st;
-        p.colsum = arena.at<float>(at);
-    }
-    const dim3 grid((g.N + 255) / 256, row_blocks);
+    const ActGradParams p{g, g.dbias ? arena.at<float>(g.colsum_at) : nullptr, overlap ? 1 : 0};
+    const dim3 grid((g.N + 255) / 256, grad_row_blocks(g));
     const bool vec = g.N % 8 == 0 && g.dy_ld % 8 == 0;
-    pgemm_status st;
     if (g.u != nullptr)
-        st = vec ? launch_small(act_grad_kernel<true, true>, grid, dim3(256), s, p)
-                 : launch_small(act_grad_kernel<false, true>, grid, dim3(256), s, p);
-    else
-        st = vec ? launch_small(act_grad_kernel<true, false>, grid, dim3(256), s, p)
-                 : launch_small(act_grad_kernel<false, false>, grid, dim3(256), s, p);
-    if (st == PGEMM_OK && g.dbias != nullptr)
-        st = launch_small(colsum_join_kernel, dim3((g.N + 31) / 32), dim3(256), s,
-                          static_cast<const float *>(p.colsum), row_blocks, g.N, g.dbias);
-    return st;
+        return vec ? launch_small(act_grad_kernel<true, true>, grid, dim3(256), s, p)
+                   : launch_small(act_grad_kernel<false, true>, grid, dim3(256), s, p);
+    return vec ? launch_small(act_grad_kernel<true, false>, grid, dim3(256), s, p)
+               : launch_small(act_grad_kernel<false, false>, grid, dim3(256), s, p);
+}
+
+pgemm_status op_act_grad_join(const OpDevice &, const OpActGrad &g, const OpArena &arena,
+                              bool overlap, cudaStream_t s) {
+    if (g.M <= 0 || g.N <= 0 || g.dbias == nullptr) return PGEMM_OK;
+    return launch_small(colsum_join_kernel, dim3((g.N + 31) / 32), dim3(256), s,
+                        static_cast<const float *>(arena.at<float>(g.colsum_at)),
+                        grad_row_blocks(g), g.N, g.dbias, overlap ? 1 : 0);
 }
 
 // --------------------------------------------------------------- relayout ---

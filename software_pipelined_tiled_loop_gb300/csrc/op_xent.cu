@@ -700,6 +700,25 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
         }
         at_x = arena.add(op_parts_ld(D) * op_parts_rows(T) * 4 * x_parts);
     }
+    // the products of a piece, planned for the first (the widest): the others'
+    // parts need no more room
+    OpProduct px, pw;
+    const auto shape = [&](int cols) {
+        px.form = OpForm::NN;
+        px.M = T;
+        px.N = D;
+        px.K = cols;
+        px.out[0] = dX;
+        pw.form = OpForm::TN;
+        pw.M = cols;
+        pw.N = D;
+        pw.K = T;
+    };
+    if (pieces) {
+        shape(static_cast<int>(V < piece ? V : piece));
+        if (want_x && !x_pieces) op_product_plan(dev, px, arena);
+        if (want_w) op_product_plan(dev, pw, arena);
+    }
     if ((st = arena.alloc()) != PGEMM_OK) return st;
     if ((st = rl.run(dev, arena, s)) != PGEMM_OK) return st;
     float *lse_buf = lse ? lse : arena.at<float>(at_l);
@@ -764,33 +783,27 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
                      : launch_logits<XentOne>(dev, T, cols, D, x, w, v0, maps, e, s);
         }
         if (st != PGEMM_OK) return st;
+        shape(cols);
         if (want_x) {
-            OpProduct p;
-            p.form = OpForm::NN;
-            p.M = T;
-            p.N = D;
-            p.K = cols;
-            p.A[0] = OpMat{P, piece};
-            p.B[0] = OpMat{w.p + v0 * w.ld, w.ld};
-            p.out[0] = dX;
+            px.A[0] = OpMat{P, piece};
+            px.B[0] = OpMat{w.p + v0 * w.ld, w.ld};
             if (x_pieces) {
-                p.parts_area = arena.at<float>(at_x) +
-                               op_parts_ld(D) * op_parts_rows(T) * static_cast<long long>(x_done);
-                x_done += op_product_parts(dev, T, D, cols, 1);
+                px.parts_area = arena.at<float>(at_x) +
+                                op_parts_ld(D) * op_parts_rows(T) * static_cast<long long>(x_done);
+                op_product_plan(dev, px, arena);  // this piece's; reserves nothing
+                x_done += px.plan.parts;
             }
-            if ((st = op_product(dev, p, s)) != PGEMM_OK) return st;
+            if ((st = op_product(dev, px, arena, s)) != PGEMM_OK) return st;
         }
         if (want_w) {
-            OpProduct p;
-            p.form = OpForm::TN;
-            p.M = cols;
-            p.N = D;
-            p.K = T;
-            p.A[0] = OpMat{P, piece};
-            p.B[0] = x;
-            p.out[0] = dW + v0 * D;
-            if ((st = op_product(dev, p, s)) != PGEMM_OK) return st;
+            pw.A[0] = OpMat{P, piece};
+            pw.B[0] = x;
+            pw.out[0] = dW + v0 * D;
+            pw.overlap = want_x;  // behind dX, which has waited for P
+            if ((st = op_product(dev, pw, arena, s)) != PGEMM_OK) return st;
+            if ((st = op_product_join(dev, pw, arena, s)) != PGEMM_OK) return st;
         }
+        if (want_x && !x_pieces && (st = op_product_join(dev, px, arena, s)) != PGEMM_OK) return st;
     }
     if (x_pieces) {
         uint16_t *out[2] = {dX, nullptr};
