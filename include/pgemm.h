@@ -293,9 +293,11 @@ PGEMM_API pgemm_status xent_bf16(int T, int V, int D, const uint16_t *X, const u
                                  pgemm_stream_t stream);
 
 /* xent_bf16 together with its gradients: with
- * P[t][v] = (exp(L[t][v] - lse[t]) - (v == target[t])) * dloss[t] (rounded to
- * bf16, as the products' operand; dloss NULL: ones; rows that do not count:
- * zero), dX (T x D) <- P W and dW (V x D) <- P^T X.  Either may be NULL.
+ * P[t][v] = (exp(L[t][v] - lse[t]) - (v == target[t])) * dloss[t] (dloss
+ * NULL: ones; rows that do not count: zero), dX (T x D) <- P W and
+ * dW (V x D) <- P^T X.  P is rounded to bf16, as the products' operand, after
+ * division by the largest |dloss| of a row that counts, which multiplies the
+ * sums instead.  Either may be NULL.
  * workspace_bytes bounds the scratch that holds P, 2 T V bytes, or with
  * T <= 64 the logits and P, 6 T V bytes (0: the library's choice, 2 GiB); more
  * than that goes by in pieces of the vocabulary, whose logits are computed a

@@ -21,27 +21,33 @@ struct EpiGated {
                                         const OpUnit &w, Acc &acc, uint32_t e) const {
         int col0, width;
         const bool mine = epi_cols_dual<Cfg>(w, e, col0, width);
-        const bool have = acc.have();
-        if (!acc.wait()) return false;
-        if (!mine) {
-            acc.release();
-            return true;
-        }
-        const uint32_t t_row = acc.row() + col0;
+        if (!mine) return acc.skip();
         const int n0 = w.n0 + col0;
         uint32_t g[2][32], u[2][32], p[32];
-        if (have) {
+        if constexpr (Cfg::ROUND > 0) {
+            float x[64], y[64];
+            if (!acc_sum<64, 64>(acc, col0, x, width + col0, y)) return false;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                tmem_ld_32x32b_x32(t_row + 32 * k, g[k]);
-                tmem_ld_32x32b_x32(t_row + width + 32 * k, u[k]);
+            for (int j = 0; j < 64; ++j) {
+                g[j / 32][j % 32] = __float_as_uint(x[j]);
+                u[j / 32][j % 32] = __float_as_uint(y[j]);
             }
-            tmem_ld_wait();
         } else {
+            if (!acc.wait()) return false;
+            const uint32_t t_row = acc.row() + col0;
+            if (acc.have()) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) g[0][j] = g[1][j] = u[0][j] = u[1][j] = 0u;
+                for (int k = 0; k < 2; ++k) {
+                    tmem_ld_32x32b_x32(t_row + 32 * k, g[k]);
+                    tmem_ld_32x32b_x32(t_row + width + 32 * k, u[k]);
+                }
+                tmem_ld_wait();
+            } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) g[0][j] = g[1][j] = u[0][j] = u[1][j] = 0u;
+            }
+            acc.release();
         }
-        acc.release();
         if (preact != nullptr) {
             const CUtensorMap *mg = tma_preact ? &maps.c[1] : nullptr;
             const CUtensorMap *mu = tma_preact ? &maps.c[2] : nullptr;
@@ -52,7 +58,7 @@ struct EpiGated {
                             u[k / 2] + 16 * (k % 2));
             }
         }
-        with_act(act, [&](auto A) {
+        auto combine = [&](auto A) {
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -62,7 +68,11 @@ struct EpiGated {
                             __uint_as_float(u[k][2 * j]),
                         act_value<decltype(A)::value>(__uint_as_float(g[k][2 * j + 1])) *
                             __uint_as_float(u[k][2 * j + 1]));
-        });
+        };
+        if constexpr (Cfg::ROUND > 0)
+            combine(std::integral_constant<int, PGEMM_ACT_RELU>{});
+        else
+            with_act(act, combine);
         if (tma_h) {
             put_rows32_batch<2>(c, &maps.c[0], n0, p);
         } else {
@@ -88,25 +98,16 @@ struct EpiGatedGrad {
                                         const OpUnit &w, Acc &acc, uint32_t e) const {
         int col0, width;
         const bool mine = epi_cols_dual<Cfg>(w, e, col0, width);
-        const bool have = acc.have();
+        if (!mine) return acc.skip();
         RowsIn in{dh, ld};
-        if (mine) in.load(c, w.n0 + col0);  // travels while the products finish
-        if (!acc.wait()) return false;
-        if (!mine) {
-            acc.release();
-            return true;
-        }
-        const uint32_t t_row = acc.row() + col0;
-#pragma unroll 1
-        for (int k = 0; k < 2; ++k) {
+        in.load(c, w.n0 + col0);  // travels while the products finish
+        // 32 columns from w.n0 + col0 + 32 k
+        auto finish = [&](int k, const uint32_t *g, const uint32_t *u) {
             const int n = w.n0 + col0 + 32 * k;
-            uint32_t g[32], u[32], r[16], p[16], q[16];
-            acc_cols32(t_row + 32 * k, have, g);
-            acc_cols32(t_row + width + 32 * k, have, u);
-            if (k == 1) acc.release();
+            uint32_t r[16], p[16], q[16];
             in.take(c, r);
             if (k == 0) in.load(c, n + 32);
-            with_act(act, [&](auto A) {
+            auto derive = [&](auto A) {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     const float y0 = bf16_lo(r[j]), y1 = bf16_hi(r[j]);
@@ -119,9 +120,39 @@ struct EpiGatedGrad {
                                      y1 * d1 * __uint_as_float(u[2 * j + 1]));
                     q[j] = pack_bf16(y0 * a0, y1 * a1);
                 }
-            });
+            };
+            if constexpr (Cfg::ROUND > 0)
+                derive(std::integral_constant<int, PGEMM_ACT_RELU>{});
+            else
+                with_act(act, derive);
             put_rows32(c, &maps.c[0], dg, dz_ld, n, p);
             put_rows32(c, &maps.c[1], du, dz_ld, n, q);
+        };
+        if constexpr (Cfg::ROUND > 0) {
+            float x[64], y[64];
+            if (!acc_sum<64, 64>(acc, col0, x, width + col0, y)) return false;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint32_t g[32], u[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    g[j] = __float_as_uint(x[32 * k + j]);
+                    u[j] = __float_as_uint(y[32 * k + j]);
+                }
+                finish(k, g, u);
+            }
+            return true;
+        }
+        const bool have = acc.have();
+        if (!acc.wait()) return false;
+        const uint32_t t_row = acc.row() + col0;
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+            uint32_t g[32], u[32];
+            acc_cols32(t_row + 32 * k, have, g);
+            acc_cols32(t_row + width + 32 * k, have, u);
+            if (k == 1) acc.release();
+            finish(k, g, u);
         }
         return true;
     }
@@ -152,13 +183,20 @@ static pgemm_status launch_dual(const OpDevice &dev, int M, int F, int K, const 
 using DualPair = OpCfg<256, 3, 2, 2, false, false, true>;
 using DualOne = OpCfg<128, 6, 1, 1, false, false, true>;
 
+using SignDualPair = OpCfg<256, 3, 2, 2, false, false, true, SignPair::value>;
+using SignDualOne = OpCfg<128, 6, 1, 1, false, false, true, SignOne::value>;
+
+// sign: the epilogue decides a ReLU's derivative, or keeps what will.
 template <class Epi>
 static pgemm_status launch_dual_size(const OpDevice &dev, int M, int F, int K, const OpMat &X,
                                      const OpMat &Wg, const OpMat &Wu, OpMaps &maps, const Epi &e,
-                                     cudaStream_t s) {
-    return op_use_pair(dev, M, F, 128, 64, 1)
-               ? launch_dual<DualPair>(dev, M, F, K, X, Wg, Wu, maps, e, s)
-               : launch_dual<DualOne>(dev, M, F, K, X, Wg, Wu, maps, e, s);
+                                     bool sign, cudaStream_t s) {
+    const bool pair = op_use_pair(dev, M, F, 128, 64, 1);
+    if (sign && op_sign_rounds(e.act, K))
+        return pair ? launch_dual<SignDualPair>(dev, M, F, K, X, Wg, Wu, maps, e, s)
+                    : launch_dual<SignDualOne>(dev, M, F, K, X, Wg, Wu, maps, e, s);
+    return pair ? launch_dual<DualPair>(dev, M, F, K, X, Wg, Wu, maps, e, s)
+                : launch_dual<DualOne>(dev, M, F, K, X, Wg, Wu, maps, e, s);
 }
 
 static bool act_known(int act) { return act >= PGEMM_ACT_NONE && act <= PGEMM_ACT_SILU; }
@@ -196,7 +234,7 @@ static pgemm_status gated_forward(int M, int F, int K, const uint16_t *X, const 
                                M, F);
     }
     if (st != PGEMM_OK) return st;
-    return launch_dual_size(dev, M, F, K, x, wg, wu, maps, e, s);
+    return launch_dual_size(dev, M, F, K, x, wg, wu, maps, e, preact != nullptr, s);
 }
 
 static pgemm_status gated_backward(int M, int F, int K, const uint16_t *X, const uint16_t *Wg,
@@ -273,7 +311,7 @@ static pgemm_status gated_backward(int M, int F, int K, const uint16_t *X, const
             if (st == PGEMM_OK)
                 st = op_encode_out(&maps.c[1], OpElem::BF16, du_buf, F, M, du.ld);
             if (st == PGEMM_OK)
-                st = launch_dual_size(dev, M, F, K, x, wg, wu, maps, e, s);
+                st = launch_dual_size(dev, M, F, K, x, wg, wu, maps, e, true, s);
         }
         if (st != PGEMM_OK) return st;
     }

@@ -33,6 +33,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "op_host.h"
 #include "ptx.cuh"
@@ -445,6 +447,15 @@ struct OpAcc {
         }
         ++gr;
     }
+    // pass all of the unit's rounds on unread
+    __device__ __forceinline__ bool skip() {
+#pragma unroll 1
+        for (int r = 0; r < rounds; ++r) {
+            if (!wait()) return false;
+            release();
+        }
+        return true;
+    }
 };
 
 // Epi: a struct of kernel parameters with
@@ -716,6 +727,49 @@ __device__ __forceinline__ void acc_cols32(uint32_t taddr, bool have, uint32_t (
         for (int j = 0; j < 32; ++j) v[j] = 0u;
     }
 }
+
+// v += N accumulator columns from taddr.
+template <int N>
+__device__ __forceinline__ void acc_add(uint32_t taddr, float *v) {
+#pragma unroll
+    for (int c = 0; c < N; c += 16) {
+        uint32_t x[16];
+        tmem_ld_32x32b_x16(taddr + c, x);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[c + j] += __uint_as_float(x[j]);
+    }
+}
+
+// All rounds of a unit, added in fp32 registers: N columns from col, and with
+// N2 > 0 another N2 from col2.  false: a wait ran out.
+template <int N, int N2, class Acc>
+__device__ __forceinline__ bool acc_sum(Acc &acc, int col, float *v, int col2, float *v2) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < N2; ++j) v2[j] = 0.0f;
+#pragma unroll 1
+    for (int r = 0; r < acc.rounds; ++r) {
+        if (!acc.wait()) return false;
+        const uint32_t t = acc.row();
+        acc_add<N>(t + col, v);
+        if constexpr (N2 > 0) acc_add<N2>(t + col2, v2);
+        acc.release();
+    }
+    return true;
+}
+
+// What a ReLU's derivative needs: it jumps at zero, and a pre-activation whose
+// sign the rounding of its sum flips puts a whole dY in the wrong place.  The
+// tensor core truncates its running sum every 16 products, toward zero: a chain
+// of K = 8192 ends 4e-6 of itself short, an fp32 sum with rounding 1e-6.  Rounds of
+// 512 products added in registers end at 5e-7.  So products whose Z decides a
+// ReLU run in rounds when K is longer than one; smooth activations do not need it.
+constexpr int kSignRound = 512;
+inline bool op_sign_rounds(int act, int K) { return act == PGEMM_ACT_RELU && K > kSignRound; }
+using SignPair = std::integral_constant<int, kSignRound / 128>;  // K-tiles a round
+using SignOne = std::integral_constant<int, kSignRound / 64>;
 
 // ------------------------------------------------------------------- host ---
 // Schedule slots: one block (or pair) per SM.

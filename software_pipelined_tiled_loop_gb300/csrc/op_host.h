@@ -120,6 +120,7 @@ struct OpEpilogue {
     int act = PGEMM_ACT_NONE;
     const uint16_t *residual = nullptr;  // M x N, rows of N
     float *preact = nullptr;             // M x N fp32, rows of N: acc + bias
+    const float *scale = nullptr;        // one value on the device that multiplies acc
 };
 
 // out[j] (bf16, rows of N) = epilogue(sum over K segments of A * B).

@@ -24,14 +24,10 @@ struct EpiLinearGrad {
         const bool have = acc.have();
         RowsIn in{dy, dy_ld};
         in.load(c, nf);  // travels while the products finish
-        if (!acc.wait()) return false;
-        const uint32_t t_row = acc.row() + col0;
-#pragma unroll 1
-        for (int cc = 0; cc < cols; cc += 32) {
+        // 32 columns from nf + cc: v holds the accumulator's
+        auto finish = [&](int cc, uint32_t *v) {
             const int n = nf + cc;
-            uint32_t v[32], r[16], p[16];
-            acc_cols32(t_row + cc, have, v);
-            if (cc + 32 >= cols) acc.release();
+            uint32_t r[16], p[16];
             if (bias != nullptr) {
                 float b[32];
                 get_vec32(bias, c.N, n, b);
@@ -40,7 +36,7 @@ struct EpiLinearGrad {
             }
             in.take(c, r);
             if (cc + 32 < cols) in.load(c, n + 32);
-            with_act(act, [&](auto A) {
+            auto derive = [&](auto A) {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     float value;
@@ -52,8 +48,34 @@ struct EpiLinearGrad {
                         act_value_grad<decltype(A)::value>(__uint_as_float(v[2 * j + 1]), value);
                     p[j] = pack_bf16(lo, hi);
                 }
-            });
+            };
+            if constexpr (Cfg::ROUND > 0)
+                derive(std::integral_constant<int, PGEMM_ACT_RELU>{});
+            else
+                with_act(act, derive);
             put_rows32(c, &maps.c[0], dz, dz_ld, n, p);
+        };
+        if constexpr (Cfg::ROUND > 0) {
+            float f[Cfg::EPI_COLS];
+            if (!acc_sum<Cfg::EPI_COLS, 0>(acc, col0, f, 0, nullptr)) return false;
+#pragma unroll
+            for (int b = 0; b < Cfg::EPI_COLS / 32; ++b) {
+                if (32 * b >= cols) break;
+                uint32_t v[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(f[32 * b + j]);
+                finish(32 * b, v);
+            }
+            return true;
+        }
+        if (!acc.wait()) return false;
+        const uint32_t t_row = acc.row() + col0;
+#pragma unroll 1
+        for (int cc = 0; cc < cols; cc += 32) {
+            uint32_t v[32];
+            acc_cols32(t_row + cc, have, v);
+            if (cc + 32 >= cols) acc.release();
+            finish(cc, v);
         }
         return true;
     }
@@ -200,9 +222,15 @@ static pgemm_status linear_backward(int M, int N, int K, const uint16_t *X, cons
             st = op_act_grad(dev, g, arena, false, s);
         } else {
             const EpiLinearGrad e{bias, dY, N, dz_buf, dz.ld, act};
-            st = op_use_pair(dev, M, N, 256, 128, 1)
-                     ? launch_grad<OpCfg<256, 3, 2, 2, false, false>>(dev, M, N, K, x, w, e, s)
-                     : launch_grad<OpCfg<128, 6, 1, 1, false, false>>(dev, M, N, K, x, w, e, s);
+            const bool pair = op_use_pair(dev, M, N, 256, 128, 1);
+            if (op_sign_rounds(act, K))
+                st = pair ? launch_grad<OpCfg<256, 3, 2, 2, false, false, false, SignPair::value>>(
+                                dev, M, N, K, x, w, e, s)
+                          : launch_grad<OpCfg<128, 6, 1, 1, false, false, false, SignOne::value>>(
+                                dev, M, N, K, x, w, e, s);
+            else
+                st = pair ? launch_grad<OpCfg<256, 3, 2, 2, false, false>>(dev, M, N, K, x, w, e, s)
+                          : launch_grad<OpCfg<128, 6, 1, 1, false, false>>(dev, M, N, K, x, w, e, s);
         }
         if (st != PGEMM_OK) return st;
     }

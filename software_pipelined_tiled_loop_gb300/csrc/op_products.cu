@@ -20,6 +20,7 @@ template <bool FULL>
 struct EpiOut {
     const uint16_t *bias, *residual;
     float *preact, *parts;
+    const float *scale;     // one device value that multiplies acc, or nullptr
     uint16_t *out[2];
     long long ldo;          // row length of out, residual and preact
     long long parts_ld, parts_rows;
@@ -35,56 +36,27 @@ struct EpiOut {
         epi_cols<Cfg>(w, e, col0, cols);
         const int nf = w.n0 + col0;
         const bool have = acc.have();
-        if (parts != nullptr) {
-            if (!acc.wait()) return false;
-            const uint32_t t_row = acc.row() + col0;
-            const int row0 = static_cast<int>(
-                (static_cast<long long>(w.part) * parts_segments + w.seg) * parts_rows + c.m0);
-#pragma unroll 1
-            for (int cc = 0; cc < cols; cc += 32) {
-                uint32_t v[32];
-                acc_cols32(t_row + cc, have, v);
-                if (cc + 32 >= cols) acc.release();
-                put_words16(c, &maps.c[0], nullptr, 0, row0, nf + cc, v);
-                put_words16(c, &maps.c[0], nullptr, 0, row0, nf + cc + 16, v + 16);
-            }
-            return true;
-        }
         const CUtensorMap *map = tma_out ? &maps.c[w.seg] : nullptr;
         uint16_t *o = out[w.seg];
-        if (plain && map != nullptr && have && cols == Cfg::EPI_COLS) {
-            // nothing but rounding: read the whole accumulator at once, hand it
-            // back, and stage as much as fits in one go
-            if (!acc.wait()) return false;
-            const uint32_t t_row = acc.row() + col0;
-            constexpr int C = Cfg::EPI_COLS / 32, B = C < Cfg::NBUF ? C : Cfg::NBUF;
-            uint32_t v[32 * C];
-#pragma unroll
-            for (int b = 0; b < C; ++b)
-                tmem_ld_32x32b_x32(t_row + 32 * b, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * b));
-            tmem_ld_wait();
-            acc.release();
-#pragma unroll
-            for (int j = 0; j < 16 * C; ++j)
-                v[j] = pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-#pragma unroll
-            for (int b = 0; b < C; b += B)
-                put_rows32_batch<B>(c, map, nf + 32 * b, v + 16 * b);
-            return true;
-        }
-        // 32 columns at a time.  The residual's next columns travel while the
-        // products finish, and then while the present ones are worked on.
+        const int row0 = static_cast<int>(
+            (static_cast<long long>(w.part) * parts_segments + w.seg) * parts_rows + c.m0);
+        auto put_part = [&](int n, const uint32_t *v) {
+            put_words16(c, &maps.c[0], nullptr, 0, row0, n, v);
+            put_words16(c, &maps.c[0], nullptr, 0, row0, n + 16, v + 16);
+        };
+        // the residual's next columns travel while the products finish, and then
+        // while the present ones are worked on
         RowsIn res{residual, ldo};
-        const bool have_r = FULL && residual != nullptr;
-        if (have_r) res.load(c, nf);
-        if (!acc.wait()) return false;
-        const uint32_t t_row = acc.row() + col0;
-#pragma unroll 1
-        for (int cc = 0; cc < cols; cc += 32) {
+        const bool have_r = FULL && residual != nullptr && parts == nullptr;
+        // 32 columns from nf + cc: v holds the accumulator's
+        auto finish = [&](int cc, uint32_t *v) {
             const int n = nf + cc;
-            uint32_t v[32], p[16];
-            acc_cols32(t_row + cc, have, v);
-            if (cc + 32 >= cols) acc.release();
+            uint32_t p[16];
+            if (scale != nullptr) {
+                const float f = *scale;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
+            }
             if constexpr (FULL) {
                 if (bias != nullptr) {
                     float b[32];
@@ -98,13 +70,16 @@ struct EpiOut {
                     put_words16(c, mz, preact, ldo, c.m0, n, v);
                     put_words16(c, mz, preact, ldo, c.m0, n + 16, v + 16);
                 }
-                if (act != PGEMM_ACT_NONE)
-                    with_act(act, [&](auto A) {
+                auto activate = [&](auto A) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            v[j] = __float_as_uint(
-                                act_value<decltype(A)::value>(__uint_as_float(v[j])));
-                    });
+                    for (int j = 0; j < 32; ++j)
+                        v[j] = __float_as_uint(
+                            act_value<decltype(A)::value>(__uint_as_float(v[j])));
+                };
+                if constexpr (Cfg::ROUND > 0)
+                    activate(std::integral_constant<int, PGEMM_ACT_RELU>{});
+                else if (act != PGEMM_ACT_NONE)
+                    with_act(act, activate);
                 if (have_r) {
                     uint32_t r[16];
                     res.take(c, r);
@@ -121,6 +96,66 @@ struct EpiOut {
             for (int j = 0; j < 16; ++j)
                 p[j] = pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
             put_rows32(c, map, o, ldo, n, p);
+        };
+        if constexpr (Cfg::ROUND > 0) {
+            float f[Cfg::EPI_COLS];
+            if (have_r) res.load(c, nf);
+            // (a half-width unit's second warps read columns of the other unit's
+            // width, which hold whatever was there: finish() is not given them)
+            if (!acc_sum<Cfg::EPI_COLS, 0>(acc, col0, f, 0, nullptr)) return false;
+#pragma unroll
+            for (int b = 0; b < Cfg::EPI_COLS / 32; ++b) {
+                if (32 * b >= cols) break;
+                uint32_t v[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(f[32 * b + j]);
+                if (parts != nullptr)
+                    put_part(nf + 32 * b, v);
+                else
+                    finish(32 * b, v);
+            }
+            return true;
+        }
+        if (plain && parts == nullptr && map != nullptr && have && cols == Cfg::EPI_COLS) {
+            // nothing but rounding: read the whole accumulator at once, hand it
+            // back, and stage as much as fits in one go
+            if (!acc.wait()) return false;
+            const uint32_t t_row = acc.row() + col0;
+            constexpr int C = Cfg::EPI_COLS / 32, B = C < Cfg::NBUF ? C : Cfg::NBUF;
+            uint32_t v[32 * C];
+#pragma unroll
+            for (int b = 0; b < C; ++b)
+                tmem_ld_32x32b_x32(t_row + 32 * b, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * b));
+            tmem_ld_wait();
+            acc.release();
+            if (scale != nullptr) {
+                const float f = *scale;
+#pragma unroll
+                for (int j = 0; j < 16 * C; ++j)
+                    v[j] = pack_bf16(__uint_as_float(v[2 * j]) * f,
+                                     __uint_as_float(v[2 * j + 1]) * f);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16 * C; ++j)
+                    v[j] = pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+            }
+#pragma unroll
+            for (int b = 0; b < C; b += B)
+                put_rows32_batch<B>(c, map, nf + 32 * b, v + 16 * b);
+            return true;
+        }
+        if (have_r) res.load(c, nf);
+        if (!acc.wait()) return false;
+        const uint32_t t_row = acc.row() + col0;
+#pragma unroll 1
+        for (int cc = 0; cc < cols; cc += 32) {
+            uint32_t v[32];
+            acc_cols32(t_row + cc, have, v);
+            if (cc + 32 >= cols) acc.release();
+            if (parts != nullptr)
+                put_part(nf + cc, v);
+            else
+                finish(cc, v);
         }
         return true;
     }
@@ -197,6 +232,7 @@ static pgemm_status launch_form(const OpDevice &dev, const OpProduct &p, float *
     }
     EpiOut<FULL> e{};
     e.act = p.epi.act;
+    e.scale = p.epi.scale;
     e.bias = p.epi.bias;
     e.residual = p.epi.residual;
     e.preact = p.epi.preact;
@@ -254,11 +290,18 @@ template <bool A_MN, bool B_K>
 using ShortCfg = OpCfg<256, 5, 1, 2, A_MN, B_K, false, 0, 4>;
 template <bool A_MN, bool B_K>
 using OneCfg = OpCfg<128, 6, 1, 1, A_MN, B_K>;
+using SignPairCfg = OpCfg<256, 3, 2, 2, false, false, false, SignPair::value>;
+using SignOneCfg = OpCfg<128, 6, 1, 1, false, false, false, SignOne::value>;
 
 template <bool FULL, bool A_MN, bool B_K>
 static pgemm_status launch_size(const OpDevice &dev, const OpProduct &p, float *area,
                                 cudaStream_t s) {
     const OpPlan &plan = p.plan;
+    if constexpr (FULL) {
+        if (p.epi.preact && op_sign_rounds(p.epi.act, p.K))
+            return plan.pair ? launch_form<SignPairCfg, FULL>(dev, p, area, plan.parts, s)
+                             : launch_form<SignOneCfg, FULL>(dev, p, area, plan.parts, s);
+    }
     if (plan.pair && static_cast<long long>(p.K) * p.k_segments <= kShortK)
         return launch_form<ShortCfg<A_MN, B_K>, FULL>(dev, p, area, plan.parts, s);
     return plan.pair ? launch_form<PairCfg<A_MN, B_K>, FULL>(dev, p, area, plan.parts, s)
@@ -335,6 +378,10 @@ __global__ void __launch_bounds__(256) join_parts_kernel(const JoinParams p) {
         }
         const long long at = m * p.N + n;
         const int cols = min(4, p.N - n);
+        if (p.e.scale) {
+            const float f = *p.e.scale;
+            for (int j = 0; j < 4; ++j) v[j] *= f;
+        }
         for (int j = 0; j < cols; ++j) {
             if (p.e.bias) v[j] += __uint_as_float(static_cast<uint32_t>(p.e.bias[n + j]) << 16);
             if (p.e.preact) p.e.preact[at + j] = v[j];

@@ -2,8 +2,15 @@
 // (W: one row of D for each of V tokens), and its gradients, without keeping L.
 //
 //   lse_t  = log sum_v exp L_tv          loss_t = lse_t - L_t,y(t)
-//   P_tv   = (exp(L_tv - lse_t) - [v = y(t)]) dloss_t
-//   dX     = P W                         dW = P^T X
+//   P_tv   = (exp(L_tv - lse_t) - [v = y(t)]) dloss_t / c,  c = max_t |dloss_t|
+//   dX     = c P W                       dW = c P^T X
+//
+// P is rounded to bf16 as an operand of the last two products; c is what keeps
+// that rounding from adding up.  A row's entry at its target is nearly -dloss_t
+// and outweighs the rest of the row; with dloss the same for all rows (a mean)
+// every one of them would round by the same up to 2^-9 of itself, and the whole
+// gradient with them.  Divided by c those entries start from exactly -1; c
+// itself multiplies the sums in fp32.
 //
 // Forward: the product's epilogue folds every accumulator into a running
 // maximum m and sum s of exp(L - m) for each row and column block (a thread
@@ -59,32 +66,10 @@ struct EpiXentStats {
         // the one it has
         constexpr int COLS = Cfg::EPI_COLS;
         const int col0 = static_cast<int>(e >> 2) * COLS;
-        if (Cfg::HALVES && w.half && e >= 4) {
-#pragma unroll 1
-            for (int r = 0; r < acc.rounds; ++r) {
-                if (!acc.wait()) return false;
-                acc.release();
-            }
-            return true;
-        }
+        if (Cfg::HALVES && w.half && e >= 4) return acc.skip();
         const int n0 = w.n0 + col0;
         float v[COLS];
-#pragma unroll
-        for (int j = 0; j < COLS; ++j) v[j] = 0.0f;
-#pragma unroll 1
-        for (int r = 0; r < acc.rounds; ++r) {
-            if (!acc.wait()) return false;
-            const uint32_t t_row = acc.row() + col0;
-#pragma unroll
-            for (int cc = 0; cc < COLS; cc += 16) {
-                uint32_t x[16];
-                tmem_ld_32x32b_x16(t_row + cc, x);
-                tmem_ld_wait();
-#pragma unroll
-                for (int j = 0; j < 16; ++j) v[cc + j] += __uint_as_float(x[j]);
-            }
-            acc.release();
-        }
+        if (!acc_sum<COLS, 0>(acc, col0, v, 0, nullptr)) return false;
         const int left = c.N - n0;  // columns of the vocabulary in this block
         if (left <= 0) return true;
         if (left < COLS) {
@@ -125,7 +110,7 @@ struct EpiXentStats {
 // P of one piece of the vocabulary.
 struct EpiXentGrad {
     const int64_t *target;
-    const float *lse, *dloss;  // dloss nullptr: 1
+    const float *lse, *dloss, *scale;  // dloss nullptr: 1, and no scale
     long long v0;              // the piece's first token
     long long V;
 
@@ -140,7 +125,7 @@ struct EpiXentGrad {
         const int64_t y = in ? __ldg(target + c.row()) : -1;
         const bool counts = y >= 0 && y < V;
         const float l = counts ? lse[c.row()] * kLog2e : 0.0f;
-        const float g = counts ? (dloss ? dloss[c.row()] : 1.0f) : 0.0f;
+        const float g = counts ? (dloss ? dloss[c.row()] / *scale : 1.0f) : 0.0f;
         const int64_t yc = y - v0 - n0;
         if (!acc.wait()) return false;
         const uint32_t t_row = acc.row() + col0;
@@ -181,7 +166,7 @@ template <int ROWS>
 __global__ void __launch_bounds__(256)
     xent_join_kernel(const float *part_m, const float *part_s, long long rows, int blocks, int T,
                      long long V, int D, const OpMat X, const OpMat W, const int64_t *target,
-                     float *loss, float *lse) {
+                     float *loss, float *lse, const float *dloss, float *scale) {
     grid_dependency_wait();
     grid_launch_dependents();
     __shared__ float sm[8][ROWS], ss[8][ROWS], dot[8];
@@ -251,6 +236,26 @@ __global__ void __launch_bounds__(256)
         if (lse) lse[t] = l;
         if (loss) loss[t] = y >= 0 && y < V ? l - d : 0.0f;
     }
+    if (dloss != nullptr && blockIdx.x == 0) {
+        // the common scale of P (xent): the largest |dloss| of a row that counts
+        __syncthreads();
+        float g = 0.0f;
+#pragma unroll 8
+        for (int i = static_cast<int>(threadIdx.x); i < T; i += 256) {
+            const int64_t y = target[i];
+            const float v = fabsf(dloss[i]);
+            if (y >= 0 && y < V && v < CUDART_INF_F) g = fmaxf(g, v);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+        if (lane == 0) dot[w] = g;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+#pragma unroll
+            for (int i = 1; i < 8; ++i) g = fmaxf(g, dot[i]);
+            *scale = g > 0.0f ? g : 1.0f;
+        }
+    }
 }
 
 // P from the kept exponentials, in place (fp16 to bf16):
@@ -261,7 +266,8 @@ __global__ void __launch_bounds__(256)
 template <int COLS>
 __global__ void __launch_bounds__(256)
     xent_scale_kernel(uint16_t *P, long long ld, int T, int V, const float *part_m, long long rows,
-                      const float *lse, const int64_t *target, const float *dloss) {
+                      const float *lse, const int64_t *target, const float *dloss,
+                      const float *scale) {
     grid_dependency_wait();
     grid_launch_dependents();
     constexpr int NB = 1024 / COLS;
@@ -274,7 +280,7 @@ __global__ void __launch_bounds__(256)
     const int t = row0 + lane;
     const int64_t y = t < T ? target[t] : -1;
     const bool counts = y >= 0 && y < V;
-    const float gt = counts ? (dloss ? dloss[t] : 1.0f) : 0.0f;
+    const float gt = counts ? (dloss ? dloss[t] / *scale : 1.0f) : 0.0f;
     if (w == 0) {
         g[lane] = gt;
         yc[lane] = counts && y >= c0 && y < c0 + 1024 ? static_cast<int>(y - c0) : -1;
@@ -534,7 +540,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
 // P from kept logits: a thread eight columns of a row.
 __global__ void __launch_bounds__(256)
     xent_probs_kernel(const float *logits, uint16_t *P, long long ld, int T, int V,
-                      const float *lse, const int64_t *target, const float *dloss) {
+                      const float *lse, const int64_t *target, const float *dloss,
+                      const float *scale) {
     grid_dependency_wait();
     grid_launch_dependents();
     const int octets = (V + 7) / 8;
@@ -544,7 +551,7 @@ __global__ void __launch_bounds__(256)
         const int c = static_cast<int>(i - static_cast<long long>(t) * octets) * 8;
         const int64_t y = target[t];
         const bool counts = y >= 0 && y < V;
-        const float g = counts ? (dloss ? dloss[t] : 1.0f) : 0.0f;
+        const float g = counts ? (dloss ? dloss[t] / *scale : 1.0f) : 0.0f;
         const float l = counts ? lse[t] * kLog2e : 0.0f;
         const float4 *src = reinterpret_cast<const float4 *>(logits + t * ld + c);
         const float4 p = src[0], q = src[1];
@@ -687,6 +694,8 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
     const long long at_m = arena.add(blocks * rows * 4);
     const long long at_s = arena.add(blocks * rows * 4);
     const long long at_l = lse ? 0 : arena.add(rows * 4);
+    if (pieces == 0) dloss = nullptr;
+    const long long at_c = dloss ? arena.add(4) : 0;
     const long long at_p = pieces ? arena.add(piece * T * 2) : 0;
     const bool keep_logits = few && pieces == 1;
     const long long at_z = keep_logits ? arena.add(piece * T * 4) : 0;
@@ -722,6 +731,8 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
     if ((st = arena.alloc()) != PGEMM_OK) return st;
     if ((st = rl.run(dev, arena, s)) != PGEMM_OK) return st;
     float *lse_buf = lse ? lse : arena.at<float>(at_l);
+    float *scale = dloss ? arena.at<float>(at_c) : nullptr;  // c
+    px.epi.scale = pw.epi.scale = scale;
 
     // One piece: its exponentials are kept and P follows from them.
     const bool keep = pieces == 1 && D >= kKeepMinD && !few;
@@ -752,7 +763,7 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
                           dim3(by_row ? T : (T + 7) / 8), dim3(256), s,
                           static_cast<const float *>(part_m), static_cast<const float *>(part_s),
                           rows, blocks, T, static_cast<long long>(V), D, x, w, target, loss,
-                          lse_buf);
+                          lse_buf, dloss, scale);
         if (st != PGEMM_OK) return st;
     }
 
@@ -765,19 +776,21 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
             const long long most = dev.sm_count * 8ll;
             st = launch_small(xent_probs_kernel, dim3(static_cast<unsigned>(n < most ? n : most)),
                               dim3(256), s, static_cast<const float *>(arena.at<float>(at_z)), P,
-                              piece, T, V, static_cast<const float *>(lse_buf), target, dloss);
+                              piece, T, V, static_cast<const float *>(lse_buf), target, dloss,
+                              static_cast<const float *>(scale));
         } else if (keep) {
             const dim3 grid(static_cast<unsigned>((V + 1023) / 1024) * ((T + 31) / 32));
             st = launch_small(pair ? xent_scale_kernel<StatsPair::EPI_COLS>
                                    : xent_scale_kernel<StatsOne::EPI_COLS>,
                               grid, dim3(256), s, P, piece, T, V,
                               static_cast<const float *>(part_m), rows,
-                              static_cast<const float *>(lse_buf), target, dloss);
+                              static_cast<const float *>(lse_buf), target, dloss,
+                              static_cast<const float *>(scale));
         } else {
             OpMaps maps{};
             st = op_encode_out(&maps.c[0], OpElem::BF16, P, cols, T, piece);
             if (st != PGEMM_OK) return st;
-            const EpiXentGrad e{target, lse_buf, dloss, v0, V};
+            const EpiXentGrad e{target, lse_buf, dloss, scale, v0, V};
             st = op_use_pair(dev, T, cols, 256, 128, 1)
                      ? launch_logits<XentPair>(dev, T, cols, D, x, w, v0, maps, e, s)
                      : launch_logits<XentOne>(dev, T, cols, D, x, w, v0, maps, e, s);
@@ -807,7 +820,9 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
     }
     if (x_pieces) {
         uint16_t *out[2] = {dX, nullptr};
-        st = op_join_parts(dev, arena.at<float>(at_x), x_parts, 1, T, D, out, OpEpilogue{}, s);
+        OpEpilogue scaled;
+        scaled.scale = scale;
+        st = op_join_parts(dev, arena.at<float>(at_x), x_parts, 1, T, D, out, scaled, s);
     }
     return st;
 }

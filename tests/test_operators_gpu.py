@@ -124,6 +124,50 @@ def test_linear_backward_activations_and_absent_outputs(name):
     ref.check(db, *want["db"], "dbias")
 
 
+# one CTA's tiles; pairs, and half-width units; parts along K
+RELU_SIZES = [(150, 264, 1100), (2500, 1400, 1032), (260, 136, 4104)]
+
+
+@pytest.mark.parametrize("M,N,K", RELU_SIZES)
+def test_relu_pre_activations_are_summed_in_rounds(M, N, K):
+    # rounds of 512 products, added with rounding: a chain of 32 steps and one
+    # more for each round
+    X, W, b, R = linear_inputs(M, N, K, 520)
+    Y, Z = nan_like(M, N), nan_like(M, N, dtype=torch.float32)
+    pg.linear_bf16(M, N, K, X, W, b, "relu", R, Y, preact=Z)
+    y, bound, z, _ = ref.linear(X, W, b, "relu", R)
+    ref.check(Y, y, bound, "Y")
+    size = X.double().abs() @ W.double().abs() + b.double().abs()
+    ref.check(Z, z, ref.step(512 + 16 * (K // 512 + 1)) * size, "preact")
+    dY = rnd(521, M, N)
+    want = ref.linear_backward(X, W, b, "relu", dY)
+    for kept in (Z, None):
+        dX, dW, db = nan_like(M, K), nan_like(K, N), nan_like(N)
+        pg.linear_bf16_backward(M, N, K, X, W, b, "relu", dY, dX, dW, db, preact=kept)
+        ref.check(dX, *want["dX"], "dX")
+        ref.check(dW, *want["dW0"], "dW")
+        ref.check(db, *want["db"], "dbias")
+
+
+@pytest.mark.parametrize("M,F,K", RELU_SIZES)
+def test_gated_relu_in_rounds(M, F, K):
+    X, Wg, Wu = gated_inputs(M, F, K, 530)
+    H, Z = nan_like(M, F), nan_like(2, M, F, dtype=torch.float32)
+    pg.gated_bf16(M, F, K, X, Wg, Wu, "relu", H, preact=Z)
+    h, bound, g, u, eg, eu, _, _ = ref.gated(X, Wg, Wu, "relu")
+    ref.check(H, h, bound, "H")
+    ref.check(Z[0], g, eg, "X Wg")
+    ref.check(Z[1], u, eu, "X Wu")
+    dH = rnd(531, M, F)
+    want = ref.gated_backward(X, Wg, Wu, "relu", dH)
+    for kept in (Z, None):
+        dX, dWg, dWu = nan_like(M, K), nan_like(K, F), nan_like(K, F)
+        pg.gated_bf16_backward(M, F, K, X, Wg, Wu, "relu", dH, dX, dWg, dWu, preact=kept)
+        ref.check(dX, *want["dX"], "dX")
+        ref.check(dWg, *want["dW0"], "dWg")
+        ref.check(dWu, *want["dW1"], "dWu")
+
+
 def test_linear_backward_of_nothing():
     dW, db, dX = nan_like(24, 40), nan_like(40), nan_like(5, 24)
     pg.linear_bf16_backward(0, 40, 24, None, rnd(1, 24, 40), None, "silu", None, None, dW, db)
@@ -304,6 +348,32 @@ def test_xent_column_blocks_of_nothing_but_minus_infinity():
     want = torch.full((T,), -320.0 + math.log(128), device="cuda")
     assert torch.allclose(lse, want, rtol=1e-6)
     assert torch.allclose(loss, torch.full_like(want, math.log(128)), rtol=1e-4)
+
+
+@pytest.mark.parametrize("T", [40, 300])
+@pytest.mark.parametrize("weights", ["mean", "random", "signs", "wide"])
+def test_xent_scale_of_the_loss(T, weights):
+    # the products' operand is rounded after division by the largest weight of a
+    # row that counts, so that a mean's common factor rounds nothing
+    V, D = 1001, 72
+    X, W, y, dl = xent_inputs(T, V, D, 1040)
+    if weights == "mean":
+        dl = torch.full((T,), 1.0 / 417, device="cuda")
+    elif weights == "signs":
+        dl = torch.where(dl > 0.5, dl, -dl)
+    elif weights == "wide":
+        dl = torch.pow(10.0, -30 * dl)
+        dl[y < 0] = float("inf")  # a row that does not count may hold anything
+    dX, dW = nan_like(T, D), nan_like(V, D)
+    pg.xent_bf16_grad(T, V, D, X, W, y, dl, None, None, dX, dW)
+    want = ref.xent(X, W, y, torch.where(y < 0, torch.zeros_like(dl), dl))
+    ref.check(dX, *want["dX"], "dX")
+    ref.check(dW, *want["dW"], "dW")
+    if weights == "mean":
+        # -1 / 417 rounds to bf16 1.0e-3 off: unscaled, so would everything
+        for got, key in ((dX, "dX"), (dW, "dW")):
+            d, r = got.double(), want[key][0]
+            assert abs((d * r).sum() / (r * r).sum() - 1) < 5e-4
 
 
 def test_xent_no_tokens():
