@@ -100,7 +100,7 @@ struct EpiGatedGrad {
         const bool mine = epi_cols_dual<Cfg>(w, e, col0, width);
         if (!mine) return acc.skip();
         RowsIn in{dh, ld};
-        in.load(c, w.n0 + col0);  // travels while the products finish
+        if (Cfg::ROUND == 0) in.load(c, w.n0 + col0);  // travels while the products finish
         // 32 columns from w.n0 + col0 + 32 k
         auto finish = [&](int k, const uint32_t *g, const uint32_t *u) {
             const int n = w.n0 + col0 + 32 * k;
@@ -131,6 +131,7 @@ struct EpiGatedGrad {
         if constexpr (Cfg::ROUND > 0) {
             float x[64], y[64];
             if (!acc_sum<64, 64>(acc, col0, x, width + col0, y)) return false;
+            in.load(c, w.n0 + col0);  // (the sums fill the registers until here)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 uint32_t g[32], u[32];

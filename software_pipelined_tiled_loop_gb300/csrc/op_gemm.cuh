@@ -731,13 +731,24 @@ __device__ __forceinline__ void acc_cols32(uint32_t taddr, bool have, uint32_t (
 // v += N accumulator columns from taddr.
 template <int N>
 __device__ __forceinline__ void acc_add(uint32_t taddr, float *v) {
+    if constexpr (N <= 64) {  // room in the register file for longer loads
 #pragma unroll
-    for (int c = 0; c < N; c += 16) {
-        uint32_t x[16];
-        tmem_ld_32x32b_x16(taddr + c, x);
-        tmem_ld_wait();
+        for (int c = 0; c < N; c += 32) {
+            uint32_t x[32];
+            tmem_ld_32x32b_x32(taddr + c, x);
+            tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[c + j] += __uint_as_float(x[j]);
+            for (int j = 0; j < 32; ++j) v[c + j] += __uint_as_float(x[j]);
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < N; c += 16) {
+            uint32_t x[16];
+            tmem_ld_32x32b_x16(taddr + c, x);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[c + j] += __uint_as_float(x[j]);
+        }
     }
 }
 
@@ -758,6 +769,16 @@ __device__ __forceinline__ bool acc_sum(Acc &acc, int col, float *v, int col2, f
         acc.release();
     }
     return true;
+}
+
+// The same for the columns of epi_cols, fewer in a half-width unit.
+template <class Cfg, class Acc>
+__device__ __forceinline__ bool acc_sum_unit(Acc &acc, int col0, int cols, float *v) {
+    if constexpr (Cfg::EPI_COLS > 64) {
+        if (cols < Cfg::EPI_COLS)
+            return acc_sum<Cfg::EPI_COLS / 2, 0>(acc, col0, v, 0, nullptr);
+    }
+    return acc_sum<Cfg::EPI_COLS, 0>(acc, col0, v, 0, nullptr);
 }
 
 // What a ReLU's derivative needs: it jumps at zero, and a pre-activation whose

@@ -23,7 +23,7 @@ struct EpiLinearGrad {
         const int nf = w.n0 + col0;
         const bool have = acc.have();
         RowsIn in{dy, dy_ld};
-        in.load(c, nf);  // travels while the products finish
+        if (Cfg::ROUND == 0) in.load(c, nf);  // travels while the products finish
         // 32 columns from nf + cc: v holds the accumulator's
         auto finish = [&](int cc, uint32_t *v) {
             const int n = nf + cc;
@@ -57,7 +57,8 @@ struct EpiLinearGrad {
         };
         if constexpr (Cfg::ROUND > 0) {
             float f[Cfg::EPI_COLS];
-            if (!acc_sum<Cfg::EPI_COLS, 0>(acc, col0, f, 0, nullptr)) return false;
+            if (!acc_sum_unit<Cfg>(acc, col0, cols, f)) return false;
+            in.load(c, nf);  // (the sums fill the registers until here)
 #pragma unroll
             for (int b = 0; b < Cfg::EPI_COLS / 32; ++b) {
                 if (32 * b >= cols) break;

@@ -99,10 +99,8 @@ struct EpiOut {
         };
         if constexpr (Cfg::ROUND > 0) {
             float f[Cfg::EPI_COLS];
-            if (have_r) res.load(c, nf);
-            // (a half-width unit's second warps read columns of the other unit's
-            // width, which hold whatever was there: finish() is not given them)
-            if (!acc_sum<Cfg::EPI_COLS, 0>(acc, col0, f, 0, nullptr)) return false;
+            if (!acc_sum_unit<Cfg>(acc, col0, cols, f)) return false;
+            if (have_r) res.load(c, nf);  // (the sums fill the registers until here)
 #pragma unroll
             for (int b = 0; b < Cfg::EPI_COLS / 32; ++b) {
                 if (32 * b >= cols) break;
