@@ -192,7 +192,7 @@ template <class Epi>
 static pgemm_status launch_dual_size(const OpDevice &dev, int M, int F, int K, const OpMat &X,
                                      const OpMat &Wg, const OpMat &Wu, OpMaps &maps, const Epi &e,
                                      bool sign, cudaStream_t s) {
-    const bool pair = op_use_pair(dev, M, F, 128, 64, 1);
+    const bool pair = op_use_pair(dev, M, F, K, 128, 64);
     if (sign && op_sign_rounds(e.act, K))
         return pair ? launch_dual<SignDualPair>(dev, M, F, K, X, Wg, Wu, maps, e, s)
                     : launch_dual<SignDualOne>(dev, M, F, K, X, Wg, Wu, maps, e, s);

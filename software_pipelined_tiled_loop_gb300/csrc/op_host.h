@@ -174,10 +174,10 @@ pgemm_status op_join_parts(const OpDevice &dev, const float *area, int parts, in
                            int N, uint16_t *const out[2], const OpEpilogue &epi,
                            cudaStream_t s);
 
-// The larger tile on a CTA pair, or 128 x 128 on one CTA: whichever needs
-// less time for this many rows and columns (op_products.cu explains).
-bool op_use_pair(const OpDevice &dev, long long M, long long N, long long pair_n, long long one_n,
-                 int segments);
+// The larger tile on a CTA pair (256 x pair_n outputs), or one CTA's (128 x
+// one_n): whichever needs less time for an M x N x K product (op_products.cu).
+bool op_use_pair(const OpDevice &dev, long long M, long long N, long long K, long long pair_n,
+                 long long one_n);
 
 // dZ = dY * act'(Z) from kept fp32 pre-activations, and column sums of dZ
 // (act none and dz nullptr: of dY itself).  op_products.cu.

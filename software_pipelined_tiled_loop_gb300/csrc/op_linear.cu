@@ -223,7 +223,7 @@ static pgemm_status linear_backward(int M, int N, int K, const uint16_t *X, cons
             st = op_act_grad(dev, g, arena, false, s);
         } else {
             const EpiLinearGrad e{bias, dY, N, dz_buf, dz.ld, act};
-            const bool pair = op_use_pair(dev, M, N, 256, 128, 1);
+            const bool pair = op_use_pair(dev, M, N, K, 256, 128);
             if (op_sign_rounds(act, K))
                 st = pair ? launch_grad<OpCfg<256, 3, 2, 2, false, false, false, SignPair::value>>(
                                 dev, M, N, K, x, w, e, s)

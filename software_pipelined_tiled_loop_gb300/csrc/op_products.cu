@@ -160,29 +160,44 @@ struct EpiOut {
 };
 
 // --------------------------------------------------------------- choice ---
-// Time of a product in units of one 64-wide K step of a 128 x 256 share of a
-// CTA pair's tile: a wave of pair tiles costs 1 a step, a wave of 128 x 128
-// tiles on single CTAs kOneStep (they do half the work at a lower rate: each
-// operand panel feeds half as many products).  Parts along K shorten the
-// waves and add the join's traffic: parts * M * N fp32 values written and read.
-constexpr double kStepUs = 0.36, kOneStep = 0.65, kHalfWave = 0.6;
+// Time of a product, from graphs of calls on warm operands (us, 19 shapes from
+// 135 x 256 x 208 to 2560 x 1384 x 3432, within 10 %): a launch and its first
+// tile's pipeline and epilogue, then for every wave its 64-wide K steps, and an
+// epilogue between waves that the next tile does not hide.  A CTA pair's tiles
+// (256 x 256) go faster a product but cost more to start than 128 x 128 tiles on
+// single CTAs; its leftover tiles run as half-width units where those fit.
+// Parts along K shorten the waves and add the join: its launch, and parts * M * N
+// fp32 values written and read.
+struct WaveCost {
+    double fixed, step, half_step;
+};
+constexpr WaveCost kPairCost{5.0, 0.32, 0.25}, kOneCost{3.4, 0.29, 0.29};
+constexpr double kWaveGapUs = 0.8, kJoinUs = 4.0, kJoinUsPerMB = 2.0 / 5.0;
+
+static double wave_us(bool pair, long long tiles, int sm_count, long long steps) {
+    const WaveCost &c = pair ? kPairCost : kOneCost;
+    const long long slots = pair ? sm_count / 2 : sm_count;
+    const long long whole = tiles / slots, left = tiles % slots;
+    double us = c.fixed + static_cast<double>(whole) * static_cast<double>(steps) * c.step;
+    if (left > 0)
+        us += static_cast<double>(steps) * (pair && 2 * left <= slots ? c.half_step : c.step);
+    return us + kWaveGapUs * static_cast<double>(whole + (left > 0) - 1);
+}
+
 static OpPlan plan_product(int sm_count, long long M, long long N, long long K, int segments,
                            bool split) {
     const long long steps = (K + 63) / 64;
     OpPlan best{false, 1};
     double best_us = 1e30;
     for (int pair = 0; pair < 2; ++pair) {
-        const long long bm = pair ? 256 : 128;
-        const long long tiles = ((M + bm - 1) / bm) * ((N + bm - 1) / bm) * segments;
-        const long long slots = pair ? sm_count / 2 : sm_count;
+        const long long b = pair ? 256 : 128;
+        const long long tiles = ((M + b - 1) / b) * ((N + b - 1) / b) * segments;
         for (const int parts : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
             if (parts > 1 && (!split || steps / parts < 8)) break;
-            // a pair's leftover tiles run as half-width units where those fit
-            const long long units = tiles * parts, left = units % slots;
-            double waves = static_cast<double>(units / slots);
-            if (left > 0) waves += pair && 2 * left <= slots ? kHalfWave : 1.0;
-            double us = waves * ((pair ? 1.0 : kOneStep) * kStepUs * ((steps + parts - 1) / parts) + 1.0);
-            if (parts > 1) us += 4.0 + parts * 8e-6 * M * N * segments / 5.0;
+            double us = wave_us(pair != 0, tiles * parts, sm_count, (steps + parts - 1) / parts);
+            if (parts > 1)
+                us += kJoinUs + kJoinUsPerMB * 4e-6 * parts * static_cast<double>(M) *
+                                    static_cast<double>(N) * segments;
             if (us < best_us * 0.999) {
                 best_us = us;
                 best = OpPlan{pair != 0, parts};
@@ -192,15 +207,12 @@ static OpPlan plan_product(int sm_count, long long M, long long N, long long K, 
     return best;
 }
 
-bool op_use_pair(const OpDevice &dev, long long M, long long N, long long pair_n, long long one_n,
-                 int segments) {
-    const long long tp = ((M + 255) / 256) * ((N + pair_n - 1) / pair_n) * segments;
-    const long long t1 = ((M + 127) / 128) * ((N + one_n - 1) / one_n) * segments;
-    const long long sp = dev.sm_count / 2, s1 = dev.sm_count;
-    const long long left = tp % sp;
-    const double pair_waves =
-        static_cast<double>(tp / sp) + (left == 0 ? 0.0 : 2 * left <= sp ? kHalfWave : 1.0);
-    return pair_waves <= kOneStep * static_cast<double>((t1 + s1 - 1) / s1);
+bool op_use_pair(const OpDevice &dev, long long M, long long N, long long K, long long pair_n,
+                 long long one_n) {
+    const long long steps = (K + 63) / 64;
+    const long long tp = ((M + 255) / 256) * ((N + pair_n - 1) / pair_n);
+    const long long t1 = ((M + 127) / 128) * ((N + one_n - 1) / one_n);
+    return wave_us(true, tp, dev.sm_count, steps) <= wave_us(false, t1, dev.sm_count, steps);
 }
 
 int op_product_parts(const OpDevice &dev, int M, int N, int K, int segments) {

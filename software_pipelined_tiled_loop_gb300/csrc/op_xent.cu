@@ -659,7 +659,7 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
                    : PGEMM_ERR_CUDA;
 
     const bool few = T <= kFewMax;
-    const bool pair = op_use_pair(dev, T, V, 256, 128, 1);
+    const bool pair = op_use_pair(dev, T, V, D, 256, 128);
     const int block_cols = pair ? StatsPair::EPI_COLS : StatsOne::EPI_COLS;
     // (m, s) of a row: one for each column block, or for each CTA
     int blocks = (V + block_cols - 1) / block_cols;
@@ -791,7 +791,7 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
             st = op_encode_out(&maps.c[0], OpElem::BF16, P, cols, T, piece);
             if (st != PGEMM_OK) return st;
             const EpiXentGrad e{target, lse_buf, dloss, scale, v0, V};
-            st = op_use_pair(dev, T, cols, 256, 128, 1)
+            st = op_use_pair(dev, T, cols, D, 256, 128)
                      ? launch_logits<XentPair>(dev, T, cols, D, x, w, v0, maps, e, s)
                      : launch_logits<XentOne>(dev, T, cols, D, x, w, v0, maps, e, s);
         }
