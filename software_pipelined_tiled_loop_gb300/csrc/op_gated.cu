@@ -266,8 +266,9 @@ static pgemm_status gated_backward(int M, int F, int K, const uint16_t *X, const
         dg_at = arena.add(dg.ld * M * 2);
         du_at = arena.add(du.ld * M * 2);
     }
+    const bool tokens = M <= kTokensMax, x_tokens = op_tokens_fit(dev, M, K, 2ll * F);
     OpProduct px, pw;
-    if (want_x) {
+    if (want_x && !x_tokens) {
         px.form = OpForm::NT;
         px.M = M;
         px.N = K;
@@ -305,6 +306,8 @@ static pgemm_status gated_backward(int M, int F, int K, const uint16_t *X, const
             g.du = du_buf;
             g.dz_ld = dg.ld;
             st = op_act_grad(dev, g, arena, false, s);
+        } else if (tokens) {
+            st = op_tokens_gated_grad(dev, M, F, K, x, wg, wu, act, dH, dg_buf, du_buf, dg.ld, s);
         } else {
             OpMaps maps{};
             EpiGatedGrad e{dH, F, dg_buf, du_buf, dg.ld, act};
@@ -321,7 +324,9 @@ static pgemm_status gated_backward(int M, int F, int K, const uint16_t *X, const
         px.A[1] = du;
         px.B[0] = wg;
         px.B[1] = wu;
-        if ((st = op_product(dev, px, arena, s)) != PGEMM_OK) return st;
+        st = x_tokens ? op_tokens_transposed(dev, M, K, F, px.A, px.B, 2, dX, s)
+                      : op_product(dev, px, arena, s);
+        if (st != PGEMM_OK) return st;
     }
     if (want_w) {
         pw.A[0] = x;

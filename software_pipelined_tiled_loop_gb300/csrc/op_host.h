@@ -158,11 +158,28 @@ pgemm_status op_product_join(const OpDevice &dev, const OpProduct &p, const OpAr
 
 // The same products of a few rows, bound by reading the weights (op_tokens.cu).
 constexpr int kTokensMax = 128;
+// Whether a gradient product of M rows (N outputs, K reduction columns) goes that
+// way.  A cluster shares a tile's K among eight CTAs at most, so few columns with a
+// long K leave most SMs idle, where the tiled product takes up to 32 parts (a whole
+// cross-entropy gradient, streaming against tiled dX: 4 tokens x 82768 x 592
+// 117 against 95 us, 16 x 15640 x 520 35 against 39).
+bool op_tokens_fit(const OpDevice &dev, int M, long long N, long long K);
 pgemm_status op_tokens_linear(const OpDevice &dev, int M, int N, int K, const OpMat &X,
                               const OpMat &W, const OpEpilogue &e, uint16_t *Y, cudaStream_t s);
 pgemm_status op_tokens_gated(const OpDevice &dev, int M, int F, int K, const OpMat &X,
                              const OpMat &Wg, const OpMat &Wu, int act, uint16_t *H,
                              float *preact, cudaStream_t s);
+// dZ = dY act'(X W + b); dG and dU of a gated block (rows of dz_ld elements).
+pgemm_status op_tokens_linear_grad(const OpDevice &dev, int M, int N, int K, const OpMat &X,
+                                   const OpMat &W, const uint16_t *bias, int act,
+                                   const uint16_t *dy, uint16_t *dz, long long dz_ld,
+                                   cudaStream_t s);
+pgemm_status op_tokens_gated_grad(const OpDevice &dev, int M, int F, int K, const OpMat &X,
+                                  const OpMat &Wg, const OpMat &Wu, int act, const uint16_t *dh,
+                                  uint16_t *dg, uint16_t *du, long long dz_ld, cudaStream_t s);
+// out (M x N) = the sum over segments of X[j] W[j]^T, X M x K, W N x K.
+pgemm_status op_tokens_transposed(const OpDevice &dev, int M, int N, int K, const OpMat *X,
+                                  const OpMat *W, int segments, uint16_t *out, cudaStream_t s);
 
 // Parts a product of these sizes would be split into (parts_area: M padded to
 // 32 rows, N to 64 columns, one such matrix a part and segment).

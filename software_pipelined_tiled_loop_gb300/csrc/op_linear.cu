@@ -179,8 +179,9 @@ static pgemm_status linear_backward(int M, int N, int K, const uint16_t *X, cons
     } else if (some) {
         rl.add(&dz, dY, M, N, arena);
     }
+    const bool tokens = M <= kTokensMax, x_tokens = op_tokens_fit(dev, M, K, N);
     OpProduct px, pw;
-    if (want_x) {
+    if (want_x && !x_tokens) {
         px.form = OpForm::NT;
         px.M = M;
         px.N = K;
@@ -221,6 +222,8 @@ static pgemm_status linear_backward(int M, int N, int K, const uint16_t *X, cons
             g.dz = dz_buf;
             g.dz_ld = dz.ld;
             st = op_act_grad(dev, g, arena, false, s);
+        } else if (tokens) {
+            st = op_tokens_linear_grad(dev, M, N, K, x, w, bias, act, dY, dz_buf, dz.ld, s);
         } else {
             const EpiLinearGrad e{bias, dY, N, dz_buf, dz.ld, act};
             const bool pair = op_use_pair(dev, M, N, K, 256, 128);
@@ -239,7 +242,9 @@ static pgemm_status linear_backward(int M, int N, int K, const uint16_t *X, cons
     if (want_x) {
         px.A[0] = dz;
         px.B[0] = w;
-        if ((st = op_product(dev, px, arena, s)) != PGEMM_OK) return st;
+        st = x_tokens ? op_tokens_transposed(dev, M, K, N, px.A, px.B, 1, dX, s)
+                      : op_product(dev, px, arena, s);
+        if (st != PGEMM_OK) return st;
         overlap = true;
     }
     if (want_w) {

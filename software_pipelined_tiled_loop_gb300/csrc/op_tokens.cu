@@ -1,12 +1,14 @@
-// Products of a few rows (up to 128 tokens of a decoding step): Y = act(X W + b)
-// + R and H = act(X Wg) * (X Wu), bound by streaming the weights once.
+// Products of a few rows (up to 128 tokens, of a decoding step or a small batch):
+// Y = act(X W + b) + R, H = act(X Wg) * (X Wu), what their backward passes
+// recompute, and dX = dZ W^T; all bound by streaming the weights once.
 //
 // The weights take the tensor core's M side: D[n][t] = sum_k W[k][n] X[t][k],
 // A = W^T read M-major straight from the K x N rows by TMA (64-column boxes of
 // 64 k-rows), B = X K-major with N = 16 .. 128 tokens.  An SM's ring then holds
 // weights, not padding of X: 128 x 128 tiles with a token a row would load as
 // many bytes for one token as for 128.  A thread owns one output column, so
-// bias, residual and stores run along n, coalesced for every token.
+// bias, residual and stores run along n, coalesced for every token.  dX = dZ W^T
+// reads the same rows as D[k][t] = sum_n W[k][n] dZ[t][n], A = W K-major.
 //
 // Long axis: a cluster of S CTAs shares a 128-column tile, CTA r taking K steps
 // [r T / S, (r + 1) T / S).  The fp32 partial sums meet in the CTAs' own shared
@@ -28,26 +30,38 @@
 namespace pg {
 
 struct TokensArgs {
-    int M, N, K;
-    int k_tiles;
-    // linear
-    const uint16_t *bias, *residual;
-    // gated: preact holds both products
-    float *preact;
-    uint16_t *out;
+    int M, N, K;            // outputs M x N; K: reduction columns of one segment
+    int k_tiles, k_seg;     // K steps over all segments, and of one
+    const uint16_t *bias, *residual;  // linear
+    float *preact;          // gated: both products
+    const uint16_t *dy;     // gradients: M x N
+    const float *scale;     // one device value times the sums, or nullptr
+    uint16_t *out, *out2;   // out2: dU of a gated gradient
+    long long ldo;          // row length of out and out2
     int act;
 };
 
 struct TokensMaps {
-    CUtensorMap x, w[2];
+    CUtensorMap x[2], w[2];
 };
 
-// TOK: tokens of the MMA's N side; DUAL: two weight matrices (gated), whose
+enum class Tok {
+    LINEAR,       // act(X W + b) + R
+    GATED,        // act(X Wg) * (X Wu)
+    LINEAR_GRAD,  // dY act'(X W + b)
+    GATED_GRAD,   // dH U act'(G), dH act(G)
+    TRANSPOSED,   // sum over segments of X W^T
+};
+
+// TOK: tokens of the MMA's N side.  DUAL: two weight matrices (gated), whose
 // accumulators lie side by side in tensor memory.
-template <int TOK_, bool DUAL_>
+template <int TOK_, Tok MODE_>
 struct TokCfg {
     static constexpr int TOK = TOK_, BN = 128, BK = 64;
-    static constexpr bool DUAL = DUAL_;
+    static constexpr Tok MODE = MODE_;
+    static constexpr bool DUAL = MODE == Tok::GATED || MODE == Tok::GATED_GRAD;
+    static constexpr bool GRAD = MODE == Tok::LINEAR_GRAD || MODE == Tok::GATED_GRAD;
+    static constexpr bool W_K = MODE == Tok::TRANSPOSED;  // W's rows run along the reduction
     static constexpr int NW = DUAL ? 2 : 1;
     static constexpr int W_SUB = BN * BK * 2;  // one matrix, 64 k-rows
     static constexpr int X_SUB = TOK * BK * 2;
@@ -102,6 +116,19 @@ __device__ __forceinline__ void get4(const uint16_t *p, int cols, bool vec, floa
     }
 }
 
+__device__ __forceinline__ void put4(uint16_t *p, int cols, bool vec, const float (&f)[4]) {
+    const uint32_t lo = pack_bf16(f[0], f[1]), hi = pack_bf16(f[2], f[3]);
+    // (vec: rows padded to four columns at least)
+    if (vec) {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(lo, hi);
+    } else {
+        const uint32_t w[4] = {lo & 0xffffu, lo >> 16, hi & 0xffffu, hi >> 16};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < cols) p[j] = static_cast<uint16_t>(w[j]);
+    }
+}
+
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     tokens_kernel(const __grid_constant__ TokensMaps maps, const TokensArgs a,
@@ -123,7 +150,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
 
     if (warp == 0 && lane == 0) {
         if (a.k_tiles > 0) {
-            prefetch_tmap(&maps.x);
+            prefetch_tmap(&maps.x[0]);
             prefetch_tmap(&maps.w[0]);
         }
         for (int s = 0; s < STAGES; ++s) {
@@ -135,11 +162,18 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     }
     if (warp == 2 && lane == 0) {
         for (int kt = kb; kt < min(ke, kb + Cfg::PREFETCH); ++kt)
+        {
+            const int sg = kt >= a.k_seg ? 1 : 0, k0 = (kt - sg * a.k_seg) * BK;
+            if constexpr (Cfg::W_K) {
+                tma_prefetch_2d(&maps.w[sg], k0, n0);
+            } else {
 #pragma unroll
-            for (int d = 0; d < Cfg::NW; ++d)
+                for (int d = 0; d < Cfg::NW; ++d)
 #pragma unroll
-                for (int j = 0; j < BN / 64; ++j)
-                    if (n0 + 64 * j < a.N) tma_prefetch_2d(&maps.w[d], n0 + 64 * j, kt * BK);
+                    for (int j = 0; j < BN / 64; ++j)
+                        if (n0 + 64 * j < a.N) tma_prefetch_2d(&maps.w[d], n0 + 64 * j, k0);
+            }
+        }
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, Cfg::TMEM_COLS);
@@ -160,18 +194,23 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                 if (!mbar_wait(&empty[s], ph ^ 1u, ctx, kSiteProducerEmpty)) break;
                 uint8_t *st = smem + s * Cfg::STAGE_BYTES;
                 mbar_arrive_expect_tx(&full[s], Cfg::STAGE_BYTES);
+                const int sg = kt >= a.k_seg ? 1 : 0, k0 = (kt - sg * a.k_seg) * BK;
+                if constexpr (Cfg::W_K) {
+                    tma_load_2d(st, &maps.w[sg], &full[s], k0, n0);
+                } else {
 #pragma unroll
-                for (int d = 0; d < Cfg::NW; ++d)
+                    for (int d = 0; d < Cfg::NW; ++d)
 #pragma unroll
-                    for (int j = 0; j < BN / 64; ++j)
-                        tma_load_2d(st + d * Cfg::W_SUB + j * (BK * 128), &maps.w[d], &full[s],
-                                    n0 + 64 * j, kt * BK);
-                tma_load_2d(st + Cfg::NW * Cfg::W_SUB, &maps.x, &full[s], kt * BK, 0);
+                        for (int j = 0; j < BN / 64; ++j)
+                            tma_load_2d(st + d * Cfg::W_SUB + j * (BK * 128), &maps.w[d], &full[s],
+                                        n0 + 64 * j, k0);
+                }
+                tma_load_2d(st + Cfg::NW * Cfg::W_SUB, &maps.x[sg], &full[s], k0, 0);
             }
         }
     } else if (warp == 1) {
         if (lane == 0) {
-            constexpr uint32_t idesc = idesc_f16(BN, TOK, 1, /*A M-major*/ 1, /*B K-major*/ 0);
+            constexpr uint32_t idesc = idesc_f16(BN, TOK, 1, /*A*/ Cfg::W_K ? 0 : 1, /*B K-major*/ 0);
             int it = 0;
             for (int kt = kb; kt < ke; ++kt, ++it) {
                 const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
@@ -185,7 +224,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
 #pragma unroll
                     for (int d = 0; d < Cfg::NW; ++d) {
                         const uint64_t ad =
-                            smem_desc_sw128(st + d * Cfg::W_SUB + k * 2048, BK * 128, 1024);
+                            Cfg::W_K ? smem_desc_sw128(st + k * 32, 16, 1024)
+                                     : smem_desc_sw128(st + d * Cfg::W_SUB + k * 2048, BK * 128,
+                                                       1024);
                         umma_f16_ss(tmem + d * TOK, ad, bd, idesc,
                                     (kt == kb && k == 0) ? 0u : 1u);
                     }
@@ -230,15 +271,17 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
         // tokens rank, rank + S, ... are this CTA's; its warps take them in turn
         const int n = n0 + static_cast<int>(lane) * 4;
         const int cols = a.N - n;
-        const bool vec = a.N % 4 == 0;  // rows on 8-byte boundaries
+        const bool vec = a.N % 4 == 0;  // the caller's rows on 8-byte boundaries
+        const bool vec_out = a.ldo % 4 == 0;
         if (cols > 0) {
             float b[4] = {0.f, 0.f, 0.f, 0.f};
-            if (!Cfg::DUAL && a.bias) get4(a.bias + n, cols, vec, b);
+            if (a.bias) get4(a.bias + n, cols, vec, b);
             for (int t = static_cast<int>(rank + S * (warp - 2)); t < a.M;
                  t += static_cast<int>(S) * Cfg::EPI) {
                 const long long at = static_cast<long long>(t) * a.N + n;
                 float r[4] = {0.f, 0.f, 0.f, 0.f};
-                if (!Cfg::DUAL && a.residual) get4(a.residual + at, cols, vec, r);
+                if (a.residual) get4(a.residual + at, cols, vec, r);
+                if (Cfg::GRAD) get4(a.dy + at, cols, vec, r);
                 float4 part[Cfg::NW][8];
 #pragma unroll
                 for (int d = 0; d < Cfg::NW; ++d) {
@@ -266,7 +309,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                             z[d][3] += part[d][i].w;
                         }
                 }
-                float y[4];
+                if (a.scale) {
+                    const float f = *a.scale;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) z[0][j] *= f;
+                }
                 if constexpr (!Cfg::DUAL) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) z[0][j] += b[j];
@@ -279,22 +326,25 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                             if (j < cols)
                                 a.preact[d * static_cast<long long>(a.M) * a.N + at + j] = z[d][j];
                 }
+                float y[4], y2[4] = {0.f, 0.f, 0.f, 0.f};
                 with_act(a.act, [&](auto A) {
+                    constexpr int ACT = decltype(A)::value;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        y[j] = act_value<decltype(A)::value>(z[0][j]);
-                        y[j] = Cfg::DUAL ? y[j] * z[Cfg::NW - 1][j] : y[j] + r[j];
+                        if constexpr (Cfg::GRAD) {
+                            float value;
+                            const float d = act_value_grad<ACT>(z[0][j], value);
+                            y[j] = r[j] * d * (Cfg::DUAL ? z[Cfg::NW - 1][j] : 1.0f);
+                            y2[j] = r[j] * value;
+                        } else {
+                            y[j] = act_value<ACT>(z[0][j]);
+                            y[j] = Cfg::DUAL ? y[j] * z[Cfg::NW - 1][j] : y[j] + r[j];
+                        }
                     }
                 });
-                const uint32_t lo = pack_bf16(y[0], y[1]), hi = pack_bf16(y[2], y[3]);
-                if (vec) {
-                    *reinterpret_cast<uint2 *>(a.out + at) = make_uint2(lo, hi);
-                } else {
-                    const uint32_t w[4] = {lo & 0xffffu, lo >> 16, hi & 0xffffu, hi >> 16};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (j < cols) a.out[at + j] = static_cast<uint16_t>(w[j]);
-                }
+                const long long to = static_cast<long long>(t) * a.ldo + n;
+                put4(a.out + to, cols, vec_out, y);
+                if constexpr (Cfg::MODE == Tok::GATED_GRAD) put4(a.out2 + to, cols, vec_out, y2);
             }
         }
     }
@@ -330,9 +380,17 @@ static int cluster_share(int slots, int n_tiles, int k_tiles) {
     return best;
 }
 
+bool op_tokens_fit(const OpDevice &dev, int M, long long N, long long K) {
+    if (M > kTokensMax) return false;
+    const int n_tiles = static_cast<int>((N + 127) / 128);
+    const int k_tiles = static_cast<int>((K + 63) / 64);
+    const int S = cluster_share(2 * dev.sm_count, n_tiles, k_tiles);
+    return n_tiles * S >= dev.sm_count || k_tiles / S <= 32;
+}
+
 template <class Cfg>
-static pgemm_status launch_tokens(const OpDevice &dev, TokensArgs a, const OpMat &X,
-                                  const OpMat *W, cudaStream_t s) {
+static pgemm_status launch_tokens(const OpDevice &dev, TokensArgs a, const OpMat *X,
+                                  const OpMat *W, int segments, cudaStream_t s) {
     static const KernelInfo info = [] {
         KernelInfo k;
         k.threads = Cfg::THREADS;
@@ -344,13 +402,16 @@ static pgemm_status launch_tokens(const OpDevice &dev, TokensArgs a, const OpMat
     pgemm_status st = op_kernel_setup(dev, info, &slots);
     TokensMaps maps{};
     if (a.K > 0) {
-        if (st == PGEMM_OK)
-            st = op_encode(&maps.x, X.p, a.K, a.M, X.ld, Cfg::TOK);
-        for (int d = 0; d < Cfg::NW && st == PGEMM_OK; ++d)
-            st = op_encode(&maps.w[d], W[d].p, a.N, a.K, W[d].ld, 64);
+        for (int d = 0; d < segments && st == PGEMM_OK; ++d)
+            st = op_encode(&maps.x[d], X[d].p, a.K, a.M, X[d].ld, Cfg::TOK);
+        const int matrices = Cfg::DUAL ? 2 : segments;
+        for (int d = 0; d < matrices && st == PGEMM_OK; ++d)
+            st = Cfg::W_K ? op_encode(&maps.w[d], W[d].p, a.K, a.N, W[d].ld, 128)
+                          : op_encode(&maps.w[d], W[d].p, a.N, a.K, W[d].ld, 64);
     }
     if (st != PGEMM_OK) return st;
-    a.k_tiles = (a.K + Cfg::BK - 1) / Cfg::BK;
+    a.k_seg = (a.K + Cfg::BK - 1) / Cfg::BK;
+    a.k_tiles = a.k_seg * segments;
     const int n_tiles = (a.N + Cfg::BN - 1) / Cfg::BN;
     const int S = cluster_share(dev.sm_count * Cfg::CTAS, n_tiles, a.k_tiles);
     cudaLaunchAttribute attr[2];
@@ -372,27 +433,88 @@ static pgemm_status launch_tokens(const OpDevice &dev, TokensArgs a, const OpMat
                : PGEMM_ERR_CUDA;
 }
 
-template <bool DUAL>
-static pgemm_status launch_tokens_size(const OpDevice &dev, const TokensArgs &a, const OpMat &X,
-                                       const OpMat *W, cudaStream_t s) {
-    if (a.M <= 16) return launch_tokens<TokCfg<16, DUAL>>(dev, a, X, W, s);
-    if (a.M <= 32) return launch_tokens<TokCfg<32, DUAL>>(dev, a, X, W, s);
-    if (a.M <= 64) return launch_tokens<TokCfg<64, DUAL>>(dev, a, X, W, s);
-    return launch_tokens<TokCfg<128, DUAL>>(dev, a, X, W, s);
+template <Tok MODE>
+static pgemm_status launch_tokens_size(const OpDevice &dev, const TokensArgs &a, const OpMat *X,
+                                       const OpMat *W, int segments, cudaStream_t s) {
+    if (a.M <= 16) return launch_tokens<TokCfg<16, MODE>>(dev, a, X, W, segments, s);
+    if (a.M <= 32) return launch_tokens<TokCfg<32, MODE>>(dev, a, X, W, segments, s);
+    if (a.M <= 64) return launch_tokens<TokCfg<64, MODE>>(dev, a, X, W, segments, s);
+    return launch_tokens<TokCfg<128, MODE>>(dev, a, X, W, segments, s);
 }
 
 pgemm_status op_tokens_linear(const OpDevice &dev, int M, int N, int K, const OpMat &X,
                               const OpMat &W, const OpEpilogue &e, uint16_t *Y, cudaStream_t s) {
-    const TokensArgs a{M, N, K, 0, e.bias, e.residual, e.preact, Y, e.act};
-    return launch_tokens_size<false>(dev, a, X, &W, s);
+    TokensArgs a{};
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.bias = e.bias;
+    a.residual = e.residual;
+    a.preact = e.preact;
+    a.scale = e.scale;
+    a.act = e.act;
+    a.out = Y;
+    a.ldo = N;
+    return launch_tokens_size<Tok::LINEAR>(dev, a, &X, &W, 1, s);
 }
 
 pgemm_status op_tokens_gated(const OpDevice &dev, int M, int F, int K, const OpMat &X,
                              const OpMat &Wg, const OpMat &Wu, int act, uint16_t *H,
                              float *preact, cudaStream_t s) {
-    const TokensArgs a{M, F, K, 0, nullptr, nullptr, preact, H, act};
+    TokensArgs a{};
+    a.M = M;
+    a.N = F;
+    a.K = K;
+    a.preact = preact;
+    a.act = act;
+    a.out = H;
+    a.ldo = F;
     const OpMat w[2] = {Wg, Wu};
-    return launch_tokens_size<true>(dev, a, X, w, s);
+    return launch_tokens_size<Tok::GATED>(dev, a, &X, w, 1, s);
+}
+
+pgemm_status op_tokens_linear_grad(const OpDevice &dev, int M, int N, int K, const OpMat &X,
+                                   const OpMat &W, const uint16_t *bias, int act,
+                                   const uint16_t *dy, uint16_t *dz, long long dz_ld,
+                                   cudaStream_t s) {
+    TokensArgs a{};
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.bias = bias;
+    a.dy = dy;
+    a.act = act;
+    a.out = dz;
+    a.ldo = dz_ld;
+    return launch_tokens_size<Tok::LINEAR_GRAD>(dev, a, &X, &W, 1, s);
+}
+
+pgemm_status op_tokens_gated_grad(const OpDevice &dev, int M, int F, int K, const OpMat &X,
+                                  const OpMat &Wg, const OpMat &Wu, int act, const uint16_t *dh,
+                                  uint16_t *dg, uint16_t *du, long long dz_ld, cudaStream_t s) {
+    TokensArgs a{};
+    a.M = M;
+    a.N = F;
+    a.K = K;
+    a.dy = dh;
+    a.act = act;
+    a.out = dg;
+    a.out2 = du;
+    a.ldo = dz_ld;
+    const OpMat w[2] = {Wg, Wu};
+    return launch_tokens_size<Tok::GATED_GRAD>(dev, a, &X, w, 1, s);
+}
+
+pgemm_status op_tokens_transposed(const OpDevice &dev, int M, int N, int K, const OpMat *X,
+                                  const OpMat *W, int segments, uint16_t *out, cudaStream_t s) {
+    TokensArgs a{};
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.act = PGEMM_ACT_NONE;
+    a.out = out;
+    a.ldo = N;
+    return launch_tokens_size<Tok::TRANSPOSED>(dev, a, X, W, segments, s);
 }
 
 }  // namespace pg

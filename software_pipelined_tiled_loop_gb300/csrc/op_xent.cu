@@ -711,6 +711,7 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
     }
     // the products of a piece, planned for the first (the widest): the others'
     // parts need no more room
+    const bool x_tokens = !x_pieces && op_tokens_fit(dev, T, D, V);
     OpProduct px, pw;
     const auto shape = [&](int cols) {
         px.form = OpForm::NN;
@@ -725,7 +726,7 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
     };
     if (pieces) {
         shape(static_cast<int>(V < piece ? V : piece));
-        if (want_x && !x_pieces) op_product_plan(dev, px, arena);
+        if (want_x && !x_pieces && !x_tokens) op_product_plan(dev, px, arena);
         if (want_w) op_product_plan(dev, pw, arena);
     }
     if ((st = arena.alloc()) != PGEMM_OK) return st;
@@ -806,7 +807,9 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
                 op_product_plan(dev, px, arena);  // this piece's; reserves nothing
                 x_done += px.plan.parts;
             }
-            if ((st = op_product(dev, px, arena, s)) != PGEMM_OK) return st;
+            st = x_tokens ? op_tokens_linear(dev, T, D, cols, px.A[0], px.B[0], px.epi, dX, s)
+                          : op_product(dev, px, arena, s);
+            if (st != PGEMM_OK) return st;
         }
         if (want_w) {
             pw.A[0] = OpMat{P, piece};
