@@ -1,0 +1,83 @@
+"""Operators whose outputs or scratch pass 2^31 elements: rows at the top, middle
+and bottom (and gradients that sum over all rows) against 64 bits."""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import operator_reference as ref  # noqa: E402
+import software_pipelined_tiled_loop_gb300 as pg  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from software_pipelined_tiled_loop_gb300 import build
+    build.build()
+    pg.lib()
+    yield
+    assert pg.pgemm_get_device_status() == 0
+    torch.cuda.empty_cache()
+    pg.pgemm_trim_scratch()
+
+
+def rnd(seed, *shape, std=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    out = torch.empty(shape, device="cuda", dtype=torch.bfloat16)
+    for part in out.view(-1).split(1 << 28):  # few fp32 temporaries
+        part.copy_(torch.randn(part.shape, generator=g, device="cuda") * std)
+    return out
+
+
+def some_rows(M):
+    return [*range(0, 40), *range(M // 2, M // 2 + 40), *range(M - 40, M)]
+
+
+@pytest.mark.parametrize("N", [33024, 33001])  # TMA stores; plain stores
+def test_linear_output_past_31_bits(N):
+    M, K = 66000, 64
+    X, W, b, R = rnd(1, M, K), rnd(2, K, N, std=0.125), rnd(3, N), rnd(4, M, N)
+    rows = some_rows(M)
+    y, bound, _, _ = ref.linear(X[rows], W, b, "silu", R[rows])
+    pg.linear_bf16(M, N, K, X, W, b, "silu", R, R)
+    ref.check(R[rows], y, bound, "Y")
+
+
+def test_gated_pre_activations_past_31_bits():
+    M, F, K = 40000, 33024, 64  # 2 M F > 2^31
+    X, Wg, Wu = rnd(5, M, K), rnd(6, K, F, std=0.125), rnd(7, K, F, std=0.125)
+    H = torch.empty(M, F, device="cuda", dtype=torch.bfloat16)
+    Z = torch.empty(2, M, F, device="cuda")
+    pg.gated_bf16(M, F, K, X, Wg, Wu, "silu", H, preact=Z)
+    rows = some_rows(M)
+    h, bound, g, u, eg, eu, _, _ = ref.gated(X[rows], Wg, Wu, "silu")
+    ref.check(H[rows], h, bound, "H")
+    ref.check(Z[0, rows], g, eg, "X Wg")
+    ref.check(Z[1, rows], u, eu, "X Wu")
+    # the elementwise gradient reads all of Z: dX of those rows
+    dH = H  # any values
+    dX = torch.empty_like(X)
+    pg.gated_bf16_backward(M, F, K, X, Wg, Wu, "silu", dH, dX, None, None, preact=Z)
+    want = ref.gated_backward(X[rows], Wg, Wu, "silu", dH[rows])
+    ref.check(dX[rows], *want["dX"], "dX")
+
+
+@pytest.mark.parametrize("D", [64, 648])  # P from logits computed again; from kept exponentials
+def test_xent_probabilities_past_31_bits(D):
+    T, V = 9000, 240000  # P has 2.16e9 entries, kept in one piece
+    X, W = rnd(8, T, D), rnd(9, V, D, std=2 * D ** -0.5)
+    g = torch.Generator(device="cuda").manual_seed(10)
+    y = torch.randint(0, V, (T,), generator=g, device="cuda")
+    loss, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    dX, dW = torch.empty_like(X), torch.empty_like(W)
+    pg.xent_bf16_grad(T, V, D, X, W, y, None, loss, lse, dX, dW, workspace_bytes=6 << 30)
+    rows = some_rows(T)
+    want = ref.xent(X[rows], W, y[rows], torch.ones(len(rows), device="cuda"))
+    for name, got in (("lse", lse), ("loss", loss), ("dX", dX)):
+        ref.check(got[rows], *want[name], name)
+    # the same gradient in pieces of the vocabulary
+    dX2, dW2 = torch.empty_like(X), torch.empty_like(W)
+    pg.xent_bf16_grad(T, V, D, X, W, y, None, None, None, dX2, dW2)
+    for a, b in ((dX, dX2), (dW, dW2)):
+        assert ((a.float() - b.float()).norm() / b.float().norm()).item() < 4e-3
