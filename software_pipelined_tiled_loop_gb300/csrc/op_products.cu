@@ -172,7 +172,7 @@ struct WaveCost {
     double fixed, step, half_step;
 };
 constexpr WaveCost kPairCost{5.0, 0.32, 0.25}, kOneCost{3.4, 0.29, 0.29};
-constexpr double kWaveGapUs = 0.8, kJoinUs = 4.0, kJoinUsPerMB = 2.0 / 5.0;
+constexpr double kWaveGapUs = 0.8, kJoinUs = 4.0, kJoinUsPerMB = 0.25;
 
 static double wave_us(bool pair, long long tiles, int sm_count, long long steps) {
     const WaveCost &c = pair ? kPairCost : kOneCost;
@@ -346,9 +346,11 @@ pgemm_status op_product_join(const OpDevice &dev, const OpProduct &p, const OpAr
 }
 
 // ------------------------------------------------------------------- join ---
-// Memory-bound: reads parts * M * N fp32 values once, writes M * N bf16.  A
+// Memory-bound: reads parts * M * N fp32 values once, writes M * N bf16 (two
+// parts of 4096 x 4096: 34 us, 4.9 TB/s; 54 us with one place a thread).  A
 // thread owns four columns of a row, so loads are 16 bytes and the parts are
-// added in order (the result does not depend on timing).
+// added in order (the result does not depend on timing).  Eight loads travel at
+// a time: of eight parts, or with few parts two each of four places.
 struct JoinParams {
     const float *area;
     long long ld, rows;
@@ -357,59 +359,93 @@ struct JoinParams {
     OpEpilogue e;
 };
 
+template <int PLACES>
 __global__ void __launch_bounds__(256) join_parts_kernel(const JoinParams p) {
     grid_dependency_wait();
     grid_launch_dependents();
-    const int quads = (p.N + 3) / 4;
+    constexpr int AHEAD = 8 / PLACES;
+    const unsigned quads = (p.N + 3) / 4;
     const long long total = static_cast<long long>(p.M) * quads * p.segments;
-    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-        const long long sm = i / quads;  // segment * M + row
-        const int n = static_cast<int>(i - sm * quads) * 4;
-        const int seg = sm >= p.M ? 1 : 0;
-        const long long m = sm - static_cast<long long>(seg) * p.M;
-        const float *src = p.area + (seg * p.rows + m) * p.ld + n;
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-        const long long step = p.segments * p.rows * p.ld;
-        constexpr int AHEAD = 8;  // loads in flight
+    const long long step = p.segments * p.rows * p.ld;
+    for (long long i0 = blockIdx.x * (256ll * PLACES) + threadIdx.x; i0 < total;
+         i0 += gridDim.x * (256ll * PLACES)) {
+        const float *src[PLACES];
+        long long at[PLACES];
+        int n[PLACES], seg[PLACES];
+        float v[PLACES][4];
+#pragma unroll
+        for (int u = 0; u < PLACES; ++u) {
+            const long long i = i0 + 256 * u < total ? i0 + 256 * u : i0;
+            // segment * M + row (a 32-bit division where it fits)
+            const long long sm = total <= 0xffffffffll
+                                     ? static_cast<unsigned>(i) / quads
+                                     : i / static_cast<long long>(quads);
+            n[u] = static_cast<int>(i - sm * quads) * 4;
+            seg[u] = sm >= p.M ? 1 : 0;
+            const long long m = sm - (seg[u] ? p.M : 0);
+            src[u] = p.area + (seg[u] * p.rows + m) * p.ld + n[u];
+            at[u] = m * p.N + n[u];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[u][j] = 0.0f;
+        }
         for (int k = 0; k < p.parts; k += AHEAD) {
-            float4 x[AHEAD];
+            float4 x[PLACES][AHEAD];
 #pragma unroll
-            for (int j = 0; j < AHEAD; ++j)
-                x[j] = k + j < p.parts
-                           ? __ldcs(reinterpret_cast<const float4 *>(src + (k + j) * step))
-                           : make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int u = 0; u < PLACES; ++u)
 #pragma unroll
-            for (int j = 0; j < AHEAD; ++j) {
-                v[0] += x[j].x;
-                v[1] += x[j].y;
-                v[2] += x[j].z;
-                v[3] += x[j].w;
+                for (int j = 0; j < AHEAD; ++j)
+                    x[u][j] = k + j < p.parts
+                                  ? __ldcs(reinterpret_cast<const float4 *>(src[u] + (k + j) * step))
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int u = 0; u < PLACES; ++u)
+#pragma unroll
+                for (int j = 0; j < AHEAD; ++j) {
+                    v[u][0] += x[u][j].x;
+                    v[u][1] += x[u][j].y;
+                    v[u][2] += x[u][j].z;
+                    v[u][3] += x[u][j].w;
+                }
+        }
+#pragma unroll
+        for (int u = 0; u < PLACES; ++u) {
+            if (u > 0 && i0 + 256 * u >= total) break;
+            const int cols = min(4, p.N - n[u]);
+            if (p.e.scale) {
+                const float f = *p.e.scale;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[u][j] *= f;
             }
-        }
-        const long long at = m * p.N + n;
-        const int cols = min(4, p.N - n);
-        if (p.e.scale) {
-            const float f = *p.e.scale;
-            for (int j = 0; j < 4; ++j) v[j] *= f;
-        }
-        for (int j = 0; j < cols; ++j) {
-            if (p.e.bias) v[j] += __uint_as_float(static_cast<uint32_t>(p.e.bias[n + j]) << 16);
-            if (p.e.preact) p.e.preact[at + j] = v[j];
-        }
-        with_act(p.e.act, [&](auto A) {
+            if (p.e.bias || p.e.preact) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = act_value<decltype(A)::value>(v[j]);
-        });
-        if (p.e.residual)
-            for (int j = 0; j < cols; ++j)
-                v[j] += __uint_as_float(static_cast<uint32_t>(p.e.residual[at + j]) << 16);
-        uint16_t *o = p.out[seg] + at;
-        const uint32_t lo = pack_bf16(v[0], v[1]), hi = pack_bf16(v[2], v[3]);
-        if (p.N % 4 == 0) {
-            *reinterpret_cast<uint2 *>(o) = make_uint2(lo, hi);
-        } else {
-            const uint32_t w[4] = {lo & 0xffffu, lo >> 16, hi & 0xffffu, hi >> 16};
-            for (int j = 0; j < cols; ++j) o[j] = static_cast<uint16_t>(w[j]);
+                for (int j = 0; j < 4; ++j) {
+                    if (j >= cols) break;
+                    if (p.e.bias)
+                        v[u][j] += __uint_as_float(static_cast<uint32_t>(p.e.bias[n[u] + j]) << 16);
+                    if (p.e.preact) p.e.preact[at[u] + j] = v[u][j];
+                }
+            }
+            with_act(p.e.act, [&](auto A) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[u][j] = act_value<decltype(A)::value>(v[u][j]);
+            });
+            if (p.e.residual) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j < cols)
+                        v[u][j] +=
+                            __uint_as_float(static_cast<uint32_t>(p.e.residual[at[u] + j]) << 16);
+            }
+            uint16_t *o = (seg[u] ? p.out[1] : p.out[0]) + at[u];
+            const uint32_t lo = pack_bf16(v[u][0], v[u][1]), hi = pack_bf16(v[u][2], v[u][3]);
+            if (p.N % 4 == 0) {
+                *reinterpret_cast<uint2 *>(o) = make_uint2(lo, hi);
+            } else {
+                const uint32_t w[4] = {lo & 0xffffu, lo >> 16, hi & 0xffffu, hi >> 16};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j < cols) o[j] = static_cast<uint16_t>(w[j]);
+            }
         }
     }
 }
@@ -428,17 +464,22 @@ pgemm_status op_join_parts(const OpDevice &dev, const float *area, int parts, in
     p.out[0] = out[0];
     p.out[1] = out[1];
     p.e = epi;
-    const long long blocks = (static_cast<long long>(M) * ((N + 3) / 4) * segments + 255) / 256;
+    // four places a thread where there are blocks enough for every SM all the same
+    const long long places = static_cast<long long>(M) * ((N + 3) / 4) * segments;
+    const bool four = parts <= 4 && places >= 1024ll * 2 * dev.sm_count;
+    const long long blocks = (places + (four ? 1023 : 255)) / (four ? 1024 : 256);
     const long long most = dev.sm_count * 8ll;
-    return launch_small(join_parts_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)),
-                        dim3(256), s, p);
+    return launch_small(four ? join_parts_kernel<4> : join_parts_kernel<1>,
+                        dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(256), s, p);
 }
 
 // --------------------------------------------------- activation gradient ---
 // dZ = dY * act'(Z) (linear), dG = dH * U * act'(G) and dU = dH * act(G)
 // (gated), elementwise in fp32 from the kept fp32 pre-activations, rounded to
 // bf16 because the tensor core multiplies them next; column sums of the
-// unrounded dZ for the bias.  Memory-bound: 8 (gated 14) bytes an element.
+// unrounded dZ for the bias.  Memory-bound: 8 (gated 14) bytes an element; gated
+// 8192 x 8192 takes 128 us (7.3 TB/s, some of Z still in L2), linear 4096 x 4096
+// 24 us (5.6 TB/s).
 // A block covers 256 columns x kGradRows rows; a thread eight columns of every
 // eighth row, so its part of a column sum stays in registers.  VEC: the eight
 // columns are adjacent (16-byte accesses; row lengths multiples of 8), else 32

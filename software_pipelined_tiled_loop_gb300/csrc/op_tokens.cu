@@ -17,7 +17,13 @@
 // peers' sums come as 16-byte loads) and writes those outputs.  No scratch, no
 // second kernel, the same bits every time.
 //
-// Rings are sized for two CTAs an SM, and the next kernel in the stream may
+// Bound by HBM: a call from a graph over cold weights reads 134 MB (gated 1 x
+// 8192 x 4096) in 22.3 us (6.0 TB/s of a measured 6.8), 67 MB (24 x 16384 x
+// 2048) in 15.4, 33.5 MB (1 x 4096 x 4096) in 9.3 and nothing to speak of (1 x
+// 512 x 512) in 4.1: some 4 us are launch, first loads, barriers and exit.
+//
+// Rings are sized for two CTAs an SM (S chosen for one such CTA an SM took 11.8 us
+// for 1 x 4096 x 4096 and 30 for 24 x 16384 x 2048), and the next kernel in the stream may
 // start its CTAs while this one drains: before they wait for it they ask L2 for
 // their first weights.  That is safe whatever the kernel before writes, since
 // a prefetch moves nothing past L2, where all writes meet.
