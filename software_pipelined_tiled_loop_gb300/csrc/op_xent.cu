@@ -12,14 +12,15 @@
 // gradient with them.  Divided by c those entries start from exactly -1; c
 // itself multiplies the sums in fp32.
 //
-// Forward: the product's epilogue folds every accumulator into a running
-// maximum m and sum s of exp(L - m) for each row and column block (a thread
-// holds a whole row segment, so neither needs a shuffle), and the logit of the
-// row's own target is written by the thread that holds it.  A second kernel
-// joins the blocks of a row: lse = M + log sum_b s_b exp(m_b - M).
-// Gradient: the vocabulary goes by in pieces whose P fits the workspace; each
-// piece's logits are recomputed by the same product, whose epilogue writes P
-// (rounded to bf16 once, as an operand of the gradient products).
+// Forward: the product's epilogue folds every accumulator into a maximum m and
+// sum s of exp(L - m) for each row and column block (a thread holds a whole row
+// segment, so neither needs a shuffle).  A second kernel joins the blocks of a
+// row, lse = M + log sum_b s_b exp(m_b - M), and multiplies out the row's own
+// target logit.
+// Gradient: where all of P fits the workspace the forward epilogue also keeps the
+// exponentials, which one elementwise pass turns into P; else the vocabulary goes by
+// in pieces, whose logits the same product computes a second time and whose epilogue
+// writes P.
 //
 // Tensor-bound beyond some 300 tokens: 4096 x 131072 x 4096 with gradients takes
 // 8.2 ms for three products of 4.4e12 operations each (1.61 PFLOP/s overall, 95 %
@@ -58,8 +59,11 @@ __device__ __forceinline__ float ex2(float x) {
 //
 // KEEP: the exponentials themselves are stored as fp16, 2^(L log2(e) - m) with
 // the block's own m, so that the gradient pass turns them into P without the
-// logits' product a second time.  They lie in (0, 1] and fp16 carries them to
-// 2^-11 of their size, an eighth of what rounding P to bf16 costs.
+// logits' product a second time: 4 bytes of traffic a logit instead of 2 D
+// operations (with gradients, kept against computed again: 4096 x 32768 x 128 294
+// against 298 us, x 768 504 against 566, 3472 x 5843 x 336 82 against 94).  They lie
+// in (0, 1] and fp16 carries them to 2^-11 of their size, an eighth of what rounding
+// P to bf16 costs.
 template <bool KEEP>
 struct EpiXentStats {
     float *part_m, *part_s;  // [column block][rows]
@@ -168,6 +172,24 @@ __device__ __forceinline__ void join_ms(float &m, float &s, float m2, float s2) 
     m = n;
 }
 
+// A thread's part of the dot product of two rows (16-byte aligned): columns from
+// k, eight at a time.
+__device__ __forceinline__ float row_dot(const uint16_t *x, const uint16_t *e, int D, int k,
+                                         int step) {
+    float d = 0.0f;
+    for (; k < D; k += step) {
+        const uint4 a = *reinterpret_cast<const uint4 *>(x + k);
+        const uint4 b = *reinterpret_cast<const uint4 *>(e + k);
+        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (k + 2 * i < D) d = fmaf(bf16_lo(aw[i]), bf16_lo(bw[i]), d);
+            if (k + 2 * i + 1 < D) d = fmaf(bf16_hi(aw[i]), bf16_hi(bw[i]), d);
+        }
+    }
+    return d;
+}
+
 template <int ROWS>
 __global__ void __launch_bounds__(256)
     xent_join_kernel(const float *part_m, const float *part_s, long long rows, int blocks, int T,
@@ -209,20 +231,10 @@ __global__ void __launch_bounds__(256)
         const int tw = blockIdx.x * ROWS + (ROWS > 1 ? w : 0);
         const int64_t y = tw < T ? target[tw] : -1;
         float d = 0.0f;
-        if (loss && y >= 0 && y < V) {
-            const uint16_t *x = X.p + tw * X.ld, *e = W.p + y * W.ld;  // 16-byte-aligned rows
-            for (int k = (ROWS > 1 ? lane : static_cast<int>(threadIdx.x)) * 8; k < D;
-                 k += ROWS > 1 ? 256 : 2048) {
-                const uint4 a = *reinterpret_cast<const uint4 *>(x + k);
-                const uint4 b = *reinterpret_cast<const uint4 *>(e + k);
-                const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (k + 2 * i < D) d = fmaf(bf16_lo(aw[i]), bf16_lo(bw[i]), d);
-                    if (k + 2 * i + 1 < D) d = fmaf(bf16_hi(aw[i]), bf16_hi(bw[i]), d);
-                }
-            }
-        }
+        if (loss && y >= 0 && y < V)
+            d = row_dot(X.p + tw * X.ld, W.p + y * W.ld, D,
+                        (ROWS > 1 ? lane : static_cast<int>(threadIdx.x)) * 8,
+                        ROWS > 1 ? 256 : 2048);
 #pragma unroll
         for (int o = 16; o > 0; o /= 2) d += __shfl_xor_sync(0xffffffffu, d, o);
         if (lane == 0) dot[w] = d;
@@ -543,33 +555,82 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     }
 }
 
-// P from kept logits: a thread eight columns of a row.
+// P from kept logits, with what xent_join_kernel does for other gradients: a
+// block takes kProbCols columns of a row, joins the row's (m, s) itself (a few hundred
+// pairs from L2) and the weights' common scale, and leaves a launch out.  The first
+// block of a row also writes its loss and lse.
+constexpr int kProbCols = 2048;  // eight a thread
 __global__ void __launch_bounds__(256)
-    xent_probs_kernel(const float *logits, uint16_t *P, long long ld, int T, int V,
-                      const float *lse, const int64_t *target, const float *dloss,
-                      const float *scale) {
+    xent_probs_kernel(const float *part_m, const float *part_s, long long rows, int blocks,
+                      const float *logits, uint16_t *P, long long ld, int T, int V, int D,
+                      const OpMat X, const OpMat W, const int64_t *target, float *loss,
+                      float *lse, const float *dloss, float *scale) {
     grid_dependency_wait();
     grid_launch_dependents();
-    const int octets = (V + 7) / 8;
-    const long long total = static_cast<long long>(T) * octets;
-    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-        const int t = static_cast<int>(i / octets);
-        const int c = static_cast<int>(i - static_cast<long long>(t) * octets) * 8;
-        const int64_t y = target[t];
-        const bool counts = y >= 0 && y < V;
-        const float g = counts ? (dloss ? dloss[t] / *scale : 1.0f) : 0.0f;
-        const float l = counts ? lse[t] * kLog2e : 0.0f;
-        const float4 *src = reinterpret_cast<const float4 *>(logits + t * ld + c);
+    __shared__ float sm[8], ss[8], dot[8], sc[8];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int across = (V + kProbCols - 1) / kProbCols;
+    const int t = blockIdx.x / across;
+    const int c0 = (blockIdx.x - t * across) * kProbCols;
+    const int64_t y = target[t];
+    const bool counts = y >= 0 && y < V;
+    float m = -CUDART_INF_F, s = 0.0f, d = 0.0f, g = 0.0f;
+    for (int b = threadIdx.x; b < blocks; b += 256)
+        join_ms(m, s, part_m[b * rows + t], part_s[b * rows + t]);
+    if (dloss != nullptr && threadIdx.x < T) {  // T <= kFewMax threads
+        const int64_t yi = target[threadIdx.x];
+        const float v = fabsf(dloss[threadIdx.x]);
+        if (yi >= 0 && yi < V && v < CUDART_INF_F) g = v;
+    }
+    if (c0 == 0 && loss != nullptr && counts)
+        d = row_dot(X.p + t * X.ld, W.p + y * W.ld, D, static_cast<int>(threadIdx.x) * 8, 2048);
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, o);
+        const float s2 = __shfl_xor_sync(0xffffffffu, s, o);
+        join_ms(m, s, m2, s2);
+        d += __shfl_xor_sync(0xffffffffu, d, o);
+        g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+    }
+    if (lane == 0) {
+        sm[w] = m;
+        ss[w] = s;
+        dot[w] = d;
+        sc[w] = g;
+    }
+    __syncthreads();
+    m = sm[0];
+    s = ss[0];
+    d = dot[0];
+    g = sc[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+        join_ms(m, s, sm[i], ss[i]);
+        d += dot[i];
+        g = fmaxf(g, sc[i]);
+    }
+    const float c = dloss != nullptr && g > 0.0f ? g : 1.0f;
+    const float l2 = m + log2f(s);
+    if (threadIdx.x == 0 && c0 == 0) {
+        if (lse) lse[t] = kLn2 * l2;
+        if (loss) loss[t] = counts ? kLn2 * l2 - d : 0.0f;
+        if (dloss != nullptr && t == 0) *scale = c;
+    }
+    const float gt = counts ? (dloss ? dloss[t] / c : 1.0f) : 0.0f;
+    const int c1 = min(V, c0 + kProbCols);
+    const int k = c0 + static_cast<int>(threadIdx.x) * 8;
+    if (k < c1) {
+        const float4 *src = reinterpret_cast<const float4 *>(logits + t * ld + k);
         const float4 p = src[0], q = src[1];
         const float x[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
         float o[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            float e = exp2f(fmaf(x[j], kLog2e, -l));
-            if (y == c + j) e -= 1.0f;
-            o[j] = counts ? e * g : 0.0f;
+            float e = exp2f(fmaf(x[j], kLog2e, -l2));
+            if (y == k + j) e -= 1.0f;
+            o[j] = counts ? e * gt : 0.0f;
         }
-        *reinterpret_cast<uint4 *>(P + t * ld + c) =
+        *reinterpret_cast<uint4 *>(P + t * ld + k) =
             make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]),
                        pack_bf16(o[6], o[7]));
     }
@@ -641,10 +702,6 @@ static pgemm_status launch_logits(const OpDevice &dev, int T, int cols, int D, c
 // Workspace of a gradient's P when the caller names none: 2 GiB (all of P up
 // to 8192 tokens x 131072).
 constexpr long long kDefaultWorkspace = 2ll << 30;
-
-// Kept exponentials cost 4 bytes of traffic a logit, computing it again 2 D
-// operations: even near D = 600 at the measured peaks.
-constexpr int kKeepMinD = 640;
 
 static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t *W,
                          const int64_t *target, const float *dloss, float *loss, float *lse,
@@ -742,7 +799,7 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
     px.epi.scale = pw.epi.scale = scale;
 
     // One piece: its exponentials are kept and P follows from them.
-    const bool keep = pieces == 1 && D >= kKeepMinD && !few;
+    const bool keep = pieces == 1 && !few;
     float *part_m = arena.at<float>(at_m), *part_s = arena.at<float>(at_s);
     uint16_t *P = pieces ? arena.at<uint16_t>(at_p) : nullptr;
     {
@@ -765,12 +822,22 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
                       : launch_logits<StatsOne>(dev, T, V, D, x, w, 0, maps, e, s);
         }
         if (st != PGEMM_OK) return st;
-        const bool by_row = T < 8 * dev.sm_count;  // fewer than a block of 8 rows an SM
-        st = launch_small(by_row ? xent_join_kernel<1> : xent_join_kernel<8>,
-                          dim3(by_row ? T : (T + 7) / 8), dim3(256), s,
-                          static_cast<const float *>(part_m), static_cast<const float *>(part_s),
-                          rows, blocks, T, static_cast<long long>(V), D, x, w, target, loss,
-                          lse_buf, dloss, scale);
+        if (keep_logits) {
+            const unsigned across = (V + kProbCols - 1) / kProbCols;
+            st = launch_small(xent_probs_kernel, dim3(across * T), dim3(256), s,
+                              static_cast<const float *>(part_m),
+                              static_cast<const float *>(part_s), rows, blocks,
+                              static_cast<const float *>(arena.at<float>(at_z)), P, piece, T, V, D,
+                              x, w, target, loss, lse, dloss, scale);
+        } else {
+            const bool by_row = T < 8 * dev.sm_count;  // fewer than a block of 8 rows an SM
+            st = launch_small(by_row ? xent_join_kernel<1> : xent_join_kernel<8>,
+                              dim3(by_row ? T : (T + 7) / 8), dim3(256), s,
+                              static_cast<const float *>(part_m),
+                              static_cast<const float *>(part_s), rows, blocks, T,
+                              static_cast<long long>(V), D, x, w, target, loss, lse_buf, dloss,
+                              scale);
+        }
         if (st != PGEMM_OK) return st;
     }
 
@@ -779,12 +846,7 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
         const long long v0 = i * piece;
         const int cols = static_cast<int>(V - v0 < piece ? V - v0 : piece);
         if (keep_logits) {
-            const long long n = (static_cast<long long>(T) * ((V + 7) / 8) + 255) / 256;
-            const long long most = dev.sm_count * 8ll;
-            st = launch_small(xent_probs_kernel, dim3(static_cast<unsigned>(n < most ? n : most)),
-                              dim3(256), s, static_cast<const float *>(arena.at<float>(at_z)), P,
-                              piece, T, V, static_cast<const float *>(lse_buf), target, dloss,
-                              static_cast<const float *>(scale));
+            // P is there already
         } else if (keep) {
             const dim3 grid(static_cast<unsigned>((V + 1023) / 1024) * ((T + 31) / 32));
             st = launch_small(pair ? xent_scale_kernel<StatsPair::EPI_COLS>

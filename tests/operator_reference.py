@@ -140,9 +140,9 @@ def gated_backward(X, Wg, Wu, name, dH):
 
 
 def xent(X, W, y, dl=None):
-    """loss, lse and (with dl) dX, dW, each with its bound.  From D = 640 on the
-    exponentials may have been kept as fp16 relative to a column block's largest:
-    2^-11 of themselves, or half an fp16 subnormal step of the row's largest."""
+    """loss, lse and (with dl) dX, dW, each with its bound.  The exponentials may
+    have been kept as fp16 relative to a column block's largest: 2^-11 of
+    themselves, or half an fp16 subnormal step of the row's largest."""
     X, W = X.double(), W.double()
     T, D = X.shape
     V = W.shape[0]
@@ -166,8 +166,7 @@ def xent(X, W, y, dl=None):
     w = torch.where(valid, dl.double(), zero).unsqueeze(1)
     p = torch.exp(logits - lse.unsqueeze(1))
     ep = p * (torch.expm1(el + elog.unsqueeze(1)) + 2.0 ** -20 + 2.0 ** -22 * logits.abs())
-    if D >= 640:
-        ep = ep + 2.0 ** -11 * p + 2.0 ** -25 * p.amax(1, keepdim=True)
+    ep = ep + 2.0 ** -11 * p + 2.0 ** -25 * p.amax(1, keepdim=True)
     p = p.scatter_add(1, at, -torch.ones_like(at, dtype=torch.float64))
     d, e = p * w, ep * w.abs()
     e = e + HALF * (d.abs() + e) + TINY

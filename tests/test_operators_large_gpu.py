@@ -63,7 +63,7 @@ def test_gated_pre_activations_past_31_bits():
     ref.check(dX[rows], *want["dX"], "dX")
 
 
-@pytest.mark.parametrize("D", [64, 648])  # P from logits computed again; from kept exponentials
+@pytest.mark.parametrize("D", [64, 648])
 def test_xent_probabilities_past_31_bits(D):
     T, V = 9000, 240000  # P has 2.16e9 entries, kept in one piece
     X, W = rnd(8, T, D), rnd(9, V, D, std=2 * D ** -0.5)
