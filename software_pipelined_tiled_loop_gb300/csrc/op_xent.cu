@@ -344,9 +344,10 @@ __global__ void __launch_bounds__(256)
 
 // ------------------------------------------------------------ few tokens ---
 // Up to 64 tokens: the pass is bound by reading W once.  The rows of W take the
-// tensor core's M side (128 of the vocabulary a tile), the tokens its N side, so
+// tensor core's M side (up to 128 of the vocabulary a tile), the tokens its N side, so
 // that a ring stage is 16 KB of W beside 2 to 8 KB of X; with a token a row it
-// would be half padding (V = 98392, D = 1472, 24 tokens: 72 us, 4.0 TB/s of W).
+// would be half padding (V = 98392, D = 1472, 24 tokens: 72 us so, 50 here, 5.8 TB/s
+// of W).
 // A thread holds one vocabulary entry's logits of 16 or 32 tokens and keeps
 // running (m, s) for each through all of its CTA's tiles; lanes and warps are
 // joined once at the end.  KEEP: the logits themselves are stored (fp32, T x V,
@@ -375,6 +376,7 @@ struct FewCfg {
 
 struct FewArgs {
     int T, V, D, k_tiles, tiles;
+    int tile_rows;           // rows of W a tile, at most 128
     float *part_m, *part_s;  // [CTA][rows]
     long long rows;
     float *logits;           // T x V, pitch ld; or nullptr
@@ -426,6 +428,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
 
     if (warp == 0) {
         if (lane == 0) {
+            const uint32_t stage_tx = a.tile_rows * BK * 2 + Cfg::X_BYTES;
             uint32_t it = 0;
             bool ok = true;
             for (int tile = blockIdx.x; ok && tile < a.tiles; tile += gridDim.x) {
@@ -436,8 +439,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                         break;
                     }
                     uint8_t *st = smem + s * Cfg::STAGE_BYTES;
-                    mbar_arrive_expect_tx(&full[s], Cfg::STAGE_BYTES);
-                    tma_load_2d(st, &map_w, &full[s], kt * BK, tile * 128);
+                    mbar_arrive_expect_tx(&full[s], stage_tx);
+                    tma_load_2d(st, &map_w, &full[s], kt * BK, tile * a.tile_rows);
                     tma_load_2d(st + Cfg::W_BYTES, &map_x, &full[s], kt * BK, 0);
                 }
             }
@@ -510,8 +513,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                 }
                 acc.release();
             }
-            const long long v = static_cast<long long>(tile) * 128 + q * 32 + lane;
-            if (!ok || v >= a.V) continue;
+            // the MMA's rows beyond the tile's hold what the stage held before
+            const int row = static_cast<int>(q * 32 + lane);
+            const long long v = static_cast<long long>(tile) * a.tile_rows + row;
+            if (!ok || row >= a.tile_rows || v >= a.V) continue;
 #pragma unroll
             for (int j = 0; j < TT; ++j) {
                 if (a.logits != nullptr && t0 + j < a.T)
@@ -650,7 +655,7 @@ static pgemm_status launch_few(const OpDevice &dev, FewArgs a, const OpMat &X, c
     pgemm_status st = op_kernel_setup(dev, info, &slots);
     CUtensorMap mw{}, mx{};
     if (a.D > 0) {
-        if (st == PGEMM_OK) st = op_encode(&mw, W.p, a.D, a.V, W.ld, 128);
+        if (st == PGEMM_OK) st = op_encode(&mw, W.p, a.D, a.V, W.ld, a.tile_rows);
         if (st == PGEMM_OK) st = op_encode(&mx, X.p, a.D, a.T, X.ld, Cfg::TOK);
     }
     if (st != PGEMM_OK) return st;
@@ -670,6 +675,7 @@ static pgemm_status launch_few(const OpDevice &dev, FewArgs a, const OpMat &X, c
                : PGEMM_ERR_CUDA;
 }
 constexpr int kFewMax = 64;
+constexpr int kFewEvenD = 512;  // from here on every CTA gets the same number of tiles
 
 // rounds of 1024 products for the statistics
 using StatsPair = OpCfg<256, 3, 2, 2, false, true, false, 8>;
@@ -726,9 +732,21 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
     const int block_cols = pair ? StatsPair::EPI_COLS : StatsOne::EPI_COLS;
     // (m, s) of a row: one for each column block, or for each CTA
     int blocks = (V + block_cols - 1) / block_cols;
+    int few_rows = 128, few_tiles = 0;
     if (few) {
-        const int tiles = (V + 127) / 128, ctas = dev.sm_count * (T <= 32 ? 2 : 1);
-        blocks = tiles < ctas ? tiles : ctas;
+        // 128 rows a tile, unless the CTAs take several each: then the same number for
+        // every CTA, since a few left over would cost a wave of their own.  39928 x
+        // 2048, one token: 38.7 us with whole tiles, 33.8 so; 50257 x 1024: 25.0 and
+        // 23.5.  A short D pays more for the further tile than for the wave (39928 x
+        // 160: 8.7 and 9.6 us), and CTAs with one tile each lose by shorter ones
+        // (18488 x 1024: 12.3 and 13.7).
+        const long long ctas = dev.sm_count * (T <= 32 ? 2 : 1);
+        const long long waves = (V + 128 * ctas - 1) / (128 * ctas);
+        if (waves > 1 && D >= kFewEvenD)
+            few_rows = static_cast<int>(
+                op_round_up((V + waves * ctas - 1) / (waves * ctas), 8));
+        few_tiles = (V + few_rows - 1) / few_rows;
+        blocks = static_cast<int>(few_tiles < ctas ? few_tiles : ctas);
     }
     const long long rows = op_round_up(T, 32);
     // vocabulary pieces, whole tiles wide
@@ -805,7 +823,7 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
     {
         OpMaps maps{};
         if (few) {
-            const FewArgs a{T, V, D, 0, (V + 127) / 128, part_m, part_s, rows,
+            const FewArgs a{T, V, D, 0, few_tiles, few_rows, part_m, part_s, rows,
                             keep_logits ? arena.at<float>(at_z) : nullptr, piece};
             st = T <= 16   ? launch_few<FewCfg<16>>(dev, a, x, w, blocks, s)
                  : T <= 32 ? launch_few<FewCfg<32>>(dev, a, x, w, blocks, s)

@@ -2,6 +2,7 @@
 64 bits, forward and backward, at the sizes and values where they can go
 wrong.  Bounds: operator_reference.py."""
 import math
+import threading
 
 import pytest
 
@@ -278,6 +279,21 @@ def test_xent_grad(i, size, workspace):
         ref.check(got, *want[name], name)
 
 
+# vocabularies a little beyond what one tile of every block of the few-token kernel covers
+@pytest.mark.parametrize("i,size", list(enumerate([(1, 39001, 520), (20, 40003, 512),
+                                                   (64, 20001, 776), (33, 60007, 520)])))
+def test_xent_few_tokens_several_tiles(i, size):
+    T, V, D = size
+    X, W, y, dl = xent_inputs(T, V, D, 970 + i)
+    y[0] = V - 1
+    loss, lse = nan_like(T, dtype=torch.float32), nan_like(T, dtype=torch.float32)
+    dX, dW = nan_like(T, D), nan_like(V, D)
+    pg.xent_bf16_grad(T, V, D, X, W, y, dl, loss, lse, dX, dW)
+    want = ref.xent(X, W, y, dl)
+    for name, got in (("lse", lse), ("loss", loss), ("dX", dX), ("dW", dW)):
+        ref.check(got, *want[name], name)
+
+
 def test_xent_outputs_may_be_absent():
     T, V, D = 70, 1001, 72
     X, W, y, _ = xent_inputs(T, V, D, 1000)
@@ -489,6 +505,32 @@ def test_results_do_not_depend_on_timing_or_stream():
     call2()
     side.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(first, bufs2))
+
+
+def test_operators_from_several_threads():
+    call, bufs = all_operators()
+    call()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    jobs = [all_operators(stream=st) for st in streams]
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(k):
+        try:
+            for _ in range(5):
+                jobs[k][0]()
+            streams[k].synchronize()
+        except Exception as e:  # reported by the main thread
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for _, got in jobs:
+        assert all(torch.equal(a, b) for a, b in zip(bufs, got))
 
 
 def test_operators_in_a_captured_graph():
