@@ -62,10 +62,9 @@ __device__ __forceinline__ float act_value(float z) {
     if constexpr (ACT == PGEMM_ACT_RELU) {
         return z < 0.0f ? 0.0f : z;  // a NaN stays one
     } else if constexpr (ACT == PGEMM_ACT_GELU) {
-        // z Phi(z) = max(z, 0) - |z| Phi(-|z|) on either side
         float e;
         const float h = normal_tail(z, e);
-        return fmaf(-fabsf(z), h, z < 0.0f ? 0.0f : z);
+        return z * (z < 0.0f ? h : 1.0f - h);
     } else if constexpr (ACT == PGEMM_ACT_GELU_TANH) {
         return z * sigmoid_neg2(z * fmaf(z * z, kTanhC * 0.044715f, kTanhC));
     } else if constexpr (ACT == PGEMM_ACT_SILU) {
@@ -84,8 +83,9 @@ __device__ __forceinline__ float act_value_grad(float z, float &value) {
     } else if constexpr (ACT == PGEMM_ACT_GELU) {
         float e;
         const float h = normal_tail(z, e);
-        value = fmaf(-fabsf(z), h, z < 0.0f ? 0.0f : z);
-        return fmaf(z * 0.39894228040143268f, e, z < 0.0f ? h : 1.0f - h);
+        const float phi = z < 0.0f ? h : 1.0f - h;
+        value = z * phi;
+        return fmaf(z * 0.39894228040143268f, e, phi);
     } else if constexpr (ACT == PGEMM_ACT_GELU_TANH) {
         const float z2 = z * z;
         const float s = sigmoid_neg2(z * fmaf(z2, kTanhC * 0.044715f, kTanhC));

@@ -80,6 +80,28 @@ def test_linear_activations(name, M):
     ref.check(Y, y, bound, name)
 
 
+@pytest.mark.parametrize("name", ACTS)
+@pytest.mark.parametrize("M,K", [(3, 96), (130, 96), (130, 0), (130, 1100)])
+def test_activations_of_infinities_and_nan(name, M, K):
+    # a column of each through the bias; its neighbours stay as they are
+    X, W, b, _ = linear_inputs(M, 264, K, 310)
+    special = {5: math.inf, 70: -math.inf, 263: math.nan}
+    plain = nan_like(M, 264)
+    pg.linear_bf16(M, 264, K, X, W, b, name, None, plain, preact=nan_like(
+        M, 264, dtype=torch.float32))
+    b = b.clone()
+    for column, value in special.items():
+        b[column] = value
+    Y, Z = nan_like(M, 264), nan_like(M, 264, dtype=torch.float32)
+    pg.linear_bf16(M, 264, K, X, W, b, name, None, Y, preact=Z)
+    for column, value in special.items():
+        want = ref.act(torch.full((M,), value, dtype=torch.float64, device="cuda"), name)
+        assert torch.equal(Y[:, column].double().nan_to_num(7.0, 9.0, -9.0),
+                           want.nan_to_num(7.0, 9.0, -9.0)), (name, value)
+        plain[:, column] = Y[:, column] = 0
+    assert torch.equal(Y, plain)
+
+
 @pytest.mark.parametrize("M,N,K", [(3, 264, 96), (130, 264, 96), (130, 261, 96), (8, 128, 8192),
                                    (128, 128, 8192)])
 def test_linear_residual_in_place(M, N, K):
