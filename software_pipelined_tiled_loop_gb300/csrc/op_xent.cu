@@ -48,7 +48,7 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // Softmax statistics are kept to base 2: m is the largest L log2(e) of a row's
-// column block, s the block's sum of 2^(L log2(e) - m).
+// column block (or 15 less, see KEEP), s the block's sum of 2^(L log2(e) - m).
 //
 // Accumulation rounds of 1024 products are added in fp32 registers.  The
 // tensor core truncates its running sum at every step of 16 products, always
@@ -58,12 +58,14 @@ __device__ __forceinline__ float ex2(float x) {
 // additions leave a quarter of it.
 //
 // KEEP: the exponentials themselves are stored as fp16, 2^(L log2(e) - m) with
-// the block's own m, so that the gradient pass turns them into P without the
+// the block's own m, 15 below its largest, so that the gradient pass turns them into P without the
 // logits' product a second time: 4 bytes of traffic a logit instead of 2 D
 // operations (with gradients, kept against computed again: 4096 x 32768 x 128 294
 // against 298 us, x 768 504 against 566, 3472 x 5843 x 336 82 against 94).  They lie
-// in (0, 1] and fp16 carries them to 2^-11 of their size, an eighth of what rounding
-// P to bf16 costs.
+// in (0, 2^15], just within fp16, which carries them to 2^-11 of their size, an eighth
+// of what rounding P to bf16 costs, down to 2^-29 of the block's largest, and to 2^-40
+// of that largest below: an unlikely token beside a likely one keeps its gradient.
+constexpr float kKeepShift = 15.0f;
 template <bool KEEP>
 struct EpiXentStats {
     float *part_m, *part_s;  // [column block][rows]
@@ -90,7 +92,8 @@ struct EpiXentStats {
         float mx[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
         for (int j = 4; j < COLS; ++j) mx[j & 3] = fmaxf(mx[j & 3], v[j]);
-        const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kLog2e;
+        const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kLog2e -
+                        (KEEP ? kKeepShift : 0.0f);
         // nothing but -inf: any finite reference gives sums of zero
         const float ref = m == -CUDART_INF_F ? 0.0f : m;
         float s[4] = {0.f, 0.f, 0.f, 0.f};

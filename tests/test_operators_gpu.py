@@ -316,6 +316,26 @@ def test_xent_few_tokens_several_tiles(i, size):
         ref.check(got, *want[name], name)
 
 
+@pytest.mark.parametrize("T", [3, 200, 700])
+def test_xent_unlikely_tokens_beside_a_likely_one(T):
+    # Token 0 takes all but exp(-20) of every row: the other rows of dW come from
+    # probabilities of 2e-9 alone, which do not cancel: bf16's relative error twice (P's
+    # rounding and the output's, 2^-8 each), 2^-11 of a kept exponential, and less than
+    # 2^-12 from the logits' and sums' own errors.
+    V, D = 96, 64
+    X = torch.zeros(T, D, device="cuda", dtype=torch.bfloat16)
+    X[:, 0] = 1
+    X[:, 1:] = rnd(990, T, D - 1).abs()
+    W = torch.zeros(V, D, device="cuda", dtype=torch.bfloat16)
+    W[0, 0] = 20
+    y = torch.zeros(T, device="cuda", dtype=torch.int64)
+    dW = nan_like(V, D)
+    pg.xent_bf16_grad(T, V, D, X, W, y, None, None, None, None, dW)
+    p = torch.softmax(X.double() @ W.double().t(), 1)
+    want = p[:, 1:].t() @ X.double()
+    assert ((dW[1:].double() - want).abs() <= (2.0 ** -7 + 2.0 ** -10) * want).all()
+
+
 def test_xent_outputs_may_be_absent():
     T, V, D = 70, 1001, 72
     X, W, y, _ = xent_inputs(T, V, D, 1000)
