@@ -262,6 +262,13 @@ def _operand(x, name, count, itemsize) -> int:
     return p
 
 
+_DIM_MAX = 2 ** 31 - 1  # the C interface's sizes are 32-bit
+
+
+def _too_large(what):
+    raise ValueError(f"{what}: sizes are at most {_DIM_MAX}")
+
+
 def _act(act) -> int:
     if isinstance(act, str):
         if act not in ACTIVATIONS:
@@ -275,6 +282,8 @@ def linear_bf16(M, N, K, X, W, bias, act, residual, Y, preact=None, stream=None)
     W: K x N; bias (N) and residual (M x N, may be Y) may be None; ``act`` is a
     name of ACTIVATIONS.  ``preact`` (M x N fp32) receives X @ W + bias for the
     backward call.  Asynchronous on ``stream``."""
+    if M | N | K > _DIM_MAX:
+        _too_large("linear_bf16")
     _check(lib().linear_bf16(M, N, K, _operand(X, "X", M * K, 2), _operand(W, "W", K * N, 2),
                              _operand(bias, "bias", N, 2), _act(act),
                              _operand(residual, "residual", M * N, 2),
@@ -286,6 +295,8 @@ def linear_bf16_backward(M, N, K, X, W, bias, act, dY, dX, dW, dbias, preact=Non
     """Gradients of linear_bf16 for dY (M x N) into dX (M x K), dW (K x N) and
     dbias (N), each skipped when None.  ``preact``: what the forward call kept,
     or None to compute it again.  Asynchronous."""
+    if M | N | K > _DIM_MAX:
+        _too_large("linear_bf16_backward")
     _check(lib().linear_bf16_backward(
         M, N, K, _operand(X, "X", M * K, 2), _operand(W, "W", K * N, 2),
         _operand(bias, "bias", N, 2), _act(act), _operand(dY, "dY", M * N, 2),
@@ -298,6 +309,8 @@ def gated_bf16(M, F, K, X, Wg, Wu, act, H, preact=None, stream=None):
     """H <- act(X @ Wg) * (X @ Wu), bf16 with fp32 arithmetic.  X: M x K, Wg and
     Wu: K x F, H: M x F.  ``preact`` (2 x M x F fp32) receives both products
     for the backward call.  Asynchronous on ``stream``."""
+    if M | F | K > _DIM_MAX:
+        _too_large("gated_bf16")
     _check(lib().gated_bf16(M, F, K, _operand(X, "X", M * K, 2), _operand(Wg, "Wg", K * F, 2),
                             _operand(Wu, "Wu", K * F, 2), _act(act), _operand(H, "H", M * F, 2),
                             _operand(preact, "preact", 2 * M * F, 4), _stream(stream)),
@@ -308,6 +321,8 @@ def gated_bf16_backward(M, F, K, X, Wg, Wu, act, dH, dX, dWg, dWu, preact=None, 
     """Gradients of gated_bf16 for dH (M x F) into dX (M x K), dWg and dWu
     (K x F); dX, or dWg and dWu together, may be None.  ``preact``: what the
     forward call kept, or None to compute it again.  Asynchronous."""
+    if M | F | K > _DIM_MAX:
+        _too_large("gated_bf16_backward")
     _check(lib().gated_bf16_backward(
         M, F, K, _operand(X, "X", M * K, 2), _operand(Wg, "Wg", K * F, 2),
         _operand(Wu, "Wu", K * F, 2), _act(act), _operand(dH, "dH", M * F, 2),
@@ -320,6 +335,8 @@ def xent_bf16(T, V, D, X, W, target, loss, lse, stream=None):
     """Softmax cross entropy of logits X @ W.T over a vocabulary: X: T x D, W:
     V x D bf16, target: T int64 (outside [0, V): the row does not count, loss
     0); loss and lse: T fp32, either may be None.  Asynchronous."""
+    if T | V | D > _DIM_MAX:
+        _too_large("xent_bf16")
     _check(lib().xent_bf16(T, V, D, _operand(X, "X", T * D, 2), _operand(W, "W", V * D, 2),
                            _operand(target, "target", T, 8), _operand(loss, "loss", T, 4),
                            _operand(lse, "lse", T, 4), _stream(stream)), "xent_bf16")
@@ -331,6 +348,8 @@ def xent_bf16_grad(T, V, D, X, W, target, dloss, loss, lse, dX, dW, workspace_by
     (T x D) and dW (V x D), either of which may be None.  ``workspace_bytes``
     bounds the scratch for the probabilities (0: the library's choice); larger
     ones go by in pieces of the vocabulary.  Asynchronous."""
+    if T | V | D > _DIM_MAX:
+        _too_large("xent_bf16_grad")
     _check(lib().xent_bf16_grad(
         T, V, D, _operand(X, "X", T * D, 2), _operand(W, "W", V * D, 2),
         _operand(target, "target", T, 8), _operand(dloss, "dloss", T, 4),

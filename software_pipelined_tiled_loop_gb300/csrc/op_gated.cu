@@ -177,9 +177,9 @@ static pgemm_status launch_dual(const OpDevice &dev, int M, int F, int K, const 
     a.M = M;
     a.N = F;
     a.K = K;
-    a.m_tiles = (M + TM - 1) / TM;
-    a.n_seg = a.n_tiles = (F + Cfg::TILE_N - 1) / Cfg::TILE_N;
-    a.k_seg = a.k_tiles = (K + Cfg::SBK - 1) / Cfg::SBK;
+    a.m_tiles = op_blocks(M, TM);
+    a.n_seg = a.n_tiles = op_blocks(F, Cfg::TILE_N);
+    a.k_seg = a.k_tiles = op_blocks(K, Cfg::SBK);
     a.parts = 1;
     return op_launch<Cfg, Epi>(dev, maps, a, e, s);
 }

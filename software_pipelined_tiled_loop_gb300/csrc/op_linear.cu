@@ -101,9 +101,9 @@ static pgemm_status launch_grad(const OpDevice &dev, int M, int N, int K, const 
     a.M = M;
     a.N = N;
     a.K = K;
-    a.m_tiles = (M + TM - 1) / TM;
-    a.n_seg = a.n_tiles = (N + Cfg::TILE_N - 1) / Cfg::TILE_N;
-    a.k_seg = a.k_tiles = (K + Cfg::SBK - 1) / Cfg::SBK;
+    a.m_tiles = op_blocks(M, TM);
+    a.n_seg = a.n_tiles = op_blocks(N, Cfg::TILE_N);
+    a.k_seg = a.k_tiles = op_blocks(K, Cfg::SBK);
     a.parts = 1;
     return op_launch<Cfg, EpiLinearGrad>(dev, maps, a, e, s);
 }

@@ -252,6 +252,7 @@ static pgemm_status launch_form(const OpDevice &dev, const OpProduct &p, float *
     e.parts = parts_area;
     e.plain = !e.bias && !e.residual && !e.preact && e.act == PGEMM_ACT_NONE;
     if (parts_area != nullptr) {
+        if (op_parts_ld(p.N) > 0x7fffffffll) return PGEMM_ERR_INVALID_VALUE;
         e.parts_ld = op_parts_ld(p.N);
         e.parts_rows = op_parts_rows(p.M);
         e.parts_segments = p.n_segments;
@@ -278,10 +279,10 @@ static pgemm_status launch_form(const OpDevice &dev, const OpProduct &p, float *
     // the parts' padding columns are written too, so that the join reads whole vectors
     a.N = parts_area != nullptr ? static_cast<int>(op_parts_ld(p.N)) : p.N;
     a.K = p.K;
-    a.m_tiles = (p.M + TM - 1) / TM;
-    a.n_seg = (p.N + TN - 1) / TN;
+    a.m_tiles = op_blocks(p.M, TM);
+    a.n_seg = op_blocks(p.N, TN);
     a.n_tiles = a.n_seg * p.n_segments;
-    a.k_seg = (p.K + Cfg::SBK - 1) / Cfg::SBK;
+    a.k_seg = op_blocks(p.K, Cfg::SBK);
     a.k_tiles = a.k_seg * p.k_segments;
     a.parts = parts;
     a.overlap = p.overlap ? 1 : 0;
@@ -364,7 +365,7 @@ __global__ void __launch_bounds__(256) join_parts_kernel(const JoinParams p) {
     grid_dependency_wait();
     grid_launch_dependents();
     constexpr int AHEAD = 8 / PLACES;
-    const unsigned quads = (p.N + 3) / 4;
+    const unsigned quads = (static_cast<unsigned>(p.N) + 3) / 4;
     const long long total = static_cast<long long>(p.M) * quads * p.segments;
     const long long step = p.segments * p.rows * p.ld;
     for (long long i0 = blockIdx.x * (256ll * PLACES) + threadIdx.x; i0 < total;
@@ -465,7 +466,7 @@ pgemm_status op_join_parts(const OpDevice &dev, const float *area, int parts, in
     p.out[1] = out[1];
     p.e = epi;
     // four places a thread where there are blocks enough for every SM all the same
-    const long long places = static_cast<long long>(M) * ((N + 3) / 4) * segments;
+    const long long places = static_cast<long long>(M) * op_blocks(N, 4) * segments;
     const bool four = parts <= 4 && places >= 1024ll * 2 * dev.sm_count;
     const long long blocks = (places + (four ? 1023 : 255)) / (four ? 1024 : 256);
     const long long most = dev.sm_count * 8ll;
@@ -477,7 +478,8 @@ pgemm_status op_join_parts(const OpDevice &dev, const float *area, int parts, in
 // dZ = dY * act'(Z) (linear), dG = dH * U * act'(G) and dU = dH * act(G)
 // (gated), elementwise in fp32 from the kept fp32 pre-activations, rounded to
 // bf16 because the tensor core multiplies them next; column sums of the
-// unrounded dZ for the bias.  Memory-bound: 8 (gated 14) bytes an element; gated
+// dZ for the bias (unrounded here; where a product computed Z again, of the bf16 dZ
+// that it left).  Memory-bound: 8 (gated 14) bytes an element; gated
 // 8192 x 8192 takes 128 us (7.3 TB/s, some of Z still in L2), linear 4096 x 4096
 // 24 us (5.6 TB/s).
 // A block covers 256 columns x kGradRows rows; a thread eight columns of every
@@ -604,7 +606,7 @@ __global__ void __launch_bounds__(256)
 }
 
 static int grad_row_blocks(const OpActGrad &g) {
-    const int all = (g.M + kGradRows - 1) / kGradRows;
+    const int all = op_blocks(g.M, kGradRows);
     return all < 512 ? all : 512;
 }
 
@@ -616,7 +618,7 @@ pgemm_status op_act_grad(const OpDevice &, const OpActGrad &g, const OpArena &ar
                          cudaStream_t s) {
     if (g.M <= 0 || g.N <= 0) return PGEMM_OK;
     const ActGradParams p{g, g.dbias ? arena.at<float>(g.colsum_at) : nullptr, overlap ? 1 : 0};
-    const dim3 grid((g.N + 255) / 256, grad_row_blocks(g));
+    const dim3 grid(op_blocks(g.N, 256), grad_row_blocks(g));
     const bool vec = g.N % 8 == 0 && g.dy_ld % 8 == 0;
     if (g.u != nullptr)
         return vec ? launch_small(act_grad_kernel<true, true>, grid, dim3(256), s, p)
@@ -628,7 +630,7 @@ pgemm_status op_act_grad(const OpDevice &, const OpActGrad &g, const OpArena &ar
 pgemm_status op_act_grad_join(const OpDevice &, const OpActGrad &g, const OpArena &arena,
                               bool overlap, cudaStream_t s) {
     if (g.M <= 0 || g.N <= 0 || g.dbias == nullptr) return PGEMM_OK;
-    return launch_small(colsum_join_kernel, dim3((g.N + 31) / 32), dim3(256), s,
+    return launch_small(colsum_join_kernel, dim3(op_blocks(g.N, 32)), dim3(256), s,
                         static_cast<const float *>(arena.at<float>(g.colsum_at)),
                         grad_row_blocks(g), g.N, g.dbias, overlap ? 1 : 0);
 }

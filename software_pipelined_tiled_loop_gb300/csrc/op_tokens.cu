@@ -388,8 +388,8 @@ static int cluster_share(int slots, int n_tiles, int k_tiles) {
 
 bool op_tokens_fit(const OpDevice &dev, int M, long long N, long long K) {
     if (M > kTokensMax) return false;
-    const int n_tiles = static_cast<int>((N + 127) / 128);
-    const int k_tiles = static_cast<int>((K + 63) / 64);
+    const int n_tiles = op_blocks(N, 128);
+    const int k_tiles = op_blocks(K, 64);
     const int S = cluster_share(2 * dev.sm_count, n_tiles, k_tiles);
     return n_tiles * S >= dev.sm_count || k_tiles / S <= 32;
 }
@@ -416,9 +416,9 @@ static pgemm_status launch_tokens(const OpDevice &dev, TokensArgs a, const OpMat
                           : op_encode(&maps.w[d], W[d].p, a.N, a.K, W[d].ld, 64);
     }
     if (st != PGEMM_OK) return st;
-    a.k_seg = (a.K + Cfg::BK - 1) / Cfg::BK;
+    a.k_seg = op_blocks(a.K, Cfg::BK);
     a.k_tiles = a.k_seg * segments;
-    const int n_tiles = (a.N + Cfg::BN - 1) / Cfg::BN;
+    const int n_tiles = op_blocks(a.N, Cfg::BN);
     const int S = cluster_share(dev.sm_count * Cfg::CTAS, n_tiles, a.k_tiles);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

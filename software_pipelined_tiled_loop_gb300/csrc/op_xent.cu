@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(256)
     __shared__ float f[NB][32], g[32];
     __shared__ int yc[32];  // the target's column within the block's 1024, or -1
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int across = (V + 1023) / 1024;
+    const int across = (V - 1) / 1024 + 1;
     const int c0 = static_cast<int>(blockIdx.x % across) * 1024;
     const int row0 = static_cast<int>(blockIdx.x / across) * 32;
     const int t = row0 + lane;
@@ -577,7 +577,7 @@ __global__ void __launch_bounds__(256)
     grid_launch_dependents();
     __shared__ float sm[8], ss[8], dot[8], sc[8];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int across = (V + kProbCols - 1) / kProbCols;
+    const int across = (V - 1) / kProbCols + 1;
     const int t = blockIdx.x / across;
     const int c0 = (blockIdx.x - t * across) * kProbCols;
     const int64_t y = target[t];
@@ -625,9 +625,8 @@ __global__ void __launch_bounds__(256)
         if (dloss != nullptr && t == 0) *scale = c;
     }
     const float gt = counts ? (dloss ? dloss[t] / c : 1.0f) : 0.0f;
-    const int c1 = min(V, c0 + kProbCols);
     const int k = c0 + static_cast<int>(threadIdx.x) * 8;
-    if (k < c1) {
+    if (k < V) {
         const float4 *src = reinterpret_cast<const float4 *>(logits + t * ld + k);
         const float4 p = src[0], q = src[1];
         const float x[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
@@ -662,7 +661,7 @@ static pgemm_status launch_few(const OpDevice &dev, FewArgs a, const OpMat &X, c
         if (st == PGEMM_OK) st = op_encode(&mx, X.p, a.D, a.T, X.ld, Cfg::TOK);
     }
     if (st != PGEMM_OK) return st;
-    a.k_tiles = (a.D + Cfg::BK - 1) / Cfg::BK;
+    a.k_tiles = op_blocks(a.D, Cfg::BK);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -701,9 +700,9 @@ static pgemm_status launch_logits(const OpDevice &dev, int T, int cols, int D, c
     a.M = T;
     a.N = cols;
     a.K = D;
-    a.m_tiles = (T + TM - 1) / TM;
-    a.n_seg = a.n_tiles = (cols + Cfg::TILE_N - 1) / Cfg::TILE_N;
-    a.k_seg = a.k_tiles = (D + Cfg::SBK - 1) / Cfg::SBK;
+    a.m_tiles = op_blocks(T, TM);
+    a.n_seg = a.n_tiles = op_blocks(cols, Cfg::TILE_N);
+    a.k_seg = a.k_tiles = op_blocks(D, Cfg::SBK);
     a.parts = 1;
     return op_launch<Cfg, Epi>(dev, maps, a, e, s);
 }
@@ -734,7 +733,7 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
     const bool pair = op_use_pair(dev, T, V, D, 256, 128);
     const int block_cols = pair ? StatsPair::EPI_COLS : StatsOne::EPI_COLS;
     // (m, s) of a row: one for each column block, or for each CTA
-    int blocks = (V + block_cols - 1) / block_cols;
+    int blocks = op_blocks(V, block_cols);
     int few_rows = 128, few_tiles = 0;
     if (few) {
         // 128 rows a tile, unless the CTAs take several each: then the same number for
@@ -748,7 +747,7 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
         if (waves > 1 && D >= kFewEvenD)
             few_rows = static_cast<int>(
                 op_round_up((V + waves * ctas - 1) / (waves * ctas), 8));
-        few_tiles = (V + few_rows - 1) / few_rows;
+        few_tiles = op_blocks(V, few_rows);
         blocks = static_cast<int>(few_tiles < ctas ? few_tiles : ctas);
     }
     const long long rows = op_round_up(T, 32);
@@ -762,10 +761,10 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
         piece = cap / ((few ? 6ll : 2ll) * T) / 256 * 256;
         if (piece < 256) piece = 256;
         if (piece > p_ld_all) piece = p_ld_all;
-        pieces = static_cast<int>((V + piece - 1) / piece);
+        pieces = op_blocks(V, piece);
         // of equal width, so that none is a sliver
-        piece = op_round_up((V + pieces - 1) / pieces, 256);
-        pieces = static_cast<int>((V + piece - 1) / piece);
+        piece = op_round_up(op_blocks(V, pieces), 256);
+        pieces = op_blocks(V, piece);
     }
 
     OpArena arena(dev, s);
@@ -844,7 +843,7 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
         }
         if (st != PGEMM_OK) return st;
         if (keep_logits) {
-            const unsigned across = (V + kProbCols - 1) / kProbCols;
+            const unsigned across = op_blocks(V, kProbCols);
             st = launch_small(xent_probs_kernel, dim3(across * T), dim3(256), s,
                               static_cast<const float *>(part_m),
                               static_cast<const float *>(part_s), rows, blocks,
@@ -853,7 +852,7 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
         } else {
             const bool by_row = T < 8 * dev.sm_count;  // fewer than a block of 8 rows an SM
             st = launch_small(by_row ? xent_join_kernel<1> : xent_join_kernel<8>,
-                              dim3(by_row ? T : (T + 7) / 8), dim3(256), s,
+                              dim3(by_row ? T : op_blocks(T, 8)), dim3(256), s,
                               static_cast<const float *>(part_m),
                               static_cast<const float *>(part_s), rows, blocks, T,
                               static_cast<long long>(V), D, x, w, target, loss, lse_buf, dloss,
@@ -869,7 +868,7 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
         if (keep_logits) {
             // P is there already
         } else if (keep) {
-            const dim3 grid(static_cast<unsigned>((V + 1023) / 1024) * ((T + 31) / 32));
+            const dim3 grid(static_cast<unsigned>(op_blocks(V, 1024)) * op_blocks(T, 32));
             st = launch_small(pair ? xent_scale_kernel<StatsPair::EPI_COLS>
                                    : xent_scale_kernel<StatsOne::EPI_COLS>,
                               grid, dim3(256), s, P, piece, T, V,

@@ -138,3 +138,16 @@ def test_activation_names_match_the_header(L):
     header = open(os.path.join(os.path.dirname(pgbuild.INCLUDE), "include", "pgemm.h")).read()
     found = {n.lower(): int(v) for n, v in re.findall(r"PGEMM_ACT_(\w+) = (\d+)", header)}
     assert found == pg.ACTIVATIONS
+
+
+def test_binding_refuses_sizes_beyond_32_bits(L):
+    # ctypes would pass their low 32 bits on
+    big = 1 << 32
+    for call in (lambda: pg.linear_bf16(big + 4, 4, 4, G, G, None, "none", None, G),
+                 lambda: pg.linear_bf16_backward(4, big, 4, G, G, None, "silu", G, G, G, None),
+                 lambda: pg.gated_bf16(4, 4, 1 << 31, G, G, G, "silu", G),
+                 lambda: pg.gated_bf16_backward(big + 1, 4, 4, G, G, G, "silu", G, G, G, G),
+                 lambda: pg.xent_bf16(4, big + 4, 4, G, G, G, G, G),
+                 lambda: pg.xent_bf16_grad(4, 4, big + 4, G, G, G, None, G, G, G, G)):
+        with pytest.raises(ValueError, match="sizes are at most"):
+            call()

@@ -1,5 +1,7 @@
 """Operators whose outputs or scratch pass 2^31 elements: rows at the top, middle
 and bottom (and gradients that sum over all rows) against 64 bits."""
+import math
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -81,3 +83,35 @@ def test_xent_probabilities_past_31_bits(D):
     pg.xent_bf16_grad(T, V, D, X, W, y, None, None, None, dX2, dW2)
     for a, b in ((dX, dX2), (dW, dW2)):
         assert ((a.float() - b.float()).norm() / b.float().norm()).item() < 4e-3
+
+
+# The largest sizes an int holds, where rounding up to whole tiles passes it.
+LAST = 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("T", [1, 65])
+def test_xent_largest_vocabulary(T):
+    D = 8
+    X = torch.ones(T, D, device="cuda", dtype=torch.bfloat16)
+    W = torch.zeros(LAST, D, device="cuda", dtype=torch.bfloat16)
+    W[LAST - 1] = 3  # its logit is 24, all others 0
+    y = torch.full((T,), LAST - 1, device="cuda", dtype=torch.int64)
+    loss = torch.empty(T, device="cuda")
+    pg.xent_bf16(T, LAST, D, X, W, y, loss, None)
+    want = math.log(math.exp(24.0) + LAST - 1) - 24.0
+    # two logarithms near 24 subtracted, and the sums' own errors: 2^-20 of 24 is ample
+    assert (loss - want).abs().max().item() <= 24 * 2.0 ** -20
+
+
+@pytest.mark.parametrize("M,N", [(LAST, 8), (3, LAST), (200, 1 << 24)])
+def test_linear_largest_extents(M, N):
+    K = 8
+    X, W = rnd(21, M, K), rnd(22, K, N)
+    Y = torch.empty(M, N, device="cuda", dtype=torch.bfloat16)
+    pg.linear_bf16(M, N, K, X, W, None, "none", None, Y)
+    rows, cols = (some_rows(M) if M > 1000 else range(M)), slice(None)
+    if N > 1000:
+        cols = torch.tensor(some_rows(N), device="cuda")
+    rows = torch.tensor(list(rows), device="cuda")
+    y, bound, _, _ = ref.linear(X[rows], W[:, cols], None, "none", None)
+    ref.check(Y[rows][:, cols] if N <= 1000 else Y[:, cols], y, bound, "Y")
