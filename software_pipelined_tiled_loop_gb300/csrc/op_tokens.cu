@@ -367,17 +367,34 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     }
 }
 
-// CTAs that share a tile along K: the S of 1, 2, 4, 8 whose waves (`slots` CTAs
-// at once, each 1 / S of a tile's K steps) end soonest, with at least four
-// steps a CTA, and half a step's worth for each doubling of the join.
-static int cluster_share(int slots, int n_tiles, int k_tiles) {
+// CTAs that share a tile along K: the S of 1, 2, 4, 8 whose waves (`slots` clusters
+// at once, each CTA 1 / S of a tile's K steps) end soonest, with at least four
+// steps a CTA, and half a step's worth for each doubling of the join.  A wave costs
+// `wave` steps beside its own: its CTAs' set-up, first loads and join.  (Over 84 shapes
+// from 1000 x 512 to 65536 x 2048 and up to 128 tokens that S is 0.9 % slower than the
+// best of the four, 27 % at worst; without the term 11 %, and 1.9 times.)
+constexpr int kWaveSteps = 16;
+
+// Clusters of 1, 2, 4 and 8 CTAs that run at once, `ctas` CTAs an SM.  A cluster stays
+// within one of the GPU's own clusters of 16 to 20 SMs: of eight CTAs with an SM each
+// only 15 fit on 152 SMs.  The other sizes lose one or two, which is not counted: a
+// cluster left over by that costs less than a wave.
+struct ClusterSlots {
+    int n[4];
+};
+static ClusterSlots cluster_slots(int sm_count, int ctas) {
+    const int all = sm_count * ctas;
+    return ClusterSlots{{all, all / 2, all / 4, ctas == 1 ? sm_count / 10 : all / 8}};
+}
+
+static int cluster_share(const ClusterSlots &slots, int n_tiles, int k_tiles, int wave) {
     int best = 1;
     double best_cost = 1e30, join = 0.0;
-    for (int S = 1; S <= 8; S *= 2, join += 0.5) {
-        if (S > 1 && k_tiles / S < 4) break;
-        const int per_wave = slots / S;
+    for (int S = 1, i = 0; S <= 8; S *= 2, ++i, join += 0.5) {
+        const int per_wave = slots.n[i];
+        if ((S > 1 && k_tiles / S < 4) || per_wave < 1) break;
         const double waves = (n_tiles + per_wave - 1) / per_wave;
-        const double cost = waves * ((k_tiles + S - 1) / S) + join;
+        const double cost = waves * ((k_tiles + S - 1) / S + wave) + join;
         if (cost < best_cost) {
             best_cost = cost;
             best = S;
@@ -390,7 +407,7 @@ bool op_tokens_fit(const OpDevice &dev, int M, long long N, long long K) {
     if (M > kTokensMax) return false;
     const int n_tiles = op_blocks(N, 128);
     const int k_tiles = op_blocks(K, 64);
-    const int S = cluster_share(2 * dev.sm_count, n_tiles, k_tiles);
+    const int S = cluster_share(cluster_slots(dev.sm_count, 2), n_tiles, k_tiles, kWaveSteps);
     return n_tiles * S >= dev.sm_count || k_tiles / S <= 32;
 }
 
@@ -419,7 +436,8 @@ static pgemm_status launch_tokens(const OpDevice &dev, TokensArgs a, const OpMat
     a.k_seg = op_blocks(a.K, Cfg::BK);
     a.k_tiles = a.k_seg * segments;
     const int n_tiles = op_blocks(a.N, Cfg::BN);
-    const int S = cluster_share(dev.sm_count * Cfg::CTAS, n_tiles, a.k_tiles);
+    const int S = cluster_share(cluster_slots(dev.sm_count, Cfg::CTAS), n_tiles, a.k_tiles,
+                                kWaveSteps);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
