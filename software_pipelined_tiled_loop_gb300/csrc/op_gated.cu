@@ -217,17 +217,24 @@ static pgemm_status gated_forward(int M, int F, int K, const uint16_t *X, const 
     OpDevice dev;
     pgemm_status st = op_device(&dev);
     if (st != PGEMM_OK) return st;
+    const bool tokens = M <= kTokensMax;
     OpArena arena(dev, s);
     OpRelayout rl;
     OpMat x, wg, wu;
     if (K > 0) {
         rl.add(&x, X, M, K, arena);
-        rl.add(&wg, Wg, K, F, arena);
-        rl.add(&wu, Wu, K, F, arena);
+        if (tokens && op_raw_us(dev, M, F, K, true, false) <=
+                          op_relayout_us(2ll * K, F, K % 8 != 0)) {
+            wg = OpMat{Wg, F};  // read where they are, whatever their pitch
+            wu = OpMat{Wu, F};
+        } else {
+            rl.add(&wg, Wg, K, F, arena);
+            rl.add(&wu, Wu, K, F, arena);
+        }
     }
     if ((st = arena.alloc()) != PGEMM_OK) return st;
     if ((st = rl.run(dev, arena, s)) != PGEMM_OK) return st;
-    if (M <= kTokensMax) return op_tokens_gated(dev, M, F, K, x, wg, wu, act, H, preact, s);
+    if (tokens) return op_tokens_gated(dev, M, F, K, x, wg, wu, act, H, preact, s);
     OpMaps maps{};
     EpiGated e{H, preact, F, act, F % 8 == 0, preact != nullptr && F % 4 == 0};
     if (e.tma_h) st = op_encode_out(&maps.c[0], OpElem::BF16, H, F, M, F);
@@ -259,17 +266,27 @@ static pgemm_status gated_backward(int M, int F, int K, const uint16_t *X, const
     if (st != PGEMM_OK) return st;
     OpArena arena(dev, s);
     OpRelayout rl;
+    const bool tokens = M <= kTokensMax, x_tokens = op_tokens_fit(dev, M, K, 2ll * F);
     OpMat x, wg, wu, dg, du;
     long long dg_at = 0, du_at = 0;
     if (some) {
         rl.add(&x, X, M, K, arena);
-        rl.add(&wg, Wg, K, F, arena);
-        rl.add(&wu, Wu, K, F, arena);
+        // the products of a few rows can read them where they are
+        const bool in_place = (!want_x || x_tokens) && (preact || tokens) &&
+                              (want_x ? op_raw_us(dev, M, K, 2ll * F, false, true) : 0.0) +
+                                      (preact ? 0.0 : op_raw_us(dev, M, F, K, true, false)) <=
+                                  op_relayout_us(2ll * K, F, K % 8 != 0);
+        if (in_place) {
+            wg = OpMat{Wg, F};
+            wu = OpMat{Wu, F};
+        } else {
+            rl.add(&wg, Wg, K, F, arena);
+            rl.add(&wu, Wu, K, F, arena);
+        }
         dg.ld = du.ld = op_round_up(F, 64);
         dg_at = arena.add(dg.ld * M * 2);
         du_at = arena.add(du.ld * M * 2);
     }
-    const bool tokens = M <= kTokensMax, x_tokens = op_tokens_fit(dev, M, K, 2ll * F);
     OpProduct px, pw;
     if (want_x && !x_tokens) {
         px.form = OpForm::NT;

@@ -166,6 +166,15 @@ constexpr int kTokensMax = 128;
 // cross-entropy gradient, streaming against tiled dX: 4 tokens x 82768 x 592
 // 117 against 95 us, 16 x 15640 x 520 35 against 39).
 bool op_tokens_fit(const OpDevice &dev, int M, long long N, long long K);
+// What weights whose rows TMA cannot read cost those products beyond others (N
+// outputs, K reduction columns), and what copying a matrix to another pitch costs
+// instead (`others`: in a launch that is needed anyway): us, estimates that choose
+// between the two.
+double op_raw_us(const OpDevice &dev, int M, long long N, long long K, bool dual,
+                 bool transposed);
+inline double op_relayout_us(long long rows, long long cols, bool others) {
+    return (others ? 1.8 : 3.5) + static_cast<double>(rows) * static_cast<double>(cols) * 4 / 7.5e6;
+}
 pgemm_status op_tokens_linear(const OpDevice &dev, int M, int N, int K, const OpMat &X,
                               const OpMat &W, const OpEpilogue &e, uint16_t *Y, cudaStream_t s);
 pgemm_status op_tokens_gated(const OpDevice &dev, int M, int F, int K, const OpMat &X,

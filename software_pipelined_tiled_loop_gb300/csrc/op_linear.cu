@@ -122,6 +122,7 @@ static pgemm_status linear_forward(int M, int N, int K, const uint16_t *X, const
     OpDevice dev;
     pgemm_status st = op_device(&dev);
     if (st != PGEMM_OK) return st;
+    const bool tokens = M <= kTokensMax;
     OpProduct p;
     p.form = OpForm::NN;
     p.M = M;
@@ -133,9 +134,12 @@ static pgemm_status linear_forward(int M, int N, int K, const uint16_t *X, const
     OpRelayout rl;
     if (K > 0) {
         rl.add(&p.A[0], X, M, K, arena);
-        rl.add(&p.B[0], W, K, N, arena);
+        if (tokens && op_raw_us(dev, M, N, K, false, false) <=
+                          op_relayout_us(K, N, K % 8 != 0))
+            p.B[0] = OpMat{W, N};  // read where it is, whatever its pitch
+        else
+            rl.add(&p.B[0], W, K, N, arena);
     }
-    const bool tokens = M <= kTokensMax;
     if (!tokens) op_product_plan(dev, p, arena);
     if ((st = arena.alloc()) != PGEMM_OK) return st;
     if ((st = rl.run(dev, arena, s)) != PGEMM_OK) return st;
@@ -169,10 +173,20 @@ static pgemm_status linear_backward(int M, int N, int K, const uint16_t *X, cons
 
     OpArena arena(dev, s);
     OpRelayout rl;
+    const bool tokens = M <= kTokensMax, x_tokens = op_tokens_fit(dev, M, K, N);
     OpMat x, w, dz;
     if (some && K > 0) {
         if (X && (want_w || recompute)) rl.add(&x, X, M, K, arena);
-        if (W && (want_x || recompute)) rl.add(&w, W, K, N, arena);
+        // the products of a few rows can read it where it is
+        const bool others = ((want_w || recompute) && K % 8 != 0) || act == PGEMM_ACT_NONE;
+        const bool in_place = (!want_x || x_tokens) && (!recompute || tokens) &&
+                              (want_x ? op_raw_us(dev, M, K, N, false, true) : 0.0) +
+                                      (recompute ? op_raw_us(dev, M, N, K, false, false) : 0.0) <=
+                                  op_relayout_us(K, N, others);
+        if (in_place)
+            w = OpMat{W, N};
+        else
+            rl.add(&w, W, K, N, arena);
     }
     const bool own_dz = some && act != PGEMM_ACT_NONE;  // dZ is not dY itself
     long long dz_at = 0;
@@ -182,7 +196,6 @@ static pgemm_status linear_backward(int M, int N, int K, const uint16_t *X, cons
     } else if (some) {
         rl.add(&dz, dY, M, N, arena);
     }
-    const bool tokens = M <= kTokensMax, x_tokens = op_tokens_fit(dev, M, K, N);
     OpProduct px, pw;
     if (want_x && !x_tokens) {
         px.form = OpForm::NT;

@@ -27,6 +27,9 @@
 // start its CTAs while this one drains: before they wait for it they ask L2 for
 // their first weights.  That is safe whatever the kernel before writes, since
 // a prefetch moves nothing past L2, where all writes meet.
+//
+// Weights whose rows TMA cannot read (no multiples of 16 bytes) come through the
+// epilogue's warps, idle until the sums are complete (raw_weights).
 #include <algorithm>
 
 #include "op_act.cuh"
@@ -42,6 +45,8 @@ struct TokensArgs {
     float *preact;          // gated: both products
     const uint16_t *dy;     // gradients: M x N
     const float *scale;     // one device value times the sums, or nullptr
+    const uint16_t *w[2];   // RAW: the weights and their row length
+    long long w_ld;
     uint16_t *out, *out2;   // out2: dU of a gated gradient
     long long ldo;          // row length of out and out2
     int act;
@@ -60,9 +65,11 @@ enum class Tok {
 };
 
 // TOK: tokens of the MMA's N side.  DUAL: two weight matrices (gated), whose
-// accumulators lie side by side in tensor memory.
-template <int TOK_, Tok MODE_>
+// accumulators lie side by side in tensor memory.  RAW: weights whose rows are not
+// multiples of 16 bytes, which TMA cannot read (raw_weights).
+template <int TOK_, Tok MODE_, bool RAW_ = false>
 struct TokCfg {
+    static constexpr bool RAW = RAW_;
     static constexpr int TOK = TOK_, BN = 128, BK = 64;
     static constexpr Tok MODE = MODE_;
     static constexpr bool DUAL = MODE == Tok::GATED || MODE == Tok::GATED_GRAD;
@@ -73,17 +80,30 @@ struct TokCfg {
     static constexpr int X_SUB = TOK * BK * 2;
     static constexpr int STAGE_BYTES = NW * W_SUB + X_SUB;
     static constexpr int SUM_BYTES = NW * TOK * BN * 4;  // partial sums, over the drained ring
-    // two CTAs an SM, unless the partial sums alone are more than half of it
+    // RAW: weight rows of a K step, the aligned 16-byte chunks that cover a row, and
+    // the steps on the way
+    static constexpr int RAW_ALL = W_K ? BN : NW * BK;
+    static constexpr int RAW_CHUNKS = (W_K ? BK : BN) / 8 + 1;
+    static constexpr int RAW_STEPS = DUAL && TOK == 128 ? 2 : 3;  // (what fits)
+    static constexpr int RAW_BYTES = RAW ? RAW_STEPS * RAW_ALL * RAW_CHUNKS * 16 : 0;
+    // two CTAs an SM, unless the partial sums alone (RAW: with two stages' worth of
+    // ring beside the fetched rows) are more than half of it
     static constexpr int HALF_SM = kSmemPerSm / 2 - kSmemReservedPerBlock - 2048;
-    static constexpr int CTAS = SUM_BYTES <= HALF_SM ? 2 : 1;
-    static constexpr int STAGES = (CTAS == 2 ? HALF_SM : 232448 - 2048) / STAGE_BYTES;
+    static constexpr int LEAST = RAW && SUM_BYTES < 2 * STAGE_BYTES ? 2 * STAGE_BYTES : SUM_BYTES;
+    static constexpr int CTAS = LEAST + RAW_BYTES <= HALF_SM ? 2 : 1;
+    static constexpr int STAGES =
+        ((CTAS == 2 ? HALF_SM : 232448 - 2048) - RAW_BYTES) / STAGE_BYTES;
     static constexpr int RING = STAGES * STAGE_BYTES;
-    static constexpr int BAR_OFFSET = RING;
+    static constexpr int RAW_OFFSET = RING;
+    static constexpr int BAR_OFFSET = RING + RAW_BYTES;
     static constexpr int USED = BAR_OFFSET + (2 * STAGES + 1) * 8 + 16;
     static constexpr int SMEM_BYTES = smem_request(USED + 1024, CTAS);
     static constexpr int ACC = NW * TOK;
     static constexpr int TMEM_COLS = ACC <= 32 ? 32 : ACC <= 64 ? 64 : ACC <= 128 ? 128 : 256;
-    static constexpr int EPI = 8;  // epilogue warps: two for each TMEM lane quadrant
+    // epilogue warps: two for each TMEM lane quadrant, or four where one CTA an SM has
+    // to shift all weights
+    static constexpr int EPI = RAW && CTAS == 1 ? 16 : 8;
+    static constexpr int RAW_ROWS = RAW_ALL / EPI;  // a warp's
     static constexpr int THREADS = 64 + 32 * EPI;
     static constexpr int PREFETCH = 4;  // K steps asked for ahead of the kernel before
     static_assert(STAGES >= 2 && SUM_BYTES <= RING && SMEM_BYTES <= 232448, "shared memory");
@@ -135,6 +155,127 @@ __device__ __forceinline__ void put4(uint16_t *p, int cols, bool vec, const floa
     }
 }
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// 16 bytes from byte `off` (even) of the 32 in lo, hi.
+__device__ __forceinline__ void shift16(const uint4 &lo, const uint4 &hi, uint32_t off,
+                                        uint32_t (&o)[4]) {
+    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    uint32_t a[7], b[5];
+#pragma unroll
+    for (int i = 0; i < 7; ++i) a[i] = off & 4u ? w[i + 1] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) b[i] = off & 8u ? a[i + 2] : a[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = __funnelshift_r(b[i], b[i + 1], (off & 2u) * 8u);
+}
+
+// RAW: each epilogue warp w brings its rows of every K step into the ring.  Rows start on
+// any even byte: the aligned 16-byte chunks that cover a row's part of the tile come
+// by cp.async, RAW_STEPS ahead, into the warp's own buffers (zero beyond the row, so
+// that nothing outside the matrix is read and the reduction's tail is zero), and are
+// shifted from there into the layout that TMA would have written.  A K step moves every
+// address by a multiple of 16 bytes (64 rows, or 64 columns), so a lane's chunks keep
+// their alignment and their place, and are worked out once.
+template <class Cfg>
+__device__ __forceinline__ void raw_weights(const TokensArgs &a, const KernelCtx &ctx,
+                                            uint8_t *smem, uint64_t *full, uint64_t *empty,
+                                            int n0, int kb, int ke, int w, int lane) {
+    constexpr int ROWS = Cfg::RAW_ROWS, CH = Cfg::RAW_CHUNKS, STEPS = Cfg::RAW_STEPS;
+    constexpr int BK = Cfg::BK, STEP_BYTES = ROWS * CH * 16;
+    constexpr int NF = (ROWS * CH + 31) / 32;   // chunks a lane fetches of a step
+    constexpr int RPI = 32 / (CH - 1);          // rows that the warp shifts at a time
+    const uint32_t raw = smem_u32(smem + Cfg::RAW_OFFSET) + w * (STEPS * STEP_BYTES);
+    const long long move = Cfg::W_K ? BK * 2 : BK * 2 * a.w_ld;  // bytes from step to step
+
+    // chunk lane + 32 i: where it starts, and the bytes from there to the row's end
+    const uint8_t *src[NF];
+    int left[NF];
+    auto start = [&](int kt) {
+        const int sg = kt >= a.k_seg ? 1 : 0, k0 = (kt - sg * a.k_seg) * BK;
+#pragma unroll
+        for (int i = 0; i < NF; ++i) {
+            const int c = lane + 32 * i, row = c / CH, r = w * ROWS + row;
+            const bool second = Cfg::W_K ? sg == 1 : r >= BK;
+            const uint16_t *m = second ? a.w[1] : a.w[0];
+            const long long g = Cfg::W_K ? n0 + r : k0 + r % BK;
+            const long long col = Cfg::W_K ? k0 : n0;
+            const long long at = ((g * a.w_ld + col) & ~7ll) + 8 * (c - row * CH);
+            const long long l = (g * a.w_ld + (Cfg::W_K ? a.K : a.N) - at) * 2;
+            const bool in = l > 0 && c < ROWS * CH && (!Cfg::W_K || g < a.N);
+            src[i] = reinterpret_cast<const uint8_t *>(in ? m + at : m);
+            left[i] = !in ? 0 : l < 0x40000000 ? static_cast<int>(l) : 0x40000000;
+        }
+    };
+    auto fetch = [&](int kt) {
+        if (kt < ke) {
+            if (kt == kb || (Cfg::W_K && kt == a.k_seg)) start(kt);
+            const uint32_t to = raw + (kt - kb) % STEPS * STEP_BYTES + lane * 16;
+            const bool tail = !Cfg::W_K && (kt + 1) * static_cast<long long>(BK) > a.K;
+#pragma unroll
+            for (int i = 0; i < NF; ++i) {
+                const int c = lane + 32 * i;
+                int bytes = max(0, min(16, left[i]));
+                if (tail && kt * BK + (w * ROWS + c / CH) % BK >= a.K) bytes = 0;
+                const uint8_t *from =
+                    bytes > 0 ? src[i] : reinterpret_cast<const uint8_t *>(a.w[0]);
+                if (c < ROWS * CH) cp_async16(to + 512 * i, from, bytes);
+                src[i] += move;
+                if (Cfg::W_K) left[i] -= BK * 2;
+            }
+        }
+        cp_async_commit();
+    };
+    // the 16 bytes that lane shifts of every RPI rows: row, chunk, place in the ring
+    const int row = lane / (CH - 1), j = lane % (CH - 1), r = w * ROWS + row;
+    const uint32_t at0 =
+        static_cast<uint32_t>((Cfg::W_K ? n0 + r : r % BK) * a.w_ld) & 7u;  // (n0, k0: 0 mod 8)
+    const uint32_t shift = static_cast<uint32_t>(RPI * a.w_ld) & 7u;
+    // 128-byte rows, chunk j of row r at j ^ (r % 8)
+    const uint32_t ring = Cfg::W_K ? r * 128 + ((j ^ (r & 7)) << 4)
+                                   : r / BK * Cfg::W_SUB + (j >> 3) * (BK * 128) +
+                                         r % BK * 128 + (((j ^ r) & 7) << 4);
+#pragma unroll
+    for (int i = 0; i < STEPS - 1; ++i) fetch(kb + i);
+    int s = 0;
+    uint32_t ph = 0, step = 0;
+    for (int kt = kb; kt < ke; ++kt) {
+        fetch(kt + STEPS - 1);
+        if (!mbar_wait(&empty[s], ph ^ 1u, ctx, kSiteProducerEmpty)) break;
+        cp_async_wait<STEPS - 1>();
+        __syncwarp();
+        const uint32_t from = raw + step * STEP_BYTES + (row * CH + j) * 16;
+        const uint32_t to = smem_u32(smem) + s * Cfg::STAGE_BYTES + ring;
+#pragma unroll
+        for (int i = 0; i < ROWS / RPI; ++i) {
+            const uint4 lo = lds_u4(from + i * RPI * CH * 16);
+            const uint4 hi = lds_u4(from + i * RPI * CH * 16 + 16);
+            uint32_t o[4];
+            shift16(lo, hi, ((at0 + i * shift) & 7u) * 2u, o);
+            sts128((to ^ ((RPI * i & 7) << 4)) + RPI * i * 128, o[0], o[1], o[2], o[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[s]);
+        if (++s == Cfg::STAGES) {
+            s = 0;
+            ph ^= 1u;
+        }
+        if (++step == STEPS) step = 0;
+    }
+    cp_async_wait<0>();
+}
+
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     tokens_kernel(const __grid_constant__ TokensMaps maps, const TokensArgs a,
@@ -157,16 +298,16 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     if (warp == 0 && lane == 0) {
         if (a.k_tiles > 0) {
             prefetch_tmap(&maps.x[0]);
-            prefetch_tmap(&maps.w[0]);
+            if (!Cfg::RAW) prefetch_tmap(&maps.w[0]);
         }
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], Cfg::RAW ? 1 + Cfg::EPI : 1);
             mbar_init(&empty[s], 1);
         }
         mbar_init(done, 1);
         fence_barrier_init();
     }
-    if (warp == 2 && lane == 0) {
+    if (!Cfg::RAW && warp == 2 && lane == 0) {
         for (int kt = kb; kt < min(ke, kb + Cfg::PREFETCH); ++kt)
         {
             const int sg = kt >= a.k_seg ? 1 : 0, k0 = (kt - sg * a.k_seg) * BK;
@@ -199,9 +340,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                 const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
                 if (!mbar_wait(&empty[s], ph ^ 1u, ctx, kSiteProducerEmpty)) break;
                 uint8_t *st = smem + s * Cfg::STAGE_BYTES;
-                mbar_arrive_expect_tx(&full[s], Cfg::STAGE_BYTES);
+                mbar_arrive_expect_tx(&full[s], Cfg::RAW ? Cfg::X_SUB : Cfg::STAGE_BYTES);
                 const int sg = kt >= a.k_seg ? 1 : 0, k0 = (kt - sg * a.k_seg) * BK;
-                if constexpr (Cfg::W_K) {
+                if constexpr (Cfg::RAW) {
+                    // the epilogue's warps bring the weights
+                } else if constexpr (Cfg::W_K) {
                     tma_load_2d(st, &maps.w[sg], &full[s], k0, n0);
                 } else {
 #pragma unroll
@@ -241,6 +384,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
             }
             umma_commit(done);
         }
+    } else if constexpr (Cfg::RAW) {
+        raw_weights<Cfg>(a, ctx, smem, full, empty, n0, kb, ke, static_cast<int>(warp) - 2,
+                         static_cast<int>(lane));
     }
     // Every MMA of this CTA has completed: the ring is free, the sums final.
     // (With an empty K range the commit arrives at once.)
@@ -252,9 +398,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
         const uint32_t q = warp & 3u;
         const int col = static_cast<int>(q * 32 + lane);
         const uint32_t t_row = tmem + ((q * 32u) << 16);
-        // each of a quadrant's two warps every other 16 accumulator columns
+        // a quadrant's warps take 16 accumulator columns in turn
 #pragma unroll 1
-        for (int c = static_cast<int>((warp - 2) >> 2) * 16; c < Cfg::ACC; c += 32) {
+        for (int c = static_cast<int>((warp - 2) >> 2) * 16; c < Cfg::ACC;
+             c += 4 * Cfg::EPI) {
             if (c % TOK >= a.M) continue;  // no tokens there
             uint32_t v[16];
             if (ke > kb && ok) {
@@ -372,13 +519,16 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
 // steps a CTA, and half a step's worth for each doubling of the join.  A wave costs
 // `wave` steps beside its own: its CTAs' set-up, first loads and join.  (Over 84 shapes
 // from 1000 x 512 to 65536 x 2048 and up to 128 tokens that S is 0.9 % slower than the
-// best of the four, 27 % at worst; without the term 11 %, and 1.9 times.)
-constexpr int kWaveSteps = 16;
+// best of the four, 27 % at worst; without the term 11 %, and 1.9 times.  Rows that
+// TMA cannot read take longer a step: 16 would cost 2.7 % there, 12 costs 0.8 %.)
+constexpr int kWaveSteps = 16, kRawWaveSteps = 12;
 
 // Clusters of 1, 2, 4 and 8 CTAs that run at once, `ctas` CTAs an SM.  A cluster stays
 // within one of the GPU's own clusters of 16 to 20 SMs: of eight CTAs with an SM each
-// only 15 fit on 152 SMs.  The other sizes lose one or two, which is not counted: a
-// cluster left over by that costs less than a wave.
+// only 15 fit on 152 SMs (gated 1 x 2033 x 2256, 16 tiles, as one wave of such: 20.5 us,
+// as 4 CTAs a tile 14.4).  The other sizes lose one or two, which is not counted: a
+// cluster left over by that costs less than a wave (37 tiles by eight, two CTAs an SM, 1 x
+// 4619 x 7120: 29.4 us, by four 31.0).
 struct ClusterSlots {
     int n[4];
 };
@@ -411,6 +561,21 @@ bool op_tokens_fit(const OpDevice &dev, int M, long long N, long long K) {
     return n_tiles * S >= dev.sm_count || k_tiles / S <= 32;
 }
 
+// Measured, a call from a graph with the weights read in place / copied first / at a
+// pitch of whole vectors: 1 x 16383 x 2048 20.6 / 33.0 / 13.1 us, 1 x 1001 x 1000 6.4 /
+// 7.6 / 4.3, gated 1 x 8191 x 4096 38 / 64 / 22, 1 x 1001 x 1000 8.8 / 9.9 / 5.3; dX of
+// 1 x 8191 x 4096 22.8 / 31.1 / 13.3, of 1 x 1537 x 512 8.7 / 7.9 / 4.6.  A step takes
+// some 0.5 us more (gated 0.8, W^T 0.35), which few CTAs with many steps feel most.
+double op_raw_us(const OpDevice &dev, int M, long long N, long long K, bool dual,
+                 bool transposed) {
+    const ClusterSlots slots = cluster_slots(dev.sm_count, M <= 64 && !dual ? 2 : 1);
+    const int n_tiles = op_blocks(N, 128), k_tiles = op_blocks(K, 64);
+    const int S = cluster_share(slots, n_tiles, k_tiles, kRawWaveSteps);
+    const int per_wave = slots.n[S == 1 ? 0 : S == 2 ? 1 : S == 4 ? 2 : 3];
+    const double waves = (n_tiles + per_wave - 1) / per_wave;
+    return waves * ((k_tiles + S - 1) / S) * (transposed ? 0.35 : dual ? 0.8 : 0.5);
+}
+
 template <class Cfg>
 static pgemm_status launch_tokens(const OpDevice &dev, TokensArgs a, const OpMat *X,
                                   const OpMat *W, int segments, cudaStream_t s) {
@@ -428,16 +593,19 @@ static pgemm_status launch_tokens(const OpDevice &dev, TokensArgs a, const OpMat
         for (int d = 0; d < segments && st == PGEMM_OK; ++d)
             st = op_encode(&maps.x[d], X[d].p, a.K, a.M, X[d].ld, Cfg::TOK);
         const int matrices = Cfg::DUAL ? 2 : segments;
-        for (int d = 0; d < matrices && st == PGEMM_OK; ++d)
+        for (int d = 0; d < matrices && st == PGEMM_OK && !Cfg::RAW; ++d)
             st = Cfg::W_K ? op_encode(&maps.w[d], W[d].p, a.K, a.N, W[d].ld, 128)
                           : op_encode(&maps.w[d], W[d].p, a.N, a.K, W[d].ld, 64);
     }
     if (st != PGEMM_OK) return st;
+    a.w[0] = W[0].p;
+    a.w[1] = W[Cfg::DUAL || segments == 2 ? 1 : 0].p;
+    a.w_ld = W[0].ld;
     a.k_seg = op_blocks(a.K, Cfg::BK);
     a.k_tiles = a.k_seg * segments;
     const int n_tiles = op_blocks(a.N, Cfg::BN);
     const int S = cluster_share(cluster_slots(dev.sm_count, Cfg::CTAS), n_tiles, a.k_tiles,
-                                kWaveSteps);
+                                Cfg::RAW ? kRawWaveSteps : kWaveSteps);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -457,13 +625,20 @@ static pgemm_status launch_tokens(const OpDevice &dev, TokensArgs a, const OpMat
                : PGEMM_ERR_CUDA;
 }
 
+template <Tok MODE, bool RAW>
+static pgemm_status launch_tokens_rows(const OpDevice &dev, const TokensArgs &a, const OpMat *X,
+                                       const OpMat *W, int segments, cudaStream_t s) {
+    if (a.M <= 16) return launch_tokens<TokCfg<16, MODE, RAW>>(dev, a, X, W, segments, s);
+    if (a.M <= 32) return launch_tokens<TokCfg<32, MODE, RAW>>(dev, a, X, W, segments, s);
+    if (a.M <= 64) return launch_tokens<TokCfg<64, MODE, RAW>>(dev, a, X, W, segments, s);
+    return launch_tokens<TokCfg<128, MODE, RAW>>(dev, a, X, W, segments, s);
+}
+
 template <Tok MODE>
 static pgemm_status launch_tokens_size(const OpDevice &dev, const TokensArgs &a, const OpMat *X,
                                        const OpMat *W, int segments, cudaStream_t s) {
-    if (a.M <= 16) return launch_tokens<TokCfg<16, MODE>>(dev, a, X, W, segments, s);
-    if (a.M <= 32) return launch_tokens<TokCfg<32, MODE>>(dev, a, X, W, segments, s);
-    if (a.M <= 64) return launch_tokens<TokCfg<64, MODE>>(dev, a, X, W, segments, s);
-    return launch_tokens<TokCfg<128, MODE>>(dev, a, X, W, segments, s);
+    return W[0].ld % 8 == 0 ? launch_tokens_rows<MODE, false>(dev, a, X, W, segments, s)
+                            : launch_tokens_rows<MODE, true>(dev, a, X, W, segments, s);
 }
 
 pgemm_status op_tokens_linear(const OpDevice &dev, int M, int N, int K, const OpMat &X,

@@ -255,6 +255,68 @@ def test_gated_backward_of_nothing():
     assert not dX.any()
 
 
+# ------------------------------------- few rows of weights at any pitch ---
+# every alignment of a weight row, tiles that end in a row, short and long K
+ODD_SIZES = [(1, 257, 64), (1, 1001, 700), (3, 130, 65), (16, 139, 200), (17, 517, 136),
+             (33, 263, 1000), (64, 1294, 72), (65, 133, 520), (128, 407, 333), (100, 7, 4100),
+             (128, 20003, 24)]
+
+
+@pytest.mark.parametrize("i,size", list(enumerate(ODD_SIZES)))
+def test_linear_few_rows_odd_pitch(i, size):
+    M, N, K = size
+    X, W, b, R = linear_inputs(M, N, K, 1400 + i)
+    name = ACTS[i % len(ACTS)]
+    Y = nan_like(M, N)
+    pg.linear_bf16(M, N, K, X, W, b, name, R, Y)
+    y, bound, _, _ = ref.linear(X, W, b, name, R)
+    ref.check(Y, y, bound, "Y")
+    dY = rnd(1450 + i, M, N)
+    dX, dW, db = nan_like(M, K), nan_like(K, N), nan_like(N)
+    pg.linear_bf16_backward(M, N, K, X, W, b, name, dY, dX, dW, db)
+    want = ref.linear_backward(X, W, b, name, dY)
+    for key, got in (("dX", dX), ("dW0", dW), ("db", db)):
+        ref.check(got, *want[key], key)
+
+
+@pytest.mark.parametrize("i,size", list(enumerate(ODD_SIZES)))
+def test_gated_few_rows_odd_pitch(i, size):
+    M, F, K = size
+    X, Wg, Wu = gated_inputs(M, F, K, 1500 + i)
+    name = ACTS[i % len(ACTS)]
+    H = nan_like(M, F)
+    pg.gated_bf16(M, F, K, X, Wg, Wu, name, H)
+    h, bound = ref.gated(X, Wg, Wu, name)[:2]
+    ref.check(H, h, bound, "H")
+    dH = rnd(1550 + i, M, F)
+    dX, dWg, dWu = nan_like(M, K), nan_like(K, F), nan_like(K, F)
+    pg.gated_bf16_backward(M, F, K, X, Wg, Wu, name, dH, dX, dWg, dWu)
+    want = ref.gated_backward(X, Wg, Wu, name, dH)
+    for key, got in (("dX", dX), ("dW0", dWg), ("dW1", dWu)):
+        ref.check(got, *want[key], key)
+
+
+@pytest.mark.parametrize("N", [135, 136, 261])
+def test_few_rows_keep_a_nan_in_its_column(N):
+    # the first and last weights of rows lie beside their neighbours' in memory
+    M, K = 5, 150
+    X, W, _, _ = linear_inputs(M, N, K, 1600)
+    dY = rnd(1601, M, N)
+    Y, dX = nan_like(M, N), nan_like(M, K)
+    pg.linear_bf16(M, N, K, X, W, None, "none", None, Y)
+    pg.linear_bf16_backward(M, N, K, X, W, None, "none", dY, dX, None, None)
+    bad = W.clone()
+    bad[70, 0] = math.nan
+    bad[149, N - 1] = math.inf
+    Y2, dX2 = nan_like(M, N), nan_like(M, K)
+    pg.linear_bf16(M, N, K, X, bad, None, "none", None, Y2)
+    pg.linear_bf16_backward(M, N, K, X, bad, None, "none", dY, dX2, None, None)
+    assert Y2[:, 0].isnan().all() and not Y2[:, N - 1].isfinite().any()
+    assert dX2[:, 70].isnan().all() and not dX2[:, 149].isfinite().any()
+    Y2[:, 0], Y2[:, N - 1], dX2[:, 70], dX2[:, 149] = Y[:, 0], Y[:, N - 1], dX[:, 70], dX[:, 149]
+    assert torch.equal(Y, Y2) and torch.equal(dX, dX2)
+
+
 # ----------------------------------------------------------------- xent ---
 def xent_inputs(T, V, D, seed, padded=0.2):
     g = torch.Generator(device="cuda")
