@@ -217,13 +217,15 @@ static pgemm_status gated_forward(int M, int F, int K, const uint16_t *X, const 
     OpDevice dev;
     pgemm_status st = op_device(&dev);
     if (st != PGEMM_OK) return st;
-    const bool tokens = M <= kTokensMax;
+    // (what may decide a ReLU's derivative goes in rounds, op_sign_rounds)
+    const bool tokens =
+        M <= kTokensMax || (!op_sign_rounds(act, K) && op_tokens_gated_fit(dev, M, F, K));
     OpArena arena(dev, s);
     OpRelayout rl;
     OpMat x, wg, wu;
     if (K > 0) {
         rl.add(&x, X, M, K, arena);
-        if (tokens && op_raw_us(dev, M, F, K, true, false) <=
+        if (M <= kTokensMax && op_raw_us(dev, M, F, K, true, false) <=
                           op_relayout_us(2ll * K, F, K % 8 != 0)) {
             wg = OpMat{Wg, F};  // read where they are, whatever their pitch
             wu = OpMat{Wu, F};
@@ -266,13 +268,15 @@ static pgemm_status gated_backward(int M, int F, int K, const uint16_t *X, const
     if (st != PGEMM_OK) return st;
     OpArena arena(dev, s);
     OpRelayout rl;
-    const bool tokens = M <= kTokensMax, x_tokens = op_tokens_fit(dev, M, K, 2ll * F);
+    const bool x_tokens = want_x && op_tokens_fit(dev, M, K, 2ll * F);
+    const bool tokens = M <= kTokensMax || (!preact && !op_sign_rounds(act, K) &&
+                                            op_tokens_gated_fit(dev, M, F, K));
     OpMat x, wg, wu, dg, du;
     long long dg_at = 0, du_at = 0;
     if (some) {
         rl.add(&x, X, M, K, arena);
         // the products of a few rows can read them where they are
-        const bool in_place = (!want_x || x_tokens) && (preact || tokens) &&
+        const bool in_place = M <= kTokensMax && (!want_x || x_tokens) && (preact || tokens) &&
                               (want_x ? op_raw_us(dev, M, K, 2ll * F, false, true) : 0.0) +
                                       (preact ? 0.0 : op_raw_us(dev, M, F, K, true, false)) <=
                                   op_relayout_us(2ll * K, F, K % 8 != 0);

@@ -158,14 +158,17 @@ pgemm_status op_product(const OpDevice &dev, const OpProduct &p, const OpArena &
 pgemm_status op_product_join(const OpDevice &dev, const OpProduct &p, const OpArena &arena,
                              cudaStream_t s);
 
-// The same products of a few rows, bound by reading the weights (op_tokens.cu).
+// The same products of a few rows, bound by reading the weights, and of more rows whose
+// tiles are too few for the GPU (op_tokens.cu).
 constexpr int kTokensMax = 128;
 // Whether a gradient product of M rows (N outputs, K reduction columns) goes that
 // way.  A cluster shares a tile's K among eight CTAs at most, so few columns with a
 // long K leave most SMs idle, where the tiled product takes up to 32 parts (a whole
 // cross-entropy gradient, streaming against tiled dX: 4 tokens x 82768 x 592
 // 117 against 95 us, 16 x 15640 x 520 35 against 39).
+// With more rows: where that is quicker than the tiled product.
 bool op_tokens_fit(const OpDevice &dev, int M, long long N, long long K);
+bool op_tokens_gated_fit(const OpDevice &dev, int M, int F, int K);
 // What weights whose rows TMA cannot read cost those products beyond others (N
 // outputs, K reduction columns), and what copying a matrix to another pitch costs
 // instead (`others`: in a launch that is needed anyway): us, estimates that choose
@@ -192,6 +195,10 @@ pgemm_status op_tokens_gated_grad(const OpDevice &dev, int M, int F, int K, cons
 pgemm_status op_tokens_transposed(const OpDevice &dev, int M, int N, int K, const OpMat *X,
                                   const OpMat *W, int segments, uint16_t *out, cudaStream_t s);
 
+// What a product takes by the estimate that chooses its tiles and parts, us; the same for
+// a gated product (F columns of both).
+double op_product_us(const OpDevice &dev, long long M, long long N, long long K);
+double op_gated_us(const OpDevice &dev, long long M, long long F, long long K);
 // Parts a product of these sizes would be split into (parts_area: M padded to
 // 32 rows, N to 64 columns, one such matrix a part and segment).
 int op_product_parts(const OpDevice &dev, int M, int N, int K, int segments);

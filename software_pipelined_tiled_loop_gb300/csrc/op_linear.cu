@@ -122,7 +122,9 @@ static pgemm_status linear_forward(int M, int N, int K, const uint16_t *X, const
     OpDevice dev;
     pgemm_status st = op_device(&dev);
     if (st != PGEMM_OK) return st;
-    const bool tokens = M <= kTokensMax;
+    // (what may decide a ReLU's derivative goes in rounds, op_sign_rounds)
+    const bool tokens =
+        M <= kTokensMax || (!op_sign_rounds(act, K) && op_tokens_fit(dev, M, N, K));
     OpProduct p;
     p.form = OpForm::NN;
     p.M = M;
@@ -134,7 +136,7 @@ static pgemm_status linear_forward(int M, int N, int K, const uint16_t *X, const
     OpRelayout rl;
     if (K > 0) {
         rl.add(&p.A[0], X, M, K, arena);
-        if (tokens && op_raw_us(dev, M, N, K, false, false) <=
+        if (M <= kTokensMax && op_raw_us(dev, M, N, K, false, false) <=
                           op_relayout_us(K, N, K % 8 != 0))
             p.B[0] = OpMat{W, N};  // read where it is, whatever its pitch
         else
@@ -173,13 +175,15 @@ static pgemm_status linear_backward(int M, int N, int K, const uint16_t *X, cons
 
     OpArena arena(dev, s);
     OpRelayout rl;
-    const bool tokens = M <= kTokensMax, x_tokens = op_tokens_fit(dev, M, K, N);
+    const bool x_tokens = want_x && op_tokens_fit(dev, M, K, N);
+    const bool tokens = M <= kTokensMax || (recompute && !op_sign_rounds(act, K) &&
+                                            op_tokens_fit(dev, M, N, K));
     OpMat x, w, dz;
     if (some && K > 0) {
         if (X && (want_w || recompute)) rl.add(&x, X, M, K, arena);
         // the products of a few rows can read it where it is
         const bool others = ((want_w || recompute) && K % 8 != 0) || act == PGEMM_ACT_NONE;
-        const bool in_place = (!want_x || x_tokens) && (!recompute || tokens) &&
+        const bool in_place = M <= kTokensMax && (!want_x || x_tokens) && (!recompute || tokens) &&
                               (want_x ? op_raw_us(dev, M, K, N, false, true) : 0.0) +
                                       (recompute ? op_raw_us(dev, M, N, K, false, false) : 0.0) <=
                                   op_relayout_us(K, N, others);

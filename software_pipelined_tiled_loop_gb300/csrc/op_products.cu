@@ -185,7 +185,7 @@ static double wave_us(bool pair, long long tiles, int sm_count, long long steps)
 }
 
 static OpPlan plan_product(int sm_count, long long M, long long N, long long K, int segments,
-                           bool split) {
+                           bool split, double *best_time = nullptr) {
     const long long steps = (K + 63) / 64;
     OpPlan best{false, 1};
     double best_us = 1e30;
@@ -204,7 +204,20 @@ static OpPlan plan_product(int sm_count, long long M, long long N, long long K, 
             }
         }
     }
+    if (best_time != nullptr) *best_time = best_us;
     return best;
+}
+
+double op_product_us(const OpDevice &dev, long long M, long long N, long long K) {
+    double us = 0.0;
+    plan_product(dev.sm_count, M, N, K, 1, true, &us);
+    return us;
+}
+double op_gated_us(const OpDevice &dev, long long M, long long F, long long K) {
+    const long long steps = (K + 63) / 64;
+    const double pair = wave_us(true, ((M + 255) / 256) * ((F + 127) / 128), dev.sm_count, steps);
+    const double one = wave_us(false, ((M + 127) / 128) * ((F + 63) / 64), dev.sm_count, steps);
+    return pair < one ? pair : one;
 }
 
 bool op_use_pair(const OpDevice &dev, long long M, long long N, long long K, long long pair_n,

@@ -1,4 +1,5 @@
-// Products of a few rows (up to 128 tokens, of a decoding step or a small batch):
+// Products of a few rows (up to 128 tokens, of a decoding step or a small batch; more
+// where there are too few tiles for the GPU otherwise, tokens_beat):
 // Y = act(X W + b) + R, H = act(X Wg) * (X Wu), what their backward passes
 // recompute, and dX = dZ W^T; all bound by streaming the weights once.
 //
@@ -292,6 +293,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(S));
     const uint32_t rank = S > 1 ? cluster_ctarank() : 0u;
     const int n0 = static_cast<int>(blockIdx.x / S) * BN;
+    const int m0 = static_cast<int>(blockIdx.y) * TOK, rows = min(TOK, a.M - m0);
     const int kb = static_cast<int>(static_cast<long long>(rank) * a.k_tiles / S);
     const int ke = static_cast<int>(static_cast<long long>(rank + 1) * a.k_tiles / S);
 
@@ -354,7 +356,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                             tma_load_2d(st + d * Cfg::W_SUB + j * (BK * 128), &maps.w[d], &full[s],
                                         n0 + 64 * j, k0);
                 }
-                tma_load_2d(st + Cfg::NW * Cfg::W_SUB, &maps.x[sg], &full[s], k0, 0);
+                tma_load_2d(st + Cfg::NW * Cfg::W_SUB, &maps.x[sg], &full[s], k0, m0);
             }
         }
     } else if (warp == 1) {
@@ -402,7 +404,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
 #pragma unroll 1
         for (int c = static_cast<int>((warp - 2) >> 2) * 16; c < Cfg::ACC;
              c += 4 * Cfg::EPI) {
-            if (c % TOK >= a.M) continue;  // no tokens there
+            if (c % TOK >= rows) continue;  // no tokens there
             uint32_t v[16];
             if (ke > kb && ok) {
                 tmem_ld_32x32b_x16(t_row + c, v);
@@ -429,9 +431,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
         if (cols > 0) {
             float b[4] = {0.f, 0.f, 0.f, 0.f};
             if (a.bias) get4(a.bias + n, cols, vec, b);
-            for (int t = static_cast<int>(rank + S * (warp - 2)); t < a.M;
+            for (int t = static_cast<int>(rank + S * (warp - 2)); t < rows;
                  t += static_cast<int>(S) * Cfg::EPI) {
-                const long long at = static_cast<long long>(t) * a.N + n;
+                const long long at = static_cast<long long>(m0 + t) * a.N + n;
                 float r[4] = {0.f, 0.f, 0.f, 0.f};
                 if (a.residual) get4(a.residual + at, cols, vec, r);
                 if (Cfg::GRAD) get4(a.dy + at, cols, vec, r);
@@ -495,7 +497,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                         }
                     }
                 });
-                const long long to = static_cast<long long>(t) * a.ldo + n;
+                const long long to = static_cast<long long>(m0 + t) * a.ldo + n;
                 put4(a.out + to, cols, vec_out, y);
                 if constexpr (Cfg::MODE == Tok::GATED_GRAD) put4(a.out2 + to, cols, vec_out, y2);
             }
@@ -553,12 +555,37 @@ static int cluster_share(const ClusterSlots &slots, int n_tiles, int k_tiles, in
     return best;
 }
 
+// More than 128 rows: tiles of 128 x 128 whose K a cluster shares, which saves the tiled
+// product's parts and the kernel that joins them, while one wave holds them all.  Times
+// fitted to 112 shapes of 136 to 1024 rows (us, one CTA an SM and two); a call from a
+// graph by this and by tiles: 136 x 520 x 2736 7.6 / 10.4, 512 x 2048 x 2736 12.6 / 16.2,
+// 300 x 520 x 1024 7.0 / 9.5; gated, whose tiles have no parts, 136 x 520 x 8192 15.5 /
+// 34.2, 512 x 520 x 2736 13.1 / 15.0.
+static bool tokens_beat(const OpDevice &dev, int M, long long N, long long K, int ctas, double us0,
+                        double step0, double us1, double step1, double tiled_us) {
+    const long long tiles = static_cast<long long>(op_blocks(M, 128)) * op_blocks(N, 128);
+    if (tiles > ctas * dev.sm_count) return false;
+    const int k_tiles = op_blocks(K, 64);
+    const ClusterSlots slots = cluster_slots(dev.sm_count, ctas);
+    const int S = cluster_share(slots, static_cast<int>(tiles), k_tiles, kWaveSteps);
+    if (tiles > slots.n[S == 1 ? 0 : S == 2 ? 1 : S == 4 ? 2 : 3]) return false;
+    const int steps = (k_tiles + S - 1) / S;
+    const double us = tiles * S <= dev.sm_count ? us0 + step0 * steps : us1 + step1 * steps;
+    return us < 0.93 * tiled_us;
+}
+
 bool op_tokens_fit(const OpDevice &dev, int M, long long N, long long K) {
-    if (M > kTokensMax) return false;
+    if (M > kTokensMax)
+        return tokens_beat(dev, M, N, K, 2, 5.7, 0.32, 8.5, 0.47, op_product_us(dev, M, N, K));
     const int n_tiles = op_blocks(N, 128);
     const int k_tiles = op_blocks(K, 64);
     const int S = cluster_share(cluster_slots(dev.sm_count, 2), n_tiles, k_tiles, kWaveSteps);
     return n_tiles * S >= dev.sm_count || k_tiles / S <= 32;
+}
+
+bool op_tokens_gated_fit(const OpDevice &dev, int M, int F, int K) {
+    if (M <= kTokensMax) return true;
+    return tokens_beat(dev, M, F, K, 1, 8.8, 0.48, 8.8, 0.48, op_gated_us(dev, M, F, K));
 }
 
 // Measured, a call from a graph with the weights read in place / copied first / at a
@@ -604,7 +631,8 @@ static pgemm_status launch_tokens(const OpDevice &dev, TokensArgs a, const OpMat
     a.k_seg = op_blocks(a.K, Cfg::BK);
     a.k_tiles = a.k_seg * segments;
     const int n_tiles = op_blocks(a.N, Cfg::BN);
-    const int S = cluster_share(cluster_slots(dev.sm_count, Cfg::CTAS), n_tiles, a.k_tiles,
+    const int m_tiles = op_blocks(a.M, Cfg::TOK);
+    const int S = cluster_share(cluster_slots(dev.sm_count, Cfg::CTAS), n_tiles * m_tiles, a.k_tiles,
                                 Cfg::RAW ? kRawWaveSteps : kWaveSteps);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -614,7 +642,7 @@ static pgemm_status launch_tokens(const OpDevice &dev, TokensArgs a, const OpMat
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t lc{};
-    lc.gridDim = dim3(static_cast<unsigned>(n_tiles) * S);
+    lc.gridDim = dim3(static_cast<unsigned>(n_tiles) * S, static_cast<unsigned>(m_tiles));
     lc.blockDim = dim3(Cfg::THREADS);
     lc.dynamicSmemBytes = Cfg::SMEM_BYTES;
     lc.stream = s;

@@ -317,6 +317,56 @@ def test_few_rows_keep_a_nan_in_its_column(N):
     assert torch.equal(Y, Y2) and torch.equal(dX, dX2)
 
 
+# --------------------------- few tiles of many rows share their K in clusters ---
+SHARED_SIZES = [(129, 520, 1100), (136, 40, 4100), (200, 1368, 2736), (300, 130, 1024),
+                (257, 517, 1048), (513, 264, 1500), (777, 136, 3001), (1030, 130, 2050)]
+
+
+@pytest.mark.parametrize("act", [0, 2])
+@pytest.mark.parametrize("i,size", list(enumerate(SHARED_SIZES)))
+def test_linear_few_tiles(i, size, act):
+    M, N, K = size
+    X, W, b, R = linear_inputs(M, N, K, 1700 + i)
+    name = ACTS[(i + act) % len(ACTS)]
+    Y, Z = nan_like(M, N), nan_like(M, N, dtype=torch.float32)
+    pg.linear_bf16(M, N, K, X, W, b, name, R, Y, preact=Z)
+    y, bound, z, ez = ref.linear(X, W, b, name, R)
+    ref.check(Y, y, bound, "Y")
+    ref.check(Z, z, ez + 1e-30, "preact")
+    dY = rnd(1750 + i, M, N)
+    want = ref.linear_backward(X, W, b, name, dY)
+    for kept in (None, Z):
+        dX, dW, db = nan_like(M, K), nan_like(K, N), nan_like(N)
+        pg.linear_bf16_backward(M, N, K, X, W, b, name, dY, dX, dW, db, preact=kept)
+        for key, got in (("dX", dX), ("dW0", dW), ("db", db)):
+            ref.check(got, *want[key], key)
+    # the reduction the other way round: M x K outputs from N columns
+    X, W, b, _ = linear_inputs(M, K, N, 1780 + i)
+    dY, dX = rnd(1790 + i, M, K), nan_like(M, N)
+    pg.linear_bf16_backward(M, K, N, X, W, b, "silu", dY, dX, None, None)
+    ref.check(dX, *ref.linear_backward(X, W, b, "silu", dY)["dX"], "dX of many columns")
+
+
+@pytest.mark.parametrize("i,size", list(enumerate(SHARED_SIZES)))
+def test_gated_few_tiles(i, size):
+    M, F, K = size
+    X, Wg, Wu = gated_inputs(M, F, K, 1800 + i)
+    name = ACTS[(i + 2) % len(ACTS)]
+    H, Z = nan_like(M, F), nan_like(2, M, F, dtype=torch.float32)
+    pg.gated_bf16(M, F, K, X, Wg, Wu, name, H, preact=Z)
+    h, bound, g, u, eg, eu, _, _ = ref.gated(X, Wg, Wu, name)
+    ref.check(H, h, bound, "H")
+    ref.check(Z[0], g, eg + 1e-30, "X Wg")
+    ref.check(Z[1], u, eu + 1e-30, "X Wu")
+    dH = rnd(1850 + i, M, F)
+    want = ref.gated_backward(X, Wg, Wu, name, dH)
+    for kept in (None, Z):
+        dX, dWg, dWu = nan_like(M, K), nan_like(K, F), nan_like(K, F)
+        pg.gated_bf16_backward(M, F, K, X, Wg, Wu, name, dH, dX, dWg, dWu, preact=kept)
+        for key, got in (("dX", dX), ("dW0", dWg), ("dW1", dWu)):
+            ref.check(got, *want[key], key)
+
+
 # ----------------------------------------------------------------- xent ---
 def xent_inputs(T, V, D, seed, padded=0.2):
     g = torch.Generator(device="cuda")
@@ -330,7 +380,8 @@ def xent_inputs(T, V, D, seed, padded=0.2):
 # one token of one; odd vocabularies; tails below and above a tile; pairs
 XENT_SIZES = [(1, 1, 8), (1, 3, 1), (1, 1000, 64), (5, 129, 33), (33, 257, 40), (64, 4096, 64),
               (130, 1001, 72), (257, 515, 136), (3, 7, 0), (1100, 9000, 64), (2, 50257, 24),
-              (65, 1001, 648), (1, 129, 1100), (40, 3000, 2500), (1100, 9001, 704)]
+              (65, 1001, 648), (1, 129, 1100), (40, 3000, 2500), (1100, 9001, 704),
+              (200, 12001, 264)]
 
 
 @pytest.mark.parametrize("i,size", list(enumerate(XENT_SIZES)))
