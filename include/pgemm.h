@@ -302,7 +302,8 @@ PGEMM_API pgemm_status xent_bf16(int T, int V, int D, const uint16_t *X, const u
  * T <= 64 the logits and P, 6 T V bytes (0: the library's choice, 2 GiB); more
  * than that goes by in pieces of the vocabulary, whose logits are computed a
  * second time.  Results under different bounds agree to the rounding of fp32
- * sums and of P. */
+ * sums, of P, and of the fp16 exponentials that P comes from when all of it
+ * fits and T > 64. */
 PGEMM_API pgemm_status xent_bf16_grad(int T, int V, int D, const uint16_t *X, const uint16_t *W,
                                       const int64_t *target, const float *dloss, float *loss,
                                       float *lse, uint16_t *dX, uint16_t *dW,
