@@ -189,7 +189,7 @@ static pgemm_status linear_backward(int M, int N, int K, const uint16_t *X, cons
                                   op_relayout_us(K, N, others);
         if (in_place)
             w = OpMat{W, N};
-        else
+        else if (want_x || recompute)  // (else W may be absent)
             rl.add(&w, W, K, N, arena);
     }
     const bool own_dz = some && act != PGEMM_ACT_NONE;  // dZ is not dY itself
