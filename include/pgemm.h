@@ -258,8 +258,9 @@ PGEMM_API pgemm_status linear_bf16(int M, int N, int K, const uint16_t *X, const
  * dZ = dY * act'(Z) (rounded to bf16, as the products' operand),
  * dX (M x K) <- dZ W^T, dW (K x N) <- X^T dZ, dbias (N) <- column sums of dZ.
  * Any of the three may be NULL: not computed.  preact: what linear_bf16 kept,
- * or NULL: Z is computed again (act NONE needs neither).  The residual's
- * gradient is dY. */
+ * or NULL: Z is computed again (act NONE needs neither).  X is read only for dW
+ * and W only for dX, and both to compute Z again; what is not read may be NULL.
+ * The residual's gradient is dY. */
 PGEMM_API pgemm_status linear_bf16_backward(int M, int N, int K, const uint16_t *X,
                                             const uint16_t *W, const uint16_t *bias, int act,
                                             const uint16_t *dY, const float *preact, uint16_t *dX,
@@ -276,7 +277,9 @@ PGEMM_API pgemm_status gated_bf16(int M, int F, int K, const uint16_t *X, const 
  * dG = dH * U * act'(G) and dU = dH * act(G) (each rounded to bf16, as the
  * products' operands), dX (M x K) <- dG Wg^T + dU Wu^T, dWg and dWu (K x F)
  * <- X^T dG, X^T dU.  dX, or dWg and dWu together, may be NULL.  preact: what
- * gated_bf16 kept, or NULL: G and U are computed again. */
+ * gated_bf16 kept, or NULL: G and U are computed again.  X is read only for dWg
+ * and dWu, Wg and Wu only for dX, and all three to compute G and U again; what is
+ * not read may be NULL. */
 PGEMM_API pgemm_status gated_bf16_backward(int M, int F, int K, const uint16_t *X,
                                            const uint16_t *Wg, const uint16_t *Wu, int act,
                                            const uint16_t *dH, const float *preact, uint16_t *dX,

@@ -293,8 +293,9 @@ def linear_bf16(M, N, K, X, W, bias, act, residual, Y, preact=None, stream=None)
 
 def linear_bf16_backward(M, N, K, X, W, bias, act, dY, dX, dW, dbias, preact=None, stream=None):
     """Gradients of linear_bf16 for dY (M x N) into dX (M x K), dW (K x N) and
-    dbias (N), each skipped when None.  ``preact``: what the forward call kept,
-    or None to compute it again.  Asynchronous."""
+    dbias (N), each skipped when None; X and W may be None where nothing wanted
+    reads them.  ``preact``: what the forward call kept, or None to compute it
+    again.  Asynchronous."""
     if M | N | K > _DIM_MAX:
         _too_large("linear_bf16_backward")
     _check(lib().linear_bf16_backward(
@@ -319,8 +320,9 @@ def gated_bf16(M, F, K, X, Wg, Wu, act, H, preact=None, stream=None):
 
 def gated_bf16_backward(M, F, K, X, Wg, Wu, act, dH, dX, dWg, dWu, preact=None, stream=None):
     """Gradients of gated_bf16 for dH (M x F) into dX (M x K), dWg and dWu
-    (K x F); dX, or dWg and dWu together, may be None.  ``preact``: what the
-    forward call kept, or None to compute it again.  Asynchronous."""
+    (K x F); dX, or dWg and dWu together, may be None, and so may X, Wg and Wu
+    where nothing wanted reads them.  ``preact``: what the forward call kept, or
+    None to compute it again.  Asynchronous."""
     if M | F | K > _DIM_MAX:
         _too_large("gated_bf16_backward")
     _check(lib().gated_bf16_backward(

@@ -259,7 +259,10 @@ static pgemm_status gated_backward(int M, int F, int K, const uint16_t *X, const
     const bool want_x = dX && M > 0 && K > 0, want_w = dWg && K > 0 && F > 0;
     if (!want_x && !want_w) return PGEMM_OK;  // K > 0 from here on
     const bool some = M > 0 && F > 0;
-    if (some && (!dH || !Wg || !Wu || !X)) return PGEMM_ERR_INVALID_VALUE;
+    // what some kernel of this call reads; the rest may be absent
+    const bool need_x = want_w || !preact, need_w = want_x || !preact;
+    if (some && (!dH || (need_x && !X) || (need_w && (!Wg || !Wu))))
+        return PGEMM_ERR_INVALID_VALUE;
     if (!op_aligned16(X) || !op_aligned16(Wg) || !op_aligned16(Wu) || !op_aligned16(dH) ||
         !op_aligned16(preact) || !op_aligned16(dX) || !op_aligned16(dWg) || !op_aligned16(dWu))
         return PGEMM_ERR_MISALIGNED;
@@ -274,7 +277,7 @@ static pgemm_status gated_backward(int M, int F, int K, const uint16_t *X, const
     OpMat x, wg, wu, dg, du;
     long long dg_at = 0, du_at = 0;
     if (some) {
-        rl.add(&x, X, M, K, arena);
+        if (need_x) rl.add(&x, X, M, K, arena);
         // the products of a few rows can read them where they are
         const bool in_place = M <= kTokensMax && (!want_x || x_tokens) && (preact || tokens) &&
                               (want_x ? op_raw_us(dev, M, K, 2ll * F, false, true) : 0.0) +
@@ -283,7 +286,7 @@ static pgemm_status gated_backward(int M, int F, int K, const uint16_t *X, const
         if (in_place) {
             wg = OpMat{Wg, F};
             wu = OpMat{Wu, F};
-        } else {
+        } else if (need_w) {
             rl.add(&wg, Wg, K, F, arena);
             rl.add(&wu, Wu, K, F, arena);
         }

@@ -197,7 +197,7 @@ static pgemm_status linear_backward(int M, int N, int K, const uint16_t *X, cons
     if (own_dz) {
         dz.ld = op_round_up(N, 64);
         dz_at = arena.add(dz.ld * M * 2);
-    } else if (some) {
+    } else if (some && (want_x || want_w)) {  // (the column sums read dY itself)
         rl.add(&dz, dY, M, N, arena);
     }
     OpProduct px, pw;

@@ -52,3 +52,18 @@ def test_linear_weight_gradients_without_weights(M, N, name):
     ref.check(dW, *want["dW0"], "dW")
     ref.check(db, *want["db"], "db")
     assert torch.equal(db, db2)
+
+
+@pytest.mark.parametrize("M", [3, 200])
+@pytest.mark.parametrize("F,K", [(261, 72), (264, 77)])
+def test_gated_gradients_without_what_they_do_not_read(M, F, K):
+    X, Wg, Wu, dH = (rnd(11, M, K), rnd(12, K, F, std=K ** -0.5), rnd(13, K, F, std=K ** -0.5),
+                     rnd(14, M, F))
+    Z = nan_like(2, M, F, dtype=torch.float32)
+    pg.gated_bf16(M, F, K, X, Wg, Wu, "silu", nan_like(M, F), preact=Z)
+    want = ref.gated_backward(X, Wg, Wu, "silu", dH)
+    dX, dWg, dWu = nan_like(M, K), nan_like(K, F), nan_like(K, F)
+    pg.gated_bf16_backward(M, F, K, None, Wg, Wu, "silu", dH, dX, None, None, preact=Z)
+    pg.gated_bf16_backward(M, F, K, X, None, None, "silu", dH, None, dWg, dWu, preact=Z)
+    for key, got in (("dX", dX), ("dW0", dWg), ("dW1", dWu)):
+        ref.check(got, *want[key], key)
