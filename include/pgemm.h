@@ -304,7 +304,8 @@ PGEMM_API pgemm_status xent_bf16(int T, int V, int D, const uint16_t *X, const u
  * workspace_bytes bounds the scratch that holds P, 2 T V bytes, or with
  * T <= 64 the logits and P, 6 T V bytes (0: the library's choice, 2 GiB); more
  * than that goes by in pieces of the vocabulary, whose logits are computed a
- * second time.  Results under different bounds agree to the rounding of fp32
+ * second time.  Then as much again holds fp32 partial sums of dX, T D values each,
+ * at least a running sum and what one piece's product leaves.  Results under different bounds agree to the rounding of fp32
  * sums, of P, and of the fp16 exponentials that P comes from when all of it
  * fits and T > 64. */
 PGEMM_API pgemm_status xent_bf16_grad(int T, int V, int D, const uint16_t *X, const uint16_t *W,

@@ -208,6 +208,9 @@ long long op_parts_rows(int M);
 pgemm_status op_join_parts(const OpDevice &dev, const float *area, int parts, int segments, int M,
                            int N, uint16_t *const out[2], const OpEpilogue &epi,
                            cudaStream_t s);
+// The first of `parts` such matrices <- their sum, in order.
+pgemm_status op_fold_parts(const OpDevice &dev, float *area, int parts, int M, int N,
+                           cudaStream_t s);
 
 // The larger tile on a CTA pair (256 x pair_n outputs), or one CTA's (128 x
 // one_n): whichever needs less time for an M x N x K product (op_products.cu).

@@ -487,6 +487,43 @@ pgemm_status op_join_parts(const OpDevice &dev, const float *area, int parts, in
                         dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(256), s, p);
 }
 
+// Adds in the order that join_parts_kernel does, so that folding some parts before
+// the rest are joined changes no bit.  Memory-bound: a running sum of 4096 x 4096 and
+// one more such matrix take 24 us among a piece's products (201 MB, some of it in L2).
+__global__ void __launch_bounds__(256)
+    fold_parts_kernel(float4 *area, int parts, long long step, long long total) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    constexpr int AHEAD = 4;
+    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < parts; k += AHEAD) {
+            float4 x[AHEAD];
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j)
+                x[j] = k + j < parts ? __ldcs(area + (k + j) * step + i)
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) {
+                v.x += x[j].x;
+                v.y += x[j].y;
+                v.z += x[j].z;
+                v.w += x[j].w;
+            }
+        }
+        area[i] = v;
+    }
+}
+
+pgemm_status op_fold_parts(const OpDevice &dev, float *area, int parts, int M, int N,
+                           cudaStream_t s) {
+    const long long total = op_parts_ld(N) / 4 * M;
+    const long long blocks = (total + 255) / 256, most = dev.sm_count * 8ll;
+    return launch_small(fold_parts_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)),
+                        dim3(256), s, reinterpret_cast<float4 *>(area), parts,
+                        op_parts_ld(N) / 4 * op_parts_rows(M), total);
+}
+
 // --------------------------------------------------- activation gradient ---
 // dZ = dY * act'(Z) (linear), dG = dH * U * act'(G) and dU = dH * act(G)
 // (gated), elementwise in fp32 from the kept fp32 pre-activations, rounded to

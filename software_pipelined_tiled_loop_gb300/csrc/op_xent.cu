@@ -32,6 +32,8 @@
 #include <cuda_fp16.h>
 #include <math_constants.h>
 
+#include <algorithm>
+
 #include "op_gemm.cuh"
 #include "op_host.h"
 
@@ -755,8 +757,8 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
     const long long p_ld_all = op_round_up(V, 256);
     long long piece = 0;
     int pieces = 0;
+    const long long cap = workspace > 0 ? workspace : kDefaultWorkspace;
     if (want_x || want_w) {
-        const long long cap = workspace > 0 ? workspace : kDefaultWorkspace;
         // bytes an entry: P, and with few tokens its fp32 logits
         piece = cap / ((few ? 6ll : 2ll) * T) / 256 * 256;
         if (piece < 256) piece = 256;
@@ -782,15 +784,24 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
     const long long at_p = pieces ? arena.add(piece * T * 2) : 0;
     const bool keep_logits = few && pieces == 1;
     const long long at_z = keep_logits ? arena.add(piece * T * 4) : 0;
+    // dX of several pieces: fp32 partial sums, T x D each.  As many as the workspace
+    // holds again, at least a running sum and one piece's parts; when they are full the
+    // running sum takes them in (sums over more pieces in less memory).
     long long at_x = 0;
-    int x_parts = 0;
+    int x_slots = 0;
+    const long long x_slot = op_parts_ld(D) * op_parts_rows(T);
     const bool x_pieces = want_x && pieces > 1;
     if (x_pieces) {
+        long long all = 0, most = 0;
         for (int i = 0; i < pieces; ++i) {
             const long long cols = V - i * piece < piece ? V - i * piece : piece;
-            x_parts += op_product_parts(dev, T, D, static_cast<int>(cols), 1);
+            const int parts = op_product_parts(dev, T, D, static_cast<int>(cols), 1);
+            all += parts;
+            most = parts > most ? parts : most;
         }
-        at_x = arena.add(op_parts_ld(D) * op_parts_rows(T) * 4 * x_parts);
+        const long long fit = cap / (x_slot * 4), least = 1 + most;
+        x_slots = static_cast<int>(std::min(all, std::max(least, fit)));
+        at_x = arena.add(x_slot * 4 * x_slots);
     }
     // the products of a piece, planned for the first (the widest): the others'
     // parts need no more room
@@ -892,9 +903,13 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
             px.A[0] = OpMat{P, piece};
             px.B[0] = OpMat{w.p + v0 * w.ld, w.ld};
             if (x_pieces) {
-                px.parts_area = arena.at<float>(at_x) +
-                                op_parts_ld(D) * op_parts_rows(T) * static_cast<long long>(x_done);
+                float *sums = px.parts_area = arena.at<float>(at_x);
                 op_product_plan(dev, px, arena);  // this piece's; reserves nothing
+                if (x_done + px.plan.parts > x_slots) {
+                    if ((st = op_fold_parts(dev, sums, x_done, T, D, s)) != PGEMM_OK) return st;
+                    x_done = 1;
+                }
+                px.parts_area = sums + x_slot * x_done;
                 x_done += px.plan.parts;
             }
             st = x_tokens ? op_tokens_linear(dev, T, D, cols, px.A[0], px.B[0], px.epi, dX, s)
@@ -915,7 +930,7 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
         uint16_t *out[2] = {dX, nullptr};
         OpEpilogue scaled;
         scaled.scale = scale;
-        st = op_join_parts(dev, arena.at<float>(at_x), x_parts, 1, T, D, out, scaled, s);
+        st = op_join_parts(dev, arena.at<float>(at_x), x_done, 1, T, D, out, scaled, s);
     }
     return st;
 }

@@ -67,3 +67,44 @@ def test_gated_gradients_without_what_they_do_not_read(M, F, K):
     pg.gated_bf16_backward(M, F, K, X, None, None, "silu", dH, None, dWg, dWu, preact=Z)
     for key, got in (("dX", dX), ("dW0", dWg), ("dW1", dWu)):
         ref.check(got, *want[key], key)
+
+
+# ------------------------------------------------------- cross entropy's scratch ---
+def scratch_of(call):
+    """Bytes that the library's pool holds after a call that found it empty."""
+    torch.cuda.synchronize()
+    pg.pgemm_trim_scratch()
+    before = torch.cuda.mem_get_info()[0]
+    call()
+    torch.cuda.synchronize()
+    return before - torch.cuda.mem_get_info()[0]
+
+
+def test_xent_small_workspace_takes_little_scratch():
+    # 256 pieces of the vocabulary: the statistics' 4 MB, P of one piece, a running sum
+    # of dX and one piece's (8 MB each), dW's parts (4 MB at most); the pool grows by
+    # blocks of some 32 MB.  A sum kept for every piece would be 2 GB.
+    T, V, D = 1024, 65536, 2048
+    X, W, dl = rnd(21, T, D), rnd(22, V, D, std=2 * D ** -0.5), torch.rand(T, device="cuda")
+    y = torch.randint(0, V, (T,), device="cuda")
+    dX, dW = nan_like(T, D), nan_like(V, D)
+    pg.xent_bf16_grad(T, V, D, X, W, y, dl, None, None, dX, dW)  # (code and tables loaded)
+    took = {ws: scratch_of(lambda: pg.xent_bf16_grad(T, V, D, X, W, y, dl, None, None, dX, dW,
+                                                     workspace_bytes=ws)) for ws in (0, 1)}
+    assert took[1] < 128 << 20 and took[1] < took[0], took
+    want = ref.xent(X, W, y, dl)
+    ref.check(dX, *want["dX"], "dX")
+    ref.check(dW, *want["dW"], "dW")
+
+
+@pytest.mark.parametrize("workspace", [1 << 20, 3 << 20, 16 << 20])
+def test_xent_sums_of_dx_taken_in_now_and_then(workspace):
+    # room for 2, 6 and 32 partial sums of dX (512 KB each) beside 16, 5 and 1 pieces
+    T, V, D = 256, 30001, 512
+    X, W, dl = rnd(23, T, D), rnd(24, V, D, std=2 * D ** -0.5), torch.rand(T, device="cuda")
+    y = torch.randint(0, V, (T,), device="cuda")
+    dX, dW = nan_like(T, D), nan_like(V, D)
+    pg.xent_bf16_grad(T, V, D, X, W, y, dl, None, None, dX, dW, workspace_bytes=workspace)
+    want = ref.xent(X, W, y, dl)
+    ref.check(dX, *want["dX"], "dX")
+    ref.check(dW, *want["dW"], "dW")
