@@ -794,7 +794,8 @@ __device__ __forceinline__ bool acc_sum_unit(Acc &acc, int col0, int cols, float
 // tensor core truncates its running sum every 16 products, toward zero: a chain
 // of K = 8192 ends 4e-6 of itself short, an fp32 sum with rounding 1e-6.  Rounds of
 // 512 products added in registers end at 5e-7.  So products whose Z decides a
-// ReLU run in rounds when K is longer than one; smooth activations do not need it.
+// ReLU run in rounds when K is longer than one (of few rows: a CTA's share of K);
+// smooth activations do not need it.
 constexpr int kSignRound = 512;
 inline bool op_sign_rounds(int act, int K) { return act == PGEMM_ACT_RELU && K > kSignRound; }
 using SignPair = std::integral_constant<int, kSignRound / 128>;  // K-tiles a round

@@ -67,10 +67,15 @@ enum class Tok {
 
 // TOK: tokens of the MMA's N side.  DUAL: two weight matrices (gated), whose
 // accumulators lie side by side in tensor memory.  RAW: weights whose rows are not
-// multiples of 16 bytes, which TMA cannot read (raw_weights).
-template <int TOK_, Tok MODE_, bool RAW_ = false>
+// multiples of 16 bytes, which TMA cannot read (raw_weights).  ROUND: K steps of an
+// accumulation round (0: a CTA's whole share), whose sums the epilogue warps add in
+// fp32 registers while the next round fills a second accumulator; for a Z that decides
+// a ReLU (op_sign_rounds).  Hidden behind the weights' loads: 64 x 20000 x 8192 with Z
+// kept 60.3 us, 59.8 as one chain.
+template <int TOK_, Tok MODE_, bool RAW_ = false, int ROUND_ = 0>
 struct TokCfg {
     static constexpr bool RAW = RAW_;
+    static constexpr int ROUND = ROUND_;
     static constexpr int TOK = TOK_, BN = 128, BK = 64;
     static constexpr Tok MODE = MODE_;
     static constexpr bool DUAL = MODE == Tok::GATED || MODE == Tok::GATED_GRAD;
@@ -97,18 +102,25 @@ struct TokCfg {
     static constexpr int RING = STAGES * STAGE_BYTES;
     static constexpr int RAW_OFFSET = RING;
     static constexpr int BAR_OFFSET = RING + RAW_BYTES;
-    static constexpr int USED = BAR_OFFSET + (2 * STAGES + 1) * 8 + 16;
+    static constexpr int USED = BAR_OFFSET + (2 * STAGES + (ROUND > 0 ? 5 : 1)) * 8 + 16;
     static constexpr int SMEM_BYTES = smem_request(USED + 1024, CTAS);
     static constexpr int ACC = NW * TOK;
-    static constexpr int TMEM_COLS = ACC <= 32 ? 32 : ACC <= 64 ? 64 : ACC <= 128 ? 128 : 256;
+    static constexpr int ACCS = ACC * (ROUND > 0 ? 2 : 1);  // of two CTAs: 512 columns at most
+    static constexpr int TMEM_COLS = ACCS <= 32    ? 32
+                                     : ACCS <= 64  ? 64
+                                     : ACCS <= 128 ? 128
+                                     : ACCS <= 256 ? 256
+                                                   : 512;
     // epilogue warps: two for each TMEM lane quadrant, or four where one CTA an SM has
-    // to shift all weights
-    static constexpr int EPI = RAW && CTAS == 1 ? 16 : 8;
+    // to shift all weights, or to hold 256 columns of sums
+    static constexpr int EPI = (RAW || ROUND > 0) && CTAS == 1 ? 16 : 8;
+    static constexpr int CHUNKS = (ACC + 4 * EPI - 1) / (4 * EPI);  // 16 columns, a warp's
     static constexpr int RAW_ROWS = RAW_ALL / EPI;  // a warp's
     static constexpr int THREADS = 64 + 32 * EPI;
     static constexpr int PREFETCH = 4;  // K steps asked for ahead of the kernel before
     static_assert(STAGES >= 2 && SUM_BYTES <= RING && SMEM_BYTES <= 232448, "shared memory");
     static_assert(TOK % 16 == 0 && TOK <= 128, "TOK");
+    static_assert(TMEM_COLS * CTAS <= 512, "accumulators");
 };
 
 __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
@@ -188,10 +200,12 @@ __device__ __forceinline__ void shift16(const uint4 &lo, const uint4 &hi, uint32
 // shifted from there into the layout that TMA would have written.  A K step moves every
 // address by a multiple of 16 bytes (64 rows, or 64 columns), so a lane's chunks keep
 // their alignment and their place, and are worked out once.
-template <class Cfg>
+// after(i) is called when step i of the share has been handed over.
+template <class Cfg, class After>
 __device__ __forceinline__ void raw_weights(const TokensArgs &a, const KernelCtx &ctx,
                                             uint8_t *smem, uint64_t *full, uint64_t *empty,
-                                            int n0, int kb, int ke, int w, int lane) {
+                                            int n0, int kb, int ke, int w, int lane,
+                                            After &&after) {
     constexpr int ROWS = Cfg::RAW_ROWS, CH = Cfg::RAW_CHUNKS, STEPS = Cfg::RAW_STEPS;
     constexpr int BK = Cfg::BK, STEP_BYTES = ROWS * CH * 16;
     constexpr int NF = (ROWS * CH + 31) / 32;   // chunks a lane fetches of a step
@@ -273,6 +287,7 @@ __device__ __forceinline__ void raw_weights(const TokensArgs &a, const KernelCtx
             ph ^= 1u;
         }
         if (++step == STEPS) step = 0;
+        after(kt - kb);
     }
     cp_async_wait<0>();
 }
@@ -287,7 +302,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + Cfg::BAR_OFFSET);
     uint64_t *empty = full + STAGES;
     uint64_t *done = empty + STAGES;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+    uint64_t *acc_full = done + 1, *acc_empty = acc_full + 2;  // [2] each, with ROUND
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + (Cfg::ROUND > 0 ? 5 : 1));
     const uint32_t warp = warp_id_uniform(), lane = lane_id();
     uint32_t S;
     asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(S));
@@ -307,6 +323,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
             mbar_init(&empty[s], 1);
         }
         mbar_init(done, 1);
+        for (int b = 0; Cfg::ROUND > 0 && b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], Cfg::EPI);
+        }
         fence_barrier_init();
     }
     if (!Cfg::RAW && warp == 2 && lane == 0) {
@@ -335,6 +355,33 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     grid_dependency_wait();
     grid_launch_dependents();
 
+    // ROUND: the sums of a warp's columns, 16 from every 4 * EPI, and the rounds in them
+    float acc[Cfg::ROUND > 0 ? Cfg::CHUNKS : 1][16];
+    const int c0 = static_cast<int>((warp - 2) >> 2) * 16;
+    const uint32_t t_row = tmem + (((warp & 3u) * 32u) << 16);
+    const int rounds = Cfg::ROUND > 0 ? (ke - kb + Cfg::ROUND - 1) / Cfg::ROUND : 0;
+    int taken = 0;
+    auto take_round = [&] {
+        const int r = taken++;
+        if (!mbar_wait(&acc_full[r & 1], (r >> 1) & 1, ctx, kSiteEpilogueFull)) {
+            taken = rounds;  // (the call has failed)
+            return;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < Cfg::CHUNKS; ++i) {
+            const int c = c0 + i * 4 * Cfg::EPI;
+            if (c >= Cfg::ACC || c % TOK >= rows) continue;  // no tokens there
+            uint32_t v[16];
+            tmem_ld_32x32b_x16(t_row + (r & 1) * Cfg::ACC + c, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[i][j] += __uint_as_float(v[j]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[r & 1]);
+    };
     if (warp == 0) {
         if (lane == 0) {
             int it = 0;
@@ -363,9 +410,29 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
         if (lane == 0) {
             constexpr uint32_t idesc = idesc_f16(BN, TOK, 1, /*A*/ Cfg::W_K ? 0 : 1, /*B K-major*/ 0);
             int it = 0;
+            bool ok = true;
+            uint32_t d_tmem = tmem;
             for (int kt = kb; kt < ke; ++kt, ++it) {
+                bool first = kt == kb;
+                if constexpr (Cfg::ROUND > 0) {
+                    first = it % Cfg::ROUND == 0;
+                    if (first) {
+                        const uint32_t r = it / Cfg::ROUND;
+                        if (r > 0) umma_commit(&acc_full[(r - 1) & 1u]);
+                        if (!mbar_wait(&acc_empty[r & 1u], ((r >> 1) & 1u) ^ 1u, ctx,
+                                       kSiteMmaAccEmpty)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        d_tmem = tmem + (r & 1u) * Cfg::ACC;
+                    }
+                }
                 const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
-                if (!mbar_wait(&full[s], ph, ctx, kSiteMmaFull)) break;
+                if (!mbar_wait(&full[s], ph, ctx, kSiteMmaFull)) {
+                    ok = false;
+                    break;
+                }
                 tc_fence_after();
                 const uint32_t st = smem_u32(smem + s * Cfg::STAGE_BYTES);
 #pragma unroll
@@ -378,17 +445,33 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                             Cfg::W_K ? smem_desc_sw128(st + k * 32, 16, 1024)
                                      : smem_desc_sw128(st + d * Cfg::W_SUB + k * 2048, BK * 128,
                                                        1024);
-                        umma_f16_ss(tmem + d * TOK, ad, bd, idesc,
-                                    (kt == kb && k == 0) ? 0u : 1u);
+                        umma_f16_ss(d_tmem + d * TOK, ad, bd, idesc, (first && k == 0) ? 0u : 1u);
                     }
                 }
                 umma_commit(&empty[s]);
             }
+            if (Cfg::ROUND > 0 && ok && ke > kb)
+                umma_commit(&acc_full[((ke - kb - 1) / Cfg::ROUND) & 1]);
             umma_commit(done);
         }
-    } else if constexpr (Cfg::RAW) {
-        raw_weights<Cfg>(a, ctx, smem, full, empty, n0, kb, ke, static_cast<int>(warp) - 2,
-                         static_cast<int>(lane));
+    } else {
+        if constexpr (Cfg::ROUND > 0) {
+#pragma unroll
+            for (int i = 0; i < Cfg::CHUNKS; ++i)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) acc[i][j] = 0.0f;
+        }
+        if constexpr (Cfg::RAW)
+            raw_weights<Cfg>(a, ctx, smem, full, empty, n0, kb, ke, static_cast<int>(warp) - 2,
+                             static_cast<int>(lane), [&](int i) {
+                                 // half a round on, the last one's products have ended
+                                 if constexpr (Cfg::ROUND > 0)
+                                     if (i >= Cfg::ROUND && i % Cfg::ROUND == Cfg::ROUND / 2 &&
+                                         taken < rounds)
+                                         take_round();
+                             });
+        if constexpr (Cfg::ROUND > 0)
+            while (taken < rounds) take_round();
     }
     // Every MMA of this CTA has completed: the ring is free, the sums final.
     // (With an empty K range the commit arrives at once.)
@@ -399,22 +482,30 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     if (warp >= 2) {
         const uint32_t q = warp & 3u;
         const int col = static_cast<int>(q * 32 + lane);
-        const uint32_t t_row = tmem + ((q * 32u) << 16);
         // a quadrant's warps take 16 accumulator columns in turn
-#pragma unroll 1
-        for (int c = static_cast<int>((warp - 2) >> 2) * 16; c < Cfg::ACC;
-             c += 4 * Cfg::EPI) {
-            if (c % TOK >= rows) continue;  // no tokens there
-            uint32_t v[16];
-            if (ke > kb && ok) {
-                tmem_ld_32x32b_x16(t_row + c, v);
-                tmem_ld_wait();
-            } else {
+        if constexpr (Cfg::ROUND > 0) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = 0u;
+            for (int i = 0; i < Cfg::CHUNKS; ++i) {
+                const int c = c0 + i * 4 * Cfg::EPI;
+                if (c >= Cfg::ACC || c % TOK >= rows) continue;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) sums[(c + j) * BN + col] = acc[i][j];
             }
+        } else {
+#pragma unroll 1
+            for (int c = c0; c < Cfg::ACC; c += 4 * Cfg::EPI) {
+                if (c % TOK >= rows) continue;  // no tokens there
+                uint32_t v[16];
+                if (ke > kb && ok) {
+                    tmem_ld_32x32b_x16(t_row + c, v);
+                    tmem_ld_wait();
+                } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) sums[(c + j) * BN + col] = __uint_as_float(v[j]);
+                    for (int j = 0; j < 16; ++j) v[j] = 0u;
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j) sums[(c + j) * BN + col] = __uint_as_float(v[j]);
+            }
         }
     }
     __syncwarp();
@@ -603,9 +694,23 @@ double op_raw_us(const OpDevice &dev, int M, long long N, long long K, bool dual
     return waves * ((k_tiles + S - 1) / S) * (transposed ? 0.35 : dual ? 0.8 : 0.5);
 }
 
+constexpr int kSignSteps = kSignRound / 64;  // K steps of a round
+
+// sign: the call's Z decides a ReLU's derivative, here or in the backward pass.
 template <class Cfg>
 static pgemm_status launch_tokens(const OpDevice &dev, TokensArgs a, const OpMat *X,
-                                  const OpMat *W, int segments, cudaStream_t s) {
+                                  const OpMat *W, int segments, bool sign, cudaStream_t s) {
+    a.k_seg = op_blocks(a.K, Cfg::BK);
+    a.k_tiles = a.k_seg * segments;
+    const int n_tiles = op_blocks(a.N, Cfg::BN);
+    const int m_tiles = op_blocks(a.M, Cfg::TOK);
+    const int S = cluster_share(cluster_slots(dev.sm_count, Cfg::CTAS), n_tiles * m_tiles, a.k_tiles,
+                                Cfg::RAW ? kRawWaveSteps : kWaveSteps);
+    if constexpr (!Cfg::W_K && Cfg::ROUND == 0) {
+        if (sign && op_blocks(a.k_tiles, S) > kSignSteps)
+            return launch_tokens<TokCfg<Cfg::TOK, Cfg::MODE, Cfg::RAW, kSignSteps>>(
+                dev, a, X, W, segments, sign, s);
+    }
     static const KernelInfo info = [] {
         KernelInfo k;
         k.threads = Cfg::THREADS;
@@ -628,12 +733,6 @@ static pgemm_status launch_tokens(const OpDevice &dev, TokensArgs a, const OpMat
     a.w[0] = W[0].p;
     a.w[1] = W[Cfg::DUAL || segments == 2 ? 1 : 0].p;
     a.w_ld = W[0].ld;
-    a.k_seg = op_blocks(a.K, Cfg::BK);
-    a.k_tiles = a.k_seg * segments;
-    const int n_tiles = op_blocks(a.N, Cfg::BN);
-    const int m_tiles = op_blocks(a.M, Cfg::TOK);
-    const int S = cluster_share(cluster_slots(dev.sm_count, Cfg::CTAS), n_tiles * m_tiles, a.k_tiles,
-                                Cfg::RAW ? kRawWaveSteps : kWaveSteps);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -655,18 +754,18 @@ static pgemm_status launch_tokens(const OpDevice &dev, TokensArgs a, const OpMat
 
 template <Tok MODE, bool RAW>
 static pgemm_status launch_tokens_rows(const OpDevice &dev, const TokensArgs &a, const OpMat *X,
-                                       const OpMat *W, int segments, cudaStream_t s) {
-    if (a.M <= 16) return launch_tokens<TokCfg<16, MODE, RAW>>(dev, a, X, W, segments, s);
-    if (a.M <= 32) return launch_tokens<TokCfg<32, MODE, RAW>>(dev, a, X, W, segments, s);
-    if (a.M <= 64) return launch_tokens<TokCfg<64, MODE, RAW>>(dev, a, X, W, segments, s);
-    return launch_tokens<TokCfg<128, MODE, RAW>>(dev, a, X, W, segments, s);
+                                       const OpMat *W, int segments, bool sign, cudaStream_t s) {
+    if (a.M <= 16) return launch_tokens<TokCfg<16, MODE, RAW>>(dev, a, X, W, segments, sign, s);
+    if (a.M <= 32) return launch_tokens<TokCfg<32, MODE, RAW>>(dev, a, X, W, segments, sign, s);
+    if (a.M <= 64) return launch_tokens<TokCfg<64, MODE, RAW>>(dev, a, X, W, segments, sign, s);
+    return launch_tokens<TokCfg<128, MODE, RAW>>(dev, a, X, W, segments, sign, s);
 }
 
 template <Tok MODE>
 static pgemm_status launch_tokens_size(const OpDevice &dev, const TokensArgs &a, const OpMat *X,
-                                       const OpMat *W, int segments, cudaStream_t s) {
-    return W[0].ld % 8 == 0 ? launch_tokens_rows<MODE, false>(dev, a, X, W, segments, s)
-                            : launch_tokens_rows<MODE, true>(dev, a, X, W, segments, s);
+                                       const OpMat *W, int segments, bool sign, cudaStream_t s) {
+    return W[0].ld % 8 == 0 ? launch_tokens_rows<MODE, false>(dev, a, X, W, segments, sign, s)
+                            : launch_tokens_rows<MODE, true>(dev, a, X, W, segments, sign, s);
 }
 
 pgemm_status op_tokens_linear(const OpDevice &dev, int M, int N, int K, const OpMat &X,
@@ -682,7 +781,8 @@ pgemm_status op_tokens_linear(const OpDevice &dev, int M, int N, int K, const Op
     a.act = e.act;
     a.out = Y;
     a.ldo = N;
-    return launch_tokens_size<Tok::LINEAR>(dev, a, &X, &W, 1, s);
+    return launch_tokens_size<Tok::LINEAR>(dev, a, &X, &W, 1,
+                                           e.preact && e.act == PGEMM_ACT_RELU, s);
 }
 
 pgemm_status op_tokens_gated(const OpDevice &dev, int M, int F, int K, const OpMat &X,
@@ -697,7 +797,7 @@ pgemm_status op_tokens_gated(const OpDevice &dev, int M, int F, int K, const OpM
     a.out = H;
     a.ldo = F;
     const OpMat w[2] = {Wg, Wu};
-    return launch_tokens_size<Tok::GATED>(dev, a, &X, w, 1, s);
+    return launch_tokens_size<Tok::GATED>(dev, a, &X, w, 1, preact && act == PGEMM_ACT_RELU, s);
 }
 
 pgemm_status op_tokens_linear_grad(const OpDevice &dev, int M, int N, int K, const OpMat &X,
@@ -713,7 +813,7 @@ pgemm_status op_tokens_linear_grad(const OpDevice &dev, int M, int N, int K, con
     a.act = act;
     a.out = dz;
     a.ldo = dz_ld;
-    return launch_tokens_size<Tok::LINEAR_GRAD>(dev, a, &X, &W, 1, s);
+    return launch_tokens_size<Tok::LINEAR_GRAD>(dev, a, &X, &W, 1, act == PGEMM_ACT_RELU, s);
 }
 
 pgemm_status op_tokens_gated_grad(const OpDevice &dev, int M, int F, int K, const OpMat &X,
@@ -729,7 +829,7 @@ pgemm_status op_tokens_gated_grad(const OpDevice &dev, int M, int F, int K, cons
     a.out2 = du;
     a.ldo = dz_ld;
     const OpMat w[2] = {Wg, Wu};
-    return launch_tokens_size<Tok::GATED_GRAD>(dev, a, &X, w, 1, s);
+    return launch_tokens_size<Tok::GATED_GRAD>(dev, a, &X, w, 1, act == PGEMM_ACT_RELU, s);
 }
 
 pgemm_status op_tokens_transposed(const OpDevice &dev, int M, int N, int K, const OpMat *X,
@@ -741,7 +841,7 @@ pgemm_status op_tokens_transposed(const OpDevice &dev, int M, int N, int K, cons
     a.act = PGEMM_ACT_NONE;
     a.out = out;
     a.ldo = N;
-    return launch_tokens_size<Tok::TRANSPOSED>(dev, a, X, W, segments, s);
+    return launch_tokens_size<Tok::TRANSPOSED>(dev, a, X, W, segments, false, s);
 }
 
 }  // namespace pg

@@ -108,3 +108,59 @@ def test_xent_sums_of_dx_taken_in_now_and_then(workspace):
     want = ref.xent(X, W, y, dl)
     ref.check(dX, *want["dX"], "dX")
     ref.check(dW, *want["dW"], "dW")
+
+
+# ------------------------------------------------- ReLU sums of few rows ---
+# A Z that decides a ReLU's derivative is summed in rounds of 512 products at any number
+# of rows.  With all products positive every truncation falls short: half an ulp, at
+# most 2^-24 of the running sum, on average over many outputs, 32 times a round, while
+# the running sum grows evenly to the round's own: (32 + 1) / 2 * 2^-24 of it, and the
+# rounds' additions round to nearest either way.  A tenth more for the sampling.  Chains
+# of a block's whole share (K = 8192 of one block) fall 16 times as short.
+RELU_MEAN = 1.1 * 16.5 * 2.0 ** -24
+FEW_RELU = [(1, 20000, 8192), (17, 264, 8192), (64, 20000, 8192), (128, 264, 9001),
+            (128, 39000, 4104), (3, 20001, 8192), (100, 20003, 4100)]
+
+
+def positive(seed, *shape):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.rand(shape, generator=g, device="cuda") + 0.25).to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("M,N,K", FEW_RELU)
+def test_few_rows_sum_relu_pre_activations_in_rounds(M, N, K):
+    X, W = positive(31, M, K), positive(32, K, N)
+    Y, Z = nan_like(M, N), nan_like(M, N, dtype=torch.float32)
+    pg.linear_bf16(M, N, K, X, W, None, "relu", None, Y, preact=Z)
+    z = X.double() @ W.double()
+    assert ((Z.double() - z) / z).mean().abs().item() < RELU_MEAN
+    G = nan_like(2, M, N, dtype=torch.float32)
+    H = nan_like(M, N)
+    pg.gated_bf16(M, N, K, X, W, W, "relu", H, preact=G)
+    for g in G:
+        assert ((g.double() - z) / z).mean().abs().item() < RELU_MEAN
+
+
+@pytest.mark.parametrize("M,N,K", FEW_RELU)
+def test_few_rows_compute_relu_pre_activations_alike(M, N, K):
+    # what a backward pass computes again has the signs of what a forward pass kept
+    X, W, b, dY = rnd(33, M, K), rnd(34, K, N, std=K ** -0.5), rnd(35, N), rnd(36, M, N)
+    Y, Z = nan_like(M, N), nan_like(M, N, dtype=torch.float32)
+    pg.linear_bf16(M, N, K, X, W, b, "relu", None, Y, preact=Z)
+    y, bound, z, _ = ref.linear(X, W, b, "relu", None)
+    ref.check(Y, y, bound, "Y")
+    size = X.double().abs() @ W.double().abs() + b.double().abs()
+    # the longest chain, an addition a round, and one a block of a shared tile
+    ref.check(Z, z, ref.step(512 + 16 * (K // 512 + 9)) * size, "preact")
+    del size, z, y, bound
+    got = []
+    for kept in (Z, None):
+        dX, db = nan_like(M, K), nan_like(N)
+        pg.linear_bf16_backward(M, N, K, X, W, b, "relu", dY, dX, None, db, preact=kept)
+        got.append((dX, db))
+    want = ref.linear_backward(X, W, b, "relu", dY)
+    for dX, db in got:
+        ref.check(dX, *want["dX"], "dX")
+        ref.check(db, *want["db"], "db")
+    if N % 8 == 0:
+        assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
