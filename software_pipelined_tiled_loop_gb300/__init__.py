@@ -245,20 +245,40 @@ def gemm_i8_ex(M, N, K, alpha, A, B, beta, C, config=None, stream=None):
                             _cfg(config), _stream(stream)), "gemm_i8_ex")
 
 
-def _operand(x, name, count, itemsize) -> int:
+class _Kind:
+    """An operand's element type: its size and the torch types that hold it."""
+
+    def __init__(self, itemsize, *names):
+        self.itemsize, self.names = itemsize, names
+        self.seen = set()  # torch's own objects for them, once met
+
+
+# (bf16 bit patterns also travel as 16-bit integers, as gemm_bf16 takes them)
+_BF16 = _Kind(2, "torch.bfloat16", "torch.int16", "torch.uint16")
+_F32 = _Kind(4, "torch.float32")
+_I64 = _Kind(8, "torch.int64")
+
+
+def _operand(x, name, count, kind) -> int:
     """_ptr of an operator's operand, which must hold at least ``count``
-    elements of ``itemsize`` bytes (checked for tensors; None passes)."""
+    elements of ``kind`` (checked for tensors; None and addresses pass)."""
     try:
-        if (x.is_cuda and x.element_size() == itemsize and x.numel() >= count
-                and x.is_contiguous()):
+        if (x.is_cuda and x.dtype in kind.seen and x.numel() >= count and x.is_contiguous()):
             return x.data_ptr()
     except AttributeError:
-        return _ptr(x)  # None, a raw pointer, or nothing that has an address
+        pass  # None, a raw pointer, or nothing that has an address
     p = _ptr(x)
-    if x.element_size() != itemsize:
-        raise ValueError(f"{name}: elements of {x.element_size()} bytes, {itemsize} wanted")
+    if not hasattr(x, "element_size"):
+        return p
+    if x.element_size() != kind.itemsize:
+        raise ValueError(f"{name}: elements of {x.element_size()} bytes, {kind.itemsize} wanted")
+    dtype = getattr(x, "dtype", None)
+    if dtype is not None and str(dtype) not in kind.names:
+        raise ValueError(f"{name}: elements of type {dtype}, {kind.names[0]} wanted")
     if x.numel() < count:
         raise ValueError(f"{name}: {x.numel()} elements, at least {count} wanted")
+    if dtype is not None:
+        kind.seen.add(dtype)
     return p
 
 
@@ -284,11 +304,11 @@ def linear_bf16(M, N, K, X, W, bias, act, residual, Y, preact=None, stream=None)
     backward call.  Asynchronous on ``stream``."""
     if M | N | K > _DIM_MAX:
         _too_large("linear_bf16")
-    _check(lib().linear_bf16(M, N, K, _operand(X, "X", M * K, 2), _operand(W, "W", K * N, 2),
-                             _operand(bias, "bias", N, 2), _act(act),
-                             _operand(residual, "residual", M * N, 2),
-                             _operand(Y, "Y", M * N, 2), _operand(preact, "preact", M * N, 4),
-                             _stream(stream)), "linear_bf16")
+    _check(lib().linear_bf16(
+        M, N, K, _operand(X, "X", M * K, _BF16), _operand(W, "W", K * N, _BF16),
+        _operand(bias, "bias", N, _BF16), _act(act), _operand(residual, "residual", M * N, _BF16),
+        _operand(Y, "Y", M * N, _BF16), _operand(preact, "preact", M * N, _F32),
+        _stream(stream)), "linear_bf16")
 
 
 def linear_bf16_backward(M, N, K, X, W, bias, act, dY, dX, dW, dbias, preact=None, stream=None):
@@ -299,10 +319,10 @@ def linear_bf16_backward(M, N, K, X, W, bias, act, dY, dX, dW, dbias, preact=Non
     if M | N | K > _DIM_MAX:
         _too_large("linear_bf16_backward")
     _check(lib().linear_bf16_backward(
-        M, N, K, _operand(X, "X", M * K, 2), _operand(W, "W", K * N, 2),
-        _operand(bias, "bias", N, 2), _act(act), _operand(dY, "dY", M * N, 2),
-        _operand(preact, "preact", M * N, 4), _operand(dX, "dX", M * K, 2),
-        _operand(dW, "dW", K * N, 2), _operand(dbias, "dbias", N, 2), _stream(stream)),
+        M, N, K, _operand(X, "X", M * K, _BF16), _operand(W, "W", K * N, _BF16),
+        _operand(bias, "bias", N, _BF16), _act(act), _operand(dY, "dY", M * N, _BF16),
+        _operand(preact, "preact", M * N, _F32), _operand(dX, "dX", M * K, _BF16),
+        _operand(dW, "dW", K * N, _BF16), _operand(dbias, "dbias", N, _BF16), _stream(stream)),
         "linear_bf16_backward")
 
 
@@ -312,10 +332,10 @@ def gated_bf16(M, F, K, X, Wg, Wu, act, H, preact=None, stream=None):
     for the backward call.  Asynchronous on ``stream``."""
     if M | F | K > _DIM_MAX:
         _too_large("gated_bf16")
-    _check(lib().gated_bf16(M, F, K, _operand(X, "X", M * K, 2), _operand(Wg, "Wg", K * F, 2),
-                            _operand(Wu, "Wu", K * F, 2), _act(act), _operand(H, "H", M * F, 2),
-                            _operand(preact, "preact", 2 * M * F, 4), _stream(stream)),
-           "gated_bf16")
+    _check(lib().gated_bf16(
+        M, F, K, _operand(X, "X", M * K, _BF16), _operand(Wg, "Wg", K * F, _BF16),
+        _operand(Wu, "Wu", K * F, _BF16), _act(act), _operand(H, "H", M * F, _BF16),
+        _operand(preact, "preact", 2 * M * F, _F32), _stream(stream)), "gated_bf16")
 
 
 def gated_bf16_backward(M, F, K, X, Wg, Wu, act, dH, dX, dWg, dWu, preact=None, stream=None):
@@ -326,10 +346,10 @@ def gated_bf16_backward(M, F, K, X, Wg, Wu, act, dH, dX, dWg, dWu, preact=None, 
     if M | F | K > _DIM_MAX:
         _too_large("gated_bf16_backward")
     _check(lib().gated_bf16_backward(
-        M, F, K, _operand(X, "X", M * K, 2), _operand(Wg, "Wg", K * F, 2),
-        _operand(Wu, "Wu", K * F, 2), _act(act), _operand(dH, "dH", M * F, 2),
-        _operand(preact, "preact", 2 * M * F, 4), _operand(dX, "dX", M * K, 2),
-        _operand(dWg, "dWg", K * F, 2), _operand(dWu, "dWu", K * F, 2), _stream(stream)),
+        M, F, K, _operand(X, "X", M * K, _BF16), _operand(Wg, "Wg", K * F, _BF16),
+        _operand(Wu, "Wu", K * F, _BF16), _act(act), _operand(dH, "dH", M * F, _BF16),
+        _operand(preact, "preact", 2 * M * F, _F32), _operand(dX, "dX", M * K, _BF16),
+        _operand(dWg, "dWg", K * F, _BF16), _operand(dWu, "dWu", K * F, _BF16), _stream(stream)),
         "gated_bf16_backward")
 
 
@@ -339,9 +359,10 @@ def xent_bf16(T, V, D, X, W, target, loss, lse, stream=None):
     0); loss and lse: T fp32, either may be None.  Asynchronous."""
     if T | V | D > _DIM_MAX:
         _too_large("xent_bf16")
-    _check(lib().xent_bf16(T, V, D, _operand(X, "X", T * D, 2), _operand(W, "W", V * D, 2),
-                           _operand(target, "target", T, 8), _operand(loss, "loss", T, 4),
-                           _operand(lse, "lse", T, 4), _stream(stream)), "xent_bf16")
+    _check(lib().xent_bf16(
+        T, V, D, _operand(X, "X", T * D, _BF16), _operand(W, "W", V * D, _BF16),
+        _operand(target, "target", T, _I64), _operand(loss, "loss", T, _F32),
+        _operand(lse, "lse", T, _F32), _stream(stream)), "xent_bf16")
 
 
 def xent_bf16_grad(T, V, D, X, W, target, dloss, loss, lse, dX, dW, workspace_bytes=0,
@@ -353,10 +374,10 @@ def xent_bf16_grad(T, V, D, X, W, target, dloss, loss, lse, dX, dW, workspace_by
     if T | V | D > _DIM_MAX:
         _too_large("xent_bf16_grad")
     _check(lib().xent_bf16_grad(
-        T, V, D, _operand(X, "X", T * D, 2), _operand(W, "W", V * D, 2),
-        _operand(target, "target", T, 8), _operand(dloss, "dloss", T, 4),
-        _operand(loss, "loss", T, 4), _operand(lse, "lse", T, 4), _operand(dX, "dX", T * D, 2),
-        _operand(dW, "dW", V * D, 2), int(workspace_bytes), _stream(stream)), "xent_bf16_grad")
+        T, V, D, _operand(X, "X", T * D, _BF16), _operand(W, "W", V * D, _BF16),
+        _operand(target, "target", T, _I64), _operand(dloss, "dloss", T, _F32),
+        _operand(loss, "loss", T, _F32), _operand(lse, "lse", T, _F32),
+        _operand(dX, "dX", T * D, _BF16), _operand(dW, "dW", V * D, _BF16), int(workspace_bytes), _stream(stream)), "xent_bf16_grad")
 
 
 def pgemm_stage_reuse_demo(X, rows, cols, perm, out, check_reuse, delay_warp=-1, delay_ns=0,

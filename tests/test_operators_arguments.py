@@ -39,3 +39,49 @@ def test_linear_backward_asks_only_for_what_it_reads(L):
     for kw in ({"X": None}, {"W": None}, {"X": None, "dW": None, "pre": None},
                {"W": None, "dX": None, "pre": None}):
         assert call(**kw) == INVALID, kw
+
+
+class FakeCuda:
+    """A contiguous CUDA tensor as the binding looks at it."""
+    is_cuda = True
+
+    def __init__(self, dtype, numel=16):
+        self.dtype, self.n = dtype, numel
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return G
+
+    def numel(self):
+        return self.n
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+
+def test_binding_checks_element_types(L):
+    torch = pytest.importorskip("torch")
+    ok, short = FakeCuda(torch.bfloat16), FakeCuda(torch.bfloat16, 15)
+    f16, i32, f64 = (FakeCuda(t) for t in (torch.float16, torch.int32, torch.float64))
+    f32, i64 = FakeCuda(torch.float32, 32), FakeCuda(torch.int64)
+    for bad, call in (
+            ("X", lambda: pg.linear_bf16(4, 4, 4, f16, ok, None, "none", None, ok)),
+            ("bias", lambda: pg.linear_bf16(4, 4, 4, ok, ok, f16, "none", None, ok)),
+            ("preact", lambda: pg.linear_bf16(4, 4, 4, ok, ok, None, "relu", None, ok, preact=i32)),
+            ("dY", lambda: pg.linear_bf16_backward(4, 4, 4, ok, ok, None, "relu", f16, ok, ok, ok)),
+            ("Wu", lambda: pg.gated_bf16(4, 4, 4, ok, ok, f16, "silu", ok)),
+            ("preact", lambda: pg.gated_bf16_backward(4, 4, 2, ok, ok, ok, "silu", ok, ok, ok, ok,
+                                                      preact=FakeCuda(torch.int32, 32))),
+            ("target", lambda: pg.xent_bf16(4, 4, 4, ok, ok, f64, f32, f32)),
+            ("loss", lambda: pg.xent_bf16(4, 4, 4, ok, ok, i64, i32, f32)),
+            ("dloss", lambda: pg.xent_bf16_grad(4, 4, 4, ok, ok, i64, i32, f32, f32, ok, ok)),
+            ("dW", lambda: pg.xent_bf16_grad(4, 4, 4, ok, ok, i64, f32, f32, f32, ok, f16))):
+        for _ in range(2):  # (the second call finds the right types met before)
+            with pytest.raises(ValueError, match=f"^{bad}: elements of type"):
+                call()
+    # right types pass on to the next check; so do bf16 bit patterns as integers
+    for t in (torch.bfloat16, torch.int16):
+        with pytest.raises(ValueError, match="^W: 15 elements"):
+            pg.linear_bf16(4, 4, 4, FakeCuda(t), short, None, "none", None, ok)
