@@ -285,8 +285,12 @@ def _operand(x, name, count, kind) -> int:
 _DIM_MAX = 2 ** 31 - 1  # the C interface's sizes are 32-bit
 
 
-def _too_large(what):
-    raise ValueError(f"{what}: sizes are at most {_DIM_MAX}")
+def _sizes(what, bits):
+    """Refuse sizes, given as their bitwise or, of which ctypes would pass only the
+    low 32 bits.  (Negative 32-bit sizes are left to the C function, which refuses
+    them; what their or may hide has negative low bits itself or stands beside them.)"""
+    if not -_DIM_MAX <= bits + 1 <= _DIM_MAX + 1:
+        raise ValueError(f"{what}: sizes are at most {_DIM_MAX}")
 
 
 def _act(act) -> int:
@@ -302,8 +306,7 @@ def linear_bf16(M, N, K, X, W, bias, act, residual, Y, preact=None, stream=None)
     W: K x N; bias (N) and residual (M x N, may be Y) may be None; ``act`` is a
     name of ACTIVATIONS.  ``preact`` (M x N fp32) receives X @ W + bias for the
     backward call.  Asynchronous on ``stream``."""
-    if M | N | K > _DIM_MAX:
-        _too_large("linear_bf16")
+    _sizes("linear_bf16", M | N | K)
     _check(lib().linear_bf16(
         M, N, K, _operand(X, "X", M * K, _BF16), _operand(W, "W", K * N, _BF16),
         _operand(bias, "bias", N, _BF16), _act(act), _operand(residual, "residual", M * N, _BF16),
@@ -316,8 +319,7 @@ def linear_bf16_backward(M, N, K, X, W, bias, act, dY, dX, dW, dbias, preact=Non
     dbias (N), each skipped when None; X and W may be None where nothing wanted
     reads them.  ``preact``: what the forward call kept, or None to compute it
     again.  Asynchronous."""
-    if M | N | K > _DIM_MAX:
-        _too_large("linear_bf16_backward")
+    _sizes("linear_bf16_backward", M | N | K)
     _check(lib().linear_bf16_backward(
         M, N, K, _operand(X, "X", M * K, _BF16), _operand(W, "W", K * N, _BF16),
         _operand(bias, "bias", N, _BF16), _act(act), _operand(dY, "dY", M * N, _BF16),
@@ -330,8 +332,7 @@ def gated_bf16(M, F, K, X, Wg, Wu, act, H, preact=None, stream=None):
     """H <- act(X @ Wg) * (X @ Wu), bf16 with fp32 arithmetic.  X: M x K, Wg and
     Wu: K x F, H: M x F.  ``preact`` (2 x M x F fp32) receives both products
     for the backward call.  Asynchronous on ``stream``."""
-    if M | F | K > _DIM_MAX:
-        _too_large("gated_bf16")
+    _sizes("gated_bf16", M | F | K)
     _check(lib().gated_bf16(
         M, F, K, _operand(X, "X", M * K, _BF16), _operand(Wg, "Wg", K * F, _BF16),
         _operand(Wu, "Wu", K * F, _BF16), _act(act), _operand(H, "H", M * F, _BF16),
@@ -343,8 +344,7 @@ def gated_bf16_backward(M, F, K, X, Wg, Wu, act, dH, dX, dWg, dWu, preact=None, 
     (K x F); dX, or dWg and dWu together, may be None, and so may X, Wg and Wu
     where nothing wanted reads them.  ``preact``: what the forward call kept, or
     None to compute it again.  Asynchronous."""
-    if M | F | K > _DIM_MAX:
-        _too_large("gated_bf16_backward")
+    _sizes("gated_bf16_backward", M | F | K)
     _check(lib().gated_bf16_backward(
         M, F, K, _operand(X, "X", M * K, _BF16), _operand(Wg, "Wg", K * F, _BF16),
         _operand(Wu, "Wu", K * F, _BF16), _act(act), _operand(dH, "dH", M * F, _BF16),
@@ -357,8 +357,7 @@ def xent_bf16(T, V, D, X, W, target, loss, lse, stream=None):
     """Softmax cross entropy of logits X @ W.T over a vocabulary: X: T x D, W:
     V x D bf16, target: T int64 (outside [0, V): the row does not count, loss
     0); loss and lse: T fp32, either may be None.  Asynchronous."""
-    if T | V | D > _DIM_MAX:
-        _too_large("xent_bf16")
+    _sizes("xent_bf16", T | V | D)
     _check(lib().xent_bf16(
         T, V, D, _operand(X, "X", T * D, _BF16), _operand(W, "W", V * D, _BF16),
         _operand(target, "target", T, _I64), _operand(loss, "loss", T, _F32),
@@ -371,13 +370,13 @@ def xent_bf16_grad(T, V, D, X, W, target, dloss, loss, lse, dX, dW, workspace_by
     (T x D) and dW (V x D), either of which may be None.  ``workspace_bytes``
     bounds the scratch for the probabilities (0: the library's choice); larger
     ones go by in pieces of the vocabulary.  Asynchronous."""
-    if T | V | D > _DIM_MAX:
-        _too_large("xent_bf16_grad")
+    _sizes("xent_bf16_grad", T | V | D)
     _check(lib().xent_bf16_grad(
         T, V, D, _operand(X, "X", T * D, _BF16), _operand(W, "W", V * D, _BF16),
         _operand(target, "target", T, _I64), _operand(dloss, "dloss", T, _F32),
         _operand(loss, "loss", T, _F32), _operand(lse, "lse", T, _F32),
-        _operand(dX, "dX", T * D, _BF16), _operand(dW, "dW", V * D, _BF16), int(workspace_bytes), _stream(stream)), "xent_bf16_grad")
+        _operand(dX, "dX", T * D, _BF16), _operand(dW, "dW", V * D, _BF16), int(workspace_bytes),
+        _stream(stream)), "xent_bf16_grad")
 
 
 def pgemm_stage_reuse_demo(X, rows, cols, perm, out, check_reuse, delay_warp=-1, delay_ns=0,

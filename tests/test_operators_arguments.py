@@ -85,3 +85,34 @@ def test_binding_checks_element_types(L):
     for t in (torch.bfloat16, torch.int16):
         with pytest.raises(ValueError, match="^W: 15 elements"):
             pg.linear_bf16(4, 4, 4, FakeCuda(t), short, None, "none", None, ok)
+
+
+def test_binding_refuses_sizes_below_32_bits(L):
+    # ctypes would pass their low 32 bits on: -(1 << 32) + 4 as 4
+    low = -(1 << 32)
+    for call in (lambda: pg.linear_bf16(low + 4, 4, 4, G, G, None, "none", None, G),
+                 lambda: pg.linear_bf16_backward(4, low, 4, G, G, None, "silu", G, G, G, None),
+                 lambda: pg.gated_bf16(4, 4, low + 8, G, G, G, "silu", G),
+                 lambda: pg.gated_bf16_backward(low + 1, 4, 4, G, G, G, "silu", G, G, G, G),
+                 lambda: pg.xent_bf16(4, low + 4, 4, G, G, G, G, G),
+                 lambda: pg.xent_bf16_grad(4, 4, 3 * low + 4, G, G, G, None, G, G, G, G)):
+        with pytest.raises(ValueError, match="sizes are at most"):
+            call()
+    for small in (-1, -(1 << 31)):  # what 32 bits hold is refused by the C function
+        with pytest.raises(pg.PgemmError):
+            pg.linear_bf16(small, 4, 4, G, G, None, "none", None, G)
+
+
+def test_no_size_beyond_32_bits_reaches_the_library():
+    # every mixture of sizes around the powers of two, against what ctypes would make of it
+    import ctypes
+    import itertools
+    edge = [k * (1 << 31) + d for k in range(-4, 5) for d in (-1, 0, 1, 5)]
+    for dims in itertools.product(edge, repeat=3):
+        try:
+            pg._sizes("f", dims[0] | dims[1] | dims[2])
+        except ValueError:
+            assert any(d != ctypes.c_int(d).value for d in dims), dims
+        else:  # all pass unchanged, or the C function refuses one for being negative
+            seen = [ctypes.c_int(d).value for d in dims]
+            assert list(dims) == seen or min(seen) < 0, dims
