@@ -288,8 +288,9 @@ PGEMM_API pgemm_status gated_bf16_backward(int M, int F, int K, const uint16_t *
 /* Softmax cross entropy of T tokens over a vocabulary of V: with logits
  * L = X W^T (X T x D; W V x D, one row a token of the vocabulary, as an
  * embedding table is stored), lse[t] <- log sum_v exp L[t][v] and
- * loss[t] <- lse[t] - L[t][target[t]].  A target outside [0, V) does not
- * count: its loss is 0.  loss or lse may be NULL.  The logits are never
+ * loss[t] <- lse[t] - L[t][target[t]], both summed in fp32 on their own (good to
+ * a few 1e-6 of the logits' size) and no less than 0.  A target outside [0, V)
+ * does not count: its loss is 0.  loss or lse may be NULL.  The logits are never
  * stored.  V >= 1. */
 PGEMM_API pgemm_status xent_bf16(int T, int V, int D, const uint16_t *X, const uint16_t *W,
                                  const int64_t *target, float *loss, float *lse,

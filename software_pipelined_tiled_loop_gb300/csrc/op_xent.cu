@@ -195,6 +195,14 @@ __device__ __forceinline__ float row_dot(const uint16_t *x, const uint16_t *e, i
     return d;
 }
 
+// lse and the target's logit d are sums of their own, each rounded on its way: of a
+// nearly certain token their difference may come out some 3e-6 of d below the zero that
+// bounds it (a NaN stays one).
+__device__ __forceinline__ float loss_of(float lse, float d) {
+    const float x = lse - d;
+    return x < 0.0f ? 0.0f : x;
+}
+
 template <int ROWS>
 __global__ void __launch_bounds__(256)
     xent_join_kernel(const float *part_m, const float *part_s, long long rows, int blocks, int T,
@@ -257,7 +265,7 @@ __global__ void __launch_bounds__(256)
         const float l = kLn2 * (m + log2f(s));
         const int64_t y = target[t];
         if (lse) lse[t] = l;
-        if (loss) loss[t] = y >= 0 && y < V ? l - d : 0.0f;
+        if (loss) loss[t] = y >= 0 && y < V ? loss_of(l, d) : 0.0f;
     }
     if (dloss != nullptr && blockIdx.x == 0) {
         // the common scale of P (xent): the largest |dloss| of a row that counts
@@ -623,7 +631,7 @@ __global__ void __launch_bounds__(256)
     const float l2 = m + log2f(s);
     if (threadIdx.x == 0 && c0 == 0) {
         if (lse) lse[t] = kLn2 * l2;
-        if (loss) loss[t] = counts ? kLn2 * l2 - d : 0.0f;
+        if (loss) loss[t] = counts ? loss_of(kLn2 * l2, d) : 0.0f;
         if (dloss != nullptr && t == 0) *scale = c;
     }
     const float gt = counts ? (dloss ? dloss[t] / c : 1.0f) : 0.0f;

@@ -164,3 +164,25 @@ def test_few_rows_compute_relu_pre_activations_alike(M, N, K):
         ref.check(db, *want["db"], "db")
     if N % 8 == 0:
         assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+# ----------------------------------------------------------- losses near zero ---
+@pytest.mark.parametrize("T", [1, 40, 300, 1300])
+def test_xent_losses_of_certain_tokens_are_not_negative(T):
+    # Logits of 24 at the targets beside others of at most some 4: losses of 1e-7, where
+    # lse and the target's logit are off by up to the bound's 1e-5 each.
+    V, D = 1001, 1024
+    W = rnd(41, V, D)
+    y = torch.randint(0, V, (T,), device="cuda",
+                      generator=torch.Generator(device="cuda").manual_seed(42))
+    X = (W[y].float() * (24.0 / D)).to(torch.bfloat16)
+    want = ref.xent(X, W, y)["loss"]
+    alone = nan_like(T, dtype=torch.float32)
+    pg.xent_bf16(T, V, D, X, W, y, alone, None)
+    loss, dX, dW = nan_like(T, dtype=torch.float32), nan_like(T, D), nan_like(V, D)
+    pg.xent_bf16_grad(T, V, D, X, W, y, None, loss, None, dX, dW)
+    pieces = nan_like(T, dtype=torch.float32)
+    pg.xent_bf16_grad(T, V, D, X, W, y, None, pieces, None, dX, dW, workspace_bytes=1)
+    for got in (alone, loss, pieces):
+        ref.check(got, *want, "loss")
+        assert (got >= 0).all(), got.min().item()
