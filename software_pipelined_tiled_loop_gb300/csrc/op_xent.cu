@@ -98,6 +98,14 @@ struct EpiXentStats {
                         (KEEP ? kKeepShift : 0.0f);
         // nothing but -inf: any finite reference gives sums of zero
         const float ref = m == -CUDART_INF_F ? 0.0f : m;
+        // +inf among them: less itself it is no number, but the sum is infinite, unless
+        // one of them was none before
+        float inf_sum = CUDART_INF_F;
+        if (m == CUDART_INF_F) {
+#pragma unroll
+            for (int j = 0; j < COLS; ++j)
+                if (isnan(v[j])) inf_sum = v[j];
+        }
         float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int cc = 0; cc < COLS; cc += 32) {
@@ -116,7 +124,7 @@ struct EpiXentStats {
         if (c.row() < c.M) {
             const long long at = static_cast<long long>(n0 / COLS) * rows + c.row();
             part_m[at] = m;
-            part_s[at] = (s[0] + s[1]) + (s[2] + s[3]);
+            part_s[at] = m == CUDART_INF_F ? inf_sum : (s[0] + s[1]) + (s[2] + s[3]);
         }
         return true;
     }
@@ -172,7 +180,7 @@ struct EpiXentGrad {
 // and each row gets a block), then a warp a row multiplies X[t] by W[target].
 __device__ __forceinline__ void join_ms(float &m, float &s, float m2, float s2) {
     const float n = fmaxf(m, m2);
-    const float ref = n == -CUDART_INF_F ? 0.0f : n;
+    const float ref = fabsf(n) == CUDART_INF_F ? 0.0f : n;  // (+inf: an infinite sum)
     s = s * ex2(m - ref) + s2 * ex2(m2 - ref);
     m = n;
 }
@@ -319,9 +327,10 @@ __global__ void __launch_bounds__(256)
     const float l = counts ? lse[t] * kLog2e : 0.0f;
     for (int b = w; b < NB; b += 8) {
         const int col = c0 + b * COLS;
-        f[b][lane] = counts && col < V
-                         ? exp2f(part_m[static_cast<long long>(col / COLS) * rows + t] - l) * gt
-                         : 0.0f;
+        const float m =
+            counts && col < V ? part_m[static_cast<long long>(col / COLS) * rows + t] : 0.0f;
+        // (a block with a logit of +inf: its E are 0, or NaN for that logit)
+        f[b][lane] = !counts || col >= V ? 0.0f : m == CUDART_INF_F ? gt : exp2f(m - l) * gt;
     }
     __syncthreads();
     // warp w: rows w, w + 8, ...; four vectors of 8 columns a lane and row
@@ -536,7 +545,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                     a.logits[static_cast<long long>(t0 + j) * a.ld + v] = x[j];
                 const float b = x[j] * kLog2e;
                 const float n = fmaxf(m[j], b);
-                const float ref = n == -CUDART_INF_F ? 0.0f : n;
+                const float ref = fabsf(n) == CUDART_INF_F ? 0.0f : n;
                 s[j] = fmaf(s[j], ex2(m[j] - ref), ex2(b - ref));
                 m[j] = n;
             }

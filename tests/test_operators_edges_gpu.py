@@ -186,3 +186,52 @@ def test_xent_losses_of_certain_tokens_are_not_negative(T):
     for got in (alone, loss, pieces):
         ref.check(got, *want, "loss")
         assert (got >= 0).all(), got.min().item()
+
+
+# ------------------------------------------------------------ infinite logits ---
+@pytest.mark.parametrize("T", [9, 100, 1300])
+@pytest.mark.parametrize("workspace", [0, 1])
+def test_xent_of_infinite_logits(T, workspace):
+    # token 7's logits are +inf in every other row (a +inf weight times a positive or a
+    # zero input would be NaN: those rows hold -1, whose product is -inf); row 3 holds a
+    # NaN beside them
+    V, D = 700, 40
+    X, W = rnd(51, T, D), rnd(52, V, D, std=D ** -0.5)
+    X[:, 5] = 1
+    X[1::2, 5] = -1
+    W[7, 5] = float("inf")
+    y = torch.arange(T, device="cuda") % 300 + 8
+    y[4] = 7  # the infinite one itself
+    X[3, 2] = float("nan")
+    rows = torch.arange(T, device="cuda")
+    up = (rows % 2 == 0)
+    fine = ~up & (rows != 3)
+    loss, lse = nan_like(T, dtype=torch.float32), nan_like(T, dtype=torch.float32)
+    pg.xent_bf16(T, V, D, X, W, y, loss, lse)
+    loss2, lse2 = nan_like(T, dtype=torch.float32), nan_like(T, dtype=torch.float32)
+    dX, dW = torch.zeros_like(X), torch.zeros_like(W)
+    pg.xent_bf16_grad(T, V, D, X, W, y, None, loss2, lse2, dX, dW, workspace_bytes=workspace)
+    # W without that token, for what is finite
+    rest = torch.arange(V, device="cuda") != 7
+    want = ref.xent(X[fine], W[rest], torch.where(y[fine] > 7, y[fine] - 1, y[fine]))
+    for got, total in ((loss, lse), (loss2, lse2)):
+        assert (total[up] == float("inf")).all() and total[3].isnan() and got[3].isnan()
+        assert (got[up & (rows != 4)] == float("inf")).all() and got[4].isnan()
+        ref.check(total[fine], *want["lse"], "lse")
+        ref.check(got[fine], *want["loss"], "loss")
+    # an infinite sum leaves the finite tokens nothing: their own rows take P = -1 at the
+    # target alone, and only token 7's P is no number
+    dW1 = torch.zeros_like(W)
+    only = torch.where(up, y, -100)
+    pg.xent_bf16_grad(T, V, D, X, W, only, None, None, None, None, dW1, workspace_bytes=workspace)
+    p = torch.zeros(T, V, device="cuda", dtype=torch.float64)
+    p[rows[up], y[up]] = -1.0
+    finite = torch.where(X.isnan(), torch.zeros_like(X), X).double()
+    # (row 3 does not count here, but its zeros meet the NaN of X: leave its column out)
+    cols = torch.arange(D, device="cuda") != 2
+    exact = (p.t() @ finite)[:, cols]
+    keep = rest
+    got = dW1[:, cols][keep].double()
+    assert ((got - exact[keep]).abs() <= 2.0 ** -8 * exact[keep].abs()
+            + ref.step(T) * (p.abs().t() @ finite.abs())[:, cols][keep]).all()
+    assert dW1[7].isnan().all()
