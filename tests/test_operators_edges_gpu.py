@@ -235,3 +235,55 @@ def test_xent_of_infinite_logits(T, workspace):
     assert ((got - exact[keep]).abs() <= 2.0 ** -8 * exact[keep].abs()
             + ref.step(T) * (p.abs().t() @ finite.abs())[:, cols][keep]).all()
     assert dW1[7].isnan().all()
+
+
+# -------------------------------------------------------- far tails of activations ---
+def tails():
+    """Every bf16 from 2^-6 to 13 and its negative, as one row."""
+    z = torch.arange(0x3C80, 0x4150, dtype=torch.int16, device="cuda").view(torch.bfloat16)
+    return torch.cat([z, -z])
+
+
+@pytest.mark.parametrize("M", [1, 200])
+@pytest.mark.parametrize("name", ["gelu", "gelu_tanh", "silu"])
+def test_activations_are_right_relatively(M, name):
+    # Z is one exact product.  The value: 2^-8 of itself by rounding to bf16 and 2^-13
+    # for everything before, which bounds the documented 4.4e-5 of the tail with the
+    # exponential's and the reciprocal's own errors (an argument of 2^7 carries 2^-18).
+    # gelu_tanh's tail: its argument 0.8 (z + 0.045 z^3) is as large as 2^7.2 at -13, where
+    # the 64-bit form needs its own way to the tail, z / (1 + exp(2 y)).
+    z = tails()
+    N = z.numel()
+    X = torch.ones(M, 1, device="cuda", dtype=torch.bfloat16)
+    Y, H = nan_like(M, N), nan_like(M, N)
+    pg.linear_bf16(M, N, 1, X, z.view(1, N), None, name, None, Y)
+    pg.gated_bf16(M, N, 1, X, z.view(1, N), torch.ones_like(z).view(1, N), name, H)
+    zd = z.double()
+    if name == "gelu_tanh":
+        y = zd / (1 + torch.exp(2 * (2 / torch.pi) ** 0.5 * -(zd + 0.044715 * zd ** 3)))
+    else:
+        y = ref.act(zd, name)
+    seen = y.abs() >= 2.0 ** -110  # (smaller ones may be flushed on the way)
+    assert seen.sum() > 0.7 * N
+    for got in (Y, H):
+        over = (got.double() - y).abs() - (2.0 ** -8 + 2.0 ** -13) * y.abs()
+        assert (over[:, seen] <= 0).all(), z[seen][over[:, seen].amax(0).argmax()].item()
+        assert (got[:, ~seen].abs().double() <= 2.0 ** -100).all()
+
+
+@pytest.mark.parametrize("kept", [False, True])
+def test_gelu_gradient_of_the_tail(kept):
+    # dbias of one row is gelu'(z) = Phi + z phi, whose terms differ in sign below zero:
+    # 2^-13 of each, and two roundings to bf16
+    z = tails()
+    N = z.numel()
+    X, ones = torch.ones(1, 1, device="cuda", dtype=torch.bfloat16), torch.ones_like(z).view(1, N)
+    Z = z.float().view(1, N).contiguous() if kept else None
+    db = nan_like(N)
+    pg.linear_bf16_backward(1, N, 1, X, z.view(1, N), None, "gelu", ones, None, None, db, preact=Z)
+    zd = z.double()
+    phi = torch.exp(-zd * zd / 2) / (2 * torch.pi) ** 0.5
+    Phi = 0.5 * torch.erfc(-zd / 2 ** 0.5)
+    d = Phi + zd * phi
+    bound = 2.0 ** -7 * (1 + 2.0 ** -8) * d.abs() + 2.0 ** -13 * (Phi + zd.abs() * phi) + 2.0 ** -110
+    assert ((db.double() - d).abs() <= bound).all()
