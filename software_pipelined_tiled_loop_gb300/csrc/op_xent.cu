@@ -67,6 +67,7 @@ __device__ __forceinline__ float ex2(float x) {
 // in (0, 2^15], just within fp16, which carries them to 2^-11 of their size, an eighth
 // of what rounding P to bf16 costs, down to 2^-29 of the block's largest, and to 2^-40
 // of that largest below: an unlikely token beside a likely one keeps its gradient.
+constexpr int kStatsRound = 1024;
 constexpr float kKeepShift = 15.0f;
 template <bool KEEP>
 struct EpiXentStats {
@@ -130,7 +131,10 @@ struct EpiXentStats {
     }
 };
 
-// P of one piece of the vocabulary.
+// P of one piece of the vocabulary.  Its logits are summed in the same rounds as the
+// statistics' (kStatsRound): from one long chain every exp(L - lse) of a row would be
+// short by what the truncation takes from L: 7e-4 of itself for logits of 24 at D =
+// 8192, products all positive.
 struct EpiXentGrad {
     const int64_t *target;
     const float *lse, *dloss, *scale;  // dloss nullptr: 1, and no scale
@@ -150,23 +154,40 @@ struct EpiXentGrad {
         const float l = counts ? lse[c.row()] * kLog2e : 0.0f;
         const float g = counts ? (dloss ? dloss[c.row()] / *scale : 1.0f) : 0.0f;
         const int64_t yc = y - v0 - n0;
+        auto finish = [&](int cc, const uint32_t *v) {
+            float x[32];
+            uint32_t p[16];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                x[j] = exp2f(fmaf(__uint_as_float(v[j]), kLog2e, -l));
+                if (yc == cc + j) x[j] -= 1.0f;
+                x[j] = counts ? x[j] * g : 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) p[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
+            put_rows32(c, &maps.c[0], nullptr, 0, n0 + cc, p);
+        };
+        if constexpr (Cfg::ROUND > 0) {
+            float f[Cfg::EPI_COLS];
+            if (!acc_sum_unit<Cfg>(acc, col0, cols, f)) return false;
+#pragma unroll
+            for (int b = 0; b < Cfg::EPI_COLS / 32; ++b) {
+                if (32 * b >= cols) break;
+                uint32_t v[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(f[32 * b + j]);
+                finish(32 * b, v);
+            }
+            return true;
+        }
         if (!acc.wait()) return false;
         const uint32_t t_row = acc.row() + col0;
 #pragma unroll 1
         for (int cc = 0; cc < cols; cc += 32) {
-            uint32_t v[32], p[16];
+            uint32_t v[32];
             acc_cols32(t_row + cc, have, v);
             if (cc + 32 >= cols) acc.release();
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                float x = exp2f(fmaf(__uint_as_float(v[j]), kLog2e, -l));
-                if (yc == cc + j) x -= 1.0f;
-                v[j] = __float_as_uint(counts ? x * g : 0.0f);
-            }
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                p[j] = pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-            put_rows32(c, &maps.c[0], nullptr, 0, n0 + cc, p);
+            finish(cc, v);
         }
         return true;
     }
@@ -387,7 +408,7 @@ struct FewCfg {
     static constexpr int ROOM =
         (CTAS == 2 ? kSmemPerSm / 2 - kSmemReservedPerBlock : 232448) - 3072;
     static constexpr int STAGES = ROOM / STAGE_BYTES;
-    static constexpr int ROUND = 16;  // K steps of a round: 1024 products, as above
+    static constexpr int ROUND = kStatsRound / 64;  // K steps of a round
     static constexpr int BAR_OFFSET = STAGES * STAGE_BYTES;
     static constexpr int SMEM_BYTES =
         smem_request(BAR_OFFSET + (2 * STAGES + 5) * 8 + 16 + 1024, CTAS);
@@ -698,9 +719,10 @@ static pgemm_status launch_few(const OpDevice &dev, FewArgs a, const OpMat &X, c
 constexpr int kFewMax = 64;
 constexpr int kFewEvenD = 512;  // from here on every CTA gets the same number of tiles
 
-// rounds of 1024 products for the statistics
-using StatsPair = OpCfg<256, 3, 2, 2, false, true, false, 8>;
-using StatsOne = OpCfg<128, 6, 1, 1, false, true, false, 16>;
+// the statistics' tiles (rounds of kStatsRound products), and P's where D is no longer
+// than a round
+using StatsPair = OpCfg<256, 3, 2, 2, false, true, false, kStatsRound / 128>;
+using StatsOne = OpCfg<128, 6, 1, 1, false, true, false, kStatsRound / 64>;
 using XentPair = OpCfg<256, 3, 2, 2, false, true>;
 using XentOne = OpCfg<128, 6, 1, 1, false, true>;
 
@@ -910,9 +932,13 @@ static pgemm_status xent(int T, int V, int D, const uint16_t *X, const uint16_t 
             st = op_encode_out(&maps.c[0], OpElem::BF16, P, cols, T, piece);
             if (st != PGEMM_OK) return st;
             const EpiXentGrad e{target, lse_buf, dloss, scale, v0, V};
-            st = op_use_pair(dev, T, cols, D, 256, 128)
-                     ? launch_logits<XentPair>(dev, T, cols, D, x, w, v0, maps, e, s)
-                     : launch_logits<XentOne>(dev, T, cols, D, x, w, v0, maps, e, s);
+            const bool two = op_use_pair(dev, T, cols, D, 256, 128);
+            if (D > kStatsRound)
+                st = two ? launch_logits<StatsPair>(dev, T, cols, D, x, w, v0, maps, e, s)
+                         : launch_logits<StatsOne>(dev, T, cols, D, x, w, v0, maps, e, s);
+            else
+                st = two ? launch_logits<XentPair>(dev, T, cols, D, x, w, v0, maps, e, s)
+                         : launch_logits<XentOne>(dev, T, cols, D, x, w, v0, maps, e, s);
         }
         if (st != PGEMM_OK) return st;
         shape(cols);

@@ -287,3 +287,26 @@ def test_gelu_gradient_of_the_tail(kept):
     d = Phi + zd * phi
     bound = 2.0 ** -7 * (1 + 2.0 ** -8) * d.abs() + 2.0 ** -13 * (Phi + zd.abs() * phi) + 2.0 ** -110
     assert ((db.double() - d).abs() <= bound).all()
+
+
+# ----------------------------------------------- P of pieces and the sums it divides by ---
+@pytest.mark.parametrize("T", [40, 100, 1100])
+@pytest.mark.parametrize("workspace", [0, 1])
+def test_xent_probabilities_share_the_sums_of_their_statistics(T, workspace):
+    # All products are positive, logits about 24 with a deviation of 0.2: a sum that the
+    # tensor core truncates 512 times ends some 512 / 2 * 2^-24 * 24 = 3.7e-4 short, and a
+    # probability taken from it against a log-sum-exp of shorter rounds as much of itself.
+    # With the same rounds both shorten alike.  Rows of dW of tokens that are no target
+    # are then off by roundings to nearest alone, which average out over 1e5 and more
+    # probabilities (2^-9 / 300 = 6e-6), by lse's own in fp32 (2e-6, twice) and by 2^-11 of
+    # kept exponentials, rounded to nearest too.
+    V, D = 2500, 8192
+    X = (positive(61, T, D).float() * (24 / (0.5625 * D))).to(torch.bfloat16)
+    W = positive(62, V, D)
+    y = torch.zeros(T, device="cuda", dtype=torch.int64)
+    dW = nan_like(V, D)
+    pg.xent_bf16_grad(T, V, D, X, W, y, None, None, None, None, dW, workspace_bytes=workspace)
+    p = torch.softmax(X.double() @ W.double().t(), 1)
+    want = p[:, 1:].t() @ X.double()
+    off = ((dW[1:].double() - want) / want).mean().item()
+    assert abs(off) < 3e-5, off
