@@ -95,8 +95,12 @@ struct EpiXentStats {
         float mx[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
         for (int j = 4; j < COLS; ++j) mx[j & 3] = fmaxf(mx[j & 3], v[j]);
-        const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kLog2e -
-                        (KEEP ? kKeepShift : 0.0f);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        // (KEEP: 2^-22 of itself more than its two roundings could take from it, so that the
+        // exponentials of logits of millions stay within fp16 too)
+        float m = top * kLog2e;
+        if (KEEP && top != -CUDART_INF_F)
+            m = fmaf(fabsf(top), kLog2e * 2.384185791015625e-7f, m) - kKeepShift;
         // nothing but -inf: any finite reference gives sums of zero
         const float ref = m == -CUDART_INF_F ? 0.0f : m;
         // +inf among them: less itself it is no number, but the sum is infinite, unless

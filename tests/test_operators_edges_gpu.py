@@ -310,3 +310,47 @@ def test_xent_probabilities_share_the_sums_of_their_statistics(T, workspace):
     want = p[:, 1:].t() @ X.double()
     off = ((dW[1:].double() - want) / want).mean().item()
     assert abs(off) < 3e-5, off
+
+
+@pytest.mark.parametrize("T", [100, 1100])
+def test_xent_of_logits_in_the_millions_stays_finite(T):
+    # a logit's own rounding is some units here, so that nothing but the order of
+    # magnitude of a probability is left: at most e^16 of lse's rounding at 2^27
+    V, D = 600, 8
+    X = torch.zeros(T, D, device="cuda", dtype=torch.bfloat16)
+    X[:, 0] = positive(71, T) * 2.0 ** 13
+    W = torch.zeros(V, D, device="cuda", dtype=torch.bfloat16)
+    W[:, 0] = 2.0 ** 13
+    W[:, 1:] = rnd(72, V, D - 1)
+    y = torch.randint(0, V, (T,), device="cuda")
+    loss, lse = nan_like(T, dtype=torch.float32), nan_like(T, dtype=torch.float32)
+    dX, dW = nan_like(T, D), nan_like(V, D)
+    for sign in (1, -1):
+        pg.xent_bf16_grad(T, V, D, sign * X, W, y, None, loss, lse, dX, dW)
+        want = torch.logsumexp(sign * X.double() @ W.double().t(), 1)
+        assert ((lse.double() - want).abs() <= 2.0 ** -22 * want.abs()).all()
+        assert all(t.isfinite().all() for t in (loss, dX, dW))
+
+
+@pytest.mark.parametrize("T", [9, 100, 1100])
+@pytest.mark.parametrize("workspace", [0, 1])
+def test_xent_gradient_beside_blocks_of_minus_infinity(T, workspace):
+    # whole column blocks of -inf logits, whose tokens have no probability (dX is left
+    # out: it would multiply their zeros by their infinite weights)
+    V, D = 1024, 8
+    X = torch.ones(T, D, device="cuda", dtype=torch.bfloat16)
+    W = torch.full((V, D), float("-inf"), device="cuda", dtype=torch.bfloat16)
+    W[512:640] = -40.0
+    y = torch.arange(T, device="cuda") % 128 + 512
+    loss, lse, dW = nan_like(T, dtype=torch.float32), nan_like(T, dtype=torch.float32), nan_like(V, D)
+    pg.xent_bf16_grad(T, V, D, X, W, y, None, loss, lse, None, dW, workspace_bytes=workspace)
+    log = torch.log(torch.tensor(128.0, dtype=torch.float64)).item()
+    assert ((lse.double() - (log - 320)).abs() <= 2.0 ** -22 * 320).all()
+    assert ((loss.double() - log).abs() <= 2.0 ** -21 * 320).all()
+    p = torch.full((T, V), 0.0, device="cuda", dtype=torch.float64)
+    p[:, 512:640] = 1 / 128
+    p[torch.arange(T, device="cuda"), y] -= 1.0
+    want = p.t() @ X.double()
+    # P: two roundings to 2^-8 and what 2^-21 of 320 and 2^-11 make of an exponential
+    bound = (2.0 ** -8 * 2 + 2.0 ** -10) * (p.abs().t() @ X.double()) + 2.0 ** -8 * want.abs()
+    assert ((dW.double() - want).abs() <= bound).all()
