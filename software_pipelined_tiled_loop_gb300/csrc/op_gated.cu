@@ -203,12 +203,10 @@ static pgemm_status launch_dual_size(const OpDevice &dev, int M, int F, int K, c
                 : launch_dual<DualOne>(dev, M, F, K, X, Wg, Wu, maps, e, s);
 }
 
-static bool act_known(int act) { return act >= PGEMM_ACT_NONE && act <= PGEMM_ACT_SILU; }
-
 static pgemm_status gated_forward(int M, int F, int K, const uint16_t *X, const uint16_t *Wg,
                                   const uint16_t *Wu, int act, uint16_t *H, float *preact,
                                   cudaStream_t s) {
-    if (M < 0 || F < 0 || K < 0 || !act_known(act)) return PGEMM_ERR_INVALID_VALUE;
+    if (M < 0 || F < 0 || K < 0 || !op_act_known(act)) return PGEMM_ERR_INVALID_VALUE;
     if (M == 0 || F == 0) return PGEMM_OK;
     if (!H || (K > 0 && (!X || !Wg || !Wu))) return PGEMM_ERR_INVALID_VALUE;
     if (!op_aligned16(X) || !op_aligned16(Wg) || !op_aligned16(Wu) || !op_aligned16(H) ||
@@ -254,7 +252,7 @@ static pgemm_status gated_backward(int M, int F, int K, const uint16_t *X, const
                                    const uint16_t *Wu, int act, const uint16_t *dH,
                                    const float *preact, uint16_t *dX, uint16_t *dWg,
                                    uint16_t *dWu, cudaStream_t s) {
-    if (M < 0 || F < 0 || K < 0 || !act_known(act)) return PGEMM_ERR_INVALID_VALUE;
+    if (M < 0 || F < 0 || K < 0 || !op_act_known(act)) return PGEMM_ERR_INVALID_VALUE;
     if ((dWg == nullptr) != (dWu == nullptr)) return PGEMM_ERR_INVALID_VALUE;
     const bool want_x = dX && M > 0 && K > 0, want_w = dWg && K > 0 && F > 0;
     if (!want_x && !want_w) return PGEMM_OK;  // K > 0 from here on

@@ -39,6 +39,7 @@ cudaError_t launch_repack(const void *src0, long long sld0, void *dst0, long lon
 inline long long op_round_up(long long v, long long m) { return (v + m - 1) / m * m; }
 // ceil(v / m): v up to 2^31 - 1 would overflow in 32 bits
 inline int op_blocks(long long v, long long m) { return static_cast<int>((v + m - 1) / m); }
+inline bool op_act_known(int act) { return act >= PGEMM_ACT_NONE && act <= PGEMM_ACT_SILU; }
 inline bool op_aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Stream-ordered scratch of one call: sizes are added first, allocated in one

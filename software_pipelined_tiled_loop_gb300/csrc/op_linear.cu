@@ -108,12 +108,10 @@ static pgemm_status launch_grad(const OpDevice &dev, int M, int N, int K, const 
     return op_launch<Cfg, EpiLinearGrad>(dev, maps, a, e, s);
 }
 
-static bool act_known(int act) { return act >= PGEMM_ACT_NONE && act <= PGEMM_ACT_SILU; }
-
 static pgemm_status linear_forward(int M, int N, int K, const uint16_t *X, const uint16_t *W,
                                    const uint16_t *bias, int act, const uint16_t *residual,
                                    uint16_t *Y, float *preact, cudaStream_t s) {
-    if (M < 0 || N < 0 || K < 0 || !act_known(act)) return PGEMM_ERR_INVALID_VALUE;
+    if (M < 0 || N < 0 || K < 0 || !op_act_known(act)) return PGEMM_ERR_INVALID_VALUE;
     if (M == 0 || N == 0) return PGEMM_OK;
     if (!Y || (K > 0 && (!X || !W))) return PGEMM_ERR_INVALID_VALUE;
     if (!op_aligned16(X) || !op_aligned16(W) || !op_aligned16(bias) || !op_aligned16(residual) ||
@@ -154,7 +152,7 @@ static pgemm_status linear_backward(int M, int N, int K, const uint16_t *X, cons
                                     const uint16_t *bias, int act, const uint16_t *dY,
                                     const float *preact, uint16_t *dX, uint16_t *dW,
                                     uint16_t *dbias, cudaStream_t s) {
-    if (M < 0 || N < 0 || K < 0 || !act_known(act)) return PGEMM_ERR_INVALID_VALUE;
+    if (M < 0 || N < 0 || K < 0 || !op_act_known(act)) return PGEMM_ERR_INVALID_VALUE;
     const bool want_x = dX && M > 0 && K > 0, want_w = dW && K > 0 && N > 0;
     const bool want_b = dbias && N > 0;
     if (!want_x && !want_w && !want_b) return PGEMM_OK;

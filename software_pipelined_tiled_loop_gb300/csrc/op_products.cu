@@ -3,8 +3,6 @@
 // elementwise gradient pass in front of the gradient products.
 #include <cuda_runtime.h>
 
-#include <mutex>
-
 #include "op_act.cuh"
 #include "op_gemm.cuh"
 #include "op_host.h"
@@ -23,7 +21,7 @@ struct EpiOut {
     const float *scale;     // one device value that multiplies acc, or nullptr
     uint16_t *out[2];
     long long ldo;          // row length of out, residual and preact
-    long long parts_ld, parts_rows;
+    long long parts_rows;
     int parts_segments;
     int act;
     int tma_out, tma_preact;
@@ -266,12 +264,11 @@ static pgemm_status launch_form(const OpDevice &dev, const OpProduct &p, float *
     e.plain = !e.bias && !e.residual && !e.preact && e.act == PGEMM_ACT_NONE;
     if (parts_area != nullptr) {
         if (op_parts_ld(p.N) > 0x7fffffffll) return PGEMM_ERR_INVALID_VALUE;
-        e.parts_ld = op_parts_ld(p.N);
         e.parts_rows = op_parts_rows(p.M);
         e.parts_segments = p.n_segments;
         const pgemm_status st =
-            op_encode_out(&maps.c[0], OpElem::F32, parts_area, e.parts_ld,
-                          e.parts_rows * parts * p.n_segments, e.parts_ld);
+            op_encode_out(&maps.c[0], OpElem::F32, parts_area, op_parts_ld(p.N),
+                          e.parts_rows * parts * p.n_segments, op_parts_ld(p.N));
         if (st != PGEMM_OK) return st;
     } else {
         e.tma_out = p.N % 8 == 0;

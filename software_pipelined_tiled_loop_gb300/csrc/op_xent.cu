@@ -34,6 +34,7 @@
 
 #include <algorithm>
 
+#include "op_act.cuh"
 #include "op_gemm.cuh"
 #include "op_host.h"
 
@@ -41,13 +42,8 @@ namespace pg {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// For statistics: results below 2^-126 of the block's largest count as zero.
+// Statistics take ex2_ftz: results below 2^-126 of the block's largest count as zero.
 // Probabilities themselves take exp2f, which keeps subnormal results.
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // Softmax statistics are kept to base 2: m is the largest L log2(e) of a row's
 // column block (or 15 less, see KEEP), s the block's sum of 2^(L log2(e) - m).
@@ -117,8 +113,8 @@ struct EpiXentStats {
             uint32_t p[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-                const float a = ex2(fmaf(v[cc + 2 * j], kLog2e, -ref));
-                const float b = ex2(fmaf(v[cc + 2 * j + 1], kLog2e, -ref));
+                const float a = ex2_ftz(fmaf(v[cc + 2 * j], kLog2e, -ref));
+                const float b = ex2_ftz(fmaf(v[cc + 2 * j + 1], kLog2e, -ref));
                 s[(2 * j) & 3] += a;
                 s[(2 * j + 1) & 3] += b;
                 if constexpr (KEEP)
@@ -206,7 +202,7 @@ struct EpiXentGrad {
 __device__ __forceinline__ void join_ms(float &m, float &s, float m2, float s2) {
     const float n = fmaxf(m, m2);
     const float ref = fabsf(n) == CUDART_INF_F ? 0.0f : n;  // (+inf: an infinite sum)
-    s = s * ex2(m - ref) + s2 * ex2(m2 - ref);
+    s = s * ex2_ftz(m - ref) + s2 * ex2_ftz(m2 - ref);
     m = n;
 }
 
@@ -571,7 +567,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                 const float b = x[j] * kLog2e;
                 const float n = fmaxf(m[j], b);
                 const float ref = fabsf(n) == CUDART_INF_F ? 0.0f : n;
-                s[j] = fmaf(s[j], ex2(m[j] - ref), ex2(b - ref));
+                s[j] = fmaf(s[j], ex2_ftz(m[j] - ref), ex2_ftz(b - ref));
                 m[j] = n;
             }
         }
