@@ -256,7 +256,8 @@ PGEMM_API pgemm_status linear_bf16(int M, int N, int K, const uint16_t *X, const
 
 /* Gradients of linear_bf16 for dY (M x N): with Z = X W + bias and
  * dZ = dY * act'(Z) (rounded to bf16, as the products' operand),
- * dX (M x K) <- dZ W^T, dW (K x N) <- X^T dZ, dbias (N) <- column sums of dZ.
+ * dX (M x K) <- dZ W^T, dW (K x N) <- X^T dZ, dbias (N) <- column sums of dZ
+ * (unrounded where preact gives Z, of the bf16 operand where Z is computed again).
  * Any of the three may be NULL: not computed.  preact: what linear_bf16 kept,
  * or NULL: Z is computed again (act NONE needs neither).  X is read only for dW
  * and W only for dX, and both to compute Z again; what is not read may be NULL.

@@ -4,8 +4,8 @@
 // X Wg, the right half X Wu for the same columns, so X is read once and an
 // epilogue thread holds both values of every element it writes: H costs one pass of
 // the tensor core over X, and nothing goes to memory between the projections and
-// the product.  Tensor-bound: 4096 x 16384 x 4096 620 us, one call after another
-// (1.77 PFLOP/s, above the 1.69 that plain products sustain under the power cap).
+// the product.  Tensor-bound: 4096 x 16384 x 4096 624 us, one call after another
+// (1.76 PFLOP/s, above the 1.69 that plain products sustain under the power cap).
 #include "op_act.cuh"
 #include "op_gemm.cuh"
 #include "op_host.h"

@@ -839,10 +839,9 @@ static KernelInfo op_info() {
     return k;
 }
 
-// Sets the kernel up on the device (once), then launches it on `stream`.
-// Programmatic stream serialisation: every thread waits for the kernel before
-// it (grid_dependency_wait) ahead of its first access to memory, so only the
-// prologue (barriers, tensor memory) overlaps that kernel's tail.
+// Sets the kernel up on the device (once), then launches it on `stream` under
+// programmatic stream serialisation: the kernel waits for the one before it ahead of its
+// first access to memory, or with a.overlap at its end (op_begin).
 template <class Cfg, class Epi>
 static pgemm_status op_launch(const OpDevice &dev, const OpMaps &maps, OpArgs a, const Epi &epi,
                               cudaStream_t stream) {
@@ -884,7 +883,7 @@ static pgemm_status op_launch(const OpDevice &dev, const OpMaps &maps, OpArgs a,
                : PGEMM_ERR_CUDA;
 }
 
-// As op_launch launches: the kernel waits before it touches memory.
+// As op_launch launches: the kernel waits before it touches memory, or as op_begin says.
 template <class... KArgs, class... Args>
 static pgemm_status launch_small(void (*kernel)(KArgs...), dim3 grid, dim3 block,
                                  cudaStream_t s, Args... args) {

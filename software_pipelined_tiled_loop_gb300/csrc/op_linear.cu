@@ -1,6 +1,6 @@
 // linear_bf16: Y = act(X W + b) + R, and its gradients dX = dZ W^T, dW = X^T dZ and
 // db = colsum dZ with dZ = dY act'(Z).  Z is kept in fp32 (a bf16 Z would add an
-// error of 2^-9 of its size to the derivative) or computed again; keeping costs
+// error of up to 2^-8 of its size to the derivative) or computed again; keeping costs
 // 8 bytes an element of traffic, computing 2 K operations, even near K = 1000.
 #include "op_act.cuh"
 #include "op_gemm.cuh"

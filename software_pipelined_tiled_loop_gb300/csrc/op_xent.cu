@@ -8,7 +8,7 @@
 // P is rounded to bf16 as an operand of the last two products; c is what keeps
 // that rounding from adding up.  A row's entry at its target is nearly -dloss_t
 // and outweighs the rest of the row; with dloss the same for all rows (a mean)
-// every one of them would round by the same up to 2^-9 of itself, and the whole
+// every one of them would round by the same up to 2^-8 of itself, and the whole
 // gradient with them.  Divided by c those entries start from exactly -1; c
 // itself multiplies the sums in fp32.
 //
