@@ -315,6 +315,123 @@ PGEMM_API pgemm_status xent_bf16_grad(int T, int V, int D, const uint16_t *X, co
                                       float *lse, uint16_t *dX, uint16_t *dW,
                                       long long workspace_bytes, pgemm_stream_t stream);
 
+/* Root-mean-square norm with the residual's addition: S <- X + residual, and
+ * y = S gain / sqrt(mean over the row of S^2 + eps) to Y.  X, residual (NULL:
+ * none), S (NULL: not kept; may be X or the residual) and Y are T x D, gain D
+ * (NULL: ones).  S is rounded to bf16, and y is made of that.  eps >= 0.
+ * D <= 32768 (else PGEMM_ERR_TOO_LARGE). */
+PGEMM_API pgemm_status rmsnorm_bf16(int T, int D, const uint16_t *X, const uint16_t *residual,
+                                    const uint16_t *gain, float eps, uint16_t *S, uint16_t *Y,
+                                    pgemm_stream_t stream);
+
+/* The same with y as int8, for gemm_i8: scale[t] = max over the row of |y| / 127,
+ * Q = y / scale[t] rounded to the nearest integer (ties to even), so that y is about
+ * Q * scale[t].  A row of zeros has scale 0; a row with an infinity or a NaN in y has
+ * scale NaN and Q 0. */
+PGEMM_API pgemm_status rmsnorm_i8(int T, int D, const uint16_t *X, const uint16_t *residual,
+                                  const uint16_t *gain, float eps, uint16_t *S, int8_t *Q,
+                                  float *scale, pgemm_stream_t stream);
+
+/* Gradients of rmsnorm_bf16 for dY (T x D), from S as it was kept (without a
+ * residual: X): with n = S / sqrt(mean(S^2) + eps) and a = dY * gain, each row of
+ * dX <- dS + (a - n mean(a n)) / sqrt(mean(S^2) + eps) and dgain (D) <- the sum over
+ * rows of dY * n.  dS (NULL: none): what else flows back into S; may be dX itself.  dX
+ * is the gradient of X and of the residual alike.  dX or dgain may be NULL. */
+PGEMM_API pgemm_status rmsnorm_bf16_backward(int T, int D, const uint16_t *S, const uint16_t *gain,
+                                             float eps, const uint16_t *dY, const uint16_t *dS,
+                                             uint16_t *dX, uint16_t *dgain, pgemm_stream_t stream);
+
+/* Routing of T tokens to k of E experts by logits (T x E fp32, as gemm_bf16 leaves
+ * them): experts (T x k) <- the k largest of a row, in descending order, ties to the
+ * lowest index; weights (T x k) <- their softmax, over the chosen (normalise != 0) or
+ * over all E (normalise == 0).  An expert whose logit is -inf is closed: where fewer
+ * than k are open, the last choices are -1 with weight 0.  A NaN ranks above all and
+ * makes the row's weights NaN.  1 <= k <= E; E <= 1024 and k <= 32 (else
+ * PGEMM_ERR_TOO_LARGE). */
+PGEMM_API pgemm_status route_topk(int T, int E, int k, const float *logits, int normalise,
+                                  int32_t *experts, float *weights, pgemm_stream_t stream);
+
+/* Gradient of route_topk's weights for dweights (T x k) into dlogits (T x E), with the
+ * choices as it made them (a choice outside [0, E) does not count). */
+PGEMM_API pgemm_status route_topk_backward(int T, int E, int k, const float *logits,
+                                           int normalise, const int32_t *experts,
+                                           const float *dweights, float *dlogits,
+                                           pgemm_stream_t stream);
+
+/* Sorts the T k slots (token t's j-th choice) by expert, slots of one expert in their
+ * order: offsets (E + 1) <- the first row of each expert and the number of rows,
+ * slot_row (T x k) <- each slot's row, or -1 where experts (T x k) is outside [0, E).
+ * E <= 1024, T k < 2^31 (else PGEMM_ERR_TOO_LARGE). */
+PGEMM_API pgemm_status expert_sort(int T, int E, int k, const int32_t *experts, int32_t *offsets,
+                                   int32_t *slot_row, pgemm_stream_t stream);
+
+/* Tokens to their rows: Xs[slot_row[t][j]] <- X[t].  X is T x D, Xs T k x D; rows that
+ * no slot has stay as they were, and a slot_row outside [0, T k) does not count.  Its
+ * gradient is expert_combine_bf16 without weights and residual. */
+PGEMM_API pgemm_status expert_gather_bf16(int T, int k, int D, const uint16_t *X,
+                                          const int32_t *slot_row, uint16_t *Xs,
+                                          pgemm_stream_t stream);
+
+/* Rows back to their tokens: Y[t] <- residual[t] + sum over j of weights[t][j]
+ * Ys[slot_row[t][j]], in the order of j.  Ys is T k x D, residual (NULL: none; may be Y)
+ * and Y T x D, weights T x k fp32 (NULL: ones).  A slot_row outside [0, T k) does not
+ * count: a token without any keeps its residual, or zero. */
+PGEMM_API pgemm_status expert_combine_bf16(int T, int k, int D, const uint16_t *Ys,
+                                           const int32_t *slot_row, const float *weights,
+                                           const uint16_t *residual, uint16_t *Y,
+                                           pgemm_stream_t stream);
+
+/* Gradients of expert_combine_bf16 for dY (T x D): dYs[slot_row[t][j]] <-
+ * weights[t][j] dY[t] (other rows stay as they were), dweights[t][j] <- the dot product
+ * of dY[t] and Ys[slot_row[t][j]] (0 where the slot does not count).  Either may be
+ * NULL; Ys is read only for dweights.  No two slots may have the same row.  The
+ * residual's gradient is dY. */
+PGEMM_API pgemm_status expert_combine_bf16_backward(int T, int k, int D, const uint16_t *Ys,
+                                                    const int32_t *slot_row, const float *weights,
+                                                    const uint16_t *dY, uint16_t *dYs,
+                                                    float *dweights, pgemm_stream_t stream);
+
+/* Products of rows sorted by expert: Y[r] <- X[r] W[e] for the rows offsets[e] <= r <
+ * offsets[e + 1] of expert e.  X is R x K, W E x K x N, Y R x N; offsets (E + 1, on the
+ * device) as expert_sort leaves them: not decreasing, at most R (what is beyond R counts
+ * as R, below 0 as 0).  Rows of Y from offsets[E] on stay as they were.  No host
+ * synchronisation.  K == 0 counts the products as zero.  E <= 1024, E K < 2^31 (else
+ * PGEMM_ERR_TOO_LARGE). */
+PGEMM_API pgemm_status experts_linear_bf16(int R, int N, int K, int E, const int32_t *offsets,
+                                           const uint16_t *X, const uint16_t *W, uint16_t *Y,
+                                           pgemm_stream_t stream);
+
+/* Gradients of experts_linear_bf16 for dY (R x N): dX (R x K) <- dY W[e]^T row by row
+ * (rows from offsets[E] on stay as they were), dW (E x K x N) <- X_e^T dY_e over the
+ * expert's rows (zeros without any).  Either may be NULL; X is read only for dW and W
+ * only for dX. */
+PGEMM_API pgemm_status experts_linear_bf16_backward(int R, int N, int K, int E,
+                                                    const int32_t *offsets, const uint16_t *X,
+                                                    const uint16_t *W, const uint16_t *dY,
+                                                    uint16_t *dX, uint16_t *dW,
+                                                    pgemm_stream_t stream);
+
+/* H[r] <- act(X[r] Wg[e]) * (X[r] Wu[e]), as experts_linear_bf16: Wg and Wu are E x K x F,
+ * H R x F.  preact (NULL: not kept): 2 x R x F fp32, receives both products for
+ * experts_gated_bf16_backward.  act is not PGEMM_ACT_RELU, whose derivative would hang on
+ * the rounding of sums next to zero. */
+PGEMM_API pgemm_status experts_gated_bf16(int R, int F, int K, int E, const int32_t *offsets,
+                                          const uint16_t *X, const uint16_t *Wg,
+                                          const uint16_t *Wu, int act, uint16_t *H, float *preact,
+                                          pgemm_stream_t stream);
+
+/* Gradients of experts_gated_bf16 for dH (R x F): dG and dU as gated_bf16_backward's
+ * (rounded to bf16), dX (R x K) <- dG Wg[e]^T + dU Wu[e]^T, dWg and dWu (E x K x F) <-
+ * X_e^T dG_e, X_e^T dU_e.  dX, or dWg and dWu together, may be NULL.  preact: what
+ * experts_gated_bf16 kept, or NULL: the products are computed again.  X is read only for
+ * dWg and dWu, Wg and Wu only for dX, and all three to compute the products again. */
+PGEMM_API pgemm_status experts_gated_bf16_backward(int R, int F, int K, int E,
+                                                   const int32_t *offsets, const uint16_t *X,
+                                                   const uint16_t *Wg, const uint16_t *Wu, int act,
+                                                   const uint16_t *dH, const float *preact,
+                                                   uint16_t *dX, uint16_t *dWg, uint16_t *dWu,
+                                                   pgemm_stream_t stream);
+
 /* The configuration the library picks for a shape (the per-shape table). */
 PGEMM_API pgemm_status pgemm_default_config(pgemm_dtype dtype, int M, int N, int K, pgemm_config *out);
 

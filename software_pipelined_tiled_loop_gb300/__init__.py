@@ -23,7 +23,10 @@ __all__ = [
     "pgemm_stage_reuse_demo", "pgemm_schedule", "pgemm_stream_k_plan", "pgemm_trim_scratch",
     "DTYPES", "STATUS", "EXPORTED", "PRODUCERS", "ENGINES", "ACTIVATIONS",
     "linear_bf16", "linear_bf16_backward", "gated_bf16", "gated_bf16_backward", "xent_bf16",
-    "xent_bf16_grad",
+    "xent_bf16_grad", "rmsnorm_bf16", "rmsnorm_i8", "rmsnorm_bf16_backward", "route_topk",
+    "route_topk_backward", "expert_sort", "expert_gather_bf16", "expert_combine_bf16",
+    "expert_combine_bf16_backward", "experts_linear_bf16", "experts_linear_bf16_backward",
+    "experts_gated_bf16", "experts_gated_bf16_backward",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -51,7 +54,10 @@ EXPORTED = [
     "pgemm_version", "gemm_i8_noalloc", "pgemm_stage_reuse_demo", "pgemm_schedule",
     "pgemm_stream_k_plan", "pgemm_trim_scratch",
     "linear_bf16", "linear_bf16_backward", "gated_bf16", "gated_bf16_backward", "xent_bf16",
-    "xent_bf16_grad",
+    "xent_bf16_grad", "rmsnorm_bf16", "rmsnorm_i8", "rmsnorm_bf16_backward", "route_topk",
+    "route_topk_backward", "expert_sort", "expert_gather_bf16", "expert_combine_bf16",
+    "expert_combine_bf16_backward", "experts_linear_bf16", "experts_linear_bf16_backward",
+    "experts_gated_bf16", "experts_gated_bf16_backward",
 ]
 
 
@@ -118,6 +124,19 @@ def _declare(L: ctypes.CDLL) -> ctypes.CDLL:
         "gated_bf16_backward": [i, i, i, vp, vp, vp, i, vp, vp, vp, vp, vp, vp],
         "xent_bf16": [i, i, i, vp, vp, vp, vp, vp, vp],
         "xent_bf16_grad": [i, i, i, vp, vp, vp, vp, vp, vp, vp, vp, ll, vp],
+        "rmsnorm_bf16": [i, i, vp, vp, vp, f, vp, vp, vp],
+        "rmsnorm_i8": [i, i, vp, vp, vp, f, vp, vp, vp, vp],
+        "rmsnorm_bf16_backward": [i, i, vp, vp, f, vp, vp, vp, vp, vp],
+        "route_topk": [i, i, i, vp, i, vp, vp, vp],
+        "route_topk_backward": [i, i, i, vp, i, vp, vp, vp, vp],
+        "expert_sort": [i, i, i, vp, vp, vp, vp],
+        "expert_gather_bf16": [i, i, i, vp, vp, vp, vp],
+        "expert_combine_bf16": [i, i, i, vp, vp, vp, vp, vp, vp],
+        "expert_combine_bf16_backward": [i, i, i, vp, vp, vp, vp, vp, vp, vp],
+        "experts_linear_bf16": [i, i, i, i, vp, vp, vp, vp, vp],
+        "experts_linear_bf16_backward": [i, i, i, i, vp, vp, vp, vp, vp, vp, vp],
+        "experts_gated_bf16": [i, i, i, i, vp, vp, vp, vp, i, vp, vp, vp],
+        "experts_gated_bf16_backward": [i, i, i, i, vp, vp, vp, vp, i, vp, vp, vp, vp, vp, vp],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -257,6 +276,8 @@ class _Kind:
 _BF16 = _Kind(2, "torch.bfloat16", "torch.int16", "torch.uint16")
 _F32 = _Kind(4, "torch.float32")
 _I64 = _Kind(8, "torch.int64")
+_I32 = _Kind(4, "torch.int32")
+_I8 = _Kind(1, "torch.int8")
 
 
 def _operand(x, name, count, kind) -> int:
@@ -377,6 +398,158 @@ def xent_bf16_grad(T, V, D, X, W, target, dloss, loss, lse, dX, dW, workspace_by
         _operand(loss, "loss", T, _F32), _operand(lse, "lse", T, _F32),
         _operand(dX, "dX", T * D, _BF16), _operand(dW, "dW", V * D, _BF16), int(workspace_bytes),
         _stream(stream)), "xent_bf16_grad")
+
+
+def rmsnorm_bf16(T, D, X, residual, gain, eps, S, Y, stream=None):
+    """S <- X + residual (bf16) and Y <- S * gain / sqrt(mean(S^2) + eps), row by row.
+    X, residual, S and Y: T x D; gain: D.  residual, gain (ones) and S (not kept; may be
+    X or residual) may be None.  Asynchronous on ``stream``."""
+    _sizes("rmsnorm_bf16", T | D)
+    _check(lib().rmsnorm_bf16(
+        T, D, _operand(X, "X", T * D, _BF16), _operand(residual, "residual", T * D, _BF16),
+        _operand(gain, "gain", D, _BF16), eps, _operand(S, "S", T * D, _BF16),
+        _operand(Y, "Y", T * D, _BF16), _stream(stream)), "rmsnorm_bf16")
+
+
+def rmsnorm_i8(T, D, X, residual, gain, eps, S, Q, scale, stream=None):
+    """rmsnorm_bf16 with the result as int8 (Q: T x D) and a scale a row (T fp32):
+    Q * scale is the result to within half a scale.  Asynchronous."""
+    _sizes("rmsnorm_i8", T | D)
+    _check(lib().rmsnorm_i8(
+        T, D, _operand(X, "X", T * D, _BF16), _operand(residual, "residual", T * D, _BF16),
+        _operand(gain, "gain", D, _BF16), eps, _operand(S, "S", T * D, _BF16),
+        _operand(Q, "Q", T * D, _I8), _operand(scale, "scale", T, _F32), _stream(stream)),
+        "rmsnorm_i8")
+
+
+def rmsnorm_bf16_backward(T, D, S, gain, eps, dY, dS, dX, dgain, stream=None):
+    """Gradients of rmsnorm_bf16 for dY (T x D) and, where S flows on, dS (or None) into
+    dX (the gradient of X and of the residual; may be dS) and dgain (D), either of which
+    may be None.  Asynchronous."""
+    _sizes("rmsnorm_bf16_backward", T | D)
+    _check(lib().rmsnorm_bf16_backward(
+        T, D, _operand(S, "S", T * D, _BF16), _operand(gain, "gain", D, _BF16), eps,
+        _operand(dY, "dY", T * D, _BF16), _operand(dS, "dS", T * D, _BF16),
+        _operand(dX, "dX", T * D, _BF16), _operand(dgain, "dgain", D, _BF16), _stream(stream)),
+        "rmsnorm_bf16_backward")
+
+
+def route_topk(T, E, k, logits, normalise, experts, weights, stream=None):
+    """The k largest of each token's E logits (T x E fp32) into experts (T x k int32, ties
+    to the lowest index, -1 where fewer are above -inf) and their softmax over the chosen
+    (``normalise``) or over all E into weights (T x k fp32).  Asynchronous."""
+    _sizes("route_topk", T | E | k)
+    _check(lib().route_topk(
+        T, E, k, _operand(logits, "logits", T * E, _F32), int(bool(normalise)),
+        _operand(experts, "experts", T * k, _I32), _operand(weights, "weights", T * k, _F32),
+        _stream(stream)), "route_topk")
+
+
+def route_topk_backward(T, E, k, logits, normalise, experts, dweights, dlogits, stream=None):
+    """Gradient of route_topk's weights for dweights (T x k) into dlogits (T x E); experts
+    as it left them.  Asynchronous."""
+    _sizes("route_topk_backward", T | E | k)
+    _check(lib().route_topk_backward(
+        T, E, k, _operand(logits, "logits", T * E, _F32), int(bool(normalise)),
+        _operand(experts, "experts", T * k, _I32), _operand(dweights, "dweights", T * k, _F32),
+        _operand(dlogits, "dlogits", T * E, _F32), _stream(stream)), "route_topk_backward")
+
+
+def expert_sort(T, E, k, experts, offsets, slot_row, stream=None):
+    """Sort the slots of experts (T x k int32) by expert, stably: offsets (E + 1 int32)
+    receives each expert's first row and the number of rows, slot_row (T x k int32) each
+    slot's row (-1: an expert outside [0, E)).  Asynchronous."""
+    _sizes("expert_sort", T | E | k)
+    _check(lib().expert_sort(
+        T, E, k, _operand(experts, "experts", T * k, _I32),
+        _operand(offsets, "offsets", E + 1, _I32), _operand(slot_row, "slot_row", T * k, _I32),
+        _stream(stream)), "expert_sort")
+
+
+def expert_gather_bf16(T, k, D, X, slot_row, Xs, stream=None):
+    """Xs[slot_row[t, j]] <- X[t].  X: T x D, Xs: T k x D (rows no slot has stay as they
+    were).  The gradient is expert_combine_bf16 without weights and residual.
+    Asynchronous."""
+    _sizes("expert_gather_bf16", T | k | D)
+    _check(lib().expert_gather_bf16(
+        T, k, D, _operand(X, "X", T * D, _BF16), _operand(slot_row, "slot_row", T * k, _I32),
+        _operand(Xs, "Xs", T * k * D, _BF16), _stream(stream)), "expert_gather_bf16")
+
+
+def expert_combine_bf16(T, k, D, Ys, slot_row, weights, residual, Y, stream=None):
+    """Y[t] <- residual[t] + sum over j of weights[t, j] * Ys[slot_row[t, j]].  Ys: T k x
+    D, weights: T x k fp32 or None (ones), residual: T x D or None (may be Y).
+    Asynchronous."""
+    _sizes("expert_combine_bf16", T | k | D)
+    _check(lib().expert_combine_bf16(
+        T, k, D, _operand(Ys, "Ys", T * k * D, _BF16),
+        _operand(slot_row, "slot_row", T * k, _I32), _operand(weights, "weights", T * k, _F32),
+        _operand(residual, "residual", T * D, _BF16), _operand(Y, "Y", T * D, _BF16),
+        _stream(stream)), "expert_combine_bf16")
+
+
+def expert_combine_bf16_backward(T, k, D, Ys, slot_row, weights, dY, dYs, dweights, stream=None):
+    """Gradients of expert_combine_bf16 for dY (T x D) into dYs (T k x D; rows no slot has
+    stay as they were) and dweights (T x k fp32), either of which may be None; Ys may be
+    None without dweights.  Asynchronous."""
+    _sizes("expert_combine_bf16_backward", T | k | D)
+    _check(lib().expert_combine_bf16_backward(
+        T, k, D, _operand(Ys, "Ys", T * k * D, _BF16),
+        _operand(slot_row, "slot_row", T * k, _I32), _operand(weights, "weights", T * k, _F32),
+        _operand(dY, "dY", T * D, _BF16), _operand(dYs, "dYs", T * k * D, _BF16),
+        _operand(dweights, "dweights", T * k, _F32), _stream(stream)),
+        "expert_combine_bf16_backward")
+
+
+def experts_linear_bf16(R, N, K, E, offsets, X, W, Y, stream=None):
+    """Y[r] <- X[r] @ W[e] for the rows offsets[e] <= r < offsets[e + 1] of expert e.  X: R
+    x K, W: E x K x N, Y: R x N (rows from offsets[E] on stay as they were), offsets: E + 1
+    int32, as expert_sort leaves them.  Asynchronous, without a host synchronisation."""
+    _sizes("experts_linear_bf16", R | N | K | E)
+    _check(lib().experts_linear_bf16(
+        R, N, K, E, _operand(offsets, "offsets", E + 1, _I32), _operand(X, "X", R * K, _BF16),
+        _operand(W, "W", E * K * N, _BF16), _operand(Y, "Y", R * N, _BF16), _stream(stream)),
+        "experts_linear_bf16")
+
+
+def experts_linear_bf16_backward(R, N, K, E, offsets, X, W, dY, dX, dW, stream=None):
+    """Gradients of experts_linear_bf16 for dY (R x N) into dX (R x K; rows from offsets[E]
+    on stay as they were) and dW (E x K x N), either of which may be None, and so may X
+    without dW and W without dX.  Asynchronous."""
+    _sizes("experts_linear_bf16_backward", R | N | K | E)
+    _check(lib().experts_linear_bf16_backward(
+        R, N, K, E, _operand(offsets, "offsets", E + 1, _I32), _operand(X, "X", R * K, _BF16),
+        _operand(W, "W", E * K * N, _BF16), _operand(dY, "dY", R * N, _BF16),
+        _operand(dX, "dX", R * K, _BF16), _operand(dW, "dW", E * K * N, _BF16), _stream(stream)),
+        "experts_linear_bf16_backward")
+
+
+def experts_gated_bf16(R, F, K, E, offsets, X, Wg, Wu, act, H, preact=None, stream=None):
+    """H[r] <- act(X[r] @ Wg[e]) * (X[r] @ Wu[e]) for the rows of each expert, as
+    experts_linear_bf16.  Wg and Wu: E x K x F, H: R x F; ``act``: a name of ACTIVATIONS but
+    relu.  ``preact`` (2 x R x F fp32) receives both products for the backward call.
+    Asynchronous."""
+    _sizes("experts_gated_bf16", R | F | K | E)
+    _check(lib().experts_gated_bf16(
+        R, F, K, E, _operand(offsets, "offsets", E + 1, _I32), _operand(X, "X", R * K, _BF16),
+        _operand(Wg, "Wg", E * K * F, _BF16), _operand(Wu, "Wu", E * K * F, _BF16), _act(act),
+        _operand(H, "H", R * F, _BF16), _operand(preact, "preact", 2 * R * F, _F32),
+        _stream(stream)), "experts_gated_bf16")
+
+
+def experts_gated_bf16_backward(R, F, K, E, offsets, X, Wg, Wu, act, dH, dX, dWg, dWu,
+                                preact=None, stream=None):
+    """Gradients of experts_gated_bf16 for dH (R x F) into dX (R x K), dWg and dWu (E x K x
+    F); dX, or dWg and dWu together, may be None, and so may X, Wg and Wu where nothing
+    wanted reads them.  ``preact``: what the forward call kept, or None to compute it
+    again.  Asynchronous."""
+    _sizes("experts_gated_bf16_backward", R | F | K | E)
+    _check(lib().experts_gated_bf16_backward(
+        R, F, K, E, _operand(offsets, "offsets", E + 1, _I32), _operand(X, "X", R * K, _BF16),
+        _operand(Wg, "Wg", E * K * F, _BF16), _operand(Wu, "Wu", E * K * F, _BF16), _act(act),
+        _operand(dH, "dH", R * F, _BF16), _operand(preact, "preact", 2 * R * F, _F32),
+        _operand(dX, "dX", R * K, _BF16), _operand(dWg, "dWg", E * K * F, _BF16),
+        _operand(dWu, "dWu", E * K * F, _BF16), _stream(stream)), "experts_gated_bf16_backward")
 
 
 def pgemm_stage_reuse_demo(X, rows, cols, perm, out, check_reuse, delay_warp=-1, delay_ns=0,

@@ -298,6 +298,22 @@ static pgemm_status encode_2d(CUtensorMap *map, CUtensorMapDataType type, int el
     return r == CUDA_SUCCESS ? PGEMM_OK : PGEMM_ERR_CUDA;
 }
 
+// `depth` bf16 matrices behind one another; boxes of one of them.
+static pgemm_status encode_3d(CUtensorMap *map, const void *base, long long inner, long long outer,
+                              long long depth, long long ld, int box_x, int box_y,
+                              CUtensorMapSwizzle swizzle) {
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer),
+                          static_cast<cuuint64_t>(depth)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2,
+                             static_cast<cuuint64_t>(ld) * 2 * static_cast<cuuint64_t>(outer)};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(box_x), static_cast<cuuint32_t>(box_y), 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims,
+                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? PGEMM_OK : PGEMM_ERR_CUDA;
+}
+
 static pgemm_status encode_2d(CUtensorMap *map, CUtensorMapDataType type, int elem_bytes,
                               const void *base, long long inner, long long outer, long long ld,
                               int box_x, int box_y, bool swizzle128) {
@@ -683,6 +699,16 @@ pgemm_status op_encode_out(CUtensorMap *map, OpElem type, const void *base, long
     return encode_2d(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                      f32 ? 4 : 2, base, inner, outer, ld, f32 ? 16 : 32, 32,
                      CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+pgemm_status op_encode_3d(CUtensorMap *map, const void *base, long long inner, long long outer,
+                          long long depth, long long ld, int box_y) {
+    return encode_3d(map, base, inner, outer, depth, ld, 64, box_y, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+pgemm_status op_encode_out_3d(CUtensorMap *map, const void *base, long long inner, long long outer,
+                              long long depth, long long ld) {
+    return encode_3d(map, base, inner, outer, depth, ld, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 // A block that waits, with a short limit, on an mbarrier nothing arrives on.

@@ -1,0 +1,1146 @@
+// The experts' products: rows sorted by expert, expert e's rows [offsets[e], offsets[e + 1])
+// times its own matrices.
+//
+//   experts_linear  Y[r] = X[r] W[e];  dX[r] = dY[r] W[e]^T, dW[e] = X_e^T dY_e
+//   experts_gated   H[r] = act(X[r] Wg[e]) * (X[r] Wu[e]); dG = dH U act'(G), dU = dH act(G),
+//                   dX = dG Wg^T + dU Wu^T, dWg[e] = X_e^T dG_e, dWu[e] = X_e^T dU_e
+//
+// The groups' sizes are known on the device alone: every CTA reads the offsets and works
+// out the same list of units, so a call needs no host round trip and can be captured.
+//
+// Rows (forward and dX): experts_rows_kernel.  The weights take the tensor core's M side,
+// D[n][t] = sum_k W[e][k][n] X[t][k]: A = W^T read M-major from the K x N rows (dX: the
+// same rows K-major), B = a group's rows K-major, N = as many of them as there are, rounded
+// up to 32 (16 on one CTA).  A group of 40 rows then costs 64 columns of products, where
+// 256-row tiles on the M side would pay for 256; groups are ragged in one direction only,
+// and the instruction's N follows them.  A group of more rows than a tile takes is dealt
+// out evenly.  A thread owns one feature of the output: a warp's store covers 32 features
+// of a row, full 32-byte sectors, so rows need no staging, no alignment and no tensor map,
+// and stop where the group does.
+//
+// Gated: a CTA's 128 accumulator lanes are 64 features of Wg and the same 64 of Wu, so the
+// two products of an element lie in lanes of different warps; each of the two warps hands
+// the other half of its columns through shared memory and finishes the other half.
+//
+// Weights' gradients: experts_weights_kernel, the tiled TN product with a group's rows
+// as its K range.  The range starts and ends anywhere; in its last K step the rows behind
+// the group (the next group's, which may hold anything) are cleared in shared memory.
+#include <algorithm>
+#include <climits>
+
+#include "op_act.cuh"
+#include "op_gemm.cuh"
+#include "op_host.h"
+
+namespace pg {
+
+constexpr int kExpertsMax = 1024;
+
+enum class Exp {
+    LINEAR,      // X W
+    GATED,       // act(X Wg) * (X Wu)
+    GATED_GRAD,  // dH U act'(G), dH act(G)
+    TRANSPOSED,  // sum over segments of X W^T
+};
+
+struct ExpertsMaps {
+    CUtensorMap x[2], w[2], c[2];
+};
+
+struct ExpertsArgs {
+    int R, E;             // rows at most; experts
+    int M;                // features of an output (gated: of one product)
+    int K;                // reduction columns of one segment
+    int k_tiles, k_seg;   // K steps over all segments, and of one
+    int f_tiles;          // tiles of features
+    const int32_t *offsets;
+    uint16_t *out, *out2;
+    long long ldo;        // row length of out and out2
+    float *preact;        // gated: both products, R x M each
+    const uint16_t *dy;   // gated gradient: R x M
+    int act;
+    int tma_out;          // weights' gradient: the outputs have tensor maps
+    int n_seg;            // weights' gradient: tiles along N of one output
+    int segments;         // and outputs
+};
+
+// CG CTAs work on a tile of CG * 128 accumulator lanes x up to TOK rows.
+template <int CG_, int TOK_, int STAGES_, Exp MODE_>
+struct ExpCfg {
+    static constexpr int CG = CG_, TOK = TOK_, STAGES = STAGES_, BK = 64, BM = 128;
+    static constexpr Exp MODE = MODE_;
+    static constexpr bool DUAL = MODE == Exp::GATED || MODE == Exp::GATED_GRAD;
+    static constexpr bool W_K = MODE == Exp::TRANSPOSED;  // W's rows run along the reduction
+    static constexpr int FEATS = DUAL ? 64 : 128;         // features of a CTA
+    static constexpr int STEP = 16 * CG;                  // granularity of a tile's rows
+    static constexpr int BOX = CG == 2 ? 32 : 16;         // rows of a TMA box
+    static constexpr int A_BYTES = BM * BK * 2, B_BYTES = TOK / CG * BK * 2;
+    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+    static constexpr int EPI = 8;
+    static constexpr int SWAP_BYTES = DUAL ? EPI * 2048 : 0;
+    static constexpr int SWAP_OFFSET = STAGES * STAGE_BYTES;
+    static constexpr int BAR_OFFSET = SWAP_OFFSET + SWAP_BYTES;
+    static constexpr int TABLE_OFFSET = BAR_OFFSET + (2 * STAGES + 5) * 8 + 24;
+    static constexpr int USED = TABLE_OFFSET + (3 * kExpertsMax + 1) * 4;
+    static constexpr int TMEM_COLS = 2 * TOK;
+    static constexpr int THREADS = 64 + 32 * EPI;
+    static constexpr int SMEM_BYTES = smem_request(USED + 1024, 1);
+    static_assert(USED + 1024 <= 232448, "shared memory");
+    static_assert(TOK % 32 == 0 && TMEM_COLS >= 32 && TMEM_COLS <= 512, "TOK");
+};
+
+// The list of units, the same in every CTA: begin[e], end[e] (clamped to the rows there
+// are) and first[e], the units before expert e's.
+struct ExpertsTable {
+    int32_t *begin, *end, *first;
+    int E;
+    __device__ __forceinline__ int units() const { return first[E]; }
+    // the expert of unit u
+    __device__ __forceinline__ int expert(int u) const {
+        int lo = 0, hi = E;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (first[mid] <= u)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        return lo;
+    }
+};
+
+// All threads; count(rows) gives an expert's units.
+template <class Count>
+__device__ __forceinline__ ExpertsTable experts_table(const ExpertsArgs &a, uint8_t *at,
+                                                      Count &&count) {
+    ExpertsTable t;
+    t.begin = reinterpret_cast<int32_t *>(at);
+    t.end = t.begin + kExpertsMax;
+    t.first = t.end + kExpertsMax;
+    t.E = a.E;
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        int before = 0;
+#pragma unroll 1
+        for (int e0 = 0; e0 < a.E; e0 += 32) {
+            const int e = e0 + lane;
+            int n = 0;
+            if (e < a.E) {
+                const int b = min(max(a.offsets[e], 0), a.R);
+                const int d = min(max(a.offsets[e + 1], b), a.R);
+                t.begin[e] = b;
+                t.end[e] = d;
+                n = count(d - b);
+            }
+            int sum = n;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, sum, d);
+                if (lane >= d) sum += o;
+            }
+            if (e < a.E) t.first[e] = before + sum - n;
+            before += __shfl_sync(0xffffffffu, sum, 31);
+        }
+        if (lane == 0) t.first[a.E] = before;
+    }
+    __syncthreads();
+    return t;
+}
+
+// One unit: rows [row0, row0 + rows) of an expert, `cols` accumulator columns, features
+// from f0 (the whole tile's).
+struct RowsUnit {
+    int expert, row0, rows, cols, f0;
+};
+
+template <class Cfg>
+__device__ __forceinline__ int row_tiles(int rows) {
+    return (rows + Cfg::TOK - 1) / Cfg::TOK;
+}
+
+// Units of an expert: down its tiles of rows, up to sixteen of them, then one tile of
+// features across, so that the CTAs running at once share panels of weights and of rows.
+template <class Cfg>
+__device__ __forceinline__ RowsUnit rows_unit(const ExpertsTable &t, const ExpertsArgs &a, int u) {
+    RowsUnit w;
+    w.expert = t.expert(u);
+    const int begin = t.begin[w.expert], n = t.end[w.expert] - begin;
+    const int r = u - t.first[w.expert];
+    const int tiles = row_tiles<Cfg>(n);
+    const int group = r / (16 * a.f_tiles), first = group * 16;
+    const int g = min(tiles - first, 16), q = r - group * 16 * a.f_tiles;
+    const int rt = first + q % g;
+    w.f0 = q / g * (Cfg::FEATS * Cfg::CG);
+    const int each = ((n + tiles - 1) / tiles + Cfg::STEP - 1) / Cfg::STEP * Cfg::STEP;
+    w.row0 = begin + rt * each;
+    w.rows = min(each, n - rt * each);
+    w.cols = (w.rows + Cfg::STEP - 1) / Cfg::STEP * Cfg::STEP;
+    return w;
+}
+
+__device__ __forceinline__ void put_bf16(uint16_t *p, float v) {
+    *p = static_cast<uint16_t>(pack_bf16(v, 0.0f) & 0xffffu);
+}
+
+template <class Cfg>
+__global__ void __launch_bounds__(Cfg::THREADS, 1)
+    experts_rows_kernel(const __grid_constant__ ExpertsMaps maps, const ExpertsArgs a,
+                        const KernelCtx ctx) {
+    constexpr int CG = Cfg::CG, STAGES = Cfg::STAGES, BK = Cfg::BK, TOK = Cfg::TOK;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = align_1024(smem_raw);
+    uint8_t *sA = smem, *sB = smem + STAGES * Cfg::A_BYTES;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + Cfg::BAR_OFFSET);
+    uint64_t *empty = full + STAGES;
+    uint64_t *acc_full = empty + STAGES;  // [2]
+    uint64_t *acc_empty = acc_full + 2;   // [2]
+    uint64_t *mma_done = acc_empty + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
+    const uint32_t warp = warp_id_uniform(), lane = lane_id();
+    if (warp == 0 && lane == 0) {
+        if (a.k_tiles > 0) {
+            prefetch_tmap(&maps.x[0]);
+            prefetch_tmap(&maps.w[0]);
+        }
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], Cfg::EPI * CG);
+        }
+        mbar_init(mma_done, 1);
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        if constexpr (CG == 2) {
+            tmem_alloc_pair(tmem_slot, Cfg::TMEM_COLS);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(tmem_slot, Cfg::TMEM_COLS);
+            tmem_relinquish();
+        }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if constexpr (CG == 2)
+        cluster_sync();
+    else
+        __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    op_begin(0);
+    const ExpertsTable table =
+        experts_table(a, smem + Cfg::TABLE_OFFSET,
+                      [&](int rows) { return row_tiles<Cfg>(rows) * a.f_tiles; });
+    const int units = table.units();
+    const int crank = CG == 2 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int slot = static_cast<int>(blockIdx.x) / CG;
+    const int slots = static_cast<int>(gridDim.x) / CG;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---------------- producer ----------------
+            uint32_t it = 0;
+            bool ok = true;
+            for (int u = slot; ok && u < units; u += slots) {
+                const RowsUnit w = rows_unit<Cfg>(table, a, u);
+                const int half = w.cols / CG;  // columns of B in this CTA
+                const int boxes = (half + Cfg::BOX - 1) / Cfg::BOX;
+                const int y0 = w.row0 + crank * half;
+                const uint32_t tx = CG * (Cfg::A_BYTES + boxes * Cfg::BOX * 128);
+                for (int kt = 0; kt < a.k_tiles; ++kt, ++it) {
+                    const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
+                    if (!mbar_wait(&empty[s], ph ^ 1u, ctx, kSiteProducerEmpty)) {
+                        ok = false;
+                        break;
+                    }
+                    const int sg = kt >= a.k_seg ? 1 : 0, k0 = (kt - sg * a.k_seg) * BK;
+                    const uint32_t lead =
+                        CG == 2 ? mapa_shared(smem_u32(&full[s]), 0) : smem_u32(&full[s]);
+                    if (crank == 0) mbar_arrive_expect_tx(&full[s], tx);
+                    auto load_w = [&](uint8_t *dst, const CUtensorMap *map, int x, int y) {
+                        if constexpr (CG == 2)
+                            tma_load_3d_pair(dst, map, lead, x, y, w.expert);
+                        else
+                            tma_load_3d(dst, map, &full[s], x, y, w.expert);
+                    };
+                    uint8_t *da = sA + s * Cfg::A_BYTES, *db = sB + s * Cfg::B_BYTES;
+                    if constexpr (Cfg::W_K) {
+                        load_w(da, &maps.w[sg], k0, w.f0 + crank * 128);
+                    } else if constexpr (Cfg::DUAL) {
+                        load_w(da, &maps.w[0], w.f0 + crank * 64, k0);
+                        load_w(da + BK * 128, &maps.w[1], w.f0 + crank * 64, k0);
+                    } else {
+                        load_w(da, &maps.w[0], w.f0 + crank * 128, k0);
+                        load_w(da + BK * 128, &maps.w[0], w.f0 + crank * 128 + 64, k0);
+                    }
+                    for (int j = 0; j < boxes; ++j) {
+                        uint8_t *dst = db + j * (Cfg::BOX * 128);
+                        if constexpr (CG == 2)
+                            tma_load_2d_pair(dst, &maps.x[sg], lead, k0, y0 + j * Cfg::BOX);
+                        else
+                            tma_load_2d(dst, &maps.x[sg], &full[s], k0, y0 + j * Cfg::BOX);
+                    }
+                }
+            }
+            if constexpr (CG == 2) {
+                // the pair's last multicast releases of this CTA's barriers must
+                // have landed before the cluster is left
+                for (int i = 0; ok && i < STAGES; ++i, ++it) {
+                    const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
+                    ok = mbar_wait(&empty[s], ph ^ 1u, ctx, kSiteProducerEmpty);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && crank == 0) {
+            // ---------------- MMA issuer ----------------
+            constexpr uint16_t kPair = 3;
+            uint32_t it = 0, n = 0;
+            bool ok = true;
+            for (int u = slot; ok && u < units && a.k_tiles > 0; u += slots, ++n) {
+                const RowsUnit w = rows_unit<Cfg>(table, a, u);
+                const uint32_t idesc =
+                    idesc_f16(Cfg::BM * CG, w.cols, 1, Cfg::W_K ? 0 : 1, /*B K-major*/ 0);
+                const uint32_t ab = n & 1u;
+                if (!mbar_wait(&acc_empty[ab], ((n >> 1) & 1u) ^ 1u, ctx, kSiteMmaAccEmpty)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d = tmem + ab * TOK;
+                for (int kt = 0; kt < a.k_tiles; ++kt, ++it) {
+                    const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
+                    if (!mbar_wait(&full[s], ph, ctx, kSiteMmaFull)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = smem_u32(sA + s * Cfg::A_BYTES);
+                    const uint32_t sb = smem_u32(sB + s * Cfg::B_BYTES);
+#pragma unroll
+                    for (int k = 0; k < BK / 16; ++k) {
+                        const uint64_t ad = Cfg::W_K
+                                                ? smem_desc_sw128(sa + k * 32, 16, 1024)
+                                                : smem_desc_sw128(sa + k * 2048, BK * 128, 1024);
+                        const uint64_t bd = smem_desc_sw128(sb + k * 32, 16, 1024);
+                        const uint32_t acc = (kt == 0 && k == 0) ? 0u : 1u;
+                        if constexpr (CG == 2)
+                            umma_f16_ss_pair(d, ad, bd, idesc, acc);
+                        else
+                            umma_f16_ss(d, ad, bd, idesc, acc);
+                    }
+                    if constexpr (CG == 2)
+                        umma_commit_pair_multicast(&empty[s], kPair);
+                    else
+                        umma_commit(&empty[s]);
+                }
+                if (ok) {
+                    if constexpr (CG == 2)
+                        umma_commit_pair_multicast(&acc_full[ab], kPair);
+                    else
+                        umma_commit(&acc_full[ab]);
+                }
+            }
+            if constexpr (CG == 2)
+                umma_commit_pair_multicast(mma_done, 1);
+            else
+                umma_commit(mma_done);
+            mbar_wait(mma_done, 0, ctx, kSiteMmaDone);
+        }
+    } else {
+        // ---------------- epilogue ----------------
+        const int e = static_cast<int>(warp) - 2, h = e >> 2;
+        const uint32_t q = warp & 3u;  // the TMEM lane quadrant this warp may read
+        // gated: quadrants 0 and 1 hold Wg's 64 features, 2 and 3 Wu's
+        const bool gate = q < 2;
+        const int lane_feat = Cfg::DUAL ? static_cast<int>((q & 1u) * 32 + lane)
+                                        : static_cast<int>(q * 32 + lane);
+        float *swap = reinterpret_cast<float *>(smem + Cfg::SWAP_OFFSET) + lane;
+        uint32_t n = 0, turn = 0;
+        bool ok = true;  // a wait that ran out: the rest goes by unread, barriers and all
+        for (int u = slot; u < units; u += slots, ++n) {
+            const RowsUnit w = rows_unit<Cfg>(table, a, u);
+            const int feat = w.f0 + crank * Cfg::FEATS + lane_feat;
+            const bool mine = feat < a.M;
+            const uint32_t ab = n & 1u;
+            const bool have = a.k_tiles > 0;
+            const uint32_t t_row = tmem + ((q * 32u) << 16) + ab * TOK;
+            const int chunks = (w.rows + 15) / 16;
+            if (have) {
+                if (ok) ok = mbar_wait(&acc_full[ab], (n >> 1) & 1u, ctx, kSiteEpilogueFull);
+                ok = __all_sync(0xffffffffu, ok);
+                tc_fence_after();
+            }
+#pragma unroll 1
+            for (int c = h; c < chunks; c += 2) {
+                uint32_t v[16];
+                if (have && ok) {
+                    tmem_ld_32x32b_x16(t_row + c * 16, v);
+                    tmem_ld_wait();
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = 0u;
+                }
+                const int left = ok ? w.rows - c * 16 : 0;  // rows from this chunk on
+                const long long row = w.row0 + c * 16;
+                if constexpr (!Cfg::DUAL) {
+                    uint16_t *o = a.out + row * a.ldo + feat;
+                    if (mine) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            if (j < left) put_bf16(o, __uint_as_float(v[j]));
+                            o += a.ldo;
+                        }
+                    }
+                } else {
+                    if (Cfg::MODE == Exp::GATED && a.preact != nullptr && mine) {
+                        float *z = a.preact + (gate ? 0 : static_cast<long long>(a.R) * a.M) +
+                                   row * a.M + feat;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            if (j < left) *z = __uint_as_float(v[j]);
+                            z += a.M;
+                        }
+                    }
+                    // the gate's warp finishes the chunk's first eight columns, the
+                    // other one the rest
+                    const int c0 = gate ? 0 : 8;
+                    float dh[8];
+                    if constexpr (Cfg::MODE == Exp::GATED_GRAD) {
+                        const uint16_t *in = a.dy + (row + c0) * a.M + feat;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            dh[j] = mine && c0 + j < left
+                                        ? __uint_as_float(static_cast<uint32_t>(*in) << 16)
+                                        : 0.0f;
+                            in += a.M;
+                        }
+                    }
+                    float *own = swap + (2 * e + turn) * 256;
+                    const float *other = swap + (2 * (e ^ 2) + turn) * 256;
+                    turn ^= 1u;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) own[32 * j] = __uint_as_float(gate ? v[8 + j] : v[j]);
+                    named_barrier(1 + h * 2 + (q & 1u), 64);
+                    float g[8], up[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float kept = __uint_as_float(gate ? v[j] : v[8 + j]);
+                        const float got = other[32 * j];
+                        g[j] = gate ? kept : got;
+                        up[j] = gate ? got : kept;
+                    }
+                    const long long at = (row + c0) * a.ldo + feat;
+                    with_act(a.act, [&](auto A) {
+                        constexpr int ACT = decltype(A)::value;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            if constexpr (Cfg::MODE == Exp::GATED_GRAD) {
+                                float value;
+                                const float d = act_value_grad<ACT>(g[j], value);
+                                g[j] = dh[j] * up[j] * d;
+                                up[j] = dh[j] * value;
+                            } else {
+                                g[j] = act_value<ACT>(g[j]) * up[j];
+                            }
+                        }
+                    });
+                    if (mine) {
+                        uint16_t *o = a.out + at;
+                        uint16_t *o2 = Cfg::MODE == Exp::GATED_GRAD ? a.out2 + at : nullptr;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            if (c0 + j < left) {
+                                put_bf16(o, g[j]);
+                                if constexpr (Cfg::MODE == Exp::GATED_GRAD) put_bf16(o2, up[j]);
+                            }
+                            o += a.ldo;
+                            if constexpr (Cfg::MODE == Exp::GATED_GRAD) o2 += a.ldo;
+                        }
+                    }
+                }
+            }
+            if (have) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (CG == 2)
+                        mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[ab]), 0));
+                    else
+                        mbar_arrive(&acc_empty[ab]);
+                }
+            }
+        }
+    }
+
+    // ---------------- teardown ----------------
+    tc_fence_before();
+    __syncwarp();
+    if constexpr (CG == 2)
+        cluster_sync();
+    else
+        __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        if constexpr (CG == 2)
+            tmem_dealloc_pair(tmem, Cfg::TMEM_COLS);
+        else
+            tmem_dealloc(tmem, Cfg::TMEM_COLS);
+    }
+}
+
+// ------------------------------------------------------ weights' gradients ---
+// dW[e] = X_e^T dZ_e in 256 x 256 tiles on a CTA pair: A = X^T M-major, B = dZ N-major,
+// both in boxes of 64 columns x 64 rows.
+template <int STAGES_, int NBUF_>
+struct ExpWeightsCfg {
+    static constexpr int BM = 128, BN = 256, BK = 64, STAGES = STAGES_, NBUF = NBUF_;
+    static constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN / 2 * BK * 2;
+    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+    static constexpr int EPI = 8, EPI_COLS = BN / 2;
+    static constexpr int STAGING_OFFSET = STAGES * STAGE_BYTES;
+    static constexpr int BAR_OFFSET = STAGING_OFFSET + EPI * NBUF * 2048;
+    static constexpr int TABLE_OFFSET = BAR_OFFSET + (2 * STAGES + 6) * 8 + 16;
+    static constexpr int USED = TABLE_OFFSET + (3 * kExpertsMax + 1) * 4;
+    static constexpr int TMEM_COLS = 2 * BN;
+    static constexpr int THREADS = 64 + 32 * EPI;
+    static constexpr int SMEM_BYTES = smem_request(USED + 1024, 1);
+    static_assert(USED + 1024 <= 232448, "shared memory");
+    static_assert(EPI_COLS / 32 % NBUF == 0, "whole batches");
+};
+
+struct WeightsUnit {
+    int expert, begin, end, seg, m0, n0;
+};
+
+template <class Cfg>
+__device__ __forceinline__ WeightsUnit weights_unit(const ExpertsTable &t, const ExpertsArgs &a,
+                                                    int u) {
+    WeightsUnit w;
+    const int n_tiles = a.n_seg * a.segments, per = a.f_tiles * n_tiles;
+    w.expert = u / per;
+    w.begin = t.begin[w.expert];
+    w.end = t.end[w.expert];
+    const int r = u - w.expert * per;
+    const int group = r / (8 * n_tiles), first = group * 8;
+    const int g = min(a.f_tiles - first, 8), q = r - group * 8 * n_tiles;
+    const int nt = q / g;
+    w.m0 = (first + q % g) * (Cfg::BM * 2);
+    w.seg = nt >= a.n_seg ? 1 : 0;
+    w.n0 = (nt - w.seg * a.n_seg) * Cfg::BN;
+    return w;
+}
+
+// put_rows32_batch for a matrix of a 3-D map.
+template <int B, class Ctx>
+__device__ __forceinline__ void put_rows32_batch_3d(Ctx &c, const CUtensorMap *map, int z, int col,
+                                                    const uint32_t *p) {
+    static_assert(B <= Ctx::NB, "staging buffers");
+    if (c.m0 >= c.M || col >= c.N) return;
+    c.template free<B>();
+    uint32_t buf[B];
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+        buf[b] = c.take_buf();
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            sts128(staged(buf[b], c.lane, j), p[16 * b + 4 * j], p[16 * b + 4 * j + 1],
+                   p[16 * b + 4 * j + 2], p[16 * b + 4 * j + 3]);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (c.lane == 0) {
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+            if (col + 32 * b < c.N)
+                tma_store_3d(map, c.bufs + (buf[b] - smem_u32(c.bufs)), col + 32 * b, c.m0, z);
+        // one group holds all B stores; the others keep the count
+#pragma unroll
+        for (int b = 0; b < B; ++b) bulk_commit();
+    }
+    __syncwarp();
+}
+
+template <class Cfg>
+__global__ void __launch_bounds__(Cfg::THREADS, 1)
+    experts_weights_kernel(const __grid_constant__ ExpertsMaps maps, const ExpertsArgs a,
+                           const KernelCtx ctx) {
+    constexpr int STAGES = Cfg::STAGES, BK = Cfg::BK, BM = Cfg::BM, BN = Cfg::BN;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = align_1024(smem_raw);
+    uint8_t *sA = smem, *sB = smem + STAGES * Cfg::A_BYTES;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + Cfg::BAR_OFFSET);
+    uint64_t *empty = full + STAGES;
+    uint64_t *acc_full = empty + STAGES;  // [2]
+    uint64_t *acc_empty = acc_full + 2;   // [2]
+    uint64_t *mma_done = acc_empty + 2;
+    uint64_t *tail = mma_done + 1;        // a group's last K step, in this CTA
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tail + 1);
+    const uint32_t warp = warp_id_uniform(), lane = lane_id();
+    const int crank = static_cast<int>(cluster_ctarank());
+    if (warp == 0 && lane == 0) {
+        prefetch_tmap(&maps.x[0]);
+        prefetch_tmap(&maps.w[0]);
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&full[s], 2);  // a producer of each CTA
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], Cfg::EPI * 2);
+        }
+        mbar_init(mma_done, 1);
+        mbar_init(tail, 1);
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, Cfg::TMEM_COLS);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    op_begin(0);
+    const ExpertsTable table =
+        experts_table(a, smem + Cfg::TABLE_OFFSET, [](int) { return 0; });
+    const int units = a.E * a.f_tiles * a.n_seg * a.segments;
+    const int slot = static_cast<int>(blockIdx.x) / 2, slots = static_cast<int>(gridDim.x) / 2;
+
+    if (warp == 0) {
+        // ---------------- producer (the whole warp, for the groups' ends) ----------------
+        uint32_t it = 0, tails = 0;
+        bool ok = true;
+        for (int u = slot; ok && u < units; u += slots) {
+            const WeightsUnit w = weights_unit<Cfg>(table, a, u);
+            const CUtensorMap *mb = &maps.w[w.seg];
+            for (int y = w.begin; y < w.end; y += BK, ++it) {
+                const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
+                uint8_t *da = sA + s * Cfg::A_BYTES, *db = sB + s * Cfg::B_BYTES;
+                const int ma = w.m0 + crank * BM, nb = w.n0 + crank * (BN / 2);
+                const int rows = w.end - y;
+                if (lane == 0) ok = mbar_wait(&empty[s], ph ^ 1u, ctx, kSiteProducerEmpty);
+                ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0) != 0;
+                if (!ok) break;
+                const uint32_t lead = mapa_shared(smem_u32(&full[s]), 0);
+                if (rows >= BK) {
+                    if (lane == 0) {
+                        // both CTAs' bytes are counted by the leader's barrier
+                        if (crank == 0)
+                            mbar_arrive_expect_tx(&full[s], 2 * Cfg::STAGE_BYTES);
+                        else
+                            mbar_arrive_cluster(lead);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            tma_load_2d_pair(da + j * 8192, &maps.x[0], lead, ma + 64 * j, y);
+                            tma_load_2d_pair(db + j * 8192, mb, lead, nb + 64 * j, y);
+                        }
+                    }
+                } else {
+                    // what follows the group's last row in the step belongs to others
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(tail, Cfg::STAGE_BYTES);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            tma_load_2d(da + j * 8192, &maps.x[0], tail, ma + 64 * j, y);
+                            tma_load_2d(db + j * 8192, mb, tail, nb + 64 * j, y);
+                        }
+                    }
+                    // (every lane waits: it must see the copies before it overwrites them)
+                    ok = mbar_wait(tail, tails & 1u, ctx, kSiteGroupTail);
+                    ok = __all_sync(0xffffffffu, ok);
+                    ++tails;
+                    if (!ok) break;
+                    for (int r = rows * 8 + static_cast<int>(lane); r < BK * 8; r += 32)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            sts128(smem_u32(da) + j * 8192 + r * 16, 0u, 0u, 0u, 0u);
+                            sts128(smem_u32(db) + j * 8192 + r * 16, 0u, 0u, 0u, 0u);
+                        }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(lead);
+                }
+            }
+        }
+        // the pair's last multicast releases of this CTA's barriers must have landed
+        // before the cluster is left
+        if (lane == 0)
+            for (int i = 0; ok && i < STAGES; ++i, ++it) {
+                const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
+                ok = mbar_wait(&empty[s], ph ^ 1u, ctx, kSiteProducerEmpty);
+            }
+    } else if (warp == 1) {
+        if (lane == 0 && crank == 0) {
+            // ---------------- MMA issuer ----------------
+            constexpr uint16_t kPair = 3;
+            constexpr uint32_t idesc = idesc_f16(BM * 2, BN, 1, 1, 1);
+            uint32_t it = 0, n = 0;
+            bool ok = true;
+            for (int u = slot; ok && u < units; u += slots) {
+                const WeightsUnit w = weights_unit<Cfg>(table, a, u);
+                if (w.end <= w.begin) continue;
+                const uint32_t ab = n & 1u;
+                if (!mbar_wait(&acc_empty[ab], ((n >> 1) & 1u) ^ 1u, ctx, kSiteMmaAccEmpty)) {
+                    ok = false;
+                    break;
+                }
+                ++n;
+                tc_fence_after();
+                const uint32_t d = tmem + ab * BN;
+                for (int y = w.begin; y < w.end; y += BK, ++it) {
+                    const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
+                    if (!mbar_wait_cluster(&full[s], ph, ctx, kSiteMmaFull)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = smem_u32(sA + s * Cfg::A_BYTES);
+                    const uint32_t sb = smem_u32(sB + s * Cfg::B_BYTES);
+#pragma unroll
+                    for (int k = 0; k < BK / 16; ++k)
+                        umma_f16_ss_pair(d, smem_desc_sw128(sa + k * 2048, BK * 128, 1024),
+                                         smem_desc_sw128(sb + k * 2048, BK * 128, 1024), idesc,
+                                         (y == w.begin && k == 0) ? 0u : 1u);
+                    umma_commit_pair_multicast(&empty[s], kPair);
+                }
+                if (ok) umma_commit_pair_multicast(&acc_full[ab], kPair);
+            }
+            umma_commit_pair_multicast(mma_done, 1);
+            mbar_wait(mma_done, 0, ctx, kSiteMmaDone);
+        }
+    } else {
+        // ---------------- epilogue ----------------
+        const uint32_t e = warp - 2, q = warp & 3u;
+        EpiCtx<Cfg::NBUF> c;
+        c.bufs = smem + Cfg::STAGING_OFFSET + e * (Cfg::NBUF * 2048);
+        c.n = 0;
+        c.M = a.K;  // dW is K x M: the rows of X are its output's rows here
+        c.N = a.M;
+        c.lane = lane;
+        const int col0 = static_cast<int>(e >> 2) * Cfg::EPI_COLS;
+        uint32_t n = 0;
+        for (int u = slot; u < units; u += slots) {
+            const WeightsUnit w = weights_unit<Cfg>(table, a, u);
+            c.m0 = w.m0 + crank * BM + static_cast<int>(q * 32);
+            const uint32_t ab = n & 1u;
+            const bool have = w.end > w.begin;
+            constexpr int C = Cfg::EPI_COLS / 32, B = C < Cfg::NBUF ? C : Cfg::NBUF;
+            uint32_t v[32 * C];
+            if (have) {
+                if (!mbar_wait(&acc_full[ab], (n >> 1) & 1u, ctx, kSiteEpilogueFull)) break;
+                tc_fence_after();
+                const uint32_t t_row = tmem + ((q * 32u) << 16) + ab * BN + col0;
+#pragma unroll
+                for (int b = 0; b < C; ++b)
+                    tmem_ld_32x32b_x32(t_row + 32 * b,
+                                       *reinterpret_cast<uint32_t(*)[32]>(v + 32 * b));
+                tmem_ld_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[ab]), 0));
+                ++n;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 32 * C; ++j) v[j] = 0u;
+            }
+#pragma unroll
+            for (int j = 0; j < 16 * C; ++j)
+                v[j] = pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+            if (a.tma_out) {
+#pragma unroll
+                for (int b = 0; b < C; b += B)
+                    put_rows32_batch_3d<B>(c, &maps.c[w.seg], w.expert, w.n0 + col0 + 32 * b,
+                                           v + 16 * b);
+            } else {
+                uint16_t *o = (w.seg ? a.out2 : a.out) +
+                              static_cast<long long>(w.expert) * a.K * a.M;
+#pragma unroll
+                for (int b = 0; b < C; ++b)
+                    put_rows32(c, nullptr, o, a.M, w.n0 + col0 + 32 * b, v + 16 * b);
+            }
+        }
+        if (lane == 0) bulk_wait_all();  // this warp's stores have landed
+        __syncwarp();
+    }
+
+    // ---------------- teardown ----------------
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, Cfg::TMEM_COLS);
+    }
+}
+
+// ------------------------------------------------------------------- host ---
+using ExpKernel = void (*)(const ExpertsMaps, const ExpertsArgs, const KernelCtx);
+
+template <int CG>
+static cudaError_t exp_slots_of(const void *func, int threads, int smem, int sm_count, int *slots) {
+    if constexpr (CG == 1) {
+        *slots = sm_count;
+        return cudaSuccess;
+    } else {
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = CG;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cudaLaunchConfig_t lc{};
+        lc.blockDim = dim3(threads);
+        lc.dynamicSmemBytes = smem;
+        lc.gridDim = dim3(CG * sm_count);
+        lc.attrs = attr;
+        lc.numAttrs = 1;
+        int clusters = 0;
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(&clusters, func, &lc);
+        if (e != cudaSuccess) return e;
+        if (clusters < 1) return cudaErrorInvalidConfiguration;
+        *slots = clusters;
+        return cudaSuccess;
+    }
+}
+
+// One launch on as many CTAs (pairs) as run at once, or as there can be units.
+template <class Cfg, int CG, ExpKernel KERNEL>
+static pgemm_status exp_launch(const OpDevice &dev, const ExpertsMaps &maps, const ExpertsArgs &a,
+                               long long most_units, cudaStream_t stream) {
+    static const KernelInfo info = [] {
+        KernelInfo k;
+        k.threads = Cfg::THREADS;
+        k.smem_bytes = Cfg::SMEM_BYTES;
+        k.func = reinterpret_cast<const void *>(KERNEL);
+        k.schedule_slots = [](const LaunchCommon &p, int *slots) {
+            return exp_slots_of<CG>(reinterpret_cast<const void *>(KERNEL), Cfg::THREADS,
+                                    Cfg::SMEM_BYTES, p.sm_count, slots);
+        };
+        return k;
+    }();
+    int slots = 0;
+    const pgemm_status st = op_kernel_setup(dev, info, &slots);
+    if (st != PGEMM_OK) return st;
+    if (most_units > INT_MAX / 2) return PGEMM_ERR_TOO_LARGE;
+    cudaLaunchAttribute attr[2];
+    int nattr = 0;
+    attr[nattr].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[nattr].val.programmaticStreamSerializationAllowed = 1;
+    ++nattr;
+    if constexpr (CG == 2) {
+        attr[nattr].id = cudaLaunchAttributeClusterDimension;
+        attr[nattr].val.clusterDim.x = 2;
+        attr[nattr].val.clusterDim.y = 1;
+        attr[nattr].val.clusterDim.z = 1;
+        ++nattr;
+    }
+    cudaLaunchConfig_t lc{};
+    lc.blockDim = dim3(Cfg::THREADS);
+    lc.gridDim = dim3(CG * static_cast<int>(most_units < slots ? most_units : slots));
+    lc.dynamicSmemBytes = Cfg::SMEM_BYTES;
+    lc.stream = stream;
+    lc.attrs = attr;
+    lc.numAttrs = nattr;
+    return cudaLaunchKernelEx(&lc, KERNEL, maps, a, dev.ctx) == cudaSuccess ? PGEMM_OK
+                                                                            : PGEMM_ERR_CUDA;
+}
+
+// A call's sizes: R rows, N outputs (gated: features), K reduction columns, E experts.
+struct ExpSizes {
+    int R, N, K, E;
+    const int32_t *offsets;
+};
+
+template <class Cfg>
+static pgemm_status rows_launch(const OpDevice &dev, const ExpSizes &z, const OpMat *x,
+                                const OpMat *w, int segments, ExpertsArgs a, cudaStream_t s) {
+    // TRANSPOSED: z.N is the reduction, z.K the features
+    constexpr bool T = Cfg::W_K;
+    a.R = z.R;
+    a.E = z.E;
+    a.M = T ? z.K : z.N;
+    a.K = T ? z.N : z.K;
+    a.offsets = z.offsets;
+    a.k_seg = op_blocks(a.K, Cfg::BK);
+    a.k_tiles = a.k_seg * segments;
+    a.f_tiles = op_blocks(a.M, Cfg::FEATS * Cfg::CG);
+    ExpertsMaps maps{};
+    const int ws = Cfg::DUAL ? 2 : segments;
+    pgemm_status st = PGEMM_OK;
+    for (int j = 0; a.K > 0 && j < segments && st == PGEMM_OK; ++j)
+        st = op_encode(&maps.x[j], x[j].p, a.K, z.R, x[j].ld, Cfg::BOX);
+    for (int j = 0; a.K > 0 && j < ws && st == PGEMM_OK; ++j)
+        st = op_encode_3d(&maps.w[j], w[j].p, z.N, z.K, z.E, w[j].ld, T ? 128 : 64);
+    if (st != PGEMM_OK) return st;
+    // units at most: every tile of rows full, and a partial one more for each expert
+    const long long live = z.R < z.E ? z.R : z.E;
+    const long long most = (z.R / Cfg::TOK + live) * a.f_tiles;
+    return exp_launch<Cfg, Cfg::CG, experts_rows_kernel<Cfg>>(dev, maps, a, most, s);
+}
+
+template <Exp MODE>
+static pgemm_status rows_product(const OpDevice &dev, const ExpSizes &z, const OpMat *x,
+                                 const OpMat *w, int segments, const ExpertsArgs &a,
+                                 cudaStream_t s) {
+    // few rows a group: the weights are all there is to read, and single CTAs with small
+    // tiles of rows keep more of them on the way
+    if (z.R <= 48ll * z.E) return rows_launch<ExpCfg<1, 64, 8, MODE>>(dev, z, x, w, segments, a, s);
+    return rows_launch<ExpCfg<2, 256, 6 - (MODE == Exp::GATED || MODE == Exp::GATED_GRAD), MODE>>(
+        dev, z, x, w, segments, a, s);
+}
+
+// dW[j][e] = x_e^T dz[j]_e for each of `segments` outputs.
+static pgemm_status weights_product(const OpDevice &dev, const ExpSizes &z, const OpMat &x,
+                                    const OpMat *dz, int segments, uint16_t *const *out,
+                                    cudaStream_t s) {
+    using Cfg = ExpWeightsCfg<5, 2>;
+    ExpertsArgs a{};
+    a.R = z.R;
+    a.E = z.E;
+    a.M = z.N;
+    a.K = z.K;
+    a.offsets = z.offsets;
+    a.f_tiles = op_blocks(z.K, 256);
+    a.n_seg = op_blocks(z.N, 256);
+    a.segments = segments;
+    a.out = out[0];
+    a.out2 = segments > 1 ? out[1] : nullptr;
+    a.tma_out = z.N % 8 == 0;
+    ExpertsMaps maps{};
+    pgemm_status st = op_encode(&maps.x[0], x.p, z.K, z.R, x.ld, 64);
+    for (int j = 0; j < segments && st == PGEMM_OK; ++j) {
+        st = op_encode(&maps.w[j], dz[j].p, z.N, z.R, dz[j].ld, 64);
+        if (st == PGEMM_OK && a.tma_out)
+            st = op_encode_out_3d(&maps.c[j], out[j], z.N, z.K, z.E, z.N);
+    }
+    if (st != PGEMM_OK) return st;
+    const long long units = static_cast<long long>(z.E) * a.f_tiles * a.n_seg * segments;
+    return exp_launch<Cfg, 2, experts_weights_kernel<Cfg>>(dev, maps, a, units, s);
+}
+
+static pgemm_status exp_check(const ExpSizes &z) {
+    if (z.R < 0 || z.N < 0 || z.K < 0 || z.E < 1) return PGEMM_ERR_INVALID_VALUE;
+    if (z.E > kExpertsMax || static_cast<long long>(z.E) * z.K > INT_MAX)
+        return PGEMM_ERR_TOO_LARGE;
+    return PGEMM_OK;
+}
+
+static pgemm_status zero_bf16(uint16_t *p, long long n, cudaStream_t s) {
+    return n == 0 || cudaMemsetAsync(p, 0, static_cast<size_t>(n) * 2, s) == cudaSuccess
+               ? PGEMM_OK
+               : PGEMM_ERR_CUDA;
+}
+
+static pgemm_status experts_linear_forward(const ExpSizes &z, const uint16_t *X, const uint16_t *W,
+                                           uint16_t *Y, cudaStream_t s) {
+    pgemm_status st = exp_check(z);
+    if (st != PGEMM_OK || z.R == 0 || z.N == 0) return st;
+    if (!z.offsets || !Y || (z.K > 0 && (!X || !W))) return PGEMM_ERR_INVALID_VALUE;
+    if (!op_aligned16(z.offsets) || !op_aligned16(X) || !op_aligned16(W) || !op_aligned16(Y))
+        return PGEMM_ERR_MISALIGNED;
+    OpDevice dev;
+    if ((st = op_device(&dev)) != PGEMM_OK) return st;
+    OpArena arena(dev, s);
+    OpRelayout rl;
+    OpMat x, w;
+    rl.add(&x, X, z.R, z.K, arena);
+    rl.add(&w, W, static_cast<long long>(z.E) * z.K, z.N, arena);
+    if ((st = arena.alloc()) != PGEMM_OK) return st;
+    if (z.K > 0 && (st = rl.run(dev, arena, s)) != PGEMM_OK) return st;
+    ExpertsArgs a{};
+    a.out = Y;
+    a.ldo = z.N;
+    return rows_product<Exp::LINEAR>(dev, z, &x, &w, 1, a, s);
+}
+
+static pgemm_status experts_linear_backward(const ExpSizes &z, const uint16_t *X,
+                                            const uint16_t *W, const uint16_t *dY, uint16_t *dX,
+                                            uint16_t *dW, cudaStream_t s) {
+    pgemm_status st = exp_check(z);
+    if (st != PGEMM_OK) return st;
+    const bool want_x = dX && z.R > 0 && z.K > 0, want_w = dW && z.K > 0 && z.N > 0;
+    if (!want_x && !want_w) return PGEMM_OK;
+    const bool some = z.R > 0 && z.N > 0;
+    if (!z.offsets || (some && (!dY || (want_w && !X) || (want_x && !W))))
+        return PGEMM_ERR_INVALID_VALUE;
+    if (!op_aligned16(z.offsets) || !op_aligned16(X) || !op_aligned16(W) || !op_aligned16(dY) ||
+        !op_aligned16(dX) || !op_aligned16(dW))
+        return PGEMM_ERR_MISALIGNED;
+    OpDevice dev;
+    if ((st = op_device(&dev)) != PGEMM_OK) return st;
+    if (z.R == 0) return zero_bf16(dW, static_cast<long long>(z.E) * z.K * z.N, s);
+    OpArena arena(dev, s);
+    OpRelayout rl;
+    OpMat x, w, dy;
+    if (some) {
+        rl.add(&dy, dY, z.R, z.N, arena);
+        if (want_w) rl.add(&x, X, z.R, z.K, arena);
+        if (want_x) rl.add(&w, W, static_cast<long long>(z.E) * z.K, z.N, arena);
+    }
+    if ((st = arena.alloc()) != PGEMM_OK) return st;
+    if ((st = rl.run(dev, arena, s)) != PGEMM_OK) return st;
+    if (want_x) {
+        ExpertsArgs a{};
+        a.out = dX;
+        a.ldo = z.K;
+        st = rows_product<Exp::TRANSPOSED>(dev, z, &dy, &w, 1, a, s);
+        if (st != PGEMM_OK) return st;
+    }
+    return want_w ? weights_product(dev, z, x, &dy, 1, &dW, s) : PGEMM_OK;
+}
+
+// A ReLU gate is not offered: its derivative hangs on the sign of a sum that the tensor
+// core truncates (see op_sign_rounds), and the rounds that would mend it need registers
+// that this epilogue does not have.
+static bool exp_act_known(int act) { return op_act_known(act) && act != PGEMM_ACT_RELU; }
+
+static pgemm_status experts_gated_forward(const ExpSizes &z, const uint16_t *X, const uint16_t *Wg,
+                                          const uint16_t *Wu, int act, uint16_t *H, float *preact,
+                                          cudaStream_t s) {
+    pgemm_status st = exp_check(z);
+    if (st != PGEMM_OK) return st;
+    if (!exp_act_known(act)) return PGEMM_ERR_INVALID_VALUE;
+    if (z.R == 0 || z.N == 0) return PGEMM_OK;
+    if (!z.offsets || !H || (z.K > 0 && (!X || !Wg || !Wu))) return PGEMM_ERR_INVALID_VALUE;
+    if (!op_aligned16(z.offsets) || !op_aligned16(X) || !op_aligned16(Wg) || !op_aligned16(Wu) ||
+        !op_aligned16(H) || !op_aligned16(preact))
+        return PGEMM_ERR_MISALIGNED;
+    OpDevice dev;
+    if ((st = op_device(&dev)) != PGEMM_OK) return st;
+    OpArena arena(dev, s);
+    OpRelayout rl;
+    OpMat x, w[2];
+    rl.add(&x, X, z.R, z.K, arena);
+    rl.add(&w[0], Wg, static_cast<long long>(z.E) * z.K, z.N, arena);
+    rl.add(&w[1], Wu, static_cast<long long>(z.E) * z.K, z.N, arena);
+    if ((st = arena.alloc()) != PGEMM_OK) return st;
+    if (z.K > 0 && (st = rl.run(dev, arena, s)) != PGEMM_OK) return st;
+    ExpertsArgs a{};
+    a.out = H;
+    a.ldo = z.N;
+    a.preact = preact;
+    a.act = act;
+    return rows_product<Exp::GATED>(dev, z, &x, w, 1, a, s);
+}
+
+static pgemm_status experts_gated_backward(const ExpSizes &z, const uint16_t *X,
+                                           const uint16_t *Wg, const uint16_t *Wu, int act,
+                                           const uint16_t *dH, const float *preact, uint16_t *dX,
+                                           uint16_t *dWg, uint16_t *dWu, cudaStream_t s) {
+    pgemm_status st = exp_check(z);
+    if (st != PGEMM_OK) return st;
+    if (!exp_act_known(act) || (!dWg) != (!dWu)) return PGEMM_ERR_INVALID_VALUE;
+    const bool want_x = dX && z.R > 0 && z.K > 0, want_w = dWg && z.K > 0 && z.N > 0;
+    if (!want_x && !want_w) return PGEMM_OK;
+    const bool some = z.R > 0 && z.N > 0;
+    const bool recompute = some && !preact;
+    if (!z.offsets || (some && (!dH || ((want_w || recompute) && !X) ||
+                                ((want_x || recompute) && (!Wg || !Wu)))))
+        return PGEMM_ERR_INVALID_VALUE;
+    if (!op_aligned16(z.offsets) || !op_aligned16(X) || !op_aligned16(Wg) || !op_aligned16(Wu) ||
+        !op_aligned16(dH) || !op_aligned16(preact) || !op_aligned16(dX) || !op_aligned16(dWg) ||
+        !op_aligned16(dWu))
+        return PGEMM_ERR_MISALIGNED;
+    OpDevice dev;
+    if ((st = op_device(&dev)) != PGEMM_OK) return st;
+    const long long size = static_cast<long long>(z.E) * z.K * z.N;
+    if (z.R == 0) {
+        st = zero_bf16(dWg, size, s);
+        return st == PGEMM_OK ? zero_bf16(dWu, size, s) : st;
+    }
+    OpArena arena(dev, s);
+    OpRelayout rl;
+    OpMat x, w[2], dz[2];
+    if (some) {
+        if (want_w || recompute) rl.add(&x, X, z.R, z.K, arena);
+        if (want_x || recompute) {
+            rl.add(&w[0], Wg, static_cast<long long>(z.E) * z.K, z.N, arena);
+            rl.add(&w[1], Wu, static_cast<long long>(z.E) * z.K, z.N, arena);
+        }
+    }
+    const long long dz_ld = op_round_up(z.N, 64);
+    const long long at0 = arena.add(dz_ld * z.R * 2), at1 = arena.add(dz_ld * z.R * 2);
+    if ((st = arena.alloc()) != PGEMM_OK) return st;
+    if ((st = rl.run(dev, arena, s)) != PGEMM_OK) return st;
+    for (int j = 0; j < 2; ++j) dz[j] = OpMat{arena.at<uint16_t>(j ? at1 : at0), dz_ld};
+    if (some && preact) {
+        OpActGrad g;
+        g.M = z.R;
+        g.N = z.N;
+        g.act = act;
+        g.z = preact;
+        g.u = preact + static_cast<long long>(z.R) * z.N;
+        g.dy = dH;
+        g.dy_ld = z.N;
+        g.dz = arena.at<uint16_t>(at0);
+        g.du = arena.at<uint16_t>(at1);
+        g.dz_ld = dz_ld;
+        if ((st = op_act_grad(dev, g, arena, false, s)) != PGEMM_OK) return st;
+    } else if (some) {
+        ExpertsArgs a{};
+        a.out = arena.at<uint16_t>(at0);
+        a.out2 = arena.at<uint16_t>(at1);
+        a.ldo = dz_ld;
+        a.dy = dH;
+        a.act = act;
+        st = rows_product<Exp::GATED_GRAD>(dev, z, &x, w, 1, a, s);
+        if (st != PGEMM_OK) return st;
+    }
+    if (want_x) {
+        ExpertsArgs a{};
+        a.out = dX;
+        a.ldo = z.K;
+        if ((st = rows_product<Exp::TRANSPOSED>(dev, z, dz, w, 2, a, s)) != PGEMM_OK) return st;
+    }
+    uint16_t *out[2] = {dWg, dWu};
+    return want_w ? weights_product(dev, z, x, dz, 2, out, s) : PGEMM_OK;
+}
+
+}  // namespace pg
+
+extern "C" {
+
+pgemm_status experts_linear_bf16(int R, int N, int K, int E, const int32_t *offsets,
+                                 const uint16_t *X, const uint16_t *W, uint16_t *Y,
+                                 pgemm_stream_t stream) {
+    return pg::op_guard([&] {
+        return pg::experts_linear_forward(pg::ExpSizes{R, N, K, E, offsets}, X, W, Y, stream);
+    });
+}
+
+pgemm_status experts_linear_bf16_backward(int R, int N, int K, int E, const int32_t *offsets,
+                                          const uint16_t *X, const uint16_t *W, const uint16_t *dY,
+                                          uint16_t *dX, uint16_t *dW, pgemm_stream_t stream) {
+    return pg::op_guard([&] {
+        return pg::experts_linear_backward(pg::ExpSizes{R, N, K, E, offsets}, X, W, dY, dX, dW,
+                                           stream);
+    });
+}
+
+pgemm_status experts_gated_bf16(int R, int F, int K, int E, const int32_t *offsets,
+                                const uint16_t *X, const uint16_t *Wg, const uint16_t *Wu, int act,
+                                uint16_t *H, float *preact, pgemm_stream_t stream) {
+    return pg::op_guard([&] {
+        return pg::experts_gated_forward(pg::ExpSizes{R, F, K, E, offsets}, X, Wg, Wu, act, H,
+                                         preact, stream);
+    });
+}
+
+pgemm_status experts_gated_bf16_backward(int R, int F, int K, int E, const int32_t *offsets,
+                                         const uint16_t *X, const uint16_t *Wg, const uint16_t *Wu,
+                                         int act, const uint16_t *dH, const float *preact,
+                                         uint16_t *dX, uint16_t *dWg, uint16_t *dWu,
+                                         pgemm_stream_t stream) {
+    return pg::op_guard([&] {
+        return pg::experts_gated_backward(pg::ExpSizes{R, F, K, E, offsets}, X, Wg, Wu, act, dH,
+                                          preact, dX, dWg, dWu, stream);
+    });
+}
+
+}  // extern "C"

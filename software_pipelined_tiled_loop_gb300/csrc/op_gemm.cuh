@@ -885,18 +885,24 @@ static pgemm_status op_launch(const OpDevice &dev, const OpMaps &maps, OpArgs a,
 
 // As op_launch launches: the kernel waits before it touches memory, or as op_begin says.
 template <class... KArgs, class... Args>
-static pgemm_status launch_small(void (*kernel)(KArgs...), dim3 grid, dim3 block,
-                                 cudaStream_t s, Args... args) {
+static pgemm_status launch_small_smem(void (*kernel)(KArgs...), dim3 grid, dim3 block,
+                                      size_t smem_bytes, cudaStream_t s, Args... args) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t lc{};
     lc.gridDim = grid;
     lc.blockDim = block;
+    lc.dynamicSmemBytes = smem_bytes;
     lc.stream = s;
     lc.attrs = attr;
     lc.numAttrs = 1;
     return cudaLaunchKernelEx(&lc, kernel, args...) == cudaSuccess ? PGEMM_OK : PGEMM_ERR_CUDA;
+}
+template <class... KArgs, class... Args>
+static pgemm_status launch_small(void (*kernel)(KArgs...), dim3 grid, dim3 block,
+                                 cudaStream_t s, Args... args) {
+    return launch_small_smem(kernel, grid, block, 0, s, args...);
 }
 
 }  // namespace pg

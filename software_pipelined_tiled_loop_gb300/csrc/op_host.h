@@ -32,6 +32,11 @@ pgemm_status op_encode(CUtensorMap *map, const void *base, long long inner, long
 enum class OpElem { BF16, F32 };
 pgemm_status op_encode_out(CUtensorMap *map, OpElem type, const void *base, long long inner,
                            long long outer, long long ld);
+// The same of `depth` matrices behind one another, pitch ld * outer elements; boxes of one.
+pgemm_status op_encode_3d(CUtensorMap *map, const void *base, long long inner, long long outer,
+                          long long depth, long long ld, int box_y);
+pgemm_status op_encode_out_3d(CUtensorMap *map, const void *base, long long inner, long long outer,
+                              long long depth, long long ld);
 cudaError_t launch_repack(const void *src0, long long sld0, void *dst0, long long dld0, int rows0,
                           int cols0, const void *src1, long long sld1, void *dst1, long long dld1,
                           int rows1, int cols1, int eb, int sm_count, cudaStream_t s);

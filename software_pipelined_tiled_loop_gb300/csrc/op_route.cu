@@ -1,0 +1,837 @@
+// Routing tokens to experts, and tokens sorted by expert and back.
+//
+//   route_topk     the k largest of a token's E logits (ties to the lowest index) and
+//                  their weights: the softmax over the chosen, or over all E.
+//   expert_sort    a stable counting sort of the T k slots (token t's j-th choice is slot
+//                  t k + j) by expert: offsets[e], the first row of expert e, and
+//                  slot_row[slot], the slot's row.
+//   expert_gather  Xs[slot_row[t][j]] = X[t].
+//   expert_combine Y[t] = R[t] + sum_j w[t][j] Ys[slot_row[t][j]], and its gradients
+//                  dYs[slot_row[t][j]] = w[t][j] dY[t], dw[t][j] = <dY[t], Ys[slot_row[t][j]]>.
+//                  With weights of one it is the gather's gradient.
+//
+// Every sum has an order of its own, so results do not depend on timing; no atomics.
+// Choosing is bound by its T E logits for many tokens and by latency for few; sorting by
+// latency (some 12 bytes a slot); gather and combine by HBM.
+#include <cuda_runtime.h>
+
+#include <climits>
+
+#include "op_gemm.cuh"
+#include "op_host.h"
+
+namespace pg {
+
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxChoices = 32;
+
+// ---------------------------------------------------------------- routing ---
+// A logit as an unsigned number of the same order.  -0 counts as +0, a NaN above
+// everything (it is chosen, and the weights say so); -inf is the lowest that occurs.
+__device__ __forceinline__ uint32_t order_key(float z) {
+    if (z != z) return 0xffffffffu;
+    const uint32_t b = __float_as_uint(z + 0.0f);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+constexpr uint32_t kClosedKey = 0x007fffffu;  // order_key(-inf): this expert is not chosen
+__device__ __forceinline__ float key_logit(uint32_t key) {
+    if (key == 0xffffffffu) return __int_as_float(0x7fc00000);
+    return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+}
+
+struct RouteParams {
+    int T, E, k, normalise;
+    const float *logits;
+    int32_t *experts;
+    float *weights;
+    const int32_t *experts_in;
+    const float *dweights;
+    float *dlogits;
+};
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    return x;
+}
+__device__ __forceinline__ uint32_t warp_max(uint32_t x) {
+    return __reduce_max_sync(0xffffffffu, x);
+}
+
+// A warp a token; lane l holds experts l, l + 32, ...
+template <int NV>
+__device__ __forceinline__ void row_read(const float *p, int E, int lane, float (&z)[NV]) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int e = lane + 32 * i;
+        z[i] = e < E ? p[e] : -__int_as_float(0x7f800000);
+    }
+}
+
+template <int NV>
+__global__ void __launch_bounds__(128) route_kernel(const RouteParams p) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    for (long long t = blockIdx.x * 4ll + (threadIdx.x >> 5); t < p.T; t += gridDim.x * 4ll) {
+        float z[NV];
+        row_read<NV>(p.logits + t * p.E, p.E, lane, z);
+        uint32_t key[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) key[i] = order_key(z[i]);
+        // choice lane's expert and logit, k <= 32 of them
+        int mine = -1;
+        float logit = 0.0f;
+        for (int j = 0; j < p.k; ++j) {
+            uint32_t best = key[0];
+#pragma unroll
+            for (int i = 1; i < NV; ++i) best = max(best, key[i]);
+            best = warp_max(best);
+            if (best <= kClosedKey) break;
+            int at = INT_MAX;
+#pragma unroll
+            for (int i = NV - 1; i >= 0; --i)
+                if (key[i] == best) at = lane + 32 * i;
+            at = static_cast<int>(__reduce_min_sync(0xffffffffu, static_cast<unsigned>(at)));
+            float v = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (at == lane + 32 * i) {
+                    v = z[i];
+                    key[i] = 0u;
+                }
+            v = __shfl_sync(0xffffffffu, v, at & 31);
+            if (lane == j) {
+                mine = at;
+                logit = v;
+            }
+        }
+        const float top = __shfl_sync(0xffffffffu, logit, 0);
+        float e = mine >= 0 ? expf(logit - top) : 0.0f, total = e;
+        if (!p.normalise) {
+            const bool any = __shfl_sync(0xffffffffu, mine, 0) >= 0;
+            total = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (any && lane + 32 * i < p.E) total += expf(z[i] - top);
+        }
+        total = warp_sum(total);
+        if (lane < p.k) {
+            p.experts[t * p.k + lane] = mine;
+            p.weights[t * p.k + lane] = mine >= 0 ? e / total : 0.0f;
+        }
+    }
+}
+
+// dlogits from dweights: with w the weights and dot = sum over the chosen of w dw,
+// w (dw - dot) at the chosen (softmax over the chosen), or p ([chosen] dw - dot)
+// everywhere (softmax over all).  A choice outside [0, E) does not count.
+template <int NV>
+__global__ void __launch_bounds__(128) route_backward_kernel(const RouteParams p) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    for (long long t = blockIdx.x * 4ll + (threadIdx.x >> 5); t < p.T; t += gridDim.x * 4ll) {
+        float z[NV];
+        row_read<NV>(p.logits + t * p.E, p.E, lane, z);
+        int mine = -1;
+        float dw = 0.0f;
+        if (lane < p.k) {
+            mine = p.experts_in[t * p.k + lane];
+            dw = p.dweights[t * p.k + lane];
+            if (mine < 0 || mine >= p.E) {
+                mine = -1;
+                dw = 0.0f;
+            }
+        }
+        const float logit = mine >= 0 ? p.logits[t * p.E + mine] : 0.0f;
+        // the largest of what the softmax is over; none where everything is closed
+        uint32_t best = p.normalise && mine >= 0 ? order_key(logit) : 0u;
+        if (!p.normalise) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) best = max(best, order_key(z[i]));
+        }
+        best = warp_max(best);
+        const bool any = best > kClosedKey;
+        const float top = any ? key_logit(best) : 0.0f;
+        const float e = any && mine >= 0 ? expf(logit - top) : 0.0f;
+        float total = e;
+        float ez[NV];
+        if (!p.normalise) {
+            total = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                ez[i] = any && lane + 32 * i < p.E ? expf(z[i] - top) : 0.0f;
+                total += ez[i];
+            }
+        }
+        total = warp_sum(total);
+        const float w = any && mine >= 0 ? e / total : 0.0f;
+        const float dot = warp_sum(w * dw);
+        float d[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            d[i] = p.normalise || !any ? 0.0f : -(ez[i] / total) * dot;
+        const float own = p.normalise ? w * (dw - dot) : w * dw;
+        for (int j = 0; j < p.k; ++j) {
+            const int at = __shfl_sync(0xffffffffu, mine, j);
+            const float v = __shfl_sync(0xffffffffu, own, j);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (at == lane + 32 * i) d[i] += v;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (lane + 32 * i < p.E) p.dlogits[t * p.E + lane + 32 * i] = d[i];
+    }
+}
+
+template <class F>
+static pgemm_status with_experts(int E, F &&f) {
+    using std::integral_constant;
+    if (E <= 32) return f(integral_constant<int, 1>{});
+    if (E <= 64) return f(integral_constant<int, 2>{});
+    if (E <= 128) return f(integral_constant<int, 4>{});
+    if (E <= 256) return f(integral_constant<int, 8>{});
+    if (E <= 512) return f(integral_constant<int, 16>{});
+    return f(integral_constant<int, 32>{});
+}
+
+static pgemm_status route_check(int T, int E, int k) {
+    if (T < 0 || E < 1 || k < 1 || k > E) return PGEMM_ERR_INVALID_VALUE;
+    return E > kMaxExperts || k > kMaxChoices ? PGEMM_ERR_TOO_LARGE : PGEMM_OK;
+}
+
+static dim3 route_grid(const OpDevice &dev, int T) {
+    const int blocks = op_blocks(T, 4), most = dev.sm_count * 16;
+    return dim3(blocks < most ? blocks : most);
+}
+
+static pgemm_status route_forward(int T, int E, int k, const float *logits, int normalise,
+                                  int32_t *experts, float *weights, cudaStream_t s) {
+    pgemm_status st = route_check(T, E, k);
+    if (st != PGEMM_OK || T == 0) return st;
+    if (!logits || !experts || !weights) return PGEMM_ERR_INVALID_VALUE;
+    if (!op_aligned16(logits) || !op_aligned16(experts) || !op_aligned16(weights))
+        return PGEMM_ERR_MISALIGNED;
+    OpDevice dev;
+    if ((st = op_device(&dev)) != PGEMM_OK) return st;
+    RouteParams p{};
+    p.T = T;
+    p.E = E;
+    p.k = k;
+    p.normalise = normalise;
+    p.logits = logits;
+    p.experts = experts;
+    p.weights = weights;
+    return with_experts(E, [&](auto nv) {
+        return launch_small(route_kernel<decltype(nv)::value>, route_grid(dev, T), dim3(128), s, p);
+    });
+}
+
+static pgemm_status route_backward(int T, int E, int k, const float *logits, int normalise,
+                                   const int32_t *experts, const float *dweights, float *dlogits,
+                                   cudaStream_t s) {
+    pgemm_status st = route_check(T, E, k);
+    if (st != PGEMM_OK || T == 0) return st;
+    if (!logits || !experts || !dweights || !dlogits) return PGEMM_ERR_INVALID_VALUE;
+    if (!op_aligned16(logits) || !op_aligned16(experts) || !op_aligned16(dweights) ||
+        !op_aligned16(dlogits))
+        return PGEMM_ERR_MISALIGNED;
+    OpDevice dev;
+    if ((st = op_device(&dev)) != PGEMM_OK) return st;
+    RouteParams p{};
+    p.T = T;
+    p.E = E;
+    p.k = k;
+    p.normalise = normalise;
+    p.logits = logits;
+    p.experts_in = experts;
+    p.dweights = dweights;
+    p.dlogits = dlogits;
+    return with_experts(E, [&](auto nv) {
+        return launch_small(route_backward_kernel<decltype(nv)::value>, route_grid(dev, T),
+                            dim3(128), s, p);
+    });
+}
+
+// ------------------------------------------------------------------- sort ---
+// A block takes kSortChunk slots, a warp a run of them in order, 32 at a time: slots of
+// one expert among the 32 find one another by match, and the warp's counters of each
+// expert give the rest of a slot's rank.  Two passes over the slots (count, then place),
+// with the counters turned into first rows in between: over the block's warps, over the
+// blocks before this one, over the experts before this one.  Up to kSortChunk slots one
+// block does all of it; more take a launch that counts and one that places, each of whose
+// blocks sums the others' counts itself, or with many blocks a launch between them.
+constexpr int kSortChunk = 4096, kSortWarps = 32, kSortOwnSums = 64;
+
+struct SortParams {
+    long long slots;
+    int E, blocks;
+    const int32_t *experts;
+    int32_t *offsets, *slot_row;
+    int32_t *counts;  // [E][blocks]
+    int32_t *totals;  // [E], and counts summed over the blocks before: sort_scan_kernel's
+};
+
+// the counters of warp w: count[w * E + e]
+__device__ __forceinline__ void sort_count(const SortParams &p, int32_t *count, int warp,
+                                           int lane) {
+    constexpr int RUN = kSortChunk / kSortWarps;
+    const long long first = blockIdx.x * static_cast<long long>(kSortChunk) + warp * RUN;
+    int32_t *mine = count + warp * p.E;
+#pragma unroll 1
+    for (int i = 0; i < RUN; i += 32) {
+        const long long slot = first + i + lane;
+        const int e = slot < p.slots ? p.experts[slot] : -1;
+        const bool in = e >= 0 && e < p.E;
+        const unsigned same = __match_any_sync(0xffffffffu, in ? e : -1);
+        if (in && lane == __ffs(same) - 1) mine[e] += __popc(same);
+        __syncwarp();
+    }
+}
+
+template <bool PLACE>
+__global__ void __launch_bounds__(kSortWarps * 32) sort_kernel(const SortParams p) {
+    extern __shared__ int32_t count[];  // [kSortWarps][E]
+    __shared__ int32_t warp_total[32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int i = threadIdx.x; i < kSortWarps * p.E; i += blockDim.x) count[i] = 0;
+    __syncthreads();
+    grid_dependency_wait();
+    grid_launch_dependents();
+    sort_count(p, count, warp, lane);
+    __syncthreads();
+    // thread e: the block's count of expert e, and where each warp's part of it begins
+    const int e = threadIdx.x;
+    int all = 0;
+    if (e < p.E) {
+#pragma unroll 8
+        for (int w = 0; w < kSortWarps; ++w) {
+            const int n = count[w * p.E + e];
+            count[w * p.E + e] = all;
+            all += n;
+        }
+    }
+    if constexpr (!PLACE) {
+        if (e < p.E) p.counts[static_cast<long long>(e) * p.blocks + blockIdx.x] = all;
+        return;
+    }
+    int before = 0;  // rows of this expert in earlier blocks
+    if (p.totals != nullptr && e < p.E) {
+        before = p.counts[static_cast<long long>(e) * p.blocks + blockIdx.x];
+        all = p.totals[e];
+    } else if (p.blocks > 1 && e < p.E) {
+        all = 0;
+#pragma unroll 8
+        for (int b = 0; b < p.blocks; ++b) {
+            const int n = p.counts[static_cast<long long>(e) * p.blocks + b];
+            if (b < static_cast<int>(blockIdx.x)) before += n;
+            all += n;
+        }
+    }
+    // first rows: an exclusive sum over the experts
+    int sum = all;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int n = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += n;
+    }
+    if (lane == 31) warp_total[warp] = sum;
+    __syncthreads();
+    if (warp == 0) {
+        int t = warp_total[lane];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int n = __shfl_up_sync(0xffffffffu, t, d);
+            if (lane >= d) t += n;
+        }
+        warp_total[lane] = t;
+    }
+    __syncthreads();
+    const int first_row = sum - all + (warp > 0 ? warp_total[warp - 1] : 0);
+    if (e < p.E) {
+        if (blockIdx.x == 0) {
+            p.offsets[e] = first_row;
+            if (e == p.E - 1) p.offsets[p.E] = first_row + all;
+        }
+#pragma unroll 8
+        for (int w = 0; w < kSortWarps; ++w) count[w * p.E + e] += first_row + before;
+    }
+    __syncthreads();
+    constexpr int RUN = kSortChunk / kSortWarps;
+    const long long first = blockIdx.x * static_cast<long long>(kSortChunk) + warp * RUN;
+    int32_t *mine = count + warp * p.E;
+#pragma unroll 1
+    for (int i = 0; i < RUN; i += 32) {
+        const long long slot = first + i + lane;
+        const int x = slot < p.slots ? p.experts[slot] : -1;
+        const bool in = x >= 0 && x < p.E;
+        const unsigned same = __match_any_sync(0xffffffffu, in ? x : -1);
+        const int row = in ? mine[x] + __popc(same & ((1u << lane) - 1u)) : -1;
+        __syncwarp();
+        if (in && lane == __ffs(same) - 1) mine[x] += __popc(same);
+        __syncwarp();
+        if (slot < p.slots) p.slot_row[slot] = row;
+    }
+}
+
+// Each expert's counts <- their sums over the blocks before; a warp an expert.
+__global__ void __launch_bounds__(128) sort_scan_kernel(const SortParams p) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int e = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (e >= p.E) return;
+    int32_t *c = p.counts + static_cast<long long>(e) * p.blocks;
+    int before = 0;
+    for (int b0 = 0; b0 < p.blocks; b0 += 32) {
+        const int n = b0 + lane < p.blocks ? c[b0 + lane] : 0;
+        int sum = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, sum, d);
+            if (lane >= d) sum += o;
+        }
+        if (b0 + lane < p.blocks) c[b0 + lane] = before + sum - n;
+        before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (lane == 0) p.totals[e] = before;
+}
+
+static pgemm_status expert_sort_run(int T, int E, int k, const int32_t *experts, int32_t *offsets,
+                                    int32_t *slot_row, cudaStream_t s) {
+    if (T < 0 || E < 1 || k < 1) return PGEMM_ERR_INVALID_VALUE;
+    const long long slots = static_cast<long long>(T) * k;
+    if (E > kMaxExperts || slots > INT_MAX) return PGEMM_ERR_TOO_LARGE;
+    if (!offsets || (slots > 0 && (!experts || !slot_row))) return PGEMM_ERR_INVALID_VALUE;
+    if (!op_aligned16(experts) || !op_aligned16(offsets) || !op_aligned16(slot_row))
+        return PGEMM_ERR_MISALIGNED;
+    OpDevice dev;
+    pgemm_status st = op_device(&dev);
+    if (st != PGEMM_OK) return st;
+    if (slots == 0)
+        return cudaMemsetAsync(offsets, 0, (static_cast<size_t>(E) + 1) * 4, s) == cudaSuccess
+                   ? PGEMM_OK
+                   : PGEMM_ERR_CUDA;
+    static const KernelInfo place = [] {
+        KernelInfo k;
+        k.threads = kSortWarps * 32;
+        k.smem_bytes = kSortWarps * kMaxExperts * 4;
+        k.func = reinterpret_cast<const void *>(sort_kernel<true>);
+        return k;
+    }();
+    static const KernelInfo count = [] {
+        KernelInfo k = place;
+        k.func = reinterpret_cast<const void *>(sort_kernel<false>);
+        return k;
+    }();
+    if ((st = op_kernel_setup(dev, place, nullptr)) != PGEMM_OK) return st;
+    SortParams p{};
+    p.slots = slots;
+    p.E = E;
+    p.blocks = op_blocks(slots, kSortChunk);
+    p.experts = experts;
+    p.offsets = offsets;
+    p.slot_row = slot_row;
+    OpArena arena(dev, s);
+    const bool scan = p.blocks > kSortOwnSums;
+    const long long at = arena.add(p.blocks > 1 ? 4ll * p.blocks * E : 0);
+    const long long totals_at = arena.add(scan ? 4ll * E : 0);
+    if ((st = arena.alloc()) != PGEMM_OK) return st;
+    const size_t smem = static_cast<size_t>(kSortWarps) * E * 4;
+    if (p.blocks > 1) {
+        p.counts = arena.at<int32_t>(at);
+        if ((st = op_kernel_setup(dev, count, nullptr)) != PGEMM_OK) return st;
+        st = launch_small_smem(sort_kernel<false>, dim3(p.blocks), dim3(kSortWarps * 32), smem, s,
+                               p);
+        if (st != PGEMM_OK) return st;
+        if (scan) {
+            p.totals = arena.at<int32_t>(totals_at);
+            st = launch_small(sort_scan_kernel, dim3(op_blocks(E, 4)), dim3(128), s, p);
+            if (st != PGEMM_OK) return st;
+        }
+    }
+    return launch_small_smem(sort_kernel<true>, dim3(p.blocks), dim3(kSortWarps * 32), smem, s, p);
+}
+
+// ----------------------------------------------------- gather and combine ---
+// Rows as vectors of W bf16 values: 8 where rows are multiples of 16 bytes, else 2 or 1
+// (a token's row and its sorted rows then start at different places of a vector).  A
+// group of threads takes a token; the row of X or dY is read once, the k sorted rows
+// travel together.
+struct RowsParams {
+    int T, k, D;
+    long long rows;  // T k: a slot_row outside [0, rows) does not count
+    const uint16_t *x;        // gather: X; combine: the residual; backward: dY
+    const uint16_t *ys;       // combine and backward: Ys
+    const int32_t *slot_row;
+    const float *weights;     // nullptr: ones
+    uint16_t *out;            // gather: Xs; combine: Y; backward: dYs
+    float *dweights;
+};
+
+template <int W>
+struct Vec;
+template <>
+struct Vec<8> {
+    using T = uint4;
+};
+template <>
+struct Vec<2> {
+    using T = uint32_t;
+};
+template <>
+struct Vec<1> {
+    using T = uint16_t;
+};
+
+template <int W>
+__device__ __forceinline__ void vec_get(const typename Vec<W>::T &x, float (&f)[W]) {
+    if constexpr (W == 8) {
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = bf16_lo(w[i]);
+            f[2 * i + 1] = bf16_hi(w[i]);
+        }
+    } else if constexpr (W == 2) {
+        f[0] = bf16_lo(x);
+        f[1] = bf16_hi(x);
+    } else {
+        f[0] = __uint_as_float(static_cast<uint32_t>(x) << 16);
+    }
+}
+template <int W>
+__device__ __forceinline__ typename Vec<W>::T vec_put(const float (&f)[W]) {
+    if constexpr (W == 8)
+        return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                          pack_bf16(f[6], f[7]));
+    else if constexpr (W == 2)
+        return pack_bf16(f[0], f[1]);
+    else
+        return static_cast<uint16_t>(pack_bf16(f[0], 0.0f) & 0xffffu);
+}
+template <int W>
+__device__ __forceinline__ typename Vec<W>::T vec_zero() {
+    if constexpr (W == 8)
+        return make_uint4(0u, 0u, 0u, 0u);
+    else
+        return 0;
+}
+
+constexpr int kRowsThreads = 256;
+constexpr int kAhead = 4;  // sorted rows on the way
+
+// PER: threads of a token (a power of two up to kRowsThreads)
+template <int W>
+__global__ void __launch_bounds__(kRowsThreads) gather_kernel(const RowsParams p, int per) {
+    using V = typename Vec<W>::T;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int group = threadIdx.x / per, lane = threadIdx.x % per, groups = kRowsThreads / per;
+    const int vecs = p.D / W;
+    for (long long t = blockIdx.x * static_cast<long long>(groups) + group; t < p.T;
+         t += static_cast<long long>(gridDim.x) * groups) {
+        const V *src = reinterpret_cast<const V *>(p.x + t * p.D);
+        const int32_t *to = p.slot_row + t * p.k;
+        for (int v = lane; v < vecs; v += per) {
+            const V x = src[v];
+            for (int j = 0; j < p.k; ++j) {
+                const int r = to[j];
+                if (r >= 0 && r < p.rows)
+                    reinterpret_cast<V *>(p.out + static_cast<long long>(r) * p.D)[v] = x;
+            }
+        }
+    }
+}
+
+template <int W>
+__global__ void __launch_bounds__(kRowsThreads) combine_kernel(const RowsParams p, int per) {
+    using V = typename Vec<W>::T;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int group = threadIdx.x / per, lane = threadIdx.x % per, groups = kRowsThreads / per;
+    const int vecs = p.D / W;
+    for (long long t = blockIdx.x * static_cast<long long>(groups) + group; t < p.T;
+         t += static_cast<long long>(gridDim.x) * groups) {
+        const int32_t *from = p.slot_row + t * p.k;
+        const float *w = p.weights ? p.weights + t * p.k : nullptr;
+        for (int v = lane; v < vecs; v += per) {
+            float sum[W];
+            V res = vec_zero<W>();
+            if (p.x) res = reinterpret_cast<const V *>(p.x + t * p.D)[v];
+#pragma unroll
+            for (int i = 0; i < W; ++i) sum[i] = 0.0f;
+            for (int j0 = 0; j0 < p.k; j0 += kAhead) {
+                V y[kAhead];
+                bool in[kAhead];
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j) {
+                    const int r = j0 + j < p.k ? from[j0 + j] : -1;
+                    in[j] = r >= 0 && r < p.rows;
+                    if (in[j])
+                        y[j] = reinterpret_cast<const V *>(p.ys + static_cast<long long>(r) *
+                                                                      p.D)[v];
+                }
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j)
+                    if (in[j]) {
+                        const float wj = w ? w[j0 + j] : 1.0f;
+                        float f[W];
+                        vec_get<W>(y[j], f);
+#pragma unroll
+                        for (int i = 0; i < W; ++i) sum[i] = fmaf(wj, f[i], sum[i]);
+                    }
+            }
+            float f[W];
+            vec_get<W>(res, f);
+#pragma unroll
+            for (int i = 0; i < W; ++i) sum[i] += f[i];
+            reinterpret_cast<V *>(p.out + t * p.D)[v] = vec_put<W>(sum);
+        }
+    }
+}
+
+// PER threads a token: a warp or more.  The slots' dot products of kAhead choices at a
+// time, over the lanes' columns, then over the lanes, then over the group's warps.
+template <int W, int PER>
+__global__ void __launch_bounds__(kRowsThreads) combine_backward_kernel(const RowsParams p) {
+    using V = typename Vec<W>::T;
+    constexpr int GROUPS = kRowsThreads / PER, WARPS = PER / 32;
+    __shared__ float part[GROUPS][WARPS][kAhead];
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int group = threadIdx.x / PER, lane = threadIdx.x % PER;
+    const int vecs = p.D / W;
+    // (every group of a block makes as many rounds: they share the barriers)
+    for (long long t0 = blockIdx.x * static_cast<long long>(GROUPS); t0 < p.T;
+         t0 += static_cast<long long>(gridDim.x) * GROUPS) {
+        const long long t = t0 + group;
+        const bool have = t < p.T;
+        for (int j0 = 0; j0 < p.k; j0 += kAhead) {
+            long long row[kAhead];
+            float w[kAhead], dot[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                int r = -1;
+                w[j] = 1.0f;
+                dot[j] = 0.0f;
+                if (have && j0 + j < p.k) {
+                    r = p.slot_row[t * p.k + j0 + j];
+                    if (p.weights) w[j] = p.weights[t * p.k + j0 + j];
+                }
+                row[j] = r >= 0 && r < p.rows ? static_cast<long long>(r) * p.D : -1;
+            }
+            for (int v = lane; have && v < vecs; v += PER) {
+                float d[W];
+                const V x = reinterpret_cast<const V *>(p.x + t * p.D)[v];
+                V y[kAhead];
+                if (p.dweights) {
+#pragma unroll
+                    for (int j = 0; j < kAhead; ++j)
+                        if (row[j] >= 0) y[j] = reinterpret_cast<const V *>(p.ys + row[j])[v];
+                }
+                vec_get<W>(x, d);
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j) {
+                    if (row[j] < 0) continue;
+                    if (p.dweights) {
+                        float f[W];
+                        vec_get<W>(y[j], f);
+#pragma unroll
+                        for (int i = 0; i < W; ++i) dot[j] = fmaf(d[i], f[i], dot[j]);
+                    }
+                    if (p.out) {
+                        float o[W];
+#pragma unroll
+                        for (int i = 0; i < W; ++i) o[i] = w[j] * d[i];
+                        reinterpret_cast<V *>(p.out + row[j])[v] = vec_put<W>(o);
+                    }
+                }
+            }
+            if (!p.dweights) continue;
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) dot[j] = warp_sum(dot[j]);
+            if constexpr (WARPS > 1) {
+                if ((lane & 31) == 0) {
+#pragma unroll
+                    for (int j = 0; j < kAhead; ++j) part[group][lane >> 5][j] = dot[j];
+                }
+                __syncthreads();
+                if (lane < kAhead && have && j0 + lane < p.k) {
+                    float s = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < WARPS; ++i) s += part[group][i][lane];
+                    p.dweights[t * p.k + j0 + lane] = s;
+                }
+                __syncthreads();
+            } else if (have && lane == 0) {
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j)
+                    if (j0 + j < p.k) p.dweights[t * p.k + j0 + j] = dot[j];
+            }
+        }
+    }
+}
+
+static int rows_width(int D) { return D % 8 == 0 ? 8 : D % 2 == 0 ? 2 : 1; }
+// threads of a token: as many as it has vectors, a warp at least, a block at most
+static int rows_per(int D) {
+    const int vecs = D / rows_width(D);
+    int per = 32;
+    while (per < vecs && per < kRowsThreads) per *= 2;
+    return per;
+}
+static dim3 rows_grid(const OpDevice &dev, int T, int per) {
+    const int blocks = op_blocks(T, kRowsThreads / per), most = dev.sm_count * 16;
+    return dim3(blocks < most ? blocks : most);
+}
+template <class F>
+static pgemm_status with_width(int D, F &&f) {
+    using std::integral_constant;
+    switch (rows_width(D)) {
+        case 8: return f(integral_constant<int, 8>{});
+        case 2: return f(integral_constant<int, 2>{});
+        default: return f(integral_constant<int, 1>{});
+    }
+}
+
+static pgemm_status rows_check(int T, int k, int D) {
+    if (T < 0 || k < 1 || D < 0) return PGEMM_ERR_INVALID_VALUE;
+    return static_cast<long long>(T) * k > INT_MAX ? PGEMM_ERR_TOO_LARGE : PGEMM_OK;
+}
+
+static RowsParams rows_params(int T, int k, int D, const int32_t *slot_row) {
+    RowsParams p{};
+    p.T = T;
+    p.k = k;
+    p.D = D;
+    p.rows = static_cast<long long>(T) * k;
+    p.slot_row = slot_row;
+    return p;
+}
+
+static pgemm_status gather_run(int T, int k, int D, const uint16_t *X, const int32_t *slot_row,
+                               uint16_t *Xs, cudaStream_t s) {
+    pgemm_status st = rows_check(T, k, D);
+    if (st != PGEMM_OK || T == 0 || D == 0) return st;
+    if (!X || !slot_row || !Xs) return PGEMM_ERR_INVALID_VALUE;
+    if (!op_aligned16(X) || !op_aligned16(slot_row) || !op_aligned16(Xs))
+        return PGEMM_ERR_MISALIGNED;
+    OpDevice dev;
+    if ((st = op_device(&dev)) != PGEMM_OK) return st;
+    RowsParams p = rows_params(T, k, D, slot_row);
+    p.x = X;
+    p.out = Xs;
+    const int per = rows_per(D);
+    return with_width(D, [&](auto w) {
+        return launch_small(gather_kernel<decltype(w)::value>, rows_grid(dev, T, per),
+                            dim3(kRowsThreads), s, p, per);
+    });
+}
+
+static pgemm_status combine_run(int T, int k, int D, const uint16_t *Ys, const int32_t *slot_row,
+                                const float *weights, const uint16_t *residual, uint16_t *Y,
+                                cudaStream_t s) {
+    pgemm_status st = rows_check(T, k, D);
+    if (st != PGEMM_OK || T == 0 || D == 0) return st;
+    if (!Ys || !slot_row || !Y) return PGEMM_ERR_INVALID_VALUE;
+    if (!op_aligned16(Ys) || !op_aligned16(slot_row) || !op_aligned16(weights) ||
+        !op_aligned16(residual) || !op_aligned16(Y))
+        return PGEMM_ERR_MISALIGNED;
+    OpDevice dev;
+    if ((st = op_device(&dev)) != PGEMM_OK) return st;
+    RowsParams p = rows_params(T, k, D, slot_row);
+    p.x = residual;
+    p.ys = Ys;
+    p.weights = weights;
+    p.out = Y;
+    const int per = rows_per(D);
+    return with_width(D, [&](auto w) {
+        return launch_small(combine_kernel<decltype(w)::value>, rows_grid(dev, T, per),
+                            dim3(kRowsThreads), s, p, per);
+    });
+}
+
+static pgemm_status combine_backward_run(int T, int k, int D, const uint16_t *Ys,
+                                         const int32_t *slot_row, const float *weights,
+                                         const uint16_t *dY, uint16_t *dYs, float *dweights,
+                                         cudaStream_t s) {
+    pgemm_status st = rows_check(T, k, D);
+    if (st != PGEMM_OK || T == 0 || (!dYs && !dweights)) return st;
+    if (!slot_row || (D > 0 && (!dY || (dweights && !Ys)))) return PGEMM_ERR_INVALID_VALUE;
+    if (!op_aligned16(Ys) || !op_aligned16(slot_row) || !op_aligned16(weights) ||
+        !op_aligned16(dY) || !op_aligned16(dYs) || !op_aligned16(dweights))
+        return PGEMM_ERR_MISALIGNED;
+    OpDevice dev;
+    if ((st = op_device(&dev)) != PGEMM_OK) return st;
+    RowsParams p = rows_params(T, k, D, slot_row);
+    p.x = dY;
+    p.ys = Ys;
+    p.weights = weights;
+    p.out = dYs;
+    p.dweights = dweights;
+    const int per = rows_per(D);
+    return with_width(D, [&](auto w) {
+        constexpr int W = decltype(w)::value;
+        auto go = [&](auto n) {
+            return launch_small(combine_backward_kernel<W, decltype(n)::value>,
+                                rows_grid(dev, T, decltype(n)::value), dim3(kRowsThreads), s, p);
+        };
+        switch (per) {
+            case 32: return go(std::integral_constant<int, 32>{});
+            case 64: return go(std::integral_constant<int, 64>{});
+            case 128: return go(std::integral_constant<int, 128>{});
+            default: return go(std::integral_constant<int, 256>{});
+        }
+    });
+}
+
+}  // namespace pg
+
+extern "C" {
+
+pgemm_status route_topk(int T, int E, int k, const float *logits, int normalise, int32_t *experts,
+                        float *weights, pgemm_stream_t stream) {
+    return pg::op_guard([&] {
+        return pg::route_forward(T, E, k, logits, normalise, experts, weights, stream);
+    });
+}
+
+pgemm_status route_topk_backward(int T, int E, int k, const float *logits, int normalise,
+                                 const int32_t *experts, const float *dweights, float *dlogits,
+                                 pgemm_stream_t stream) {
+    return pg::op_guard([&] {
+        return pg::route_backward(T, E, k, logits, normalise, experts, dweights, dlogits, stream);
+    });
+}
+
+pgemm_status expert_sort(int T, int E, int k, const int32_t *experts, int32_t *offsets,
+                         int32_t *slot_row, pgemm_stream_t stream) {
+    return pg::op_guard(
+        [&] { return pg::expert_sort_run(T, E, k, experts, offsets, slot_row, stream); });
+}
+
+pgemm_status expert_gather_bf16(int T, int k, int D, const uint16_t *X, const int32_t *slot_row,
+                                uint16_t *Xs, pgemm_stream_t stream) {
+    return pg::op_guard([&] { return pg::gather_run(T, k, D, X, slot_row, Xs, stream); });
+}
+
+pgemm_status expert_combine_bf16(int T, int k, int D, const uint16_t *Ys, const int32_t *slot_row,
+                                 const float *weights, const uint16_t *residual, uint16_t *Y,
+                                 pgemm_stream_t stream) {
+    return pg::op_guard([&] {
+        return pg::combine_run(T, k, D, Ys, slot_row, weights, residual, Y, stream);
+    });
+}
+
+pgemm_status expert_combine_bf16_backward(int T, int k, int D, const uint16_t *Ys,
+                                          const int32_t *slot_row, const float *weights,
+                                          const uint16_t *dY, uint16_t *dYs, float *dweights,
+                                          pgemm_stream_t stream) {
+    return pg::op_guard([&] {
+        return pg::combine_backward_run(T, k, D, Ys, slot_row, weights, dY, dYs, dweights, stream);
+    });
+}
+
+}  // extern "C"
