@@ -44,7 +44,12 @@ enum class Exp {
 };
 
 struct ExpertsMaps {
-    CUtensorMap x[2], w[2], c[2];
+    CUtensorMap x[2][3];     // rows, in boxes of three sizes
+    CUtensorMap w[2], c[2];
+};
+struct ExpertsWeightsMaps {
+    CUtensorMap x[4], z[2][4];  // boxes of 96, 64, 32 and 16 rows
+    CUtensorMap c[2];
 };
 
 struct ExpertsArgs {
@@ -64,16 +69,20 @@ struct ExpertsArgs {
     int segments;         // and outputs
 };
 
-// CG CTAs work on a tile of CG * 128 accumulator lanes x up to TOK rows.
-template <int CG_, int TOK_, int STAGES_, Exp MODE_>
+// CG CTAs work on a tile of CG * 128 accumulator lanes x up to TOK rows, BK columns of the
+// reduction a step.  What a step's copies cost is their number: with a pair, boxes of 32
+// rows and steps of 64 columns (six copies a CTA) took 404 us for 8192 x 8192 x 4096, one
+// of 128 rows instead of the four 323.
+template <int CG_, int TOK_, int BK_, int STAGES_, Exp MODE_>
 struct ExpCfg {
-    static constexpr int CG = CG_, TOK = TOK_, STAGES = STAGES_, BK = 64, BM = 128;
+    static constexpr int CG = CG_, TOK = TOK_, STAGES = STAGES_, BK = BK_, BM = 128;
     static constexpr Exp MODE = MODE_;
     static constexpr bool DUAL = MODE == Exp::GATED || MODE == Exp::GATED_GRAD;
     static constexpr bool W_K = MODE == Exp::TRANSPOSED;  // W's rows run along the reduction
     static constexpr int FEATS = DUAL ? 64 : 128;         // features of a CTA
     static constexpr int STEP = 16 * CG;                  // granularity of a tile's rows
-    static constexpr int BOX = CG == 2 ? 32 : 16;         // rows of a TMA box
+    static constexpr int BOX = TOK / CG / 4;              // rows of the smallest TMA box
+    static constexpr int B_SUB = TOK / CG * 128;          // 64 columns of all rows
     static constexpr int A_BYTES = BM * BK * 2, B_BYTES = TOK / CG * BK * 2;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int EPI = 8;
@@ -86,7 +95,8 @@ struct ExpCfg {
     static constexpr int THREADS = 64 + 32 * EPI;
     static constexpr int SMEM_BYTES = smem_request(USED + 1024, 1);
     static_assert(USED + 1024 <= 232448, "shared memory");
-    static_assert(TOK % 32 == 0 && TMEM_COLS >= 32 && TMEM_COLS <= 512, "TOK");
+    static_assert(BK == 64 || BK == 128, "BK");
+    static_assert(BOX % 8 == 0 && TMEM_COLS >= 32 && TMEM_COLS <= 512, "TOK");
 };
 
 // The list of units, the same in every CTA: begin[e], end[e] (clamped to the rows there
@@ -147,6 +157,18 @@ __device__ __forceinline__ ExpertsTable experts_table(const ExpertsArgs &a, uint
     return t;
 }
 
+// Where a ring of stages is: stage s, in its phase.
+template <int STAGES>
+struct Ring {
+    uint32_t s = 0, phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++s == STAGES) {
+            s = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
 // One unit: rows [row0, row0 + rows) of an expert, `cols` accumulator columns, features
 // from f0 (the whole tile's).
 struct RowsUnit {
@@ -199,7 +221,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     const uint32_t warp = warp_id_uniform(), lane = lane_id();
     if (warp == 0 && lane == 0) {
         if (a.k_tiles > 0) {
-            prefetch_tmap(&maps.x[0]);
+            prefetch_tmap(&maps.x[0][0]);
             prefetch_tmap(&maps.w[0]);
         }
         for (int s = 0; s < STAGES; ++s) {
@@ -242,68 +264,87 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     if (warp == 0) {
         if (lane == 0) {
             // ---------------- producer ----------------
-            uint32_t it = 0;
+            Ring<STAGES> ring;
             bool ok = true;
+            RowsUnit next = slot < units ? rows_unit<Cfg>(table, a, slot) : RowsUnit{};
             for (int u = slot; ok && u < units; u += slots) {
-                const RowsUnit w = rows_unit<Cfg>(table, a, u);
+                const RowsUnit w = next;
                 const int half = w.cols / CG;  // columns of B in this CTA
-                const int boxes = (half + Cfg::BOX - 1) / Cfg::BOX;
+                const int boxes = (half + Cfg::BOX - 1) / Cfg::BOX;  // 1 .. 4
+                const int box = boxes == 4 ? 0 : boxes >= 2 ? 1 : 2;
                 const int y0 = w.row0 + crank * half;
-                const uint32_t tx = CG * (Cfg::A_BYTES + boxes * Cfg::BOX * 128);
-                for (int kt = 0; kt < a.k_tiles; ++kt, ++it) {
-                    const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
-                    if (!mbar_wait(&empty[s], ph ^ 1u, ctx, kSiteProducerEmpty)) {
-                        ok = false;
-                        break;
+                const uint32_t tx = CG * (Cfg::A_BYTES + boxes * Cfg::BOX * BK * 2);
+                const int f0 = w.f0 + crank * Cfg::FEATS;
+                const int segments = a.k_tiles > a.k_seg ? 2 : 1;
+                for (int sg = 0; ok && sg < segments; ++sg) {
+                    const CUtensorMap *mx = &maps.x[sg][box], *mw = &maps.w[sg];
+                    for (int k0 = 0; k0 < a.K; k0 += BK, ring.next()) {
+                        const uint32_t s = ring.s;
+                        if (!mbar_wait(&empty[s], ring.phase ^ 1u, ctx, kSiteProducerEmpty)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t lead =
+                            CG == 2 ? mapa_shared(smem_u32(&full[s]), 0) : smem_u32(&full[s]);
+                        if (crank == 0) mbar_arrive_expect_tx(&full[s], tx);
+                        auto load_w = [&](uint8_t *dst, const CUtensorMap *map, int x, int y) {
+                            if constexpr (CG == 2)
+                                tma_load_3d_pair(dst, map, lead, x, y, w.expert);
+                            else
+                                tma_load_3d(dst, map, &full[s], x, y, w.expert);
+                        };
+                        auto load_x = [&](uint8_t *dst, const CUtensorMap *map, int x, int y) {
+                            if constexpr (CG == 2)
+                                tma_load_2d_pair(dst, map, lead, x, y);
+                            else
+                                tma_load_2d(dst, map, &full[s], x, y);
+                        };
+                        uint8_t *da = sA + s * Cfg::A_BYTES, *db = sB + s * Cfg::B_BYTES;
+                        if constexpr (Cfg::W_K) {
+#pragma unroll
+                            for (int q = 0; q < BK / 64; ++q)
+                                load_w(da + q * 16384, mw, k0 + 64 * q, f0);
+                        } else {
+                            load_w(da, &maps.w[0], f0, k0);
+                            load_w(da + BK * 128, &maps.w[Cfg::DUAL ? 1 : 0],
+                                   Cfg::DUAL ? f0 : f0 + 64, k0);
+                        }
+#pragma unroll
+                        for (int q = 0; q < BK / 64; ++q)
+                            load_x(db + q * Cfg::B_SUB, mx, k0 + 64 * q, y0);
+                        if (boxes == 3) {
+#pragma unroll
+                            for (int q = 0; q < BK / 64; ++q)
+                                load_x(db + q * Cfg::B_SUB + 2 * Cfg::BOX * 128, &maps.x[sg][2],
+                                       k0 + 64 * q, y0 + 2 * Cfg::BOX);
+                        }
                     }
-                    const int sg = kt >= a.k_seg ? 1 : 0, k0 = (kt - sg * a.k_seg) * BK;
-                    const uint32_t lead =
-                        CG == 2 ? mapa_shared(smem_u32(&full[s]), 0) : smem_u32(&full[s]);
-                    if (crank == 0) mbar_arrive_expect_tx(&full[s], tx);
-                    auto load_w = [&](uint8_t *dst, const CUtensorMap *map, int x, int y) {
-                        if constexpr (CG == 2)
-                            tma_load_3d_pair(dst, map, lead, x, y, w.expert);
-                        else
-                            tma_load_3d(dst, map, &full[s], x, y, w.expert);
-                    };
-                    uint8_t *da = sA + s * Cfg::A_BYTES, *db = sB + s * Cfg::B_BYTES;
-                    if constexpr (Cfg::W_K) {
-                        load_w(da, &maps.w[sg], k0, w.f0 + crank * 128);
-                    } else if constexpr (Cfg::DUAL) {
-                        load_w(da, &maps.w[0], w.f0 + crank * 64, k0);
-                        load_w(da + BK * 128, &maps.w[1], w.f0 + crank * 64, k0);
-                    } else {
-                        load_w(da, &maps.w[0], w.f0 + crank * 128, k0);
-                        load_w(da + BK * 128, &maps.w[0], w.f0 + crank * 128 + 64, k0);
-                    }
-                    for (int j = 0; j < boxes; ++j) {
-                        uint8_t *dst = db + j * (Cfg::BOX * 128);
-                        if constexpr (CG == 2)
-                            tma_load_2d_pair(dst, &maps.x[sg], lead, k0, y0 + j * Cfg::BOX);
-                        else
-                            tma_load_2d(dst, &maps.x[sg], &full[s], k0, y0 + j * Cfg::BOX);
-                    }
+                    // (found while these copies travel)
+                    if (sg == 0 && u + slots < units)
+                        next = rows_unit<Cfg>(table, a, u + slots);
                 }
             }
             if constexpr (CG == 2) {
                 // the pair's last multicast releases of this CTA's barriers must
                 // have landed before the cluster is left
-                for (int i = 0; ok && i < STAGES; ++i, ++it) {
-                    const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
-                    ok = mbar_wait(&empty[s], ph ^ 1u, ctx, kSiteProducerEmpty);
-                }
+                for (int i = 0; ok && i < STAGES; ++i, ring.next())
+                    ok = mbar_wait(&empty[ring.s], ring.phase ^ 1u, ctx, kSiteProducerEmpty);
             }
         }
     } else if (warp == 1) {
         if (lane == 0 && crank == 0) {
             // ---------------- MMA issuer ----------------
             constexpr uint16_t kPair = 3;
-            uint32_t it = 0, n = 0;
+            // descriptors of the first stage; addresses count in 16 bytes
+            const uint64_t a0 = smem_desc_sw128(smem_u32(sA), Cfg::W_K ? 16 : BK * 128, 1024);
+            const uint64_t b0 = smem_desc_sw128(smem_u32(sB), 16, 1024);
+            Ring<STAGES> ring;
+            uint32_t n = 0;
             bool ok = true;
-            for (int u = slot; ok && u < units && a.k_tiles > 0; u += slots, ++n) {
-                const RowsUnit w = rows_unit<Cfg>(table, a, u);
+            int cols = slot < units ? rows_unit<Cfg>(table, a, slot).cols : 0, next = 0;
+            for (int u = slot; ok && u < units && a.k_tiles > 0; u += slots, ++n, cols = next) {
                 const uint32_t idesc =
-                    idesc_f16(Cfg::BM * CG, w.cols, 1, Cfg::W_K ? 0 : 1, /*B K-major*/ 0);
+                    idesc_f16(Cfg::BM * CG, cols, 1, Cfg::W_K ? 0 : 1, /*B K-major*/ 0);
                 const uint32_t ab = n & 1u;
                 if (!mbar_wait(&acc_empty[ab], ((n >> 1) & 1u) ^ 1u, ctx, kSiteMmaAccEmpty)) {
                     ok = false;
@@ -311,32 +352,42 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 }
                 tc_fence_after();
                 const uint32_t d = tmem + ab * TOK;
-                for (int kt = 0; kt < a.k_tiles; ++kt, ++it) {
-                    const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
-                    if (!mbar_wait(&full[s], ph, ctx, kSiteMmaFull)) {
+                int left = a.K;  // of the segment
+                uint32_t acc = 0;
+                for (int kt = 0; kt < a.k_tiles; ++kt, ring.next()) {
+                    const uint32_t s = ring.s;
+                    if (!mbar_wait(&full[s], ring.phase, ctx, kSiteMmaFull)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t sa = smem_u32(sA + s * Cfg::A_BYTES);
-                    const uint32_t sb = smem_u32(sB + s * Cfg::B_BYTES);
-#pragma unroll
-                    for (int k = 0; k < BK / 16; ++k) {
-                        const uint64_t ad = Cfg::W_K
-                                                ? smem_desc_sw128(sa + k * 32, 16, 1024)
-                                                : smem_desc_sw128(sa + k * 2048, BK * 128, 1024);
-                        const uint64_t bd = smem_desc_sw128(sb + k * 32, 16, 1024);
-                        const uint32_t acc = (kt == 0 && k == 0) ? 0u : 1u;
+                    const uint64_t as = a0 + s * (Cfg::A_BYTES / 16), bs = b0 + s * (Cfg::B_BYTES / 16);
+                    auto multiply = [&](int k) {
+                        const uint64_t ad =
+                            as + (Cfg::W_K ? k / 4 * 16384 + k % 4 * 32 : k * 2048) / 16;
+                        const uint64_t bd = bs + (k / 4 * Cfg::B_SUB + k % 4 * 32) / 16;
                         if constexpr (CG == 2)
                             umma_f16_ss_pair(d, ad, bd, idesc, acc);
                         else
                             umma_f16_ss(d, ad, bd, idesc, acc);
+                        acc = 1;
+                    };
+                    if (left >= BK) {
+#pragma unroll
+                        for (int k = 0; k < BK / 16; ++k) multiply(k);
+                        left -= BK;
+                    } else {  // what lies wholly beyond K is zero fill
+#pragma unroll 1
+                        for (int k = 0; 16 * k < left; ++k) multiply(k);
+                        left = 0;
                     }
+                    if (left == 0) left = a.K;
                     if constexpr (CG == 2)
                         umma_commit_pair_multicast(&empty[s], kPair);
                     else
                         umma_commit(&empty[s]);
                 }
+                if (u + slots < units) next = rows_unit<Cfg>(table, a, u + slots).cols;
                 if (ok) {
                     if constexpr (CG == 2)
                         umma_commit_pair_multicast(&acc_full[ab], kPair);
@@ -494,37 +545,47 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 }
 
 // ------------------------------------------------------ weights' gradients ---
-// dW[e] = X_e^T dZ_e in 256 x 256 tiles on a CTA pair: A = X^T M-major, B = dZ N-major,
-// both in boxes of 64 columns x 64 rows.
-template <int STAGES_, int NBUF_>
+// dW[e] = X_e^T dZ_e in 256 x 256 tiles on a CTA pair, BK rows a step: A = X^T M-major,
+// B = dZ N-major, both in boxes of 64 columns.
+//
+// A product of the tensor core takes 16 rows.  A group's rows in whole sixteens go through
+// the ring; what is left of the sixteen that its last row lies in belongs to the next
+// group, and may hold anything.  Those 16 rows have buffers of their own: they are fetched
+// when the unit begins, a warp of each CTA clears what is not the group's, and they are
+// multiplied last, so that neither the clearing nor the two CTAs' agreement on it is
+// waited for.  (Cleared in the ring's last stage, groups of 520 rows took 258 us for 32
+// experts' 2048 x 4096, 512 rows 182.)
+template <int BK_, int STAGES_, int NBUF_>
 struct ExpWeightsCfg {
-    static constexpr int BM = 128, BN = 256, BK = 64, STAGES = STAGES_, NBUF = NBUF_;
+    static constexpr int BM = 128, BN = 256, BK = BK_, STAGES = STAGES_, NBUF = NBUF_;
     static constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN / 2 * BK * 2;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+    static constexpr int TAIL_HALF = 128 * 16 * 2, TAIL_BYTES = 2 * TAIL_HALF;  // a buffer
     static constexpr int EPI = 8, EPI_COLS = BN / 2;
-    static constexpr int STAGING_OFFSET = STAGES * STAGE_BYTES;
+    static constexpr int TAIL_OFFSET = STAGES * STAGE_BYTES;
+    static constexpr int STAGING_OFFSET = TAIL_OFFSET + 2 * TAIL_BYTES;
     static constexpr int BAR_OFFSET = STAGING_OFFSET + EPI * NBUF * 2048;
-    static constexpr int TABLE_OFFSET = BAR_OFFSET + (2 * STAGES + 6) * 8 + 16;
-    static constexpr int USED = TABLE_OFFSET + (3 * kExpertsMax + 1) * 4;
+    static constexpr int USED = BAR_OFFSET + (2 * STAGES + 13) * 8 + 16;
     static constexpr int TMEM_COLS = 2 * BN;
-    static constexpr int THREADS = 64 + 32 * EPI;
+    static constexpr int THREADS = 64 + 32 * EPI + 32;
     static constexpr int SMEM_BYTES = smem_request(USED + 1024, 1);
     static_assert(USED + 1024 <= 232448, "shared memory");
     static_assert(EPI_COLS / 32 % NBUF == 0, "whole batches");
+    static_assert(BK == 96, "a step is a box of 96 rows, or shorter ones of 64 and 32");
 };
 
 struct WeightsUnit {
     int expert, begin, end, seg, m0, n0;
+    __device__ __forceinline__ int whole() const { return begin + (end - begin) / 16 * 16; }
 };
 
 template <class Cfg>
-__device__ __forceinline__ WeightsUnit weights_unit(const ExpertsTable &t, const ExpertsArgs &a,
-                                                    int u) {
+__device__ __forceinline__ WeightsUnit weights_unit(const ExpertsArgs &a, int u) {
     WeightsUnit w;
     const int n_tiles = a.n_seg * a.segments, per = a.f_tiles * n_tiles;
     w.expert = u / per;
-    w.begin = t.begin[w.expert];
-    w.end = t.end[w.expert];
+    w.begin = min(max(a.offsets[w.expert], 0), a.R);
+    w.end = min(max(a.offsets[w.expert + 1], w.begin), a.R);
     const int r = u - w.expert * per;
     const int group = r / (8 * n_tiles), first = group * 8;
     const int g = min(a.f_tiles - first, 8), q = r - group * 8 * n_tiles;
@@ -567,7 +628,7 @@ __device__ __forceinline__ void put_rows32_batch_3d(Ctx &c, const CUtensorMap *m
 
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
-    experts_weights_kernel(const __grid_constant__ ExpertsMaps maps, const ExpertsArgs a,
+    experts_weights_kernel(const __grid_constant__ ExpertsWeightsMaps maps, const ExpertsArgs a,
                            const KernelCtx ctx) {
     constexpr int STAGES = Cfg::STAGES, BK = Cfg::BK, BM = Cfg::BM, BN = Cfg::BN;
     extern __shared__ uint8_t smem_raw[];
@@ -578,23 +639,31 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     uint64_t *acc_full = empty + STAGES;  // [2]
     uint64_t *acc_empty = acc_full + 2;   // [2]
     uint64_t *mma_done = acc_empty + 2;
-    uint64_t *tail = mma_done + 1;        // a group's last K step, in this CTA
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tail + 1);
+    uint64_t *tail_full = mma_done + 1;   // [2] last rows fetched, in this CTA
+    uint64_t *tail_peer = tail_full + 2;  // [2] the peer's are cleared
+    uint64_t *tail_ready = tail_peer + 2; // [2] both are
+    uint64_t *tail_empty = tail_ready + 2;  // [2] they have been multiplied
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tail_empty + 2);
     const uint32_t warp = warp_id_uniform(), lane = lane_id();
     const int crank = static_cast<int>(cluster_ctarank());
     if (warp == 0 && lane == 0) {
         prefetch_tmap(&maps.x[0]);
-        prefetch_tmap(&maps.w[0]);
+        prefetch_tmap(&maps.z[0][0]);
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(&full[s], 2);  // a producer of each CTA
+            mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&tail_full[b], 1);
+            mbar_init(&tail_peer[b], 1);
+            mbar_init(&tail_ready[b], 1);
+            mbar_init(&tail_empty[b], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_empty[b], Cfg::EPI * 2);
         }
         mbar_init(mma_done, 1);
-        mbar_init(tail, 1);
         fence_barrier_init();
     }
     if (warp == 1) {
@@ -607,83 +676,100 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     op_begin(0);
-    const ExpertsTable table =
-        experts_table(a, smem + Cfg::TABLE_OFFSET, [](int) { return 0; });
     const int units = a.E * a.f_tiles * a.n_seg * a.segments;
     const int slot = static_cast<int>(blockIdx.x) / 2, slots = static_cast<int>(gridDim.x) / 2;
 
     if (warp == 0) {
-        // ---------------- producer (the whole warp, for the groups' ends) ----------------
-        uint32_t it = 0, tails = 0;
-        bool ok = true;
-        for (int u = slot; ok && u < units; u += slots) {
-            const WeightsUnit w = weights_unit<Cfg>(table, a, u);
-            const CUtensorMap *mb = &maps.w[w.seg];
-            for (int y = w.begin; y < w.end; y += BK, ++it) {
-                const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
-                uint8_t *da = sA + s * Cfg::A_BYTES, *db = sB + s * Cfg::B_BYTES;
+        if (lane == 0) {
+            // ---------------- producer ----------------
+            Ring<STAGES> ring;
+            uint32_t tails = 0;
+            bool ok = true;
+            for (int u = slot; ok && u < units; u += slots) {
+                const WeightsUnit w = weights_unit<Cfg>(a, u);
+                const CUtensorMap *mx = maps.x, *mz = maps.z[w.seg];
                 const int ma = w.m0 + crank * BM, nb = w.n0 + crank * (BN / 2);
-                const int rows = w.end - y;
-                if (lane == 0) ok = mbar_wait(&empty[s], ph ^ 1u, ctx, kSiteProducerEmpty);
-                ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0) != 0;
-                if (!ok) break;
-                const uint32_t lead = mapa_shared(smem_u32(&full[s]), 0);
-                if (rows >= BK) {
-                    if (lane == 0) {
-                        // both CTAs' bytes are counted by the leader's barrier
-                        if (crank == 0)
-                            mbar_arrive_expect_tx(&full[s], 2 * Cfg::STAGE_BYTES);
-                        else
-                            mbar_arrive_cluster(lead);
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            tma_load_2d_pair(da + j * 8192, &maps.x[0], lead, ma + 64 * j, y);
-                            tma_load_2d_pair(db + j * 8192, mb, lead, nb + 64 * j, y);
-                        }
+                const int whole = w.whole();
+                if (whole < w.end) {
+                    const uint32_t b = tails & 1u;
+                    if (!mbar_wait(&tail_empty[b], ((tails >> 1) & 1u) ^ 1u, ctx, kSiteGroupTail)) {
+                        ok = false;
+                        break;
                     }
-                } else {
-                    // what follows the group's last row in the step belongs to others
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(tail, Cfg::STAGE_BYTES);
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            tma_load_2d(da + j * 8192, &maps.x[0], tail, ma + 64 * j, y);
-                            tma_load_2d(db + j * 8192, mb, tail, nb + 64 * j, y);
-                        }
-                    }
-                    // (every lane waits: it must see the copies before it overwrites them)
-                    ok = mbar_wait(tail, tails & 1u, ctx, kSiteGroupTail);
-                    ok = __all_sync(0xffffffffu, ok);
                     ++tails;
-                    if (!ok) break;
-                    for (int r = rows * 8 + static_cast<int>(lane); r < BK * 8; r += 32)
+                    uint8_t *d = smem + Cfg::TAIL_OFFSET + b * Cfg::TAIL_BYTES;
+                    mbar_arrive_expect_tx(&tail_full[b], Cfg::TAIL_BYTES);
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            sts128(smem_u32(da) + j * 8192 + r * 16, 0u, 0u, 0u, 0u);
-                            sts128(smem_u32(db) + j * 8192 + r * 16, 0u, 0u, 0u, 0u);
-                        }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(lead);
+                    for (int j = 0; j < 2; ++j) {
+                        tma_load_2d(d + j * 2048, &mx[3], &tail_full[b], ma + 64 * j, whole);
+                        tma_load_2d(d + Cfg::TAIL_HALF + j * 2048, &mz[3], &tail_full[b],
+                                    nb + 64 * j, whole);
+                    }
+                }
+                for (int y = w.begin; y < whole; y += BK, ring.next()) {
+                    const uint32_t s = ring.s;
+                    if (!mbar_wait(&empty[s], ring.phase ^ 1u, ctx, kSiteProducerEmpty)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *da = sA + s * Cfg::A_BYTES, *db = sB + s * Cfg::B_BYTES;
+                    const uint32_t lead = mapa_shared(smem_u32(&full[s]), 0);
+                    // a box of 96 rows, in a last step perhaps of 64 or 32
+                    const int thirds = min(3, (whole - y + 31) / 32);
+                    if (crank == 0)
+                        mbar_arrive_expect_tx(&full[s], thirds * (2 * Cfg::STAGE_BYTES / 3));
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        tma_load_2d_pair(da + j * (BK * 128), &mx[3 - thirds], lead, ma + 64 * j, y);
+                        tma_load_2d_pair(db + j * (BK * 128), &mz[3 - thirds], lead, nb + 64 * j, y);
+                    }
                 }
             }
+            // the pair's last multicast releases of this CTA's barriers must have landed
+            // before the cluster is left
+            for (int i = 0; ok && i < STAGES; ++i, ring.next())
+                ok = mbar_wait(&empty[ring.s], ring.phase ^ 1u, ctx, kSiteProducerEmpty);
+            for (int i = 0; ok && i < 2; ++i, ++tails)
+                ok = mbar_wait(&tail_empty[tails & 1u], ((tails >> 1) & 1u) ^ 1u, ctx,
+                               kSiteGroupTail);
         }
-        // the pair's last multicast releases of this CTA's barriers must have landed
-        // before the cluster is left
-        if (lane == 0)
-            for (int i = 0; ok && i < STAGES; ++i, ++it) {
-                const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
-                ok = mbar_wait(&empty[s], ph ^ 1u, ctx, kSiteProducerEmpty);
+    } else if (warp == Cfg::THREADS / 32 - 1) {
+        // ---------------- the groups' last rows ----------------
+        uint32_t tails = 0;
+        for (int u = slot; u < units; u += slots) {
+            const WeightsUnit w = weights_unit<Cfg>(a, u);
+            const int rows = w.end - w.whole();
+            if (rows == 0) continue;
+            const uint32_t b = tails & 1u, ph = (tails >> 1) & 1u;
+            ++tails;
+            // (every lane waits: it must see the copies before it overwrites them)
+            if (!__all_sync(0xffffffffu, mbar_wait(&tail_full[b], ph, ctx, kSiteGroupTail))) break;
+            const uint32_t d = smem_u32(smem + Cfg::TAIL_OFFSET + b * Cfg::TAIL_BYTES);
+            for (int r = rows * 8 + static_cast<int>(lane); r < 16 * 8; r += 32)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sts128(d + j * 2048 + r * 16, 0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                if (crank == 1)
+                    mbar_arrive_cluster(mapa_shared(smem_u32(&tail_peer[b]), 0));
+                else if (mbar_wait_cluster(&tail_peer[b], ph, ctx, kSiteGroupTail))
+                    mbar_arrive(&tail_ready[b]);
             }
+            __syncwarp();
+        }
     } else if (warp == 1) {
         if (lane == 0 && crank == 0) {
             // ---------------- MMA issuer ----------------
             constexpr uint16_t kPair = 3;
             constexpr uint32_t idesc = idesc_f16(BM * 2, BN, 1, 1, 1);
-            uint32_t it = 0, n = 0;
+            const uint64_t a0 = smem_desc_sw128(smem_u32(sA), BK * 128, 1024);
+            const uint64_t b0 = smem_desc_sw128(smem_u32(sB), BK * 128, 1024);
+            Ring<STAGES> ring;
+            uint32_t n = 0, tails = 0;
             bool ok = true;
             for (int u = slot; ok && u < units; u += slots) {
-                const WeightsUnit w = weights_unit<Cfg>(table, a, u);
+                const WeightsUnit w = weights_unit<Cfg>(a, u);
                 if (w.end <= w.begin) continue;
                 const uint32_t ab = n & 1u;
                 if (!mbar_wait(&acc_empty[ab], ((n >> 1) & 1u) ^ 1u, ctx, kSiteMmaAccEmpty)) {
@@ -693,21 +779,41 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 ++n;
                 tc_fence_after();
                 const uint32_t d = tmem + ab * BN;
-                for (int y = w.begin; y < w.end; y += BK, ++it) {
-                    const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
-                    if (!mbar_wait_cluster(&full[s], ph, ctx, kSiteMmaFull)) {
+                const int whole = w.whole();
+                uint32_t acc = 0;
+                for (int y = w.begin; y < whole; y += BK, ring.next()) {
+                    const uint32_t s = ring.s;
+                    if (!mbar_wait(&full[s], ring.phase, ctx, kSiteMmaFull)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t sa = smem_u32(sA + s * Cfg::A_BYTES);
-                    const uint32_t sb = smem_u32(sB + s * Cfg::B_BYTES);
+                    const uint64_t as = a0 + s * (Cfg::A_BYTES / 16), bs = b0 + s * (Cfg::B_BYTES / 16);
+                    auto multiply = [&](int k) {
+                        umma_f16_ss_pair(d, as + k * 128, bs + k * 128, idesc, acc);
+                        acc = 1;
+                    };
+                    if (whole - y >= BK) {
 #pragma unroll
-                    for (int k = 0; k < BK / 16; ++k)
-                        umma_f16_ss_pair(d, smem_desc_sw128(sa + k * 2048, BK * 128, 1024),
-                                         smem_desc_sw128(sb + k * 2048, BK * 128, 1024), idesc,
-                                         (y == w.begin && k == 0) ? 0u : 1u);
+                        for (int k = 0; k < BK / 16; ++k) multiply(k);
+                    } else {
+#pragma unroll 1
+                        for (int k = 0; 16 * k < whole - y; ++k) multiply(k);
+                    }
                     umma_commit_pair_multicast(&empty[s], kPair);
+                }
+                if (ok && whole < w.end) {
+                    const uint32_t b = tails & 1u;
+                    if (!mbar_wait(&tail_ready[b], (tails >> 1) & 1u, ctx, kSiteGroupTail)) {
+                        ok = false;
+                        break;
+                    }
+                    ++tails;
+                    tc_fence_after();
+                    const uint32_t st = smem_u32(smem + Cfg::TAIL_OFFSET + b * Cfg::TAIL_BYTES);
+                    umma_f16_ss_pair(d, smem_desc_sw128(st, 2048, 1024),
+                                     smem_desc_sw128(st + Cfg::TAIL_HALF, 2048, 1024), idesc, acc);
+                    umma_commit_pair_multicast(&tail_empty[b], kPair);
                 }
                 if (ok) umma_commit_pair_multicast(&acc_full[ab], kPair);
             }
@@ -726,7 +832,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         const int col0 = static_cast<int>(e >> 2) * Cfg::EPI_COLS;
         uint32_t n = 0;
         for (int u = slot; u < units; u += slots) {
-            const WeightsUnit w = weights_unit<Cfg>(table, a, u);
+            const WeightsUnit w = weights_unit<Cfg>(a, u);
             c.m0 = w.m0 + crank * BM + static_cast<int>(q * 32);
             const uint32_t ab = n & 1u;
             const bool have = w.end > w.begin;
@@ -781,7 +887,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 }
 
 // ------------------------------------------------------------------- host ---
-using ExpKernel = void (*)(const ExpertsMaps, const ExpertsArgs, const KernelCtx);
+template <class Maps>
+using ExpKernel = void (*)(const Maps, const ExpertsArgs, const KernelCtx);
 
 template <int CG>
 static cudaError_t exp_slots_of(const void *func, int threads, int smem, int sm_count, int *slots) {
@@ -810,8 +917,8 @@ static cudaError_t exp_slots_of(const void *func, int threads, int smem, int sm_
 }
 
 // One launch on as many CTAs (pairs) as run at once, or as there can be units.
-template <class Cfg, int CG, ExpKernel KERNEL>
-static pgemm_status exp_launch(const OpDevice &dev, const ExpertsMaps &maps, const ExpertsArgs &a,
+template <class Cfg, int CG, class Maps, ExpKernel<Maps> KERNEL>
+static pgemm_status exp_launch(const OpDevice &dev, const Maps &maps, const ExpertsArgs &a,
                                long long most_units, cudaStream_t stream) {
     static const KernelInfo info = [] {
         KernelInfo k;
@@ -873,15 +980,16 @@ static pgemm_status rows_launch(const OpDevice &dev, const ExpSizes &z, const Op
     ExpertsMaps maps{};
     const int ws = Cfg::DUAL ? 2 : segments;
     pgemm_status st = PGEMM_OK;
-    for (int j = 0; a.K > 0 && j < segments && st == PGEMM_OK; ++j)
-        st = op_encode(&maps.x[j], x[j].p, a.K, z.R, x[j].ld, Cfg::BOX);
+    for (int j = 0; a.K > 0 && j < segments; ++j)
+        for (int b = 0; b < 3 && st == PGEMM_OK; ++b)
+            st = op_encode(&maps.x[j][b], x[j].p, a.K, z.R, x[j].ld, Cfg::BOX * (4 >> b));
     for (int j = 0; a.K > 0 && j < ws && st == PGEMM_OK; ++j)
-        st = op_encode_3d(&maps.w[j], w[j].p, z.N, z.K, z.E, w[j].ld, T ? 128 : 64);
+        st = op_encode_3d(&maps.w[j], w[j].p, z.N, z.K, z.E, w[j].ld, T ? 128 : Cfg::BK);
     if (st != PGEMM_OK) return st;
     // units at most: every tile of rows full, and a partial one more for each expert
     const long long live = z.R < z.E ? z.R : z.E;
     const long long most = (z.R / Cfg::TOK + live) * a.f_tiles;
-    return exp_launch<Cfg, Cfg::CG, experts_rows_kernel<Cfg>>(dev, maps, a, most, s);
+    return exp_launch<Cfg, Cfg::CG, ExpertsMaps, experts_rows_kernel<Cfg>>(dev, maps, a, most, s);
 }
 
 template <Exp MODE>
@@ -890,16 +998,15 @@ static pgemm_status rows_product(const OpDevice &dev, const ExpSizes &z, const O
                                  cudaStream_t s) {
     // few rows a group: the weights are all there is to read, and single CTAs with small
     // tiles of rows keep more of them on the way
-    if (z.R <= 48ll * z.E) return rows_launch<ExpCfg<1, 64, 8, MODE>>(dev, z, x, w, segments, a, s);
-    return rows_launch<ExpCfg<2, 256, 6 - (MODE == Exp::GATED || MODE == Exp::GATED_GRAD), MODE>>(
-        dev, z, x, w, segments, a, s);
+    if (z.R <= 48ll * z.E) return rows_launch<ExpCfg<1, 64, 128, 4, MODE>>(dev, z, x, w, segments, a, s);
+    return rows_launch<ExpCfg<2, 256, 128, 3, MODE>>(dev, z, x, w, segments, a, s);
 }
 
 // dW[j][e] = x_e^T dz[j]_e for each of `segments` outputs.
 static pgemm_status weights_product(const OpDevice &dev, const ExpSizes &z, const OpMat &x,
                                     const OpMat *dz, int segments, uint16_t *const *out,
                                     cudaStream_t s) {
-    using Cfg = ExpWeightsCfg<5, 2>;
+    using Cfg = ExpWeightsCfg<96, 4, 1>;
     ExpertsArgs a{};
     a.R = z.R;
     a.E = z.E;
@@ -912,16 +1019,20 @@ static pgemm_status weights_product(const OpDevice &dev, const ExpSizes &z, cons
     a.out = out[0];
     a.out2 = segments > 1 ? out[1] : nullptr;
     a.tma_out = z.N % 8 == 0;
-    ExpertsMaps maps{};
-    pgemm_status st = op_encode(&maps.x[0], x.p, z.K, z.R, x.ld, 64);
+    ExpertsWeightsMaps maps{};
+    constexpr int kBoxes[4] = {Cfg::BK, 64, 32, 16};
+    pgemm_status st = PGEMM_OK;
+    for (int b = 0; b < 4 && st == PGEMM_OK; ++b)
+        st = op_encode(&maps.x[b], x.p, z.K, z.R, x.ld, kBoxes[b]);
     for (int j = 0; j < segments && st == PGEMM_OK; ++j) {
-        st = op_encode(&maps.w[j], dz[j].p, z.N, z.R, dz[j].ld, 64);
+        for (int b = 0; b < 4 && st == PGEMM_OK; ++b)
+            st = op_encode(&maps.z[j][b], dz[j].p, z.N, z.R, dz[j].ld, kBoxes[b]);
         if (st == PGEMM_OK && a.tma_out)
             st = op_encode_out_3d(&maps.c[j], out[j], z.N, z.K, z.E, z.N);
     }
     if (st != PGEMM_OK) return st;
     const long long units = static_cast<long long>(z.E) * a.f_tiles * a.n_seg * segments;
-    return exp_launch<Cfg, 2, experts_weights_kernel<Cfg>>(dev, maps, a, units, s);
+    return exp_launch<Cfg, 2, ExpertsWeightsMaps, experts_weights_kernel<Cfg>>(dev, maps, a, units, s);
 }
 
 static pgemm_status exp_check(const ExpSizes &z) {
