@@ -8,10 +8,10 @@
 // whole either way, and its sum of squares costs nothing beside that.
 //
 // A block takes a row at a time and keeps it in registers between the sum and the
-// outputs, so every operand is read once.  All operands have the same pitch and
-// 16-byte-aligned bases, so a row starts at the same place of a 16-byte vector in each:
-// a thread takes whole aligned vectors (eight elements of the flat matrix), masked at
-// the row's two ends, whatever the width.
+// outputs, so every operand is read once; the next row's operands travel meanwhile.  All
+// operands have the same pitch and 16-byte-aligned bases, so a row starts at the same place
+// of a 16-byte vector in each: a thread takes whole aligned vectors (eight elements of the
+// flat matrix), masked at the row's two ends, whatever the width.  Bound by HBM.
 #include <cuda_runtime.h>
 
 #include "op_gemm.cuh"
@@ -105,21 +105,28 @@ struct Larger {  // a NaN stays one
     }
 };
 
-// op over the block's threads, in an order that does not depend on timing; the same in
-// every thread.  `part` (32 floats) may be used again after the block's next barrier.
-template <int THREADS, class Op>
-__device__ __forceinline__ float block_reduce(float x, float *part, Op op) {
+// op of N values over the block's threads, in an order that does not depend on timing; the
+// same in every thread.  `part` may be used again after the block's next barrier.
+template <int N, class Op>
+__device__ __forceinline__ void block_reduce(float (&x)[N], float (*part)[32], Op op) {
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) x = op(x, __shfl_xor_sync(0xffffffffu, x, d));
-    if constexpr (THREADS > 32) {
-        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = x;
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) x[i] = op(x[i], __shfl_xor_sync(0xffffffffu, x[i], d));
+    const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+    if (warps > 1) {
+        if (lane == 0) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) part[i][threadIdx.x >> 5] = x[i];
+        }
         __syncthreads();
-        constexpr int W = THREADS / 32;
-        x = part[(threadIdx.x & 31) % W];
 #pragma unroll
-        for (int d = W / 2; d > 0; d >>= 1) x = op(x, __shfl_xor_sync(0xffffffffu, x, d));
+        for (int i = 0; i < N; ++i) {
+            x[i] = lane < warps ? part[i][lane] : 0.0f;
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) x[i] = op(x[i], __shfl_xor_sync(0xffffffffu, x[i], d));
+        }
     }
-    return x;
 }
 
 struct NormParams {
@@ -135,83 +142,136 @@ struct NormParams {
     float *dgain;  // [blocks][D] partial sums, or nullptr
 };
 
-template <int THREADS, int V, bool I8>
-__global__ void __launch_bounds__(THREADS) rmsnorm_kernel(const NormParams p) {
-    __shared__ float part[2][32];
+// The gains of a thread's vectors: where rows start on vectors they are the same for every
+// row, and stay in registers.
+template <int V, bool ALIGNED>
+struct Gains {
+    uint4 kept[ALIGNED ? V : 1];
+    __device__ __forceinline__ Gains(const NormParams &p) {
+        if constexpr (ALIGNED) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int v = threadIdx.x + i * blockDim.x;
+                kept[i] = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+                if (p.gain != nullptr && 8 * v < p.D)
+                    kept[i] = *(reinterpret_cast<const uint4 *>(p.gain) + v);
+            }
+        }
+    }
+    __device__ __forceinline__ void get(const NormParams &p, const RowSpan &row, int i, int v,
+                                        float (&g)[8]) const {
+        if constexpr (ALIGNED)
+            unpack8(kept[i], g);
+        else
+            gain_load(p.gain, row, v, g);
+    }
+};
+
+// V vectors a thread; ALIGNED: D is a multiple of 8.  With more than two vectors a thread
+// the next row is not fetched ahead, for want of registers.
+template <int V, bool ALIGNED, bool I8>
+__global__ void __launch_bounds__(V <= 2 ? 512 : 1024) rmsnorm_kernel(const NormParams p) {
+    __shared__ float part[2][1][32];
+    constexpr bool AHEAD = V <= 2;
     grid_dependency_wait();
     grid_launch_dependents();
+    const Gains<V, ALIGNED> gains(p);
     int turn = 0;
-    for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
+    uint4 a[V], b[V];
+    auto fetch = [&](int t) {
         const RowSpan row(t, p.D);
-        float f[V][8];
-        float sum = 0.0f;
-        uint4 a[V], b[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int v = threadIdx.x + i * THREADS;
+            const int v = threadIdx.x + i * blockDim.x;
             a[i] = b[i] = make_uint4(0u, 0u, 0u, 0u);
             if (v < row.vecs) {
                 a[i] = row_load(p.x, row, v);
                 if (p.r) b[i] = row_load(p.r, row, v);
             }
         }
+    };
+    int t = blockIdx.x;
+    if (AHEAD && t < p.T) fetch(t);
+    for (; t < p.T; t += gridDim.x) {
+        if (!AHEAD) fetch(t);
+        const RowSpan row(t, p.D);
+        uint4 s[V];
+        float sum[1] = {0.0f};
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int v = threadIdx.x + i * THREADS;
+            const int v = threadIdx.x + i * blockDim.x;
+            float f[8];
+            unpack8(a[i], f);
+            s[i] = a[i];
             if (p.r) {
-                float fa[8], fb[8];
-                unpack8(a[i], fa);
-                unpack8(b[i], fb);
+                float g[8];
+                unpack8(b[i], g);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) fa[j] += fb[j];
-                a[i] = pack8(fa);  // S as it is stored
+                for (int j = 0; j < 8; ++j) f[j] += g[j];
+                s[i] = pack8(f);  // S as it is stored
+                unpack8(s[i], f);
             }
-            if (p.s && v < row.vecs) row_store(p.s, row, v, a[i]);
-            unpack8(a[i], f[i]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum = fmaf(f[i][j], f[i][j], sum);
+            for (int j = 0; j < 8; ++j) sum[0] = fmaf(f[j], f[j], sum[0]);
+            if (p.s && v < row.vecs) row_store(p.s, row, v, s[i]);
         }
-        sum = block_reduce<THREADS>(sum, part[turn], Add{});
+        // (S may be X or R: a row's stores touch no other row)
+        if (AHEAD && t + static_cast<int>(gridDim.x) < p.T) fetch(t + gridDim.x);
+        block_reduce(sum, part[turn], Add{});
         turn ^= 1;
-        const float rstd = 1.0f / sqrtf(sum / static_cast<float>(p.D) + p.eps);
-        float most = 0.0f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int v = threadIdx.x + i * THREADS;
-            if (v >= row.vecs) break;
+        const float rstd = 1.0f / sqrtf(sum[0] / static_cast<float>(p.D) + p.eps);
+        auto value = [&](int i, int v, float (&y)[8]) {
             float g[8];
-            gain_load(p.gain, row, v, g);
+            gains.get(p, row, i, v, g);
+            unpack8(s[i], y);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                f[i][j] = f[i][j] * rstd * g[j];
-                if (I8) {
-                    const int c = row.col(v) + j;
-                    if (c >= 0 && c < p.D) most = Larger{}(fabsf(f[i][j]), most);
-                }
-            }
-            if constexpr (!I8) row_store(p.y, row, v, pack8(f[i]));
-        }
-        if constexpr (I8) {
-            most = block_reduce<THREADS>(most, part[turn], Larger{});
-            turn ^= 1;
-            const bool fine = most < __int_as_float(0x7f800000);
-            if (threadIdx.x == 0)
-                p.scale[t] = fine ? most / 127.0f : __int_as_float(0x7fc00000);
-            // far below 1 everything is scaled up first, so that the reciprocal is finite
-            const float up = most < 8.6736174e-19f ? 1.1529215e18f : 1.0f;  // 2^-60, 2^60
-            const float inv = fine && most > 0.0f ? 127.0f / (most * up) : 0.0f;
+            for (int j = 0; j < 8; ++j) y[j] = y[j] * rstd * g[j];
+        };
+        if constexpr (!I8) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const int v = threadIdx.x + i * THREADS;
+                const int v = threadIdx.x + i * blockDim.x;
                 if (v >= row.vecs) break;
+                float y[8];
+                value(i, v, y);
+                row_store(p.y, row, v, pack8(y));
+            }
+        } else {
+            float most[1] = {0.0f};
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int v = threadIdx.x + i * blockDim.x;
+                if (v >= row.vecs) break;
+                float y[8];
+                value(i, v, y);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int c = row.col(v) + j;
+                    if (ALIGNED || (c >= 0 && c < p.D)) most[0] = Larger{}(fabsf(y[j]), most[0]);
+                }
+            }
+            block_reduce(most, part[turn], Larger{});
+            turn ^= 1;
+            const bool fine = most[0] < __int_as_float(0x7f800000);
+            if (threadIdx.x == 0)
+                p.scale[t] = fine ? most[0] / 127.0f : __int_as_float(0x7fc00000);
+            // far below 1 everything is scaled up first, so that the reciprocal is finite
+            const float up = most[0] < 8.6736174e-19f ? 1.1529215e18f : 1.0f;  // 2^-60, 2^60
+            const float inv = fine && most[0] > 0.0f ? 127.0f / (most[0] * up) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int v = threadIdx.x + i * blockDim.x;
+                if (v >= row.vecs) break;
+                float y[8];
+                value(i, v, y);
                 uint32_t w[2] = {0u, 0u};
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const int q = fine ? __float2int_rn(f[i][j] * up * inv) : 0;
+                    const int q = fine ? __float2int_rn(y[j] * up * inv) : 0;
                     w[j / 4] |= (static_cast<uint32_t>(q) & 0xffu) << (j % 4 * 8);
                 }
                 int8_t *at = p.q + row.first + 8ll * v;
-                if (row.whole(v)) {
+                if (ALIGNED || row.whole(v)) {
                     *reinterpret_cast<uint2 *>(at) = make_uint2(w[0], w[1]);
                 } else {
 #pragma unroll
@@ -226,26 +286,38 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_kernel(const NormParams p) {
     }
 }
 
-// The gains' gradient: each block adds its rows' dY n in shared memory, column c at
-// (c % 8) * pitch + c / 8, so that a warp's eight elements a lane fall on different
-// banks, and leaves the sums for norm_join_kernel.
-template <int THREADS, int V>
-__global__ void __launch_bounds__(THREADS) rmsnorm_backward_kernel(const NormParams p) {
+// The gains' gradient: each block leaves the sums of its rows' dY n for norm_join_kernel.
+// Rows that start on vectors give a thread the same columns every time, and the sums stay
+// in its registers; others are added in shared memory, column c at (c % 8) * pitch + c / 8,
+// so that a warp's eight elements a lane fall on different banks.
+enum class GainSum { NONE, REGISTERS, SHARED };
+
+template <int V, bool ALIGNED, GainSum SUM>
+__global__ void __launch_bounds__(V <= 2 ? 512 : 1024) rmsnorm_backward_kernel(const NormParams p) {
     extern __shared__ float sums[];
     __shared__ float part[2][2][32];
+    constexpr bool AHEAD = V <= 2;
+    static_assert(SUM != GainSum::REGISTERS || ALIGNED, "columns move from row to row");
     const int pitch = (p.D + 7) / 8;
-    if (p.dgain)
-        for (int i = threadIdx.x; i < 8 * pitch; i += THREADS) sums[i] = 0.0f;
-    __syncthreads();
+    if (SUM == GainSum::SHARED) {
+        for (int i = threadIdx.x; i < 8 * pitch; i += blockDim.x) sums[i] = 0.0f;
+        __syncthreads();
+    }
+    float own[SUM == GainSum::REGISTERS ? V : 1][8];
+#pragma unroll
+    for (int i = 0; i < (SUM == GainSum::REGISTERS ? V : 1); ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) own[i][j] = 0.0f;
     grid_dependency_wait();
     grid_launch_dependents();
+    const Gains<V, ALIGNED> gains(p);
     int turn = 0;
-    for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
+    uint4 s[V], dy[V], ds[V];
+    auto fetch = [&](int t, uint4 (&s)[V], uint4 (&dy)[V], uint4 (&ds)[V]) {
         const RowSpan row(t, p.D);
-        uint4 s[V], dy[V], ds[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int v = threadIdx.x + i * THREADS;
+            const int v = threadIdx.x + i * blockDim.x;
             s[i] = dy[i] = ds[i] = make_uint4(0u, 0u, 0u, 0u);
             if (v < row.vecs) {
                 s[i] = row_load(p.x, row, v);
@@ -253,100 +325,127 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_backward_kernel(const NormPar
                 if (p.ds) ds[i] = row_load(p.ds, row, v);
             }
         }
-        float sum = 0.0f, dot = 0.0f;
+    };
+    int t = blockIdx.x;
+    if (t < p.T) fetch(t, s, dy, ds);
+    for (; t < p.T; t += gridDim.x) {
+        const RowSpan row(t, p.D);
+        float both[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int v = threadIdx.x + i * THREADS;
+            const int v = threadIdx.x + i * blockDim.x;
             if (v >= row.vecs) break;
             float fs[8], fd[8], g[8];
             unpack8(s[i], fs);
             unpack8(dy[i], fd);
-            gain_load(p.gain, row, v, g);
+            gains.get(p, row, i, v, g);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                sum = fmaf(fs[j], fs[j], sum);
-                dot = fmaf(fd[j] * g[j], fs[j], dot);
+                both[0] = fmaf(fs[j], fs[j], both[0]);
+                both[1] = fmaf(fd[j] * g[j], fs[j], both[1]);
             }
         }
-        sum = block_reduce<THREADS>(sum, part[turn][0], Add{});
-        dot = block_reduce<THREADS>(dot, part[turn][1], Add{});
+        const int after = t + static_cast<int>(gridDim.x);
+        uint4 s1[V], dy1[V], ds1[V];
+        if (AHEAD && after < p.T) fetch(after, s1, dy1, ds1);
+        block_reduce(both, part[turn], Add{});
         turn ^= 1;
-        const float rstd = 1.0f / sqrtf(sum / static_cast<float>(p.D) + p.eps);
-        const float m = dot * rstd / static_cast<float>(p.D);  // mean(a n)
+        const float rstd = 1.0f / sqrtf(both[0] / static_cast<float>(p.D) + p.eps);
+        const float m = both[1] * rstd / static_cast<float>(p.D);  // mean(a n)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int v = threadIdx.x + i * THREADS;
+            const int v = threadIdx.x + i * blockDim.x;
             if (v >= row.vecs) break;
             float fs[8], fd[8], g[8], o[8];
             unpack8(s[i], fs);
             unpack8(dy[i], fd);
-            gain_load(p.gain, row, v, g);
+            gains.get(p, row, i, v, g);
             unpack8(ds[i], o);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float n = fs[j] * rstd;
                 o[j] += rstd * fmaf(-n, m, fd[j] * g[j]);
-                const int c = row.col(v) + j;
-                if (p.dgain && c >= 0 && c < p.D) {
-                    float *at = sums + (c & 7) * pitch + (c >> 3);
-                    *at = fmaf(fd[j], n, *at);
+                if constexpr (SUM == GainSum::REGISTERS) {
+                    own[i][j] = fmaf(fd[j], n, own[i][j]);
+                } else if constexpr (SUM == GainSum::SHARED) {
+                    const int c = row.col(v) + j;
+                    if (c >= 0 && c < p.D) {
+                        float *at = sums + (c & 7) * pitch + (c >> 3);
+                        *at = fmaf(fd[j], n, *at);
+                    }
                 }
             }
             if (p.dx) row_store(p.dx, row, v, pack8(o));
         }
-        // (with rows that start anywhere in a vector, the next row's columns are other
-        // threads': its two block_reduce barriers stand between)
-        if (THREADS == 32) __syncwarp();
+        // (columns that move to other threads with the next row: a barrier of its
+        // block_reduce stands between, or this)
+        __syncwarp();
+        if (AHEAD) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                s[i] = s1[i];
+                dy[i] = dy1[i];
+                ds[i] = ds1[i];
+            }
+        } else if (after < p.T) {
+            fetch(after, s, dy, ds);
+        }
     }
-    if (p.dgain) {
+    float *out = p.dgain + static_cast<long long>(blockIdx.x) * p.D;
+    if constexpr (SUM == GainSum::REGISTERS) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = 8 * (threadIdx.x + i * blockDim.x);
+            if (c >= p.D) break;
+            *reinterpret_cast<float4 *>(out + c) =
+                make_float4(own[i][0], own[i][1], own[i][2], own[i][3]);
+            *reinterpret_cast<float4 *>(out + c + 4) =
+                make_float4(own[i][4], own[i][5], own[i][6], own[i][7]);
+        }
+    } else if constexpr (SUM == GainSum::SHARED) {
         __syncthreads();
-        float *out = p.dgain + static_cast<long long>(blockIdx.x) * p.D;
-        for (int c = threadIdx.x; c < p.D; c += THREADS) out[c] = sums[(c & 7) * pitch + (c >> 3)];
+        for (int c = threadIdx.x; c < p.D; c += blockDim.x) out[c] = sums[(c & 7) * pitch + (c >> 3)];
     }
 }
 
-// dgain = sum of the blocks' sums, in order: eight warps take every eighth block's, 32
-// columns a block.
-__global__ void __launch_bounds__(256)
+// dgain = sum of the blocks' sums, in order: a warp takes every 32nd block's, 32 columns a
+// block.
+__global__ void __launch_bounds__(1024)
     norm_join_kernel(const float *part, int blocks, int D, uint16_t *out) {
     grid_dependency_wait();
     grid_launch_dependents();
-    __shared__ float s[8][32];
+    __shared__ float s[32][32];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
     float t = 0.0f;
     if (c < D) {
 #pragma unroll 8
-        for (int b = w; b < blocks; b += 8) t += part[static_cast<long long>(b) * D + c];
+        for (int b = w; b < blocks; b += 32) t += part[static_cast<long long>(b) * D + c];
     }
     s[w][lane] = t;
     __syncthreads();
     if (w == 0 && c < D) {
 #pragma unroll
-        for (int i = 1; i < 8; ++i) t += s[i][lane];
+        for (int i = 1; i < 32; ++i) t += s[i][lane];
         out[c] = static_cast<uint16_t>(pack_bf16(t, 0.0f) & 0xffffu);
     }
 }
 
-// f(threads, vectors a thread) as integral constants for rows of D: two vectors a thread
-// where rows are many, one where the row's own latency counts.
+// f(vectors a thread, whether rows start on vectors) as constants, and threads.  Two vectors
+// a thread or one (`one`: up to 512): forward, two are quicker with rows for every SM (8192 x
+// 4096 42.0 us against 49.2) and one where a row's own latency counts; backward, whose
+// thread holds three operands and the next row's, one is (52.5 us against 59.4).
 template <class F>
-static pgemm_status with_row(int D, bool few, F &&f) {
+static pgemm_status with_row(int D, bool one, F &&f) {
     const int vecs = D % 8 == 0 ? D / 8 : (D + 14) / 8;
     using std::integral_constant;
-    auto pick = [&](auto threads) {
-        constexpr int N = decltype(threads)::value;
-        return vecs <= N ? f(threads, integral_constant<int, 1>{})
-                         : f(threads, integral_constant<int, 2>{});
+    auto pick = [&](auto v) {
+        const int threads = op_blocks(op_blocks(vecs, decltype(v)::value), 32) * 32;
+        return D % 8 == 0 ? f(v, std::true_type{}, threads) : f(v, std::false_type{}, threads);
     };
-    const int per = few ? 1 : 2;
-    if (vecs <= 32 * per) return pick(integral_constant<int, 32>{});
-    if (vecs <= 64 * per) return pick(integral_constant<int, 64>{});
-    if (vecs <= 128 * per) return pick(integral_constant<int, 128>{});
-    if (vecs <= 256 * per) return pick(integral_constant<int, 256>{});
-    if (vecs <= 512 * per) return pick(integral_constant<int, 512>{});
-    if (vecs <= 2048) return pick(integral_constant<int, 1024>{});
-    return f(integral_constant<int, 1024>{}, integral_constant<int, 5>{});
+    if (vecs <= (one ? 512 : 32)) return pick(integral_constant<int, 1>{});
+    if (vecs <= 1024) return pick(integral_constant<int, 2>{});
+    return pick(integral_constant<int, 5>{});
 }
 
 static pgemm_status norm_check(int T, int D) {
@@ -378,12 +477,13 @@ static pgemm_status norm_forward(bool i8, int T, int D, const uint16_t *X, const
     p.y = i8 ? nullptr : static_cast<uint16_t *>(out);
     p.q = i8 ? static_cast<int8_t *>(out) : nullptr;
     p.scale = scale;
-    return with_row(D, T < 2 * dev.sm_count, [&](auto threads, auto v) {
-        constexpr int N = decltype(threads)::value, V = decltype(v)::value;
-        const long long most = dev.sm_count * (N >= 2048 / 32 ? 2048ll / N : 32ll);
+    return with_row(D, T < 4 * dev.sm_count, [&](auto v, auto aligned, int threads) {
+        constexpr int V = decltype(v)::value;
+        constexpr bool A = decltype(aligned)::value;
+        const long long most = dev.sm_count * (threads >= 64 ? 2048ll / threads : 32ll);
         const dim3 grid(static_cast<unsigned>(T < most ? T : most));
-        return i8 ? launch_small(rmsnorm_kernel<N, V, true>, grid, dim3(N), s, p)
-                  : launch_small(rmsnorm_kernel<N, V, false>, grid, dim3(N), s, p);
+        return i8 ? launch_small(rmsnorm_kernel<V, A, true>, grid, dim3(threads), s, p)
+                  : launch_small(rmsnorm_kernel<V, A, false>, grid, dim3(threads), s, p);
     });
 }
 
@@ -413,32 +513,40 @@ static pgemm_status norm_backward(int T, int D, const uint16_t *S, const uint16_
     p.dy = dY;
     p.ds = dS;
     p.dx = dX;
-    return with_row(D, true, [&](auto threads, auto v) -> pgemm_status {
-        constexpr int N = decltype(threads)::value, V = decltype(v)::value;
-        // blocks of an SM: what threads and shared memory allow, eight at most, since
+    return with_row(D, true, [&](auto v, auto aligned, int threads) -> pgemm_status {
+        constexpr int V = decltype(v)::value;
+        constexpr bool A = decltype(aligned)::value;
+        constexpr GainSum SUM = A && V <= 2 ? GainSum::REGISTERS : GainSum::SHARED;
+        // blocks of an SM: what registers and shared memory allow, eight at most, since
         // each leaves a row of sums behind
-        const int smem = dgain ? (D + 7) / 8 * 32 : 0;
-        int per_sm = 2048 / N < 8 ? 2048 / N : 8;
+        const int smem = dgain && SUM == GainSum::SHARED ? (D + 7) / 8 * 32 : 0;
+        int per_sm = threads <= 128 ? 8 : 1024 / threads;
         while (per_sm > 1 && per_sm * (smem + 2048) > kSmemPerSm) --per_sm;
         const int most = dev.sm_count * per_sm;
         const int blocks = T < most ? T : most;
-        static const KernelInfo info = [] {
-            KernelInfo k;
-            k.threads = N;
-            k.smem_bytes = kNormMaxD * 4;
-            k.func = reinterpret_cast<const void *>(rmsnorm_backward_kernel<N, V>);
-            return k;
-        }();
-        pgemm_status e = op_kernel_setup(dev, info, nullptr);
-        if (e != PGEMM_OK) return e;
         OpArena arena(dev, s);
         const long long at = arena.add(dgain ? 4ll * blocks * D : 0);
-        if ((e = arena.alloc()) != PGEMM_OK) return e;
+        pgemm_status e = arena.alloc();
+        if (e != PGEMM_OK) return e;
+        if (!dgain)
+            return launch_small(rmsnorm_backward_kernel<V, A, GainSum::NONE>, dim3(blocks),
+                                dim3(threads), s, p);
         NormParams q = p;
-        q.dgain = dgain ? arena.at<float>(at) : nullptr;
-        e = launch_small_smem(rmsnorm_backward_kernel<N, V>, dim3(blocks), dim3(N), smem, s, q);
-        if (e != PGEMM_OK || !dgain) return e;
-        return launch_small(norm_join_kernel, dim3(op_blocks(D, 32)), dim3(256), s,
+        q.dgain = arena.at<float>(at);
+        if (SUM == GainSum::SHARED) {
+            static const KernelInfo info = [] {
+                KernelInfo k;
+                k.threads = 32;
+                k.smem_bytes = kNormMaxD * 4;
+                k.func = reinterpret_cast<const void *>(rmsnorm_backward_kernel<V, A, SUM>);
+                return k;
+            }();
+            if ((e = op_kernel_setup(dev, info, nullptr)) != PGEMM_OK) return e;
+        }
+        e = launch_small_smem(rmsnorm_backward_kernel<V, A, SUM>, dim3(blocks), dim3(threads),
+                              smem, s, q);
+        if (e != PGEMM_OK) return e;
+        return launch_small(norm_join_kernel, dim3(op_blocks(D, 32)), dim3(1024), s,
                             static_cast<const float *>(q.dgain), blocks, D, dgain);
     });
 }

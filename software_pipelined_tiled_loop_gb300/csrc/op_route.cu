@@ -49,73 +49,96 @@ struct RouteParams {
     float *dlogits;
 };
 
-__device__ __forceinline__ float warp_sum(float x) {
+__device__ __forceinline__ float lanes_sum(float x) {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
     return x;
 }
-__device__ __forceinline__ uint32_t warp_max(uint32_t x) {
-    return __reduce_max_sync(0xffffffffu, x);
-}
 
-// A warp a token; lane l holds experts l, l + 32, ...
-template <int NV>
-__device__ __forceinline__ void row_read(const float *p, int E, int lane, float (&z)[NV]) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int e = lane + 32 * i;
-        z[i] = e < E ? p[e] : -__int_as_float(0x7f800000);
-    }
-}
-
+// A warp a token; lane l holds experts l, l + 32, ...  Up to four of them a lane keeps in
+// order, so that a choice compares the lanes' best alone; of more it finds its best again
+// every time.  Bound by instructions for many tokens, which the order saves a third of
+// (16384 tokens, eight of 128 experts, softmax over all: 11.3 us without it).
 template <int NV>
 __global__ void __launch_bounds__(128) route_kernel(const RouteParams p) {
+    constexpr bool ORDERED = NV <= 4;
     grid_dependency_wait();
     grid_launch_dependents();
     const int lane = threadIdx.x & 31;
     for (long long t = blockIdx.x * 4ll + (threadIdx.x >> 5); t < p.T; t += gridDim.x * 4ll) {
+        const float *row = p.logits + t * p.E;
         float z[NV];
-        row_read<NV>(p.logits + t * p.E, p.E, lane, z);
         uint32_t key[NV];
 #pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int e = lane + 32 * i;
+            z[i] = e < p.E ? row[e] : -__int_as_float(0x7f800000);
+        }
+#pragma unroll
         for (int i = 0; i < NV; ++i) key[i] = order_key(z[i]);
-        // choice lane's expert and logit, k <= 32 of them
+        // which of the lane's experts key[0], key[1], ... are, two bits each
+        uint32_t which = 0xe4u;
+        if constexpr (ORDERED) {
+#pragma unroll
+            for (int pass = 0; pass < NV - 1; ++pass)
+#pragma unroll
+                for (int i = 0; i + 1 < NV - pass; ++i)
+                    if (key[i + 1] > key[i]) {  // (equal ones stay: the lower index first)
+                        const uint32_t k = key[i];
+                        key[i] = key[i + 1];
+                        key[i + 1] = k;
+                        const uint32_t two = which >> (2 * i) & 15u;
+                        which ^= (two ^ (two >> 2 | two << 2 & 12u)) << (2 * i);
+                    }
+        }
+        // choice `lane`: its expert and the key of its logit
         int mine = -1;
-        float logit = 0.0f;
+        uint32_t mine_key = 0u, top_key = 0u;
         for (int j = 0; j < p.k; ++j) {
             uint32_t best = key[0];
+            int at = lane + 32 * static_cast<int>(which & 3u);
+            if constexpr (!ORDERED) {
+                at = lane;
 #pragma unroll
-            for (int i = 1; i < NV; ++i) best = max(best, key[i]);
-            best = warp_max(best);
-            if (best <= kClosedKey) break;
-            int at = INT_MAX;
-#pragma unroll
-            for (int i = NV - 1; i >= 0; --i)
-                if (key[i] == best) at = lane + 32 * i;
-            at = static_cast<int>(__reduce_min_sync(0xffffffffu, static_cast<unsigned>(at)));
-            float v = 0.0f;
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (at == lane + 32 * i) {
-                    v = z[i];
-                    key[i] = 0u;
-                }
-            v = __shfl_sync(0xffffffffu, v, at & 31);
+                for (int i = 1; i < NV; ++i)
+                    if (key[i] > best) {
+                        best = key[i];
+                        at = lane + 32 * i;
+                    }
+            }
+            const uint32_t most = __reduce_max_sync(0xffffffffu, best);
+            if (most <= kClosedKey) break;
+            at = static_cast<int>(__reduce_min_sync(
+                0xffffffffu, best == most ? static_cast<unsigned>(at) : 0xffffffffu));
+            if (j == 0) top_key = most;
             if (lane == j) {
                 mine = at;
-                logit = v;
+                mine_key = most;
+            }
+            if constexpr (ORDERED) {
+                if (lane == (at & 31)) {
+#pragma unroll
+                    for (int i = 0; i + 1 < NV; ++i) key[i] = key[i + 1];
+                    key[NV - 1] = 0u;
+                    which >>= 2;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (at == lane + 32 * i) key[i] = 0u;
             }
         }
-        const float top = __shfl_sync(0xffffffffu, logit, 0);
-        float e = mine >= 0 ? expf(logit - top) : 0.0f, total = e;
+        const bool any = top_key != 0u;
+        const float top = any ? key_logit(top_key) : 0.0f;
+        const float e = mine >= 0 ? expf(key_logit(mine_key) - top) : 0.0f;
+        float total = e;
         if (!p.normalise) {
-            const bool any = __shfl_sync(0xffffffffu, mine, 0) >= 0;
             total = 0.0f;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (any && lane + 32 * i < p.E) total += expf(z[i] - top);
         }
-        total = warp_sum(total);
+        total = lanes_sum(total);
         if (lane < p.k) {
             p.experts[t * p.k + lane] = mine;
             p.weights[t * p.k + lane] = mine >= 0 ? e / total : 0.0f;
@@ -125,64 +148,63 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteParams p) {
 
 // dlogits from dweights: with w the weights and dot = sum over the chosen of w dw,
 // w (dw - dot) at the chosen (softmax over the chosen), or p ([chosen] dw - dot)
-// everywhere (softmax over all).  A choice outside [0, E) does not count.
+// everywhere (softmax over all).  A choice outside [0, E) does not count.  A warp a token:
+// lane l takes experts l, l + 32, ... and choice l.
 template <int NV>
 __global__ void __launch_bounds__(128) route_backward_kernel(const RouteParams p) {
     grid_dependency_wait();
     grid_launch_dependents();
     const int lane = threadIdx.x & 31;
     for (long long t = blockIdx.x * 4ll + (threadIdx.x >> 5); t < p.T; t += gridDim.x * 4ll) {
+        const float *row = p.logits + t * p.E;
         float z[NV];
-        row_read<NV>(p.logits + t * p.E, p.E, lane, z);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int e = lane + 32 * i;
+            z[i] = !p.normalise && e < p.E ? row[e] : -__int_as_float(0x7f800000);
+        }
         int mine = -1;
-        float dw = 0.0f;
+        float dw = 0.0f, logit = 0.0f;
         if (lane < p.k) {
             mine = p.experts_in[t * p.k + lane];
-            dw = p.dweights[t * p.k + lane];
-            if (mine < 0 || mine >= p.E) {
+            if (mine >= 0 && mine < p.E) {
+                dw = p.dweights[t * p.k + lane];
+                logit = row[mine];
+            } else {
                 mine = -1;
-                dw = 0.0f;
             }
         }
-        const float logit = mine >= 0 ? p.logits[t * p.E + mine] : 0.0f;
         // the largest of what the softmax is over; none where everything is closed
         uint32_t best = p.normalise && mine >= 0 ? order_key(logit) : 0u;
         if (!p.normalise) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) best = max(best, order_key(z[i]));
         }
-        best = warp_max(best);
+        best = __reduce_max_sync(0xffffffffu, best);
         const bool any = best > kClosedKey;
         const float top = any ? key_logit(best) : 0.0f;
         const float e = any && mine >= 0 ? expf(logit - top) : 0.0f;
         float total = e;
-        float ez[NV];
         if (!p.normalise) {
             total = 0.0f;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                ez[i] = any && lane + 32 * i < p.E ? expf(z[i] - top) : 0.0f;
-                total += ez[i];
+                z[i] = any && lane + 32 * i < p.E ? expf(z[i] - top) : 0.0f;
+                total += z[i];
             }
         }
-        total = warp_sum(total);
+        total = lanes_sum(total);
         const float w = any && mine >= 0 ? e / total : 0.0f;
-        const float dot = warp_sum(w * dw);
-        float d[NV];
+        const float dot = lanes_sum(w * dw);
+        float *out = p.dlogits + t * p.E;
+        const float scale = p.normalise || !any ? 0.0f : -dot / total;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            d[i] = p.normalise || !any ? 0.0f : -(ez[i] / total) * dot;
-        const float own = p.normalise ? w * (dw - dot) : w * dw;
-        for (int j = 0; j < p.k; ++j) {
-            const int at = __shfl_sync(0xffffffffu, mine, j);
-            const float v = __shfl_sync(0xffffffffu, own, j);
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (at == lane + 32 * i) d[i] += v;
-        }
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (lane + 32 * i < p.E) p.dlogits[t * p.E + lane + 32 * i] = d[i];
+            if (lane + 32 * i < p.E)
+                out[lane + 32 * i] = p.normalise || !any ? 0.0f : z[i] * scale;
+        __syncwarp();  // the chosen ones' values replace those
+        if (mine >= 0) out[mine] = w * (dw - dot);
+        __syncwarp();
     }
 }
 
@@ -256,18 +278,19 @@ static pgemm_status route_backward(int T, int E, int k, const float *logits, int
 }
 
 // ------------------------------------------------------------------- sort ---
-// A block takes kSortChunk slots, a warp a run of them in order, 32 at a time: slots of
-// one expert among the 32 find one another by match, and the warp's counters of each
-// expert give the rest of a slot's rank.  Two passes over the slots (count, then place),
-// with the counters turned into first rows in between: over the block's warps, over the
-// blocks before this one, over the experts before this one.  Up to kSortChunk slots one
-// block does all of it; more take a launch that counts and one that places, each of whose
-// blocks sums the others' counts itself, or with many blocks a launch between them.
-constexpr int kSortChunk = 4096, kSortWarps = 32, kSortOwnSums = 64;
+// A block takes `chunk` slots, a warp a run of them in order, 32 at a time: slots of one
+// expert among the 32 find one another by match, and the warp's counters of each expert
+// give the rest of a slot's rank.  Two passes over the slots (count, then place), with the
+// counters turned into first rows in between: over the block's warps, over the blocks
+// before this one, over the experts before this one.  Up to kSortOne slots one block does
+// all of it (a launch more would cost longer); more take blocks of 1024, a launch that
+// counts and one that places, each of whose blocks sums the others' counts itself, or with
+// many blocks a launch between them.
+constexpr int kSortWarps = 32, kSortOne = 4096, kSortChunk = 1024, kSortOwnSums = 64;
 
 struct SortParams {
     long long slots;
-    int E, blocks;
+    int E, blocks, chunk;
     const int32_t *experts;
     int32_t *offsets, *slot_row;
     int32_t *counts;  // [E][blocks]
@@ -277,11 +300,11 @@ struct SortParams {
 // the counters of warp w: count[w * E + e]
 __device__ __forceinline__ void sort_count(const SortParams &p, int32_t *count, int warp,
                                            int lane) {
-    constexpr int RUN = kSortChunk / kSortWarps;
-    const long long first = blockIdx.x * static_cast<long long>(kSortChunk) + warp * RUN;
+    const int run = p.chunk / kSortWarps;
+    const long long first = blockIdx.x * static_cast<long long>(p.chunk) + warp * run;
     int32_t *mine = count + warp * p.E;
 #pragma unroll 1
-    for (int i = 0; i < RUN; i += 32) {
+    for (int i = 0; i < run && first + i < p.slots; i += 32) {
         const long long slot = first + i + lane;
         const int e = slot < p.slots ? p.experts[slot] : -1;
         const bool in = e >= 0 && e < p.E;
@@ -359,11 +382,11 @@ __global__ void __launch_bounds__(kSortWarps * 32) sort_kernel(const SortParams 
         for (int w = 0; w < kSortWarps; ++w) count[w * p.E + e] += first_row + before;
     }
     __syncthreads();
-    constexpr int RUN = kSortChunk / kSortWarps;
-    const long long first = blockIdx.x * static_cast<long long>(kSortChunk) + warp * RUN;
+    const int run = p.chunk / kSortWarps;
+    const long long first = blockIdx.x * static_cast<long long>(p.chunk) + warp * run;
     int32_t *mine = count + warp * p.E;
 #pragma unroll 1
-    for (int i = 0; i < RUN; i += 32) {
+    for (int i = 0; i < run && first + i < p.slots; i += 32) {
         const long long slot = first + i + lane;
         const int x = slot < p.slots ? p.experts[slot] : -1;
         const bool in = x >= 0 && x < p.E;
@@ -429,7 +452,8 @@ static pgemm_status expert_sort_run(int T, int E, int k, const int32_t *experts,
     SortParams p{};
     p.slots = slots;
     p.E = E;
-    p.blocks = op_blocks(slots, kSortChunk);
+    p.chunk = slots <= kSortOne ? kSortOne : kSortChunk;
+    p.blocks = op_blocks(slots, p.chunk);
     p.experts = experts;
     p.offsets = offsets;
     p.slot_row = slot_row;
@@ -556,6 +580,20 @@ __global__ void __launch_bounds__(kRowsThreads) combine_kernel(const RowsParams 
          t += static_cast<long long>(gridDim.x) * groups) {
         const int32_t *from = p.slot_row + t * p.k;
         const float *w = p.weights ? p.weights + t * p.k : nullptr;
+        // the first choices' rows and weights, for all of the token's vectors
+        const V *row[kAhead];
+        float weight[kAhead];
+        auto choices = [&](int j0) {
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const int r = j0 + j < p.k ? from[j0 + j] : -1;
+                const bool in = r >= 0 && r < p.rows;
+                row[j] = in ? reinterpret_cast<const V *>(p.ys + static_cast<long long>(r) * p.D)
+                            : nullptr;
+                weight[j] = in && w ? w[j0 + j] : 1.0f;
+            }
+        };
+        if (p.k <= kAhead) choices(0);
         for (int v = lane; v < vecs; v += per) {
             float sum[W];
             V res = vec_zero<W>();
@@ -563,24 +601,18 @@ __global__ void __launch_bounds__(kRowsThreads) combine_kernel(const RowsParams 
 #pragma unroll
             for (int i = 0; i < W; ++i) sum[i] = 0.0f;
             for (int j0 = 0; j0 < p.k; j0 += kAhead) {
+                if (p.k > kAhead) choices(j0);
                 V y[kAhead];
-                bool in[kAhead];
-#pragma unroll
-                for (int j = 0; j < kAhead; ++j) {
-                    const int r = j0 + j < p.k ? from[j0 + j] : -1;
-                    in[j] = r >= 0 && r < p.rows;
-                    if (in[j])
-                        y[j] = reinterpret_cast<const V *>(p.ys + static_cast<long long>(r) *
-                                                                      p.D)[v];
-                }
 #pragma unroll
                 for (int j = 0; j < kAhead; ++j)
-                    if (in[j]) {
-                        const float wj = w ? w[j0 + j] : 1.0f;
+                    if (row[j] != nullptr) y[j] = row[j][v];
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j)
+                    if (row[j] != nullptr) {
                         float f[W];
                         vec_get<W>(y[j], f);
 #pragma unroll
-                        for (int i = 0; i < W; ++i) sum[i] = fmaf(wj, f[i], sum[i]);
+                        for (int i = 0; i < W; ++i) sum[i] = fmaf(weight[j], f[i], sum[i]);
                     }
             }
             float f[W];
@@ -651,7 +683,7 @@ __global__ void __launch_bounds__(kRowsThreads) combine_backward_kernel(const Ro
             }
             if (!p.dweights) continue;
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) dot[j] = warp_sum(dot[j]);
+            for (int j = 0; j < kAhead; ++j) dot[j] = lanes_sum(dot[j]);
             if constexpr (WARPS > 1) {
                 if ((lane & 31) == 0) {
 #pragma unroll
