@@ -177,7 +177,7 @@ struct RowsUnit {
 
 template <class Cfg>
 __device__ __forceinline__ int row_tiles(int rows) {
-    return (rows + Cfg::TOK - 1) / Cfg::TOK;
+    return rows > 0 ? (rows - 1) / Cfg::TOK + 1 : 0;  // (rows up to 2^31 - 1)
 }
 
 // Units of an expert: down its tiles of rows, up to sixteen of them, then one tile of
@@ -193,7 +193,7 @@ __device__ __forceinline__ RowsUnit rows_unit(const ExpertsTable &t, const Exper
     const int g = min(tiles - first, 16), q = r - group * 16 * a.f_tiles;
     const int rt = first + q % g;
     w.f0 = q / g * (Cfg::FEATS * Cfg::CG);
-    const int each = ((n + tiles - 1) / tiles + Cfg::STEP - 1) / Cfg::STEP * Cfg::STEP;
+    const int each = ((n - 1) / tiles + Cfg::STEP) / Cfg::STEP * Cfg::STEP;
     w.row0 = begin + rt * each;
     w.rows = min(each, n - rt * each);
     w.cols = (w.rows + Cfg::STEP - 1) / Cfg::STEP * Cfg::STEP;
@@ -272,13 +272,15 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 const int half = w.cols / CG;  // columns of B in this CTA
                 const int boxes = (half + Cfg::BOX - 1) / Cfg::BOX;  // 1 .. 4
                 const int box = boxes == 4 ? 0 : boxes >= 2 ? 1 : 2;
-                const int y0 = w.row0 + crank * half;
+                // (may pass 2^31 where the rows have ended: zero fill either way)
+                const int y0 = static_cast<int>(static_cast<uint32_t>(w.row0) + crank * half);
                 const uint32_t tx = CG * (Cfg::A_BYTES + boxes * Cfg::BOX * BK * 2);
                 const int f0 = w.f0 + crank * Cfg::FEATS;
                 const int segments = a.k_tiles > a.k_seg ? 2 : 1;
                 for (int sg = 0; ok && sg < segments; ++sg) {
                     const CUtensorMap *mx = &maps.x[sg][box], *mw = &maps.w[sg];
-                    for (int k0 = 0; k0 < a.K; k0 += BK, ring.next()) {
+                    for (int left = a.K; left > 0; left -= BK, ring.next()) {
+                        const int k0 = a.K - left;
                         const uint32_t s = ring.s;
                         if (!mbar_wait(&empty[s], ring.phase ^ 1u, ctx, kSiteProducerEmpty)) {
                             ok = false;
@@ -706,7 +708,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                                     nb + 64 * j, whole);
                     }
                 }
-                for (int y = w.begin; y < whole; y += BK, ring.next()) {
+                for (int left = whole - w.begin; left > 0; left -= BK, ring.next()) {
+                    const int y = whole - left;
                     const uint32_t s = ring.s;
                     if (!mbar_wait(&empty[s], ring.phase ^ 1u, ctx, kSiteProducerEmpty)) {
                         ok = false;
@@ -715,7 +718,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                     uint8_t *da = sA + s * Cfg::A_BYTES, *db = sB + s * Cfg::B_BYTES;
                     const uint32_t lead = mapa_shared(smem_u32(&full[s]), 0);
                     // a box of 96 rows, in a last step perhaps of 64 or 32
-                    const int thirds = min(3, (whole - y + 31) / 32);
+                    const int thirds = left > 64 ? 3 : (left + 31) / 32;
                     if (crank == 0)
                         mbar_arrive_expect_tx(&full[s], thirds * (2 * Cfg::STAGE_BYTES / 3));
 #pragma unroll
@@ -781,7 +784,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 const uint32_t d = tmem + ab * BN;
                 const int whole = w.whole();
                 uint32_t acc = 0;
-                for (int y = w.begin; y < whole; y += BK, ring.next()) {
+                for (int left = whole - w.begin; left > 0; left -= BK, ring.next()) {
                     const uint32_t s = ring.s;
                     if (!mbar_wait(&full[s], ring.phase, ctx, kSiteMmaFull)) {
                         ok = false;
@@ -793,12 +796,12 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                         umma_f16_ss_pair(d, as + k * 128, bs + k * 128, idesc, acc);
                         acc = 1;
                     };
-                    if (whole - y >= BK) {
+                    if (left >= BK) {
 #pragma unroll
                         for (int k = 0; k < BK / 16; ++k) multiply(k);
                     } else {
 #pragma unroll 1
-                        for (int k = 0; 16 * k < whole - y; ++k) multiply(k);
+                        for (int k = 0; 16 * k < left; ++k) multiply(k);
                     }
                     umma_commit_pair_multicast(&empty[s], kPair);
                 }

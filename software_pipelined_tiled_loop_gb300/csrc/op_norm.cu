@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(V <= 2 ? 512 : 1024) rmsnorm_kernel(const Norm
     const Gains<V, ALIGNED> gains(p);
     int turn = 0;
     uint4 a[V], b[V];
-    auto fetch = [&](int t) {
+    auto fetch = [&](unsigned t) {
         const RowSpan row(t, p.D);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -190,9 +190,10 @@ __global__ void __launch_bounds__(V <= 2 ? 512 : 1024) rmsnorm_kernel(const Norm
             }
         }
     };
-    int t = blockIdx.x;
-    if (AHEAD && t < p.T) fetch(t);
-    for (; t < p.T; t += gridDim.x) {
+    const unsigned T = p.T;  // (unsigned: a step behind the last row may pass 2^31)
+    unsigned t = blockIdx.x;
+    if (AHEAD && t < T) fetch(t);
+    for (; t < T; t += gridDim.x) {
         if (!AHEAD) fetch(t);
         const RowSpan row(t, p.D);
         uint4 s[V];
@@ -216,7 +217,7 @@ __global__ void __launch_bounds__(V <= 2 ? 512 : 1024) rmsnorm_kernel(const Norm
             if (p.s && v < row.vecs) row_store(p.s, row, v, s[i]);
         }
         // (S may be X or R: a row's stores touch no other row)
-        if (AHEAD && t + static_cast<int>(gridDim.x) < p.T) fetch(t + gridDim.x);
+        if (AHEAD && t + gridDim.x < T) fetch(t + gridDim.x);
         block_reduce(sum, part[turn], Add{});
         turn ^= 1;
         const float rstd = 1.0f / sqrtf(sum[0] / static_cast<float>(p.D) + p.eps);
@@ -313,7 +314,7 @@ __global__ void __launch_bounds__(V <= 2 ? 512 : 1024) rmsnorm_backward_kernel(c
     const Gains<V, ALIGNED> gains(p);
     int turn = 0;
     uint4 s[V], dy[V], ds[V];
-    auto fetch = [&](int t, uint4 (&s)[V], uint4 (&dy)[V], uint4 (&ds)[V]) {
+    auto fetch = [&](unsigned t, uint4 (&s)[V], uint4 (&dy)[V], uint4 (&ds)[V]) {
         const RowSpan row(t, p.D);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -326,9 +327,10 @@ __global__ void __launch_bounds__(V <= 2 ? 512 : 1024) rmsnorm_backward_kernel(c
             }
         }
     };
-    int t = blockIdx.x;
-    if (t < p.T) fetch(t, s, dy, ds);
-    for (; t < p.T; t += gridDim.x) {
+    const unsigned T = p.T;
+    unsigned t = blockIdx.x;
+    if (t < T) fetch(t, s, dy, ds);
+    for (; t < T; t += gridDim.x) {
         const RowSpan row(t, p.D);
         float both[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -345,9 +347,9 @@ __global__ void __launch_bounds__(V <= 2 ? 512 : 1024) rmsnorm_backward_kernel(c
                 both[1] = fmaf(fd[j] * g[j], fs[j], both[1]);
             }
         }
-        const int after = t + static_cast<int>(gridDim.x);
+        const unsigned after = t + gridDim.x;
         uint4 s1[V], dy1[V], ds1[V];
-        if (AHEAD && after < p.T) fetch(after, s1, dy1, ds1);
+        if (AHEAD && after < T) fetch(after, s1, dy1, ds1);
         block_reduce(both, part[turn], Add{});
         turn ^= 1;
         const float rstd = 1.0f / sqrtf(both[0] / static_cast<float>(p.D) + p.eps);
@@ -387,7 +389,7 @@ __global__ void __launch_bounds__(V <= 2 ? 512 : 1024) rmsnorm_backward_kernel(c
                 dy[i] = dy1[i];
                 ds[i] = ds1[i];
             }
-        } else if (after < p.T) {
+        } else if (after < T) {
             fetch(after, s, dy, ds);
         }
     }

@@ -553,12 +553,12 @@ __global__ void __launch_bounds__(kRowsThreads) gather_kernel(const RowsParams p
     grid_dependency_wait();
     grid_launch_dependents();
     const int group = threadIdx.x / per, lane = threadIdx.x % per, groups = kRowsThreads / per;
-    const int vecs = p.D / W;
+    const unsigned vecs = p.D / W;  // (unsigned: a step may pass 2^31)
     for (long long t = blockIdx.x * static_cast<long long>(groups) + group; t < p.T;
          t += static_cast<long long>(gridDim.x) * groups) {
         const V *src = reinterpret_cast<const V *>(p.x + t * p.D);
         const int32_t *to = p.slot_row + t * p.k;
-        for (int v = lane; v < vecs; v += per) {
+        for (unsigned v = lane; v < vecs; v += per) {
             const V x = src[v];
             for (int j = 0; j < p.k; ++j) {
                 const int r = to[j];
@@ -575,7 +575,7 @@ __global__ void __launch_bounds__(kRowsThreads) combine_kernel(const RowsParams 
     grid_dependency_wait();
     grid_launch_dependents();
     const int group = threadIdx.x / per, lane = threadIdx.x % per, groups = kRowsThreads / per;
-    const int vecs = p.D / W;
+    const unsigned vecs = p.D / W;  // (unsigned: a step may pass 2^31)
     for (long long t = blockIdx.x * static_cast<long long>(groups) + group; t < p.T;
          t += static_cast<long long>(gridDim.x) * groups) {
         const int32_t *from = p.slot_row + t * p.k;
@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(kRowsThreads) combine_kernel(const RowsParams 
             }
         };
         if (p.k <= kAhead) choices(0);
-        for (int v = lane; v < vecs; v += per) {
+        for (unsigned v = lane; v < vecs; v += per) {
             float sum[W];
             V res = vec_zero<W>();
             if (p.x) res = reinterpret_cast<const V *>(p.x + t * p.D)[v];
@@ -634,7 +634,7 @@ __global__ void __launch_bounds__(kRowsThreads) combine_backward_kernel(const Ro
     grid_dependency_wait();
     grid_launch_dependents();
     const int group = threadIdx.x / PER, lane = threadIdx.x % PER;
-    const int vecs = p.D / W;
+    const unsigned vecs = p.D / W;  // (unsigned: a step may pass 2^31)
     // (every group of a block makes as many rounds: they share the barriers)
     for (long long t0 = blockIdx.x * static_cast<long long>(GROUPS); t0 < p.T;
          t0 += static_cast<long long>(gridDim.x) * GROUPS) {
@@ -654,7 +654,7 @@ __global__ void __launch_bounds__(kRowsThreads) combine_backward_kernel(const Ro
                 }
                 row[j] = r >= 0 && r < p.rows ? static_cast<long long>(r) * p.D : -1;
             }
-            for (int v = lane; have && v < vecs; v += PER) {
+            for (unsigned v = lane; have && v < vecs; v += PER) {
                 float d[W];
                 const V x = reinterpret_cast<const V *>(p.x + t * p.D)[v];
                 V y[kAhead];
