@@ -67,6 +67,7 @@ struct ExpertsArgs {
     int tma_out;          // weights' gradient: the outputs have tensor maps
     int n_seg;            // weights' gradient: tiles along N of one output
     int segments;         // and outputs
+    int overlap;          // weights' gradient: see op_begin
 };
 
 // CG CTAs work on a tile of CG * 128 accumulator lanes x up to TOK rows, BK columns of the
@@ -86,7 +87,8 @@ struct ExpCfg {
     static constexpr int A_BYTES = BM * BK * 2, B_BYTES = TOK / CG * BK * 2;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int EPI = 8;
-    static constexpr int SWAP_BYTES = DUAL ? EPI * 2048 : 0;
+    static constexpr int CHUNK = CG == 2 ? 32 : 16;       // columns an epilogue warp takes at once
+    static constexpr int SWAP_BYTES = DUAL ? EPI * CHUNK / 2 * 128 : 0;
     static constexpr int SWAP_OFFSET = STAGES * STAGE_BYTES;
     static constexpr int BAR_OFFSET = SWAP_OFFSET + SWAP_BYTES;
     static constexpr int TABLE_OFFSET = BAR_OFFSET + (2 * STAGES + 5) * 8 + 24;
@@ -388,8 +390,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                         umma_commit_pair_multicast(&empty[s], kPair);
                     else
                         umma_commit(&empty[s]);
+                    // (found while these products run)
+                    if (kt == 0 && u + slots < units)
+                        next = rows_unit<Cfg>(table, a, u + slots).cols;
                 }
-                if (u + slots < units) next = rows_unit<Cfg>(table, a, u + slots).cols;
                 if (ok) {
                     if constexpr (CG == 2)
                         umma_commit_pair_multicast(&acc_full[ab], kPair);
@@ -405,46 +409,90 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         }
     } else {
         // ---------------- epilogue ----------------
+        // A quadrant's two warps take W accumulator columns (rows of the output) in turn;
+        // the next ones are on their way from tensor memory while these are worked on.
+        constexpr int W = Cfg::CHUNK, KEEP = W / 2;
         const int e = static_cast<int>(warp) - 2, h = e >> 2;
         const uint32_t q = warp & 3u;  // the TMEM lane quadrant this warp may read
         // gated: quadrants 0 and 1 hold Wg's 64 features, 2 and 3 Wu's
         const bool gate = q < 2;
         const int lane_feat = Cfg::DUAL ? static_cast<int>((q & 1u) * 32 + lane)
                                         : static_cast<int>(q * 32 + lane);
-        float *swap = reinterpret_cast<float *>(smem + Cfg::SWAP_OFFSET) + lane;
-        uint32_t n = 0, turn = 0;
+        const bool have = a.k_tiles > 0;
+        uint32_t n = 0;
         bool ok = true;  // a wait that ran out: the rest goes by unread, barriers and all
         for (int u = slot; u < units; u += slots, ++n) {
             const RowsUnit w = rows_unit<Cfg>(table, a, u);
             const int feat = w.f0 + crank * Cfg::FEATS + lane_feat;
             const bool mine = feat < a.M;
             const uint32_t ab = n & 1u;
-            const bool have = a.k_tiles > 0;
             const uint32_t t_row = tmem + ((q * 32u) << 16) + ab * TOK;
-            const int chunks = (w.rows + 15) / 16;
+            const int chunks = (w.rows + W - 1) / W;
+            uint32_t v[W];
+            // gated gradient: dH of the columns that this warp finishes (the gate's warp a
+            // chunk's first half, the other one the rest)
+            const int c0 = gate ? 0 : KEEP;
+            uint16_t dh[Cfg::MODE == Exp::GATED_GRAD ? KEEP : 1];
+            auto fetch_dh = [&](int c) {
+                if constexpr (Cfg::MODE == Exp::GATED_GRAD) {
+                    const uint16_t *in = a.dy + (w.row0 + c * W + c0) * static_cast<long long>(a.M) + feat;
+#pragma unroll
+                    for (int j = 0; j < KEEP; ++j) {
+                        dh[j] = mine && c * W + c0 + j < w.rows ? *in : 0;
+                        in += a.M;
+                    }
+                }
+            };
+            auto release = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (CG == 2)
+                        mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[ab]), 0));
+                    else
+                        mbar_arrive(&acc_empty[ab]);
+                }
+            };
+            auto fetch = [&](int c) {
+                if (have && ok) {
+                    if constexpr (W == 32)
+                        tmem_ld_32x32b_x32(t_row + c * W, *reinterpret_cast<uint32_t(*)[32]>(v));
+                    else
+                        tmem_ld_32x32b_x16(t_row + c * W, v);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < W; ++j) v[j] = 0u;
+                }
+            };
+            if (h < chunks) fetch_dh(h);
             if (have) {
                 if (ok) ok = mbar_wait(&acc_full[ab], (n >> 1) & 1u, ctx, kSiteEpilogueFull);
                 ok = __all_sync(0xffffffffu, ok);
                 tc_fence_after();
             }
+            if (h < chunks)
+                fetch(h);
+            else if (have)
+                release();
 #pragma unroll 1
             for (int c = h; c < chunks; c += 2) {
-                uint32_t v[16];
-                if (have && ok) {
-                    tmem_ld_32x32b_x16(t_row + c * 16, v);
-                    tmem_ld_wait();
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] = 0u;
-                }
-                const int left = ok ? w.rows - c * 16 : 0;  // rows from this chunk on
-                const long long row = w.row0 + c * 16;
+                const int left = ok ? w.rows - c * W : 0;  // rows from this chunk on
+                const long long row = w.row0 + static_cast<long long>(c) * W;
+                const bool more = c + 2 < chunks;
+                tmem_ld_wait();
+                if (have && !more) release();
                 if constexpr (!Cfg::DUAL) {
+                    uint32_t r[W / 2];
+#pragma unroll
+                    for (int j = 0; j < W / 2; ++j)
+                        r[j] = pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+                    if (more) fetch(c + 2);
                     uint16_t *o = a.out + row * a.ldo + feat;
                     if (mine) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            if (j < left) put_bf16(o, __uint_as_float(v[j]));
+                        for (int j = 0; j < W; ++j) {
+                            if (j < left)
+                                *o = static_cast<uint16_t>(j & 1 ? r[j / 2] >> 16 : r[j / 2]);
                             o += a.ldo;
                         }
                     }
@@ -453,59 +501,58 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                         float *z = a.preact + (gate ? 0 : static_cast<long long>(a.R) * a.M) +
                                    row * a.M + feat;
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
+                        for (int j = 0; j < W; ++j) {
                             if (j < left) *z = __uint_as_float(v[j]);
                             z += a.M;
                         }
                     }
-                    // the gate's warp finishes the chunk's first eight columns, the
-                    // other one the rest
-                    const int c0 = gate ? 0 : 8;
-                    float dh[8];
-                    if constexpr (Cfg::MODE == Exp::GATED_GRAD) {
-                        const uint16_t *in = a.dy + (row + c0) * a.M + feat;
+                    // half of the columns to the other warp of the features, half from it
+                    float *own = reinterpret_cast<float *>(smem + Cfg::SWAP_OFFSET) +
+                                 e * (KEEP * 32) + lane;
+                    const float *other = own + ((e ^ 2) - e) * (KEEP * 32);
+                    const uint32_t bar = 1 + h * 2 + (q & 1u);
+                    float g[KEEP], up[KEEP], d[KEEP];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            dh[j] = mine && c0 + j < left
-                                        ? __uint_as_float(static_cast<uint32_t>(*in) << 16)
-                                        : 0.0f;
-                            in += a.M;
-                        }
+                    for (int j = 0; j < KEEP; ++j) {
+                        own[32 * j] = __uint_as_float(gate ? v[KEEP + j] : v[j]);
+                        g[j] = __uint_as_float(gate ? v[j] : v[KEEP + j]);
+                        if (Cfg::MODE == Exp::GATED_GRAD)
+                            d[j] = __uint_as_float(
+                                static_cast<uint32_t>(dh[Cfg::MODE == Exp::GATED_GRAD ? j : 0])
+                                << 16);
                     }
-                    float *own = swap + (2 * e + turn) * 256;
-                    const float *other = swap + (2 * (e ^ 2) + turn) * 256;
-                    turn ^= 1u;
+                    if (more) {
+                        fetch(c + 2);
+                        fetch_dh(c + 2);
+                    }
+                    named_barrier(bar, 64);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) own[32 * j] = __uint_as_float(gate ? v[8 + j] : v[j]);
-                    named_barrier(1 + h * 2 + (q & 1u), 64);
-                    float g[8], up[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float kept = __uint_as_float(gate ? v[j] : v[8 + j]);
+                    for (int j = 0; j < KEEP; ++j) {
                         const float got = other[32 * j];
-                        g[j] = gate ? kept : got;
-                        up[j] = gate ? got : kept;
+                        up[j] = gate ? got : g[j];
+                        g[j] = gate ? g[j] : got;
                     }
-                    const long long at = (row + c0) * a.ldo + feat;
+                    named_barrier(bar, 64);  // both have read: the next chunk may be written
                     with_act(a.act, [&](auto A) {
                         constexpr int ACT = decltype(A)::value;
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
+                        for (int j = 0; j < KEEP; ++j) {
                             if constexpr (Cfg::MODE == Exp::GATED_GRAD) {
                                 float value;
-                                const float d = act_value_grad<ACT>(g[j], value);
-                                g[j] = dh[j] * up[j] * d;
-                                up[j] = dh[j] * value;
+                                const float slope = act_value_grad<ACT>(g[j], value);
+                                g[j] = d[j] * up[j] * slope;
+                                up[j] = d[j] * value;
                             } else {
                                 g[j] = act_value<ACT>(g[j]) * up[j];
                             }
                         }
                     });
                     if (mine) {
+                        const long long at = (row + c0) * a.ldo + feat;
                         uint16_t *o = a.out + at;
                         uint16_t *o2 = Cfg::MODE == Exp::GATED_GRAD ? a.out2 + at : nullptr;
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
+                        for (int j = 0; j < KEEP; ++j) {
                             if (c0 + j < left) {
                                 put_bf16(o, g[j]);
                                 if constexpr (Cfg::MODE == Exp::GATED_GRAD) put_bf16(o2, up[j]);
@@ -514,16 +561,6 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                             if constexpr (Cfg::MODE == Exp::GATED_GRAD) o2 += a.ldo;
                         }
                     }
-                }
-            }
-            if (have) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if constexpr (CG == 2)
-                        mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[ab]), 0));
-                    else
-                        mbar_arrive(&acc_empty[ab]);
                 }
             }
         }
@@ -557,8 +594,18 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 // multiplied last, so that neither the clearing nor the two CTAs' agreement on it is
 // waited for.  (Cleared in the ring's last stage, groups of 520 rows took 258 us for 32
 // experts' 2048 x 4096, 512 rows 182.)
-template <int BK_, int STAGES_, int NBUF_>
+//
+// Few rows a group: a unit's output takes longer than its products.  Then a ring of three
+// stages instead of four makes room to stage all of a warp's output at once, 64 columns
+// wide (WIDE), whose rows of 128 bytes also write fewer 32-byte sectors in part where the
+// matrix's rows start anywhere in one.  32 experts 2048 x 4096, us with three and with four
+// stages: 256 rows each 154 and 174, 320 rows 187 and 174; 1624 x 2488, 8 rows 73 and 85.
+// What is left is writing dW (8 rows each of 64 experts 1024 x 2048: 4.1 TB/s, a memset's
+// rate) and, with more rows, the traffic of both directions beside the products (512 rows
+// 192 us, 1.43 PFLOP/s; without its stores the kernel takes 166).
+template <int BK_, int STAGES_, int NBUF_, bool WIDE_>
 struct ExpWeightsCfg {
+    static constexpr bool WIDE = WIDE_;
     static constexpr int BM = 128, BN = 256, BK = BK_, STAGES = STAGES_, NBUF = NBUF_;
     static constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN / 2 * BK * 2;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
@@ -572,7 +619,7 @@ struct ExpWeightsCfg {
     static constexpr int THREADS = 64 + 32 * EPI + 32;
     static constexpr int SMEM_BYTES = smem_request(USED + 1024, 1);
     static_assert(USED + 1024 <= 232448, "shared memory");
-    static_assert(EPI_COLS / 32 % NBUF == 0, "whole batches");
+    static_assert(WIDE ? NBUF == EPI_COLS / 32 : EPI_COLS / 32 % NBUF == 0, "whole batches");
     static_assert(BK == 96, "a step is a box of 96 rows, or shorter ones of 64 and 32");
 };
 
@@ -628,6 +675,33 @@ __device__ __forceinline__ void put_rows32_batch_3d(Ctx &c, const CUtensorMap *m
     __syncwarp();
 }
 
+// 64-column blocks side by side, in 4 KB each with the 128-byte swizzle (16-byte chunk j of
+// row r at j ^ (r % 8)), all of a warp's columns at once.
+template <int BLOCKS, class Ctx>
+__device__ __forceinline__ void put_rows64_3d(Ctx &c, const CUtensorMap *map, int z, int col,
+                                              const uint32_t *p) {
+    static_assert(2 * BLOCKS == Ctx::NB, "staging buffers");
+    if (c.m0 >= c.M || col >= c.N) return;
+    if (c.lane == 0) bulk_wait_read<0>();
+    __syncwarp();
+    const uint32_t base = smem_u32(c.bufs);
+#pragma unroll
+    for (int b = 0; b < BLOCKS; ++b)
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j)
+            sts128(base + b * 4096 + c.lane * 128 + ((j ^ (c.lane & 7u)) << 4), p[32 * b + 4 * j],
+                   p[32 * b + 4 * j + 1], p[32 * b + 4 * j + 2], p[32 * b + 4 * j + 3]);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (c.lane == 0) {
+#pragma unroll
+        for (int b = 0; b < BLOCKS; ++b)
+            if (col + 64 * b < c.N) tma_store_3d(map, c.bufs + b * 4096, col + 64 * b, c.m0, z);
+        bulk_commit();
+    }
+    __syncwarp();
+}
+
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
     experts_weights_kernel(const __grid_constant__ ExpertsWeightsMaps maps, const ExpertsArgs a,
@@ -677,7 +751,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    op_begin(0);
+    op_begin(a.overlap);
     const int units = a.E * a.f_tiles * a.n_seg * a.segments;
     const int slot = static_cast<int>(blockIdx.x) / 2, slots = static_cast<int>(gridDim.x) / 2;
 
@@ -861,7 +935,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 #pragma unroll
             for (int j = 0; j < 16 * C; ++j)
                 v[j] = pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-            if (a.tma_out) {
+            if (Cfg::WIDE && a.tma_out) {
+                if constexpr (Cfg::WIDE)
+                    put_rows64_3d<C / 2>(c, &maps.c[w.seg], w.expert, w.n0 + col0, v);
+            } else if (a.tma_out) {
 #pragma unroll
                 for (int b = 0; b < C; b += B)
                     put_rows32_batch_3d<B>(c, &maps.c[w.seg], w.expert, w.n0 + col0 + 32 * b,
@@ -887,7 +964,131 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         tc_fence_after();
         tmem_dealloc_pair(tmem, Cfg::TMEM_COLS);
     }
+    op_end(a.overlap);
 }
+
+// A call's sizes: R rows, N outputs (gated: features), K reduction columns, E experts.
+struct ExpSizes {
+    int R, N, K, E;
+    const int32_t *offsets;
+};
+
+// --------------------------------------------------------------- relayout ---
+// Matrices whose rows are no multiples of 16 bytes, to a pitch that TMA reads: many short
+// rows (an expert's weights), so a thread takes 16-byte vectors of the whole copy in turn,
+// each shifted out of the two aligned ones that cover it.  Bound by HBM: 171 MB in rows of
+// 1686 bytes in 55 us, 6.2 TB/s (a block a row at a time: 117).
+struct RelayoutParams {
+    const uint16_t *src;
+    uint16_t *dst;
+    unsigned long long vecs;  // of the copy
+    unsigned row_vecs, cols;
+    long long ld, end;        // elements of a row of the copy, and of the source
+    const int32_t *offsets;   // experts without rows stay uncopied (nullptr: all rows)
+    unsigned expert_rows;     // matrix rows of an expert
+};
+
+__global__ void __launch_bounds__(256) relayout_kernel(const RelayoutParams p) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    constexpr int AHEAD = 4;
+    const unsigned long long first = blockIdx.x * (256ull * AHEAD) + threadIdx.x;
+    uint4 lo[AHEAD], hi[AHEAD];
+    long long to[AHEAD];
+    uint32_t off[AHEAD];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+        const unsigned long long i = first + 256 * u;
+        to[u] = -1;
+        if (i >= p.vecs) continue;
+        const unsigned long long row = p.vecs >> 32 == 0
+                                           ? static_cast<unsigned>(i) / p.row_vecs
+                                           : i / p.row_vecs;
+        if (p.offsets != nullptr) {
+            const unsigned long long e = row / p.expert_rows;
+            if (p.offsets[e + 1] <= p.offsets[e]) continue;
+        }
+        const unsigned c = 8 * static_cast<unsigned>(i - row * p.row_vecs);
+        const long long from = static_cast<long long>(row * p.cols) + c;
+        to[u] = static_cast<long long>(row) * p.ld + c;
+        off[u] = static_cast<uint32_t>(from & 7) * 2u;
+        const long long at = from & ~7ll;
+        if (at + 16 <= p.end) {
+            lo[u] = __ldg(reinterpret_cast<const uint4 *>(p.src + at));
+            hi[u] = __ldg(reinterpret_cast<const uint4 *>(p.src + at) + 1);
+        } else {  // the source's last elements, one by one
+            uint32_t w[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (at + j < p.end)
+                    w[j / 2] |= static_cast<uint32_t>(p.src[at + j]) << (j % 2 * 16);
+            lo[u] = make_uint4(w[0], w[1], w[2], w[3]);
+            hi[u] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+        if (to[u] < 0) continue;
+        uint32_t w[4];
+        shift16(lo[u], hi[u], off[u], w);
+        *reinterpret_cast<uint4 *>(p.dst + to[u]) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// As OpRelayout: the copies are planned, then made; a matrix that TMA reads stays.
+class ExpRelayout {
+  public:
+    void add(OpMat *out, const uint16_t *src, long long rows, long long cols, OpArena &arena) {
+        out->p = src;
+        out->ld = cols;
+        if (cols % 8 == 0 || rows == 0 || cols == 0) return;
+        const long long ld = op_round_up(cols, 64);
+        jobs_[n_++] = Job{out, src, rows, cols, ld, arena.add(rows * ld * 2), nullptr, 1};
+    }
+    // E matrices of K x N; with fewer rows than experts, of those that have rows
+    void add_weights(OpMat *out, const uint16_t *src, const ExpSizes &z, OpArena &arena) {
+        const int before = n_;
+        add(out, src, static_cast<long long>(z.E) * z.K, z.N, arena);
+        if (n_ > before && z.R < z.E) {
+            jobs_[before].offsets = z.offsets;
+            jobs_[before].expert_rows = z.K;
+        }
+    }
+    pgemm_status run(OpArena &arena, cudaStream_t s) {
+        for (int i = 0; i < n_; ++i) {
+            const Job &j = jobs_[i];
+            RelayoutParams p{};
+            p.src = j.src;
+            p.dst = arena.at<uint16_t>(j.at);
+            p.row_vecs = static_cast<unsigned>((j.cols + 7) / 8);
+            p.vecs = static_cast<unsigned long long>(j.rows) * p.row_vecs;
+            p.cols = static_cast<unsigned>(j.cols);
+            p.ld = j.ld;
+            p.end = j.rows * j.cols;
+            p.offsets = j.offsets;
+            p.expert_rows = static_cast<unsigned>(j.expert_rows);
+            j.out->p = p.dst;
+            j.out->ld = j.ld;
+            const unsigned long long blocks = (p.vecs + 1023) / 1024;
+            if (blocks > INT_MAX) return PGEMM_ERR_TOO_LARGE;
+            const pgemm_status st = launch_small(
+                relayout_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), s, p);
+            if (st != PGEMM_OK) return st;
+        }
+        return PGEMM_OK;
+    }
+
+  private:
+    struct Job {
+        OpMat *out;
+        const uint16_t *src;
+        long long rows, cols, ld, at;
+        const int32_t *offsets;
+        int expert_rows;
+    };
+    Job jobs_[4];
+    int n_ = 0;
+};
 
 // ------------------------------------------------------------------- host ---
 template <class Maps>
@@ -961,12 +1162,6 @@ static pgemm_status exp_launch(const OpDevice &dev, const Maps &maps, const Expe
                                                                             : PGEMM_ERR_CUDA;
 }
 
-// A call's sizes: R rows, N outputs (gated: features), K reduction columns, E experts.
-struct ExpSizes {
-    int R, N, K, E;
-    const int32_t *offsets;
-};
-
 template <class Cfg>
 static pgemm_status rows_launch(const OpDevice &dev, const ExpSizes &z, const OpMat *x,
                                 const OpMat *w, int segments, ExpertsArgs a, cudaStream_t s) {
@@ -999,17 +1194,23 @@ template <Exp MODE>
 static pgemm_status rows_product(const OpDevice &dev, const ExpSizes &z, const OpMat *x,
                                  const OpMat *w, int segments, const ExpertsArgs &a,
                                  cudaStream_t s) {
-    // few rows a group: the weights are all there is to read, and single CTAs with small
-    // tiles of rows keep more of them on the way
-    if (z.R <= 48ll * z.E) return rows_launch<ExpCfg<1, 64, 128, 4, MODE>>(dev, z, x, w, segments, a, s);
+    // Few rows a group: the weights are all there is to read, and single CTAs with small
+    // tiles of rows keep more of them on the way (64 experts 2048 x 1024, 16 rows each: 47
+    // us against 50 on pairs), until groups pass a tile's 64 rows and read them twice (96
+    // rows: 71 against 54); groups are uneven, so that begins below a mean of 64.  And few
+    // tiles: smaller ones on more SMs.
+    const long long live = z.R < z.E ? z.R : z.E;
+    const long long pairs =
+        (z.R / 256 + live) * op_blocks(MODE == Exp::TRANSPOSED ? z.K : z.N,
+                                       MODE == Exp::LINEAR || MODE == Exp::TRANSPOSED ? 256 : 128);
+    if (z.R <= 24ll * z.E || 4 * pairs <= dev.sm_count) return rows_launch<ExpCfg<1, 64, 128, 4, MODE>>(dev, z, x, w, segments, a, s);
     return rows_launch<ExpCfg<2, 256, 128, 3, MODE>>(dev, z, x, w, segments, a, s);
 }
 
-// dW[j][e] = x_e^T dz[j]_e for each of `segments` outputs.
-static pgemm_status weights_product(const OpDevice &dev, const ExpSizes &z, const OpMat &x,
-                                    const OpMat *dz, int segments, uint16_t *const *out,
-                                    cudaStream_t s) {
-    using Cfg = ExpWeightsCfg<96, 4, 1>;
+template <class Cfg>
+static pgemm_status weights_launch(const OpDevice &dev, const ExpSizes &z, const OpMat &x,
+                                   const OpMat *dz, int segments, uint16_t *const *out,
+                                   bool overlap, cudaStream_t s) {
     ExpertsArgs a{};
     a.R = z.R;
     a.E = z.E;
@@ -1022,6 +1223,7 @@ static pgemm_status weights_product(const OpDevice &dev, const ExpSizes &z, cons
     a.out = out[0];
     a.out2 = segments > 1 ? out[1] : nullptr;
     a.tma_out = z.N % 8 == 0;
+    a.overlap = overlap ? 1 : 0;
     ExpertsWeightsMaps maps{};
     constexpr int kBoxes[4] = {Cfg::BK, 64, 32, 16};
     pgemm_status st = PGEMM_OK;
@@ -1031,11 +1233,22 @@ static pgemm_status weights_product(const OpDevice &dev, const ExpSizes &z, cons
         for (int b = 0; b < 4 && st == PGEMM_OK; ++b)
             st = op_encode(&maps.z[j][b], dz[j].p, z.N, z.R, dz[j].ld, kBoxes[b]);
         if (st == PGEMM_OK && a.tma_out)
-            st = op_encode_out_3d(&maps.c[j], out[j], z.N, z.K, z.E, z.N);
+            st = Cfg::WIDE ? op_encode_3d(&maps.c[j], out[j], z.N, z.K, z.E, z.N, 32)
+                           : op_encode_out_3d(&maps.c[j], out[j], z.N, z.K, z.E, z.N);
     }
     if (st != PGEMM_OK) return st;
     const long long units = static_cast<long long>(z.E) * a.f_tiles * a.n_seg * segments;
     return exp_launch<Cfg, 2, ExpertsWeightsMaps, experts_weights_kernel<Cfg>>(dev, maps, a, units, s);
+}
+
+// dW[j][e] = x_e^T dz[j]_e for each of `segments` outputs.  overlap: behind the product for
+// dX, which reads what this one reads and writes nothing of it.
+static pgemm_status weights_product(const OpDevice &dev, const ExpSizes &z, const OpMat &x,
+                                    const OpMat *dz, int segments, uint16_t *const *out,
+                                    bool overlap, cudaStream_t s) {
+    if (z.R <= 256ll * z.E)
+        return weights_launch<ExpWeightsCfg<96, 3, 4, true>>(dev, z, x, dz, segments, out, overlap, s);
+    return weights_launch<ExpWeightsCfg<96, 4, 1, false>>(dev, z, x, dz, segments, out, overlap, s);
 }
 
 static pgemm_status exp_check(const ExpSizes &z) {
@@ -1061,12 +1274,12 @@ static pgemm_status experts_linear_forward(const ExpSizes &z, const uint16_t *X,
     OpDevice dev;
     if ((st = op_device(&dev)) != PGEMM_OK) return st;
     OpArena arena(dev, s);
-    OpRelayout rl;
+    ExpRelayout rl;
     OpMat x, w;
     rl.add(&x, X, z.R, z.K, arena);
-    rl.add(&w, W, static_cast<long long>(z.E) * z.K, z.N, arena);
+    rl.add_weights(&w, W, z, arena);
     if ((st = arena.alloc()) != PGEMM_OK) return st;
-    if (z.K > 0 && (st = rl.run(dev, arena, s)) != PGEMM_OK) return st;
+    if (z.K > 0 && (st = rl.run(arena, s)) != PGEMM_OK) return st;
     ExpertsArgs a{};
     a.out = Y;
     a.ldo = z.N;
@@ -1090,15 +1303,15 @@ static pgemm_status experts_linear_backward(const ExpSizes &z, const uint16_t *X
     if ((st = op_device(&dev)) != PGEMM_OK) return st;
     if (z.R == 0) return zero_bf16(dW, static_cast<long long>(z.E) * z.K * z.N, s);
     OpArena arena(dev, s);
-    OpRelayout rl;
+    ExpRelayout rl;
     OpMat x, w, dy;
     if (some) {
         rl.add(&dy, dY, z.R, z.N, arena);
         if (want_w) rl.add(&x, X, z.R, z.K, arena);
-        if (want_x) rl.add(&w, W, static_cast<long long>(z.E) * z.K, z.N, arena);
+        if (want_x) rl.add_weights(&w, W, z, arena);
     }
     if ((st = arena.alloc()) != PGEMM_OK) return st;
-    if ((st = rl.run(dev, arena, s)) != PGEMM_OK) return st;
+    if ((st = rl.run(arena, s)) != PGEMM_OK) return st;
     if (want_x) {
         ExpertsArgs a{};
         a.out = dX;
@@ -1106,7 +1319,7 @@ static pgemm_status experts_linear_backward(const ExpSizes &z, const uint16_t *X
         st = rows_product<Exp::TRANSPOSED>(dev, z, &dy, &w, 1, a, s);
         if (st != PGEMM_OK) return st;
     }
-    return want_w ? weights_product(dev, z, x, &dy, 1, &dW, s) : PGEMM_OK;
+    return want_w ? weights_product(dev, z, x, &dy, 1, &dW, want_x, s) : PGEMM_OK;
 }
 
 // A ReLU gate is not offered: its derivative hangs on the sign of a sum that the tensor
@@ -1128,13 +1341,13 @@ static pgemm_status experts_gated_forward(const ExpSizes &z, const uint16_t *X, 
     OpDevice dev;
     if ((st = op_device(&dev)) != PGEMM_OK) return st;
     OpArena arena(dev, s);
-    OpRelayout rl;
+    ExpRelayout rl;
     OpMat x, w[2];
     rl.add(&x, X, z.R, z.K, arena);
-    rl.add(&w[0], Wg, static_cast<long long>(z.E) * z.K, z.N, arena);
-    rl.add(&w[1], Wu, static_cast<long long>(z.E) * z.K, z.N, arena);
+    rl.add_weights(&w[0], Wg, z, arena);
+    rl.add_weights(&w[1], Wu, z, arena);
     if ((st = arena.alloc()) != PGEMM_OK) return st;
-    if (z.K > 0 && (st = rl.run(dev, arena, s)) != PGEMM_OK) return st;
+    if (z.K > 0 && (st = rl.run(arena, s)) != PGEMM_OK) return st;
     ExpertsArgs a{};
     a.out = H;
     a.ldo = z.N;
@@ -1169,19 +1382,19 @@ static pgemm_status experts_gated_backward(const ExpSizes &z, const uint16_t *X,
         return st == PGEMM_OK ? zero_bf16(dWu, size, s) : st;
     }
     OpArena arena(dev, s);
-    OpRelayout rl;
+    ExpRelayout rl;
     OpMat x, w[2], dz[2];
     if (some) {
         if (want_w || recompute) rl.add(&x, X, z.R, z.K, arena);
         if (want_x || recompute) {
-            rl.add(&w[0], Wg, static_cast<long long>(z.E) * z.K, z.N, arena);
-            rl.add(&w[1], Wu, static_cast<long long>(z.E) * z.K, z.N, arena);
+            rl.add_weights(&w[0], Wg, z, arena);
+            rl.add_weights(&w[1], Wu, z, arena);
         }
     }
     const long long dz_ld = op_round_up(z.N, 64);
     const long long at0 = arena.add(dz_ld * z.R * 2), at1 = arena.add(dz_ld * z.R * 2);
     if ((st = arena.alloc()) != PGEMM_OK) return st;
-    if ((st = rl.run(dev, arena, s)) != PGEMM_OK) return st;
+    if ((st = rl.run(arena, s)) != PGEMM_OK) return st;
     for (int j = 0; j < 2; ++j) dz[j] = OpMat{arena.at<uint16_t>(j ? at1 : at0), dz_ld};
     if (some && preact) {
         OpActGrad g;
@@ -1213,7 +1426,7 @@ static pgemm_status experts_gated_backward(const ExpSizes &z, const uint16_t *X,
         if ((st = rows_product<Exp::TRANSPOSED>(dev, z, dz, w, 2, a, s)) != PGEMM_OK) return st;
     }
     uint16_t *out[2] = {dWg, dWu};
-    return want_w ? weights_product(dev, z, x, dz, 2, out, s) : PGEMM_OK;
+    return want_w ? weights_product(dev, z, x, dz, 2, out, want_x, s) : PGEMM_OK;
 }
 
 }  // namespace pg

@@ -339,6 +339,19 @@ struct RowsIn {
     }
 };
 
+// 16 bytes from byte `off` (even) of the 32 in lo, hi.
+__device__ __forceinline__ void shift16(const uint4 &lo, const uint4 &hi, uint32_t off,
+                                        uint32_t (&o)[4]) {
+    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    uint32_t a[7], b[5];
+#pragma unroll
+    for (int i = 0; i < 7; ++i) a[i] = off & 4u ? w[i + 1] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) b[i] = off & 8u ? a[i + 2] : a[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = __funnelshift_r(b[i], b[i + 1], (off & 2u) * 8u);
+}
+
 // 32 values of a bf16 vector from index col (zero beyond n), the same in
 // every lane.  The vector's base is 16-byte aligned and col a multiple of 32.
 __device__ __forceinline__ void get_vec32(const uint16_t *v, int n, int col, float (&f)[32]) {

@@ -83,8 +83,11 @@ __device__ __forceinline__ void gain_load(const uint16_t *g, const RowSpan &r, i
     if (g == nullptr) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] = 1.0f;
-    } else if (r.shift == 0 && r.whole(v)) {
-        unpack8(__ldg(reinterpret_cast<const uint4 *>(g) + v), f);
+    } else if (r.whole(v) && r.col(v) / 8 * 8 + 16 <= r.D) {
+        const uint4 *at = reinterpret_cast<const uint4 *>(g) + r.col(v) / 8;
+        uint32_t w[4];
+        shift16(__ldg(at), __ldg(at + 1), static_cast<uint32_t>(r.col(v) & 7) * 2u, w);
+        unpack8(make_uint4(w[0], w[1], w[2], w[3]), f);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -519,10 +522,10 @@ static pgemm_status norm_backward(int T, int D, const uint16_t *S, const uint16_
         constexpr int V = decltype(v)::value;
         constexpr bool A = decltype(aligned)::value;
         constexpr GainSum SUM = A && V <= 2 ? GainSum::REGISTERS : GainSum::SHARED;
-        // blocks of an SM: what registers and shared memory allow, eight at most, since
-        // each leaves a row of sums behind
+        // blocks of an SM: what registers and shared memory allow, four at most, since each
+        // leaves a row of sums behind
         const int smem = dgain && SUM == GainSum::SHARED ? (D + 7) / 8 * 32 : 0;
-        int per_sm = threads <= 128 ? 8 : 1024 / threads;
+        int per_sm = threads <= 256 ? 4 : 1024 / threads;
         while (per_sm > 1 && per_sm * (smem + 2048) > kSmemPerSm) --per_sm;
         const int most = dev.sm_count * per_sm;
         const int blocks = T < most ? T : most;

@@ -480,9 +480,9 @@ static pgemm_status expert_sort_run(int T, int E, int k, const int32_t *experts,
 
 // ----------------------------------------------------- gather and combine ---
 // Rows as vectors of W bf16 values: 8 where rows are multiples of 16 bytes, else 2 or 1
-// (a token's row and its sorted rows then start at different places of a vector).  A
-// group of threads takes a token; the row of X or dY is read once, the k sorted rows
-// travel together.
+// (a token's row and its sorted rows then start at different places of a vector).  Gather
+// and combine take the vectors of all tokens in turn, a thread one of them, so that every
+// thread has one whatever the width; the k sorted rows' travel together.
 struct RowsParams {
     int T, k, D;
     long long rows;  // T k: a slot_row outside [0, rows) does not count
@@ -546,81 +546,87 @@ __device__ __forceinline__ typename Vec<W>::T vec_zero() {
 constexpr int kRowsThreads = 256;
 constexpr int kAhead = 4;  // sorted rows on the way
 
-// PER: threads of a token (a power of two up to kRowsThreads)
+// Vector i of all tokens': token t, vector v of its row.
+struct RowsAt {
+    long long t;
+    unsigned v;
+    __device__ __forceinline__ RowsAt(unsigned long long i, unsigned vecs) {
+        if (i >> 32 == 0) {  // (a 32-bit division where it fits)
+            const unsigned q = static_cast<unsigned>(i) / vecs;
+            t = q;
+            v = static_cast<unsigned>(i) - q * vecs;
+        } else {
+            const unsigned long long q = i / vecs;
+            t = static_cast<long long>(q);
+            v = static_cast<unsigned>(i - q * vecs);
+        }
+    }
+};
+
 template <int W>
-__global__ void __launch_bounds__(kRowsThreads) gather_kernel(const RowsParams p, int per) {
+__global__ void __launch_bounds__(kRowsThreads) gather_kernel(const RowsParams p) {
     using V = typename Vec<W>::T;
     grid_dependency_wait();
     grid_launch_dependents();
-    const int group = threadIdx.x / per, lane = threadIdx.x % per, groups = kRowsThreads / per;
-    const unsigned vecs = p.D / W;  // (unsigned: a step may pass 2^31)
-    for (long long t = blockIdx.x * static_cast<long long>(groups) + group; t < p.T;
-         t += static_cast<long long>(gridDim.x) * groups) {
-        const V *src = reinterpret_cast<const V *>(p.x + t * p.D);
-        const int32_t *to = p.slot_row + t * p.k;
-        for (unsigned v = lane; v < vecs; v += per) {
-            const V x = src[v];
-            for (int j = 0; j < p.k; ++j) {
-                const int r = to[j];
-                if (r >= 0 && r < p.rows)
-                    reinterpret_cast<V *>(p.out + static_cast<long long>(r) * p.D)[v] = x;
-            }
+    const unsigned vecs = p.D / W;
+    const unsigned long long total = static_cast<unsigned long long>(p.T) * vecs;
+    for (unsigned long long i = blockIdx.x * static_cast<unsigned long long>(kRowsThreads) + threadIdx.x;
+         i < total; i += static_cast<unsigned long long>(gridDim.x) * kRowsThreads) {
+        const RowsAt at(i, vecs);
+        const V x = reinterpret_cast<const V *>(p.x)[i];
+        const int32_t *to = p.slot_row + at.t * p.k;
+        for (int j = 0; j < p.k; ++j) {
+            const int r = to[j];
+            if (r >= 0 && r < p.rows)
+                reinterpret_cast<V *>(p.out + static_cast<long long>(r) * p.D)[at.v] = x;
         }
     }
 }
 
 template <int W>
-__global__ void __launch_bounds__(kRowsThreads) combine_kernel(const RowsParams p, int per) {
+__global__ void __launch_bounds__(kRowsThreads) combine_kernel(const RowsParams p) {
     using V = typename Vec<W>::T;
     grid_dependency_wait();
     grid_launch_dependents();
-    const int group = threadIdx.x / per, lane = threadIdx.x % per, groups = kRowsThreads / per;
-    const unsigned vecs = p.D / W;  // (unsigned: a step may pass 2^31)
-    for (long long t = blockIdx.x * static_cast<long long>(groups) + group; t < p.T;
-         t += static_cast<long long>(gridDim.x) * groups) {
-        const int32_t *from = p.slot_row + t * p.k;
-        const float *w = p.weights ? p.weights + t * p.k : nullptr;
-        // the first choices' rows and weights, for all of the token's vectors
-        const V *row[kAhead];
-        float weight[kAhead];
-        auto choices = [&](int j0) {
+    const unsigned vecs = p.D / W;
+    const unsigned long long total = static_cast<unsigned long long>(p.T) * vecs;
+    for (unsigned long long i = blockIdx.x * static_cast<unsigned long long>(kRowsThreads) + threadIdx.x;
+         i < total; i += static_cast<unsigned long long>(gridDim.x) * kRowsThreads) {
+        const RowsAt at(i, vecs);
+        const int32_t *from = p.slot_row + at.t * p.k;
+        const float *w = p.weights ? p.weights + at.t * p.k : nullptr;
+        float sum[W];
+#pragma unroll
+        for (int c = 0; c < W; ++c) sum[c] = 0.0f;
+        for (int j0 = 0; j0 < p.k; j0 += kAhead) {
+            V y[kAhead];
+            int r[kAhead];
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
-                const int r = j0 + j < p.k ? from[j0 + j] : -1;
-                const bool in = r >= 0 && r < p.rows;
-                row[j] = in ? reinterpret_cast<const V *>(p.ys + static_cast<long long>(r) * p.D)
-                            : nullptr;
-                weight[j] = in && w ? w[j0 + j] : 1.0f;
+                r[j] = j0 + j < p.k ? from[j0 + j] : -1;
+                if (r[j] >= p.rows) r[j] = -1;
             }
-        };
-        if (p.k <= kAhead) choices(0);
-        for (unsigned v = lane; v < vecs; v += per) {
-            float sum[W];
-            V res = vec_zero<W>();
-            if (p.x) res = reinterpret_cast<const V *>(p.x + t * p.D)[v];
 #pragma unroll
-            for (int i = 0; i < W; ++i) sum[i] = 0.0f;
-            for (int j0 = 0; j0 < p.k; j0 += kAhead) {
-                if (p.k > kAhead) choices(j0);
-                V y[kAhead];
+            for (int j = 0; j < kAhead; ++j)
+                if (r[j] >= 0)
+                    y[j] = reinterpret_cast<const V *>(p.ys + static_cast<long long>(r[j]) * p.D)[at.v];
 #pragma unroll
-                for (int j = 0; j < kAhead; ++j)
-                    if (row[j] != nullptr) y[j] = row[j][v];
+            for (int j = 0; j < kAhead; ++j)
+                if (r[j] >= 0) {
+                    const float wj = w ? w[j0 + j] : 1.0f;
+                    float f[W];
+                    vec_get<W>(y[j], f);
 #pragma unroll
-                for (int j = 0; j < kAhead; ++j)
-                    if (row[j] != nullptr) {
-                        float f[W];
-                        vec_get<W>(y[j], f);
-#pragma unroll
-                        for (int i = 0; i < W; ++i) sum[i] = fmaf(weight[j], f[i], sum[i]);
-                    }
-            }
-            float f[W];
-            vec_get<W>(res, f);
-#pragma unroll
-            for (int i = 0; i < W; ++i) sum[i] += f[i];
-            reinterpret_cast<V *>(p.out + t * p.D)[v] = vec_put<W>(sum);
+                    for (int c = 0; c < W; ++c) sum[c] = fmaf(wj, f[c], sum[c]);
+                }
         }
+        if (p.x) {
+            float f[W];
+            vec_get<W>(reinterpret_cast<const V *>(p.x)[i], f);
+#pragma unroll
+            for (int c = 0; c < W; ++c) sum[c] += f[c];
+        }
+        reinterpret_cast<V *>(p.out)[i] = vec_put<W>(sum);
     }
 }
 
@@ -714,6 +720,12 @@ static int rows_per(int D) {
     while (per < vecs && per < kRowsThreads) per *= 2;
     return per;
 }
+// gather and combine: a vector a thread
+static dim3 vectors_grid(int T, int D) {
+    const long long blocks =
+        (static_cast<long long>(T) * (D / rows_width(D)) + kRowsThreads - 1) / kRowsThreads;
+    return dim3(static_cast<unsigned>(blocks < INT_MAX ? blocks : INT_MAX));
+}
 static dim3 rows_grid(const OpDevice &dev, int T, int per) {
     const int blocks = op_blocks(T, kRowsThreads / per), most = dev.sm_count * 16;
     return dim3(blocks < most ? blocks : most);
@@ -755,10 +767,9 @@ static pgemm_status gather_run(int T, int k, int D, const uint16_t *X, const int
     RowsParams p = rows_params(T, k, D, slot_row);
     p.x = X;
     p.out = Xs;
-    const int per = rows_per(D);
     return with_width(D, [&](auto w) {
-        return launch_small(gather_kernel<decltype(w)::value>, rows_grid(dev, T, per),
-                            dim3(kRowsThreads), s, p, per);
+        return launch_small(gather_kernel<decltype(w)::value>, vectors_grid(T, D),
+                            dim3(kRowsThreads), s, p);
     });
 }
 
@@ -778,10 +789,10 @@ static pgemm_status combine_run(int T, int k, int D, const uint16_t *Ys, const i
     p.ys = Ys;
     p.weights = weights;
     p.out = Y;
-    const int per = rows_per(D);
     return with_width(D, [&](auto w) {
-        return launch_small(combine_kernel<decltype(w)::value>, rows_grid(dev, T, per),
-                            dim3(kRowsThreads), s, p, per);
+        return launch_small(combine_kernel<decltype(w)::value>,
+                            vectors_grid(T, D),
+                            dim3(kRowsThreads), s, p);
     });
 }
 

@@ -180,19 +180,6 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// 16 bytes from byte `off` (even) of the 32 in lo, hi.
-__device__ __forceinline__ void shift16(const uint4 &lo, const uint4 &hi, uint32_t off,
-                                        uint32_t (&o)[4]) {
-    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-    uint32_t a[7], b[5];
-#pragma unroll
-    for (int i = 0; i < 7; ++i) a[i] = off & 4u ? w[i + 1] : w[i];
-#pragma unroll
-    for (int i = 0; i < 5; ++i) b[i] = off & 8u ? a[i + 2] : a[i];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = __funnelshift_r(b[i], b[i + 1], (off & 2u) * 8u);
-}
-
 // RAW: each epilogue warp w brings its rows of every K step into the ring.  Rows start on
 // any even byte: the aligned 16-byte chunks that cover a row's part of the tile come
 // by cp.async, RAW_STEPS ahead, into the warp's own buffers (zero beyond the row, so
