@@ -25,9 +25,11 @@ constexpr int kNormMaxD = 32768;
 // 8 v - shift + 7 of the row.
 struct RowSpan {
     long long first;  // flat index of vector 0's first element (a multiple of 8)
+    long long end;    // elements of the matrix
     int shift, vecs, D;
-    __device__ __forceinline__ RowSpan(long long row, int D_) : D(D_) {
+    __device__ __forceinline__ RowSpan(long long row, int T, int D_) : D(D_) {
         const long long at = row * D_;
+        end = static_cast<long long>(T) * D_;
         shift = static_cast<int>(at & 7);
         first = at - shift;
         vecs = (D_ + shift + 7) >> 3;
@@ -51,15 +53,28 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                       pack_bf16(f[6], f[7]));
 }
 
-// Vector v of a row, zeros where the row is not.
+// Vector v of a row, zeros where the row is not.  (At the row's ends the neighbour's
+// elements are read with it and dropped; only the matrix's last vector may pass its end.)
 __device__ __forceinline__ uint4 row_load(const uint16_t *p, const RowSpan &r, int v) {
-    const uint16_t *at = p + r.first + 8ll * v;
+    const long long from = r.first + 8ll * v;
+    const uint16_t *at = p + from;
     if (r.whole(v)) return *reinterpret_cast<const uint4 *>(at);
     uint32_t w[4] = {0u, 0u, 0u, 0u};
+    if (from + 8 <= r.end) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(at);
+        w[0] = x.x;
+        w[1] = x.y;
+        w[2] = x.z;
+        w[3] = x.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (from + i < r.end) w[i / 2] |= static_cast<uint32_t>(at[i]) << (i % 2 * 16);
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int c = r.col(v) + i;
-        if (c >= 0 && c < r.D) w[i / 2] |= static_cast<uint32_t>(at[i]) << (i % 2 * 16);
+        if (c < 0 || c >= r.D) w[i / 2] &= i % 2 ? 0xffffu : 0xffff0000u;
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -78,25 +93,20 @@ __device__ __forceinline__ void row_store(uint16_t *p, const RowSpan &r, int v, 
 }
 
 // The gains of vector v's columns (ones without gains; anything where the row is not).
-__device__ __forceinline__ void gain_load(const uint16_t *g, const RowSpan &r, int v,
-                                          float (&f)[8]) {
-    if (g == nullptr) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = 1.0f;
-    } else if (r.whole(v) && r.col(v) / 8 * 8 + 16 <= r.D) {
-        const uint4 *at = reinterpret_cast<const uint4 *>(g) + r.col(v) / 8;
-        uint32_t w[4];
-        shift16(__ldg(at), __ldg(at + 1), static_cast<uint32_t>(r.col(v) & 7) * 2u, w);
-        unpack8(make_uint4(w[0], w[1], w[2], w[3]), f);
+__device__ __forceinline__ uint4 gain_load(const uint16_t *g, const RowSpan &r, int v) {
+    if (g == nullptr) return make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    const int c0 = r.col(v);
+    if (r.whole(v) && c0 / 8 * 8 + 16 <= r.D) {
+        const uint4 *at = reinterpret_cast<const uint4 *>(g) + c0 / 8;
+        shift16(__ldg(at), __ldg(at + 1), static_cast<uint32_t>(c0 & 7) * 2u, w);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int c = r.col(v) + i;
-            f[i] = c >= 0 && c < r.D
-                       ? __uint_as_float(static_cast<uint32_t>(__ldg(g + c)) << 16)
-                       : 0.0f;
-        }
+        for (int i = 0; i < 8; ++i)
+            if (c0 + i >= 0 && c0 + i < r.D)
+                w[i / 2] |= static_cast<uint32_t>(__ldg(g + c0 + i)) << (i % 2 * 16);
     }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 struct Add {
@@ -145,30 +155,17 @@ struct NormParams {
     float *dgain;  // [blocks][D] partial sums, or nullptr
 };
 
-// The gains of a thread's vectors: where rows start on vectors they are the same for every
-// row, and stay in registers.
-template <int V, bool ALIGNED>
-struct Gains {
-    uint4 kept[ALIGNED ? V : 1];
-    __device__ __forceinline__ Gains(const NormParams &p) {
-        if constexpr (ALIGNED) {
+// The gains of a thread's vectors: where rows start on vectors the same for every row, else
+// fetched with each.
+template <int V>
+__device__ __forceinline__ void gains_load(const NormParams &p, const RowSpan &row,
+                                           uint4 (&gains)[V]) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int v = threadIdx.x + i * blockDim.x;
-                kept[i] = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
-                if (p.gain != nullptr && 8 * v < p.D)
-                    kept[i] = *(reinterpret_cast<const uint4 *>(p.gain) + v);
-            }
-        }
+    for (int i = 0; i < V; ++i) {
+        const int v = threadIdx.x + i * blockDim.x;
+        if (v < row.vecs) gains[i] = gain_load(p.gain, row, v);
     }
-    __device__ __forceinline__ void get(const NormParams &p, const RowSpan &row, int i, int v,
-                                        float (&g)[8]) const {
-        if constexpr (ALIGNED)
-            unpack8(kept[i], g);
-        else
-            gain_load(p.gain, row, v, g);
-    }
-};
+}
 
 // V vectors a thread; ALIGNED: D is a multiple of 8.  With more than two vectors a thread
 // the next row is not fetched ahead, for want of registers.
@@ -178,11 +175,11 @@ __global__ void __launch_bounds__(V <= 2 ? 512 : 1024) rmsnorm_kernel(const Norm
     constexpr bool AHEAD = V <= 2;
     grid_dependency_wait();
     grid_launch_dependents();
-    const Gains<V, ALIGNED> gains(p);
     int turn = 0;
-    uint4 a[V], b[V];
+    uint4 a[V], b[V], gains[V], gains_next[ALIGNED ? 1 : V];
+    if (ALIGNED) gains_load(p, RowSpan(0, p.T, p.D), gains);
     auto fetch = [&](unsigned t) {
-        const RowSpan row(t, p.D);
+        const RowSpan row(t, p.T, p.D);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int v = threadIdx.x + i * blockDim.x;
@@ -192,14 +189,19 @@ __global__ void __launch_bounds__(V <= 2 ? 512 : 1024) rmsnorm_kernel(const Norm
                 if (p.r) b[i] = row_load(p.r, row, v);
             }
         }
+        if constexpr (!ALIGNED) gains_load(p, row, gains_next);
     };
     const unsigned T = p.T;  // (unsigned: a step behind the last row may pass 2^31)
     unsigned t = blockIdx.x;
     if (AHEAD && t < T) fetch(t);
     for (; t < T; t += gridDim.x) {
         if (!AHEAD) fetch(t);
-        const RowSpan row(t, p.D);
+        const RowSpan row(t, p.T, p.D);
         uint4 s[V];
+        if constexpr (!ALIGNED) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) gains[i] = gains_next[i];
+        }
         float sum[1] = {0.0f};
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -224,9 +226,9 @@ __global__ void __launch_bounds__(V <= 2 ? 512 : 1024) rmsnorm_kernel(const Norm
         block_reduce(sum, part[turn], Add{});
         turn ^= 1;
         const float rstd = 1.0f / sqrtf(sum[0] / static_cast<float>(p.D) + p.eps);
-        auto value = [&](int i, int v, float (&y)[8]) {
+        auto value = [&](int i, float (&y)[8]) {
             float g[8];
-            gains.get(p, row, i, v, g);
+            unpack8(gains[i], g);
             unpack8(s[i], y);
 #pragma unroll
             for (int j = 0; j < 8; ++j) y[j] = y[j] * rstd * g[j];
@@ -237,7 +239,7 @@ __global__ void __launch_bounds__(V <= 2 ? 512 : 1024) rmsnorm_kernel(const Norm
                 const int v = threadIdx.x + i * blockDim.x;
                 if (v >= row.vecs) break;
                 float y[8];
-                value(i, v, y);
+                value(i, y);
                 row_store(p.y, row, v, pack8(y));
             }
         } else {
@@ -247,7 +249,7 @@ __global__ void __launch_bounds__(V <= 2 ? 512 : 1024) rmsnorm_kernel(const Norm
                 const int v = threadIdx.x + i * blockDim.x;
                 if (v >= row.vecs) break;
                 float y[8];
-                value(i, v, y);
+                value(i, y);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const int c = row.col(v) + j;
@@ -267,7 +269,7 @@ __global__ void __launch_bounds__(V <= 2 ? 512 : 1024) rmsnorm_kernel(const Norm
                 const int v = threadIdx.x + i * blockDim.x;
                 if (v >= row.vecs) break;
                 float y[8];
-                value(i, v, y);
+                value(i, y);
                 uint32_t w[2] = {0u, 0u};
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -314,11 +316,11 @@ __global__ void __launch_bounds__(V <= 2 ? 512 : 1024) rmsnorm_backward_kernel(c
         for (int j = 0; j < 8; ++j) own[i][j] = 0.0f;
     grid_dependency_wait();
     grid_launch_dependents();
-    const Gains<V, ALIGNED> gains(p);
     int turn = 0;
-    uint4 s[V], dy[V], ds[V];
+    uint4 s[V], dy[V], ds[V], gains[V], gains_next[ALIGNED ? 1 : V];
+    if (ALIGNED) gains_load(p, RowSpan(0, p.T, p.D), gains);
     auto fetch = [&](unsigned t, uint4 (&s)[V], uint4 (&dy)[V], uint4 (&ds)[V]) {
-        const RowSpan row(t, p.D);
+        const RowSpan row(t, p.T, p.D);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int v = threadIdx.x + i * blockDim.x;
@@ -329,12 +331,17 @@ __global__ void __launch_bounds__(V <= 2 ? 512 : 1024) rmsnorm_backward_kernel(c
                 if (p.ds) ds[i] = row_load(p.ds, row, v);
             }
         }
+        if constexpr (!ALIGNED) gains_load(p, row, gains_next);
     };
     const unsigned T = p.T;
     unsigned t = blockIdx.x;
     if (t < T) fetch(t, s, dy, ds);
     for (; t < T; t += gridDim.x) {
-        const RowSpan row(t, p.D);
+        const RowSpan row(t, p.T, p.D);
+        if constexpr (!ALIGNED) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) gains[i] = gains_next[i];
+        }
         float both[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -343,7 +350,7 @@ __global__ void __launch_bounds__(V <= 2 ? 512 : 1024) rmsnorm_backward_kernel(c
             float fs[8], fd[8], g[8];
             unpack8(s[i], fs);
             unpack8(dy[i], fd);
-            gains.get(p, row, i, v, g);
+            unpack8(gains[i], g);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 both[0] = fmaf(fs[j], fs[j], both[0]);
@@ -364,7 +371,7 @@ __global__ void __launch_bounds__(V <= 2 ? 512 : 1024) rmsnorm_backward_kernel(c
             float fs[8], fd[8], g[8], o[8];
             unpack8(s[i], fs);
             unpack8(dy[i], fd);
-            gains.get(p, row, i, v, g);
+            unpack8(gains[i], g);
             unpack8(ds[i], o);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -522,10 +529,10 @@ static pgemm_status norm_backward(int T, int D, const uint16_t *S, const uint16_
         constexpr int V = decltype(v)::value;
         constexpr bool A = decltype(aligned)::value;
         constexpr GainSum SUM = A && V <= 2 ? GainSum::REGISTERS : GainSum::SHARED;
-        // blocks of an SM: what registers and shared memory allow, four at most, since each
-        // leaves a row of sums behind
+        // blocks of an SM: what registers and shared memory allow, eight at most, since
+        // each leaves a row of sums behind
         const int smem = dgain && SUM == GainSum::SHARED ? (D + 7) / 8 * 32 : 0;
-        int per_sm = threads <= 256 ? 4 : 1024 / threads;
+        int per_sm = threads <= 128 ? 8 : 1024 / threads;
         while (per_sm > 1 && per_sm * (smem + 2048) > kSmemPerSm) --per_sm;
         const int most = dev.sm_count * per_sm;
         const int blocks = T < most ? T : most;

@@ -480,9 +480,8 @@ static pgemm_status expert_sort_run(int T, int E, int k, const int32_t *experts,
 
 // ----------------------------------------------------- gather and combine ---
 // Rows as vectors of W bf16 values: 8 where rows are multiples of 16 bytes, else 2 or 1
-// (a token's row and its sorted rows then start at different places of a vector).  Gather
-// and combine take the vectors of all tokens in turn, a thread one of them, so that every
-// thread has one whatever the width; the k sorted rows' travel together.
+// (a token's row and its sorted rows then start at different places of a vector).  The k
+// sorted rows of a token travel together.
 struct RowsParams {
     int T, k, D;
     long long rows;  // T k: a slot_row outside [0, rows) does not count
@@ -583,50 +582,123 @@ __global__ void __launch_bounds__(kRowsThreads) gather_kernel(const RowsParams p
     }
 }
 
+// Rows of whole 16-byte vectors: a vector of all tokens' a thread, and its next one's choices
+// looked up while this one's rows travel.  On twice as many blocks as run at once (four an
+// SM): 8192 tokens, four rows of 4096 values, 65 us; on five an SM 80, a block for every 256
+// vectors 69.
 template <int W>
-__global__ void __launch_bounds__(kRowsThreads) combine_kernel(const RowsParams p) {
+__global__ void __launch_bounds__(kRowsThreads) combine_flat_kernel(const RowsParams p) {
     using V = typename Vec<W>::T;
     grid_dependency_wait();
     grid_launch_dependents();
     const unsigned vecs = p.D / W;
     const unsigned long long total = static_cast<unsigned long long>(p.T) * vecs;
-    for (unsigned long long i = blockIdx.x * static_cast<unsigned long long>(kRowsThreads) + threadIdx.x;
-         i < total; i += static_cast<unsigned long long>(gridDim.x) * kRowsThreads) {
-        const RowsAt at(i, vecs);
-        const int32_t *from = p.slot_row + at.t * p.k;
-        const float *w = p.weights ? p.weights + at.t * p.k : nullptr;
+    const unsigned long long step = static_cast<unsigned long long>(gridDim.x) * kRowsThreads;
+    unsigned long long i = blockIdx.x * static_cast<unsigned long long>(kRowsThreads) + threadIdx.x;
+    if (i >= total) return;
+    RowsAt at(i, vecs);
+    int r[kAhead];
+    auto look_up = [&](const RowsAt &a, int j0) {
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) r[j] = j0 + j < p.k ? p.slot_row[a.t * p.k + j0 + j] : -1;
+    };
+    look_up(at, 0);
+    while (true) {
         float sum[W];
+        V res = vec_zero<W>();
+        if (p.x) res = reinterpret_cast<const V *>(p.x)[i];
 #pragma unroll
         for (int c = 0; c < W; ++c) sum[c] = 0.0f;
+        const unsigned long long next = i + step;
+        const RowsAt after(next < total ? next : i, vecs);
         for (int j0 = 0; j0 < p.k; j0 += kAhead) {
             V y[kAhead];
-            int r[kAhead];
+            bool in[kAhead];
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
-                r[j] = j0 + j < p.k ? from[j0 + j] : -1;
-                if (r[j] >= p.rows) r[j] = -1;
-            }
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j)
-                if (r[j] >= 0)
+                in[j] = r[j] >= 0 && r[j] < p.rows;
+                if (in[j])
                     y[j] = reinterpret_cast<const V *>(p.ys + static_cast<long long>(r[j]) * p.D)[at.v];
+            }
+            if (j0 + kAhead < p.k)
+                look_up(at, j0 + kAhead);
+            else
+                look_up(after, 0);
+            const float *w = p.weights ? p.weights + at.t * p.k + j0 : nullptr;
 #pragma unroll
             for (int j = 0; j < kAhead; ++j)
-                if (r[j] >= 0) {
-                    const float wj = w ? w[j0 + j] : 1.0f;
+                if (in[j]) {
+                    const float wj = w ? w[j] : 1.0f;
                     float f[W];
                     vec_get<W>(y[j], f);
 #pragma unroll
                     for (int c = 0; c < W; ++c) sum[c] = fmaf(wj, f[c], sum[c]);
                 }
         }
-        if (p.x) {
-            float f[W];
-            vec_get<W>(reinterpret_cast<const V *>(p.x)[i], f);
+        float f[W];
+        vec_get<W>(res, f);
 #pragma unroll
-            for (int c = 0; c < W; ++c) sum[c] += f[c];
-        }
+        for (int c = 0; c < W; ++c) sum[c] += f[c];
         reinterpret_cast<V *>(p.out)[i] = vec_put<W>(sum);
+        if (next >= total) break;
+        i = next;
+        at = after;
+    }
+}
+
+// Other rows: `per` threads a token, as many as it has vectors up to a block's, so that where
+// they lie is worked out once for all of a thread's.
+template <int W>
+__global__ void __launch_bounds__(kRowsThreads) combine_kernel(const RowsParams p, int per) {
+    using V = typename Vec<W>::T;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int groups = blockDim.x / per;
+    const unsigned vecs = p.D / W;
+    for (long long t = blockIdx.x * static_cast<long long>(groups) + threadIdx.x / per; t < p.T;
+         t += static_cast<long long>(gridDim.x) * groups) {
+        const int32_t *from = p.slot_row + t * p.k;
+        const float *w = p.weights ? p.weights + t * p.k : nullptr;
+        const V *row[kAhead];
+        float weight[kAhead];
+        auto choices = [&](int j0) {
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const int r = j0 + j < p.k ? from[j0 + j] : -1;
+                const bool in = r >= 0 && r < p.rows;
+                row[j] = in ? reinterpret_cast<const V *>(p.ys + static_cast<long long>(r) * p.D)
+                            : nullptr;
+                weight[j] = in && w ? w[j0 + j] : 1.0f;
+            }
+        };
+        if (p.k <= kAhead) choices(0);
+        for (unsigned v = threadIdx.x % per; v < vecs; v += per) {
+            float sum[W];
+            V res = vec_zero<W>();
+            if (p.x) res = reinterpret_cast<const V *>(p.x + t * p.D)[v];
+#pragma unroll
+            for (int i = 0; i < W; ++i) sum[i] = 0.0f;
+            for (int j0 = 0; j0 < p.k; j0 += kAhead) {
+                if (p.k > kAhead) choices(j0);
+                V y[kAhead];
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j)
+                    if (row[j] != nullptr) y[j] = row[j][v];
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j)
+                    if (row[j] != nullptr) {
+                        float f[W];
+                        vec_get<W>(y[j], f);
+#pragma unroll
+                        for (int i = 0; i < W; ++i) sum[i] = fmaf(weight[j], f[i], sum[i]);
+                    }
+            }
+            float f[W];
+            vec_get<W>(res, f);
+#pragma unroll
+            for (int i = 0; i < W; ++i) sum[i] += f[i];
+            reinterpret_cast<V *>(p.out + t * p.D)[v] = vec_put<W>(sum);
+        }
     }
 }
 
@@ -789,10 +861,19 @@ static pgemm_status combine_run(int T, int k, int D, const uint16_t *Ys, const i
     p.ys = Ys;
     p.weights = weights;
     p.out = Y;
+    const int vecs = D / rows_width(D);
+    const int per = vecs < kRowsThreads ? op_blocks(vecs, 32) * 32 : kRowsThreads;
+    const int groups = kRowsThreads / per;
     return with_width(D, [&](auto w) {
-        return launch_small(combine_kernel<decltype(w)::value>,
-                            vectors_grid(T, D),
-                            dim3(kRowsThreads), s, p);
+        constexpr int W = decltype(w)::value;
+        if constexpr (W == 8) {
+            const unsigned all = vectors_grid(T, D).x, most = 8u * dev.sm_count;
+            return launch_small(combine_flat_kernel<W>, dim3(all < most ? all : most),
+                                dim3(kRowsThreads), s, p);
+        } else {
+            return launch_small(combine_kernel<W>, dim3(op_blocks(T, groups)), dim3(per * groups),
+                                s, p, per);
+        }
     });
 }
 
