@@ -202,6 +202,11 @@ __device__ __forceinline__ RowsUnit rows_unit(const ExpertsTable &t, const Exper
     return w;
 }
 
+__device__ __forceinline__ RowsUnit warp_unit(const RowsUnit &w) {
+    return RowsUnit{warp_value(w.expert), warp_value(w.row0), warp_value(w.rows),
+                    warp_value(w.cols), warp_value(w.f0)};
+}
+
 __device__ __forceinline__ void put_bf16(uint16_t *p, float v) {
     *p = static_cast<uint16_t>(pack_bf16(v, 0.0f) & 0xffffu);
 }
@@ -258,122 +263,112 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     const ExpertsTable table =
         experts_table(a, smem + Cfg::TABLE_OFFSET,
                       [&](int rows) { return row_tiles<Cfg>(rows) * a.f_tiles; });
-    const int units = table.units();
+    const int units = warp_value(table.units());
     const int crank = CG == 2 ? static_cast<int>(cluster_ctarank()) : 0;
     const int slot = static_cast<int>(blockIdx.x) / CG;
     const int slots = static_cast<int>(gridDim.x) / CG;
 
+    // The first two warps run as one each, with one lane's instructions (see warp_value).
+    const uint32_t lead = lane == 0 ? 1u : 0u;
     if (warp == 0) {
-        if (lane == 0) {
-            // ---------------- producer ----------------
-            Ring<STAGES> ring;
-            bool ok = true;
-            RowsUnit next = slot < units ? rows_unit<Cfg>(table, a, slot) : RowsUnit{};
-            for (int u = slot; ok && u < units; u += slots) {
-                const RowsUnit w = next;
-                const int half = w.cols / CG;  // columns of B in this CTA
-                const int boxes = (half + Cfg::BOX - 1) / Cfg::BOX;  // 1 .. 4
-                const int box = boxes == 4 ? 0 : boxes >= 2 ? 1 : 2;
-                // (may pass 2^31 where the rows have ended: zero fill either way)
-                const int y0 = static_cast<int>(static_cast<uint32_t>(w.row0) + crank * half);
-                const uint32_t tx = CG * (Cfg::A_BYTES + boxes * Cfg::BOX * BK * 2);
-                const int f0 = w.f0 + crank * Cfg::FEATS;
-                const int segments = a.k_tiles > a.k_seg ? 2 : 1;
-                for (int sg = 0; ok && sg < segments; ++sg) {
-                    const CUtensorMap *mx = &maps.x[sg][box], *mw = &maps.w[sg];
-                    for (int left = a.K; left > 0; left -= BK, ring.next()) {
-                        const int k0 = a.K - left;
-                        const uint32_t s = ring.s;
-                        if (!mbar_wait(&empty[s], ring.phase ^ 1u, ctx, kSiteProducerEmpty)) {
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t lead =
-                            CG == 2 ? mapa_shared(smem_u32(&full[s]), 0) : smem_u32(&full[s]);
-                        if (crank == 0) mbar_arrive_expect_tx(&full[s], tx);
-                        auto load_w = [&](uint8_t *dst, const CUtensorMap *map, int x, int y) {
-                            if constexpr (CG == 2)
-                                tma_load_3d_pair(dst, map, lead, x, y, w.expert);
-                            else
-                                tma_load_3d(dst, map, &full[s], x, y, w.expert);
-                        };
-                        auto load_x = [&](uint8_t *dst, const CUtensorMap *map, int x, int y) {
-                            if constexpr (CG == 2)
-                                tma_load_2d_pair(dst, map, lead, x, y);
-                            else
-                                tma_load_2d(dst, map, &full[s], x, y);
-                        };
-                        uint8_t *da = sA + s * Cfg::A_BYTES, *db = sB + s * Cfg::B_BYTES;
-                        if constexpr (Cfg::W_K) {
-#pragma unroll
-                            for (int q = 0; q < BK / 64; ++q)
-                                load_w(da + q * 16384, mw, k0 + 64 * q, f0);
-                        } else {
-                            load_w(da, &maps.w[0], f0, k0);
-                            load_w(da + BK * 128, &maps.w[Cfg::DUAL ? 1 : 0],
-                                   Cfg::DUAL ? f0 : f0 + 64, k0);
-                        }
+        // ---------------- producer ----------------
+        Ring<STAGES> ring;
+        bool ok = true;
+        const uint32_t full0 = smem_u32(full);
+        const uint32_t full_lead = CG == 2 ? warp_value(mapa_shared(full0, 0)) : full0;
+        const uint32_t first = crank == 0 ? lead : 0u;
+        const int segments = a.k_tiles > a.k_seg ? 2 : 1;
+        RowsUnit next = warp_unit(slot < units ? rows_unit<Cfg>(table, a, slot) : RowsUnit{});
+        for (int u = slot; u < units; u += slots) {
+            const RowsUnit w = next;
+            const int half = w.cols / CG;  // columns of B in this CTA
+            const int boxes = (half + Cfg::BOX - 1) / Cfg::BOX;  // 1 .. 4
+            const int box = boxes == 4 ? 0 : boxes >= 2 ? 1 : 2;
+            // (may pass 2^31 where the rows have ended: zero fill either way)
+            const int y0 = static_cast<int>(static_cast<uint32_t>(w.row0) + crank * half);
+            const uint32_t tx = CG * (Cfg::A_BYTES + boxes * Cfg::BOX * BK * 2);
+            const int f0 = w.f0 + crank * Cfg::FEATS;
+            for (int sg = 0; sg < segments; ++sg) {
+                const CUtensorMap *mx = &maps.x[sg][box], *mw = &maps.w[sg];
+                for (int left = a.K; left > 0; left -= BK, ring.next()) {
+                    const int k0 = a.K - left;
+                    const uint32_t s = ring.s;
+                    if (ok)
+                        ok = warp_value(mbar_wait(&empty[s], ring.phase ^ 1u, ctx,
+                                                  kSiteProducerEmpty)) != 0;
+                    const uint32_t go = ok ? lead : 0u;  // (after a failure nothing is issued)
+                    const uint32_t bar = full_lead + s * 8;
+                    mbar_arrive_expect_tx_if(ok ? first : 0u, full0 + s * 8, tx);
+                    const uint32_t da = smem_u32(sA) + s * Cfg::A_BYTES;
+                    const uint32_t db = smem_u32(sB) + s * Cfg::B_BYTES;
+                    if constexpr (Cfg::W_K) {
 #pragma unroll
                         for (int q = 0; q < BK / 64; ++q)
-                            load_x(db + q * Cfg::B_SUB, mx, k0 + 64 * q, y0);
-                        if (boxes == 3) {
-#pragma unroll
-                            for (int q = 0; q < BK / 64; ++q)
-                                load_x(db + q * Cfg::B_SUB + 2 * Cfg::BOX * 128, &maps.x[sg][2],
-                                       k0 + 64 * q, y0 + 2 * Cfg::BOX);
-                        }
+                            tma_load_3d_if<CG>(go, da + q * 16384, mw, bar, k0 + 64 * q, f0,
+                                               w.expert);
+                    } else {
+                        tma_load_3d_if<CG>(go, da, &maps.w[0], bar, f0, k0, w.expert);
+                        tma_load_3d_if<CG>(go, da + BK * 128, &maps.w[Cfg::DUAL ? 1 : 0], bar,
+                                           Cfg::DUAL ? f0 : f0 + 64, k0, w.expert);
                     }
-                    // (found while these copies travel)
-                    if (sg == 0 && u + slots < units)
-                        next = rows_unit<Cfg>(table, a, u + slots);
+#pragma unroll
+                    for (int q = 0; q < BK / 64; ++q)
+                        tma_load_2d_if<CG>(go, db + q * Cfg::B_SUB, mx, bar, k0 + 64 * q, y0);
+                    if (boxes == 3) {
+#pragma unroll
+                        for (int q = 0; q < BK / 64; ++q)
+                            tma_load_2d_if<CG>(go, db + q * Cfg::B_SUB + 2 * Cfg::BOX * 128,
+                                               &maps.x[sg][2], bar, k0 + 64 * q,
+                                               y0 + 2 * Cfg::BOX);
+                    }
                 }
-            }
-            if constexpr (CG == 2) {
-                // the pair's last multicast releases of this CTA's barriers must
-                // have landed before the cluster is left
-                for (int i = 0; ok && i < STAGES; ++i, ring.next())
-                    ok = mbar_wait(&empty[ring.s], ring.phase ^ 1u, ctx, kSiteProducerEmpty);
+                // (found while these copies travel)
+                if (sg == 0 && u + slots < units)
+                    next = warp_unit(rows_unit<Cfg>(table, a, u + slots));
             }
         }
+        if constexpr (CG == 2) {
+            // the pair's last multicast releases of this CTA's barriers must
+            // have landed before the cluster is left
+            for (int i = 0; ok && i < STAGES; ++i, ring.next())
+                ok = warp_value(mbar_wait(&empty[ring.s], ring.phase ^ 1u, ctx,
+                                          kSiteProducerEmpty)) != 0;
+        }
     } else if (warp == 1) {
-        if (lane == 0 && crank == 0) {
+        if (crank == 0) {
             // ---------------- MMA issuer ----------------
             constexpr uint16_t kPair = 3;
             // descriptors of the first stage; addresses count in 16 bytes
             const uint64_t a0 = smem_desc_sw128(smem_u32(sA), Cfg::W_K ? 16 : BK * 128, 1024);
             const uint64_t b0 = smem_desc_sw128(smem_u32(sB), 16, 1024);
+            const uint32_t tmem_w = warp_value(tmem);
             Ring<STAGES> ring;
             uint32_t n = 0;
             bool ok = true;
-            int cols = slot < units ? rows_unit<Cfg>(table, a, slot).cols : 0, next = 0;
-            for (int u = slot; ok && u < units && a.k_tiles > 0; u += slots, ++n, cols = next) {
+            int cols = warp_value(slot < units ? rows_unit<Cfg>(table, a, slot).cols : 0), next = 0;
+            for (int u = slot; u < units && a.k_tiles > 0; u += slots, ++n, cols = next) {
                 const uint32_t idesc =
                     idesc_f16(Cfg::BM * CG, cols, 1, Cfg::W_K ? 0 : 1, /*B K-major*/ 0);
                 const uint32_t ab = n & 1u;
-                if (!mbar_wait(&acc_empty[ab], ((n >> 1) & 1u) ^ 1u, ctx, kSiteMmaAccEmpty)) {
-                    ok = false;
-                    break;
-                }
+                if (ok)
+                    ok = warp_value(mbar_wait(&acc_empty[ab], ((n >> 1) & 1u) ^ 1u, ctx,
+                                              kSiteMmaAccEmpty)) != 0;
                 tc_fence_after();
-                const uint32_t d = tmem + ab * TOK;
+                const uint32_t d = tmem_w + ab * TOK;
                 int left = a.K;  // of the segment
                 uint32_t acc = 0;
                 for (int kt = 0; kt < a.k_tiles; ++kt, ring.next()) {
                     const uint32_t s = ring.s;
-                    if (!mbar_wait(&full[s], ring.phase, ctx, kSiteMmaFull)) {
-                        ok = false;
-                        break;
-                    }
+                    if (ok)
+                        ok = warp_value(mbar_wait(&full[s], ring.phase, ctx, kSiteMmaFull)) != 0;
+                    const uint32_t go = ok ? lead : 0u;
                     tc_fence_after();
                     const uint64_t as = a0 + s * (Cfg::A_BYTES / 16), bs = b0 + s * (Cfg::B_BYTES / 16);
                     auto multiply = [&](int k) {
-                        const uint64_t ad =
-                            as + (Cfg::W_K ? k / 4 * 16384 + k % 4 * 32 : k * 2048) / 16;
-                        const uint64_t bd = bs + (k / 4 * Cfg::B_SUB + k % 4 * 32) / 16;
-                        if constexpr (CG == 2)
-                            umma_f16_ss_pair(d, ad, bd, idesc, acc);
-                        else
-                            umma_f16_ss(d, ad, bd, idesc, acc);
+                        umma_f16_ss_if<CG>(
+                            go, d,
+                            as + (Cfg::W_K ? k / 4 * 16384 + k % 4 * 32 : k * 2048) / 16,
+                            bs + (k / 4 * Cfg::B_SUB + k % 4 * 32) / 16, idesc, acc);
                         acc = 1;
                     };
                     if (left >= BK) {
@@ -386,26 +381,16 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                         left = 0;
                     }
                     if (left == 0) left = a.K;
-                    if constexpr (CG == 2)
-                        umma_commit_pair_multicast(&empty[s], kPair);
-                    else
-                        umma_commit(&empty[s]);
+                    umma_commit_if<CG>(go, smem_u32(&empty[s]), kPair);
                     // (found while these products run)
                     if (kt == 0 && u + slots < units)
-                        next = rows_unit<Cfg>(table, a, u + slots).cols;
+                        next = warp_value(rows_unit<Cfg>(table, a, u + slots).cols);
                 }
-                if (ok) {
-                    if constexpr (CG == 2)
-                        umma_commit_pair_multicast(&acc_full[ab], kPair);
-                    else
-                        umma_commit(&acc_full[ab]);
-                }
+                umma_commit_if<CG>(ok ? lead : 0u, smem_u32(&acc_full[ab]), kPair);
             }
-            if constexpr (CG == 2)
-                umma_commit_pair_multicast(mma_done, 1);
-            else
-                umma_commit(mma_done);
+            umma_commit_if<CG>(lead, smem_u32(mma_done), 1);
             mbar_wait(mma_done, 0, ctx, kSiteMmaDone);
+            __syncwarp();
         }
     } else {
         // ---------------- epilogue ----------------
@@ -633,8 +618,8 @@ __device__ __forceinline__ WeightsUnit weights_unit(const ExpertsArgs &a, int u)
     WeightsUnit w;
     const int n_tiles = a.n_seg * a.segments, per = a.f_tiles * n_tiles;
     w.expert = u / per;
-    w.begin = min(max(a.offsets[w.expert], 0), a.R);
-    w.end = min(max(a.offsets[w.expert + 1], w.begin), a.R);
+    w.begin = warp_value(min(max(a.offsets[w.expert], 0), a.R));
+    w.end = warp_value(min(max(a.offsets[w.expert + 1], w.begin), a.R));
     const int r = u - w.expert * per;
     const int group = r / (8 * n_tiles), first = group * 8;
     const int g = min(a.f_tiles - first, 8), q = r - group * 8 * n_tiles;
@@ -755,61 +740,66 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     const int units = a.E * a.f_tiles * a.n_seg * a.segments;
     const int slot = static_cast<int>(blockIdx.x) / 2, slots = static_cast<int>(gridDim.x) / 2;
 
+    // The first two warps run as one each, with one lane's instructions (see warp_value).
+    const uint32_t lead = lane == 0 ? 1u : 0u;
     if (warp == 0) {
-        if (lane == 0) {
-            // ---------------- producer ----------------
-            Ring<STAGES> ring;
-            uint32_t tails = 0;
-            bool ok = true;
-            for (int u = slot; ok && u < units; u += slots) {
-                const WeightsUnit w = weights_unit<Cfg>(a, u);
-                const CUtensorMap *mx = maps.x, *mz = maps.z[w.seg];
-                const int ma = w.m0 + crank * BM, nb = w.n0 + crank * (BN / 2);
-                const int whole = w.whole();
-                if (whole < w.end) {
-                    const uint32_t b = tails & 1u;
-                    if (!mbar_wait(&tail_empty[b], ((tails >> 1) & 1u) ^ 1u, ctx, kSiteGroupTail)) {
-                        ok = false;
-                        break;
-                    }
-                    ++tails;
-                    uint8_t *d = smem + Cfg::TAIL_OFFSET + b * Cfg::TAIL_BYTES;
-                    mbar_arrive_expect_tx(&tail_full[b], Cfg::TAIL_BYTES);
+        // ---------------- producer ----------------
+        Ring<STAGES> ring;
+        uint32_t tails = 0;
+        bool ok = true;
+        const uint32_t full0 = smem_u32(full);
+        const uint32_t full_lead = warp_value(mapa_shared(full0, 0));
+        const uint32_t first = crank == 0 ? lead : 0u;
+        for (int u = slot; u < units; u += slots) {
+            const WeightsUnit w = weights_unit<Cfg>(a, u);
+            const CUtensorMap *mx = maps.x, *mz = maps.z[w.seg];
+            const int ma = w.m0 + crank * BM, nb = w.n0 + crank * (BN / 2);
+            const int whole = w.whole();
+            if (whole < w.end) {
+                const uint32_t b = tails & 1u;
+                if (ok)
+                    ok = warp_value(mbar_wait(&tail_empty[b], ((tails >> 1) & 1u) ^ 1u, ctx,
+                                              kSiteGroupTail)) != 0;
+                ++tails;
+                const uint32_t go = ok ? lead : 0u;  // (after a failure nothing is issued)
+                const uint32_t d = smem_u32(smem + Cfg::TAIL_OFFSET) + b * Cfg::TAIL_BYTES;
+                const uint32_t bar = smem_u32(&tail_full[b]);
+                mbar_arrive_expect_tx_if(go, bar, Cfg::TAIL_BYTES);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        tma_load_2d(d + j * 2048, &mx[3], &tail_full[b], ma + 64 * j, whole);
-                        tma_load_2d(d + Cfg::TAIL_HALF + j * 2048, &mz[3], &tail_full[b],
-                                    nb + 64 * j, whole);
-                    }
-                }
-                for (int left = whole - w.begin; left > 0; left -= BK, ring.next()) {
-                    const int y = whole - left;
-                    const uint32_t s = ring.s;
-                    if (!mbar_wait(&empty[s], ring.phase ^ 1u, ctx, kSiteProducerEmpty)) {
-                        ok = false;
-                        break;
-                    }
-                    uint8_t *da = sA + s * Cfg::A_BYTES, *db = sB + s * Cfg::B_BYTES;
-                    const uint32_t lead = mapa_shared(smem_u32(&full[s]), 0);
-                    // a box of 96 rows, in a last step perhaps of 64 or 32
-                    const int thirds = left > 64 ? 3 : (left + 31) / 32;
-                    if (crank == 0)
-                        mbar_arrive_expect_tx(&full[s], thirds * (2 * Cfg::STAGE_BYTES / 3));
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        tma_load_2d_pair(da + j * (BK * 128), &mx[3 - thirds], lead, ma + 64 * j, y);
-                        tma_load_2d_pair(db + j * (BK * 128), &mz[3 - thirds], lead, nb + 64 * j, y);
-                    }
+                for (int j = 0; j < 2; ++j) {
+                    tma_load_2d_if<1>(go, d + j * 2048, &mx[3], bar, ma + 64 * j, whole);
+                    tma_load_2d_if<1>(go, d + Cfg::TAIL_HALF + j * 2048, &mz[3], bar, nb + 64 * j,
+                                      whole);
                 }
             }
-            // the pair's last multicast releases of this CTA's barriers must have landed
-            // before the cluster is left
-            for (int i = 0; ok && i < STAGES; ++i, ring.next())
-                ok = mbar_wait(&empty[ring.s], ring.phase ^ 1u, ctx, kSiteProducerEmpty);
-            for (int i = 0; ok && i < 2; ++i, ++tails)
-                ok = mbar_wait(&tail_empty[tails & 1u], ((tails >> 1) & 1u) ^ 1u, ctx,
-                               kSiteGroupTail);
+            for (int left = whole - w.begin; left > 0; left -= BK, ring.next()) {
+                const int y = whole - left;
+                const uint32_t s = ring.s;
+                if (ok)
+                    ok = warp_value(mbar_wait(&empty[s], ring.phase ^ 1u, ctx,
+                                              kSiteProducerEmpty)) != 0;
+                const uint32_t go = ok ? lead : 0u;
+                const uint32_t da = smem_u32(sA) + s * Cfg::A_BYTES;
+                const uint32_t db = smem_u32(sB) + s * Cfg::B_BYTES;
+                const uint32_t bar = full_lead + s * 8;
+                // a box of 96 rows, in a last step perhaps of 64 or 32
+                const int thirds = left > 64 ? 3 : (left + 31) / 32;
+                mbar_arrive_expect_tx_if(ok ? first : 0u, full0 + s * 8,
+                                         thirds * (2 * Cfg::STAGE_BYTES / 3));
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    tma_load_2d_if<2>(go, da + j * (BK * 128), &mx[3 - thirds], bar, ma + 64 * j, y);
+                    tma_load_2d_if<2>(go, db + j * (BK * 128), &mz[3 - thirds], bar, nb + 64 * j, y);
+                }
+            }
         }
+        // the pair's last multicast releases of this CTA's barriers must have landed
+        // before the cluster is left
+        for (int i = 0; ok && i < STAGES; ++i, ring.next())
+            ok = warp_value(mbar_wait(&empty[ring.s], ring.phase ^ 1u, ctx, kSiteProducerEmpty)) != 0;
+        for (int i = 0; ok && i < 2; ++i, ++tails)
+            ok = warp_value(mbar_wait(&tail_empty[tails & 1u], ((tails >> 1) & 1u) ^ 1u, ctx,
+                                      kSiteGroupTail)) != 0;
     } else if (warp == Cfg::THREADS / 32 - 1) {
         // ---------------- the groups' last rows ----------------
         uint32_t tails = 0;
@@ -836,38 +826,37 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             __syncwarp();
         }
     } else if (warp == 1) {
-        if (lane == 0 && crank == 0) {
+        if (crank == 0) {
             // ---------------- MMA issuer ----------------
             constexpr uint16_t kPair = 3;
             constexpr uint32_t idesc = idesc_f16(BM * 2, BN, 1, 1, 1);
             const uint64_t a0 = smem_desc_sw128(smem_u32(sA), BK * 128, 1024);
             const uint64_t b0 = smem_desc_sw128(smem_u32(sB), BK * 128, 1024);
+            const uint32_t tmem_w = warp_value(tmem);
             Ring<STAGES> ring;
             uint32_t n = 0, tails = 0;
             bool ok = true;
-            for (int u = slot; ok && u < units; u += slots) {
+            for (int u = slot; u < units; u += slots) {
                 const WeightsUnit w = weights_unit<Cfg>(a, u);
                 if (w.end <= w.begin) continue;
                 const uint32_t ab = n & 1u;
-                if (!mbar_wait(&acc_empty[ab], ((n >> 1) & 1u) ^ 1u, ctx, kSiteMmaAccEmpty)) {
-                    ok = false;
-                    break;
-                }
+                if (ok)
+                    ok = warp_value(mbar_wait(&acc_empty[ab], ((n >> 1) & 1u) ^ 1u, ctx,
+                                              kSiteMmaAccEmpty)) != 0;
                 ++n;
                 tc_fence_after();
-                const uint32_t d = tmem + ab * BN;
+                const uint32_t d = tmem_w + ab * BN;
                 const int whole = w.whole();
                 uint32_t acc = 0;
                 for (int left = whole - w.begin; left > 0; left -= BK, ring.next()) {
                     const uint32_t s = ring.s;
-                    if (!mbar_wait(&full[s], ring.phase, ctx, kSiteMmaFull)) {
-                        ok = false;
-                        break;
-                    }
+                    if (ok)
+                        ok = warp_value(mbar_wait(&full[s], ring.phase, ctx, kSiteMmaFull)) != 0;
+                    const uint32_t go = ok ? lead : 0u;
                     tc_fence_after();
                     const uint64_t as = a0 + s * (Cfg::A_BYTES / 16), bs = b0 + s * (Cfg::B_BYTES / 16);
                     auto multiply = [&](int k) {
-                        umma_f16_ss_pair(d, as + k * 128, bs + k * 128, idesc, acc);
+                        umma_f16_ss_if<2>(go, d, as + k * 128, bs + k * 128, idesc, acc);
                         acc = 1;
                     };
                     if (left >= BK) {
@@ -877,25 +866,25 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 #pragma unroll 1
                         for (int k = 0; 16 * k < left; ++k) multiply(k);
                     }
-                    umma_commit_pair_multicast(&empty[s], kPair);
+                    umma_commit_if<2>(go, smem_u32(&empty[s]), kPair);
                 }
-                if (ok && whole < w.end) {
+                if (whole < w.end) {
                     const uint32_t b = tails & 1u;
-                    if (!mbar_wait(&tail_ready[b], (tails >> 1) & 1u, ctx, kSiteGroupTail)) {
-                        ok = false;
-                        break;
-                    }
+                    if (ok)
+                        ok = warp_value(mbar_wait(&tail_ready[b], (tails >> 1) & 1u, ctx,
+                                                  kSiteGroupTail)) != 0;
                     ++tails;
                     tc_fence_after();
-                    const uint32_t st = smem_u32(smem + Cfg::TAIL_OFFSET + b * Cfg::TAIL_BYTES);
-                    umma_f16_ss_pair(d, smem_desc_sw128(st, 2048, 1024),
-                                     smem_desc_sw128(st + Cfg::TAIL_HALF, 2048, 1024), idesc, acc);
-                    umma_commit_pair_multicast(&tail_empty[b], kPair);
+                    const uint32_t st = smem_u32(smem + Cfg::TAIL_OFFSET) + b * Cfg::TAIL_BYTES;
+                    umma_f16_ss_if<2>(ok ? lead : 0u, d, smem_desc_sw128(st, 2048, 1024),
+                                      smem_desc_sw128(st + Cfg::TAIL_HALF, 2048, 1024), idesc, acc);
+                    umma_commit_if<2>(ok ? lead : 0u, smem_u32(&tail_empty[b]), kPair);
                 }
-                if (ok) umma_commit_pair_multicast(&acc_full[ab], kPair);
+                umma_commit_if<2>(ok ? lead : 0u, smem_u32(&acc_full[ab]), kPair);
             }
-            umma_commit_pair_multicast(mma_done, 1);
+            umma_commit_if<2>(lead, smem_u32(mma_done), 1);
             mbar_wait(mma_done, 0, ctx, kSiteMmaDone);
+            __syncwarp();
         }
     } else {
         // ---------------- epilogue ----------------
