@@ -605,7 +605,7 @@ struct ExpWeightsCfg {
     static constexpr int SMEM_BYTES = smem_request(USED + 1024, 1);
     static_assert(USED + 1024 <= 232448, "shared memory");
     static_assert(WIDE ? NBUF == EPI_COLS / 32 : EPI_COLS / 32 % NBUF == 0, "whole batches");
-    static_assert(BK == 96, "a step is a box of 96 rows, or shorter ones of 64 and 32");
+    static_assert(BK == 96 || BK == 64, "a step's rows are one box");
 };
 
 struct WeightsUnit {
@@ -783,13 +783,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 const uint32_t db = smem_u32(sB) + s * Cfg::B_BYTES;
                 const uint32_t bar = full_lead + s * 8;
                 // a box of 96 rows, in a last step perhaps of 64 or 32
-                const int thirds = left > 64 ? 3 : (left + 31) / 32;
+                const int box = BK == 96 && left > 64 ? 0 : left > 32 ? 1 : 2;
                 mbar_arrive_expect_tx_if(ok ? first : 0u, full0 + s * 8,
-                                         thirds * (2 * Cfg::STAGE_BYTES / 3));
+                                         (96 - 32 * box) * (2 * Cfg::STAGE_BYTES / BK));
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    tma_load_2d_if<2>(go, da + j * (BK * 128), &mx[3 - thirds], bar, ma + 64 * j, y);
-                    tma_load_2d_if<2>(go, db + j * (BK * 128), &mz[3 - thirds], bar, nb + 64 * j, y);
+                    tma_load_2d_if<2>(go, da + j * (BK * 128), &mx[box], bar, ma + 64 * j, y);
+                    tma_load_2d_if<2>(go, db + j * (BK * 128), &mz[box], bar, nb + 64 * j, y);
                 }
             }
         }
@@ -1193,7 +1193,7 @@ static pgemm_status rows_product(const OpDevice &dev, const ExpSizes &z, const O
         (z.R / 256 + live) * op_blocks(MODE == Exp::TRANSPOSED ? z.K : z.N,
                                        MODE == Exp::LINEAR || MODE == Exp::TRANSPOSED ? 256 : 128);
     if (z.R <= 24ll * z.E || 4 * pairs <= dev.sm_count) return rows_launch<ExpCfg<1, 64, 128, 4, MODE>>(dev, z, x, w, segments, a, s);
-    return rows_launch<ExpCfg<2, 256, 128, 3, MODE>>(dev, z, x, w, segments, a, s);
+    return rows_launch<ExpCfg<2, 256, 64, 6, MODE>>(dev, z, x, w, segments, a, s);
 }
 
 template <class Cfg>
@@ -1214,7 +1214,7 @@ static pgemm_status weights_launch(const OpDevice &dev, const ExpSizes &z, const
     a.tma_out = z.N % 8 == 0;
     a.overlap = overlap ? 1 : 0;
     ExpertsWeightsMaps maps{};
-    constexpr int kBoxes[4] = {Cfg::BK, 64, 32, 16};
+    constexpr int kBoxes[4] = {96, 64, 32, 16};
     pgemm_status st = PGEMM_OK;
     for (int b = 0; b < 4 && st == PGEMM_OK; ++b)
         st = op_encode(&maps.x[b], x.p, z.K, z.R, x.ld, kBoxes[b]);
