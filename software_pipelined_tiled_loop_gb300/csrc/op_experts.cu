@@ -975,11 +975,11 @@ struct RelayoutParams {
     long long ld, end;        // elements of a row of the copy, and of the source
     const int32_t *offsets;   // experts without rows stay uncopied (nullptr: all rows)
     unsigned expert_rows;     // matrix rows of an expert
+    int early;                // op_begin_early
 };
 
 __global__ void __launch_bounds__(256) relayout_kernel(const RelayoutParams p) {
-    grid_dependency_wait();
-    grid_launch_dependents();
+    op_begin_early(p.early);
     constexpr int AHEAD = 4;
     const unsigned long long first = blockIdx.x * (256ull * AHEAD) + threadIdx.x;
     uint4 lo[AHEAD], hi[AHEAD];
@@ -1043,7 +1043,7 @@ class ExpRelayout {
             jobs_[before].expert_rows = z.K;
         }
     }
-    pgemm_status run(OpArena &arena, cudaStream_t s) {
+    pgemm_status run(const OpDevice &dev, OpArena &arena, cudaStream_t s) {
         for (int i = 0; i < n_; ++i) {
             const Job &j = jobs_[i];
             RelayoutParams p{};
@@ -1060,6 +1060,7 @@ class ExpRelayout {
             j.out->ld = j.ld;
             const unsigned long long blocks = (p.vecs + 1023) / 1024;
             if (blocks > INT_MAX) return PGEMM_ERR_TOO_LARGE;
+            p.early = op_early(dev, static_cast<unsigned>(blocks));
             const pgemm_status st = launch_small(
                 relayout_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), s, p);
             if (st != PGEMM_OK) return st;
@@ -1268,7 +1269,7 @@ static pgemm_status experts_linear_forward(const ExpSizes &z, const uint16_t *X,
     rl.add(&x, X, z.R, z.K, arena);
     rl.add_weights(&w, W, z, arena);
     if ((st = arena.alloc()) != PGEMM_OK) return st;
-    if (z.K > 0 && (st = rl.run(arena, s)) != PGEMM_OK) return st;
+    if (z.K > 0 && (st = rl.run(dev, arena, s)) != PGEMM_OK) return st;
     ExpertsArgs a{};
     a.out = Y;
     a.ldo = z.N;
@@ -1300,7 +1301,7 @@ static pgemm_status experts_linear_backward(const ExpSizes &z, const uint16_t *X
         if (want_x) rl.add_weights(&w, W, z, arena);
     }
     if ((st = arena.alloc()) != PGEMM_OK) return st;
-    if ((st = rl.run(arena, s)) != PGEMM_OK) return st;
+    if ((st = rl.run(dev, arena, s)) != PGEMM_OK) return st;
     if (want_x) {
         ExpertsArgs a{};
         a.out = dX;
@@ -1336,7 +1337,7 @@ static pgemm_status experts_gated_forward(const ExpSizes &z, const uint16_t *X, 
     rl.add_weights(&w[0], Wg, z, arena);
     rl.add_weights(&w[1], Wu, z, arena);
     if ((st = arena.alloc()) != PGEMM_OK) return st;
-    if (z.K > 0 && (st = rl.run(arena, s)) != PGEMM_OK) return st;
+    if (z.K > 0 && (st = rl.run(dev, arena, s)) != PGEMM_OK) return st;
     ExpertsArgs a{};
     a.out = H;
     a.ldo = z.N;
@@ -1383,7 +1384,7 @@ static pgemm_status experts_gated_backward(const ExpSizes &z, const uint16_t *X,
     const long long dz_ld = op_round_up(z.N, 64);
     const long long at0 = arena.add(dz_ld * z.R * 2), at1 = arena.add(dz_ld * z.R * 2);
     if ((st = arena.alloc()) != PGEMM_OK) return st;
-    if ((st = rl.run(arena, s)) != PGEMM_OK) return st;
+    if ((st = rl.run(dev, arena, s)) != PGEMM_OK) return st;
     for (int j = 0; j < 2; ++j) dz[j] = OpMat{arena.at<uint16_t>(j ? at1 : at0), dz_ld};
     if (some && preact) {
         OpActGrad g;

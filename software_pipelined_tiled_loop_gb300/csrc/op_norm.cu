@@ -153,6 +153,7 @@ struct NormParams {
     const uint16_t *dy, *ds;
     uint16_t *dx;
     float *dgain;  // [blocks][D] partial sums, or nullptr
+    int early;     // op_begin_early
 };
 
 // The gains of a thread's vectors: where rows start on vectors the same for every row, else
@@ -173,8 +174,7 @@ template <int V, bool ALIGNED, bool I8>
 __global__ void __launch_bounds__(V <= 2 ? 512 : 1024) rmsnorm_kernel(const NormParams p) {
     __shared__ float part[2][1][32];
     constexpr bool AHEAD = V <= 2;
-    grid_dependency_wait();
-    grid_launch_dependents();
+    op_begin_early(p.early);
     int turn = 0;
     uint4 a[V], b[V], gains[V], gains_next[ALIGNED ? 1 : V];
     if (ALIGNED) gains_load(p, RowSpan(0, p.T, p.D), gains);
@@ -314,8 +314,7 @@ __global__ void __launch_bounds__(V <= 2 ? 512 : 1024) rmsnorm_backward_kernel(c
     for (int i = 0; i < (SUM == GainSum::REGISTERS ? V : 1); ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) own[i][j] = 0.0f;
-    grid_dependency_wait();
-    grid_launch_dependents();
+    op_begin_early(p.early);
     int turn = 0;
     uint4 s[V], dy[V], ds[V], gains[V], gains_next[ALIGNED ? 1 : V];
     if (ALIGNED) gains_load(p, RowSpan(0, p.T, p.D), gains);
@@ -494,6 +493,7 @@ static pgemm_status norm_forward(bool i8, int T, int D, const uint16_t *X, const
         constexpr bool A = decltype(aligned)::value;
         const long long most = dev.sm_count * (threads >= 64 ? 2048ll / threads : 32ll);
         const dim3 grid(static_cast<unsigned>(T < most ? T : most));
+        p.early = op_early(dev, grid.x);
         return i8 ? launch_small(rmsnorm_kernel<V, A, true>, grid, dim3(threads), s, p)
                   : launch_small(rmsnorm_kernel<V, A, false>, grid, dim3(threads), s, p);
     });
@@ -536,6 +536,7 @@ static pgemm_status norm_backward(int T, int D, const uint16_t *S, const uint16_
         while (per_sm > 1 && per_sm * (smem + 2048) > kSmemPerSm) --per_sm;
         const int most = dev.sm_count * per_sm;
         const int blocks = T < most ? T : most;
+        p.early = op_early(dev, blocks);
         OpArena arena(dev, s);
         const long long at = arena.add(dgain ? 4ll * blocks * D : 0);
         pgemm_status e = arena.alloc();

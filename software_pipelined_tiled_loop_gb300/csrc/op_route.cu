@@ -47,6 +47,7 @@ struct RouteParams {
     const int32_t *experts_in;
     const float *dweights;
     float *dlogits;
+    int early;  // op_begin_early
 };
 
 __device__ __forceinline__ float lanes_sum(float x) {
@@ -62,8 +63,7 @@ __device__ __forceinline__ float lanes_sum(float x) {
 template <int NV>
 __global__ void __launch_bounds__(128) route_kernel(const RouteParams p) {
     constexpr bool ORDERED = NV <= 4;
-    grid_dependency_wait();
-    grid_launch_dependents();
+    op_begin_early(p.early);
     const int lane = threadIdx.x & 31;
     for (long long t = blockIdx.x * 4ll + (threadIdx.x >> 5); t < p.T; t += gridDim.x * 4ll) {
         const float *row = p.logits + t * p.E;
@@ -152,8 +152,7 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteParams p) {
 // lane l takes experts l, l + 32, ... and choice l.
 template <int NV>
 __global__ void __launch_bounds__(128) route_backward_kernel(const RouteParams p) {
-    grid_dependency_wait();
-    grid_launch_dependents();
+    op_begin_early(p.early);
     const int lane = threadIdx.x & 31;
     for (long long t = blockIdx.x * 4ll + (threadIdx.x >> 5); t < p.T; t += gridDim.x * 4ll) {
         const float *row = p.logits + t * p.E;
@@ -247,7 +246,9 @@ static pgemm_status route_forward(int T, int E, int k, const float *logits, int 
     p.experts = experts;
     p.weights = weights;
     return with_experts(E, [&](auto nv) {
-        return launch_small(route_kernel<decltype(nv)::value>, route_grid(dev, T), dim3(128), s, p);
+        const dim3 grid = route_grid(dev, T);
+        p.early = op_early(dev, grid.x);
+        return launch_small(route_kernel<decltype(nv)::value>, grid, dim3(128), s, p);
     });
 }
 
@@ -272,8 +273,9 @@ static pgemm_status route_backward(int T, int E, int k, const float *logits, int
     p.dweights = dweights;
     p.dlogits = dlogits;
     return with_experts(E, [&](auto nv) {
-        return launch_small(route_backward_kernel<decltype(nv)::value>, route_grid(dev, T),
-                            dim3(128), s, p);
+        const dim3 grid = route_grid(dev, T);
+        p.early = op_early(dev, grid.x);
+        return launch_small(route_backward_kernel<decltype(nv)::value>, grid, dim3(128), s, p);
     });
 }
 
@@ -491,6 +493,7 @@ struct RowsParams {
     const float *weights;     // nullptr: ones
     uint16_t *out;            // gather: Xs; combine: Y; backward: dYs
     float *dweights;
+    int early;                // op_begin_early
 };
 
 template <int W>
@@ -565,8 +568,7 @@ struct RowsAt {
 template <int W>
 __global__ void __launch_bounds__(kRowsThreads) gather_kernel(const RowsParams p) {
     using V = typename Vec<W>::T;
-    grid_dependency_wait();
-    grid_launch_dependents();
+    op_begin_early(p.early);
     const unsigned vecs = p.D / W;
     const unsigned long long total = static_cast<unsigned long long>(p.T) * vecs;
     for (unsigned long long i = blockIdx.x * static_cast<unsigned long long>(kRowsThreads) + threadIdx.x;
@@ -589,8 +591,7 @@ __global__ void __launch_bounds__(kRowsThreads) gather_kernel(const RowsParams p
 template <int W>
 __global__ void __launch_bounds__(kRowsThreads) combine_flat_kernel(const RowsParams p) {
     using V = typename Vec<W>::T;
-    grid_dependency_wait();
-    grid_launch_dependents();
+    op_begin_early(p.early);
     const unsigned vecs = p.D / W;
     const unsigned long long total = static_cast<unsigned long long>(p.T) * vecs;
     const unsigned long long step = static_cast<unsigned long long>(gridDim.x) * kRowsThreads;
@@ -651,8 +652,7 @@ __global__ void __launch_bounds__(kRowsThreads) combine_flat_kernel(const RowsPa
 template <int W>
 __global__ void __launch_bounds__(kRowsThreads) combine_kernel(const RowsParams p, int per) {
     using V = typename Vec<W>::T;
-    grid_dependency_wait();
-    grid_launch_dependents();
+    op_begin_early(p.early);
     const int groups = blockDim.x / per;
     const unsigned vecs = p.D / W;
     for (long long t = blockIdx.x * static_cast<long long>(groups) + threadIdx.x / per; t < p.T;
@@ -709,8 +709,7 @@ __global__ void __launch_bounds__(kRowsThreads) combine_backward_kernel(const Ro
     using V = typename Vec<W>::T;
     constexpr int GROUPS = kRowsThreads / PER, WARPS = PER / 32;
     __shared__ float part[GROUPS][WARPS][kAhead];
-    grid_dependency_wait();
-    grid_launch_dependents();
+    op_begin_early(p.early);
     const int group = threadIdx.x / PER, lane = threadIdx.x % PER;
     const unsigned vecs = p.D / W;  // (unsigned: a step may pass 2^31)
     // (every group of a block makes as many rounds: they share the barriers)
@@ -840,8 +839,9 @@ static pgemm_status gather_run(int T, int k, int D, const uint16_t *X, const int
     p.x = X;
     p.out = Xs;
     return with_width(D, [&](auto w) {
-        return launch_small(gather_kernel<decltype(w)::value>, vectors_grid(T, D),
-                            dim3(kRowsThreads), s, p);
+        const dim3 grid = vectors_grid(T, D);
+        p.early = op_early(dev, grid.x);
+        return launch_small(gather_kernel<decltype(w)::value>, grid, dim3(kRowsThreads), s, p);
     });
 }
 
@@ -868,11 +868,13 @@ static pgemm_status combine_run(int T, int k, int D, const uint16_t *Ys, const i
         constexpr int W = decltype(w)::value;
         if constexpr (W == 8) {
             const unsigned all = vectors_grid(T, D).x, most = 8u * dev.sm_count;
+            p.early = op_early(dev, all);
             return launch_small(combine_flat_kernel<W>, dim3(all < most ? all : most),
                                 dim3(kRowsThreads), s, p);
         } else {
-            return launch_small(combine_kernel<W>, dim3(op_blocks(T, groups)), dim3(per * groups),
-                                s, p, per);
+            const int blocks = op_blocks(T, groups);
+            p.early = op_early(dev, blocks);
+            return launch_small(combine_kernel<W>, dim3(blocks), dim3(per * groups), s, p, per);
         }
     });
 }
@@ -899,8 +901,10 @@ static pgemm_status combine_backward_run(int T, int k, int D, const uint16_t *Ys
     return with_width(D, [&](auto w) {
         constexpr int W = decltype(w)::value;
         auto go = [&](auto n) {
-            return launch_small(combine_backward_kernel<W, decltype(n)::value>,
-                                rows_grid(dev, T, decltype(n)::value), dim3(kRowsThreads), s, p);
+            const dim3 grid = rows_grid(dev, T, decltype(n)::value);
+            p.early = op_early(dev, grid.x);
+            return launch_small(combine_backward_kernel<W, decltype(n)::value>, grid,
+                                dim3(kRowsThreads), s, p);
         };
         switch (per) {
             case 32: return go(std::integral_constant<int, 32>{});
