@@ -1398,6 +1398,7 @@ static pgemm_status experts_gated_backward(const ExpSizes &z, const uint16_t *X,
         g.dz = arena.at<uint16_t>(at0);
         g.du = arena.at<uint16_t>(at1);
         g.dz_ld = dz_ld;
+        g.early = false;
         if ((st = op_act_grad(dev, g, arena, false, s)) != PGEMM_OK) return st;
     } else if (some) {
         ExpertsArgs a{};

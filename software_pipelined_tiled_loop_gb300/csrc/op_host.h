@@ -235,6 +235,9 @@ struct OpActGrad {
     uint16_t *du = nullptr;          // gated
     long long dz_ld = 0;
     uint16_t *dbias = nullptr;       // N, or nullptr
+    // whether the next kernel is launched while this one runs (its blocks wait in places
+    // that this one's would have: see op_begin_early)
+    bool early = true;
     long long colsum_at = 0;         // op_act_grad_plan's
 };
 // Reserve the partial column sums; the elementwise pass; their sum into dbias.

@@ -550,7 +550,10 @@ __device__ __forceinline__ void load8(const float *p, float (&f)[8]) {
 
 template <bool VEC, bool GATED>
 __global__ void __launch_bounds__(256) act_grad_kernel(const ActGradParams p) {
-    op_begin(p.overlap);
+    if (p.overlap)
+        op_begin(1);
+    else
+        op_begin_early(p.g.early);
     const OpActGrad &g = p.g;
     const int lane = threadIdx.x & 31, rl = threadIdx.x >> 5;
     const int c0 = blockIdx.x * 256;
