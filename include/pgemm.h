@@ -318,7 +318,8 @@ PGEMM_API pgemm_status xent_bf16_grad(int T, int V, int D, const uint16_t *X, co
 /* Root-mean-square norm with the residual's addition: S <- X + residual, and
  * y = S gain / sqrt(mean over the row of S^2 + eps) to Y.  X, residual (NULL:
  * none), S (NULL: not kept; may be X or the residual) and Y are T x D, gain D
- * (NULL: ones).  S is rounded to bf16, and y is made of that.  eps >= 0.
+ * (NULL: ones).  S is rounded to bf16, and y is made of that.  eps >= 0.  The sum of
+ * squares is fp32: a row whose squares pass its range gives zeros.
  * D <= 32768 (else PGEMM_ERR_TOO_LARGE). */
 PGEMM_API pgemm_status rmsnorm_bf16(int T, int D, const uint16_t *X, const uint16_t *residual,
                                     const uint16_t *gain, float eps, uint16_t *S, uint16_t *Y,
@@ -352,7 +353,8 @@ PGEMM_API pgemm_status route_topk(int T, int E, int k, const float *logits, int 
                                   int32_t *experts, float *weights, pgemm_stream_t stream);
 
 /* Gradient of route_topk's weights for dweights (T x k) into dlogits (T x E), with the
- * choices as it made them (a choice outside [0, E) does not count). */
+ * choices as it made them (a choice outside [0, E) does not count, an expert chosen
+ * twice counts twice). */
 PGEMM_API pgemm_status route_topk_backward(int T, int E, int k, const float *logits,
                                            int normalise, const int32_t *experts,
                                            const float *dweights, float *dlogits,
@@ -366,8 +368,8 @@ PGEMM_API pgemm_status expert_sort(int T, int E, int k, const int32_t *experts, 
                                    int32_t *slot_row, pgemm_stream_t stream);
 
 /* Tokens to their rows: Xs[slot_row[t][j]] <- X[t].  X is T x D, Xs T k x D; rows that
- * no slot has stay as they were, and a slot_row outside [0, T k) does not count.  Its
- * gradient is expert_combine_bf16 without weights and residual. */
+ * no slot has stay as they were, and a slot_row outside [0, T k) does not count.  No two
+ * slots may have the same row.  Its gradient is expert_combine_bf16 without weights and residual. */
 PGEMM_API pgemm_status expert_gather_bf16(int T, int k, int D, const uint16_t *X,
                                           const int32_t *slot_row, uint16_t *Xs,
                                           pgemm_stream_t stream);

@@ -45,7 +45,7 @@ enum class Exp {
 
 struct ExpertsMaps {
     CUtensorMap x[2][3];     // rows, in boxes of three sizes
-    CUtensorMap w[2], c[2];
+    CUtensorMap w[2];
 };
 struct ExpertsWeightsMaps {
     CUtensorMap x[4], z[2][4];  // boxes of 96, 64, 32 and 16 rows
@@ -71,9 +71,13 @@ struct ExpertsArgs {
 };
 
 // CG CTAs work on a tile of CG * 128 accumulator lanes x up to TOK rows, BK columns of the
-// reduction a step.  What a step's copies cost is their number: with a pair, boxes of 32
-// rows and steps of 64 columns (six copies a CTA) took 404 us for 8192 x 8192 x 4096, one
-// of 128 rows instead of the four 323.
+// reduction a step.  What a step's copies cost is their number: one expert, 8192 x 8192 x
+// 4096 on pairs, took 404 us with four boxes of 32 rows a step, 323 with one of 128, and
+// 285 (1.93 PFLOP/s) since the warps that issue them run as one (warp_value).  A pair's ring
+// holds six steps of 64 columns, a load from HBM taking some six steps' products: 64 experts
+// of some 512 rows, 2048 x 1024 gated, 187 us, with three steps of 128 197.  Such ragged
+// groups (32 experts, 4096 x 2048: 1.48 PFLOP/s) pay for tiles of fewer than 256 rows, whose
+// weights are as many bytes for fewer products.
 template <int CG_, int TOK_, int BK_, int STAGES_, Exp MODE_>
 struct ExpCfg {
     static constexpr int CG = CG_, TOK = TOK_, STAGES = STAGES_, BK = BK_, BM = 128;
@@ -121,7 +125,10 @@ struct ExpertsTable {
     }
 };
 
-// All threads; count(rows) gives an expert's units.
+// All threads; count(rows) gives an expert's units, fewer than kUnitsMost (as the host
+// checks for all of a call's).  The sums stop there, so that offsets which decrease, and
+// count rows twice, still make a list whose units lie within their experts' rows.
+constexpr int kUnitsMost = INT_MAX / 2;
 template <class Count>
 __device__ __forceinline__ ExpertsTable experts_table(const ExpertsArgs &a, uint8_t *at,
                                                       Count &&count) {
@@ -148,10 +155,11 @@ __device__ __forceinline__ ExpertsTable experts_table(const ExpertsArgs &a, uint
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int o = __shfl_up_sync(0xffffffffu, sum, d);
-                if (lane >= d) sum += o;
+                if (lane >= d) sum = min(sum + o, kUnitsMost);
             }
-            if (e < a.E) t.first[e] = before + sum - n;
-            before += __shfl_sync(0xffffffffu, sum, 31);
+            const int earlier = __shfl_up_sync(0xffffffffu, sum, 1);
+            if (e < a.E) t.first[e] = min(before + (lane > 0 ? earlier : 0), kUnitsMost);
+            before = min(before + __shfl_sync(0xffffffffu, sum, 31), kUnitsMost);
         }
         if (lane == 0) t.first[a.E] = before;
     }
@@ -420,7 +428,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             uint16_t dh[Cfg::MODE == Exp::GATED_GRAD ? KEEP : 1];
             auto fetch_dh = [&](int c) {
                 if constexpr (Cfg::MODE == Exp::GATED_GRAD) {
-                    const uint16_t *in = a.dy + (w.row0 + c * W + c0) * static_cast<long long>(a.M) + feat;
+                    const long long row = static_cast<long long>(w.row0) + c * W + c0;
+                    const uint16_t *in = a.dy + row * a.M + feat;
 #pragma unroll
                     for (int j = 0; j < KEEP; ++j) {
                         dh[j] = mine && c * W + c0 + j < w.rows ? *in : 0;
@@ -583,11 +592,14 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 // Few rows a group: a unit's output takes longer than its products.  Then a ring of three
 // stages instead of four makes room to stage all of a warp's output at once, 64 columns
 // wide (WIDE), whose rows of 128 bytes also write fewer 32-byte sectors in part where the
-// matrix's rows start anywhere in one.  32 experts 2048 x 4096, us with three and with four
-// stages: 256 rows each 154 and 174, 320 rows 187 and 174; 1624 x 2488, 8 rows 73 and 85.
-// What is left is writing dW (8 rows each of 64 experts 1024 x 2048: 4.1 TB/s, a memset's
+// matrix's rows start anywhere in one.  us with three and with four stages, sizes of groups
+// that spread by half: 32 experts 2048 x 4096, 24 rows a group 123 and 127, 256 rows 153 and
+// 170, 320 rows 165 and 172, 448 rows 192 and 187; 64 experts 1024 x 1368 8 rows 52 and 60,
+// 256 rows 70 and 77, 448 rows 92 and 89.  (Where rows start on 128 bytes and experts are
+// small four stages are the quicker below some 128 rows too: 1024 x 2048, 96 rows 82 and 79.)
+// What is left is writing dW (8 rows each of 64 experts 1024 x 2048: 4.2 TB/s, a memset's
 // rate) and, with more rows, the traffic of both directions beside the products (512 rows
-// 192 us, 1.43 PFLOP/s; without its stores the kernel takes 166).
+// 183 us, 1.50 PFLOP/s; one expert of 8192 rows 1.95).
 template <int BK_, int STAGES_, int NBUF_, bool WIDE_>
 struct ExpWeightsCfg {
     static constexpr bool WIDE = WIDE_;
@@ -605,7 +617,7 @@ struct ExpWeightsCfg {
     static constexpr int SMEM_BYTES = smem_request(USED + 1024, 1);
     static_assert(USED + 1024 <= 232448, "shared memory");
     static_assert(WIDE ? NBUF == EPI_COLS / 32 : EPI_COLS / 32 % NBUF == 0, "whole batches");
-    static_assert(BK == 96 || BK == 64, "a step's rows are one box");
+    static_assert(BK == 96, "a step's rows are one box of 96, 64 or 32");
 };
 
 struct WeightsUnit {
@@ -783,7 +795,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 const uint32_t db = smem_u32(sB) + s * Cfg::B_BYTES;
                 const uint32_t bar = full_lead + s * 8;
                 // a box of 96 rows, in a last step perhaps of 64 or 32
-                const int box = BK == 96 && left > 64 ? 0 : left > 32 ? 1 : 2;
+                const int box = left > 64 ? 0 : left > 32 ? 1 : 2;
                 mbar_arrive_expect_tx_if(ok ? first : 0u, full0 + s * 8,
                                          (96 - 32 * box) * (2 * Cfg::STAGE_BYTES / BK));
 #pragma unroll
@@ -1128,7 +1140,7 @@ static pgemm_status exp_launch(const OpDevice &dev, const Maps &maps, const Expe
     int slots = 0;
     const pgemm_status st = op_kernel_setup(dev, info, &slots);
     if (st != PGEMM_OK) return st;
-    if (most_units > INT_MAX / 2) return PGEMM_ERR_TOO_LARGE;
+    if (most_units > kUnitsMost) return PGEMM_ERR_TOO_LARGE;
     cudaLaunchAttribute attr[2];
     int nattr = 0;
     attr[nattr].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1185,15 +1197,18 @@ static pgemm_status rows_product(const OpDevice &dev, const ExpSizes &z, const O
                                  const OpMat *w, int segments, const ExpertsArgs &a,
                                  cudaStream_t s) {
     // Few rows a group: the weights are all there is to read, and single CTAs with small
-    // tiles of rows keep more of them on the way (64 experts 2048 x 1024, 16 rows each: 47
-    // us against 50 on pairs), until groups pass a tile's 64 rows and read them twice (96
-    // rows: 71 against 54); groups are uneven, so that begins below a mean of 64.  And few
-    // tiles: smaller ones on more SMs.
+    // tiles of rows keep more of them on the way: 64 experts 2048 x 1024, 16 rows each, 45 us
+    // (6.1 TB/s) against 48 on pairs, 40 rows 47 against 49.5.  Groups that pass a tile's 64
+    // rows read them twice (96 rows: 63 against 52), and groups are uneven: 16 experts 1024 x
+    // 4096 of sizes that spread by half, a mean of 40 rows 25.9 against 27.3, of 48 35.5
+    // against 27.6.  And few tiles: smaller ones on more SMs (one expert, 512 rows 1024 x
+    // 2048: 10 against 16).
     const long long live = z.R < z.E ? z.R : z.E;
     const long long pairs =
         (z.R / 256 + live) * op_blocks(MODE == Exp::TRANSPOSED ? z.K : z.N,
                                        MODE == Exp::LINEAR || MODE == Exp::TRANSPOSED ? 256 : 128);
-    if (z.R <= 24ll * z.E || 4 * pairs <= dev.sm_count) return rows_launch<ExpCfg<1, 64, 128, 4, MODE>>(dev, z, x, w, segments, a, s);
+    if (z.R <= 40ll * z.E || 4 * pairs <= dev.sm_count)
+        return rows_launch<ExpCfg<1, 64, 128, 4, MODE>>(dev, z, x, w, segments, a, s);
     return rows_launch<ExpCfg<2, 256, 64, 6, MODE>>(dev, z, x, w, segments, a, s);
 }
 
@@ -1236,7 +1251,7 @@ static pgemm_status weights_launch(const OpDevice &dev, const ExpSizes &z, const
 static pgemm_status weights_product(const OpDevice &dev, const ExpSizes &z, const OpMat &x,
                                     const OpMat *dz, int segments, uint16_t *const *out,
                                     bool overlap, cudaStream_t s) {
-    if (z.R <= 256ll * z.E)
+    if (z.R <= 320ll * z.E)  // (see ExpWeightsCfg)
         return weights_launch<ExpWeightsCfg<96, 3, 4, true>>(dev, z, x, dz, segments, out, overlap, s);
     return weights_launch<ExpWeightsCfg<96, 4, 1, false>>(dev, z, x, dz, segments, out, overlap, s);
 }

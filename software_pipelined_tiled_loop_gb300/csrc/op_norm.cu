@@ -11,7 +11,9 @@
 // outputs, so every operand is read once; the next row's operands travel meanwhile.  All
 // operands have the same pitch and 16-byte-aligned bases, so a row starts at the same place
 // of a 16-byte vector in each: a thread takes whole aligned vectors (eight elements of the
-// flat matrix), masked at the row's two ends, whatever the width.  Bound by HBM.
+// flat matrix), masked at the row's two ends, whatever the width.  Bound by HBM: 8192 x 4096
+// with a residual 42 us (6.4 TB/s), as int8 46 (5.1), backward 49 (5.5; the gains' gradient
+// and its join 5 of them); 4097 x 5120 26.7 and 31.6.  One row of 4096 1.9 us from a graph.
 #include <cuda_runtime.h>
 
 #include "op_gemm.cuh"
@@ -444,8 +446,9 @@ __global__ void __launch_bounds__(1024)
 
 // f(vectors a thread, whether rows start on vectors) as constants, and threads.  Two vectors
 // a thread or one (`one`: up to 512): forward, two are quicker with rows for every SM (8192 x
-// 4096 42.0 us against 49.2) and one where a row's own latency counts; backward, whose
-// thread holds three operands and the next row's, one is (52.5 us against 59.4).
+// 4096 41.7 us against 48.9, 1500 x 4096 6.8 against 7.7) and one where a row's own latency
+// counts (1 x 4096 1.8 against 2.0); backward, whose thread holds three operands and the next
+// row's, one is (8192 x 4096 48.9 against 53.2, 400 x 4096 7.4 against 9.0).
 template <class F>
 static pgemm_status with_row(int D, bool one, F &&f) {
     const int vecs = D % 8 == 0 ? D / 8 : (D + 14) / 8;
@@ -488,7 +491,7 @@ static pgemm_status norm_forward(bool i8, int T, int D, const uint16_t *X, const
     p.y = i8 ? nullptr : static_cast<uint16_t *>(out);
     p.q = i8 ? static_cast<int8_t *>(out) : nullptr;
     p.scale = scale;
-    return with_row(D, T < 4 * dev.sm_count, [&](auto v, auto aligned, int threads) {
+    return with_row(D, T < 2 * dev.sm_count, [&](auto v, auto aligned, int threads) {
         constexpr int V = decltype(v)::value;
         constexpr bool A = decltype(aligned)::value;
         const long long most = dev.sm_count * (threads >= 64 ? 2048ll / threads : 32ll);

@@ -58,8 +58,9 @@ __device__ __forceinline__ float lanes_sum(float x) {
 
 // A warp a token; lane l holds experts l, l + 32, ...  Up to four of them a lane keeps in
 // order, so that a choice compares the lanes' best alone; of more it finds its best again
-// every time.  Bound by instructions for many tokens, which the order saves a third of
-// (16384 tokens, eight of 128 experts, softmax over all: 11.3 us without it).
+// every time.  Bound by instructions for many tokens (16384 tokens, eight of 128 experts,
+// softmax over all: 9.9 us, without the order 11.3), by latency for few (24 tokens, eight of
+// 64 experts: 1.7 us).
 template <int NV>
 __global__ void __launch_bounds__(128) route_kernel(const RouteParams p) {
     constexpr bool ORDERED = NV <= 4;
@@ -148,8 +149,9 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteParams p) {
 
 // dlogits from dweights: with w the weights and dot = sum over the chosen of w dw,
 // w (dw - dot) at the chosen (softmax over the chosen), or p ([chosen] dw - dot)
-// everywhere (softmax over all).  A choice outside [0, E) does not count.  A warp a token:
-// lane l takes experts l, l + 32, ... and choice l.
+// everywhere (softmax over all).  A choice outside [0, E) does not count, an expert chosen
+// twice counts twice: the first of its lanes adds the others' in their order.  A warp a
+// token: lane l takes experts l, l + 32, ... and choice l.  16384 tokens as above 7.0 us.
 template <int NV>
 __global__ void __launch_bounds__(128) route_backward_kernel(const RouteParams p) {
     op_begin_early(p.early);
@@ -202,7 +204,17 @@ __global__ void __launch_bounds__(128) route_backward_kernel(const RouteParams p
             if (lane + 32 * i < p.E)
                 out[lane + 32 * i] = p.normalise || !any ? 0.0f : z[i] * scale;
         __syncwarp();  // the chosen ones' values replace those
-        if (mine >= 0) out[mine] = w * (dw - dot);
+        const unsigned same = __match_any_sync(0xffffffffu, mine);
+        const bool owner = mine >= 0 && lane == __ffs(same) - 1;
+        float all = dw;
+        for (unsigned rest = __reduce_or_sync(0xffffffffu, owner ? same & (same - 1u) : 0u);
+             rest != 0u; rest &= rest - 1u) {  // lanes whose expert an earlier one has
+            const int l = __ffs(rest) - 1;
+            const float d = __shfl_sync(0xffffffffu, dw, l);
+            if (same >> l & 1u) all += d;
+        }
+        const float times = p.normalise ? static_cast<float>(__popc(same)) : 1.0f;
+        if (owner) out[mine] = w * fmaf(-times, dot, all);
         __syncwarp();
     }
 }
@@ -285,17 +297,18 @@ static pgemm_status route_backward(int T, int E, int k, const float *logits, int
 // give the rest of a slot's rank.  Two passes over the slots (count, then place), with the
 // counters turned into first rows in between: over the block's warps, over the blocks
 // before this one, over the experts before this one.  Up to kSortOne slots one block does
-// all of it (a launch more would cost longer); more take blocks of 1024, a launch that
-// counts and one that places, each of whose blocks sums the others' counts itself, or with
-// many blocks a launch between them.
-constexpr int kSortWarps = 32, kSortOne = 4096, kSortChunk = 1024, kSortOwnSums = 64;
+// all of it; more take blocks of 1024, a launch that counts and one that places, each of
+// whose blocks sums the others' counts itself, or with many blocks a launch between them.
+// Bound by latency: 192 slots of 64 experts 2.7 us, 2048 6.2 (two launches 7.1), 4096 7.1
+// (one block 9.8), 32768 8.6 (three launches 9.3), 65536 9.5 (two 10.9).
+constexpr int kSortWarps = 32, kSortOne = 2048, kSortChunk = 1024, kSortOwnSums = 32;
 
 struct SortParams {
     long long slots;
     int E, blocks, chunk;
     const int32_t *experts;
     int32_t *offsets, *slot_row;
-    int32_t *counts;  // [E][blocks]
+    int32_t *counts;  // [blocks][E]
     int32_t *totals;  // [E], and counts summed over the blocks before: sort_scan_kernel's
 };
 
@@ -313,6 +326,23 @@ __device__ __forceinline__ void sort_count(const SortParams &p, int32_t *count, 
         const unsigned same = __match_any_sync(0xffffffffu, in ? e : -1);
         if (in && lane == __ffs(same) - 1) mine[e] += __popc(same);
         __syncwarp();
+    }
+}
+
+// f(block, its count of expert e) for the blocks first .. last - 1, eight on the way (sixteen: 32768 slots
+// of 64 experts 10.8 us for 8.7).
+template <class F>
+__device__ __forceinline__ void block_counts(const SortParams &p, int e, int first, int last,
+                                             F &&f) {
+#pragma unroll 1
+    for (int b0 = first; b0 < last; b0 += 8) {
+        int n[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            n[i] = b0 + i < last ? p.counts[static_cast<long long>(b0 + i) * p.E + e] : 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (b0 + i < last) f(b0 + i, n[i]);
     }
 }
 
@@ -339,21 +369,19 @@ __global__ void __launch_bounds__(kSortWarps * 32) sort_kernel(const SortParams 
         }
     }
     if constexpr (!PLACE) {
-        if (e < p.E) p.counts[static_cast<long long>(e) * p.blocks + blockIdx.x] = all;
+        if (e < p.E) p.counts[static_cast<long long>(blockIdx.x) * p.E + e] = all;
         return;
     }
     int before = 0;  // rows of this expert in earlier blocks
     if (p.totals != nullptr && e < p.E) {
-        before = p.counts[static_cast<long long>(e) * p.blocks + blockIdx.x];
+        before = p.counts[static_cast<long long>(blockIdx.x) * p.E + e];
         all = p.totals[e];
     } else if (p.blocks > 1 && e < p.E) {
         all = 0;
-#pragma unroll 8
-        for (int b = 0; b < p.blocks; ++b) {
-            const int n = p.counts[static_cast<long long>(e) * p.blocks + b];
+        block_counts(p, e, 0, p.blocks, [&](int b, int n) {
             if (b < static_cast<int>(blockIdx.x)) before += n;
             all += n;
-        }
+        });
     }
     // first rows: an exclusive sum over the experts
     int sum = all;
@@ -401,26 +429,37 @@ __global__ void __launch_bounds__(kSortWarps * 32) sort_kernel(const SortParams 
     }
 }
 
-// Each expert's counts <- their sums over the blocks before; a warp an expert.
-__global__ void __launch_bounds__(128) sort_scan_kernel(const SortParams p) {
+// Each expert's counts <- their sums over the blocks before: 32 experts a block, a lane
+// each, a warp every 32nd part of the blocks.
+__global__ void __launch_bounds__(1024) sort_scan_kernel(const SortParams p) {
+    __shared__ int32_t sums[32][33];
     grid_dependency_wait();
     grid_launch_dependents();
-    const int e = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (e >= p.E) return;
-    int32_t *c = p.counts + static_cast<long long>(e) * p.blocks;
-    int before = 0;
-    for (int b0 = 0; b0 < p.blocks; b0 += 32) {
-        const int n = b0 + lane < p.blocks ? c[b0 + lane] : 0;
-        int sum = n;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
+    const int per = (p.blocks + 31) / 32;
+    const int first = min(warp * per, p.blocks), last = min(first + per, p.blocks);
+    int sum = 0;
+    if (e < p.E) block_counts(p, e, first, last, [&](int, int n) { sum += n; });
+    sums[warp][lane] = sum;
+    __syncthreads();
+    if (warp == 0) {
+        int before = 0;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, sum, d);
-            if (lane >= d) sum += o;
+        for (int w = 0; w < 32; ++w) {
+            const int n = sums[w][lane];
+            sums[w][lane] = before;
+            before += n;
         }
-        if (b0 + lane < p.blocks) c[b0 + lane] = before + sum - n;
-        before += __shfl_sync(0xffffffffu, sum, 31);
+        if (e < p.E) p.totals[e] = before;
     }
-    if (lane == 0) p.totals[e] = before;
+    __syncthreads();
+    if (e < p.E) {
+        int before = sums[warp][lane];
+        block_counts(p, e, first, last, [&](int b, int n) {
+            p.counts[static_cast<long long>(b) * p.E + e] = before;
+            before += n;
+        });
+    }
 }
 
 static pgemm_status expert_sort_run(int T, int E, int k, const int32_t *experts, int32_t *offsets,
@@ -454,7 +493,8 @@ static pgemm_status expert_sort_run(int T, int E, int k, const int32_t *experts,
     SortParams p{};
     p.slots = slots;
     p.E = E;
-    p.chunk = slots <= kSortOne ? kSortOne : kSortChunk;
+    // (a multiple of what the warps take at once, so that they share the slots)
+    p.chunk = slots <= kSortOne ? op_blocks(slots, kSortChunk) * kSortChunk : kSortChunk;
     p.blocks = op_blocks(slots, p.chunk);
     p.experts = experts;
     p.offsets = offsets;
@@ -473,7 +513,7 @@ static pgemm_status expert_sort_run(int T, int E, int k, const int32_t *experts,
         if (st != PGEMM_OK) return st;
         if (scan) {
             p.totals = arena.at<int32_t>(totals_at);
-            st = launch_small(sort_scan_kernel, dim3(op_blocks(E, 4)), dim3(128), s, p);
+            st = launch_small(sort_scan_kernel, dim3(op_blocks(E, 32)), dim3(1024), s, p);
             if (st != PGEMM_OK) return st;
         }
     }
@@ -565,6 +605,8 @@ struct RowsAt {
     }
 };
 
+// A vector of all tokens' a thread.  Bound by HBM: 8192 tokens to four rows of 4096 values
+// each, 51 us, 6.6 TB/s.
 template <int W>
 __global__ void __launch_bounds__(kRowsThreads) gather_kernel(const RowsParams p) {
     using V = typename Vec<W>::T;
@@ -703,7 +745,8 @@ __global__ void __launch_bounds__(kRowsThreads) combine_kernel(const RowsParams 
 }
 
 // PER threads a token: a warp or more.  The slots' dot products of kAhead choices at a
-// time, over the lanes' columns, then over the lanes, then over the group's warps.
+// time, over the lanes' columns, then over the lanes, then over the group's warps.  Bound
+// by HBM: 8192 tokens, four rows of 4096 values, 90 us, 6.7 TB/s.
 template <int W, int PER>
 __global__ void __launch_bounds__(kRowsThreads) combine_backward_kernel(const RowsParams p) {
     using V = typename Vec<W>::T;

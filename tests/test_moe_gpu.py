@@ -183,6 +183,27 @@ def test_route(T, E, k, normalise):
     ref.check(dz, *moe.route_backward(z, k, normalise, experts, dw.nan_to_num(0)), "dlogits")
 
 
+@pytest.mark.parametrize("normalise", [False, True])
+@pytest.mark.parametrize("T,E,k", [(200, 5, 5), (64, 40, 8), (300, 128, 32), (33, 300, 17)])
+def test_route_backward_expert_twice(T, E, k, normalise):
+    """Choices that route_topk would not make: an expert several times, none at all."""
+    z, dw = logits(31, T, E), rnd(32, T, k, dtype=F32)
+    g = torch.Generator("cuda").manual_seed(33)
+    experts = torch.randint(-1, E + 1, (T, k), generator=g, device="cuda", dtype=I32)
+    experts[1:T:3] = experts[1:T:3, :1].clone()  # one expert k times
+    experts[2:T:3, ::2] = experts[2:T:3, :1].clone()
+    if E == 40:
+        z = torch.zeros_like(z)
+    open_ = z.gather(1, experts.clamp(0, E - 1).long()) > -INF
+    experts = torch.where(open_, experts, -1)
+    dz = nan(T, E, dtype=F32)
+    pg.route_topk_backward(T, E, k, z, normalise, experts, dw, dz)
+    ref.check(dz, *moe.route_backward(z, k, normalise, experts, dw), "dlogits")
+    again = nan(T, E, dtype=F32)
+    pg.route_topk_backward(T, E, k, z, normalise, experts, dw, again)
+    assert torch.equal(dz, again)
+
+
 def test_route_zeros_and_extremes():
     z = torch.zeros(4, 40, device="cuda")
     z[0, 7], z[0, 3] = 0.0, -0.0           # a tie whatever the sign
