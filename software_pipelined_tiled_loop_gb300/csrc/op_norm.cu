@@ -111,37 +111,45 @@ __device__ __forceinline__ uint4 gain_load(const uint16_t *g, const RowSpan &r, 
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-struct Add {
-    __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
-};
-struct Larger {  // a NaN stays one
-    __device__ __forceinline__ float operator()(float a, float b) const {
-        return a > b || a != a ? a : b;
-    }
-};
-
-// op of N values over the block's threads, in an order that does not depend on timing; the
-// same in every thread.  `part` may be used again after the block's next barrier.
-template <int N, class Op>
-__device__ __forceinline__ void block_reduce(float (&x)[N], float (*part)[32], Op op) {
+// The sums of N values over the block's threads, in an order that does not depend on timing,
+// and the largest `most`; the same in every thread.  `part` may be used again after the
+// block's next barrier.
+template <int N, bool MOST>
+__device__ __forceinline__ void block_reduce(float (&x)[N], uint32_t &most,
+                                             uint32_t (*part)[32]) {
+    auto lanes = [&] {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
+        for (int i = 0; i < N; ++i)
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) x[i] = op(x[i], __shfl_xor_sync(0xffffffffu, x[i], d));
-    const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+            for (int d = 16; d > 0; d >>= 1) x[i] += __shfl_xor_sync(0xffffffffu, x[i], d);
+        if constexpr (MOST) most = __reduce_max_sync(0xffffffffu, most);
+    };
+    lanes();
+    const int warps = blockDim.x >> 5, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (warps > 1) {
         if (lane == 0) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) part[i][threadIdx.x >> 5] = x[i];
+            for (int i = 0; i < N; ++i) part[i][warp] = __float_as_uint(x[i]);
+            if constexpr (MOST) part[N][warp] = most;
         }
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            x[i] = lane < warps ? part[i][lane] : 0.0f;
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) x[i] = op(x[i], __shfl_xor_sync(0xffffffffu, x[i], d));
-        }
+        for (int i = 0; i < N; ++i) x[i] = lane < warps ? __uint_as_float(part[i][lane]) : 0.0f;
+        if constexpr (MOST) most = lane < warps ? part[N][lane] : 0u;
+        lanes();
     }
+}
+
+// A magnitude as bits: ordered as the numbers are, infinity behind them, NaN behind that.
+__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// Four integers of at most 127, rounded to nearest with ties to even by adding 1.5 * 2^23,
+// below which a float's last place is one.
+__device__ __forceinline__ uint32_t round4_i8(const float *x) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(x[i] + 12582912.0f);
+    return __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
 }
 
 struct NormParams {
@@ -174,7 +182,7 @@ __device__ __forceinline__ void gains_load(const NormParams &p, const RowSpan &r
 // the next row is not fetched ahead, for want of registers.
 template <int V, bool ALIGNED, bool I8>
 __global__ void __launch_bounds__(V <= 2 ? 512 : 1024) rmsnorm_kernel(const NormParams p) {
-    __shared__ float part[2][1][32];
+    __shared__ uint32_t part[2][2][32];
     constexpr bool AHEAD = V <= 2;
     op_begin_early(p.early);
     int turn = 0;
@@ -204,7 +212,8 @@ __global__ void __launch_bounds__(V <= 2 ? 512 : 1024) rmsnorm_kernel(const Norm
 #pragma unroll
             for (int i = 0; i < V; ++i) gains[i] = gains_next[i];
         }
-        float sum[1] = {0.0f};
+        float sum[1] = {0.0f};  // of squares
+        uint32_t most = 0u;     // int8: the largest |S gain|
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int v = threadIdx.x + i * blockDim.x;
@@ -221,11 +230,19 @@ __global__ void __launch_bounds__(V <= 2 ? 512 : 1024) rmsnorm_kernel(const Norm
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) sum[0] = fmaf(f[j], f[j], sum[0]);
+            if constexpr (I8) {
+                if (v < row.vecs) {
+                    float g[8];
+                    unpack8(gains[i], g);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) most = max(most, magnitude(f[j] * g[j]));
+                }
+            }
             if (p.s && v < row.vecs) row_store(p.s, row, v, s[i]);
         }
         // (S may be X or R: a row's stores touch no other row)
         if (AHEAD && t + gridDim.x < T) fetch(t + gridDim.x);
-        block_reduce(sum, part[turn], Add{});
+        block_reduce<1, I8>(sum, most, part[turn]);
         turn ^= 1;
         const float rstd = 1.0f / sqrtf(sum[0] / static_cast<float>(p.D) + p.eps);
         auto value = [&](int i, float (&y)[8]) {
@@ -245,39 +262,57 @@ __global__ void __launch_bounds__(V <= 2 ? 512 : 1024) rmsnorm_kernel(const Norm
                 row_store(p.y, row, v, pack8(y));
             }
         } else {
-            float most[1] = {0.0f};
+            // y = (S gain) rstd here, so that the largest |y| is the largest |S gain| times
+            // rstd, with no second sum over the block, and Q = (S gain) (127 / the largest).
+            // Where those come near the ends of the range the y are looked through instead,
+            // and far below 1 scaled up first, so that the reciprocal is finite.
+            const float product = __uint_as_float(most);
+            float top = product * rstd, by = 1.0f, inv = 0.0f;
+            const bool near = product > 7.8886091e-31f && product < 1.2676506e30f &&  // 2^+-100
+                              rstd > 0.0f && top < __int_as_float(0x7f800000);
+            if (near) {
+                inv = 127.0f / product;
+            } else {
+                most = 0u;
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int v = threadIdx.x + i * blockDim.x;
-                if (v >= row.vecs) break;
-                float y[8];
-                value(i, y);
+                for (int i = 0; i < V; ++i) {
+                    const int v = threadIdx.x + i * blockDim.x;
+                    if (v >= row.vecs) break;
+                    float y[8];
+                    value(i, y);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int c = row.col(v) + j;
-                    if (ALIGNED || (c >= 0 && c < p.D)) most[0] = Larger{}(fabsf(y[j]), most[0]);
+                    for (int j = 0; j < 8; ++j) {
+                        const int c = row.col(v) + j;
+                        if (ALIGNED || (c >= 0 && c < p.D)) most = max(most, magnitude(y[j]));
+                    }
                 }
+                float none[1] = {0.0f};
+                block_reduce<1, true>(none, most, part[turn]);
+                turn ^= 1;
+                top = __uint_as_float(most);
+                by = top < 8.6736174e-19f ? 1.1529215e18f : 1.0f;  // 2^-60, 2^60
+                if (top > 0.0f && top < __int_as_float(0x7f800000)) inv = 127.0f / (top * by);
             }
-            block_reduce(most, part[turn], Larger{});
-            turn ^= 1;
-            const bool fine = most[0] < __int_as_float(0x7f800000);
             if (threadIdx.x == 0)
-                p.scale[t] = fine ? most[0] / 127.0f : __int_as_float(0x7fc00000);
-            // far below 1 everything is scaled up first, so that the reciprocal is finite
-            const float up = most[0] < 8.6736174e-19f ? 1.1529215e18f : 1.0f;  // 2^-60, 2^60
-            const float inv = fine && most[0] > 0.0f ? 127.0f / (most[0] * up) : 0.0f;
+                p.scale[t] = top < __int_as_float(0x7f800000) ? top / 127.0f
+                                                              : __int_as_float(0x7fc00000);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int v = threadIdx.x + i * blockDim.x;
                 if (v >= row.vecs) break;
                 float y[8];
-                value(i, y);
-                uint32_t w[2] = {0u, 0u};
+                if (near) {
+                    float g[8];
+                    unpack8(gains[i], g);
+                    unpack8(s[i], y);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int q = fine ? __float2int_rn(y[j] * up * inv) : 0;
-                    w[j / 4] |= (static_cast<uint32_t>(q) & 0xffu) << (j % 4 * 8);
+                    for (int j = 0; j < 8; ++j) y[j] = y[j] * g[j] * inv;
+                } else {
+                    value(i, y);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) y[j] = inv > 0.0f ? y[j] * by * inv : 0.0f;
                 }
+                const uint32_t w[2] = {round4_i8(y), round4_i8(y + 4)};
                 int8_t *at = p.q + row.first + 8ll * v;
                 if (ALIGNED || row.whole(v)) {
                     *reinterpret_cast<uint2 *>(at) = make_uint2(w[0], w[1]);
@@ -303,7 +338,7 @@ enum class GainSum { NONE, REGISTERS, SHARED };
 template <int V, bool ALIGNED, GainSum SUM>
 __global__ void __launch_bounds__(V <= 2 ? 512 : 1024) rmsnorm_backward_kernel(const NormParams p) {
     extern __shared__ float sums[];
-    __shared__ float part[2][2][32];
+    __shared__ uint32_t part[2][2][32];
     constexpr bool AHEAD = V <= 2;
     static_assert(SUM != GainSum::REGISTERS || ALIGNED, "columns move from row to row");
     const int pitch = (p.D + 7) / 8;
@@ -361,7 +396,8 @@ __global__ void __launch_bounds__(V <= 2 ? 512 : 1024) rmsnorm_backward_kernel(c
         const unsigned after = t + gridDim.x;
         uint4 s1[V], dy1[V], ds1[V];
         if (AHEAD && after < T) fetch(after, s1, dy1, ds1);
-        block_reduce(both, part[turn], Add{});
+        uint32_t none = 0u;
+        block_reduce<2, false>(both, none, part[turn]);
         turn ^= 1;
         const float rstd = 1.0f / sqrtf(both[0] / static_cast<float>(p.D) + p.eps);
         const float m = both[1] * rstd / static_cast<float>(p.D);  // mean(a n)

@@ -102,6 +102,28 @@ def test_norm_not_finite_and_tiny():
         assert ((Q[t].double() * step[t] - y[t]).abs() <= step[t] * (0.5 + 127 * 4 * moe.RSTD)).all()
 
 
+@pytest.mark.parametrize("D", [40, 257, 4096, 8200])
+def test_norm_int8_ends_of_the_range(D):
+    """Rows whose S gain, or whose squares, lie near the ends of fp32's range while y does
+    not: quantised as finely as others."""
+    S, gain = rnd(8, 6, D), rnd(9, D)
+    scales = [2.0 ** 50, 2.0 ** -50, 1.0, 2.0 ** 20, 2.0 ** -20, 1.0]
+    S = (S.float() * torch.tensor(scales, device="cuda").unsqueeze(1)).to(BF16)
+    S[5] = 0
+    S[5, D // 2] = 2.0 ** -60  # one value
+    for by in (2.0 ** 60, 2.0 ** -60, 2.0 ** 110, 2.0 ** -110):
+        g = (gain.float() * by).to(BF16)
+        Q, scale = torch.full((6, D), 99, device="cuda", dtype=torch.int8), nan(6, dtype=F32)
+        pg.rmsnorm_i8(6, D, S, None, g, 1e-30, None, Q, scale)
+        y, _, _, _ = moe.norm(S, g, 1e-30)
+        step = y.abs().amax(1) / 127
+        # (a scale below the normal range is off by half of 2^-149 in itself)
+        assert ((scale.double() - step).abs() <= step * (2 * moe.RSTD) + 2.0 ** -150).all()
+        off = (Q.double() * step.unsqueeze(1) - y).abs()
+        assert (off <= step.unsqueeze(1) * (0.5 + 127 * 4 * moe.RSTD)).all()
+        assert (Q.abs().amax(1) == 127).all()
+
+
 @pytest.mark.parametrize("T,D", NORMS + [(5000, 136), (2500, 1030)])
 def test_norm_backward(T, D):
     S, gain, dY, dS = rnd(11, T, D, std=2.0), rnd(12, D), rnd(13, T, D), rnd(14, T, D)
