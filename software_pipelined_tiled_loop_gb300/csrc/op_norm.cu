@@ -12,8 +12,10 @@
 // operands have the same pitch and 16-byte-aligned bases, so a row starts at the same place
 // of a 16-byte vector in each: a thread takes whole aligned vectors (eight elements of the
 // flat matrix), masked at the row's two ends, whatever the width.  Bound by HBM: 8192 x 4096
-// with a residual 42 us (6.4 TB/s), as int8 46 (5.1), backward 49 (5.5; the gains' gradient
-// and its join 5 of them); 4097 x 5120 26.7 and 31.6.  One row of 4096 1.9 us from a graph.
+// with a residual 42 us (6.4 TB/s), as int8 40 (5.9), backward 49 (5.5; the gains' gradient
+// and its join 5 of them); 4097 x 5120 26.6, 27.3 and 46.5, 4097 x 5121 32.6, 37.1 and 50;
+// rows of more than 20480 values, which do not fit a block's registers, at half that rate
+// (1024 x 32768 55, 63, 188).  One row of 4096 1.9 us from a graph.
 #include <cuda_runtime.h>
 
 #include "op_gemm.cuh"
@@ -55,30 +57,29 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                       pack_bf16(f[6], f[7]));
 }
 
-// Vector v of a row, zeros where the row is not.  (At the row's ends the neighbour's
-// elements are read with it and dropped; only the matrix's last vector may pass its end.)
+// The aligned vector that holds vector v of a row: at the row's ends the neighbours'
+// elements come with it (row_mask drops them, when the vector is used and not here, where
+// that would wait for it); only the matrix's last vector may pass its end.
 __device__ __forceinline__ uint4 row_load(const uint16_t *p, const RowSpan &r, int v) {
     const long long from = r.first + 8ll * v;
     const uint16_t *at = p + from;
-    if (r.whole(v)) return *reinterpret_cast<const uint4 *>(at);
+    if (from + 8 <= r.end) return *reinterpret_cast<const uint4 *>(at);
     uint32_t w[4] = {0u, 0u, 0u, 0u};
-    if (from + 8 <= r.end) {
-        const uint4 x = *reinterpret_cast<const uint4 *>(at);
-        w[0] = x.x;
-        w[1] = x.y;
-        w[2] = x.z;
-        w[3] = x.w;
-    } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (from + i < r.end) w[i / 2] |= static_cast<uint32_t>(at[i]) << (i % 2 * 16);
-    }
+    for (int i = 0; i < 8; ++i)
+        if (from + i < r.end) w[i / 2] |= static_cast<uint32_t>(at[i]) << (i % 2 * 16);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// Zeros where the row is not.
+__device__ __forceinline__ void row_mask(uint4 &x, const RowSpan &r, int v) {
+    if (r.whole(v)) return;
+    uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int c = r.col(v) + i;
         if (c < 0 || c >= r.D) w[i / 2] &= i % 2 ? 0xffffu : 0xffff0000u;
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    x = make_uint4(w[0], w[1], w[2], w[3]);
 }
 __device__ __forceinline__ void row_store(uint16_t *p, const RowSpan &r, int v, const uint4 &x) {
     uint16_t *at = p + r.first + 8ll * v;
@@ -166,8 +167,9 @@ struct NormParams {
     int early;     // op_begin_early
 };
 
-// The gains of a thread's vectors: where rows start on vectors the same for every row, else
-// fetched with each.
+// The gains of a thread's vectors.  A block's rows are a multiple of eight apart (norm_grid),
+// so all of them start at the same place of a vector, and a thread has the same columns in
+// each.
 template <int V>
 __device__ __forceinline__ void gains_load(const NormParams &p, const RowSpan &row,
                                            uint4 (&gains)[V]) {
@@ -178,16 +180,17 @@ __device__ __forceinline__ void gains_load(const NormParams &p, const RowSpan &r
     }
 }
 
-// V vectors a thread; ALIGNED: D is a multiple of 8.  With more than two vectors a thread
-// the next row is not fetched ahead, for want of registers.
-template <int V, bool ALIGNED, bool I8>
-__global__ void __launch_bounds__(V <= 2 ? 512 : 1024) rmsnorm_kernel(const NormParams p) {
+// V vectors a thread, up to MOST threads; ALIGNED: D is a multiple of 8.  (Held to 64
+// registers where rows are aligned and not wide: int8 8192 x 4096 39.9 us against 48.7; of
+// other rows 4097 x 5121 would take 48.6 against 37.1, so those are left to the compiler.)
+template <int V, int MOST, bool ALIGNED, bool I8>
+__global__ void __launch_bounds__(MOST, ALIGNED && V <= 2 ? 2 : 0) rmsnorm_kernel(const NormParams p) {
     __shared__ uint32_t part[2][2][32];
-    constexpr bool AHEAD = V <= 2;
+    constexpr bool AHEAD = MOST <= 512;  // (more leave no registers for the next row)
     op_begin_early(p.early);
     int turn = 0;
-    uint4 a[V], b[V], gains[V], gains_next[ALIGNED ? 1 : V];
-    if (ALIGNED) gains_load(p, RowSpan(0, p.T, p.D), gains);
+    uint4 a[V], b[V], gains[V];
+    gains_load(p, RowSpan(ALIGNED ? 0 : blockIdx.x, p.T, p.D), gains);
     auto fetch = [&](unsigned t) {
         const RowSpan row(t, p.T, p.D);
 #pragma unroll
@@ -199,7 +202,6 @@ __global__ void __launch_bounds__(V <= 2 ? 512 : 1024) rmsnorm_kernel(const Norm
                 if (p.r) b[i] = row_load(p.r, row, v);
             }
         }
-        if constexpr (!ALIGNED) gains_load(p, row, gains_next);
     };
     const unsigned T = p.T;  // (unsigned: a step behind the last row may pass 2^31)
     unsigned t = blockIdx.x;
@@ -208,15 +210,15 @@ __global__ void __launch_bounds__(V <= 2 ? 512 : 1024) rmsnorm_kernel(const Norm
         if (!AHEAD) fetch(t);
         const RowSpan row(t, p.T, p.D);
         uint4 s[V];
-        if constexpr (!ALIGNED) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) gains[i] = gains_next[i];
-        }
         float sum[1] = {0.0f};  // of squares
         uint32_t most = 0u;     // int8: the largest |S gain|
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int v = threadIdx.x + i * blockDim.x;
+            if (!ALIGNED && v < row.vecs) {
+                row_mask(a[i], row, v);
+                row_mask(b[i], row, v);
+            }
             float f[8];
             unpack8(a[i], f);
             s[i] = a[i];
@@ -329,32 +331,34 @@ __global__ void __launch_bounds__(V <= 2 ? 512 : 1024) rmsnorm_kernel(const Norm
     }
 }
 
-// The gains' gradient: each block leaves the sums of its rows' dY n for norm_join_kernel.
-// Rows that start on vectors give a thread the same columns every time, and the sums stay
-// in its registers; others are added in shared memory, column c at (c % 8) * pitch + c / 8,
-// so that a warp's eight elements a lane fall on different banks.
+// The gains' gradient: each block leaves the sums of its rows' dY n for norm_join_kernel.  A
+// thread keeps its columns' in its registers, or where a row is so wide that it has more
+// than two vectors, in places of its own in shared memory.
 enum class GainSum { NONE, REGISTERS, SHARED };
 
-template <int V, bool ALIGNED, GainSum SUM>
-__global__ void __launch_bounds__(V <= 2 ? 512 : 1024) rmsnorm_backward_kernel(const NormParams p) {
-    extern __shared__ float sums[];
+template <int V, int MOST, bool ALIGNED, GainSum SUM>
+__global__ void __launch_bounds__(MOST) rmsnorm_backward_kernel(const NormParams p) {
+    extern __shared__ float4 sums[];  // [V][2][threads]
     __shared__ uint32_t part[2][2][32];
-    constexpr bool AHEAD = V <= 2;
-    static_assert(SUM != GainSum::REGISTERS || ALIGNED, "columns move from row to row");
-    const int pitch = (p.D + 7) / 8;
-    if (SUM == GainSum::SHARED) {
-        for (int i = threadIdx.x; i < 8 * pitch; i += blockDim.x) sums[i] = 0.0f;
-        __syncthreads();
-    }
-    float own[SUM == GainSum::REGISTERS ? V : 1][8];
+    constexpr bool AHEAD = V <= 2;  // (more leave no registers for the next row)
+    constexpr int OWN = SUM == GainSum::REGISTERS ? V : 1;
+    float own[OWN][8];
 #pragma unroll
-    for (int i = 0; i < (SUM == GainSum::REGISTERS ? V : 1); ++i)
+    for (int i = 0; i < OWN; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) own[i][j] = 0.0f;
+    auto place = [&](int i, int h) -> float4 & {
+        return sums[(2 * i + h) * blockDim.x + threadIdx.x];
+    };
+    if constexpr (SUM == GainSum::SHARED) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            place(i, 0) = place(i, 1) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
     op_begin_early(p.early);
     int turn = 0;
-    uint4 s[V], dy[V], ds[V], gains[V], gains_next[ALIGNED ? 1 : V];
-    if (ALIGNED) gains_load(p, RowSpan(0, p.T, p.D), gains);
+    uint4 s[V], dy[V], ds[V], gains[V];
+    gains_load(p, RowSpan(ALIGNED ? 0 : blockIdx.x, p.T, p.D), gains);
     auto fetch = [&](unsigned t, uint4 (&s)[V], uint4 (&dy)[V], uint4 (&ds)[V]) {
         const RowSpan row(t, p.T, p.D);
 #pragma unroll
@@ -367,22 +371,21 @@ __global__ void __launch_bounds__(V <= 2 ? 512 : 1024) rmsnorm_backward_kernel(c
                 if (p.ds) ds[i] = row_load(p.ds, row, v);
             }
         }
-        if constexpr (!ALIGNED) gains_load(p, row, gains_next);
     };
     const unsigned T = p.T;
     unsigned t = blockIdx.x;
     if (t < T) fetch(t, s, dy, ds);
     for (; t < T; t += gridDim.x) {
         const RowSpan row(t, p.T, p.D);
-        if constexpr (!ALIGNED) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) gains[i] = gains_next[i];
-        }
         float both[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int v = threadIdx.x + i * blockDim.x;
             if (v >= row.vecs) break;
+            if (!ALIGNED) {
+                row_mask(s[i], row, v);
+                row_mask(dy[i], row, v);
+            }
             float fs[8], fd[8], g[8];
             unpack8(s[i], fs);
             unpack8(dy[i], fd);
@@ -410,25 +413,29 @@ __global__ void __launch_bounds__(V <= 2 ? 512 : 1024) rmsnorm_backward_kernel(c
             unpack8(dy[i], fd);
             unpack8(gains[i], g);
             unpack8(ds[i], o);
+            float more[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float n = fs[j] * rstd;
                 o[j] += rstd * fmaf(-n, m, fd[j] * g[j]);
-                if constexpr (SUM == GainSum::REGISTERS) {
+                if constexpr (SUM == GainSum::REGISTERS)
                     own[i][j] = fmaf(fd[j], n, own[i][j]);
-                } else if constexpr (SUM == GainSum::SHARED) {
-                    const int c = row.col(v) + j;
-                    if (c >= 0 && c < p.D) {
-                        float *at = sums + (c & 7) * pitch + (c >> 3);
-                        *at = fmaf(fd[j], n, *at);
-                    }
+                else
+                    more[j] = fd[j] * n;
+            }
+            if constexpr (SUM == GainSum::SHARED) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float4 at = place(i, h);
+                    at.x += more[4 * h];
+                    at.y += more[4 * h + 1];
+                    at.z += more[4 * h + 2];
+                    at.w += more[4 * h + 3];
+                    place(i, h) = at;
                 }
             }
             if (p.dx) row_store(p.dx, row, v, pack8(o));
         }
-        // (columns that move to other threads with the next row: a barrier of its
-        // block_reduce stands between, or this)
-        __syncwarp();
         if (AHEAD) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
@@ -440,20 +447,33 @@ __global__ void __launch_bounds__(V <= 2 ? 512 : 1024) rmsnorm_backward_kernel(c
             fetch(after, s, dy, ds);
         }
     }
-    float *out = p.dgain + static_cast<long long>(blockIdx.x) * p.D;
-    if constexpr (SUM == GainSum::REGISTERS) {
+    if constexpr (SUM != GainSum::NONE) {
+        float *out = p.dgain + static_cast<long long>(blockIdx.x) * p.D;
+        const RowSpan row(blockIdx.x, p.T, p.D);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int c = 8 * (threadIdx.x + i * blockDim.x);
-            if (c >= p.D) break;
-            *reinterpret_cast<float4 *>(out + c) =
-                make_float4(own[i][0], own[i][1], own[i][2], own[i][3]);
-            *reinterpret_cast<float4 *>(out + c + 4) =
-                make_float4(own[i][4], own[i][5], own[i][6], own[i][7]);
+            const int v = threadIdx.x + i * blockDim.x;
+            if (v >= row.vecs) break;
+            float4 x[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if constexpr (SUM == GainSum::SHARED)
+                    x[h] = place(i, h);
+                else
+                    x[h] = make_float4(own[i][4 * h], own[i][4 * h + 1], own[i][4 * h + 2],
+                                       own[i][4 * h + 3]);
+            }
+            const int c = row.col(v);
+            if constexpr (ALIGNED) {
+                *reinterpret_cast<float4 *>(out + c) = x[0];
+                *reinterpret_cast<float4 *>(out + c + 4) = x[1];
+            } else {
+                const float f[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (c + j >= 0 && c + j < p.D) out[c + j] = f[j];
+            }
         }
-    } else if constexpr (SUM == GainSum::SHARED) {
-        __syncthreads();
-        for (int c = threadIdx.x; c < p.D; c += blockDim.x) out[c] = sums[(c & 7) * pitch + (c >> 3)];
     }
 }
 
@@ -480,8 +500,8 @@ __global__ void __launch_bounds__(1024)
     }
 }
 
-// f(vectors a thread, whether rows start on vectors) as constants, and threads.  Two vectors
-// a thread or one (`one`: up to 512): forward, two are quicker with rows for every SM (8192 x
+// f(vectors a thread, threads at most, whether rows start on vectors) as constants, and
+// threads.  Two vectors a thread or one (`one`: up to 512): forward, two are quicker with rows for every SM (8192 x
 // 4096 41.7 us against 48.9, 1500 x 4096 6.8 against 7.7) and one where a row's own latency
 // counts (1 x 4096 1.8 against 2.0); backward, whose thread holds three operands and the next
 // row's, one is (8192 x 4096 48.9 against 53.2, 400 x 4096 7.4 against 9.0).
@@ -489,13 +509,21 @@ template <class F>
 static pgemm_status with_row(int D, bool one, F &&f) {
     const int vecs = D % 8 == 0 ? D / 8 : (D + 14) / 8;
     using std::integral_constant;
-    auto pick = [&](auto v) {
+    auto pick = [&](auto v, auto most) {
         const int threads = op_blocks(op_blocks(vecs, decltype(v)::value), 32) * 32;
-        return D % 8 == 0 ? f(v, std::true_type{}, threads) : f(v, std::false_type{}, threads);
+        return D % 8 == 0 ? f(v, most, std::true_type{}, threads)
+                          : f(v, most, std::false_type{}, threads);
     };
-    if (vecs <= (one ? 512 : 32)) return pick(integral_constant<int, 1>{});
-    if (vecs <= 1024) return pick(integral_constant<int, 2>{});
-    return pick(integral_constant<int, 5>{});
+    const integral_constant<int, 512> few;
+    if (vecs <= (one ? 512 : 32)) return pick(integral_constant<int, 1>{}, few);
+    if (vecs <= 1024) return pick(integral_constant<int, 2>{}, few);
+    if (vecs <= 2560) return pick(integral_constant<int, 5>{}, few);
+    return pick(integral_constant<int, 5>{}, integral_constant<int, 832>{});
+}
+
+// Blocks for T rows, `most` at most: a multiple of eight where a block has more than one.
+static unsigned norm_grid(int T, long long most) {
+    return static_cast<unsigned>(T <= most ? T : most < 8 ? 1 : most / 8 * 8);
 }
 
 static pgemm_status norm_check(int T, int D) {
@@ -527,14 +555,14 @@ static pgemm_status norm_forward(bool i8, int T, int D, const uint16_t *X, const
     p.y = i8 ? nullptr : static_cast<uint16_t *>(out);
     p.q = i8 ? static_cast<int8_t *>(out) : nullptr;
     p.scale = scale;
-    return with_row(D, T < 2 * dev.sm_count, [&](auto v, auto aligned, int threads) {
-        constexpr int V = decltype(v)::value;
+    return with_row(D, T < 2 * dev.sm_count, [&](auto v, auto limit, auto aligned, int threads) {
+        constexpr int V = decltype(v)::value, MOST = decltype(limit)::value;
         constexpr bool A = decltype(aligned)::value;
         const long long most = dev.sm_count * (threads >= 64 ? 2048ll / threads : 32ll);
-        const dim3 grid(static_cast<unsigned>(T < most ? T : most));
+        const dim3 grid(norm_grid(T, most));
         p.early = op_early(dev, grid.x);
-        return i8 ? launch_small(rmsnorm_kernel<V, A, true>, grid, dim3(threads), s, p)
-                  : launch_small(rmsnorm_kernel<V, A, false>, grid, dim3(threads), s, p);
+        return i8 ? launch_small(rmsnorm_kernel<V, MOST, A, true>, grid, dim3(threads), s, p)
+                  : launch_small(rmsnorm_kernel<V, MOST, A, false>, grid, dim3(threads), s, p);
     });
 }
 
@@ -564,24 +592,23 @@ static pgemm_status norm_backward(int T, int D, const uint16_t *S, const uint16_
     p.dy = dY;
     p.ds = dS;
     p.dx = dX;
-    return with_row(D, true, [&](auto v, auto aligned, int threads) -> pgemm_status {
-        constexpr int V = decltype(v)::value;
+    return with_row(D, true, [&](auto v, auto limit, auto aligned, int threads) -> pgemm_status {
+        constexpr int V = decltype(v)::value, MOST = decltype(limit)::value;
         constexpr bool A = decltype(aligned)::value;
-        constexpr GainSum SUM = A && V <= 2 ? GainSum::REGISTERS : GainSum::SHARED;
+        constexpr GainSum SUM = V <= 2 ? GainSum::REGISTERS : GainSum::SHARED;
         // blocks of an SM: what registers and shared memory allow, eight at most, since
         // each leaves a row of sums behind
-        const int smem = dgain && SUM == GainSum::SHARED ? (D + 7) / 8 * 32 : 0;
+        const int smem = dgain && SUM == GainSum::SHARED ? 32 * V * threads : 0;
         int per_sm = threads <= 128 ? 8 : 1024 / threads;
         while (per_sm > 1 && per_sm * (smem + 2048) > kSmemPerSm) --per_sm;
-        const int most = dev.sm_count * per_sm;
-        const int blocks = T < most ? T : most;
+        const int blocks = norm_grid(T, static_cast<long long>(dev.sm_count) * per_sm);
         p.early = op_early(dev, blocks);
         OpArena arena(dev, s);
         const long long at = arena.add(dgain ? 4ll * blocks * D : 0);
         pgemm_status e = arena.alloc();
         if (e != PGEMM_OK) return e;
         if (!dgain)
-            return launch_small(rmsnorm_backward_kernel<V, A, GainSum::NONE>, dim3(blocks),
+            return launch_small(rmsnorm_backward_kernel<V, MOST, A, GainSum::NONE>, dim3(blocks),
                                 dim3(threads), s, p);
         NormParams q = p;
         q.dgain = arena.at<float>(at);
@@ -589,13 +616,13 @@ static pgemm_status norm_backward(int T, int D, const uint16_t *S, const uint16_
             static const KernelInfo info = [] {
                 KernelInfo k;
                 k.threads = 32;
-                k.smem_bytes = kNormMaxD * 4;
-                k.func = reinterpret_cast<const void *>(rmsnorm_backward_kernel<V, A, SUM>);
+                k.smem_bytes = 32 * V * MOST;
+                k.func = reinterpret_cast<const void *>(rmsnorm_backward_kernel<V, MOST, A, SUM>);
                 return k;
             }();
             if ((e = op_kernel_setup(dev, info, nullptr)) != PGEMM_OK) return e;
         }
-        e = launch_small_smem(rmsnorm_backward_kernel<V, A, SUM>, dim3(blocks), dim3(threads),
+        e = launch_small_smem(rmsnorm_backward_kernel<V, MOST, A, SUM>, dim3(blocks), dim3(threads),
                               smem, s, q);
         if (e != PGEMM_OK) return e;
         return launch_small(norm_join_kernel, dim3(op_blocks(D, 32)), dim3(1024), s,
