@@ -22,7 +22,7 @@ SOURCES = ["api.cu", "gemm_f32.cu", "gemm_bf16.cu", "gemm_i8.cu", "gemm_i8_imma.
            "stage_reuse.cu", "op_products.cu", "op_linear.cu", "op_gated.cu", "op_xent.cu",
            "op_tokens.cu", "op_norm.cu", "op_route.cu", "op_experts.cu"]
 HEADERS = ["ptx.cuh", "common.cuh", "tc_gemm.cuh", "kernels.h", "widen.cuh", "op_act.cuh",
-           "op_gemm.cuh", "op_host.h"]
+           "op_gemm.cuh", "op_host.h", "op_rows.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", *ARCH, "-Xcompiler", "-fPIC",
          "-Xcompiler", "-fvisibility=hidden", "-I", INCLUDE]

@@ -20,80 +20,11 @@
 
 #include "op_gemm.cuh"
 #include "op_host.h"
+#include "op_rows.cuh"
 
 namespace pg {
 
 constexpr int kNormMaxD = 32768;
-
-// One row as a block of threads holds it: vector v covers the elements 8 v - shift ..
-// 8 v - shift + 7 of the row.
-struct RowSpan {
-    long long first;  // flat index of vector 0's first element (a multiple of 8)
-    long long end;    // elements of the matrix
-    int shift, vecs, D;
-    __device__ __forceinline__ RowSpan(long long row, int T, int D_) : D(D_) {
-        const long long at = row * D_;
-        end = static_cast<long long>(T) * D_;
-        shift = static_cast<int>(at & 7);
-        first = at - shift;
-        vecs = (D_ + shift + 7) >> 3;
-    }
-    __device__ __forceinline__ int col(int v) const { return 8 * v - shift; }
-    __device__ __forceinline__ bool whole(int v) const {
-        return col(v) >= 0 && col(v) + 8 <= D;
-    }
-};
-
-__device__ __forceinline__ void unpack8(const uint4 &x, float (&f)[8]) {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = bf16_lo(w[i]);
-        f[2 * i + 1] = bf16_hi(w[i]);
-    }
-}
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-    return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
-                      pack_bf16(f[6], f[7]));
-}
-
-// The aligned vector that holds vector v of a row: at the row's ends the neighbours'
-// elements come with it (row_mask drops them, when the vector is used and not here, where
-// that would wait for it); only the matrix's last vector may pass its end.
-__device__ __forceinline__ uint4 row_load(const uint16_t *p, const RowSpan &r, int v) {
-    const long long from = r.first + 8ll * v;
-    const uint16_t *at = p + from;
-    if (from + 8 <= r.end) return *reinterpret_cast<const uint4 *>(at);
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (from + i < r.end) w[i / 2] |= static_cast<uint32_t>(at[i]) << (i % 2 * 16);
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-// Zeros where the row is not.
-__device__ __forceinline__ void row_mask(uint4 &x, const RowSpan &r, int v) {
-    if (r.whole(v)) return;
-    uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int c = r.col(v) + i;
-        if (c < 0 || c >= r.D) w[i / 2] &= i % 2 ? 0xffffu : 0xffff0000u;
-    }
-    x = make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ void row_store(uint16_t *p, const RowSpan &r, int v, const uint4 &x) {
-    uint16_t *at = p + r.first + 8ll * v;
-    if (r.whole(v)) {
-        *reinterpret_cast<uint4 *>(at) = x;
-        return;
-    }
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int c = r.col(v) + i;
-        if (c >= 0 && c < r.D) at[i] = static_cast<uint16_t>(w[i / 2] >> (i % 2 * 16));
-    }
-}
 
 // The gains of vector v's columns (ones without gains; anything where the row is not).
 __device__ __forceinline__ uint4 gain_load(const uint16_t *g, const RowSpan &r, int v) {

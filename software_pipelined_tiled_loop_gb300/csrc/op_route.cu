@@ -19,6 +19,7 @@
 
 #include "op_gemm.cuh"
 #include "op_host.h"
+#include "op_rows.cuh"
 
 namespace pg {
 
@@ -521,9 +522,11 @@ static pgemm_status expert_sort_run(int T, int E, int k, const int32_t *experts,
 }
 
 // ----------------------------------------------------- gather and combine ---
-// Rows as vectors of W bf16 values: 8 where rows are multiples of 16 bytes, else 2 or 1
-// (a token's row and its sorted rows then start at different places of a vector).  The k
-// sorted rows of a token travel together.
+// Rows as 16-byte vectors.  Where D is a multiple of 8 all rows start on one.  Elsewhere a
+// row that is written, or summed into, is taken in the aligned vectors that it fills, the
+// other rows' eight values are shifted out of the two vectors that hold them, and the values
+// at its two ends go one to a lane.  8192 tokens, four rows of 4097 values: gather 69 us,
+// combine 95, its gradient 115 (one by one 165, 136 and 189).
 struct RowsParams {
     int T, k, D;
     long long rows;  // T k: a slot_row outside [0, rows) does not count
@@ -535,55 +538,6 @@ struct RowsParams {
     float *dweights;
     int early;                // op_begin_early
 };
-
-template <int W>
-struct Vec;
-template <>
-struct Vec<8> {
-    using T = uint4;
-};
-template <>
-struct Vec<2> {
-    using T = uint32_t;
-};
-template <>
-struct Vec<1> {
-    using T = uint16_t;
-};
-
-template <int W>
-__device__ __forceinline__ void vec_get(const typename Vec<W>::T &x, float (&f)[W]) {
-    if constexpr (W == 8) {
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = bf16_lo(w[i]);
-            f[2 * i + 1] = bf16_hi(w[i]);
-        }
-    } else if constexpr (W == 2) {
-        f[0] = bf16_lo(x);
-        f[1] = bf16_hi(x);
-    } else {
-        f[0] = __uint_as_float(static_cast<uint32_t>(x) << 16);
-    }
-}
-template <int W>
-__device__ __forceinline__ typename Vec<W>::T vec_put(const float (&f)[W]) {
-    if constexpr (W == 8)
-        return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
-                          pack_bf16(f[6], f[7]));
-    else if constexpr (W == 2)
-        return pack_bf16(f[0], f[1]);
-    else
-        return static_cast<uint16_t>(pack_bf16(f[0], 0.0f) & 0xffffu);
-}
-template <int W>
-__device__ __forceinline__ typename Vec<W>::T vec_zero() {
-    if constexpr (W == 8)
-        return make_uint4(0u, 0u, 0u, 0u);
-    else
-        return 0;
-}
 
 constexpr int kRowsThreads = 256;
 constexpr int kAhead = 4;  // sorted rows on the way
@@ -605,36 +559,63 @@ struct RowsAt {
     }
 };
 
-// A vector of all tokens' a thread.  Bound by HBM: 8192 tokens to four rows of 4096 values
-// each, 51 us, 6.6 TB/s.
-template <int W>
+// Rows of whole vectors: a vector of all tokens' a thread.  Bound by HBM: 8192 tokens to four
+// rows of 4096 values each, 51 us, 6.6 TB/s.
 __global__ void __launch_bounds__(kRowsThreads) gather_kernel(const RowsParams p) {
-    using V = typename Vec<W>::T;
     op_begin_early(p.early);
-    const unsigned vecs = p.D / W;
+    const unsigned vecs = p.D / 8;
     const unsigned long long total = static_cast<unsigned long long>(p.T) * vecs;
     for (unsigned long long i = blockIdx.x * static_cast<unsigned long long>(kRowsThreads) + threadIdx.x;
          i < total; i += static_cast<unsigned long long>(gridDim.x) * kRowsThreads) {
         const RowsAt at(i, vecs);
-        const V x = reinterpret_cast<const V *>(p.x)[i];
+        const uint4 x = reinterpret_cast<const uint4 *>(p.x)[i];
         const int32_t *to = p.slot_row + at.t * p.k;
         for (int j = 0; j < p.k; ++j) {
             const int r = to[j];
             if (r >= 0 && r < p.rows)
-                reinterpret_cast<V *>(p.out + static_cast<long long>(r) * p.D)[at.v] = x;
+                reinterpret_cast<uint4 *>(p.out + static_cast<long long>(r) * p.D)[at.v] = x;
         }
     }
 }
 
-// Rows of whole 16-byte vectors: a vector of all tokens' a thread, and its next one's choices
-// looked up while this one's rows travel.  On twice as many blocks as run at once (four an
-// SM): 8192 tokens, four rows of 4096 values, 65 us; on five an SM 80, a block for every 256
-// vectors 69.
-template <int W>
-__global__ void __launch_bounds__(kRowsThreads) combine_flat_kernel(const RowsParams p) {
-    using V = typename Vec<W>::T;
+// Other rows: `per` threads a slot, a vector of its row each at a time.
+__global__ void __launch_bounds__(kRowsThreads) gather_any_kernel(const RowsParams p, int per) {
     op_begin_early(p.early);
-    const unsigned vecs = p.D / W;
+    const int groups = blockDim.x / per;
+    for (long long slot = blockIdx.x * static_cast<long long>(groups) + threadIdx.x / per;
+         slot < p.rows; slot += static_cast<long long>(gridDim.x) * groups) {
+        const int r = p.slot_row[slot];
+        if (r < 0 || r >= p.rows) continue;
+        const RowSpan to(r, p.rows, p.D);
+        const long long t = static_cast<uint32_t>(slot) / static_cast<uint32_t>(p.k);
+        const RowShifted from(p.x, t, p.D, to.shift);
+        const RowEnds ends(to);
+        const unsigned lane = threadIdx.x % per;
+        uint4 *out = reinterpret_cast<uint4 *>(p.out + to.first);
+        for (unsigned v = 1 + lane; v < ends.inner; v += 2 * per) {
+            uint4 lo[2], hi[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                if (v + u * per < ends.inner) {
+                    lo[u] = from.at[v + u * per];
+                    hi[u] = from.at[v + u * per + 1];
+                }
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                if (v + u * per < ends.inner) out[v + u * per] = from.value(lo[u], hi[u]);
+        }
+        const int c = lane < 32 ? ends.col(lane) : -1;
+        if (c >= 0) p.out[static_cast<long long>(r) * p.D + c] = p.x[t * p.D + c];
+    }
+}
+
+// Rows of whole vectors: a vector of all tokens' a thread, and its next one's choices
+// looked up while this one's rows travel.  On twice as many blocks as run at once (four an
+// SM): 8192 tokens, four rows of 4096 values, 64 us, 6.3 TB/s; on five an SM 80, a block for
+// every 256 vectors 69.
+__global__ void __launch_bounds__(kRowsThreads) combine_flat_kernel(const RowsParams p) {
+    op_begin_early(p.early);
+    const unsigned vecs = p.D / 8;
     const unsigned long long total = static_cast<unsigned long long>(p.T) * vecs;
     const unsigned long long step = static_cast<unsigned long long>(gridDim.x) * kRowsThreads;
     unsigned long long i = blockIdx.x * static_cast<unsigned long long>(kRowsThreads) + threadIdx.x;
@@ -647,21 +628,21 @@ __global__ void __launch_bounds__(kRowsThreads) combine_flat_kernel(const RowsPa
     };
     look_up(at, 0);
     while (true) {
-        float sum[W];
-        V res = vec_zero<W>();
-        if (p.x) res = reinterpret_cast<const V *>(p.x)[i];
+        float sum[8];
+        uint4 res = make_uint4(0u, 0u, 0u, 0u);
+        if (p.x) res = reinterpret_cast<const uint4 *>(p.x)[i];
 #pragma unroll
-        for (int c = 0; c < W; ++c) sum[c] = 0.0f;
+        for (int c = 0; c < 8; ++c) sum[c] = 0.0f;
         const unsigned long long next = i + step;
         const RowsAt after(next < total ? next : i, vecs);
         for (int j0 = 0; j0 < p.k; j0 += kAhead) {
-            V y[kAhead];
+            uint4 y[kAhead];
             bool in[kAhead];
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
                 in[j] = r[j] >= 0 && r[j] < p.rows;
                 if (in[j])
-                    y[j] = reinterpret_cast<const V *>(p.ys + static_cast<long long>(r[j]) * p.D)[at.v];
+                    y[j] = reinterpret_cast<const uint4 *>(p.ys + static_cast<long long>(r[j]) * p.D)[at.v];
             }
             if (j0 + kAhead < p.k)
                 look_up(at, j0 + kAhead);
@@ -672,99 +653,134 @@ __global__ void __launch_bounds__(kRowsThreads) combine_flat_kernel(const RowsPa
             for (int j = 0; j < kAhead; ++j)
                 if (in[j]) {
                     const float wj = w ? w[j] : 1.0f;
-                    float f[W];
-                    vec_get<W>(y[j], f);
+                    float f[8];
+                    unpack8(y[j], f);
 #pragma unroll
-                    for (int c = 0; c < W; ++c) sum[c] = fmaf(wj, f[c], sum[c]);
+                    for (int c = 0; c < 8; ++c) sum[c] = fmaf(wj, f[c], sum[c]);
                 }
         }
-        float f[W];
-        vec_get<W>(res, f);
+        float f[8];
+        unpack8(res, f);
 #pragma unroll
-        for (int c = 0; c < W; ++c) sum[c] += f[c];
-        reinterpret_cast<V *>(p.out)[i] = vec_put<W>(sum);
+        for (int c = 0; c < 8; ++c) sum[c] += f[c];
+        reinterpret_cast<uint4 *>(p.out)[i] = pack8(sum);
         if (next >= total) break;
         i = next;
         at = after;
     }
 }
 
-// Other rows: `per` threads a token, as many as it has vectors up to a block's, so that where
-// they lie is worked out once for all of a thread's.
-template <int W>
-__global__ void __launch_bounds__(kRowsThreads) combine_kernel(const RowsParams p, int per) {
-    using V = typename Vec<W>::T;
+// Other rows: `per` threads a token, so that where its rows lie is worked out once for all of
+// a thread's vectors; U of them, of AHEAD rows, on the way.  Bound by latency, so few of them
+// and four blocks an SM (8192 tokens, one row of 2047 values: 19 us with two vectors on the way,
+// 30 with four on three blocks; two rows 34, with two vectors 39).
+template <int AHEAD, int U>
+__global__ void __launch_bounds__(kRowsThreads, 4) combine_any_kernel(const RowsParams p, int per) {
     op_begin_early(p.early);
     const int groups = blockDim.x / per;
-    const unsigned vecs = p.D / W;
     for (long long t = blockIdx.x * static_cast<long long>(groups) + threadIdx.x / per; t < p.T;
          t += static_cast<long long>(gridDim.x) * groups) {
-        const int32_t *from = p.slot_row + t * p.k;
+        const int32_t *slots = p.slot_row + t * p.k;
         const float *w = p.weights ? p.weights + t * p.k : nullptr;
-        const V *row[kAhead];
-        float weight[kAhead];
+        const RowSpan to(t, p.T, p.D);
+        const RowEnds ends(to);
+        const unsigned lane = threadIdx.x % per;
+        RowShifted row[AHEAD];
+        bool in[AHEAD];
+        float weight[AHEAD];
         auto choices = [&](int j0) {
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-                const int r = j0 + j < p.k ? from[j0 + j] : -1;
-                const bool in = r >= 0 && r < p.rows;
-                row[j] = in ? reinterpret_cast<const V *>(p.ys + static_cast<long long>(r) * p.D)
-                            : nullptr;
-                weight[j] = in && w ? w[j0 + j] : 1.0f;
+            for (int j = 0; j < AHEAD; ++j) {
+                const int r = j0 + j < p.k ? slots[j0 + j] : -1;
+                weight[j] = w && j0 + j < p.k ? w[j0 + j] : 1.0f;
+                in[j] = r >= 0 && r < p.rows;
+                if (in[j]) row[j] = RowShifted(p.ys, r, p.D, to.shift);
             }
         };
-        if (p.k <= kAhead) choices(0);
-        for (unsigned v = threadIdx.x % per; v < vecs; v += per) {
-            float sum[W];
-            V res = vec_zero<W>();
-            if (p.x) res = reinterpret_cast<const V *>(p.x + t * p.D)[v];
+        if (p.k <= AHEAD) choices(0);
+        const uint4 *residual = reinterpret_cast<const uint4 *>(p.x + to.first);
+        uint4 *out = reinterpret_cast<uint4 *>(p.out + to.first);
+        for (unsigned v0 = 1 + lane; v0 < ends.inner; v0 += U * per) {
+            float sum[U][8];
+            uint4 res[U];
+            bool has[U];
 #pragma unroll
-            for (int i = 0; i < W; ++i) sum[i] = 0.0f;
-            for (int j0 = 0; j0 < p.k; j0 += kAhead) {
-                if (p.k > kAhead) choices(j0);
-                V y[kAhead];
+            for (int u = 0; u < U; ++u) {
+                has[u] = v0 + u * per < ends.inner;
+                res[u] = make_uint4(0u, 0u, 0u, 0u);
+                if (p.x && has[u]) res[u] = residual[v0 + u * per];
 #pragma unroll
-                for (int j = 0; j < kAhead; ++j)
-                    if (row[j] != nullptr) y[j] = row[j][v];
-#pragma unroll
-                for (int j = 0; j < kAhead; ++j)
-                    if (row[j] != nullptr) {
-                        float f[W];
-                        vec_get<W>(y[j], f);
-#pragma unroll
-                        for (int i = 0; i < W; ++i) sum[i] = fmaf(weight[j], f[i], sum[i]);
-                    }
+                for (int i = 0; i < 8; ++i) sum[u][i] = 0.0f;
             }
-            float f[W];
-            vec_get<W>(res, f);
+            for (int j0 = 0; j0 < p.k; j0 += AHEAD) {
+                if (p.k > AHEAD) choices(j0);
+                uint4 lo[U][AHEAD], hi[U][AHEAD];
 #pragma unroll
-            for (int i = 0; i < W; ++i) sum[i] += f[i];
-            reinterpret_cast<V *>(p.out + t * p.D)[v] = vec_put<W>(sum);
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int j = 0; j < AHEAD; ++j)
+                        if (in[j] && has[u]) {
+                            lo[u][j] = row[j].at[v0 + u * per];
+                            hi[u][j] = row[j].at[v0 + u * per + 1];
+                        }
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int j = 0; j < AHEAD; ++j)
+                        if (in[j]) {
+                            float f[8];
+                            unpack8(row[j].value(lo[u][j], hi[u][j]), f);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                sum[u][i] = fmaf(weight[j], f[i], sum[u][i]);
+                        }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float f[8];
+                unpack8(res[u], f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum[u][i] += f[i];
+                if (has[u]) out[v0 + u * per] = pack8(sum[u]);
+            }
+        }
+        const int c = lane < 32 ? ends.col(lane) : -1;
+        if (c >= 0) {
+            float sum = 0.0f;
+            for (int j = 0; j < p.k; ++j) {
+                const int r = slots[j];
+                if (r >= 0 && r < p.rows)
+                    sum = fmaf(w ? w[j] : 1.0f,
+                               bf16_at(p.ys + static_cast<long long>(r) * p.D + c), sum);
+            }
+            if (p.x) sum += bf16_at(p.x + t * p.D + c);
+            p.out[t * p.D + c] = static_cast<uint16_t>(pack_bf16(sum, 0.0f) & 0xffffu);
         }
     }
 }
 
-// PER threads a token: a warp or more.  The slots' dot products of kAhead choices at a
-// time, over the lanes' columns, then over the lanes, then over the group's warps.  Bound
-// by HBM: 8192 tokens, four rows of 4096 values, 90 us, 6.7 TB/s.
-template <int W, int PER>
-__global__ void __launch_bounds__(kRowsThreads) combine_backward_kernel(const RowsParams p) {
-    using V = typename Vec<W>::T;
+// PER threads a token: a warp or more.  The slots' dot products of AHEAD choices at a time,
+// over the lanes' columns, then over the lanes, then over the group's warps.  Each slot's row
+// in vectors of its own (ALIGNED: all rows' lie alike).  Bound by HBM: 8192 tokens, four rows
+// of 4096 values, 90 us, 6.7 TB/s.
+template <bool ALIGNED, int PER>
+__global__ void __launch_bounds__(kRowsThreads, ALIGNED ? 0 : 4)
+    combine_backward_kernel(const RowsParams p) {
     constexpr int GROUPS = kRowsThreads / PER, WARPS = PER / 32;
-    __shared__ float part[GROUPS][WARPS][kAhead];
+    constexpr int AHEAD = ALIGNED ? kAhead : kAhead / 2;
+    __shared__ float part[GROUPS][WARPS][AHEAD];
     op_begin_early(p.early);
     const int group = threadIdx.x / PER, lane = threadIdx.x % PER;
-    const unsigned vecs = p.D / W;  // (unsigned: a step may pass 2^31)
     // (every group of a block makes as many rounds: they share the barriers)
     for (long long t0 = blockIdx.x * static_cast<long long>(GROUPS); t0 < p.T;
          t0 += static_cast<long long>(gridDim.x) * GROUPS) {
         const long long t = t0 + group;
         const bool have = t < p.T;
-        for (int j0 = 0; j0 < p.k; j0 += kAhead) {
-            long long row[kAhead];
-            float w[kAhead], dot[kAhead];
+        for (int j0 = 0; j0 < p.k; j0 += AHEAD) {
+            int row[AHEAD];
+            float w[AHEAD], dot[AHEAD];
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
+            for (int j = 0; j < AHEAD; ++j) {
                 int r = -1;
                 w[j] = 1.0f;
                 dot[j] = 0.0f;
@@ -772,45 +788,89 @@ __global__ void __launch_bounds__(kRowsThreads) combine_backward_kernel(const Ro
                     r = p.slot_row[t * p.k + j0 + j];
                     if (p.weights) w[j] = p.weights[t * p.k + j0 + j];
                 }
-                row[j] = r >= 0 && r < p.rows ? static_cast<long long>(r) * p.D : -1;
+                row[j] = r < p.rows ? r : -1;
             }
-            for (unsigned v = lane; have && v < vecs; v += PER) {
-                float d[W];
-                const V x = reinterpret_cast<const V *>(p.x + t * p.D)[v];
-                V y[kAhead];
+            // eight elements of slot j's row
+            auto work = [&](int j, const uint4 &x, const uint4 &y, uint4 *out) {
+                float d[8];
+                unpack8(x, d);
                 if (p.dweights) {
+                    float f[8];
+                    unpack8(y, f);
 #pragma unroll
-                    for (int j = 0; j < kAhead; ++j)
-                        if (row[j] >= 0) y[j] = reinterpret_cast<const V *>(p.ys + row[j])[v];
+                    for (int i = 0; i < 8; ++i) dot[j] = fmaf(d[i], f[i], dot[j]);
                 }
-                vec_get<W>(x, d);
+                if (p.out) {
 #pragma unroll
-                for (int j = 0; j < kAhead; ++j) {
+                    for (int i = 0; i < 8; ++i) d[i] *= w[j];
+                    *out = pack8(d);
+                }
+            };
+            if constexpr (ALIGNED) {
+                const unsigned vecs = p.D / 8;  // (unsigned: a step may pass 2^31)
+                for (unsigned v = lane; have && v < vecs; v += PER) {
+                    const uint4 x = reinterpret_cast<const uint4 *>(p.x + t * p.D)[v];
+                    uint4 y[AHEAD];
+                    auto at = [&](int j) { return static_cast<long long>(row[j]) * p.D + 8ll * v; };
+#pragma unroll
+                    for (int j = 0; j < AHEAD; ++j)
+                        if (row[j] >= 0 && p.dweights)
+                            y[j] = *reinterpret_cast<const uint4 *>(p.ys + at(j));
+#pragma unroll
+                    for (int j = 0; j < AHEAD; ++j)
+                        if (row[j] >= 0) work(j, x, y[j], reinterpret_cast<uint4 *>(p.out + at(j)));
+                }
+            } else {
+                long long first[AHEAD];
+                unsigned inner[AHEAD];
+                RowShifted token[AHEAD];  // in slot j's vectors
+#pragma unroll
+                for (int j = 0; j < AHEAD; ++j) {
+                    inner[j] = 0;
                     if (row[j] < 0) continue;
-                    if (p.dweights) {
-                        float f[W];
-                        vec_get<W>(y[j], f);
+                    const RowSpan span(row[j], p.rows, p.D);
+                    const RowEnds ends(span);
+                    first[j] = span.first;
+                    inner[j] = ends.inner;
+                    token[j] = RowShifted(p.x, t, p.D, span.shift);
+                    const int c = lane < 32 ? ends.col(lane) : -1;
+                    if (c < 0) continue;
+                    const long long at = static_cast<long long>(row[j]) * p.D + c;
+                    const float d = bf16_at(p.x + t * p.D + c);
+                    if (p.dweights) dot[j] = d * bf16_at(p.ys + at);
+                    if (p.out)
+                        p.out[at] = static_cast<uint16_t>(pack_bf16(w[j] * d, 0.0f) & 0xffffu);
+                }
+                unsigned most = 0;
 #pragma unroll
-                        for (int i = 0; i < W; ++i) dot[j] = fmaf(d[i], f[i], dot[j]);
-                    }
-                    if (p.out) {
-                        float o[W];
+                for (int j = 0; j < AHEAD; ++j) most = max(most, inner[j]);
+                for (unsigned v = 1 + lane; v < most; v += PER) {
+                    uint4 lo[AHEAD], hi[AHEAD], y[AHEAD];
 #pragma unroll
-                        for (int i = 0; i < W; ++i) o[i] = w[j] * d[i];
-                        reinterpret_cast<V *>(p.out + row[j])[v] = vec_put<W>(o);
-                    }
+                    for (int j = 0; j < AHEAD; ++j)
+                        if (v < inner[j]) {
+                            lo[j] = token[j].at[v];
+                            hi[j] = token[j].at[v + 1];
+                            if (p.dweights)
+                                y[j] = reinterpret_cast<const uint4 *>(p.ys + first[j])[v];
+                        }
+#pragma unroll
+                    for (int j = 0; j < AHEAD; ++j)
+                        if (v < inner[j])
+                            work(j, token[j].value(lo[j], hi[j]), y[j],
+                                 reinterpret_cast<uint4 *>(p.out + first[j]) + v);
                 }
             }
             if (!p.dweights) continue;
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) dot[j] = lanes_sum(dot[j]);
+            for (int j = 0; j < AHEAD; ++j) dot[j] = lanes_sum(dot[j]);
             if constexpr (WARPS > 1) {
                 if ((lane & 31) == 0) {
 #pragma unroll
-                    for (int j = 0; j < kAhead; ++j) part[group][lane >> 5][j] = dot[j];
+                    for (int j = 0; j < AHEAD; ++j) part[group][lane >> 5][j] = dot[j];
                 }
                 __syncthreads();
-                if (lane < kAhead && have && j0 + lane < p.k) {
+                if (lane < AHEAD && have && j0 + lane < p.k) {
                     float s = 0.0f;
 #pragma unroll
                     for (int i = 0; i < WARPS; ++i) s += part[group][i][lane];
@@ -819,39 +879,31 @@ __global__ void __launch_bounds__(kRowsThreads) combine_backward_kernel(const Ro
                 __syncthreads();
             } else if (have && lane == 0) {
 #pragma unroll
-                for (int j = 0; j < kAhead; ++j)
+                for (int j = 0; j < AHEAD; ++j)
                     if (j0 + j < p.k) p.dweights[t * p.k + j0 + j] = dot[j];
             }
         }
     }
 }
 
-static int rows_width(int D) { return D % 8 == 0 ? 8 : D % 2 == 0 ? 2 : 1; }
-// threads of a token: as many as it has vectors, a warp at least, a block at most
-static int rows_per(int D) {
-    const int vecs = D / rows_width(D);
+// vectors of a row at most
+static int rows_vecs(int D) {
+    return static_cast<int>((static_cast<long long>(D) + (D % 8 == 0 ? 0 : 14)) / 8);
+}
+// Threads of a row, 32 to 256: no more than it has vectors, and no more than it takes to fill
+// the SMs, so that looking up where a row lies is paid for by as many of its vectors as can be
+// (8192 tokens, two rows of 2047 values, gradients: 32 us with 32 threads a token, 35 with 64).
+static int rows_per(const OpDevice &dev, long long rows, int D) {
+    const int vecs = rows_vecs(D);
     int per = 32;
-    while (per < vecs && per < kRowsThreads) per *= 2;
+    while (per < kRowsThreads && per < vecs && rows * per < 1024ll * dev.sm_count) per *= 2;
     return per;
 }
-// gather and combine: a vector a thread
+// a thread for each vector, D a multiple of 8
 static dim3 vectors_grid(int T, int D) {
     const long long blocks =
-        (static_cast<long long>(T) * (D / rows_width(D)) + kRowsThreads - 1) / kRowsThreads;
+        (static_cast<long long>(T) * (D / 8) + kRowsThreads - 1) / kRowsThreads;
     return dim3(static_cast<unsigned>(blocks < INT_MAX ? blocks : INT_MAX));
-}
-static dim3 rows_grid(const OpDevice &dev, int T, int per) {
-    const int blocks = op_blocks(T, kRowsThreads / per), most = dev.sm_count * 16;
-    return dim3(blocks < most ? blocks : most);
-}
-template <class F>
-static pgemm_status with_width(int D, F &&f) {
-    using std::integral_constant;
-    switch (rows_width(D)) {
-        case 8: return f(integral_constant<int, 8>{});
-        case 2: return f(integral_constant<int, 2>{});
-        default: return f(integral_constant<int, 1>{});
-    }
 }
 
 static pgemm_status rows_check(int T, int k, int D) {
@@ -881,11 +933,15 @@ static pgemm_status gather_run(int T, int k, int D, const uint16_t *X, const int
     RowsParams p = rows_params(T, k, D, slot_row);
     p.x = X;
     p.out = Xs;
-    return with_width(D, [&](auto w) {
+    if (D % 8 == 0) {
         const dim3 grid = vectors_grid(T, D);
         p.early = op_early(dev, grid.x);
-        return launch_small(gather_kernel<decltype(w)::value>, grid, dim3(kRowsThreads), s, p);
-    });
+        return launch_small(gather_kernel, grid, dim3(kRowsThreads), s, p);
+    }
+    const int per = rows_per(dev, p.rows, D);
+    const dim3 grid(op_blocks(p.rows, kRowsThreads / per));
+    p.early = op_early(dev, grid.x);
+    return launch_small(gather_any_kernel, grid, dim3(kRowsThreads), s, p, per);
 }
 
 static pgemm_status combine_run(int T, int k, int D, const uint16_t *Ys, const int32_t *slot_row,
@@ -904,22 +960,19 @@ static pgemm_status combine_run(int T, int k, int D, const uint16_t *Ys, const i
     p.ys = Ys;
     p.weights = weights;
     p.out = Y;
-    const int vecs = D / rows_width(D);
-    const int per = vecs < kRowsThreads ? op_blocks(vecs, 32) * 32 : kRowsThreads;
-    const int groups = kRowsThreads / per;
-    return with_width(D, [&](auto w) {
-        constexpr int W = decltype(w)::value;
-        if constexpr (W == 8) {
-            const unsigned all = vectors_grid(T, D).x, most = 8u * dev.sm_count;
-            p.early = op_early(dev, all);
-            return launch_small(combine_flat_kernel<W>, dim3(all < most ? all : most),
-                                dim3(kRowsThreads), s, p);
-        } else {
-            const int blocks = op_blocks(T, groups);
-            p.early = op_early(dev, blocks);
-            return launch_small(combine_kernel<W>, dim3(blocks), dim3(per * groups), s, p, per);
-        }
-    });
+    if (D % 8 == 0) {
+        const unsigned all = vectors_grid(T, D).x, most = 8u * dev.sm_count;
+        p.early = op_early(dev, all);
+        return launch_small(combine_flat_kernel, dim3(all < most ? all : most),
+                            dim3(kRowsThreads), s, p);
+    }
+    const int per = rows_per(dev, T, D);
+    const dim3 grid(op_blocks(T, kRowsThreads / per));
+    p.early = op_early(dev, grid.x);
+    auto go = [&](auto kernel) {
+        return launch_small(kernel, grid, dim3(kRowsThreads), s, p, per);
+    };
+    return k == 1 ? go(combine_any_kernel<1, 2>) : go(combine_any_kernel<2, 1>);
 }
 
 static pgemm_status combine_backward_run(int T, int k, int D, const uint16_t *Ys,
@@ -940,22 +993,25 @@ static pgemm_status combine_backward_run(int T, int k, int D, const uint16_t *Ys
     p.weights = weights;
     p.out = dYs;
     p.dweights = dweights;
-    const int per = rows_per(D);
-    return with_width(D, [&](auto w) {
-        constexpr int W = decltype(w)::value;
-        auto go = [&](auto n) {
-            const dim3 grid = rows_grid(dev, T, decltype(n)::value);
-            p.early = op_early(dev, grid.x);
-            return launch_small(combine_backward_kernel<W, decltype(n)::value>, grid,
-                                dim3(kRowsThreads), s, p);
-        };
-        switch (per) {
-            case 32: return go(std::integral_constant<int, 32>{});
-            case 64: return go(std::integral_constant<int, 64>{});
-            case 128: return go(std::integral_constant<int, 128>{});
-            default: return go(std::integral_constant<int, 256>{});
-        }
-    });
+    auto go = [&](auto aligned, auto n) {
+        constexpr int PER = decltype(n)::value;
+        const int blocks = op_blocks(T, kRowsThreads / PER), most = dev.sm_count * 16;
+        const dim3 grid(blocks < most ? blocks : most);
+        p.early = op_early(dev, grid.x);
+        return launch_small(combine_backward_kernel<decltype(aligned)::value, PER>, grid,
+                            dim3(kRowsThreads), s, p);
+    };
+    auto pick = [&](auto aligned) {
+        using std::integral_constant;
+        // (whole vectors of long rows have enough on the way with a block a token: 8192
+        // tokens, four rows of 4096 values, 90 us, by the rule 94; of 1024 30 and 24)
+        const int per = rows_per(dev, decltype(aligned)::value && D > 2048 ? 1 : T, D);
+        if (per == 32) return go(aligned, integral_constant<int, 32>{});
+        if (per == 64) return go(aligned, integral_constant<int, 64>{});
+        if (per == 128) return go(aligned, integral_constant<int, 128>{});
+        return go(aligned, integral_constant<int, 256>{});
+    };
+    return D % 8 == 0 ? pick(std::true_type{}) : pick(std::false_type{});
 }
 
 }  // namespace pg
