@@ -642,6 +642,24 @@ __device__ __forceinline__ WeightsUnit weights_unit(const ExpertsArgs &a, int u)
     return w;
 }
 
+// Zeros for an expert without rows: part `i` of `parts` of its matrix, `size` elements at p,
+// by the pair's epilogue warps, `thread` of 512.
+__device__ __forceinline__ void put_zeros(uint16_t *p, long long size, int i, int parts,
+                                          unsigned thread) {
+    const long long share = ((size - 1) / parts + 8) / 8 * 8;
+    const long long lo = min(size, i * share), hi = min(size, lo + share);
+    uint16_t *begin = p + lo, *end = p + hi;
+    // whole vectors from `a` to `z`
+    const int head = static_cast<int>((0u - static_cast<unsigned>(
+                                                reinterpret_cast<uintptr_t>(begin) >> 1)) & 7u);
+    uint16_t *a = begin + min(hi - lo, static_cast<long long>(head));
+    uint16_t *z = a + (end - a) / 8 * 8;
+    for (uint16_t *at = a + 8ll * thread; at < z; at += 8 * 512)
+        *reinterpret_cast<uint4 *>(at) = make_uint4(0u, 0u, 0u, 0u);
+    if (begin + thread < a) begin[thread] = 0;
+    if (z + thread < end) z[thread] = 0;
+}
+
 // put_rows32_batch for a matrix of a 3-D map.
 template <int B, class Ctx>
 __device__ __forceinline__ void put_rows32_batch_3d(Ctx &c, const CUtensorMap *map, int z, int col,
@@ -912,27 +930,28 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         for (int u = slot; u < units; u += slots) {
             const WeightsUnit w = weights_unit<Cfg>(a, u);
             c.m0 = w.m0 + crank * BM + static_cast<int>(q * 32);
+            uint16_t *matrix = (w.seg ? a.out2 : a.out) +
+                               static_cast<long long>(w.expert) * a.K * a.M;
+            if (w.end <= w.begin) {
+                put_zeros(matrix, static_cast<long long>(a.K) * a.M,
+                          w.m0 / (BM * 2) * a.n_seg + w.n0 / BN, a.f_tiles * a.n_seg,
+                          crank * 256 + e * 32 + lane);
+                continue;
+            }
             const uint32_t ab = n & 1u;
-            const bool have = w.end > w.begin;
             constexpr int C = Cfg::EPI_COLS / 32, B = C < Cfg::NBUF ? C : Cfg::NBUF;
             uint32_t v[32 * C];
-            if (have) {
-                if (!mbar_wait(&acc_full[ab], (n >> 1) & 1u, ctx, kSiteEpilogueFull)) break;
-                tc_fence_after();
-                const uint32_t t_row = tmem + ((q * 32u) << 16) + ab * BN + col0;
+            if (!mbar_wait(&acc_full[ab], (n >> 1) & 1u, ctx, kSiteEpilogueFull)) break;
+            tc_fence_after();
+            const uint32_t t_row = tmem + ((q * 32u) << 16) + ab * BN + col0;
 #pragma unroll
-                for (int b = 0; b < C; ++b)
-                    tmem_ld_32x32b_x32(t_row + 32 * b,
-                                       *reinterpret_cast<uint32_t(*)[32]>(v + 32 * b));
-                tmem_ld_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[ab]), 0));
-                ++n;
-            } else {
-#pragma unroll
-                for (int j = 0; j < 32 * C; ++j) v[j] = 0u;
-            }
+            for (int b = 0; b < C; ++b)
+                tmem_ld_32x32b_x32(t_row + 32 * b, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * b));
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[ab]), 0));
+            ++n;
 #pragma unroll
             for (int j = 0; j < 16 * C; ++j)
                 v[j] = pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
@@ -945,11 +964,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                     put_rows32_batch_3d<B>(c, &maps.c[w.seg], w.expert, w.n0 + col0 + 32 * b,
                                            v + 16 * b);
             } else {
-                uint16_t *o = (w.seg ? a.out2 : a.out) +
-                              static_cast<long long>(w.expert) * a.K * a.M;
 #pragma unroll
                 for (int b = 0; b < C; ++b)
-                    put_rows32(c, nullptr, o, a.M, w.n0 + col0 + 32 * b, v + 16 * b);
+                    put_rows32(c, nullptr, matrix, a.M, w.n0 + col0 + 32 * b, v + 16 * b);
             }
         }
         if (lane == 0) bulk_wait_all();  // this warp's stores have landed
@@ -977,21 +994,23 @@ struct ExpSizes {
 // --------------------------------------------------------------- relayout ---
 // Matrices whose rows are no multiples of 16 bytes, to a pitch that TMA reads: many short
 // rows (an expert's weights), so a thread takes 16-byte vectors of the whole copy in turn,
-// each shifted out of the two aligned ones that cover it.  Bound by HBM: 171 MB in rows of
-// 1686 bytes in 55 us, 6.2 TB/s (a block a row at a time: 117).
+// each shifted out of the two aligned ones that cover it.  blockIdx.y is the expert: those
+// without rows are not copied.  Bound by HBM: 171 MB in rows of 1686 bytes in 55 us, 6.2 TB/s
+// (a block a row at a time: 117).
 struct RelayoutParams {
     const uint16_t *src;
     uint16_t *dst;
-    unsigned long long vecs;  // of the copy
+    unsigned long long rows, vecs;  // of a matrix's copy
     unsigned row_vecs, cols;
-    long long ld, end;        // elements of a row of the copy, and of the source
-    const int32_t *offsets;   // experts without rows stay uncopied (nullptr: all rows)
-    unsigned expert_rows;     // matrix rows of an expert
-    int early;                // op_begin_early
+    long long ld, end;       // elements of a row of the copy, and of the source
+    const int32_t *offsets;  // nullptr: one matrix
+    int early;               // op_begin_early
 };
 
 __global__ void __launch_bounds__(256) relayout_kernel(const RelayoutParams p) {
     op_begin_early(p.early);
+    const unsigned e = blockIdx.y;
+    if (p.offsets != nullptr && p.offsets[e + 1] <= p.offsets[e]) return;
     constexpr int AHEAD = 4;
     const unsigned long long first = blockIdx.x * (256ull * AHEAD) + threadIdx.x;
     uint4 lo[AHEAD], hi[AHEAD];
@@ -1005,13 +1024,10 @@ __global__ void __launch_bounds__(256) relayout_kernel(const RelayoutParams p) {
         const unsigned long long row = p.vecs >> 32 == 0
                                            ? static_cast<unsigned>(i) / p.row_vecs
                                            : i / p.row_vecs;
-        if (p.offsets != nullptr) {
-            const unsigned long long e = row / p.expert_rows;
-            if (p.offsets[e + 1] <= p.offsets[e]) continue;
-        }
         const unsigned c = 8 * static_cast<unsigned>(i - row * p.row_vecs);
-        const long long from = static_cast<long long>(row * p.cols) + c;
-        to[u] = static_cast<long long>(row) * p.ld + c;
+        const unsigned long long all = e * p.rows + row;  // of all matrices' rows
+        const long long from = static_cast<long long>(all * p.cols) + c;
+        to[u] = static_cast<long long>(all) * p.ld + c;
         off[u] = static_cast<uint32_t>(from & 7) * 2u;
         const long long at = from & ~7ll;
         if (at + 16 <= p.end) {
@@ -1046,13 +1062,13 @@ class ExpRelayout {
         const long long ld = op_round_up(cols, 64);
         jobs_[n_++] = Job{out, src, rows, cols, ld, arena.add(rows * ld * 2), nullptr, 1};
     }
-    // E matrices of K x N; with fewer rows than experts, of those that have rows
+    // E matrices of K x N
     void add_weights(OpMat *out, const uint16_t *src, const ExpSizes &z, OpArena &arena) {
         const int before = n_;
         add(out, src, static_cast<long long>(z.E) * z.K, z.N, arena);
-        if (n_ > before && z.R < z.E) {
+        if (n_ > before) {
             jobs_[before].offsets = z.offsets;
-            jobs_[before].expert_rows = z.K;
+            jobs_[before].experts = z.E;
         }
     }
     pgemm_status run(const OpDevice &dev, OpArena &arena, cudaStream_t s) {
@@ -1062,19 +1078,19 @@ class ExpRelayout {
             p.src = j.src;
             p.dst = arena.at<uint16_t>(j.at);
             p.row_vecs = static_cast<unsigned>((j.cols + 7) / 8);
-            p.vecs = static_cast<unsigned long long>(j.rows) * p.row_vecs;
+            p.rows = static_cast<unsigned long long>(j.rows / j.experts);
+            p.vecs = p.rows * p.row_vecs;
             p.cols = static_cast<unsigned>(j.cols);
             p.ld = j.ld;
             p.end = j.rows * j.cols;
             p.offsets = j.offsets;
-            p.expert_rows = static_cast<unsigned>(j.expert_rows);
             j.out->p = p.dst;
             j.out->ld = j.ld;
             const unsigned long long blocks = (p.vecs + 1023) / 1024;
             if (blocks > INT_MAX) return PGEMM_ERR_TOO_LARGE;
-            p.early = op_early(dev, static_cast<unsigned>(blocks));
-            const pgemm_status st = launch_small(
-                relayout_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), s, p);
+            const dim3 grid(static_cast<unsigned>(blocks), j.experts);
+            p.early = blocks * j.experts <= static_cast<unsigned>(dev.sm_count);
+            const pgemm_status st = launch_small(relayout_kernel, grid, dim3(256), s, p);
             if (st != PGEMM_OK) return st;
         }
         return PGEMM_OK;
@@ -1086,7 +1102,7 @@ class ExpRelayout {
         const uint16_t *src;
         long long rows, cols, ld, at;
         const int32_t *offsets;
-        int expert_rows;
+        int experts;
     };
     Job jobs_[4];
     int n_ = 0;
