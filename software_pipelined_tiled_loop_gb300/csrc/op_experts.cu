@@ -643,7 +643,8 @@ __device__ __forceinline__ WeightsUnit weights_unit(const ExpertsArgs &a, int u)
 }
 
 // Zeros for an expert without rows: part `i` of `parts` of its matrix, `size` elements at p,
-// by the pair's epilogue warps, `thread` of 512.
+// by the pair's epilogue warps, `thread` of 512.  One contiguous run whatever the pitch (64
+// experts 1024 x 2047, seven with rows: 55 us, 4.8 TB/s; as tiles 119).
 __device__ __forceinline__ void put_zeros(uint16_t *p, long long size, int i, int parts,
                                           unsigned thread) {
     const long long share = ((size - 1) / parts + 8) / 8 * 8;
