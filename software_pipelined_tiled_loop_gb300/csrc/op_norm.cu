@@ -115,7 +115,8 @@ __device__ __forceinline__ void gains_load(const NormParams &p, const RowSpan &r
 // registers where rows are aligned and not wide: int8 8192 x 4096 39.9 us against 48.7; of
 // other rows 4097 x 5121 would take 48.6 against 37.1, so those are left to the compiler.)
 template <int V, int MOST, bool ALIGNED, bool I8>
-__global__ void __launch_bounds__(MOST, ALIGNED && V <= 2 ? 2 : 0) rmsnorm_kernel(const NormParams p) {
+__global__ void __launch_bounds__(MOST, ALIGNED && V <= 2 ? 2 : 0)
+    rmsnorm_kernel(const NormParams p) {
     __shared__ uint32_t part[2][2][32];
     constexpr bool AHEAD = MOST <= 512;  // (more leave no registers for the next row)
     op_begin_early(p.early);
@@ -432,10 +433,11 @@ __global__ void __launch_bounds__(1024)
 }
 
 // f(vectors a thread, threads at most, whether rows start on vectors) as constants, and
-// threads.  Two vectors a thread or one (`one`: up to 512): forward, two are quicker with rows for every SM (8192 x
-// 4096 41.7 us against 48.9, 1500 x 4096 6.8 against 7.7) and one where a row's own latency
-// counts (1 x 4096 1.8 against 2.0); backward, whose thread holds three operands and the next
-// row's, one is (8192 x 4096 48.9 against 53.2, 400 x 4096 7.4 against 9.0).
+// threads.  Two vectors a thread or one (`one`: up to 512): forward, two are quicker with rows
+// for every SM (8192 x 4096 41.7 us against 48.9, 1500 x 4096 6.8 against 7.7) and one where a
+// row's own latency counts (1 x 4096 1.8 against 2.0); backward, whose thread holds three
+// operands and the next row's, one is (8192 x 4096 48.9 against 53.2, 400 x 4096 7.4 against
+// 9.0).
 template <class F>
 static pgemm_status with_row(int D, bool one, F &&f) {
     const int vecs = D % 8 == 0 ? D / 8 : (D + 14) / 8;
@@ -452,9 +454,9 @@ static pgemm_status with_row(int D, bool one, F &&f) {
     return pick(integral_constant<int, 5>{}, integral_constant<int, 832>{});
 }
 
-// Blocks for T rows, `most` at most: a multiple of eight where a block has more than one.
+// Blocks for T rows, some `most` at most: a multiple of eight where one has more than a row.
 static unsigned norm_grid(int T, long long most) {
-    return static_cast<unsigned>(T <= most ? T : most < 8 ? 1 : most / 8 * 8);
+    return static_cast<unsigned>(T <= most ? T : most < 8 ? 8 : most / 8 * 8);
 }
 
 static pgemm_status norm_check(int T, int D) {

@@ -330,8 +330,8 @@ __device__ __forceinline__ void sort_count(const SortParams &p, int32_t *count, 
     }
 }
 
-// f(block, its count of expert e) for the blocks first .. last - 1, eight on the way (sixteen: 32768 slots
-// of 64 experts 10.8 us for 8.7).
+// f(block, its count of expert e) for the blocks first .. last - 1, eight on the way
+// (sixteen: 32768 slots of 64 experts 10.8 us for 8.7).
 template <class F>
 __device__ __forceinline__ void block_counts(const SortParams &p, int e, int first, int last,
                                              F &&f) {
@@ -565,8 +565,9 @@ __global__ void __launch_bounds__(kRowsThreads) gather_kernel(const RowsParams p
     op_begin_early(p.early);
     const unsigned vecs = p.D / 8;
     const unsigned long long total = static_cast<unsigned long long>(p.T) * vecs;
-    for (unsigned long long i = blockIdx.x * static_cast<unsigned long long>(kRowsThreads) + threadIdx.x;
-         i < total; i += static_cast<unsigned long long>(gridDim.x) * kRowsThreads) {
+    const unsigned long long step = static_cast<unsigned long long>(gridDim.x) * kRowsThreads;
+    for (unsigned long long i = 1ull * blockIdx.x * kRowsThreads + threadIdx.x; i < total;
+         i += step) {
         const RowsAt at(i, vecs);
         const uint4 x = reinterpret_cast<const uint4 *>(p.x)[i];
         const int32_t *to = p.slot_row + at.t * p.k;
@@ -642,7 +643,8 @@ __global__ void __launch_bounds__(kRowsThreads) combine_flat_kernel(const RowsPa
             for (int j = 0; j < kAhead; ++j) {
                 in[j] = r[j] >= 0 && r[j] < p.rows;
                 if (in[j])
-                    y[j] = reinterpret_cast<const uint4 *>(p.ys + static_cast<long long>(r[j]) * p.D)[at.v];
+                    y[j] = reinterpret_cast<const uint4 *>(
+                        p.ys + static_cast<long long>(r[j]) * p.D)[at.v];
             }
             if (j0 + kAhead < p.k)
                 look_up(at, j0 + kAhead);
