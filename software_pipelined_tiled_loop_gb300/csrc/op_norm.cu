@@ -15,7 +15,7 @@
 // with a residual 42 us (6.4 TB/s), as int8 40 (5.9), backward 49 (5.5; the gains' gradient
 // and its join 5 of them); 4097 x 5120 26.6, 27.3 and 46.5, 4097 x 5121 32.6, 37.1 and 50;
 // rows of more than 20480 values, which do not fit a block's registers, at half that rate
-// (1024 x 32768 55, 63, 188).  One row of 4096 1.9 us from a graph.
+// (1024 x 32768 55, 64, 200).  One row of 4096 1.9 us from a graph.
 #include <cuda_runtime.h>
 
 #include "op_gemm.cuh"
@@ -265,14 +265,14 @@ __global__ void __launch_bounds__(MOST, ALIGNED && V <= 2 ? 2 : 0)
 
 // The gains' gradient: each block leaves the sums of its rows' dY n for norm_join_kernel.  A
 // thread keeps its columns' in its registers, or where a row is so wide that it has more
-// than two vectors, in places of its own in shared memory.
+// more than two vectors, in places of its own in shared memory.
 enum class GainSum { NONE, REGISTERS, SHARED };
 
 template <int V, int MOST, bool ALIGNED, GainSum SUM>
 __global__ void __launch_bounds__(MOST) rmsnorm_backward_kernel(const NormParams p) {
     extern __shared__ float4 sums[];  // [V][2][threads]
     __shared__ uint32_t part[2][2][32];
-    constexpr bool AHEAD = V <= 2;  // (more leave no registers for the next row)
+    constexpr bool AHEAD = V <= 2 && MOST <= 512;  // (else no registers for the next row)
     constexpr int OWN = SUM == GainSum::REGISTERS ? V : 1;
     float own[OWN][8];
 #pragma unroll
@@ -437,8 +437,9 @@ __global__ void __launch_bounds__(1024)
 // for every SM (8192 x 4096 41.7 us against 48.9, 1500 x 4096 6.8 against 7.7) and one where a
 // row's own latency counts (1 x 4096 1.8 against 2.0); backward, whose thread holds three
 // operands and the next row's, one is (8192 x 4096 48.9 against 53.2, 400 x 4096 7.4 against
-// 9.0).
-template <class F>
+// 9.0).  Wider rows, backward: two again, without the next row, while their sums fit the
+// registers (2730 x 12288 63 us, 2048 x 16384 72; with five 103 and 93).
+template <bool BACKWARD, class F>
 static pgemm_status with_row(int D, bool one, F &&f) {
     const int vecs = D % 8 == 0 ? D / 8 : (D + 14) / 8;
     using std::integral_constant;
@@ -450,6 +451,10 @@ static pgemm_status with_row(int D, bool one, F &&f) {
     const integral_constant<int, 512> few;
     if (vecs <= (one ? 512 : 32)) return pick(integral_constant<int, 1>{}, few);
     if (vecs <= 1024) return pick(integral_constant<int, 2>{}, few);
+    if constexpr (BACKWARD) {
+        if (vecs <= 1536) return pick(integral_constant<int, 2>{}, integral_constant<int, 768>{});
+        if (vecs <= 2048) return pick(integral_constant<int, 2>{}, integral_constant<int, 1024>{});
+    }
     if (vecs <= 2560) return pick(integral_constant<int, 5>{}, few);
     return pick(integral_constant<int, 5>{}, integral_constant<int, 832>{});
 }
@@ -488,7 +493,8 @@ static pgemm_status norm_forward(bool i8, int T, int D, const uint16_t *X, const
     p.y = i8 ? nullptr : static_cast<uint16_t *>(out);
     p.q = i8 ? static_cast<int8_t *>(out) : nullptr;
     p.scale = scale;
-    return with_row(D, T < 2 * dev.sm_count, [&](auto v, auto limit, auto aligned, int threads) {
+    const bool one = T < 2 * dev.sm_count;
+    return with_row<false>(D, one, [&](auto v, auto limit, auto aligned, int threads) {
         constexpr int V = decltype(v)::value, MOST = decltype(limit)::value;
         constexpr bool A = decltype(aligned)::value;
         const long long most = dev.sm_count * (threads >= 64 ? 2048ll / threads : 32ll);
@@ -525,7 +531,8 @@ static pgemm_status norm_backward(int T, int D, const uint16_t *S, const uint16_
     p.dy = dY;
     p.ds = dS;
     p.dx = dX;
-    return with_row(D, true, [&](auto v, auto limit, auto aligned, int threads) -> pgemm_status {
+    return with_row<true>(D, true, [&](auto v, auto limit, auto aligned,
+                                       int threads) -> pgemm_status {
         constexpr int V = decltype(v)::value, MOST = decltype(limit)::value;
         constexpr bool A = decltype(aligned)::value;
         constexpr GainSum SUM = V <= 2 ? GainSum::REGISTERS : GainSum::SHARED;

@@ -100,7 +100,7 @@ def test_neighbours_do_not_leak():
 
 # more rows than blocks run at once: a block's rows all start at the same place of a vector
 @pytest.mark.parametrize("T,D", [(20000, 9), (9001, 65), (6005, 129), (3007, 1001), (2003, 2046),
-                                 (1300, 8201), (700, 16390), (400, 20487), (333, 32761)])
+                                 (1300, 8201), (700, 16390), (400, 20487), (333, 32761), (700, 10241), (450, 12290), (400, 16363)])
 def test_norm_of_odd_widths_in_many_rows(T, D):
     X, R, gain, dY = rnd(21, T, D), rnd(22, T, D), rnd(23, D), rnd(24, T, D)
     S, Y = nan(T, D), nan(T, D)
