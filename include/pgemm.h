@@ -405,8 +405,8 @@ PGEMM_API pgemm_status experts_linear_bf16(int R, int N, int K, int E, const int
 
 /* Gradients of experts_linear_bf16 for dY (R x N): dX (R x K) <- dY W[e]^T row by row
  * (rows from offsets[E] on stay as they were), dW (E x K x N) <- X_e^T dY_e over the
- * expert's rows (zeros without any).  Either may be NULL; X is read only for dW and W
- * only for dX. */
+ * expert's rows (zeros without any), as exact for many rows as for few.  Either may be
+ * NULL; X is read only for dW and W only for dX. */
 PGEMM_API pgemm_status experts_linear_bf16_backward(int R, int N, int K, int E,
                                                     const int32_t *offsets, const uint16_t *X,
                                                     const uint16_t *W, const uint16_t *dY,

@@ -21,7 +21,7 @@ enum WaitSite : uint32_t {
     kSiteSelfTest = 9,        // pgemm_selftest_wait_timeout
     kSiteSplitPartial = 10,   // last piece of a stream-K tile waiting for the others' partials
     kSiteWidenChunk = 11,     // TMA producer waiting for a K chunk widened inside the GEMM
-    kSiteGroupTail = 12,      // producer waiting for a group's last rows, to clear what follows them
+    kSiteGroupTail = 12,      // experts' dW: a group's last rows fetched, cleared, multiplied
 };
 
 // Problem description passed by value to every kernel.

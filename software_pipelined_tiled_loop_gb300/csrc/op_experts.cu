@@ -589,6 +589,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 // waited for.  (Cleared in the ring's last stage, groups of 520 rows took 258 us for 32
 // experts' 2048 x 4096, 512 rows 182.)
 //
+// The tensor core truncates its sums, so an accumulator falls behind by up to 2^-23 of the
+// magnitudes in it with every 16 rows.  A group's rows go by in rounds of kWeightsRound,
+// each from zero, which the epilogue adds in fp32 registers, rounded to nearest: the error
+// of a dW is that of one round, however long its group, and no wait lasts longer than one.
+//
 // Few rows a group: a unit's output takes longer than its products.  Then a ring of three
 // stages instead of four makes room to stage all of a warp's output at once, 64 columns
 // wide (WIDE), whose rows of 128 bytes also write fewer 32-byte sectors in part where the
@@ -620,9 +625,20 @@ struct ExpWeightsCfg {
     static_assert(BK == 96, "a step's rows are one box of 96, 64 or 32");
 };
 
+// Rows of a round: whole steps, and as many as a round's error of 516 truncations (2^-14 of
+// the sum of magnitudes, a sixty-fourth of bf16's rounding) allows.
+constexpr int kWeightsRound = 96 * 86;
+// What a step may take at most where a wait spans a unit's steps: ten times what it takes.
+constexpr uint64_t kWeightsStepNs = 4000;
+
 struct WeightsUnit {
     int expert, begin, end, seg, m0, n0;
     __device__ __forceinline__ int whole() const { return begin + (end - begin) / 16 * 16; }
+    // (one for a group of fewer than 16 rows; without rows there are none)
+    __device__ __forceinline__ int rounds() const {
+        const int rows = whole() - begin;
+        return rows > 0 ? (rows - 1) / kWeightsRound + 1 : 1;
+    }
 };
 
 template <class Cfg>
@@ -834,14 +850,20 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     } else if (warp == Cfg::THREADS / 32 - 1) {
         // ---------------- the groups' last rows ----------------
         uint32_t tails = 0;
+        uint64_t steps = 0;  // of the units since the last such rows
         for (int u = slot; u < units; u += slots) {
             const WeightsUnit w = weights_unit<Cfg>(a, u);
             const int rows = w.end - w.whole();
+            const uint64_t waited = steps;
+            steps = (rows == 0 ? steps : 0) + static_cast<uint64_t>((w.end - w.begin) / BK + 1);
             if (rows == 0) continue;
             const uint32_t b = tails & 1u, ph = (tails >> 1) & 1u;
             ++tails;
             // (every lane waits: it must see the copies before it overwrites them)
-            if (!__all_sync(0xffffffffu, mbar_wait(&tail_full[b], ph, ctx, kSiteGroupTail))) break;
+            if (!__all_sync(0xffffffffu,
+                            mbar_wait_behind(&tail_full[b], ph, ctx, kSiteGroupTail,
+                                             waited * kWeightsStepNs)))
+                break;
             const uint32_t d = smem_u32(smem + Cfg::TAIL_OFFSET + b * Cfg::TAIL_BYTES);
             for (int r = rows * 8 + static_cast<int>(lane); r < 16 * 8; r += 32)
 #pragma unroll
@@ -870,48 +892,56 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             for (int u = slot; u < units; u += slots) {
                 const WeightsUnit w = weights_unit<Cfg>(a, u);
                 if (w.end <= w.begin) continue;
-                const uint32_t ab = n & 1u;
-                if (ok)
-                    ok = warp_value(mbar_wait(&acc_empty[ab], ((n >> 1) & 1u) ^ 1u, ctx,
-                                              kSiteMmaAccEmpty)) != 0;
-                ++n;
-                tc_fence_after();
-                const uint32_t d = tmem_w + ab * BN;
                 const int whole = w.whole();
-                uint32_t acc = 0;
-                for (int left = whole - w.begin; left > 0; left -= BK, ring.next()) {
-                    const uint32_t s = ring.s;
+                int left = whole - w.begin;
+                do {  // a round
+                    const uint32_t ab = n & 1u;
                     if (ok)
-                        ok = warp_value(mbar_wait(&full[s], ring.phase, ctx, kSiteMmaFull)) != 0;
-                    const uint32_t go = ok ? lead : 0u;
+                        ok = warp_value(mbar_wait(&acc_empty[ab], ((n >> 1) & 1u) ^ 1u, ctx,
+                                                  kSiteMmaAccEmpty)) != 0;
+                    ++n;
                     tc_fence_after();
-                    const uint64_t as = a0 + s * (Cfg::A_BYTES / 16), bs = b0 + s * (Cfg::B_BYTES / 16);
-                    auto multiply = [&](int k) {
-                        umma_f16_ss_if<2>(go, d, as + k * 128, bs + k * 128, idesc, acc);
-                        acc = 1;
-                    };
-                    if (left >= BK) {
+                    const uint32_t d = tmem_w + ab * BN;
+                    const int rest = max(left - kWeightsRound, 0);  // of the rounds after
+                    uint32_t acc = 0;
+                    for (; left > rest; left -= BK, ring.next()) {
+                        const uint32_t s = ring.s;
+                        if (ok)
+                            ok = warp_value(mbar_wait(&full[s], ring.phase, ctx,
+                                                      kSiteMmaFull)) != 0;
+                        const uint32_t go = ok ? lead : 0u;
+                        tc_fence_after();
+                        const uint64_t as = a0 + s * (Cfg::A_BYTES / 16);
+                        const uint64_t bs = b0 + s * (Cfg::B_BYTES / 16);
+                        auto multiply = [&](int k) {
+                            umma_f16_ss_if<2>(go, d, as + k * 128, bs + k * 128, idesc, acc);
+                            acc = 1;
+                        };
+                        if (left >= BK) {
 #pragma unroll
-                        for (int k = 0; k < BK / 16; ++k) multiply(k);
-                    } else {
+                            for (int k = 0; k < BK / 16; ++k) multiply(k);
+                        } else {
 #pragma unroll 1
-                        for (int k = 0; 16 * k < left; ++k) multiply(k);
+                            for (int k = 0; 16 * k < left; ++k) multiply(k);
+                        }
+                        umma_commit_if<2>(go, smem_u32(&empty[s]), kPair);
                     }
-                    umma_commit_if<2>(go, smem_u32(&empty[s]), kPair);
-                }
-                if (whole < w.end) {
-                    const uint32_t b = tails & 1u;
-                    if (ok)
-                        ok = warp_value(mbar_wait(&tail_ready[b], (tails >> 1) & 1u, ctx,
-                                                  kSiteGroupTail)) != 0;
-                    ++tails;
-                    tc_fence_after();
-                    const uint32_t st = smem_u32(smem + Cfg::TAIL_OFFSET) + b * Cfg::TAIL_BYTES;
-                    umma_f16_ss_if<2>(ok ? lead : 0u, d, smem_desc_sw128(st, 2048, 1024),
-                                      smem_desc_sw128(st + Cfg::TAIL_HALF, 2048, 1024), idesc, acc);
-                    umma_commit_if<2>(ok ? lead : 0u, smem_u32(&tail_empty[b]), kPair);
-                }
-                umma_commit_if<2>(ok ? lead : 0u, smem_u32(&acc_full[ab]), kPair);
+                    if (left <= 0 && whole < w.end) {
+                        const uint32_t b = tails & 1u;
+                        if (ok)
+                            ok = warp_value(mbar_wait(&tail_ready[b], (tails >> 1) & 1u, ctx,
+                                                      kSiteGroupTail)) != 0;
+                        ++tails;
+                        tc_fence_after();
+                        const uint32_t st =
+                            smem_u32(smem + Cfg::TAIL_OFFSET) + b * Cfg::TAIL_BYTES;
+                        umma_f16_ss_if<2>(ok ? lead : 0u, d, smem_desc_sw128(st, 2048, 1024),
+                                          smem_desc_sw128(st + Cfg::TAIL_HALF, 2048, 1024), idesc,
+                                          acc);
+                        umma_commit_if<2>(ok ? lead : 0u, smem_u32(&tail_empty[b]), kPair);
+                    }
+                    umma_commit_if<2>(ok ? lead : 0u, smem_u32(&acc_full[ab]), kPair);
+                } while (left > 0);
             }
             umma_commit_if<2>(lead, smem_u32(mma_done), 1);
             mbar_wait(mma_done, 0, ctx, kSiteMmaDone);
@@ -939,20 +969,41 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                           crank * 256 + e * 32 + lane);
                 continue;
             }
-            const uint32_t ab = n & 1u;
             constexpr int C = Cfg::EPI_COLS / 32, B = C < Cfg::NBUF ? C : Cfg::NBUF;
             uint32_t v[32 * C];
-            if (!mbar_wait(&acc_full[ab], (n >> 1) & 1u, ctx, kSiteEpilogueFull)) break;
-            tc_fence_after();
-            const uint32_t t_row = tmem + ((q * 32u) << 16) + ab * BN + col0;
+            // take(the next round's accumulator); false after a wait that ran out
+            auto round = [&](auto &&take) {
+                const uint32_t ab = n & 1u;
+                if (!mbar_wait(&acc_full[ab], (n >> 1) & 1u, ctx, kSiteEpilogueFull)) return false;
+                tc_fence_after();
+                take(tmem + ((q * 32u) << 16) + ab * BN + col0);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[ab]), 0));
+                ++n;
+                return true;
+            };
+            bool ok = round([&](uint32_t t_row) {
 #pragma unroll
-            for (int b = 0; b < C; ++b)
-                tmem_ld_32x32b_x32(t_row + 32 * b, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * b));
-            tmem_ld_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[ab]), 0));
-            ++n;
+                for (int b = 0; b < C; ++b)
+                    tmem_ld_32x32b_x32(t_row + 32 * b,
+                                       *reinterpret_cast<uint32_t(*)[32]>(v + 32 * b));
+                tmem_ld_wait();
+            });
+            for (int more = w.rounds() - 1; ok && more > 0; --more)
+                ok = round([&](uint32_t t_row) {
+#pragma unroll
+                    for (int b = 0; b < C; ++b) {
+                        uint32_t x[32];
+                        tmem_ld_32x32b_x32(t_row + 32 * b, x);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            v[32 * b + j] = __float_as_uint(__uint_as_float(v[32 * b + j]) +
+                                                            __uint_as_float(x[j]));
+                    }
+                });
+            if (!ok) break;
 #pragma unroll
             for (int j = 0; j < 16 * C; ++j)
                 v[j] = pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));

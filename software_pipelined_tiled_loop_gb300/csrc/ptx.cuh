@@ -141,6 +141,26 @@ __device__ __forceinline__ bool device_failed(const KernelCtx &ctx) {
     return *reinterpret_cast<volatile uint32_t *>(ctx.status) != 0u;
 }
 
+// mbar_wait for what comes only behind other work, which may take `more_ns` longer than a
+// wait's limit.  Beyond the limit it also ends where a failure has been recorded.
+__device__ __forceinline__ bool mbar_wait_behind(uint64_t *bar, uint32_t parity,
+                                                 const KernelCtx &ctx, uint32_t site,
+                                                 uint64_t more_ns) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        const uint64_t t = globaltimer_ns() - t0;
+        if (t > ctx.wait_limit_ns &&
+            (t - ctx.wait_limit_ns > more_ns || device_failed(ctx))) {
+            atomicCAS(ctx.status, 0u, kStatusTimeout | (site & 0xffffu));
+            return false;
+        }
+    }
+}
+
 // ------------------------------------------------------------------- TMA ---
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
