@@ -397,8 +397,10 @@ PGEMM_API pgemm_status expert_combine_bf16_backward(int T, int k, int D, const u
  * offsets[e + 1] of expert e.  X is R x K, W E x K x N, Y R x N; offsets (E + 1, on the
  * device) as expert_sort leaves them: not decreasing, at most R (what is beyond R counts
  * as R, below 0 as 0).  Rows of Y from offsets[E] on stay as they were.  No host
- * synchronisation.  K == 0 counts the products as zero.  E <= 1024, E K < 2^31 (else
- * PGEMM_ERR_TOO_LARGE). */
+ * synchronisation.  K == 0 counts the products as zero.  E <= 1024, E K < 2^31, and a sum
+ * over columns (here K; a dX's N, or 2 F of both its products) has 2^19 of them at most
+ * (else PGEMM_ERR_TOO_LARGE): the tensor core truncates it by up to 2^-23 of the magnitudes
+ * with every 16. */
 PGEMM_API pgemm_status experts_linear_bf16(int R, int N, int K, int E, const int32_t *offsets,
                                            const uint16_t *X, const uint16_t *W, uint16_t *Y,
                                            pgemm_stream_t stream);

@@ -504,7 +504,8 @@ def expert_combine_bf16_backward(T, k, D, Ys, slot_row, weights, dY, dYs, dweigh
 def experts_linear_bf16(R, N, K, E, offsets, X, W, Y, stream=None):
     """Y[r] <- X[r] @ W[e] for the rows offsets[e] <= r < offsets[e + 1] of expert e.  X: R
     x K, W: E x K x N, Y: R x N (rows from offsets[E] on stay as they were), offsets: E + 1
-    int32, as expert_sort leaves them.  Asynchronous, without a host synchronisation."""
+    int32, as expert_sort leaves them.  A sum over columns (K; a dX's N, or 2 F) has 2^19
+    of them at most.  Asynchronous, without a host synchronisation."""
     _sizes("experts_linear_bf16", R | N | K | E)
     _check(lib().experts_linear_bf16(
         R, N, K, E, _operand(offsets, "offsets", E + 1, _I32), _operand(X, "X", R * K, _BF16),

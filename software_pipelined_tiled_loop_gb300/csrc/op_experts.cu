@@ -1331,6 +1331,12 @@ static pgemm_status exp_check(const ExpSizes &z) {
     return PGEMM_OK;
 }
 
+// Whether a tile's sum over so many columns is taken: every 16 of them truncate it by up to
+// 2^-23 of the magnitudes in it, 2^19 by a bf16 rounding's 2^-8.  (A unit's main loop, which
+// its epilogue waits for, is then some milliseconds long.)
+constexpr long long kSumMost = 1 << 19;
+static bool exp_sum_fits(long long columns) { return columns <= kSumMost; }
+
 static pgemm_status zero_bf16(uint16_t *p, long long n, cudaStream_t s) {
     return n == 0 || cudaMemsetAsync(p, 0, static_cast<size_t>(n) * 2, s) == cudaSuccess
                ? PGEMM_OK
@@ -1340,7 +1346,9 @@ static pgemm_status zero_bf16(uint16_t *p, long long n, cudaStream_t s) {
 static pgemm_status experts_linear_forward(const ExpSizes &z, const uint16_t *X, const uint16_t *W,
                                            uint16_t *Y, cudaStream_t s) {
     pgemm_status st = exp_check(z);
-    if (st != PGEMM_OK || z.R == 0 || z.N == 0) return st;
+    if (st != PGEMM_OK) return st;
+    if (!exp_sum_fits(z.K)) return PGEMM_ERR_TOO_LARGE;
+    if (z.R == 0 || z.N == 0) return PGEMM_OK;
     if (!z.offsets || !Y || (z.K > 0 && (!X || !W))) return PGEMM_ERR_INVALID_VALUE;
     if (!op_aligned16(z.offsets) || !op_aligned16(X) || !op_aligned16(W) || !op_aligned16(Y))
         return PGEMM_ERR_MISALIGNED;
@@ -1366,6 +1374,7 @@ static pgemm_status experts_linear_backward(const ExpSizes &z, const uint16_t *X
     if (st != PGEMM_OK) return st;
     const bool want_x = dX && z.R > 0 && z.K > 0, want_w = dW && z.K > 0 && z.N > 0;
     if (!want_x && !want_w) return PGEMM_OK;
+    if (want_x && !exp_sum_fits(z.N)) return PGEMM_ERR_TOO_LARGE;
     const bool some = z.R > 0 && z.N > 0;
     if (!z.offsets || (some && (!dY || (want_w && !X) || (want_x && !W))))
         return PGEMM_ERR_INVALID_VALUE;
@@ -1406,6 +1415,7 @@ static pgemm_status experts_gated_forward(const ExpSizes &z, const uint16_t *X, 
     pgemm_status st = exp_check(z);
     if (st != PGEMM_OK) return st;
     if (!exp_act_known(act)) return PGEMM_ERR_INVALID_VALUE;
+    if (!exp_sum_fits(z.K)) return PGEMM_ERR_TOO_LARGE;
     if (z.R == 0 || z.N == 0) return PGEMM_OK;
     if (!z.offsets || !H || (z.K > 0 && (!X || !Wg || !Wu))) return PGEMM_ERR_INVALID_VALUE;
     if (!op_aligned16(z.offsets) || !op_aligned16(X) || !op_aligned16(Wg) || !op_aligned16(Wu) ||
@@ -1440,6 +1450,8 @@ static pgemm_status experts_gated_backward(const ExpSizes &z, const uint16_t *X,
     if (!want_x && !want_w) return PGEMM_OK;
     const bool some = z.R > 0 && z.N > 0;
     const bool recompute = some && !preact;
+    if ((want_x && !exp_sum_fits(2ll * z.N)) || (recompute && !exp_sum_fits(z.K)))
+        return PGEMM_ERR_TOO_LARGE;
     if (!z.offsets || (some && (!dH || ((want_w || recompute) && !X) ||
                                 ((want_x || recompute) && (!Wg || !Wu)))))
         return PGEMM_ERR_INVALID_VALUE;

@@ -1,5 +1,5 @@
-"""The experts' weight gradients of groups of many rows: as exact as those of few, and no wait
-of the kernel's runs out, up to 2^31 - 1 rows."""
+"""The experts' products of long sums: weight gradients of many rows are as exact as of few, and
+no wait runs out, up to 2^31 - 1 rows; forward and dX at the most columns that they take."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -103,3 +103,31 @@ def test_weights_of_as_many_rows_as_an_int_counts():
     pg.experts_linear_bf16_backward(R, N, K, E, offsets_of(sizes), X, None, dY, None, dW)
     torch.cuda.synchronize()
     check_weights(dW, X, dY, sizes)
+
+
+@pytest.mark.parametrize("sizes", [[1, 3], [41] * 40])  # (tiles of one CTA, and of a pair)
+def test_sums_of_as_many_columns_as_there_may_be(sizes):
+    K, N, E, R = 2 ** 19, 24, len(sizes), sum(sizes)
+    offsets = offsets_of(sizes)
+    X, W = positive(6, R, K), positive(7, E * K, N).view(E, K, N)
+    Y, H = (torch.full((R, N), float("nan"), device="cuda", dtype=BF16) for _ in range(2))
+    pg.experts_linear_bf16(R, N, K, E, offsets, X, W, Y)
+    ref.check(Y, *moe.experts_linear(offsets, X, W)["Y"], "Y")
+    pg.experts_gated_bf16(R, N, K, E, offsets, X, W, W, "none", H)
+    ref.check(H, *moe.experts_gated(offsets, X, W, W, "none")["H"], "H")
+    Wt, dX = positive(8, E * N, K).view(E, N, K), torch.full_like(Y, float("nan"))
+    pg.experts_linear_bf16_backward(R, K, N, E, offsets, None, Wt, X, dX, None)  # X as dY
+    want = moe.experts_linear_backward(offsets, Y.zero_(), Wt, X)
+    ref.check(dX, *want["dX"], "dX")
+    g = torch.Generator(device="cuda").manual_seed(9)
+    F = K // 2
+    Z = torch.rand(2, R, F, generator=g, device="cuda")
+    pg.experts_gated_bf16_backward(R, F, N, E, offsets, None, Wt[..., :F].contiguous(),
+                                   Wt[..., F:].contiguous(), "none", X[:, :F].contiguous(), dX,
+                                   None, None, preact=Z)
+    for e, a, b in moe.groups(offsets):
+        d = X[a:b, :F].double()
+        dz = torch.cat([d * Z[1, a:b], d * Z[0, a:b]], 1)  # dG, dU: act is the identity
+        y = dz @ Wt[e].double().t()
+        # of positive terms: their rounding to bf16 and 2^-23 for every 16 columns
+        ref.check(dX[a:b], y, moe.bf16_out(y, y * (2.0 ** -8 + ref.step(K))), "gated dX")
