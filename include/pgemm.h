@@ -319,15 +319,17 @@ PGEMM_API pgemm_status xent_bf16_grad(int T, int V, int D, const uint16_t *X, co
  * y = S gain / sqrt(mean over the row of S^2 + eps) to Y.  X, residual (NULL:
  * none), S (NULL: not kept; may be X or the residual) and Y are T x D, gain D
  * (NULL: ones).  S is rounded to bf16, and y is made of that.  eps >= 0.  The sum of
- * squares is fp32: a row whose squares pass its range gives zeros.
- * D <= 32768 (else PGEMM_ERR_TOO_LARGE). */
+ * squares is fp32: a row whose squares pass its range gives zeros with an eps of 2^-100 or
+ * more, and has its norm with a smaller one, as has a row whose squares fall below it
+ * (eps = 0: a row of zeros, and it alone, has none and gives NaN).  D == 0 or T == 0: nothing
+ * is written.  D <= 32768 (else PGEMM_ERR_TOO_LARGE). */
 PGEMM_API pgemm_status rmsnorm_bf16(int T, int D, const uint16_t *X, const uint16_t *residual,
                                     const uint16_t *gain, float eps, uint16_t *S, uint16_t *Y,
                                     pgemm_stream_t stream);
 
 /* The same with y as int8, for gemm_i8: scale[t] = max over the row of |y| / 127,
  * Q = y / scale[t] rounded to the nearest integer (ties to even), so that y is about
- * Q * scale[t].  A row of zeros has scale 0; a row with an infinity or a NaN in y has
+ * Q * scale[t].  A row of zeros has scale 0 (eps > 0); a row with an infinity or a NaN in y has
  * scale NaN and Q 0. */
 PGEMM_API pgemm_status rmsnorm_i8(int T, int D, const uint16_t *X, const uint16_t *residual,
                                   const uint16_t *gain, float eps, uint16_t *S, int8_t *Q,

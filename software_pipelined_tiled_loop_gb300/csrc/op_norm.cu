@@ -84,6 +84,28 @@ __device__ __forceinline__ uint32_t round4_i8(const float *x) {
     return __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
 }
 
+// With an eps of less than 2^-100 a row's squares may all have left fp32's range and its norm
+// be finite.  Such calls have kernels of their own (ENDS): where mean(S^2) + eps lies outside
+// 2^-100 .. infinity they go through the row again as S by, with eps by^2: by = 2^76 below
+// (values under 2^-42, squares from 2^-114 to 2^84), 2^-72 above (squares up to 2^112; what
+// that takes below bf16's range is 2^-110 of the norm's ones).  They take 5 % more time
+// (8192 x 4096 backward 52.8 us for 49.4), which is why not all calls do.
+constexpr float kEndsBelow = 7.8886091e-31f;
+__device__ __forceinline__ bool var_fits(float var) {
+    return var >= kEndsBelow && var < __int_as_float(0x7f800000);
+}
+__device__ __forceinline__ float var_shift(float var) {
+    return var < 1.0f ? 7.5557864e22f : 2.1175824e-22f;
+}
+// Eight values of S, times by.
+__device__ __forceinline__ void shift8(uint4 &s, float by) {
+    float f[8];
+    unpack8(s, f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] *= by;
+    s = pack8(f);
+}
+
 struct NormParams {
     int T, D;
     float eps;
@@ -114,7 +136,7 @@ __device__ __forceinline__ void gains_load(const NormParams &p, const RowSpan &r
 // V vectors a thread, up to MOST threads; ALIGNED: D is a multiple of 8.  (Held to 64
 // registers where rows are aligned and not wide: int8 8192 x 4096 39.9 us against 48.7; of
 // other rows 4097 x 5121 would take 48.6 against 37.1, so those are left to the compiler.)
-template <int V, int MOST, bool ALIGNED, bool I8>
+template <int V, int MOST, bool ALIGNED, bool I8, bool ENDS>
 __global__ void __launch_bounds__(MOST, ALIGNED && V <= 2 ? 2 : 0)
     rmsnorm_kernel(const NormParams p) {
     __shared__ uint32_t part[2][2][32];
@@ -178,7 +200,28 @@ __global__ void __launch_bounds__(MOST, ALIGNED && V <= 2 ? 2 : 0)
         if (AHEAD && t + gridDim.x < T) fetch(t + gridDim.x);
         block_reduce<1, I8>(sum, most, part[turn]);
         turn ^= 1;
-        const float rstd = 1.0f / sqrtf(sum[0] / static_cast<float>(p.D) + p.eps);
+        float var = sum[0] / static_cast<float>(p.D) + p.eps;
+        bool fits = true;
+        if constexpr (ENDS) {
+            fits = var_fits(var);
+            if (!fits) {
+                const float by = var_shift(var);
+                sum[0] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    shift8(s[i], by);
+                    float f[8];
+                    unpack8(s[i], f);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sum[0] = fmaf(f[j], f[j], sum[0]);
+                }
+                uint32_t none = 0u;
+                block_reduce<1, false>(sum, none, part[turn]);
+                turn ^= 1;
+                var = sum[0] / static_cast<float>(p.D) + p.eps * by * by;
+            }
+        }
+        const float rstd = 1.0f / sqrtf(var);  // (ENDS: of S by)
         auto value = [&](int i, float (&y)[8]) {
             float g[8];
             unpack8(gains[i], g);
@@ -202,7 +245,7 @@ __global__ void __launch_bounds__(MOST, ALIGNED && V <= 2 ? 2 : 0)
             // and far below 1 scaled up first, so that the reciprocal is finite.
             const float product = __uint_as_float(most);
             float top = product * rstd, by = 1.0f, inv = 0.0f;
-            const bool near = product > 7.8886091e-31f && product < 1.2676506e30f &&  // 2^+-100
+            const bool near = fits && product > 7.8886091e-31f && product < 1.2676506e30f &&  // 2^+-100
                               rstd > 0.0f && top < __int_as_float(0x7f800000);
             if (near) {
                 inv = 127.0f / product;
@@ -268,7 +311,7 @@ __global__ void __launch_bounds__(MOST, ALIGNED && V <= 2 ? 2 : 0)
 // more than two vectors, in places of its own in shared memory.
 enum class GainSum { NONE, REGISTERS, SHARED };
 
-template <int V, int MOST, bool ALIGNED, GainSum SUM>
+template <int V, int MOST, bool ALIGNED, GainSum SUM, bool ENDS>
 __global__ void __launch_bounds__(MOST) rmsnorm_backward_kernel(const NormParams p) {
     extern __shared__ float4 sums[];  // [V][2][threads]
     __shared__ uint32_t part[2][2][32];
@@ -310,31 +353,47 @@ __global__ void __launch_bounds__(MOST) rmsnorm_backward_kernel(const NormParams
     for (; t < T; t += gridDim.x) {
         const RowSpan row(t, p.T, p.D);
         float both[2] = {0.0f, 0.0f};
+        auto sum_up = [&] {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int v = threadIdx.x + i * blockDim.x;
-            if (v >= row.vecs) break;
-            if (!ALIGNED) {
-                row_mask(s[i], row, v);
-                row_mask(dy[i], row, v);
-            }
-            float fs[8], fd[8], g[8];
-            unpack8(s[i], fs);
-            unpack8(dy[i], fd);
-            unpack8(gains[i], g);
+            for (int i = 0; i < V; ++i) {
+                const int v = threadIdx.x + i * blockDim.x;
+                if (v >= row.vecs) break;
+                if (!ALIGNED) {
+                    row_mask(s[i], row, v);
+                    row_mask(dy[i], row, v);
+                }
+                float fs[8], fd[8], g[8];
+                unpack8(s[i], fs);
+                unpack8(dy[i], fd);
+                unpack8(gains[i], g);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                both[0] = fmaf(fs[j], fs[j], both[0]);
-                both[1] = fmaf(fd[j] * g[j], fs[j], both[1]);
+                for (int j = 0; j < 8; ++j) {
+                    both[0] = fmaf(fs[j], fs[j], both[0]);
+                    both[1] = fmaf(fd[j] * g[j], fs[j], both[1]);
+                }
             }
-        }
+        };
+        sum_up();
         const unsigned after = t + gridDim.x;
         uint4 s1[V], dy1[V], ds1[V];
         if (AHEAD && after < T) fetch(after, s1, dy1, ds1);
         uint32_t none = 0u;
         block_reduce<2, false>(both, none, part[turn]);
         turn ^= 1;
-        const float rstd = 1.0f / sqrtf(both[0] / static_cast<float>(p.D) + p.eps);
+        float var = both[0] / static_cast<float>(p.D) + p.eps, by = 1.0f;
+        if constexpr (ENDS) {
+            if (!var_fits(var)) {
+                by = var_shift(var);
+#pragma unroll
+                for (int i = 0; i < V; ++i) shift8(s[i], by);
+                both[0] = both[1] = 0.0f;
+                sum_up();
+                block_reduce<2, false>(both, none, part[turn]);
+                turn ^= 1;
+                var = both[0] / static_cast<float>(p.D) + p.eps * by * by;
+            }
+        }
+        const float rstd = 1.0f / sqrtf(var);  // (ENDS: of S by)
         const float m = both[1] * rstd / static_cast<float>(p.D);  // mean(a n)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -349,7 +408,8 @@ __global__ void __launch_bounds__(MOST) rmsnorm_backward_kernel(const NormParams
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float n = fs[j] * rstd;
-                o[j] += rstd * fmaf(-n, m, fd[j] * g[j]);
+                const float d = fmaf(-n, m, fd[j] * g[j]);
+                o[j] += rstd * (ENDS ? by * d : d);
                 if constexpr (SUM == GainSum::REGISTERS)
                     own[i][j] = fmaf(fd[j], n, own[i][j]);
                 else
@@ -500,9 +560,33 @@ static pgemm_status norm_forward(bool i8, int T, int D, const uint16_t *X, const
         const long long most = dev.sm_count * (threads >= 64 ? 2048ll / threads : 32ll);
         const dim3 grid(norm_grid(T, most));
         p.early = op_early(dev, grid.x);
-        return i8 ? launch_small(rmsnorm_kernel<V, MOST, A, true>, grid, dim3(threads), s, p)
-                  : launch_small(rmsnorm_kernel<V, MOST, A, false>, grid, dim3(threads), s, p);
+        if (eps < kEndsBelow)
+            return launch_small(i8 ? rmsnorm_kernel<V, MOST, A, true, true>
+                                   : rmsnorm_kernel<V, MOST, A, false, true>,
+                                grid, dim3(threads), s, p);
+        return launch_small(i8 ? rmsnorm_kernel<V, MOST, A, true, false>
+                               : rmsnorm_kernel<V, MOST, A, false, false>,
+                            grid, dim3(threads), s, p);
     });
+}
+
+template <int V, int MOST, bool ALIGNED, GainSum SUM, bool ENDS>
+static pgemm_status norm_backward_launch(const OpDevice &dev, dim3 grid, int threads, int smem,
+                                         cudaStream_t s, const NormParams &p) {
+    constexpr auto kernel = rmsnorm_backward_kernel<V, MOST, ALIGNED, SUM, ENDS>;
+    if constexpr (SUM == GainSum::SHARED) {
+        static const KernelInfo info = [] {
+            KernelInfo k;
+            k.threads = 32;
+            k.smem_bytes = 32 * V * MOST;
+            k.func = reinterpret_cast<const void *>(
+                rmsnorm_backward_kernel<V, MOST, ALIGNED, SUM, ENDS>);
+            return k;
+        }();
+        const pgemm_status st = op_kernel_setup(dev, info, nullptr);
+        if (st != PGEMM_OK) return st;
+    }
+    return launch_small_smem(kernel, grid, dim3(threads), smem, s, p);
 }
 
 static pgemm_status norm_backward(int T, int D, const uint16_t *S, const uint16_t *gain, float eps,
@@ -547,26 +631,19 @@ static pgemm_status norm_backward(int T, int D, const uint16_t *S, const uint16_
         const long long at = arena.add(dgain ? 4ll * blocks * D : 0);
         pgemm_status e = arena.alloc();
         if (e != PGEMM_OK) return e;
+        p.dgain = dgain ? arena.at<float>(at) : nullptr;
+        const dim3 grid(blocks);
+        const bool ends = eps < kEndsBelow;
         if (!dgain)
-            return launch_small(rmsnorm_backward_kernel<V, MOST, A, GainSum::NONE>, dim3(blocks),
-                                dim3(threads), s, p);
-        NormParams q = p;
-        q.dgain = arena.at<float>(at);
-        if (SUM == GainSum::SHARED) {
-            static const KernelInfo info = [] {
-                KernelInfo k;
-                k.threads = 32;
-                k.smem_bytes = 32 * V * MOST;
-                k.func = reinterpret_cast<const void *>(rmsnorm_backward_kernel<V, MOST, A, SUM>);
-                return k;
-            }();
-            if ((e = op_kernel_setup(dev, info, nullptr)) != PGEMM_OK) return e;
-        }
-        e = launch_small_smem(rmsnorm_backward_kernel<V, MOST, A, SUM>, dim3(blocks), dim3(threads),
-                              smem, s, q);
+            return ends ? norm_backward_launch<V, MOST, A, GainSum::NONE, true>(dev, grid, threads,
+                                                                                0, s, p)
+                        : norm_backward_launch<V, MOST, A, GainSum::NONE, false>(dev, grid, threads,
+                                                                                 0, s, p);
+        e = ends ? norm_backward_launch<V, MOST, A, SUM, true>(dev, grid, threads, smem, s, p)
+                 : norm_backward_launch<V, MOST, A, SUM, false>(dev, grid, threads, smem, s, p);
         if (e != PGEMM_OK) return e;
         return launch_small(norm_join_kernel, dim3(op_blocks(D, 32)), dim3(1024), s,
-                            static_cast<const float *>(q.dgain), blocks, D, dgain);
+                            static_cast<const float *>(p.dgain), blocks, D, dgain);
     });
 }
 
