@@ -15,12 +15,19 @@
 // 256-row tiles on the M side would pay for 256; groups are ragged in one direction only,
 // and the instruction's N follows them.  A group of more rows than a tile takes is dealt
 // out evenly.  A thread owns one feature of the output: a warp's store covers 32 features
-// of a row, full 32-byte sectors, so rows need no staging, no alignment and no tensor map,
-// and stop where the group does.
+// of a row, 64 bytes, so rows need no staging, no alignment and no tensor map, and stop
+// where the group does.  (Whole 32-byte sectors where rows are a multiple of 16 features
+// long; elsewhere those at its two ends are written in part.)
 //
 // Gated: a CTA's 128 accumulator lanes are 64 features of Wg and the same 64 of Wu, so the
 // two products of an element lie in lanes of different warps; each of the two warps hands
 // the other half of its columns through shared memory and finishes the other half.
+//
+// The gated gradient's dG and dU are rounded to bf16, as the dense one's are: the products
+// that follow take both operands in one type, and the other one is the bf16 weights or rows.
+// In 32 bits they would be tf32 products at half of the rate, or a second bf16 product for
+// what the rounding left.  dX, dWg and dWu are off by 2.35e-3 (2-norm) with it, of which
+// their own rounding is 1.66e-3.
 //
 // Weights' gradients: experts_weights_kernel, the tiled TN product with a group's rows
 // as its K range.  The range starts and ends anywhere; in its last K step the rows behind
@@ -74,7 +81,7 @@ struct ExpertsArgs {
 // reduction a step.  What a step's copies cost is their number: one expert, 8192 x 8192 x
 // 4096 on pairs, took 404 us with four boxes of 32 rows a step, 323 with one of 128, and
 // 285 (1.93 PFLOP/s) since the warps that issue them run as one (warp_value).  A pair's ring
-// holds six steps of 64 columns, a load from HBM taking some six steps' products: 64 experts
+// holds six steps of 64 columns, so that loads from HBM have longer to arrive: 64 experts
 // of some 512 rows, 2048 x 1024 gated, 187 us, with three steps of 128 197.  Such ragged
 // groups (32 experts, 4096 x 2048: 1.48 PFLOP/s) pay for tiles of fewer than 256 rows, whose
 // weights are as many bytes for fewer products.
@@ -600,7 +607,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 // matrix's rows start anywhere in one.  us with three and with four stages, sizes of groups
 // that spread by half: 32 experts 2048 x 4096, 24 rows a group 123 and 127, 256 rows 153 and
 // 170, 320 rows 165 and 172, 448 rows 192 and 187; 64 experts 1024 x 1368 8 rows 52 and 60,
-// 256 rows 70 and 77, 448 rows 92 and 89.  (Where rows start on 128 bytes and experts are
+// 256 rows 70 and 77, 448 rows 92 and 89 (all before sums went by rounds, which cost some
+// 0.5 %).  (Where rows start on 128 bytes and experts are
 // small four stages are the quicker below some 128 rows too: 1024 x 2048, 96 rows 82 and 79.)
 // What is left is writing dW (8 rows each of 64 experts 1024 x 2048: 4.2 TB/s, a memset's
 // rate) and, with more rows, the traffic of both directions beside the products (512 rows

@@ -8,14 +8,16 @@
 // whole either way, and its sum of squares costs nothing beside that.
 //
 // A block takes a row at a time and keeps it in registers between the sum and the
-// outputs, so every operand is read once; the next row's operands travel meanwhile.  All
+// outputs, so every operand is read once; the next row's operands travel meanwhile where
+// registers hold them (up to 512 threads; backward, up to two vectors a thread).  All
 // operands have the same pitch and 16-byte-aligned bases, so a row starts at the same place
 // of a 16-byte vector in each: a thread takes whole aligned vectors (eight elements of the
 // flat matrix), masked at the row's two ends, whatever the width.  Bound by HBM: 8192 x 4096
 // with a residual 42 us (6.4 TB/s), as int8 40 (5.9), backward 49 (5.5; the gains' gradient
-// and its join 5 of them); 4097 x 5120 26.6, 27.3 and 46.5, 4097 x 5121 32.6, 37.1 and 50;
-// rows of more than 20480 values, which do not fit a block's registers, at half that rate
-// (1024 x 32768 55, 64, 200).  One row of 4096 1.9 us from a graph.
+// and its join 5 of them); 4097 x 5120 27.5, 27.8 and 46.5, 4097 x 5121 33, 37.3 and 50.5,
+// 2048 x 16384 45, 48.5 and 73.  Backward, wider rows than 4096 leave an SM one block or two
+// with too little on the way.  Above 20480 values registers spill, backward most (1024 x 32768
+// 55, 62 and 207).  One row of 4096 1.8 us from a graph.
 #include <cuda_runtime.h>
 
 #include "op_gemm.cuh"
@@ -308,7 +310,7 @@ __global__ void __launch_bounds__(MOST, ALIGNED && V <= 2 ? 2 : 0)
 
 // The gains' gradient: each block leaves the sums of its rows' dY n for norm_join_kernel.  A
 // thread keeps its columns' in its registers, or where a row is so wide that it has more
-// more than two vectors, in places of its own in shared memory.
+// than two vectors, in places of its own in shared memory.
 enum class GainSum { NONE, REGISTERS, SHARED };
 
 template <int V, int MOST, bool ALIGNED, GainSum SUM, bool ENDS>
